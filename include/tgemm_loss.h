@@ -1,0 +1,136 @@
+/*
+ * tgemm losses -- a language model's vocabulary head fused with its loss, on
+ * NVIDIA GB300 (sm_103a).  Part of libtgemm.so; same conventions as tgemm.h:
+ * plain integers and pointers, status codes of enum tgemm_status, a stream as
+ * `void*`, nothing allocated, asynchronous on `stream`, safe to call from
+ * several host threads.
+ *
+ * The head's product  z[t][v] = scale * sum_d H[t][d] W[v][d]  is computed tile
+ * by tile, and the T x V logits are never written out: a tile leaves only the
+ * maximum, the sum of exponentials and the weighted sum of each of its rows.
+ * The backward pass computes the logits again, in pieces of the vocabulary,
+ * and keeps one piece of their gradient (16-bit, in the workspace) at a time.
+ *
+ *   H: T x D hidden states, element (t, d) at H[t*ldh + d], ldh >= D
+ *   W: V x D head weight, one row per vocabulary entry, W[v*ldw + d], ldw >= D
+ *
+ * Two losses, float32, one value per row t, with
+ * lse_t = log sum_v exp(z[t][v]):
+ *
+ * Cross entropy (tgemm_xent_*): with the target y_t, eps = label_smoothing and
+ * q = (1 - eps) [v = y_t] + eps / V
+ *     loss_t = lse_t - sum_v q_v z[t][v] + z_loss * lse_t^2.
+ * A row whose target is ignore_index is ignored.
+ *
+ * Distillation from a teacher's top logits (tgemm_distill_*): row t lists K
+ * entries ids[t][k] with the teacher's logits[t][k]; an id below 0 marks an
+ * unused place.  With q = softmax over the row's used places of
+ * scale * logits (scale = 1 / temperature, on both sides),
+ *     loss_t = sum_k q_k log q_k + lse_t - sum_k q_k z[t][ids[t][k]],
+ * the divergence of the student's distribution from the teacher's renormalised
+ * top-K.  An entry listed twice counts with both masses; a logit of -inf has
+ * no mass.  A row with no used place, or whose used logits are all -inf, is
+ * ignored.  K <= TGEMM_DISTILL_MAX_K.
+ *
+ * Ignored rows have loss 0, lse 0 and no part in any gradient, whatever H
+ * holds there (NaN included); they cost no product work, since the rows that
+ * count are gathered first.  A row with a target or an id outside [0, V) that
+ * is neither ignored nor unused is an error in the data: its loss is NaN and
+ * it has no part in any gradient.
+ *
+ * Gradients, for g[t] = the gradient of the result with respect to loss_t:
+ *     dz = g ((1 + 2 z_loss lse) exp(z - lse) - q)
+ *     dH = scale * dz W,  dW = scale * dz^T H
+ * in H's and W's type, each sum held in float32 and rounded once; dz itself is
+ * rounded to H's type on its way into the two products.  dH and dW are
+ * overwritten.  Results do not depend on timing: every sum has a fixed order.
+ */
+#ifndef TGEMM_LOSS_H
+#define TGEMM_LOSS_H
+
+#include "tgemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define TGEMM_DISTILL_MAX_K 256
+
+/* Options of both losses; NULL means the defaults.  Zero-initialise and set
+ * what you need (ignore_index 0 is a vocabulary entry like any other: set it
+ * to -100, the default, or to what your targets use). */
+typedef struct tgemm_loss_options {
+  float scale;           /* factor of the logits, finite, >= 0; 0 means 1 */
+  float label_smoothing; /* eps in [0, 1]; cross entropy only */
+  float z_loss;          /* weight of lse^2, finite, >= 0; cross entropy only */
+  int piece;             /* vocabulary entries per piece of the gradient, a
+                            multiple of 256 (0: chosen by the library) */
+  int64_t ignore_index;  /* cross entropy only; default -100 */
+  int wait_timeout_us;   /* bound of every in-kernel wait (0 = 2 s) */
+  int reserved[3];       /* must be 0 */
+} tgemm_loss_options;
+
+/* Bytes of workspace a call needs: device memory owned by the caller, 256-byte
+ * aligned, no initialisation needed, contents unspecified afterwards.  Calls
+ * that may run at the same time must not share one.  backward: 0 for the
+ * forward calls, 1 for the backward calls; K: 0 for the cross entropy.  W and
+ * ldw tell whether the weight's rows are 16-byte aligned (pieces of it are
+ * copied to an aligned pitch when they are not).  Needs no GPU. */
+TGEMM_API int tgemm_loss_workspace_size(int backward, int64_t T, int64_t V, int64_t D, int64_t K,
+               const void* W, int64_t ldw, int dtype, const tgemm_loss_options* opts, size_t* bytes);
+
+/*
+ * Cross entropy, forward: loss[T] and lse[T] (lse is what the backward call
+ * takes; it may be used as is for scoring).  dtype: TGEMM_BF16, TGEMM_F16
+ * (tensor cores) or TGEMM_F32 (CUDA cores).  targets: T int64 on the device.
+ *
+ * Errors: TGEMM_ERR_INVALID_VALUE for T < 0, V < 1, D < 1, a short leading
+ * dimension, a null pointer with T > 0, a bad option, a workspace that is
+ * misaligned or smaller than tgemm_loss_workspace_size;
+ * TGEMM_ERR_UNSUPPORTED_DTYPE; TGEMM_ERR_MISALIGNED for a pointer not aligned
+ * to its element; TGEMM_ERR_ALIAS when an output overlaps an input, another
+ * output or the workspace; TGEMM_ERR_TOO_LARGE for T, V, D or a leading
+ * dimension >= 2^31, or K > TGEMM_DISTILL_MAX_K.  They are returned before any
+ * CUDA call.  T == 0: the forward calls do nothing, the backward calls zero dW.
+ */
+TGEMM_API int tgemm_xent_forward(int64_t T, int64_t V, int64_t D,
+               const void* H, int64_t ldh, const void* W, int64_t ldw,
+               const int64_t* targets, int dtype, const tgemm_loss_options* opts,
+               float* loss, float* lse,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Cross entropy, backward.  lse: the forward call's.  grad: T float32, the
+ * gradient of the result with respect to each loss (only rows that count are
+ * read).  dH (T x D, lddh >= D) and dW (V x D, lddw >= D): either may be NULL
+ * when it is not wanted. */
+TGEMM_API int tgemm_xent_backward(int64_t T, int64_t V, int64_t D,
+               const void* H, int64_t ldh, const void* W, int64_t ldw,
+               const int64_t* targets, const float* lse, const float* grad,
+               int dtype, const tgemm_loss_options* opts,
+               void* dH, int64_t lddh, void* dW, int64_t lddw,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Distillation, forward.  ids: T x K int64, row pitch ld_ids >= K; logits:
+ * T x K float32, row pitch ld_logits >= K.  K >= 1. */
+TGEMM_API int tgemm_distill_forward(int64_t T, int64_t V, int64_t D, int64_t K,
+               const void* H, int64_t ldh, const void* W, int64_t ldw,
+               const int64_t* ids, int64_t ld_ids, const float* logits, int64_t ld_logits,
+               int dtype, const tgemm_loss_options* opts,
+               float* loss, float* lse,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Distillation, backward; lse, grad, dH and dW as in tgemm_xent_backward.  The
+ * teacher's logits get no gradient. */
+TGEMM_API int tgemm_distill_backward(int64_t T, int64_t V, int64_t D, int64_t K,
+               const void* H, int64_t ldh, const void* W, int64_t ldw,
+               const int64_t* ids, int64_t ld_ids, const float* logits, int64_t ld_logits,
+               const float* lse, const float* grad,
+               int dtype, const tgemm_loss_options* opts,
+               void* dH, int64_t lddh, void* dW, int64_t lddw,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TGEMM_LOSS_H */

@@ -294,3 +294,9 @@ def matmul(a, b, out=None, out_dtype=None, options=None, stream=None):
     if st != OK:
         raise TgemmError(st, "tgemm_gemm_ex")
     return out
+
+
+# vocabulary-head losses (include/tgemm_loss.h)
+from .loss import (DISTILL_MAX_K, LOSS_EXPORTS, LossOptions, distill_backward, distill_forward,  # noqa: E402
+                   linear_cross_entropy, linear_cross_entropy_backward, linear_distillation,
+                   linear_distillation_backward, loss_workspace_size, xent_backward, xent_forward)

@@ -21,7 +21,7 @@ LIBRARY = os.path.join(HERE, "libtgemm.so")
 # the FP32 FMA-throughput probe the benchmark uses for the SIMT roofline (not part of libtgemm.so)
 PROBE_SOURCE = os.path.join(CSRC, "probe", "fp32_peak.cu")
 PROBE_LIBRARY = os.path.join(HERE, "libtgemm_probe.so")
-HEADER = os.path.join(ROOT, "include", "tgemm.h")
+HEADERS = [os.path.join(ROOT, "include", name) for name in ("tgemm.h", "tgemm_loss.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 NVCC_FLAGS = [
@@ -48,7 +48,7 @@ def sources() -> list[str]:
 def inputs() -> list[str]:
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
         sorted(glob.glob(os.path.join(CSRC, "*.h"))) + sorted(glob.glob(os.path.join(CSRC, "*.inc"))) + \
-        [HEADER, os.path.abspath(__file__)]
+        HEADERS + [os.path.abspath(__file__)]
 
 
 def stale() -> bool:

@@ -1,0 +1,579 @@
+// C ABI of the vocabulary-head losses (include/tgemm_loss.h): argument checks,
+// workspace layout, the pieces of the vocabulary and the order of launches.
+//
+// Forward:  [teacher lists]  gather  STATS (one launch over the vocabulary)  combine
+// Backward: [teacher lists]  gather  { DZ  DH  DW } per piece  last step of dH
+// (loss_rows.cu and loss_gemm.cu hold the kernels.)  A weight whose rows are
+// not 16-byte aligned is copied to an aligned pitch piece by piece.  fp32 runs
+// the same steps with the library's CUDA-core product on pieces of logits.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "../../include/tgemm_loss.h"
+#include "loss_internal.h"
+
+namespace tgemm {
+
+cudaError_t launch_repack(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int rows, int cols,
+                          int src_granule, int sms, cudaStream_t stream);
+
+namespace {
+
+constexpr double kLog2e = 1.4426950408889634;
+constexpr int64_t kMaxExtent = int64_t(1) << 31;
+// CTA pairs the layout is planned for (a GB300's 152 SMs); the layout must not
+// depend on the device, so that its size can be asked for without one.
+constexpr int kPlanPairs = 76;
+// Bytes of one piece of dz (16-bit) or of logits (fp32), and of a piece of W
+// copied to an aligned pitch.  A piece twice the size of L2 already runs tens
+// of rounds of tiles per product, so a larger one would gain nothing.
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+constexpr float kRangeF16 = 16384.0f;  // |dz| <= 2: fp16's largest value is 65504, its small normals reach 2^-14
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Call {
+  bool backward = false, distill = false;
+  int64_t T = 0, V = 0, D = 0, K = 1;
+  const void* H = nullptr;
+  int64_t ldh = 0;
+  const void* W = nullptr;
+  int64_t ldw = 0;
+  const int64_t* ids = nullptr;  // targets, or the teacher's entries
+  int64_t ld_ids = 1;
+  const float* logits = nullptr;
+  int64_t ld_logits = 0;
+  int dtype = 0;
+  const tgemm_loss_options* opts = nullptr;
+  float* loss = nullptr;
+  float* lse_out = nullptr;
+  const float* lse = nullptr;
+  const float* grad = nullptr;
+  void* dH = nullptr;
+  int64_t lddh = 0;
+  void* dW = nullptr;
+  int64_t lddw = 0;
+  void* workspace = nullptr;
+  size_t workspace_bytes = 0;
+  cudaStream_t stream = nullptr;
+};
+
+// Byte offsets into the workspace; every part starts on a 256-byte boundary.
+struct Layout {
+  int es = 2;
+  bool pack = false;           // W is copied to an aligned pitch, piece by piece
+  int64_t piece = 0, pieces = 1;
+  int64_t ldh = 0, ldw_p = 0, ldz = 0, ld_acc = 0;
+  int splits = 1, k_per_split = 0;
+  int64_t count = 0, source = 0, place = 0, ids = 0, q = 0, own = 0, flags = 0, coef = 0, h = 0;
+  int64_t ms = 0, dot = 0, z = 0, zt = 0, w = 0, wt = 0, acc = 0;
+  int64_t tiles = 0;           // statistics per row
+  int64_t total = 0;
+};
+
+// Splits of dH's long k axis (the piece's entries): with few tiles of dH the
+// pairs would idle, so each tile's k range is cut until the rounds of the
+// persistent grid balance; the splits are joined in order by the last step.
+void plan_splits(int64_t T, int64_t D, int64_t kb, Layout& l) {
+  const int64_t tiles = ceil_div(T, kHeadTile) * ceil_div(D, kHeadTile);
+  int64_t best = 1;
+  double best_cost = static_cast<double>(ceil_div(tiles, kPlanPairs) * kb);
+  for (int64_t s = 2; s <= std::min<int64_t>(32, kb / 8); ++s) {
+    if (s * T * l.ld_acc * 4 > kPieceBytes) break;
+    const double cost = static_cast<double>(ceil_div(tiles * s, kPlanPairs) * ceil_div(kb, s));
+    if (cost < 0.92 * best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  l.k_per_split = static_cast<int>(ceil_div(kb, best));
+  l.splits = static_cast<int>(ceil_div(kb, l.k_per_split));
+}
+
+Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bool distill, const void* W, int64_t ldw,
+                   int dtype, int64_t piece_opt) {
+  Layout l;
+  const bool f32 = dtype == TGEMM_F32;
+  l.es = f32 ? 4 : 2;
+  l.ldh = round_up(D, 16 / l.es);
+  l.pack = !f32 && host_granule(W, ldw, 2) < 16;
+  l.ldw_p = round_up(D, 8);
+  l.ld_acc = round_up(D, 4);
+  const int64_t whole = round_up(V, kHeadTile);
+  if (piece_opt > 0) {
+    l.piece = std::min(piece_opt, whole);
+  } else if (!backward && !f32 && !l.pack) {
+    l.piece = whole;
+  } else {
+    int64_t per = 0;  // bytes per entry of a piece
+    if (f32 || backward) per = std::max<int64_t>(per, T * l.es);
+    if (l.pack) per = std::max<int64_t>(per, l.ldw_p * 2);
+    if (f32) per = std::max<int64_t>(per, D * 4);
+    const int64_t fit = std::max<int64_t>(2048, kPieceBytes / std::max<int64_t>(1, per) / kHeadTile * kHeadTile);
+    l.piece = std::min(fit, whole);
+    l.piece = round_up(ceil_div(V, ceil_div(V, l.piece)), kHeadTile);
+  }
+  l.pieces = ceil_div(V, l.piece);
+  l.ldz = l.piece;
+  int64_t at = 0;
+  const auto take = [&at](int64_t bytes) {
+    const int64_t here = at;
+    at += round_up(std::max<int64_t>(bytes, 1), 256);
+    return here;
+  };
+  l.count = take(256);
+  l.source = take(T * 4);
+  l.place = take(T * 4);
+  l.ids = take(T * K * 4);
+  l.q = take(T * K * 4);
+  l.own = take(distill ? T * 4 : 0);
+  l.flags = take(distill ? T : 0);
+  l.coef = take(backward ? T * 16 : 0);
+  l.h = take(T * l.ldh * l.es);
+  l.tiles = f32 ? l.pieces : ceil_div(V, kHeadTile);
+  if (!backward) {
+    l.ms = take(l.tiles * T * 8);
+    l.dot = take(l.tiles * T * 4);
+  }
+  if (f32 || backward) l.z = take(T * l.ldz * l.es);
+  if (l.pack) l.w = take(l.piece * l.ldw_p * 2);
+  if (f32) l.wt = take(l.piece * D * 4);
+  if (f32 && backward) l.zt = take(l.piece * round_up(T, 4) * 4);
+  if (backward) {
+    if (!f32) plan_splits(T, D, ceil_div(std::min(l.piece, V), kTileK), l);
+    l.acc = take(l.splits * T * l.ld_acc * 4);
+  }
+  l.total = at;
+  return l;
+}
+
+int check_options(const tgemm_loss_options* o, bool distill) {
+  if (!o) return TGEMM_OK;
+  if (!std::isfinite(o->scale) || o->scale < 0.0f) return TGEMM_ERR_INVALID_VALUE;
+  if (!(o->label_smoothing >= 0.0f && o->label_smoothing <= 1.0f)) return TGEMM_ERR_INVALID_VALUE;
+  if (!std::isfinite(o->z_loss) || o->z_loss < 0.0f) return TGEMM_ERR_INVALID_VALUE;
+  if (distill && (o->label_smoothing != 0.0f || o->z_loss != 0.0f)) return TGEMM_ERR_INVALID_VALUE;
+  if (o->piece < 0 || o->piece % kHeadTile != 0 || o->wait_timeout_us < 0) return TGEMM_ERR_INVALID_VALUE;
+  for (int r : o->reserved)
+    if (r != 0) return TGEMM_ERR_INVALID_VALUE;
+  return TGEMM_OK;
+}
+
+int check_shape(int64_t T, int64_t V, int64_t D, int64_t K, bool distill, int dtype, const tgemm_loss_options* opts) {
+  if (T < 0 || V < 1 || D < 1 || (distill && K < 1)) return TGEMM_ERR_INVALID_VALUE;
+  if (dtype != TGEMM_F32 && dtype != TGEMM_F16 && dtype != TGEMM_BF16) return TGEMM_ERR_UNSUPPORTED_DTYPE;
+  const int st = check_options(opts, distill);
+  if (st != TGEMM_OK) return st;
+  // the last tile's end must stay an int, and a transpose's grid limits fp32 rows
+  if (T >= kMaxExtent - kHeadTile || V >= kMaxExtent - kHeadTile || D >= kMaxExtent - kHeadTile ||
+      (distill && K > TGEMM_DISTILL_MAX_K) || (dtype == TGEMM_F32 && T > int64_t(65535) * 64))
+    return TGEMM_ERR_TOO_LARGE;
+  return TGEMM_OK;
+}
+
+struct Span {
+  const void* p;
+  uint64_t bytes;
+  int align;
+};
+Span span(const void* p, int64_t rows, int64_t cols, int64_t ld, int es) {
+  return {p, rows > 0 ? static_cast<uint64_t>((rows - 1) * ld + cols) * es : 0, es};
+}
+
+int check_call(const Call& c) {
+  int st = check_shape(c.T, c.V, c.D, c.K, c.distill, c.dtype, c.opts);
+  if (st != TGEMM_OK) return st;
+  if (c.ldh < c.D || c.ldw < c.D || c.ld_ids < c.K || (c.distill && c.ld_logits < c.K) || (c.dH && c.lddh < c.D) ||
+      (c.dW && c.lddw < c.D))
+    return TGEMM_ERR_INVALID_VALUE;
+  for (int64_t ld : {c.ldh, c.ldw, c.ld_ids, c.ld_logits, c.lddh, c.lddw})
+    if (ld >= kMaxExtent) return TGEMM_ERR_TOO_LARGE;
+  if (c.backward && !c.dH && !c.dW) return TGEMM_OK;
+  const int es = c.dtype == TGEMM_F32 ? 4 : 2;
+  if (c.T > 0) {
+    if (!c.H || !c.W || !c.ids || (c.distill && !c.logits)) return TGEMM_ERR_INVALID_VALUE;
+    if (c.backward ? (!c.lse || !c.grad) : (!c.loss || !c.lse_out)) return TGEMM_ERR_INVALID_VALUE;
+  }
+  const Span in[] = {span(c.H, c.T, c.D, c.ldh, es),       span(c.W, c.T > 0 ? c.V : 0, c.D, c.ldw, es),
+                     span(c.ids, c.T, c.K, c.ld_ids, 8),   span(c.logits, c.distill ? c.T : 0, c.K, c.ld_logits, 4),
+                     span(c.lse, c.T, 1, 1, 4),            span(c.grad, c.T, 1, 1, 4)};
+  const Span out[] = {span(c.loss, c.T, 1, 1, 4), span(c.lse_out, c.T, 1, 1, 4),
+                      span(c.dH, c.dH ? c.T : 0, c.D, c.lddh, es), span(c.dW, c.dW ? c.V : 0, c.D, c.lddw, es),
+                      Span{c.workspace, c.workspace_bytes, 1}};
+  for (const Span& s : in)
+    if (s.p && s.bytes && reinterpret_cast<uint64_t>(s.p) % s.align) return TGEMM_ERR_MISALIGNED;
+  for (const Span& s : out)
+    if (s.p && s.bytes && reinterpret_cast<uint64_t>(s.p) % s.align) return TGEMM_ERR_MISALIGNED;
+  const auto meet = [](const Span& a, const Span& b) {
+    const uint64_t x = reinterpret_cast<uint64_t>(a.p), y = reinterpret_cast<uint64_t>(b.p);
+    return a.p && b.p && a.bytes && b.bytes && host_ranges_overlap(x, x + a.bytes, y, y + b.bytes);
+  };
+  constexpr int n_out = sizeof out / sizeof out[0];
+  for (int i = 0; i < n_out; ++i) {
+    for (const Span& s : in)
+      if (meet(out[i], s)) return TGEMM_ERR_ALIAS;
+    for (int j = i + 1; j < n_out; ++j)
+      if (meet(out[i], out[j])) return TGEMM_ERR_ALIAS;
+  }
+  return TGEMM_OK;
+}
+
+#define TGEMM_TRY(expr)                        \
+  do {                                         \
+    const int st_ = (expr);                    \
+    if (st_ != TGEMM_OK) return st_;           \
+  } while (0)
+#define TGEMM_CUDA(expr, what)                              \
+  do {                                                      \
+    const cudaError_t e_ = (expr);                          \
+    if (e_ != cudaSuccess) return host_cuda_fail(e_, what); \
+  } while (0)
+
+int run_f32(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float scale, float flat, float z_loss) {
+  float* Z = reinterpret_cast<float*>(ws + l.z);
+  float* wt = reinterpret_cast<float*>(ws + l.wt);
+  float* zt = reinterpret_cast<float*>(ws + l.zt);
+  float* acc = reinterpret_cast<float*>(ws + l.acc);
+  float2* ms = reinterpret_cast<float2*>(ws + l.ms);
+  float* dot = reinterpret_cast<float*>(ws + l.dot);
+  const float* h = static_cast<const float*>(rows.h);
+  const float* W = static_cast<const float*>(c.W);
+  const int T = static_cast<int>(c.T), D = static_cast<int>(c.D), K = static_cast<int>(c.K);
+  const float k2 = static_cast<float>(scale * kLog2e);
+  const int64_t ldzt = round_up(c.T, 4);
+  for (int64_t i = 0; i < l.pieces; ++i) {
+    const int64_t v0 = i * l.piece, n = std::min(l.piece, c.V - v0);
+    const float* w = W + v0 * c.ldw;
+    const bool vec = reinterpret_cast<uint64_t>(w) % 16 == 0 && c.ldw % 4 == 0 && l.piece % 4 == 0;
+    TGEMM_CUDA(launch_transpose(w, c.ldw, wt, l.piece, static_cast<int>(n), D, 4, vec, c.stream), "transpose launch");
+    TGEMM_TRY(host_gemm_f32(c.T, n, c.D, h, l.ldh, wt, l.piece, Z, l.ldz, 0.0f, c.stream));
+    if (!c.backward) {
+      TGEMM_CUDA(launch_stats_f32(Z, l.ldz, static_cast<int>(n), static_cast<int>(v0), T, K, k2, flat, rows,
+                                  ms + i * c.T, dot + i * c.T, c.stream),
+                 "statistics launch");
+      continue;
+    }
+    TGEMM_CUDA(launch_dz_f32(Z, l.ldz, static_cast<int>(n), static_cast<int>(v0), T, K, scale, flat, rows, c.stream),
+               "gradient launch");
+    if (c.dH) TGEMM_TRY(host_gemm_f32(c.T, c.D, n, Z, l.ldz, w, c.ldw, acc, l.ld_acc, i ? 1.0f : 0.0f, c.stream));
+    if (c.dW) {
+      TGEMM_CUDA(launch_transpose(Z, l.ldz, zt, ldzt, T, static_cast<int>(n), 4, true, c.stream), "transpose launch");
+      TGEMM_TRY(host_gemm_f32(n, c.D, c.T, zt, ldzt, h, l.ldh, static_cast<float*>(c.dW) + v0 * c.lddw, c.lddw, 0.0f,
+                              c.stream));
+    }
+  }
+  if (!c.backward)
+    TGEMM_CUDA(launch_combine(ms, dot, static_cast<int>(l.tiles), T, scale, z_loss, rows, c.loss, c.lse_out, c.stream),
+               "combine launch");
+  else if (c.dH)
+    TGEMM_CUDA(launch_finish_dh(acc, l.ld_acc, 0, 1, T, D, rows, 2, c.dH, c.lddh, c.stream), "dH launch");
+  return TGEMM_OK;
+}
+
+int run_tc(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float scale, float flat, float z_loss,
+           int sms, int pairs, unsigned int* status) {
+  if (pairs < 1) return host_cuda_fail(cudaErrorLaunchOutOfResources, "CTA pairs");
+  const int type = c.dtype == TGEMM_BF16 ? 0 : 1;
+  CUtensorMap m_h, m_w, m_wn, m_z, m_zk, m_hn, m_acc, m_dw, m_zs;
+  for (CUtensorMap* m : {&m_h, &m_w, &m_wn, &m_z, &m_zk, &m_hn, &m_acc, &m_dw, &m_zs}) std::memset(m, 0, sizeof *m);
+  HeadArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.count = rows.count;
+  a.T = static_cast<int>(c.T);
+  a.V = static_cast<int>(c.V);
+  a.K = static_cast<int>(c.K);
+  a.D = static_cast<int>(c.D);
+  a.bf16 = type == 0;
+  a.k2 = static_cast<float>(scale * kLog2e);
+  a.flat = flat;
+  a.group_m = 8;
+  a.source = rows.source;
+  a.ids = rows.ids;
+  a.q = rows.q;
+  a.ms = reinterpret_cast<float2*>(ws + l.ms);
+  a.dot = reinterpret_cast<float*>(ws + l.dot);
+  a.coef = rows.coef;
+  a.factor = rows.factor;
+  const int to_us = (c.opts && c.opts->wait_timeout_us) ? c.opts->wait_timeout_us : 2000000;
+  a.timeout_ns = static_cast<unsigned long long>(to_us) * 1000ull;
+  a.status = status;
+  const int64_t m_tiles = ceil_div(c.T, kHeadTile), d_tiles = ceil_div(c.D, kHeadTile);
+  const int d_blocks = static_cast<int>(ceil_div(c.D, kTileK));
+  TGEMM_TRY(host_map_2d(&m_h, type, rows.h, c.D, c.T, l.ldh * 2, kTileK, kTileM));
+  void* z = ws + l.z;
+  if (c.backward) {
+    TGEMM_TRY(host_map_2d(&m_zs, type, z, l.ldz, c.T, l.ldz * 2, 64, 32));
+    if (c.dH) {
+      TGEMM_TRY(host_map_2d(&m_z, type, z, l.ldz, c.T, l.ldz * 2, kTileK, kTileM));
+      TGEMM_TRY(host_map_3d(&m_acc, 2, ws + l.acc, c.D, c.T, l.splits, l.ld_acc * 4, c.T * l.ld_acc * 4, 32, 32));
+    }
+    if (c.dW) {
+      TGEMM_TRY(host_map_2d(&m_zk, type, z, l.ldz, c.T, l.ldz * 2, 64, kTileK));
+      TGEMM_TRY(host_map_2d(&m_hn, type, rows.h, c.D, c.T, l.ldh * 2, 64, kTileK));
+      a.store_granule = host_granule(c.dW, c.lddw, 2);
+      if (a.store_granule == 16) a.store_granule = 0;
+      if (a.store_granule == 0) TGEMM_TRY(host_map_2d(&m_dw, type, c.dW, c.D, c.V, c.lddw * 2, 64, 32));
+    }
+  }
+  const auto grid = [pairs](int64_t units) { return static_cast<int>(std::min<int64_t>(pairs, units)); };
+  int launches = 0;
+  for (int64_t i = 0; i < l.pieces; ++i) {
+    const int64_t v0 = i * l.piece, n = std::min(l.piece, c.V - v0);
+    const void* w = c.W;
+    int64_t ldw = c.ldw, w_rows = c.V;
+    a.b_row0 = static_cast<int>(v0);
+    if (l.pack) {
+      w = ws + l.w;
+      const char* src = static_cast<const char*>(c.W) + v0 * c.ldw * 2;
+      TGEMM_CUDA(launch_repack(src, c.ldw, ws + l.w, l.ldw_p, static_cast<int>(n), a.D, host_granule(src, c.ldw, 2), sms,
+                               c.stream),
+                 "repack launch");
+      ldw = l.ldw_p;
+      w_rows = n;  // the copy's rows past the piece hold an earlier piece
+      a.b_row0 = 0;
+    }
+    a.cols = static_cast<int>(n);
+    a.col0 = static_cast<int>(v0);
+    a.tile0 = static_cast<int>(v0 / kHeadTile);
+    a.k_blocks = d_blocks;
+    TGEMM_TRY(host_map_2d(&m_w, type, w, c.D, w_rows, ldw * 2, kTileK, kTileM));
+    const int64_t tiles = m_tiles * ceil_div(n, kHeadTile);
+    ++launches;
+    if (!c.backward) {
+      TGEMM_CUDA(launch_head(HEAD_STATS, m_h, m_w, m_w, a, grid(tiles), c.stream), "head launch");
+      continue;
+    }
+    TGEMM_CUDA(launch_head(HEAD_DZ, m_h, m_w, m_zs, a, grid(tiles), c.stream), "head launch");
+    if (c.dH) {
+      TGEMM_TRY(host_map_2d(&m_wn, type, w, c.D, w_rows, ldw * 2, 64, kTileK));
+      HeadArgs b = a;
+      b.k_blocks = static_cast<int>(ceil_div(n, kTileK));
+      b.splits = l.splits;
+      b.k_per_split = l.k_per_split;
+      b.reduce = i > 0;
+      TGEMM_CUDA(launch_head(HEAD_DH, m_z, m_wn, m_acc, b, grid(m_tiles * d_tiles * l.splits), c.stream), "head launch");
+      ++launches;
+    }
+    if (c.dW) {
+      HeadArgs b = a;
+      b.out = c.dW;
+      b.ld_out = c.lddw;
+      b.out_row0 = static_cast<int>(v0);
+      TGEMM_CUDA(launch_head(HEAD_DW, m_zk, m_hn, m_dw, b, grid(ceil_div(n, kHeadTile) * d_tiles), c.stream),
+                 "head launch");
+      ++launches;
+    }
+  }
+  host_count_launches(launches);
+  if (!c.backward)
+    TGEMM_CUDA(launch_combine(a.ms, a.dot, static_cast<int>(l.tiles), a.T, scale, z_loss, rows, c.loss, c.lse_out,
+                              c.stream),
+               "combine launch");
+  else if (c.dH)
+    TGEMM_CUDA(launch_finish_dh(reinterpret_cast<float*>(ws + l.acc), l.ld_acc, c.T * l.ld_acc, l.splits, a.T, a.D, rows,
+                                type, c.dH, c.lddh, c.stream),
+               "dH launch");
+  return TGEMM_OK;
+}
+
+int run_loss(const Call& c) {
+  TGEMM_TRY(check_call(c));
+  if (c.backward ? (!c.dH && !c.dW) : c.T == 0) return TGEMM_OK;
+  const int es = c.dtype == TGEMM_F32 ? 4 : 2;
+  const float scale = c.opts && c.opts->scale != 0.0f ? c.opts->scale : 1.0f;
+  const float smoothing = c.opts ? c.opts->label_smoothing : 0.0f;
+  const float z_loss = c.opts ? c.opts->z_loss : 0.0f;
+  const float flat = smoothing / static_cast<float>(c.V);
+  Layout l;
+  if (c.T > 0) {
+    l = plan_layout(c.backward, c.T, c.V, c.D, c.K, c.distill, c.W, c.ldw, c.dtype, c.opts ? c.opts->piece : 0);
+    if (!c.workspace || reinterpret_cast<uint64_t>(c.workspace) % 256 ||
+        c.workspace_bytes < static_cast<size_t>(l.total))
+      return TGEMM_ERR_INVALID_VALUE;
+  }
+  int sms = 0, pairs = 0;
+  unsigned int* status = nullptr;
+  TGEMM_TRY(host_device(&sms, &pairs, &status));
+  if (c.T == 0) {
+    if (c.dW) TGEMM_CUDA(launch_zero_fill(c.dW, c.V, c.D, c.lddw, es, c.stream), "zero-fill launch");
+    return TGEMM_OK;
+  }
+  char* ws = static_cast<char*>(c.workspace);
+  GatherArgs g;
+  std::memset(&g, 0, sizeof g);
+  g.rows.count = reinterpret_cast<int*>(ws + l.count);
+  g.rows.factor = reinterpret_cast<float*>(ws + l.count) + 1;
+  g.rows.source = reinterpret_cast<int*>(ws + l.source);
+  g.rows.place = reinterpret_cast<int*>(ws + l.place);
+  g.rows.ids = reinterpret_cast<int*>(ws + l.ids);
+  g.rows.q = reinterpret_cast<float*>(ws + l.q);
+  g.rows.own = c.distill ? reinterpret_cast<float*>(ws + l.own) : nullptr;
+  g.rows.flags = c.distill ? reinterpret_cast<unsigned char*>(ws + l.flags) : nullptr;
+  g.rows.coef = c.backward ? reinterpret_cast<float4*>(ws + l.coef) : nullptr;
+  g.rows.h = ws + l.h;
+  g.rows.ldh = l.ldh;
+  g.T = static_cast<int>(c.T);
+  g.V = static_cast<int>(c.V);
+  g.D = static_cast<int>(c.D);
+  g.K = static_cast<int>(c.K);
+  g.es = es;
+  g.H = c.H;
+  g.ldh = c.ldh;
+  g.granule = host_granule(c.H, c.ldh, es);
+  g.targets = c.distill ? nullptr : c.ids;
+  g.ignore_index = c.opts ? c.opts->ignore_index : -100;
+  g.smoothing = smoothing;
+  g.z_loss = z_loss;
+  g.scale = scale;
+  g.range = c.dtype == TGEMM_F32 ? 0.0f : (c.dtype == TGEMM_F16 ? kRangeF16 : 1.0f);
+  g.zero_rows = c.dtype == TGEMM_F32;
+  g.lse = c.lse;
+  g.grad = c.grad;
+  g.loss_out = c.loss;
+  g.lse_out = c.lse_out;
+  if (c.distill)
+    TGEMM_CUDA(launch_distill_lists(c.ids, c.ld_ids, c.logits, c.ld_logits, g.T, g.V, g.K, scale, g.rows, c.stream),
+               "teacher list launch");
+  TGEMM_CUDA(launch_gather(g, sms, c.stream), "gather launch");
+  if (c.dtype == TGEMM_F32) return run_f32(c, l, g.rows, ws, scale, flat, z_loss);
+  return run_tc(c, l, g.rows, ws, scale, flat, z_loss, sms, pairs, status);
+}
+
+}  // namespace
+}  // namespace tgemm
+
+extern "C" {
+
+int tgemm_loss_workspace_size(int backward, int64_t T, int64_t V, int64_t D, int64_t K, const void* W, int64_t ldw,
+                              int dtype, const tgemm_loss_options* opts, size_t* bytes) {
+  if (!bytes || (backward != 0 && backward != 1) || K < 0) return TGEMM_ERR_INVALID_VALUE;
+  const bool distill = K > 0;
+  const int st = tgemm::check_shape(T, V, D, distill ? K : 1, distill, dtype, opts);
+  if (st != TGEMM_OK) return st;
+  if (ldw < D) return TGEMM_ERR_INVALID_VALUE;
+  if (ldw >= tgemm::kMaxExtent) return TGEMM_ERR_TOO_LARGE;
+  *bytes = T == 0 ? 0
+                  : static_cast<size_t>(tgemm::plan_layout(backward != 0, T, V, D, distill ? K : 1, distill, W, ldw,
+                                                           dtype, opts ? opts->piece : 0)
+                                            .total);
+  return TGEMM_OK;
+}
+
+int tgemm_xent_forward(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh, const void* W, int64_t ldw,
+                       const int64_t* targets, int dtype, const tgemm_loss_options* opts, float* loss, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  tgemm::Call c;
+  c.T = T;
+  c.V = V;
+  c.D = D;
+  c.H = H;
+  c.ldh = ldh;
+  c.W = W;
+  c.ldw = ldw;
+  c.ids = targets;
+  c.dtype = dtype;
+  c.opts = opts;
+  c.loss = loss;
+  c.lse_out = lse;
+  c.workspace = workspace;
+  c.workspace_bytes = workspace_bytes;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return tgemm::run_loss(c);
+}
+
+int tgemm_xent_backward(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh, const void* W, int64_t ldw,
+                        const int64_t* targets, const float* lse, const float* grad, int dtype,
+                        const tgemm_loss_options* opts, void* dH, int64_t lddh, void* dW, int64_t lddw, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  tgemm::Call c;
+  c.backward = true;
+  c.T = T;
+  c.V = V;
+  c.D = D;
+  c.H = H;
+  c.ldh = ldh;
+  c.W = W;
+  c.ldw = ldw;
+  c.ids = targets;
+  c.lse = lse;
+  c.grad = grad;
+  c.dtype = dtype;
+  c.opts = opts;
+  c.dH = dH;
+  c.lddh = lddh;
+  c.dW = dW;
+  c.lddw = lddw;
+  c.workspace = workspace;
+  c.workspace_bytes = workspace_bytes;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return tgemm::run_loss(c);
+}
+
+int tgemm_distill_forward(int64_t T, int64_t V, int64_t D, int64_t K, const void* H, int64_t ldh, const void* W,
+                          int64_t ldw, const int64_t* ids, int64_t ld_ids, const float* logits, int64_t ld_logits,
+                          int dtype, const tgemm_loss_options* opts, float* loss, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  tgemm::Call c;
+  c.distill = true;
+  c.T = T;
+  c.V = V;
+  c.D = D;
+  c.K = K;
+  c.H = H;
+  c.ldh = ldh;
+  c.W = W;
+  c.ldw = ldw;
+  c.ids = ids;
+  c.ld_ids = ld_ids;
+  c.logits = logits;
+  c.ld_logits = ld_logits;
+  c.dtype = dtype;
+  c.opts = opts;
+  c.loss = loss;
+  c.lse_out = lse;
+  c.workspace = workspace;
+  c.workspace_bytes = workspace_bytes;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return tgemm::run_loss(c);
+}
+
+int tgemm_distill_backward(int64_t T, int64_t V, int64_t D, int64_t K, const void* H, int64_t ldh, const void* W,
+                           int64_t ldw, const int64_t* ids, int64_t ld_ids, const float* logits, int64_t ld_logits,
+                           const float* lse, const float* grad, int dtype, const tgemm_loss_options* opts, void* dH,
+                           int64_t lddh, void* dW, int64_t lddw, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  tgemm::Call c;
+  c.backward = true;
+  c.distill = true;
+  c.T = T;
+  c.V = V;
+  c.D = D;
+  c.K = K;
+  c.H = H;
+  c.ldh = ldh;
+  c.W = W;
+  c.ldw = ldw;
+  c.ids = ids;
+  c.ld_ids = ld_ids;
+  c.logits = logits;
+  c.ld_logits = ld_logits;
+  c.lse = lse;
+  c.grad = grad;
+  c.dtype = dtype;
+  c.opts = opts;
+  c.dH = dH;
+  c.lddh = lddh;
+  c.dW = dW;
+  c.lddw = lddw;
+  c.workspace = workspace;
+  c.workspace_bytes = workspace_bytes;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return tgemm::run_loss(c);
+}
+
+}  // extern "C"

@@ -1,0 +1,570 @@
+// Tensor-core products of the vocabulary-head losses, on CTA pairs: one 256 x
+// 256 tile per pair, tcgen05.mma.cta_group::2 (M = 256), fp32 accumulators in
+// tensor memory, two of them, so a tile's epilogue runs under the next tile's
+// MMAs.  Four products share the pipeline and differ in operand layout and
+// epilogue:
+//
+//   STATS  y = k2 H W^T       row max, sum of 2^(y - max), sum q z of the tile
+//   DZ     the same product   dz = c_p 2^(y - lse2) - c_q q, 16-bit, stored
+//   DH     dz . W             fp32 sums, stored or added (bulk-tensor reduce)
+//   DW     dz^T . H           times a factor, rounded once, stored
+//
+// with k2 = scale log2(e), so that one fused multiply-add and one 2^x serve
+// each logit.  H and W are read K-major (their rows are the k axis) by STATS
+// and DZ; W as the N-major B of DH; dz as the M-major A and H as the N-major B
+// of DW: no operand is ever transposed in memory.
+//
+// Roles (both CTAs unless noted):
+//   warp 0      bulk-tensor producer of this CTA's 128 rows of A and 128
+//               columns of B; completion on the leader CTA's full barrier
+//   warp 1      tensor-memory allocation; MMA issue by one thread of the leader
+//   warps 2..5  epilogue of this CTA's 128 rows, one row per thread
+//
+// The number of gathered rows is known on the device only (rows that do not
+// count are not gathered), so every role derives the tile list from it.  Every
+// wait is bounded (tc_common.cuh).
+#include <atomic>
+#include <climits>
+
+#include "loss_internal.h"
+#include "tc_common.cuh"
+
+namespace tgemm {
+namespace {
+
+constexpr int kSub = kTileM * kTileK * 2;        // 16 KB: one CTA's share of A or B in one stage
+constexpr int kStage = 2 * kSub;
+constexpr bool head_staged(int mode) { return mode != HEAD_STATS; }
+constexpr int head_stages(int mode) {
+  return (kSmemLimit - 1024 - (head_staged(mode) ? kEpiBytes : 0) - kBarrierBytes) / kStage;
+}
+constexpr int head_smem(int mode) {
+  return 1024 + head_stages(mode) * kStage + (head_staged(mode) ? kEpiBytes : 0) + kBarrierBytes;
+}
+constexpr bool a_m_major(int mode) { return mode == HEAD_DW; }
+constexpr bool b_n_major(int mode) { return mode == HEAD_DH || mode == HEAD_DW; }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Adds a shared-memory box to the fp32 tensor at (x, y, z).
+__device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                                  uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+
+// The tile list of one launch, derived from the gathered row count.
+struct Tiles {
+  int m, n, units, k_blocks, group_m;
+};
+
+template <int MODE>
+__device__ __forceinline__ Tiles head_tiles(const HeadArgs& a) {
+  Tiles t;
+  const int rows = max(1, min(*a.count, a.T));
+  t.group_m = a.group_m;
+  if constexpr (MODE == HEAD_DW) {
+    t.m = (a.cols + kHeadTile - 1) / kHeadTile;
+    t.n = (a.D + kHeadTile - 1) / kHeadTile;
+    t.k_blocks = (rows + kTileK - 1) / kTileK;
+  } else {
+    t.m = (rows + kHeadTile - 1) / kHeadTile;
+    t.n = ((MODE == HEAD_DH ? a.D : a.cols) + kHeadTile - 1) / kHeadTile;
+    t.k_blocks = a.k_blocks;
+  }
+  t.units = t.m * t.n * (MODE == HEAD_DH ? a.splits : 1);
+  return t;
+}
+
+struct HeadUnit {
+  int mb, nb, split, lo, hi;
+};
+
+// Unit -> tile and k-stage range: groups of group_m block-rows are walked
+// column by column (as the plain product does), split after split.
+template <int MODE>
+__device__ __forceinline__ HeadUnit head_unit(const HeadArgs& a, const Tiles& t, int u) {
+  HeadUnit w;
+  const int per = t.m * t.n;
+  w.split = MODE == HEAD_DH ? u / per : 0;
+  const int i = MODE == HEAD_DH ? u - w.split * per : u;
+  const int per_group = t.group_m * t.n;
+  const int g = i / per_group;
+  const int first = g * t.group_m;
+  const int gsz = min(t.m - first, t.group_m);
+  const int r = i - g * per_group;
+  w.mb = first + r % gsz;
+  w.nb = r / gsz;
+  w.lo = MODE == HEAD_DH ? min(w.split * a.k_per_split, t.k_blocks) : 0;
+  w.hi = MODE == HEAD_DH ? min(w.lo + a.k_per_split, t.k_blocks) : t.k_blocks;
+  return w;
+}
+
+// A row's list of targets, walked in ascending order as its columns go by.
+struct Walk {
+  const int* ids;
+  const float* q;
+  int pos, K, next;
+  __device__ __forceinline__ void start(const HeadArgs& a, int row, int n, int first) {
+    K = a.K;
+    pos = 0;
+    next = INT_MAX;
+    ids = a.ids;
+    q = a.q;
+    if (row >= n) return;
+    const int64_t at = static_cast<int64_t>(a.source[row]) * K;
+    ids += at;
+    q += at;
+    int len = K;
+    while (len > 0) {  // first place whose id is not below `first`
+      const int half = len >> 1;
+      if (ids[pos + half] < first) {
+        pos += half + 1;
+        len -= half + 1;
+      } else {
+        len = half;
+      }
+    }
+    next = pos < K ? ids[pos] : INT_MAX;
+  }
+  __device__ __forceinline__ float mass() const { return q[pos]; }
+  __device__ __forceinline__ void step() {
+    ++pos;
+    next = pos < K ? ids[pos] : INT_MAX;
+  }
+};
+
+// Statistics of this thread's row over the tile's 256 columns.
+__device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, int nb, const HeadArgs& a) {
+  const int first = a.col0 + nb * kHeadTile;  // vocabulary entry of the tile's first column
+  const int width = min(kHeadTile, a.cols - nb * kHeadTile);
+  Walk walk;
+  walk.start(a, row, n, first);
+  float m = -INFINITY, s = 0.0f, dot = 0.0f, zs = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < kHeadTile / 32; ++c) {
+    if (c * 32 >= width) break;
+    uint32_t raw[32];
+    ptx::tmem_ld_32x32b_x32(tbase + c * 32, raw);
+    ptx::tmem_wait_ld();
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+    const int limit = width - c * 32;
+    if (limit < 32) {  // columns past the piece are no entries
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = i < limit ? v[i] : -INFINITY;
+    }
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
+    const float m_new = fmaxf(m, top);
+    const float ref = m_new == -INFINITY ? 0.0f : m_new;  // nothing but -inf so far: every term is 0
+    const float off = -ref * a.k2;
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) part[i & 3] += exp2_fast(fmaf(v[i], a.k2, off));
+    s = fmaf(s, exp2_fast((m - ref) * a.k2), (part[0] + part[1]) + (part[2] + part[3]));
+    m = m_new;
+    if (a.flat != 0.0f) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) zs += i < limit ? v[i] : 0.0f;
+    }
+    const int base = first + c * 32;
+    while (__any_sync(0xffffffffu, walk.next < base + 32)) {
+      if (walk.next < base + 32) {
+        const int t = walk.next - base;
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z = i == t ? v[i] : z;
+        dot = fmaf(walk.mass(), z, dot);
+        walk.step();
+      }
+    }
+  }
+  if (row < n) {
+    const int64_t at = static_cast<int64_t>(a.tile0 + nb) * a.T + row;
+    a.ms[at] = make_float2(m * a.k2, s);
+    a.dot[at] = fmaf(a.flat, zs, dot);
+  }
+}
+
+// 32 logits of a row -> their gradient.
+__device__ __forceinline__ void gradient_chunk(uint32_t (&raw)[32], int base, int limit, const float4& k,
+                                               const HeadArgs& a, Walk& walk) {
+  const float flat = k.y * a.flat;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float p = exp2_fast(fmaf(__uint_as_float(raw[i]), a.k2, -k.z));
+    raw[i] = __float_as_uint(fmaf(k.x, p, -flat));
+  }
+  while (__any_sync(0xffffffffu, walk.next < base + 32)) {
+    if (walk.next < base + 32) {
+      const int t = walk.next - base;
+      const float d = k.y * walk.mass();
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        raw[i] = i == t ? __float_as_uint(__uint_as_float(raw[i]) - d) : raw[i];
+      walk.step();
+    }
+  }
+  if (limit < 32) {  // columns past the piece contribute nothing to the products that follow
+#pragma unroll
+    for (int i = 0; i < 32; ++i) raw[i] = i < limit ? raw[i] : 0u;
+  }
+}
+
+// Next staging buffer of this warp, free to be written.
+__device__ __forceinline__ uint8_t* staging(uint8_t* stage_base, int& sbuf, int lane) {
+  uint8_t* buf = stage_base + sbuf * 4096;
+  sbuf ^= 1;
+  if (lane == 0) ptx::bulk_wait_group_read<1>();
+  __syncwarp();
+  return buf;
+}
+
+__device__ __forceinline__ void stage_row(uint8_t* buf, int lane, const uint32_t (&w)[32]) {
+#pragma unroll
+  for (int ch = 0; ch < 8; ++ch)
+    *reinterpret_cast<uint4*>(buf + sw128_offset(lane, ch * 16)) =
+        make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+}
+
+__device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int nb, const HeadArgs& a,
+                                            const CUtensorMap* mapC, uint8_t* stage_base, int& sbuf, int lane) {
+  const int row = row0 + lane;
+  const int first = a.col0 + nb * kHeadTile;
+  const int width = min(kHeadTile, a.cols - nb * kHeadTile);
+  Walk walk;
+  walk.start(a, row, n, first);
+  const float4 k = row < n ? a.coef[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int fmt = a.bf16 ? OUT_BF16 : OUT_F16;
+#pragma unroll 1
+  for (int c = 0; c < kHeadTile / 64; ++c) {
+    if (c * 64 >= width) break;
+    uint32_t lo[32], hi[32], w[32];
+    ptx::tmem_ld_32x32b_x32(tbase + c * 64, lo);
+    ptx::tmem_ld_32x32b_x32(tbase + c * 64 + 32, hi);
+    ptx::tmem_wait_ld();
+    gradient_chunk(lo, first + c * 64, width - c * 64, k, a, walk);
+    gradient_chunk(hi, first + c * 64 + 32, width - c * 64 - 32, k, a, walk);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      w[i] = pack_pair(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]), fmt);
+      w[16 + i] = pack_pair(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]), fmt);
+    }
+    if (row >= n) {  // rows past the count: zeros, which the products read
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = 0u;
+    }
+    uint8_t* buf = staging(stage_base, sbuf, lane);
+    stage_row(buf, lane, w);
+    if (lane == 0) {
+      if (row0 < a.T) ptx::tma_store_2d(mapC, nb * kHeadTile + c * 64, row0, ptx::smem_u32(buf));
+      ptx::bulk_commit_group();
+    }
+  }
+}
+
+__device__ __forceinline__ void epilogue_dh(uint32_t tbase, int row0, const HeadUnit& u, const HeadArgs& a,
+                                            const CUtensorMap* mapC, uint8_t* stage_base, int& sbuf, int lane) {
+  if (row0 >= a.T) return;
+#pragma unroll 1
+  for (int c = 0; c < kHeadTile / 32; ++c) {
+    const int col = u.nb * kHeadTile + c * 32;
+    if (col >= a.D) break;
+    uint32_t w[32];
+    ptx::tmem_ld_32x32b_x32(tbase + c * 32, w);
+    ptx::tmem_wait_ld();
+    uint8_t* buf = staging(stage_base, sbuf, lane);
+    stage_row(buf, lane, w);
+    if (lane == 0) {
+      if (a.reduce)
+        tma_reduce_add_3d(mapC, col, row0, u.split, ptx::smem_u32(buf));
+      else
+        ptx::tma_store_3d(mapC, col, row0, u.split, ptx::smem_u32(buf));
+      ptx::bulk_commit_group();
+    }
+  }
+}
+
+__device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, const HeadArgs& a,
+                                            const CUtensorMap* mapC, uint8_t* stage_base, int& sbuf, int lane) {
+  if (row0 >= a.cols) return;
+  const float f = *a.factor;
+  const int fmt = a.bf16 ? OUT_BF16 : OUT_F16;
+  const int row = row0 + lane;
+#pragma unroll 1
+  for (int c = 0; c < kHeadTile / 64; ++c) {
+    const int col = nb * kHeadTile + c * 64;
+    if (col >= a.D) break;
+    uint32_t lo[32], hi[32], w[32];
+    ptx::tmem_ld_32x32b_x32(tbase + c * 64, lo);
+    ptx::tmem_ld_32x32b_x32(tbase + c * 64 + 32, hi);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      w[i] = pack_pair(f * __uint_as_float(lo[2 * i]), f * __uint_as_float(lo[2 * i + 1]), fmt);
+      w[16 + i] = pack_pair(f * __uint_as_float(hi[2 * i]), f * __uint_as_float(hi[2 * i + 1]), fmt);
+    }
+    if (a.store_granule == 0) {
+      uint8_t* buf = staging(stage_base, sbuf, lane);
+      stage_row(buf, lane, w);
+      if (lane == 0) {
+        ptx::tma_store_2d(mapC, col, a.out_row0 + row0, ptx::smem_u32(buf));
+        ptx::bulk_commit_group();
+      }
+    } else if (row < a.cols) {
+      uint8_t* dst = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(a.out_row0 + row) * a.ld_out + col) * 2;
+      store_segment(dst, w, min(a.D - col, 64) * 2, a.store_granule, 2);
+    }
+  }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
+    head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                const __grid_constant__ CUtensorMap mapC, const HeadArgs args) {
+  constexpr int STAGES = head_stages(MODE);
+  constexpr int ACC = 256;
+  constexpr uint32_t TMEM_COLS = 512;
+  static_assert(head_smem(MODE) <= kSmemLimit, "shared memory per CTA");
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sC = smem + STAGES * kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sC + (head_staged(MODE) ? kEpiBytes : 0));
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  static_assert((2 * STAGES + 5) * 8 + 8 <= kBarrierBytes, "barrier area");
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int half = static_cast<int>(ptx::cluster_ctarank() & 1u);
+  const bool leader = half == 0;
+  const int worker = blockIdx.x / 2;
+  const int workers = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_u32(&acc_full[b]), 1);
+      ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * kEpiWarps);
+    }
+    ptx::mbar_init(ptx::smem_u32(drain), 1);
+    *abort_flag = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&mapA);
+    ptx::tma_prefetch_desc(&mapB);
+    if (head_staged(MODE)) ptx::tma_prefetch_desc(&mapC);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), TMEM_COLS);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before_sync();
+  ptx::cluster_sync();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const Ctl ctl{abort_flag, args.timeout_ns, args.status};
+  const Tiles tiles = head_tiles<MODE>(args);
+
+  if (warp == 0) {
+    // ------------------------------------------------ bulk-tensor producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, filled = 0, last_parity = 0;
+      bool ok = true;
+      for (int i = worker; ok && i < tiles.units; i += workers) {
+        const HeadUnit u = head_unit<MODE>(args, tiles, i);
+        const int m0 = u.mb * kHeadTile + half * kTileM;
+        const int n0 = u.nb * kHeadTile + half * (kHeadTile / 2);
+        for (int kb = u.lo; kb < u.hi; ++kb) {
+          if (!wait_bounded(ptx::smem_u32(&empty[stage]), phase ^ 1u, ctl, SITE_PRODUCER_EMPTY)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = ptx::smem_u32(&full[stage]);
+          const uint32_t fb = ptx::mapa_shared(fb_local, 0);
+          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2u * kStage);
+          const uint32_t sa = ptx::smem_u32(smem + stage * kStage), sb = sa + kSub;
+          const int k0 = kb * kTileK;  // stages past the k axis load zeros
+          if constexpr (a_m_major(MODE)) {
+            ptx::tma_load_2d_pair(sa, &mapA, m0, k0, fb);
+            ptx::tma_load_2d_pair(sa + 8192, &mapA, m0 + 64, k0, fb);
+          } else {
+            ptx::tma_load_2d_pair(sa, &mapA, k0, m0, fb);
+          }
+          if constexpr (b_n_major(MODE)) {
+            const int kr = k0 + (MODE == HEAD_DH ? args.b_row0 : 0);
+            ptx::tma_load_2d_pair(sb, &mapB, n0, kr, fb);
+            ptx::tma_load_2d_pair(sb + 8192, &mapB, n0 + 64, kr, fb);
+          } else {
+            ptx::tma_load_2d_pair(sb, &mapB, k0, args.b_row0 + n0, fb);
+          }
+          filled |= 1u << stage;
+          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // loads in flight land before shared memory is released (see tc_gemm_2sm.cu)
+      for (int s = 0; s < STAGES; ++s)
+        if ((filled >> s) & 1u) {
+          const uint32_t par = (last_parity >> s) & 1u;
+          wait_teardown(ptx::smem_u32(leader ? &full[s] : &empty[s]), par, ctl, SITE_TEARDOWN);
+        }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------ MMA issuer (leader CTA only)
+    if (leader && lane == 0) {
+      // kind::f16 instruction descriptor: D fp32, A and B format, A M-major
+      // (bit 15), B N-major (bit 16), N >> 3, M >> 4
+      const uint32_t ab = args.bf16 ? 1u : 0u;
+      const uint32_t idesc = (1u << 4) | (ab << 7) | (ab << 10) | (a_m_major(MODE) ? 1u << 15 : 0u) |
+                             (b_n_major(MODE) ? 1u << 16 : 0u) | (static_cast<uint32_t>(kHeadTile >> 3) << 17) |
+                             (static_cast<uint32_t>((2 * kTileM) >> 4) << 24);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int i = worker; ok && i < tiles.units; i += workers) {
+        const HeadUnit u = head_unit<MODE>(args, tiles, i);
+        if (u.lo >= u.hi) continue;
+        if (!wait_bounded(ptx::smem_u32(&acc_empty[acc]), acc_phase ^ 1u, ctl, SITE_MMA_ACC_EMPTY)) break;
+        ptx::tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * ACC);
+        for (int kb = u.lo; kb < u.hi; ++kb) {
+          if (!wait_bounded(ptx::smem_u32(&full[stage]), phase, ctl, SITE_MMA_FULL)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after_sync();
+          const uint32_t a0 = ptx::smem_u32(smem + stage * kStage), b0 = a0 + kSub;
+#pragma unroll
+          for (int k = 0; k < kTileK / 16; ++k) {
+            const uint64_t da = a_m_major(MODE) ? sw128_desc(a0 + k * 2048, 8192, 1024) : sw128_desc(a0 + k * 32, 16, 1024);
+            const uint64_t db = b_n_major(MODE) ? sw128_desc(b0 + k * 2048, 8192, 1024) : sw128_desc(b0 + k * 32, 16, 1024);
+            ptx::tc_mma_f16_pair(d_tmem, da, db, idesc, (kb != u.lo || k != 0) ? 1u : 0u);
+          }
+          ptx::tc_commit_pair_multicast(ptx::smem_u32(&empty[stage]), 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::tc_commit_pair_multicast(ptx::smem_u32(&acc_full[acc]), 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      ptx::tc_commit_pair(ptx::smem_u32(drain));
+      wait_teardown(ptx::smem_u32(drain), 0, ctl, SITE_DRAIN);
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------- epilogue
+    const int quarter = warp & 3;
+    uint8_t* stage_base = sC + (warp - 2) * 2 * 4096;
+    const int n = MODE == HEAD_DW ? 0 : min(*args.count, args.T);
+    int acc = 0, sbuf = 0;
+    uint32_t acc_phase = 0;
+    for (int i = worker; i < tiles.units; i += workers) {
+      const HeadUnit u = head_unit<MODE>(args, tiles, i);
+      if (u.lo >= u.hi) continue;
+      if (!warp_wait(ptx::smem_u32(&acc_full[acc]), acc_phase, ctl, SITE_EPI_ACC_FULL)) break;
+      ptx::tc_fence_after_sync();
+      const uint32_t tbase =
+          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * ACC);
+      const int row0 = u.mb * kHeadTile + half * kTileM + quarter * 32;
+      if constexpr (MODE == HEAD_STATS) {
+        if (row0 < n) epilogue_stats(tbase, row0 + lane, n, u.nb, args);
+      } else if constexpr (MODE == HEAD_DZ) {
+        epilogue_dz(tbase, row0, n, u.nb, args, &mapC, stage_base, sbuf, lane);
+      } else if constexpr (MODE == HEAD_DH) {
+        epilogue_dh(tbase, row0, u, args, &mapC, stage_base, sbuf, lane);
+      } else {
+        epilogue_dw(tbase, row0, u.nb, args, &mapC, stage_base, sbuf, lane);
+      }
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) ptx::bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+
+  // ------------------------------------------------------------- teardown
+  ptx::tc_fence_before_sync();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+template <int MODE>
+cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC, const HeadArgs& args,
+                   int pairs, cudaStream_t stream) {
+  constexpr int smem = head_smem(MODE);
+  auto kernel = head_kernel<MODE>;
+  static std::atomic<uint64_t> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done_mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    done_mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs, 1, 1);
+  cfg.blockDim = dim3(32 * (2 + kEpiWarps), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mA, mB, mC, args);
+}
+
+}  // namespace
+
+cudaError_t launch_head(int mode, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
+                        const HeadArgs& args, int pairs, cudaStream_t stream) {
+  switch (mode) {
+    case HEAD_STATS: return launch<HEAD_STATS>(mapA, mapB, mapC, args, pairs, stream);
+    case HEAD_DZ: return launch<HEAD_DZ>(mapA, mapB, mapC, args, pairs, stream);
+    case HEAD_DH: return launch<HEAD_DH>(mapA, mapB, mapC, args, pairs, stream);
+    case HEAD_DW: return launch<HEAD_DW>(mapA, mapB, mapC, args, pairs, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace tgemm

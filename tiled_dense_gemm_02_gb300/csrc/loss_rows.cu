@@ -1,0 +1,464 @@
+// Row kernels of the vocabulary-head losses: the teacher's lists, the gather of
+// the rows that count, the joining of the tiles' statistics, the last step of
+// dH, and the softmax steps of the fp32 path.  All of them are bound by memory
+// or by latency and move a small part of what the products do.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+
+#include "loss_internal.h"
+
+namespace tgemm {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ------------------------------------------------------------ teacher lists
+// One warp per row: softmax over the used places, then the places in ascending
+// order of their ids (each place's rank by counting, ties by position), so that
+// a tile of the product finds its entries by a binary search.
+constexpr int kListWarps = 4;
+constexpr int kListMax = 256;  // TGEMM_DISTILL_MAX_K
+__global__ void __launch_bounds__(kListWarps * 32)
+    distill_lists_kernel(const int64_t* __restrict__ ids, int64_t ld_ids, const float* __restrict__ logits,
+                         int64_t ld_logits, int T, int V, int K, float scale, HeadRows rows) {
+  __shared__ int s_id[kListWarps][kListMax];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kListWarps + warp;
+  if (t >= T) return;
+  constexpr int PER = kListMax / 32;
+  float y[PER];
+  int id[PER];
+  float top = -INFINITY;
+  bool some = false, bad = false;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int k = lane + 32 * j;
+    id[j] = INT_MAX;
+    y[j] = -INFINITY;
+    if (k >= K) continue;
+    const int64_t v = ids[t * ld_ids + k];
+    if (v >= 0) {
+      bad |= v >= V;
+      id[j] = v >= V ? INT_MAX : static_cast<int>(v);
+      y[j] = logits[t * ld_logits + k] * scale;
+      some |= !(y[j] == -INFINITY);
+      top = fmaxf(top, y[j]);
+    }
+    s_id[warp][k] = id[j];
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  some = __any_sync(0xffffffffu, some);
+  top = warp_max(top);
+  float e[PER], total = 0.0f;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    e[j] = y[j] == -INFINITY ? 0.0f : expf(y[j] - top);
+    total += e[j];
+  }
+  total = warp_sum(total);
+  const float log_total = logf(total);
+  float own = 0.0f;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int k = lane + 32 * j;
+    if (k >= K) continue;
+    const float q = some ? e[j] / total : 0.0f;
+    own += q == 0.0f ? 0.0f : q * (y[j] - top - log_total);
+    int rank = 0;
+    for (int i = 0; i < K; ++i) {
+      const int other = s_id[warp][i];
+      rank += (other < id[j] || (other == id[j] && i < k)) ? 1 : 0;
+    }
+    const int64_t at = static_cast<int64_t>(t) * K + rank;
+    rows.ids[at] = id[j];
+    rows.q[at] = q;
+  }
+  own = warp_sum(own);
+  if (lane == 0) {
+    rows.own[t] = own;
+    rows.flags[t] = bad ? kRowBad : some ? kRowCounts : kRowIgnored;
+  }
+}
+
+// ---------------------------------------------------------------- the gather
+__device__ __forceinline__ unsigned char row_flag(const GatherArgs& a, int t) {
+  if (!a.targets) return a.rows.flags[t];
+  const int64_t y = a.targets[t];
+  if (y == a.ignore_index) return kRowIgnored;
+  return (y >= 0 && y < a.V) ? kRowCounts : kRowBad;
+}
+
+__device__ __forceinline__ float grad_p(const GatherArgs& a, int t) {
+  const float g = a.grad[t];
+  return a.z_loss == 0.0f ? g : g * (1.0f + 2.0f * a.z_loss * a.lse[t]);
+}
+
+// Copies `bytes` (a multiple of G) with 32 lanes.
+template <int G>
+__device__ __forceinline__ void copy_row(uint8_t* dst, const uint8_t* src, int64_t bytes, int lane) {
+  using Word = typename std::conditional<
+      G == 16, uint4, typename std::conditional<G == 8, uint2, typename std::conditional<G == 4, uint32_t, uint16_t>::type>::type>::type;
+  const Word* s = reinterpret_cast<const Word*>(src);
+  Word* d = reinterpret_cast<Word*>(dst);
+  const int64_t n = bytes / G;
+#pragma unroll 4
+  for (int64_t i = lane; i < n; i += 32) d[i] = s[i];
+}
+
+// Every block counts the rows that count over all T (their flags are a few KB
+// in L2) to know where its own go, so the gather is one launch with a fixed
+// order.  In the backward pass it also finds the largest |grad|, which the
+// 16-bit gradients are divided by: a mean's 1/n is then exactly 1, and small
+// gradients do not fall below the format's range.
+constexpr int kGatherThreads = 256;
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs a, int rows_per) {
+  __shared__ int s_before[kGatherThreads / 32], s_total[kGatherThreads / 32], s_warp[kGatherThreads / 32];
+  __shared__ float s_g[kGatherThreads / 32], s_c[kGatherThreads / 32];
+  __shared__ int s_src[kGatherThreads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t0 = blockIdx.x * rows_per, t1 = min(a.T, t0 + rows_per);
+  int before = 0, total = 0;
+  float gmax = 0.0f, cmax = 0.0f;
+  for (int t = tid; t < a.T; t += kGatherThreads) {
+    if (row_flag(a, t) != kRowCounts) continue;
+    ++total;
+    before += t < t0 ? 1 : 0;
+    if (a.grad) {
+      const float g = fabsf(a.grad[t]), c = fabsf(grad_p(a, t));
+      if (isfinite(g)) gmax = fmaxf(gmax, g);
+      if (isfinite(c)) cmax = fmaxf(cmax, c);
+    }
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  gmax = warp_max(gmax);
+  cmax = warp_max(cmax);
+  const int t = t0 + tid;
+  const unsigned char flag = t < t1 ? row_flag(a, t) : kRowIgnored;
+  const unsigned ballot = __ballot_sync(0xffffffffu, flag == kRowCounts);
+  if (lane == 0) {
+    s_before[warp] = before;
+    s_total[warp] = total;
+    s_g[warp] = gmax;
+    s_c[warp] = cmax;
+    s_warp[warp] = __popc(ballot);
+  }
+  __syncthreads();
+  before = total = 0;
+  gmax = cmax = 0.0f;
+  int mine = 0, local = 0;
+#pragma unroll
+  for (int w = 0; w < kGatherThreads / 32; ++w) {
+    before += s_before[w];
+    total += s_total[w];
+    gmax = fmaxf(gmax, s_g[w]);
+    cmax = fmaxf(cmax, s_c[w]);
+    if (w < warp) local += s_warp[w];
+    mine += s_warp[w];
+  }
+  // unit * pow >= every |coefficient|; pow (a power of two) only where z_loss
+  // makes the softmax's coefficient larger than the target's
+  const float unit = gmax > 0.0f ? gmax : 1.0f;
+  float pow2 = 1.0f;
+  if (a.range != 0.0f && cmax > unit) {
+    int e;
+    const float f = frexpf(cmax / unit, &e);
+    pow2 = exp2f(static_cast<float>(min(f == 0.5f ? e - 1 : e, 60)));
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    *a.rows.count = total;
+    if (a.grad) *a.rows.factor = a.range == 0.0f ? 1.0f : unit * (a.scale * pow2 / a.range);
+  }
+  if (t < t1) {
+    const int place = before + local + __popc(ballot & ((1u << lane) - 1u));
+    const bool counts = flag == kRowCounts;
+    a.rows.place[t] = counts ? place : -1;
+    if (a.targets) {
+      a.rows.ids[t] = counts ? static_cast<int>(a.targets[t]) : INT_MAX;
+      a.rows.q[t] = 1.0f - a.smoothing;
+    }
+    if (counts) {
+      a.rows.source[place] = t;
+      s_src[place - before] = t;
+      if (a.grad) {
+        float cp = grad_p(a, t), cq = a.grad[t];
+        if (a.range == 0.0f) {
+          cp *= a.scale;
+          cq *= a.scale;
+        } else {
+          const float up = a.range / pow2;
+          cp = cp / unit * up;
+          cq = cq / unit * up;
+        }
+        a.rows.coef[place] = make_float4(cp, cq, a.lse[t] * kLog2e, a.lse[t]);
+      }
+    } else if (a.loss_out) {
+      const float v = flag == kRowBad ? __int_as_float(0x7FC00000) : 0.0f;
+      a.loss_out[t] = v;
+      a.lse_out[t] = v;
+    }
+  }
+  __syncthreads();
+  const int64_t row_bytes = static_cast<int64_t>(a.D) * a.es;
+  uint8_t* const out = static_cast<uint8_t*>(a.rows.h);
+  const int64_t out_pitch = a.rows.ldh * a.es;
+  for (int r = warp; r < mine; r += kGatherThreads / 32) {
+    const uint8_t* src = static_cast<const uint8_t*>(a.H) + static_cast<int64_t>(s_src[r]) * a.ldh * a.es;
+    uint8_t* dst = out + static_cast<int64_t>(before + r) * out_pitch;
+    int g = a.granule;
+    while (row_bytes % g) g >>= 1;
+    switch (g) {
+      case 16: copy_row<16>(dst, src, row_bytes, lane); break;
+      case 8: copy_row<8>(dst, src, row_bytes, lane); break;
+      case 4: copy_row<4>(dst, src, row_bytes, lane); break;
+      default: copy_row<2>(dst, src, row_bytes, lane); break;
+    }
+  }
+  // zeros after the last gathered row (the pitch is a multiple of 16 bytes)
+  const int blocks = max(1, (total + kRowBlock - 1) / kRowBlock);
+  const int end = a.zero_rows ? a.T : static_cast<int>(min(static_cast<int64_t>(a.T), int64_t(blocks) * kRowBlock));
+  for (int r = total + blockIdx.x * (kGatherThreads / 32) + warp; r < end; r += gridDim.x * (kGatherThreads / 32)) {
+    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * out_pitch);
+    for (int64_t i = lane; i < out_pitch / 16; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// --------------------------------------------------- joining tile statistics
+// A block joins the tiles of 8 rows with 32 threads a row: 64 contiguous bytes
+// per tile are read, and T / 8 blocks suffice even for one long list of tiles.
+constexpr int kCombineRows = 8, kCombineSlots = 32;
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  s = s * exp2f(m - ref) + s2 * exp2f(m2 - ref);
+  m = top;
+}
+
+__global__ void __launch_bounds__(kCombineRows * kCombineSlots)
+    combine_kernel(const float2* __restrict__ ms, const float* __restrict__ dot, int tiles, int T, float scale,
+                   float z_loss, HeadRows rows, float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float s_m[kCombineSlots][kCombineRows], s_s[kCombineSlots][kCombineRows], s_d[kCombineSlots][kCombineRows];
+  const int n = min(*rows.count, T);
+  const int r0 = blockIdx.x * kCombineRows;
+  if (r0 >= n) return;
+  const int lr = threadIdx.x % kCombineRows, slot = threadIdx.x / kCombineRows;
+  const int r = r0 + lr;
+  float m = -INFINITY, s = 0.0f, d = 0.0f;
+  if (r < n) {
+#pragma unroll 4
+    for (int i = slot; i < tiles; i += kCombineSlots) {
+      const float2 p = ms[static_cast<int64_t>(i) * T + r];
+      d += dot[static_cast<int64_t>(i) * T + r];
+      join(m, s, p.x, p.y);
+    }
+  }
+  s_m[slot][lr] = m;
+  s_s[slot][lr] = s;
+  s_d[slot][lr] = d;
+  __syncthreads();
+  for (int w = kCombineSlots / 2; w > 0; w >>= 1) {
+    if (slot < w) {
+      float m1 = s_m[slot][lr], s1 = s_s[slot][lr];
+      join(m1, s1, s_m[slot + w][lr], s_s[slot + w][lr]);
+      s_m[slot][lr] = m1;
+      s_s[slot][lr] = s1;
+      s_d[slot][lr] += s_d[slot + w][lr];
+    }
+    __syncthreads();
+  }
+  if (slot == 0 && r < n) {
+    const int t = rows.source[r];
+    const float l = s_m[0][lr] * kLn2 + logf(s_s[0][lr]);
+    float v = (rows.own ? rows.own[t] : 0.0f) + (l - scale * s_d[0][lr]);
+    if (z_loss != 0.0f) v = fmaf(z_loss * l, l, v);
+    loss[t] = v;
+    lse[t] = l;
+  }
+}
+
+// ------------------------------------------------------------ last step of dH
+template <typename Out>
+__device__ __forceinline__ Out to_out(float v);
+template <>
+__device__ __forceinline__ float to_out<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half to_out<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// One block per row of dH; the sums' pitch is a multiple of four.
+template <typename Out>
+__global__ void __launch_bounds__(128) finish_dh_kernel(const float* __restrict__ acc, int64_t ld_acc,
+                                                        int64_t split_stride, int splits, int D, HeadRows rows,
+                                                        Out* __restrict__ dH, int64_t lddh, int wide) {
+  const int t = blockIdx.x;
+  const int place = rows.place[t];
+  const float f = *rows.factor;
+  Out* out = dH + static_cast<int64_t>(t) * lddh;
+  for (int c = threadIdx.x * 4; c < D; c += blockDim.x * 4) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (place >= 0) {
+      const float* src = acc + static_cast<int64_t>(place) * ld_acc + c;
+      for (int s = 0; s < splits; ++s) {
+        const float4 p = *reinterpret_cast<const float4*>(src + s * split_stride);
+        v.x += p.x;
+        v.y += p.y;
+        v.z += p.z;
+        v.w += p.w;
+      }
+      v.x *= f;
+      v.y *= f;
+      v.z *= f;
+      v.w *= f;
+    }
+    const Out o[4] = {to_out<Out>(v.x), to_out<Out>(v.y), to_out<Out>(v.z), to_out<Out>(v.w)};
+    if (wide && c + 4 <= D) {
+      if constexpr (sizeof(Out) == 4)
+        *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(o);
+      else
+        *reinterpret_cast<uint2*>(out + c) = *reinterpret_cast<const uint2*>(o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < D) out[c + i] = o[i];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ fp32 path
+constexpr int kF32Threads = 256;
+__device__ __forceinline__ float block_reduce(float v, bool is_max, float* s) {
+  v = is_max ? warp_max(v) : warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s[0];
+  for (int w = 1; w < kF32Threads / 32; ++w) v = is_max ? fmaxf(v, s[w]) : v + s[w];
+  return v;
+}
+
+// One block per gathered row.
+__global__ void __launch_bounds__(kF32Threads) stats_f32_kernel(const float* __restrict__ Z, int64_t ldz, int cols,
+                                                                int col0, int T, int K, float k2, float flat,
+                                                                HeadRows rows, float2* __restrict__ ms,
+                                                                float* __restrict__ dot) {
+  __shared__ float s[kF32Threads / 32];
+  const int r = blockIdx.x;
+  if (r >= min(*rows.count, T)) return;
+  const float* z = Z + static_cast<int64_t>(r) * ldz;
+  float m = -INFINITY, zs = 0.0f;
+  for (int c = threadIdx.x; c < cols; c += kF32Threads) {
+    m = fmaxf(m, z[c]);
+    zs += z[c];
+  }
+  m = block_reduce(m, true, s);
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float sum = 0.0f;
+  for (int c = threadIdx.x; c < cols; c += kF32Threads) sum += exp2f((z[c] - ref) * k2);
+  sum = block_reduce(sum, false, s);
+  const int64_t list = static_cast<int64_t>(rows.source[r]) * K;
+  float d = 0.0f;
+  for (int k = threadIdx.x; k < K; k += kF32Threads) {
+    const int c = rows.ids[list + k] - col0;
+    if (c >= 0 && c < cols) d = fmaf(rows.q[list + k], z[c], d);
+  }
+  if (flat != 0.0f) d = fmaf(flat, zs, d);
+  d = block_reduce(d, false, s);
+  if (threadIdx.x == 0) {
+    ms[r] = make_float2(m * k2, sum);
+    dot[r] = d;
+  }
+}
+
+__global__ void __launch_bounds__(kF32Threads) dz_f32_kernel(float* __restrict__ Z, int64_t ldz, int cols, int col0,
+                                                             int T, int K, float scale, float flat, HeadRows rows) {
+  const int r = blockIdx.x;
+  float* z = Z + static_cast<int64_t>(r) * ldz;
+  if (r >= min(*rows.count, T)) {
+    for (int c = threadIdx.x; c < cols; c += kF32Threads) z[c] = 0.0f;
+    return;
+  }
+  const float4 k = rows.coef[r];
+  for (int c = threadIdx.x; c < cols; c += kF32Threads) z[c] = k.x * expf(fmaf(z[c], scale, -k.w)) - k.y * flat;
+  __syncthreads();
+  // equal ids are neighbours: the first of them subtracts all their masses
+  const int64_t list = static_cast<int64_t>(rows.source[r]) * K;
+  for (int i = threadIdx.x; i < K; i += kF32Threads) {
+    const int id = rows.ids[list + i], c = id - col0;
+    if (c < 0 || c >= cols || (i > 0 && rows.ids[list + i - 1] == id)) continue;
+    float q = 0.0f;
+    for (int j = i; j < K && rows.ids[list + j] == id; ++j) q += rows.q[list + j];
+    z[c] -= k.y * q;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_distill_lists(const int64_t* ids, int64_t ld_ids, const float* logits, int64_t ld_logits, int T,
+                                 int V, int K, float scale, const HeadRows& rows, cudaStream_t stream) {
+  distill_lists_kernel<<<(T + kListWarps - 1) / kListWarps, kListWarps * 32, 0, stream>>>(ids, ld_ids, logits,
+                                                                                         ld_logits, T, V, K, scale, rows);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
+  // a few blocks per SM, at most one row per thread of a block
+  const int target = 4 * sms;
+  int rows_per = (a.T + target - 1) / target;
+  rows_per = rows_per < 8 ? 8 : (rows_per > kGatherThreads ? kGatherThreads : rows_per);
+  const int blocks = a.T > 0 ? (a.T + rows_per - 1) / rows_per : 1;
+  gather_kernel<<<blocks, kGatherThreads, 0, stream>>>(a, rows_per);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T, float scale, float z_loss,
+                           const HeadRows& rows, float* loss, float* lse, cudaStream_t stream) {
+  combine_kernel<<<(T + kCombineRows - 1) / kCombineRows, kCombineRows * kCombineSlots, 0, stream>>>(
+      ms, dot, tiles, T, scale, z_loss, rows, loss, lse);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
+                             const HeadRows& rows, int type, void* dH, int64_t lddh, cudaStream_t stream) {
+  const int es = type == 2 ? 4 : 2;
+  const int wide = reinterpret_cast<uint64_t>(dH) % (4 * es) == 0 && lddh % 4 == 0 ? 1 : 0;
+  if (type == 0)
+    finish_dh_kernel<<<T, 128, 0, stream>>>(acc, ld_acc, split_stride, splits, D, rows,
+                                            static_cast<__nv_bfloat16*>(dH), lddh, wide);
+  else if (type == 1)
+    finish_dh_kernel<<<T, 128, 0, stream>>>(acc, ld_acc, split_stride, splits, D, rows, static_cast<__half*>(dH), lddh,
+                                            wide);
+  else
+    finish_dh_kernel<<<T, 128, 0, stream>>>(acc, ld_acc, split_stride, splits, D, rows, static_cast<float*>(dH), lddh,
+                                            wide);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_stats_f32(const float* Z, int64_t ldz, int cols, int col0, int T, int K, float k2, float flat,
+                             const HeadRows& rows, float2* ms, float* dot, cudaStream_t stream) {
+  stats_f32_kernel<<<T, kF32Threads, 0, stream>>>(Z, ldz, cols, col0, T, K, k2, flat, rows, ms, dot);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dz_f32(float* Z, int64_t ldz, int cols, int col0, int T, int K, float scale, float flat,
+                          const HeadRows& rows, cudaStream_t stream) {
+  dz_f32_kernel<<<T, kF32Threads, 0, stream>>>(Z, ldz, cols, col0, T, K, scale, flat, rows);
+  return cudaGetLastError();
+}
+
+}  // namespace tgemm
