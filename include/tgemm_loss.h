@@ -44,6 +44,9 @@
  * in H's and W's type, each sum held in float32 and rounded once; dz itself is
  * rounded to H's type on its way into the two products.  dH and dW are
  * overwritten.  Results do not depend on timing: every sum has a fixed order.
+ *
+ * All products run on the tensor cores.  fp32 operands are split into three
+ * bf16 planes each (all 24 significant bits) and multiplied plane by plane.
  */
 #ifndef TGEMM_LOSS_H
 #define TGEMM_LOSS_H
@@ -75,14 +78,15 @@ typedef struct tgemm_loss_options {
  * that may run at the same time must not share one.  backward: 0 for the
  * forward calls, 1 for the backward calls; K: 0 for the cross entropy.  W and
  * ldw tell whether the weight's rows are 16-byte aligned (pieces of it are
- * copied to an aligned pitch when they are not).  Needs no GPU. */
+ * copied to an aligned pitch when they are not; only W's value modulo 16 is
+ * looked at).  Needs no GPU. */
 TGEMM_API int tgemm_loss_workspace_size(int backward, int64_t T, int64_t V, int64_t D, int64_t K,
                const void* W, int64_t ldw, int dtype, const tgemm_loss_options* opts, size_t* bytes);
 
 /*
  * Cross entropy, forward: loss[T] and lse[T] (lse is what the backward call
- * takes; it may be used as is for scoring).  dtype: TGEMM_BF16, TGEMM_F16
- * (tensor cores) or TGEMM_F32 (CUDA cores).  targets: T int64 on the device.
+ * takes; it may be used as is for scoring).  dtype: TGEMM_BF16, TGEMM_F16 or
+ * TGEMM_F32.  targets: T int64 on the device.
  *
  * Errors: TGEMM_ERR_INVALID_VALUE for T < 0, V < 1, D < 1, a short leading
  * dimension, a null pointer with T > 0, a bad option, a workspace that is

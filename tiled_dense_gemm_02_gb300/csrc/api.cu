@@ -1116,21 +1116,10 @@ static CUtensorMapDataType host_map_type(int type) {
                    : (type == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
 }
 
-int host_map_2d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t pitch_bytes,
-                uint32_t box_cols, uint32_t box_rows) {
-  return encode_2d(map, host_map_type(type), base, cols, rows, pitch_bytes, box_cols, box_rows);
-}
-
 int host_map_3d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t depth,
                 int64_t pitch_bytes, int64_t depth_bytes, uint32_t box_cols, uint32_t box_rows) {
   return encode_3d(map, host_map_type(type), base, cols, rows, depth, pitch_bytes, depth_bytes, box_cols, box_rows,
                    CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-int host_gemm_f32(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda, const float* B, int64_t ldb, float* C,
-                  int64_t ldc, float beta, cudaStream_t stream) {
-  const tgemm_epilogue e = {1.0f, beta, nullptr, TGEMM_ACT_NONE, {0, 0, 0}};
-  return run(M, N, K, A, lda, B, ldb, C, ldc, TGEMM_F32, nullptr, &e, nullptr, 0, stream);
 }
 
 void host_count_launches(int n) { g_launch_calls.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }

@@ -4,8 +4,8 @@
 // Forward:  [teacher lists]  gather  STATS (one launch over the vocabulary)  combine
 // Backward: [teacher lists]  gather  { DZ  DH  DW } per piece  last step of dH
 // (loss_rows.cu and loss_gemm.cu hold the kernels.)  A weight whose rows are
-// not 16-byte aligned is copied to an aligned pitch piece by piece.  fp32 runs
-// the same steps with the library's CUDA-core product on pieces of logits.
+// not 16-byte aligned is copied to an aligned pitch piece by piece, and an fp32
+// weight to its three bf16 planes.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -28,10 +28,15 @@ constexpr int64_t kMaxExtent = int64_t(1) << 31;
 // CTA pairs the layout is planned for (a GB300's 152 SMs); the layout must not
 // depend on the device, so that its size can be asked for without one.
 constexpr int kPlanPairs = 76;
-// Bytes of one piece of dz (16-bit) or of logits (fp32), and of a piece of W
-// copied to an aligned pitch.  A piece twice the size of L2 already runs tens
-// of rounds of tiles per product, so a larger one would gain nothing.
+// Bytes of one piece of dz, and of a piece of W that is copied.  A piece twice
+// the size of L2 already runs tens of rounds of tiles per product, so a larger
+// one would gain nothing.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
+// fp32: stages of the gradients' k axes (64 deep) summed in tensor memory
+// before they are added in fp32: the truncation of 64 steps stays below 1e-6,
+// and adding 256 KB per tile takes less time than the 96 stages of six plane
+// products that a chunk runs.
+constexpr int kChunkStages = 16;
 constexpr float kRangeF16 = 16384.0f;  // |dz| <= 2: fp16's largest value is 65504, its small normals reach 2^-14
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -65,13 +70,13 @@ struct Call {
 
 // Byte offsets into the workspace; every part starts on a 256-byte boundary.
 struct Layout {
-  int es = 2;
-  bool pack = false;           // W is copied to an aligned pitch, piece by piece
+  int planes = 1;
+  bool pack = false;           // W is copied to an aligned pitch or to planes, piece by piece
   int64_t piece = 0, pieces = 1;
   int64_t ldh = 0, ldw_p = 0, ldz = 0, ld_acc = 0;
   int splits = 1, k_per_split = 0;
   int64_t count = 0, source = 0, place = 0, ids = 0, q = 0, own = 0, flags = 0, coef = 0, h = 0;
-  int64_t ms = 0, dot = 0, z = 0, zt = 0, w = 0, wt = 0, acc = 0;
+  int64_t ms = 0, dot = 0, z = 0, w = 0, acc = 0;
   int64_t tiles = 0;           // statistics per row
   int64_t total = 0;
 };
@@ -98,23 +103,18 @@ void plan_splits(int64_t T, int64_t D, int64_t kb, Layout& l) {
 Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bool distill, const void* W, int64_t ldw,
                    int dtype, int64_t piece_opt) {
   Layout l;
-  const bool f32 = dtype == TGEMM_F32;
-  l.es = f32 ? 4 : 2;
-  l.ldh = round_up(D, 16 / l.es);
-  l.pack = !f32 && host_granule(W, ldw, 2) < 16;
-  l.ldw_p = round_up(D, 8);
+  l.planes = dtype == TGEMM_F32 ? kPlanes : 1;
+  l.ldh = l.ldw_p = round_up(D, 8);
+  l.pack = l.planes > 1 || host_granule(W, ldw, 2) < 16;
   l.ld_acc = round_up(D, 4);
   const int64_t whole = round_up(V, kHeadTile);
   if (piece_opt > 0) {
     l.piece = std::min(piece_opt, whole);
-  } else if (!backward && !f32 && !l.pack) {
+  } else if (!backward && !l.pack) {
     l.piece = whole;
   } else {
-    int64_t per = 0;  // bytes per entry of a piece
-    if (f32 || backward) per = std::max<int64_t>(per, T * l.es);
-    if (l.pack) per = std::max<int64_t>(per, l.ldw_p * 2);
-    if (f32) per = std::max<int64_t>(per, D * 4);
-    const int64_t fit = std::max<int64_t>(2048, kPieceBytes / std::max<int64_t>(1, per) / kHeadTile * kHeadTile);
+    const int64_t per = 2 * l.planes * std::max<int64_t>(backward ? T : 0, l.pack ? l.ldw_p : 0);  // bytes per entry
+    const int64_t fit = std::max<int64_t>(2048, kPieceBytes / per / kHeadTile * kHeadTile);
     l.piece = std::min(fit, whole);
     l.piece = round_up(ceil_div(V, ceil_div(V, l.piece)), kHeadTile);
   }
@@ -134,19 +134,16 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   l.own = take(distill ? T * 4 : 0);
   l.flags = take(distill ? T : 0);
   l.coef = take(backward ? T * 16 : 0);
-  l.h = take(T * l.ldh * l.es);
-  l.tiles = f32 ? l.pieces : ceil_div(V, kHeadTile);
-  if (!backward) {
+  l.h = take(T * l.ldh * 2 * l.planes);
+  l.tiles = ceil_div(V, kHeadTile);
+  if (l.pack) l.w = take(l.piece * l.ldw_p * 2 * l.planes);
+  if (backward) {
+    l.z = take(T * l.ldz * 2 * l.planes);
+    plan_splits(T, D, ceil_div(std::min(l.piece, V), kTileK), l);
+    l.acc = take(l.splits * T * l.ld_acc * 4);
+  } else {
     l.ms = take(l.tiles * T * 8);
     l.dot = take(l.tiles * T * 4);
-  }
-  if (f32 || backward) l.z = take(T * l.ldz * l.es);
-  if (l.pack) l.w = take(l.piece * l.ldw_p * 2);
-  if (f32) l.wt = take(l.piece * D * 4);
-  if (f32 && backward) l.zt = take(l.piece * round_up(T, 4) * 4);
-  if (backward) {
-    if (!f32) plan_splits(T, D, ceil_div(std::min(l.piece, V), kTileK), l);
-    l.acc = take(l.splits * T * l.ld_acc * 4);
   }
   l.total = at;
   return l;
@@ -169,9 +166,9 @@ int check_shape(int64_t T, int64_t V, int64_t D, int64_t K, bool distill, int dt
   if (dtype != TGEMM_F32 && dtype != TGEMM_F16 && dtype != TGEMM_BF16) return TGEMM_ERR_UNSUPPORTED_DTYPE;
   const int st = check_options(opts, distill);
   if (st != TGEMM_OK) return st;
-  // the last tile's end must stay an int, and a transpose's grid limits fp32 rows
+  // the last tile's end must stay an int
   if (T >= kMaxExtent - kHeadTile || V >= kMaxExtent - kHeadTile || D >= kMaxExtent - kHeadTile ||
-      (distill && K > TGEMM_DISTILL_MAX_K) || (dtype == TGEMM_F32 && T > int64_t(65535) * 64))
+      (distill && K > TGEMM_DISTILL_MAX_K))
     return TGEMM_ERR_TOO_LARGE;
   return TGEMM_OK;
 }
@@ -234,51 +231,12 @@ int check_call(const Call& c) {
     if (e_ != cudaSuccess) return host_cuda_fail(e_, what); \
   } while (0)
 
-int run_f32(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float scale, float flat, float z_loss) {
-  float* Z = reinterpret_cast<float*>(ws + l.z);
-  float* wt = reinterpret_cast<float*>(ws + l.wt);
-  float* zt = reinterpret_cast<float*>(ws + l.zt);
-  float* acc = reinterpret_cast<float*>(ws + l.acc);
-  float2* ms = reinterpret_cast<float2*>(ws + l.ms);
-  float* dot = reinterpret_cast<float*>(ws + l.dot);
-  const float* h = static_cast<const float*>(rows.h);
-  const float* W = static_cast<const float*>(c.W);
-  const int T = static_cast<int>(c.T), D = static_cast<int>(c.D), K = static_cast<int>(c.K);
-  const float k2 = static_cast<float>(scale * kLog2e);
-  const int64_t ldzt = round_up(c.T, 4);
-  for (int64_t i = 0; i < l.pieces; ++i) {
-    const int64_t v0 = i * l.piece, n = std::min(l.piece, c.V - v0);
-    const float* w = W + v0 * c.ldw;
-    const bool vec = reinterpret_cast<uint64_t>(w) % 16 == 0 && c.ldw % 4 == 0 && l.piece % 4 == 0;
-    TGEMM_CUDA(launch_transpose(w, c.ldw, wt, l.piece, static_cast<int>(n), D, 4, vec, c.stream), "transpose launch");
-    TGEMM_TRY(host_gemm_f32(c.T, n, c.D, h, l.ldh, wt, l.piece, Z, l.ldz, 0.0f, c.stream));
-    if (!c.backward) {
-      TGEMM_CUDA(launch_stats_f32(Z, l.ldz, static_cast<int>(n), static_cast<int>(v0), T, K, k2, flat, rows,
-                                  ms + i * c.T, dot + i * c.T, c.stream),
-                 "statistics launch");
-      continue;
-    }
-    TGEMM_CUDA(launch_dz_f32(Z, l.ldz, static_cast<int>(n), static_cast<int>(v0), T, K, scale, flat, rows, c.stream),
-               "gradient launch");
-    if (c.dH) TGEMM_TRY(host_gemm_f32(c.T, c.D, n, Z, l.ldz, w, c.ldw, acc, l.ld_acc, i ? 1.0f : 0.0f, c.stream));
-    if (c.dW) {
-      TGEMM_CUDA(launch_transpose(Z, l.ldz, zt, ldzt, T, static_cast<int>(n), 4, true, c.stream), "transpose launch");
-      TGEMM_TRY(host_gemm_f32(n, c.D, c.T, zt, ldzt, h, l.ldh, static_cast<float*>(c.dW) + v0 * c.lddw, c.lddw, 0.0f,
-                              c.stream));
-    }
-  }
-  if (!c.backward)
-    TGEMM_CUDA(launch_combine(ms, dot, static_cast<int>(l.tiles), T, scale, z_loss, rows, c.loss, c.lse_out, c.stream),
-               "combine launch");
-  else if (c.dH)
-    TGEMM_CUDA(launch_finish_dh(acc, l.ld_acc, 0, 1, T, D, rows, 2, c.dH, c.lddh, c.stream), "dH launch");
-  return TGEMM_OK;
-}
-
-int run_tc(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float scale, float flat, float z_loss,
-           int sms, int pairs, unsigned int* status) {
+int run_products(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float scale, float flat, float z_loss,
+                 int sms, int pairs, unsigned int* status) {
   if (pairs < 1) return host_cuda_fail(cudaErrorLaunchOutOfResources, "CTA pairs");
-  const int type = c.dtype == TGEMM_BF16 ? 0 : 1;
+  const bool f32 = l.planes > 1;
+  const int type = c.dtype == TGEMM_F16 ? 1 : 0;  // of the operands; fp32's planes are bf16
+  const int P = l.planes;
   CUtensorMap m_h, m_w, m_wn, m_z, m_zk, m_hn, m_acc, m_dw, m_zs;
   for (CUtensorMap* m : {&m_h, &m_w, &m_wn, &m_z, &m_zk, &m_hn, &m_acc, &m_dw, &m_zs}) std::memset(m, 0, sizeof *m);
   HeadArgs a;
@@ -289,9 +247,11 @@ int run_tc(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float
   a.K = static_cast<int>(c.K);
   a.D = static_cast<int>(c.D);
   a.bf16 = type == 0;
-  a.k2 = static_cast<float>(scale * kLog2e);
+  const float put_back = 1.0f + kStepLoss * static_cast<float>(ceil_div(c.D, 16));
+  a.k2 = static_cast<float>(scale * put_back * kLog2e);
   a.flat = flat;
   a.group_m = 8;
+  a.chunk = kChunkStages;
   a.source = rows.source;
   a.ids = rows.ids;
   a.q = rows.q;
@@ -304,20 +264,23 @@ int run_tc(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float
   a.status = status;
   const int64_t m_tiles = ceil_div(c.T, kHeadTile), d_tiles = ceil_div(c.D, kHeadTile);
   const int d_blocks = static_cast<int>(ceil_div(c.D, kTileK));
-  TGEMM_TRY(host_map_2d(&m_h, type, rows.h, c.D, c.T, l.ldh * 2, kTileK, kTileM));
+  const int64_t h_plane = rows.plane * 2, z_plane = c.T * l.ldz * 2;
+  TGEMM_TRY(host_map_3d(&m_h, type, rows.h, c.D, c.T, P, l.ldh * 2, h_plane, kTileK, kTileM));
   void* z = ws + l.z;
   if (c.backward) {
-    TGEMM_TRY(host_map_2d(&m_zs, type, z, l.ldz, c.T, l.ldz * 2, 64, 32));
+    TGEMM_TRY(host_map_3d(&m_zs, type, z, l.ldz, c.T, P, l.ldz * 2, z_plane, 64, 32));
     if (c.dH) {
-      TGEMM_TRY(host_map_2d(&m_z, type, z, l.ldz, c.T, l.ldz * 2, kTileK, kTileM));
+      TGEMM_TRY(host_map_3d(&m_z, type, z, l.ldz, c.T, P, l.ldz * 2, z_plane, kTileK, kTileM));
       TGEMM_TRY(host_map_3d(&m_acc, 2, ws + l.acc, c.D, c.T, l.splits, l.ld_acc * 4, c.T * l.ld_acc * 4, 32, 32));
     }
     if (c.dW) {
-      TGEMM_TRY(host_map_2d(&m_zk, type, z, l.ldz, c.T, l.ldz * 2, 64, kTileK));
-      TGEMM_TRY(host_map_2d(&m_hn, type, rows.h, c.D, c.T, l.ldh * 2, 64, kTileK));
-      a.store_granule = host_granule(c.dW, c.lddw, 2);
-      if (a.store_granule == 16) a.store_granule = 0;
-      if (a.store_granule == 0) TGEMM_TRY(host_map_2d(&m_dw, type, c.dW, c.D, c.V, c.lddw * 2, 64, 32));
+      TGEMM_TRY(host_map_3d(&m_zk, type, z, l.ldz, c.T, P, l.ldz * 2, z_plane, 64, kTileK));
+      TGEMM_TRY(host_map_3d(&m_hn, type, rows.h, c.D, c.T, P, l.ldh * 2, h_plane, 64, kTileK));
+      a.store_granule = host_granule(c.dW, c.lddw, f32 ? 4 : 2);
+      if (!f32 && a.store_granule == 16) {
+        a.store_granule = 0;
+        TGEMM_TRY(host_map_3d(&m_dw, type, c.dW, c.D, c.V, 1, c.lddw * 2, 0, 64, 32));
+      }
     }
   }
   const auto grid = [pairs](int64_t units) { return static_cast<int>(std::min<int64_t>(pairs, units)); };
@@ -326,13 +289,21 @@ int run_tc(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float
     const int64_t v0 = i * l.piece, n = std::min(l.piece, c.V - v0);
     const void* w = c.W;
     int64_t ldw = c.ldw, w_rows = c.V;
+    const int64_t w_plane = l.piece * l.ldw_p;
     a.b_row0 = static_cast<int>(v0);
     if (l.pack) {
       w = ws + l.w;
-      const char* src = static_cast<const char*>(c.W) + v0 * c.ldw * 2;
-      TGEMM_CUDA(launch_repack(src, c.ldw, ws + l.w, l.ldw_p, static_cast<int>(n), a.D, host_granule(src, c.ldw, 2), sms,
-                               c.stream),
-                 "repack launch");
+      if (f32) {
+        const float* src = static_cast<const float*>(c.W) + v0 * c.ldw;
+        TGEMM_CUDA(launch_split(src, c.ldw, ws + l.w, l.ldw_p, w_plane, static_cast<int>(n), a.D,
+                                host_granule(src, c.ldw, 4) == 16, c.stream),
+                   "split launch");
+      } else {
+        const char* src = static_cast<const char*>(c.W) + v0 * c.ldw * 2;
+        TGEMM_CUDA(launch_repack(src, c.ldw, ws + l.w, l.ldw_p, static_cast<int>(n), a.D, host_granule(src, c.ldw, 2),
+                                 sms, c.stream),
+                   "repack launch");
+      }
       ldw = l.ldw_p;
       w_rows = n;  // the copy's rows past the piece hold an earlier piece
       a.b_row0 = 0;
@@ -341,22 +312,26 @@ int run_tc(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float
     a.col0 = static_cast<int>(v0);
     a.tile0 = static_cast<int>(v0 / kHeadTile);
     a.k_blocks = d_blocks;
-    TGEMM_TRY(host_map_2d(&m_w, type, w, c.D, w_rows, ldw * 2, kTileK, kTileM));
+    TGEMM_TRY(host_map_3d(&m_w, type, w, c.D, w_rows, P, ldw * 2, w_plane * 2, kTileK, kTileM));
     const int64_t tiles = m_tiles * ceil_div(n, kHeadTile);
     ++launches;
     if (!c.backward) {
-      TGEMM_CUDA(launch_head(HEAD_STATS, m_h, m_w, m_w, a, grid(tiles), c.stream), "head launch");
+      TGEMM_CUDA(launch_head(HEAD_STATS, P, m_h, m_w, m_w, a, grid(tiles), c.stream), "head launch");
       continue;
     }
-    TGEMM_CUDA(launch_head(HEAD_DZ, m_h, m_w, m_zs, a, grid(tiles), c.stream), "head launch");
+    TGEMM_CUDA(launch_head(HEAD_DZ, P, m_h, m_w, m_zs, a, grid(tiles), c.stream), "head launch");
     if (c.dH) {
-      TGEMM_TRY(host_map_2d(&m_wn, type, w, c.D, w_rows, ldw * 2, 64, kTileK));
+      TGEMM_TRY(host_map_3d(&m_wn, type, w, c.D, w_rows, P, ldw * 2, w_plane * 2, 64, kTileK));
       HeadArgs b = a;
       b.k_blocks = static_cast<int>(ceil_div(n, kTileK));
       b.splits = l.splits;
       b.k_per_split = l.k_per_split;
       b.reduce = i > 0;
-      TGEMM_CUDA(launch_head(HEAD_DH, m_z, m_wn, m_acc, b, grid(m_tiles * d_tiles * l.splits), c.stream), "head launch");
+      b.out = ws + l.acc;
+      b.ld_out = l.ld_acc;
+      b.split_stride = c.T * l.ld_acc;
+      TGEMM_CUDA(launch_head(HEAD_DH, P, m_z, m_wn, m_acc, b, grid(m_tiles * d_tiles * l.splits), c.stream),
+                 "head launch");
       ++launches;
     }
     if (c.dW) {
@@ -364,19 +339,19 @@ int run_tc(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float
       b.out = c.dW;
       b.ld_out = c.lddw;
       b.out_row0 = static_cast<int>(v0);
-      TGEMM_CUDA(launch_head(HEAD_DW, m_zk, m_hn, m_dw, b, grid(ceil_div(n, kHeadTile) * d_tiles), c.stream),
+      TGEMM_CUDA(launch_head(HEAD_DW, P, m_zk, m_hn, m_dw, b, grid(ceil_div(n, kHeadTile) * d_tiles), c.stream),
                  "head launch");
       ++launches;
     }
   }
   host_count_launches(launches);
   if (!c.backward)
-    TGEMM_CUDA(launch_combine(a.ms, a.dot, static_cast<int>(l.tiles), a.T, scale, z_loss, rows, c.loss, c.lse_out,
-                              c.stream),
+    TGEMM_CUDA(launch_combine(a.ms, a.dot, static_cast<int>(l.tiles), a.T, scale * put_back, z_loss, rows, c.loss,
+                              c.lse_out, c.stream),
                "combine launch");
   else if (c.dH)
     TGEMM_CUDA(launch_finish_dh(reinterpret_cast<float*>(ws + l.acc), l.ld_acc, c.T * l.ld_acc, l.splits, a.T, a.D, rows,
-                                type, c.dH, c.lddh, c.stream),
+                                f32 ? 2 : type, c.dH, c.lddh, c.stream),
                "dH launch");
   return TGEMM_OK;
 }
@@ -417,6 +392,7 @@ int run_loss(const Call& c) {
   g.rows.coef = c.backward ? reinterpret_cast<float4*>(ws + l.coef) : nullptr;
   g.rows.h = ws + l.h;
   g.rows.ldh = l.ldh;
+  g.rows.plane = c.T * l.ldh;
   g.T = static_cast<int>(c.T);
   g.V = static_cast<int>(c.V);
   g.D = static_cast<int>(c.D);
@@ -430,8 +406,7 @@ int run_loss(const Call& c) {
   g.smoothing = smoothing;
   g.z_loss = z_loss;
   g.scale = scale;
-  g.range = c.dtype == TGEMM_F32 ? 0.0f : (c.dtype == TGEMM_F16 ? kRangeF16 : 1.0f);
-  g.zero_rows = c.dtype == TGEMM_F32;
+  g.range = c.dtype == TGEMM_F16 ? kRangeF16 : 1.0f;
   g.lse = c.lse;
   g.grad = c.grad;
   g.loss_out = c.loss;
@@ -440,8 +415,7 @@ int run_loss(const Call& c) {
     TGEMM_CUDA(launch_distill_lists(c.ids, c.ld_ids, c.logits, c.ld_logits, g.T, g.V, g.K, scale, g.rows, c.stream),
                "teacher list launch");
   TGEMM_CUDA(launch_gather(g, sms, c.stream), "gather launch");
-  if (c.dtype == TGEMM_F32) return run_f32(c, l, g.rows, ws, scale, flat, z_loss);
-  return run_tc(c, l, g.rows, ws, scale, flat, z_loss, sms, pairs, status);
+  return run_products(c, l, g.rows, ws, scale, flat, z_loss, sms, pairs, status);
 }
 
 }  // namespace

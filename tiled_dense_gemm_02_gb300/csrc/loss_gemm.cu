@@ -9,6 +9,13 @@
 //   DH     dz . W             fp32 sums, stored or added (bulk-tensor reduce)
 //   DW     dz^T . H           times a factor, rounded once, stored
 //
+// fp32 operands come as three bf16 planes (loss_rows.cu), and a stage of the k
+// axis is then six stages, one per pair of planes, the small terms first: the
+// last sixth alone adds to a sum of full size, so the adder's truncation is
+// that of a 16-bit product.  DH and DW, whose k axes are long, move their sums
+// out of tensor memory every `chunk` stages and add them in fp32 with rounding
+// to nearest, each element by the one thread that owns it.
+//
 // with k2 = scale log2(e), so that one fused multiply-add and one 2^x serve
 // each logit.  H and W are read K-major (their rows are the k axis) by STATS
 // and DZ; W as the N-major B of DH; dz as the M-major A and H as the N-major B
@@ -43,6 +50,11 @@ constexpr int head_smem(int mode) {
 }
 constexpr bool a_m_major(int mode) { return mode == HEAD_DW; }
 constexpr bool b_n_major(int mode) { return mode == HEAD_DH || mode == HEAD_DW; }
+
+// Pairs of planes in the order they are summed: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0).
+constexpr int plane_terms(int planes) { return planes == 1 ? 1 : 6; }
+__device__ __forceinline__ int plane_a(int term) { return (0x001102 >> (4 * term)) & 0xF; }
+__device__ __forceinline__ int plane_b(int term) { return (0x010120 >> (4 * term)) & 0xF; }
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -238,8 +250,21 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, int lane, const uint32_t
   __syncwarp();
 }
 
+// One 64-column chunk of 16-bit words of 32 rows, to the tensor at (col, row0, plane).
+__device__ __forceinline__ void store_words(const uint32_t (&w)[32], const CUtensorMap* mapC, int col, int row0,
+                                            int plane, uint8_t* stage_base, int& sbuf, int lane) {
+  uint8_t* buf = staging(stage_base, sbuf, lane);
+  stage_row(buf, lane, w);
+  if (lane == 0) {
+    ptx::tma_store_3d(mapC, col, row0, plane, ptx::smem_u32(buf));
+    ptx::bulk_commit_group();
+  }
+}
+
+template <int PLANES>
 __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int nb, const HeadArgs& a,
                                             const CUtensorMap* mapC, uint8_t* stage_base, int& sbuf, int lane) {
+  if (row0 >= a.T) return;
   const int row = row0 + lane;
   const int first = a.col0 + nb * kHeadTile;
   const int width = min(kHeadTile, a.cols - nb * kHeadTile);
@@ -256,21 +281,60 @@ __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int
     ptx::tmem_wait_ld();
     gradient_chunk(lo, first + c * 64, width - c * 64, k, a, walk);
     gradient_chunk(hi, first + c * 64 + 32, width - c * 64 - 32, k, a, walk);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      w[i] = pack_pair(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]), fmt);
-      w[16 + i] = pack_pair(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]), fmt);
-    }
     if (row >= n) {  // rows past the count: zeros, which the products read
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = 0u;
+      for (int i = 0; i < 32; ++i) lo[i] = hi[i] = 0u;
     }
-    uint8_t* buf = staging(stage_base, sbuf, lane);
-    stage_row(buf, lane, w);
-    if (lane == 0) {
-      if (row0 < a.T) ptx::tma_store_2d(mapC, nb * kHeadTile + c * 64, row0, ptx::smem_u32(buf));
-      ptx::bulk_commit_group();
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        uint32_t* v = i < 16 ? &lo[2 * i] : &hi[2 * i - 32];
+        const float x = __uint_as_float(v[0]), y = __uint_as_float(v[1]);
+        w[i] = pack_pair(x, y, PLANES == 1 ? fmt : OUT_BF16);
+        if (p + 1 < PLANES) {  // what the plane leaves (0 where it is not finite)
+          const float px = __uint_as_float(w[i] << 16), py = __uint_as_float(w[i] & 0xFFFF0000u);
+          v[0] = isfinite(px) ? __float_as_uint(x - px) : 0u;
+          v[1] = isfinite(py) ? __float_as_uint(y - py) : 0u;
+        }
+      }
+      store_words(w, mapC, nb * kHeadTile + c * 64, row0, p, stage_base, sbuf, lane);
     }
+  }
+}
+
+// 32 fp32 values of a row: stored, or added to what is there.  The same thread
+// writes an element in every chunk, so the order of the additions is fixed.
+__device__ __forceinline__ void store_row_f32(float* dst, const float (&v)[32], int valid, bool vec, bool add) {
+  if (vec && valid >= 32) {
+    float4* d = reinterpret_cast<float4*>(dst);
+    float4 o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = add ? __ldcg(d + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      __stcg(d + i, make_float4(o[i].x + v[4 * i], o[i].y + v[4 * i + 1], o[i].z + v[4 * i + 2], o[i].w + v[4 * i + 3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < valid) __stcg(dst + i, add ? __ldcg(dst + i) + v[i] : v[i]);
+  }
+}
+
+// fp32 DH and DW: one chunk's sums of this thread's row, times f.
+__device__ __forceinline__ void epilogue_f32(uint32_t tbase, float* row, bool valid_row, int col0, int cols, float f,
+                                             bool vec, bool add) {
+#pragma unroll 1
+  for (int c = 0; c < kHeadTile / 32; ++c) {
+    const int left = cols - col0 - c * 32;
+    if (left <= 0) break;
+    uint32_t w[32];
+    ptx::tmem_ld_32x32b_x32(tbase + c * 32, w);
+    ptx::tmem_wait_ld();
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = f * __uint_as_float(w[i]);
+    if (valid_row) store_row_f32(row + col0 + c * 32, v, left, vec, add);
   }
 }
 
@@ -316,12 +380,7 @@ __device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, co
       w[16 + i] = pack_pair(f * __uint_as_float(hi[2 * i]), f * __uint_as_float(hi[2 * i + 1]), fmt);
     }
     if (a.store_granule == 0) {
-      uint8_t* buf = staging(stage_base, sbuf, lane);
-      stage_row(buf, lane, w);
-      if (lane == 0) {
-        ptx::tma_store_2d(mapC, col, a.out_row0 + row0, ptx::smem_u32(buf));
-        ptx::bulk_commit_group();
-      }
+      store_words(w, mapC, col, a.out_row0 + row0, 0, stage_base, sbuf, lane);
     } else if (row < a.cols) {
       uint8_t* dst = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(a.out_row0 + row) * a.ld_out + col) * 2;
       store_segment(dst, w, min(a.D - col, 64) * 2, a.store_granule, 2);
@@ -329,7 +388,7 @@ __device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, co
   }
 }
 
-template <int MODE>
+template <int MODE, int PLANES>
 __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
     head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ CUtensorMap mapC, const HeadArgs args) {
@@ -383,9 +442,15 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
   ptx::cluster_sync();
   ptx::tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
+  // set-up overlaps the end of the kernel before; its results are read from here on
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
 
   const Ctl ctl{abort_flag, args.timeout_ns, args.status};
   const Tiles tiles = head_tiles<MODE>(args);
+  constexpr int TERMS = plane_terms(PLANES);
+  // stages summed in tensor memory at a time: all of a unit's, or a chunk
+  const int chunk = PLANES > 1 && (MODE == HEAD_DH || MODE == HEAD_DW) ? args.chunk : INT_MAX / 2;
 
   if (warp == 0) {
     // ------------------------------------------------ bulk-tensor producer
@@ -397,34 +462,39 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
         const HeadUnit u = head_unit<MODE>(args, tiles, i);
         const int m0 = u.mb * kHeadTile + half * kTileM;
         const int n0 = u.nb * kHeadTile + half * (kHeadTile / 2);
-        for (int kb = u.lo; kb < u.hi; ++kb) {
-          if (!wait_bounded(ptx::smem_u32(&empty[stage]), phase ^ 1u, ctl, SITE_PRODUCER_EMPTY)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb_local = ptx::smem_u32(&full[stage]);
-          const uint32_t fb = ptx::mapa_shared(fb_local, 0);
-          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2u * kStage);
-          const uint32_t sa = ptx::smem_u32(smem + stage * kStage), sb = sa + kSub;
-          const int k0 = kb * kTileK;  // stages past the k axis load zeros
-          if constexpr (a_m_major(MODE)) {
-            ptx::tma_load_2d_pair(sa, &mapA, m0, k0, fb);
-            ptx::tma_load_2d_pair(sa + 8192, &mapA, m0 + 64, k0, fb);
-          } else {
-            ptx::tma_load_2d_pair(sa, &mapA, k0, m0, fb);
-          }
-          if constexpr (b_n_major(MODE)) {
-            const int kr = k0 + (MODE == HEAD_DH ? args.b_row0 : 0);
-            ptx::tma_load_2d_pair(sb, &mapB, n0, kr, fb);
-            ptx::tma_load_2d_pair(sb + 8192, &mapB, n0 + 64, kr, fb);
-          } else {
-            ptx::tma_load_2d_pair(sb, &mapB, k0, args.b_row0 + n0, fb);
-          }
-          filled |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        for (int lo = u.lo; ok && lo < u.hi; lo += chunk) {
+          const int span = min(chunk, u.hi - lo);
+          for (int it = 0; it < TERMS * span; ++it) {
+            if (!wait_bounded(ptx::smem_u32(&empty[stage]), phase ^ 1u, ctl, SITE_PRODUCER_EMPTY)) {
+              ok = false;
+              break;
+            }
+            const int term = PLANES == 1 ? 0 : it / span;
+            const int k0 = (lo + it - term * span) * kTileK;  // stages past the k axis load zeros
+            const int pa = PLANES == 1 ? 0 : plane_a(term), pb = PLANES == 1 ? 0 : plane_b(term);
+            const uint32_t fb_local = ptx::smem_u32(&full[stage]);
+            const uint32_t fb = ptx::mapa_shared(fb_local, 0);
+            if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2u * kStage);
+            const uint32_t sa = ptx::smem_u32(smem + stage * kStage), sb = sa + kSub;
+            if constexpr (a_m_major(MODE)) {
+              ptx::tma_load_3d_pair(sa, &mapA, m0, k0, pa, fb);
+              ptx::tma_load_3d_pair(sa + 8192, &mapA, m0 + 64, k0, pa, fb);
+            } else {
+              ptx::tma_load_3d_pair(sa, &mapA, k0, m0, pa, fb);
+            }
+            if constexpr (b_n_major(MODE)) {
+              const int kr = k0 + (MODE == HEAD_DH ? args.b_row0 : 0);
+              ptx::tma_load_3d_pair(sb, &mapB, n0, kr, pb, fb);
+              ptx::tma_load_3d_pair(sb + 8192, &mapB, n0 + 64, kr, pb, fb);
+            } else {
+              ptx::tma_load_3d_pair(sb, &mapB, k0, args.b_row0 + n0, pb, fb);
+            }
+            filled |= 1u << stage;
+            last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
       }
@@ -449,33 +519,40 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
       bool ok = true;
       for (int i = worker; ok && i < tiles.units; i += workers) {
         const HeadUnit u = head_unit<MODE>(args, tiles, i);
-        if (u.lo >= u.hi) continue;
-        if (!wait_bounded(ptx::smem_u32(&acc_empty[acc]), acc_phase ^ 1u, ctl, SITE_MMA_ACC_EMPTY)) break;
-        ptx::tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * ACC);
-        for (int kb = u.lo; kb < u.hi; ++kb) {
-          if (!wait_bounded(ptx::smem_u32(&full[stage]), phase, ctl, SITE_MMA_FULL)) {
+        for (int lo = u.lo; ok && lo < u.hi; lo += chunk) {
+          if (!wait_bounded(ptx::smem_u32(&acc_empty[acc]), acc_phase ^ 1u, ctl, SITE_MMA_ACC_EMPTY)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after_sync();
-          const uint32_t a0 = ptx::smem_u32(smem + stage * kStage), b0 = a0 + kSub;
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * ACC);
+          const int stages = TERMS * min(chunk, u.hi - lo);
+          for (int it = 0; it < stages; ++it) {
+            if (!wait_bounded(ptx::smem_u32(&full[stage]), phase, ctl, SITE_MMA_FULL)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after_sync();
+            const uint32_t a0 = ptx::smem_u32(smem + stage * kStage), b0 = a0 + kSub;
 #pragma unroll
-          for (int k = 0; k < kTileK / 16; ++k) {
-            const uint64_t da = a_m_major(MODE) ? sw128_desc(a0 + k * 2048, 8192, 1024) : sw128_desc(a0 + k * 32, 16, 1024);
-            const uint64_t db = b_n_major(MODE) ? sw128_desc(b0 + k * 2048, 8192, 1024) : sw128_desc(b0 + k * 32, 16, 1024);
-            ptx::tc_mma_f16_pair(d_tmem, da, db, idesc, (kb != u.lo || k != 0) ? 1u : 0u);
+            for (int k = 0; k < kTileK / 16; ++k) {
+              const uint64_t da =
+                  a_m_major(MODE) ? sw128_desc(a0 + k * 2048, 8192, 1024) : sw128_desc(a0 + k * 32, 16, 1024);
+              const uint64_t db =
+                  b_n_major(MODE) ? sw128_desc(b0 + k * 2048, 8192, 1024) : sw128_desc(b0 + k * 32, 16, 1024);
+              ptx::tc_mma_f16_pair(d_tmem, da, db, idesc, (it != 0 || k != 0) ? 1u : 0u);
+            }
+            ptx::tc_commit_pair_multicast(ptx::smem_u32(&empty[stage]), 0x3);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          ptx::tc_commit_pair_multicast(ptx::smem_u32(&empty[stage]), 0x3);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (!ok) break;
+          ptx::tc_commit_pair_multicast(ptx::smem_u32(&acc_full[acc]), 0x3);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
         }
-        if (!ok) break;
-        ptx::tc_commit_pair_multicast(ptx::smem_u32(&acc_full[acc]), 0x3);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
       }
       ptx::tc_commit_pair(ptx::smem_u32(drain));
       wait_teardown(ptx::smem_u32(drain), 0, ctl, SITE_DRAIN);
@@ -485,31 +562,50 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
     // --------------------------------------------------------- epilogue
     const int quarter = warp & 3;
     uint8_t* stage_base = sC + (warp - 2) * 2 * 4096;
-    const int n = MODE == HEAD_DW ? 0 : min(*args.count, args.T);
+    const int n = min(*args.count, args.T);
     int acc = 0, sbuf = 0;
     uint32_t acc_phase = 0;
-    for (int i = worker; i < tiles.units; i += workers) {
+    bool ok = true;
+    for (int i = worker; ok && i < tiles.units; i += workers) {
       const HeadUnit u = head_unit<MODE>(args, tiles, i);
-      if (u.lo >= u.hi) continue;
-      if (!warp_wait(ptx::smem_u32(&acc_full[acc]), acc_phase, ctl, SITE_EPI_ACC_FULL)) break;
-      ptx::tc_fence_after_sync();
-      const uint32_t tbase =
-          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * ACC);
       const int row0 = u.mb * kHeadTile + half * kTileM + quarter * 32;
-      if constexpr (MODE == HEAD_STATS) {
-        if (row0 < n) epilogue_stats(tbase, row0 + lane, n, u.nb, args);
-      } else if constexpr (MODE == HEAD_DZ) {
-        epilogue_dz(tbase, row0, n, u.nb, args, &mapC, stage_base, sbuf, lane);
-      } else if constexpr (MODE == HEAD_DH) {
-        epilogue_dh(tbase, row0, u, args, &mapC, stage_base, sbuf, lane);
-      } else {
-        epilogue_dw(tbase, row0, u.nb, args, &mapC, stage_base, sbuf, lane);
+      for (int lo = u.lo; lo < u.hi; lo += chunk) {
+        if (!warp_wait(ptx::smem_u32(&acc_full[acc]), acc_phase, ctl, SITE_EPI_ACC_FULL)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after_sync();
+        const uint32_t tbase =
+            tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * ACC);
+        if constexpr (MODE == HEAD_STATS) {
+          if (row0 < n) epilogue_stats(tbase, row0 + lane, n, u.nb, args);
+        } else if constexpr (MODE == HEAD_DZ) {
+          epilogue_dz<PLANES>(tbase, row0, n, u.nb, args, &mapC, stage_base, sbuf, lane);
+        } else if constexpr (PLANES > 1) {
+          // a chunk's sum of the full-size terms took 4 steps a stage
+          const float put_back = 1.0f + kStepLoss * static_cast<float>(4 * min(chunk, u.hi - lo));
+          const int row = row0 + lane;
+          float* out = static_cast<float*>(args.out);
+          if constexpr (MODE == HEAD_DH) {
+            if (row0 < n)
+              epilogue_f32(tbase, out + u.split * args.split_stride + static_cast<int64_t>(row) * args.ld_out, row < n,
+                           u.nb * kHeadTile, args.D, put_back, true, args.reduce || lo > u.lo);
+          } else {
+            if (row0 < args.cols)
+              epilogue_f32(tbase, out + static_cast<int64_t>(args.out_row0 + row) * args.ld_out, row < args.cols,
+                           u.nb * kHeadTile, args.D, put_back * *args.factor, args.store_granule == 16, lo > u.lo);
+          }
+        } else if constexpr (MODE == HEAD_DH) {
+          epilogue_dh(tbase, row0, u, args, &mapC, stage_base, sbuf, lane);
+        } else {
+          epilogue_dw(tbase, row0, u.nb, args, &mapC, stage_base, sbuf, lane);
+        }
+        ptx::tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
       }
-      ptx::tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
     }
     if (lane == 0) ptx::bulk_wait_group_read<0>();
     __syncwarp();
@@ -524,11 +620,11 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
   }
 }
 
-template <int MODE>
+template <int MODE, int PLANES>
 cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC, const HeadArgs& args,
                    int pairs, cudaStream_t stream) {
   constexpr int smem = head_smem(MODE);
-  auto kernel = head_kernel<MODE>;
+  auto kernel = head_kernel<MODE, PLANES>;
   static std::atomic<uint64_t> done_mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -544,27 +640,34 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
   cfg.blockDim = dim3(32 * (2 + kEpiWarps), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, mA, mB, mC, args);
 }
 
 }  // namespace
 
-cudaError_t launch_head(int mode, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
-                        const HeadArgs& args, int pairs, cudaStream_t stream) {
+cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUtensorMap& mapB,
+                        const CUtensorMap& mapC, const HeadArgs& args, int pairs, cudaStream_t stream) {
+#define TGEMM_HEAD(MODE)                                                                         \
+  case MODE:                                                                                     \
+    return planes == 1 ? launch<MODE, 1>(mapA, mapB, mapC, args, pairs, stream)                  \
+                       : launch<MODE, kPlanes>(mapA, mapB, mapC, args, pairs, stream)
   switch (mode) {
-    case HEAD_STATS: return launch<HEAD_STATS>(mapA, mapB, mapC, args, pairs, stream);
-    case HEAD_DZ: return launch<HEAD_DZ>(mapA, mapB, mapC, args, pairs, stream);
-    case HEAD_DH: return launch<HEAD_DH>(mapA, mapB, mapC, args, pairs, stream);
-    case HEAD_DW: return launch<HEAD_DW>(mapA, mapB, mapC, args, pairs, stream);
+    TGEMM_HEAD(HEAD_STATS);
+    TGEMM_HEAD(HEAD_DZ);
+    TGEMM_HEAD(HEAD_DH);
+    TGEMM_HEAD(HEAD_DW);
     default: return cudaErrorInvalidValue;
   }
+#undef TGEMM_HEAD
 }
 
 }  // namespace tgemm

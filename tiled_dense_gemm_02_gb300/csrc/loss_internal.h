@@ -15,15 +15,10 @@ namespace tgemm {
 int host_device(int* sms, int* pairs, unsigned int** status);
 // Records a failed CUDA call's text and returns TGEMM_ERR_LAUNCH.
 int host_cuda_fail(cudaError_t e, const char* what);
-// Cached tensor maps, 128-byte swizzle, zero fill (after host_device).
+// Cached 3-D tensor map, 128-byte swizzle, zero fill (after host_device).
 // type: 0 bf16, 1 f16, 2 f32.
-int host_map_2d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t pitch_bytes,
-                uint32_t box_cols, uint32_t box_rows);
 int host_map_3d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t depth,
                 int64_t pitch_bytes, int64_t depth_bytes, uint32_t box_cols, uint32_t box_rows);
-// fp32 product C = A . B + beta C on the CUDA cores.
-int host_gemm_f32(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda, const float* B, int64_t ldb, float* C,
-                  int64_t ldc, float beta, cudaStream_t stream);
 // Adds tensor-core launches to the host counters.
 void host_count_launches(int n);
 bool host_ranges_overlap(uint64_t a0, uint64_t a1, uint64_t b0, uint64_t b1);
@@ -43,10 +38,16 @@ struct HeadRows {
   float* q;           // T x K
   float* own;         // T: sum q log q (distillation), else null
   unsigned char* flags;  // T (distillation), else null
-  float4* coef;       // T, gathered: {c_p, c_q, lse * log2(e), lse} (backward), else null
-  void* h;            // gathered rows, pitch ldh elements
+  float4* coef;       // T, gathered: {c_p, c_q, lse * log2(e), 0} (backward), else null
+  void* h;            // gathered rows, pitch ldh 16-bit elements
   int64_t ldh;
+  int64_t plane;      // elements between the planes of fp32 rows
 };
+
+// fp32 operands are split into three bf16 planes, x = hi + mid + lo: 3 x 8
+// significant bits hold all 24 of x.  A product of two of them is then six
+// plane products (those of relative size 2^-24 and below are left out).
+constexpr int kPlanes = 3;
 
 constexpr unsigned char kRowIgnored = 0, kRowCounts = 1, kRowBad = 2;
 // Gathered rows are zero-filled up to a multiple of this (and at least one such block), capped at T.
@@ -61,8 +62,7 @@ struct GatherArgs {
   const int64_t* targets;    // cross entropy, else null
   int64_t ignore_index;
   float smoothing, z_loss, scale;
-  float range;               // power of two that 16-bit gradients are scaled with (0: fp32, no normalisation)
-  int zero_rows;             // 1: zero every gathered row past the count, 0: up to the next block
+  float range;               // power of two that the stored gradients are scaled with
   const float* lse;          // backward: the forward call's, else null
   const float* grad;         // backward
   float* loss_out;           // forward: rows that do not count are written here
@@ -81,30 +81,28 @@ cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T,
 // dH row t = factor * sum over splits of acc[s][place[t]], or 0.
 cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
                              const HeadRows& rows, int type, void* dH, int64_t lddh, cudaStream_t stream);
-// fp32 path: statistics of one piece of logits Z [T x cols], and their
-// gradient in place.
-cudaError_t launch_stats_f32(const float* Z, int64_t ldz, int cols, int col0, int T, int K, float k2, float flat,
-                             const HeadRows& rows, float2* ms, float* dot, cudaStream_t stream);
-cudaError_t launch_dz_f32(float* Z, int64_t ldz, int cols, int col0, int T, int K, float scale, float flat,
-                          const HeadRows& rows, cudaStream_t stream);
+// The three planes of an fp32 matrix (vec: 16-byte aligned rows); each plane
+// has pitch ld_out, a multiple of 8.
+cudaError_t launch_split(const float* W, int64_t ldw, void* out, int64_t ld_out, int64_t plane, int rows, int cols,
+                         bool vec, cudaStream_t stream);
 
 // ------------------------------------------------------- pair products
 enum HeadMode : int {
   HEAD_STATS = 0,  // logits tile -> row statistics
-  HEAD_DZ = 1,     // logits tile -> gradient of the logits (16-bit)
+  HEAD_DZ = 1,     // logits tile -> gradient of the logits (16-bit, or its three planes)
   HEAD_DH = 2,     // dz . W      -> fp32 sums
-  HEAD_DW = 3      // dz^T . H    -> dW (16-bit)
+  HEAD_DW = 3      // dz^T . H    -> dW
 };
 
 struct HeadArgs {
   const int* count;
-  int T, V, K;
-  int cols;       // columns of this piece (logits), or their number rounded up to 64-deep stages' extent (DH: K)
+  int T, V, K, D;
+  int cols;       // columns of this piece
   int col0;       // vocabulary entry of the piece's column 0
-  int b_row0;     // STATS, DZ: row of the weight map for column 0; DH: the same along K
-  int D;
-  int k_blocks;   // 64-deep stages (DW: from the count)
-  int splits, k_per_split;  // DH
+  int b_row0;     // STATS, DZ, DH: row of the weight map for the piece's column 0
+  int k_blocks;   // 64-deep stages of the k axis (DW: from the count)
+  int splits, k_per_split;  // DH: ranges of the k axis summed apart
+  int chunk;      // fp32, DH and DW: stages summed in tensor memory before they are added to the result
   int reduce;     // DH: add to the sums instead of storing them
   int group_m;
   int bf16;
@@ -118,17 +116,28 @@ struct HeadArgs {
   int tile0;      // STATS: index of the piece's first column tile
   const float4* coef;     // DZ
   const float* factor;    // DW
-  void* out;              // DW
+  void* out;              // DW; fp32 DH
   int64_t ld_out;
+  int64_t split_stride;   // fp32 DH: elements between the splits' sums
   int store_granule;      // DW: 0 bulk-tensor stores, else the granule of per-thread stores
   int out_row0;           // DW: row of dW for the piece's column 0
   unsigned long long timeout_ns;
   unsigned int* status;
 };
 
+// Mean loss of one tensor-memory accumulation step (a product of 16 terms
+// added to the fp32 sum), relative to the final sum.  The adder truncates, so
+// every step moves the sum towards 0 by a part of its last bit.  Measured
+// against 64-bit sums of signed data, the sums of K terms come out smaller by
+// K / 16 steps of 0.10 to 0.15 units of 2^-23 (bf16, K = 256 to 8192; 0.14 to
+// 0.15 for fp16): an eighth is put back, which takes lse at D = 4096 from
+// 1.2e-6 off to a few 1e-7.
+constexpr float kStepLoss = 1.0f / (1 << 26);
+
 // Output tile of every mode: 256 x 256 per CTA pair.
 constexpr int kHeadTile = 256;
-cudaError_t launch_head(int mode, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
+// planes: 1 (16-bit operands) or 3 (fp32).
+cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
                         const HeadArgs& args, int pairs, cudaStream_t stream);
 
 }  // namespace tgemm

@@ -1,19 +1,43 @@
 // Row kernels of the vocabulary-head losses: the teacher's lists, the gather of
 // the rows that count, the joining of the tiles' statistics, the last step of
-// dH, and the softmax steps of the fp32 path.  All of them are bound by memory
-// or by latency and move a small part of what the products do.
+// dH, and the bf16 planes of fp32 operands.  All of them are bound by memory or
+// by latency and move a small part of what the products do.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <climits>
 
 #include "loss_internal.h"
+#include "ptx.cuh"
 
 namespace tgemm {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Every kernel of a call is launched as a programmatic dependent of the one
+// before it: its blocks may be set up while that one ends, and touch memory
+// only after it has completed.  Each kernel waits before it does anything, so
+// completion carries over the whole chain.
+__device__ __forceinline__ void chain() {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), int64_t blocks, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -36,6 +60,7 @@ __global__ void __launch_bounds__(kListWarps * 32)
     distill_lists_kernel(const int64_t* __restrict__ ids, int64_t ld_ids, const float* __restrict__ logits,
                          int64_t ld_logits, int T, int V, int K, float scale, HeadRows rows) {
   __shared__ int s_id[kListWarps][kListMax];
+  chain();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kListWarps + warp;
   if (t >= T) return;
@@ -120,6 +145,41 @@ __device__ __forceinline__ void copy_row(uint8_t* dst, const uint8_t* src, int64
   for (int64_t i = lane; i < n; i += 32) d[i] = s[i];
 }
 
+// An fp32 row as three bf16 planes.  A value that is not finite goes to the
+// first plane alone.  32 lanes, four elements each; the planes' pitch is a
+// multiple of 8, so whole groups are written.
+__device__ __forceinline__ void split_row(uint16_t* dst, int64_t plane, const float* src, int cols, bool vec,
+                                          int lane) {
+#pragma unroll 2
+  for (int c = lane * 4; c < cols; c += 128) {
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (vec && c + 4 <= cols) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(src + c));
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < cols) x[i] = __ldg(src + c + i);
+    }
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p) {
+      uint32_t w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        const float lo = __low2float(b), hi = __high2float(b);
+        x[2 * i] = isfinite(lo) ? x[2 * i] - lo : 0.0f;
+        x[2 * i + 1] = isfinite(hi) ? x[2 * i + 1] - hi : 0.0f;
+      }
+      *reinterpret_cast<uint2*>(dst + p * plane + c) = make_uint2(w[0], w[1]);
+    }
+  }
+}
+
 // Every block counts the rows that count over all T (their flags are a few KB
 // in L2) to know where its own go, so the gather is one launch with a fixed
 // order.  In the backward pass it also finds the largest |grad|, which the
@@ -130,6 +190,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
   __shared__ int s_before[kGatherThreads / 32], s_total[kGatherThreads / 32], s_warp[kGatherThreads / 32];
   __shared__ float s_g[kGatherThreads / 32], s_c[kGatherThreads / 32];
   __shared__ int s_src[kGatherThreads];
+  chain();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = blockIdx.x * rows_per, t1 = min(a.T, t0 + rows_per);
   int before = 0, total = 0;
@@ -175,14 +236,14 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
   // makes the softmax's coefficient larger than the target's
   const float unit = gmax > 0.0f ? gmax : 1.0f;
   float pow2 = 1.0f;
-  if (a.range != 0.0f && cmax > unit) {
+  if (cmax > unit) {
     int e;
     const float f = frexpf(cmax / unit, &e);
     pow2 = exp2f(static_cast<float>(min(f == 0.5f ? e - 1 : e, 60)));
   }
   if (blockIdx.x == 0 && tid == 0) {
     *a.rows.count = total;
-    if (a.grad) *a.rows.factor = a.range == 0.0f ? 1.0f : unit * (a.scale * pow2 / a.range);
+    if (a.grad) *a.rows.factor = unit * (a.scale * pow2 / a.range);
   }
   if (t < t1) {
     const int place = before + local + __popc(ballot & ((1u << lane) - 1u));
@@ -196,16 +257,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
       a.rows.source[place] = t;
       s_src[place - before] = t;
       if (a.grad) {
-        float cp = grad_p(a, t), cq = a.grad[t];
-        if (a.range == 0.0f) {
-          cp *= a.scale;
-          cq *= a.scale;
-        } else {
-          const float up = a.range / pow2;
-          cp = cp / unit * up;
-          cq = cq / unit * up;
-        }
-        a.rows.coef[place] = make_float4(cp, cq, a.lse[t] * kLog2e, a.lse[t]);
+        const float up = a.range / pow2;
+        a.rows.coef[place] = make_float4(grad_p(a, t) / unit * up, a.grad[t] / unit * up, a.lse[t] * kLog2e, 0.0f);
       }
     } else if (a.loss_out) {
       const float v = flag == kRowBad ? __int_as_float(0x7FC00000) : 0.0f;
@@ -215,11 +268,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
   }
   __syncthreads();
   const int64_t row_bytes = static_cast<int64_t>(a.D) * a.es;
-  uint8_t* const out = static_cast<uint8_t*>(a.rows.h);
-  const int64_t out_pitch = a.rows.ldh * a.es;
+  uint16_t* const out = static_cast<uint16_t*>(a.rows.h);
   for (int r = warp; r < mine; r += kGatherThreads / 32) {
     const uint8_t* src = static_cast<const uint8_t*>(a.H) + static_cast<int64_t>(s_src[r]) * a.ldh * a.es;
-    uint8_t* dst = out + static_cast<int64_t>(before + r) * out_pitch;
+    uint16_t* row = out + static_cast<int64_t>(before + r) * a.rows.ldh;
+    if (a.es == 4) {
+      split_row(row, a.rows.plane, reinterpret_cast<const float*>(src), a.D, a.granule == 16, lane);
+      continue;
+    }
+    uint8_t* dst = reinterpret_cast<uint8_t*>(row);
     int g = a.granule;
     while (row_bytes % g) g >>= 1;
     switch (g) {
@@ -229,13 +286,16 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
       default: copy_row<2>(dst, src, row_bytes, lane); break;
     }
   }
-  // zeros after the last gathered row (the pitch is a multiple of 16 bytes)
-  const int blocks = max(1, (total + kRowBlock - 1) / kRowBlock);
-  const int end = a.zero_rows ? a.T : static_cast<int>(min(static_cast<int64_t>(a.T), int64_t(blocks) * kRowBlock));
-  for (int r = total + blockIdx.x * (kGatherThreads / 32) + warp; r < end; r += gridDim.x * (kGatherThreads / 32)) {
-    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * out_pitch);
-    for (int64_t i = lane; i < out_pitch / 16; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
+  // zeros from the last gathered row to the end of its block of rows, which
+  // the products read (the pitch is a multiple of 16 bytes)
+  const int64_t blocks = max(1, (total + kRowBlock - 1) / kRowBlock);
+  const int end = static_cast<int>(min(static_cast<int64_t>(a.T), blocks * kRowBlock));
+  const int planes = a.es == 4 ? kPlanes : 1;
+  for (int r = total + blockIdx.x * (kGatherThreads / 32) + warp; r < end; r += gridDim.x * (kGatherThreads / 32))
+    for (int p = 0; p < planes; ++p) {
+      uint4* dst = reinterpret_cast<uint4*>(out + p * a.rows.plane + static_cast<int64_t>(r) * a.rows.ldh);
+      for (int64_t i = lane; i < a.rows.ldh / 8; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
 }
 
 // --------------------------------------------------- joining tile statistics
@@ -253,6 +313,7 @@ __global__ void __launch_bounds__(kCombineRows * kCombineSlots)
     combine_kernel(const float2* __restrict__ ms, const float* __restrict__ dot, int tiles, int T, float scale,
                    float z_loss, HeadRows rows, float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ float s_m[kCombineSlots][kCombineRows], s_s[kCombineSlots][kCombineRows], s_d[kCombineSlots][kCombineRows];
+  chain();
   const int n = min(*rows.count, T);
   const int r0 = blockIdx.x * kCombineRows;
   if (r0 >= n) return;
@@ -306,6 +367,7 @@ template <typename Out>
 __global__ void __launch_bounds__(128) finish_dh_kernel(const float* __restrict__ acc, int64_t ld_acc,
                                                         int64_t split_stride, int splits, int D, HeadRows rows,
                                                         Out* __restrict__ dH, int64_t lddh, int wide) {
+  chain();
   const int t = blockIdx.x;
   const int place = rows.place[t];
   const float f = *rows.factor;
@@ -340,80 +402,21 @@ __global__ void __launch_bounds__(128) finish_dh_kernel(const float* __restrict_
   }
 }
 
-// ------------------------------------------------------------------ fp32 path
-constexpr int kF32Threads = 256;
-__device__ __forceinline__ float block_reduce(float v, bool is_max, float* s) {
-  v = is_max ? warp_max(v) : warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s[0];
-  for (int w = 1; w < kF32Threads / 32; ++w) v = is_max ? fmaxf(v, s[w]) : v + s[w];
-  return v;
-}
-
-// One block per gathered row.
-__global__ void __launch_bounds__(kF32Threads) stats_f32_kernel(const float* __restrict__ Z, int64_t ldz, int cols,
-                                                                int col0, int T, int K, float k2, float flat,
-                                                                HeadRows rows, float2* __restrict__ ms,
-                                                                float* __restrict__ dot) {
-  __shared__ float s[kF32Threads / 32];
-  const int r = blockIdx.x;
-  if (r >= min(*rows.count, T)) return;
-  const float* z = Z + static_cast<int64_t>(r) * ldz;
-  float m = -INFINITY, zs = 0.0f;
-  for (int c = threadIdx.x; c < cols; c += kF32Threads) {
-    m = fmaxf(m, z[c]);
-    zs += z[c];
-  }
-  m = block_reduce(m, true, s);
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float sum = 0.0f;
-  for (int c = threadIdx.x; c < cols; c += kF32Threads) sum += exp2f((z[c] - ref) * k2);
-  sum = block_reduce(sum, false, s);
-  const int64_t list = static_cast<int64_t>(rows.source[r]) * K;
-  float d = 0.0f;
-  for (int k = threadIdx.x; k < K; k += kF32Threads) {
-    const int c = rows.ids[list + k] - col0;
-    if (c >= 0 && c < cols) d = fmaf(rows.q[list + k], z[c], d);
-  }
-  if (flat != 0.0f) d = fmaf(flat, zs, d);
-  d = block_reduce(d, false, s);
-  if (threadIdx.x == 0) {
-    ms[r] = make_float2(m * k2, sum);
-    dot[r] = d;
-  }
-}
-
-__global__ void __launch_bounds__(kF32Threads) dz_f32_kernel(float* __restrict__ Z, int64_t ldz, int cols, int col0,
-                                                             int T, int K, float scale, float flat, HeadRows rows) {
-  const int r = blockIdx.x;
-  float* z = Z + static_cast<int64_t>(r) * ldz;
-  if (r >= min(*rows.count, T)) {
-    for (int c = threadIdx.x; c < cols; c += kF32Threads) z[c] = 0.0f;
-    return;
-  }
-  const float4 k = rows.coef[r];
-  for (int c = threadIdx.x; c < cols; c += kF32Threads) z[c] = k.x * expf(fmaf(z[c], scale, -k.w)) - k.y * flat;
-  __syncthreads();
-  // equal ids are neighbours: the first of them subtracts all their masses
-  const int64_t list = static_cast<int64_t>(rows.source[r]) * K;
-  for (int i = threadIdx.x; i < K; i += kF32Threads) {
-    const int id = rows.ids[list + i], c = id - col0;
-    if (c < 0 || c >= cols || (i > 0 && rows.ids[list + i - 1] == id)) continue;
-    float q = 0.0f;
-    for (int j = i; j < K && rows.ids[list + j] == id; ++j) q += rows.q[list + j];
-    z[c] -= k.y * q;
-  }
+// One block per 4 rows of an fp32 matrix, read once and written as planes.
+__global__ void __launch_bounds__(128) split_kernel(const float* __restrict__ W, int64_t ldw, uint16_t* __restrict__ out,
+                                                    int64_t ld_out, int64_t plane, int rows, int cols, int vec) {
+  chain();
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  split_row(out + r * ld_out, plane, W + r * ldw, cols, vec != 0, threadIdx.x & 31);
 }
 
 }  // namespace
 
 cudaError_t launch_distill_lists(const int64_t* ids, int64_t ld_ids, const float* logits, int64_t ld_logits, int T,
                                  int V, int K, float scale, const HeadRows& rows, cudaStream_t stream) {
-  distill_lists_kernel<<<(T + kListWarps - 1) / kListWarps, kListWarps * 32, 0, stream>>>(ids, ld_ids, logits,
-                                                                                         ld_logits, T, V, K, scale, rows);
-  return cudaGetLastError();
+  return launch_chained(distill_lists_kernel, (T + kListWarps - 1) / kListWarps, kListWarps * 32, stream, ids, ld_ids,
+                        logits, ld_logits, T, V, K, scale, rows);
 }
 
 cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
@@ -421,16 +424,13 @@ cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
   const int target = 4 * sms;
   int rows_per = (a.T + target - 1) / target;
   rows_per = rows_per < 8 ? 8 : (rows_per > kGatherThreads ? kGatherThreads : rows_per);
-  const int blocks = a.T > 0 ? (a.T + rows_per - 1) / rows_per : 1;
-  gather_kernel<<<blocks, kGatherThreads, 0, stream>>>(a, rows_per);
-  return cudaGetLastError();
+  return launch_chained(gather_kernel, (a.T + rows_per - 1) / rows_per, kGatherThreads, stream, a, rows_per);
 }
 
 cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T, float scale, float z_loss,
                            const HeadRows& rows, float* loss, float* lse, cudaStream_t stream) {
-  combine_kernel<<<(T + kCombineRows - 1) / kCombineRows, kCombineRows * kCombineSlots, 0, stream>>>(
-      ms, dot, tiles, T, scale, z_loss, rows, loss, lse);
-  return cudaGetLastError();
+  return launch_chained(combine_kernel, (T + kCombineRows - 1) / kCombineRows, kCombineRows * kCombineSlots, stream, ms,
+                        dot, tiles, T, scale, z_loss, rows, loss, lse);
 }
 
 cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
@@ -438,27 +438,19 @@ cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_str
   const int es = type == 2 ? 4 : 2;
   const int wide = reinterpret_cast<uint64_t>(dH) % (4 * es) == 0 && lddh % 4 == 0 ? 1 : 0;
   if (type == 0)
-    finish_dh_kernel<<<T, 128, 0, stream>>>(acc, ld_acc, split_stride, splits, D, rows,
-                                            static_cast<__nv_bfloat16*>(dH), lddh, wide);
-  else if (type == 1)
-    finish_dh_kernel<<<T, 128, 0, stream>>>(acc, ld_acc, split_stride, splits, D, rows, static_cast<__half*>(dH), lddh,
-                                            wide);
-  else
-    finish_dh_kernel<<<T, 128, 0, stream>>>(acc, ld_acc, split_stride, splits, D, rows, static_cast<float*>(dH), lddh,
-                                            wide);
-  return cudaGetLastError();
+    return launch_chained(finish_dh_kernel<__nv_bfloat16>, T, 128, stream, acc, ld_acc, split_stride, splits, D, rows,
+                          static_cast<__nv_bfloat16*>(dH), lddh, wide);
+  if (type == 1)
+    return launch_chained(finish_dh_kernel<__half>, T, 128, stream, acc, ld_acc, split_stride, splits, D, rows,
+                          static_cast<__half*>(dH), lddh, wide);
+  return launch_chained(finish_dh_kernel<float>, T, 128, stream, acc, ld_acc, split_stride, splits, D, rows,
+                        static_cast<float*>(dH), lddh, wide);
 }
 
-cudaError_t launch_stats_f32(const float* Z, int64_t ldz, int cols, int col0, int T, int K, float k2, float flat,
-                             const HeadRows& rows, float2* ms, float* dot, cudaStream_t stream) {
-  stats_f32_kernel<<<T, kF32Threads, 0, stream>>>(Z, ldz, cols, col0, T, K, k2, flat, rows, ms, dot);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_dz_f32(float* Z, int64_t ldz, int cols, int col0, int T, int K, float scale, float flat,
-                          const HeadRows& rows, cudaStream_t stream) {
-  dz_f32_kernel<<<T, kF32Threads, 0, stream>>>(Z, ldz, cols, col0, T, K, scale, flat, rows);
-  return cudaGetLastError();
+cudaError_t launch_split(const float* W, int64_t ldw, void* out, int64_t ld_out, int64_t plane, int rows, int cols,
+                         bool vec, cudaStream_t stream) {
+  return launch_chained(split_kernel, (rows + 3) / 4, 128, stream, W, ldw, static_cast<uint16_t*>(out), ld_out, plane,
+                        rows, cols, vec ? 1 : 0);
 }
 
 }  // namespace tgemm

@@ -92,26 +92,42 @@ def distill_backward(T, V, D, K, H, ldh, W, ldw, ids, ld_ids, logits, ld_logits,
 
 
 # ------------------------------------------------------------ torch helpers
+# The checks below read each property of a tensor once, and what depends on
+# plain numbers only (options, workspace sizes) is computed once per set of
+# numbers: a call costs the host little more than its launches.
 
-def _ld(t):
-    return max(t.stride(0), t.shape[1], 1) if t.shape[0] > 1 else max(t.shape[1], 1)
+@functools.lru_cache(maxsize=256)
+def _options(scale, label_smoothing, z_loss, piece, ignore_index):
+    return ctypes.byref(LossOptions(scale=scale, label_smoothing=label_smoothing, z_loss=z_loss, piece=piece,
+                                    ignore_index=ignore_index))
 
 
-def _matrix(name, t, rows=None, cols=None, dtype=None):
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be a matrix of shape [{'T' if rows is None else rows}, "
-                         f"{'D' if cols is None else cols}], got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) < t.shape[1]:
+@functools.lru_cache(maxsize=1024)
+def _size(backward, T, V, D, K, w_offset, ldw, code, options):
+    n = ctypes.c_size_t(0)
+    st = _lib.tgemm_loss_workspace_size(int(backward), T, V, D, K, w_offset, ldw, code, options, ctypes.byref(n))
+    if st != OK:
+        raise TgemmError(st, "tgemm_loss_workspace_size")
+    return n.value
+
+
+def _pitch(name, t, rows, cols):
+    """Row pitch of a matrix with unit column stride and rows that do not overlap."""
+    ld, step = t.stride()
+    if rows < 2:
+        ld = cols
+    elif ld < cols:
         raise ValueError(f"{name} must have rows that do not overlap")
-    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+    if cols > 1 and step != 1 and rows:
         raise ValueError(f"{name} must have unit column stride")
+    return ld if ld > 1 else 1
 
 
-def _vector(name, t, n, dtype):
+def _vector(name, t, n, dtype, device):
     if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype:
         raise ValueError(f"{name} must be a vector of {n} {dtype} values, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the device of hidden")
     return t if n < 2 or t.stride(0) == 1 else t.contiguous()
 
 
@@ -122,9 +138,9 @@ def _on_stream(function):
 
     @functools.wraps(function)
     def call(hidden, *args, stream=None, **kwargs):
-        import torch
         if stream is None:
             return function(hidden, *args, **kwargs)
+        import torch
         other = torch.cuda.ExternalStream(stream, device=hidden.device) if stream else \
             torch.cuda.default_stream(hidden.device)
         with torch.cuda.stream(other):
@@ -134,76 +150,67 @@ def _on_stream(function):
 
 
 class _Head:
-    """The arguments every call shares, checked."""
+    """The arguments every call shares, checked, and its workspace."""
+    __slots__ = ("torch", "T", "V", "D", "code", "device", "matrices", "options", "workspace")
 
-    def __init__(self, hidden, weight, options, workspace, backward, K):
+    def __init__(self, hidden, weight, backward, K, options, workspace):
         import torch
         self.torch = torch
-        _matrix("hidden", hidden)
-        _matrix("weight", weight, cols=hidden.shape[1], dtype=hidden.dtype)
-        codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-        if hidden.dtype not in codes:
-            raise ValueError(f"unsupported dtype: {hidden.dtype}")
-        for name, t in (("hidden", hidden), ("weight", weight)):
-            if not t.is_cuda or t.device != hidden.device:
-                raise ValueError(f"{name} must be on one CUDA device")
-        self.hidden, self.weight, self.dev = hidden, weight, hidden.device
-        self.T, self.D, self.V = hidden.shape[0], hidden.shape[1], weight.shape[0]
-        self.code = codes[hidden.dtype]
-        self.ldh, self.ldw = _ld(hidden), _ld(weight)
-        self.options = _opts(options)
-        self.stream = torch.cuda.current_stream(self.dev).cuda_stream
-        n = ctypes.c_size_t(0)
-        self.check(_lib.tgemm_loss_workspace_size(int(backward), self.T, self.V, self.D, K, weight.data_ptr(),
-                                                  self.ldw, self.code, self.options, ctypes.byref(n)),
-                   "tgemm_loss_workspace_size")
+        if hidden.dim() != 2 or weight.dim() != 2:
+            raise ValueError("hidden [T, D] and weight [V, D] must be matrices")
+        T, D = hidden.shape
+        V, columns = weight.shape
+        dtype = hidden.dtype
+        if columns != D or weight.dtype != dtype:
+            raise ValueError(f"weight must be [V, {D}] {dtype}, got {tuple(weight.shape)} {weight.dtype}")
+        code = BF16 if dtype == torch.bfloat16 else F16 if dtype == torch.float16 else F32
+        if code == F32 and dtype != torch.float32:
+            raise ValueError(f"unsupported dtype: {dtype}")
+        device = hidden.get_device()
+        if device < 0 or weight.get_device() != device:
+            raise ValueError("hidden and weight must be on one CUDA device")
+        ldh, ldw = _pitch("hidden", hidden, T, D), _pitch("weight", weight, V, D)
+        w = weight.data_ptr()
+        self.T, self.V, self.D, self.code, self.device = T, V, D, code, device
+        self.matrices = (hidden.data_ptr(), ldh, w, ldw)
+        self.options = _options(*options)
+        need = _size(backward, T, V, D, K, w % 16, ldw, code, self.options)
         if workspace is None:
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=self.dev)
-        elif workspace.device != self.dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < n.value:
-            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {n.value} bytes on {self.dev}")
+            workspace = torch.empty(need, dtype=torch.uint8, device=hidden.device)
+        elif workspace.get_device() != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+                workspace.numel() < need:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on the device of "
+                             "hidden")
         self.workspace = workspace
 
-    def on_device(self, *named):
-        for name, t in named:
-            if t.device != self.dev:
-                raise ValueError(f"{name} must be on {self.dev}")
-
-    @staticmethod
-    def check(status, where):
-        if status != OK:
-            raise TgemmError(status, where)
-
     def call(self, function, *args):
-        with self.torch.cuda.device(self.dev):
-            st = function(*args, self.workspace.data_ptr(), self.workspace.numel(), self.stream)
-        self.check(st, function.__name__)
+        cuda = self.torch.cuda
+        args += (self.workspace.data_ptr(), self.workspace.numel(), cuda.current_stream(self.device).cuda_stream)
+        if cuda.current_device() == self.device:
+            st = function(*args)
+        else:
+            with cuda.device(self.device):
+                st = function(*args)
+        if st != OK:
+            raise TgemmError(st, function.__name__)
 
-    def head_args(self):
-        return self.hidden.data_ptr(), self.ldh, self.weight.data_ptr(), self.ldw
+    def losses(self, hidden):
+        f32 = self.torch.float32
+        return (self.torch.empty(self.T, dtype=f32, device=hidden.device),
+                self.torch.empty(self.T, dtype=f32, device=hidden.device))
 
-    def losses(self):
-        both = self.torch.empty((2, self.T), dtype=self.torch.float32, device=self.dev)
-        return both[0], both[1]
-
-    def gradients(self, want_hidden, want_weight):
-        """Outputs in the operands' type; their pointers and pitches (0 when not wanted)."""
-        torch = self.torch
-        dh = torch.empty((self.T, self.D), dtype=self.hidden.dtype, device=self.dev) if want_hidden else None
-        dw = torch.empty((self.V, self.D), dtype=self.weight.dtype, device=self.dev) if want_weight else None
-        args = (dh.data_ptr() if want_hidden else 0, max(self.D, 1), dw.data_ptr() if want_weight else 0,
-                max(self.D, 1))
-        return dh, dw, args
-
-
-def _xent_options(ignore_index, scale, label_smoothing, z_loss, piece):
-    return LossOptions(scale=scale, label_smoothing=label_smoothing, z_loss=z_loss, piece=piece,
-                       ignore_index=ignore_index)
+    def gradients(self, hidden, weight, want_hidden, want_weight):
+        """Outputs in the operands' type, with their pointers and pitches (0 when not wanted)."""
+        empty, D = self.torch.empty, self.D
+        dh = empty((self.T, D), dtype=hidden.dtype, device=hidden.device) if want_hidden else None
+        dw = empty((self.V, D), dtype=hidden.dtype, device=hidden.device) if want_weight else None
+        return dh, dw, (dh.data_ptr() if want_hidden else 0, D, dw.data_ptr() if want_weight else 0, D)
 
 
 def _positive(name, value):
     if not value > 0:
         raise ValueError(f"{name} must be positive, got {value}")
-    return value
+    return float(value)
 
 
 @_on_stream
@@ -217,12 +224,11 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, scale=1.
     loss and lse 0.  ``lse`` is the log of the sum of exponentials, which the
     backward call takes.  Reduce as you like: ``loss.sum() / n``.
     """
-    h = _Head(hidden, weight, _xent_options(ignore_index, _positive("scale", scale), label_smoothing, z_loss, piece),
-              workspace, False, 0)
-    targets = _vector("targets", targets, h.T, h.torch.int64)
-    h.on_device(("targets", targets))
-    loss, lse = h.losses()
-    h.call(_lib.tgemm_xent_forward, h.T, h.V, h.D, *h.head_args(), targets.data_ptr(), h.code, h.options,
+    options = (_positive("scale", scale), label_smoothing, z_loss, piece, ignore_index)
+    h = _Head(hidden, weight, False, 0, options, workspace)
+    targets = _vector("targets", targets, h.T, h.torch.int64, h.device)
+    loss, lse = h.losses(hidden)
+    h.call(_lib.tgemm_xent_forward, h.T, h.V, h.D, *h.matrices, targets.data_ptr(), h.code, h.options,
            loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
@@ -234,25 +240,33 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, *, ig
     """Gradients ``(d_hidden, d_weight)`` of ``sum(grad_loss * loss)`` in the
     operands' type; ``lse`` from the forward call with the same options,
     grad_loss [T] float32.  An unwanted gradient is not computed (None)."""
-    h = _Head(hidden, weight, _xent_options(ignore_index, _positive("scale", scale), label_smoothing, z_loss, piece),
-              workspace, True, 0)
+    options = (_positive("scale", scale), label_smoothing, z_loss, piece, ignore_index)
+    h = _Head(hidden, weight, True, 0, options, workspace)
     f32 = h.torch.float32
-    targets = _vector("targets", targets, h.T, h.torch.int64)
-    lse, grad_loss = _vector("lse", lse, h.T, f32), _vector("grad_loss", grad_loss, h.T, f32)
-    h.on_device(("targets", targets), ("lse", lse), ("grad_loss", grad_loss))
-    dh, dw, out = h.gradients(want_hidden, want_weight)
-    h.call(_lib.tgemm_xent_backward, h.T, h.V, h.D, *h.head_args(), targets.data_ptr(), lse.data_ptr(),
+    targets = _vector("targets", targets, h.T, h.torch.int64, h.device)
+    lse, grad_loss = _vector("lse", lse, h.T, f32, h.device), _vector("grad_loss", grad_loss, h.T, f32, h.device)
+    dh, dw, out = h.gradients(hidden, weight, want_hidden, want_weight)
+    h.call(_lib.tgemm_xent_backward, h.T, h.V, h.D, *h.matrices, targets.data_ptr(), lse.data_ptr(),
            grad_loss.data_ptr(), h.code, h.options, *out)
     return dh, dw
 
 
-def _teacher(h, ids, logits):
-    torch = h.torch
-    _matrix("teacher_ids", ids, rows=h.T, dtype=torch.int64)
-    logits = logits.float()
-    _matrix("teacher_logits", logits, rows=h.T, cols=ids.shape[1])
-    h.on_device(("teacher_ids", ids), ("teacher_logits", logits))
-    return logits, (ids.data_ptr(), _ld(ids), logits.data_ptr(), _ld(logits))
+def _teacher(hidden, weight, backward, ids, logits, temperature, piece, workspace):
+    """The head of a distillation call, the teacher's logits in float32, and the lists' arguments."""
+    if ids.dim() != 2 or logits.shape != ids.shape:
+        raise ValueError("teacher_ids and teacher_logits must be matrices of one shape [T, K]")
+    rows, K = ids.shape
+    h = _Head(hidden, weight, backward, K, (1.0 / _positive("temperature", temperature), 0.0, 0.0, piece, 0), workspace)
+    if rows != h.T or ids.dtype != h.torch.int64:
+        raise ValueError(f"teacher_ids must be [{h.T}, K] int64, got {tuple(ids.shape)} {ids.dtype}")
+    if K < 1:
+        raise ValueError("the teacher's lists must have at least one place")
+    if ids.get_device() != h.device or logits.get_device() != h.device:
+        raise ValueError("teacher_ids and teacher_logits must be on the device of hidden")
+    if logits.dtype != h.torch.float32:
+        logits = logits.float()
+    return h, logits, (ids.data_ptr(), _pitch("teacher_ids", ids, rows, K), logits.data_ptr(),
+                       _pitch("teacher_logits", logits, rows, K))
 
 
 @_on_stream
@@ -265,11 +279,9 @@ def linear_distillation(hidden, weight, teacher_ids, teacher_logits, *, temperat
     any float type, K up to 256.  A row without a used place gets loss and lse
     0.  The losses are not multiplied by temperature squared.
     """
-    h = _Head(hidden, weight, LossOptions(scale=1.0 / _positive("temperature", temperature), piece=piece), workspace,
-              False, teacher_ids.shape[-1])
-    logits, lists = _teacher(h, teacher_ids, teacher_logits)
-    loss, lse = h.losses()
-    h.call(_lib.tgemm_distill_forward, h.T, h.V, h.D, teacher_ids.shape[1], *h.head_args(), *lists, h.code, h.options,
+    h, logits, lists = _teacher(hidden, weight, False, teacher_ids, teacher_logits, temperature, piece, workspace)
+    loss, lse = h.losses(hidden)
+    h.call(_lib.tgemm_distill_forward, h.T, h.V, h.D, teacher_ids.shape[1], *h.matrices, *lists, h.code, h.options,
            loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
@@ -279,13 +291,10 @@ def linear_distillation_backward(hidden, weight, teacher_ids, teacher_logits, ls
                                  piece=0, want_hidden=True, want_weight=True, workspace=None):
     """Gradients ``(d_hidden, d_weight)`` of ``sum(grad_loss * loss)``; lse,
     grad_loss and unwanted gradients as in linear_cross_entropy_backward."""
-    h = _Head(hidden, weight, LossOptions(scale=1.0 / _positive("temperature", temperature), piece=piece), workspace,
-              True, teacher_ids.shape[-1])
+    h, logits, lists = _teacher(hidden, weight, True, teacher_ids, teacher_logits, temperature, piece, workspace)
     f32 = h.torch.float32
-    logits, lists = _teacher(h, teacher_ids, teacher_logits)
-    lse, grad_loss = _vector("lse", lse, h.T, f32), _vector("grad_loss", grad_loss, h.T, f32)
-    h.on_device(("lse", lse), ("grad_loss", grad_loss))
-    dh, dw, out = h.gradients(want_hidden, want_weight)
-    h.call(_lib.tgemm_distill_backward, h.T, h.V, h.D, teacher_ids.shape[1], *h.head_args(), *lists, lse.data_ptr(),
+    lse, grad_loss = _vector("lse", lse, h.T, f32, h.device), _vector("grad_loss", grad_loss, h.T, f32, h.device)
+    dh, dw, out = h.gradients(hidden, weight, want_hidden, want_weight)
+    h.call(_lib.tgemm_distill_backward, h.T, h.V, h.D, teacher_ids.shape[1], *h.matrices, *lists, lse.data_ptr(),
            grad_loss.data_ptr(), h.code, h.options, *out)
     return dh, dw
