@@ -5,7 +5,9 @@
 // Backward: [teacher lists]  gather  { DZ  DH  DW } per piece  last step of dH
 // (loss_rows.cu and loss_gemm.cu hold the kernels.)  A weight whose rows are
 // not 16-byte aligned is copied to an aligned pitch piece by piece, and an fp32
-// weight to its three bf16 planes.
+// weight to its three bf16 planes.  Forward calls skip the gather where it
+// saves nothing: up to one tile of rows that can be read in place, and the few
+// rows of loss_few.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -28,9 +30,9 @@ constexpr int64_t kMaxExtent = int64_t(1) << 31;
 // CTA pairs the layout is planned for (a GB300's 152 SMs); the layout must not
 // depend on the device, so that its size can be asked for without one.
 constexpr int kPlanPairs = 76;
-// Bytes of one piece of dz, and of a piece of W that is copied.  A piece twice
-// the size of L2 already runs tens of rounds of tiles per product, so a larger
-// one would gain nothing.
+// Bytes of one piece of dz, and of a piece of W that is copied.  Pieces of twice
+// the size of L2 run tens of rounds of tiles per product, so the rounds left
+// partly empty cost little; larger ones gain nothing.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 // fp32: stages of the gradients' k axes (64 deep) summed in tensor memory
 // before they are added in fp32: the truncation of 64 steps stays below 1e-6,
@@ -71,29 +73,34 @@ struct Call {
 // Byte offsets into the workspace; every part starts on a 256-byte boundary.
 struct Layout {
   int planes = 1;
+  bool few = false;            // forward of a few rows, on the CUDA cores
+  bool direct = false;         // forward that reads H in place
   bool pack = false;           // W is copied to an aligned pitch or to planes, piece by piece
   int64_t piece = 0, pieces = 1;
   int64_t ldh = 0, ldw_p = 0, ldz = 0, ld_acc = 0;
   int splits = 1, k_per_split = 0;
   int64_t count = 0, source = 0, place = 0, ids = 0, q = 0, own = 0, flags = 0, coef = 0, h = 0;
   int64_t ms = 0, dot = 0, z = 0, w = 0, acc = 0;
-  int64_t tiles = 0;           // statistics per row
+  int64_t parts = 0;           // statistics per row
   int64_t total = 0;
 };
 
-// Splits of dH's long k axis (the piece's entries): with few tiles of dH the
-// pairs would idle, so each tile's k range is cut until the rounds of the
-// persistent grid balance; the splits are joined in order by the last step.
-void plan_splits(int64_t T, int64_t D, int64_t kb, Layout& l) {
+// dH: its k axis (the piece's entries) is long and its tiles may be few, so
+// each tile's k range is cut into `splits` until the rounds of the persistent
+// grid balance.  The splits are joined in order by the last step, which reads
+// them all: in stages of 0.27 us (a pair's 256 x 256 x 64 at 1.7 PFLOP/s)
+// against 4 bytes an element at 5 TB/s, once.
+void plan_dh(int64_t T, int64_t D, int64_t kb, int terms, Layout& l) {
   const int64_t tiles = ceil_div(T, kHeadTile) * ceil_div(D, kHeadTile);
+  double best_us = 1e300;
   int64_t best = 1;
-  double best_cost = static_cast<double>(ceil_div(tiles, kPlanPairs) * kb);
-  for (int64_t s = 2; s <= std::min<int64_t>(32, kb / 8); ++s) {
-    if (s * T * l.ld_acc * 4 > kPieceBytes) break;
-    const double cost = static_cast<double>(ceil_div(tiles * s, kPlanPairs) * ceil_div(kb, s));
-    if (cost < 0.92 * best_cost) {
+  for (int64_t s = 1; s <= std::max<int64_t>(1, std::min<int64_t>(64, kb / 4)); ++s) {
+    if (s > 1 && s * T * l.ld_acc * 4 > kPieceBytes) break;
+    const double us = 0.27 * static_cast<double>(l.pieces * ceil_div(tiles * s, kPlanPairs) * terms * ceil_div(kb, s)) +
+                      static_cast<double>(s * T * l.ld_acc) * 4 / 5e6;
+    if (us < 0.97 * best_us) {
       best = s;
-      best_cost = cost;
+      best_us = us;
     }
   }
   l.k_per_split = static_cast<int>(ceil_div(kb, best));
@@ -103,9 +110,10 @@ void plan_splits(int64_t T, int64_t D, int64_t kb, Layout& l) {
 Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bool distill, const void* W, int64_t ldw,
                    int dtype, int64_t piece_opt) {
   Layout l;
+  l.few = !backward && few_rows(T, D);
   l.planes = dtype == TGEMM_F32 ? kPlanes : 1;
   l.ldh = l.ldw_p = round_up(D, 8);
-  l.pack = l.planes > 1 || host_granule(W, ldw, 2) < 16;
+  l.pack = !l.few && (l.planes > 1 || host_granule(W, ldw, 2) < 16);
   l.ld_acc = round_up(D, 4);
   const int64_t whole = round_up(V, kHeadTile);
   if (piece_opt > 0) {
@@ -129,21 +137,21 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   l.count = take(256);
   l.source = take(T * 4);
   l.place = take(T * 4);
-  l.ids = take(T * K * 4);
-  l.q = take(T * K * 4);
+  l.ids = take(distill ? T * K * 4 : 0);
+  l.q = take(distill ? T * K * 4 : 0);
   l.own = take(distill ? T * 4 : 0);
   l.flags = take(distill ? T : 0);
   l.coef = take(backward ? T * 16 : 0);
   l.h = take(T * l.ldh * 2 * l.planes);
-  l.tiles = ceil_div(V, kHeadTile);
   if (l.pack) l.w = take(l.piece * l.ldw_p * 2 * l.planes);
   if (backward) {
     l.z = take(T * l.ldz * 2 * l.planes);
-    plan_splits(T, D, ceil_div(std::min(l.piece, V), kTileK), l);
+    plan_dh(T, D, ceil_div(std::min(l.piece, V), kTileK), l.planes == 1 ? 1 : 6, l);
     l.acc = take(l.splits * T * l.ld_acc * 4);
   } else {
-    l.ms = take(l.tiles * T * 8);
-    l.dot = take(l.tiles * T * 4);
+    l.parts = l.few ? few_blocks(V) : ceil_div(V, kHeadTile);
+    l.ms = take(l.parts * T * 8);
+    l.dot = take(l.parts * T * 4);
   }
   l.total = at;
   return l;
@@ -231,130 +239,151 @@ int check_call(const Call& c) {
     if (e_ != cudaSuccess) return host_cuda_fail(e_, what); \
   } while (0)
 
-int run_products(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float scale, float flat, float z_loss,
-                 int sms, int pairs, unsigned int* status) {
-  if (pairs < 1) return host_cuda_fail(cudaErrorLaunchOutOfResources, "CTA pairs");
-  const bool f32 = l.planes > 1;
-  const int type = c.dtype == TGEMM_F16 ? 1 : 0;  // of the operands; fp32's planes are bf16
-  const int P = l.planes;
-  CUtensorMap m_h, m_w, m_wn, m_z, m_zk, m_hn, m_acc, m_dw, m_zs;
-  for (CUtensorMap* m : {&m_h, &m_w, &m_wn, &m_z, &m_zk, &m_hn, &m_acc, &m_dw, &m_zs}) std::memset(m, 0, sizeof *m);
-  HeadArgs a;
-  std::memset(&a, 0, sizeof a);
-  a.count = rows.count;
-  a.T = static_cast<int>(c.T);
-  a.V = static_cast<int>(c.V);
-  a.K = static_cast<int>(c.K);
-  a.D = static_cast<int>(c.D);
-  a.bf16 = type == 0;
-  const float put_back = 1.0f + kStepLoss * static_cast<float>(ceil_div(c.D, 16));
-  a.k2 = static_cast<float>(scale * put_back * kLog2e);
-  a.flat = flat;
-  a.group_m = 8;
-  a.chunk = kChunkStages;
-  a.source = rows.source;
-  a.ids = rows.ids;
-  a.q = rows.q;
-  a.ms = reinterpret_cast<float2*>(ws + l.ms);
-  a.dot = reinterpret_cast<float*>(ws + l.dot);
-  a.coef = rows.coef;
-  a.factor = rows.factor;
-  const int to_us = (c.opts && c.opts->wait_timeout_us) ? c.opts->wait_timeout_us : 2000000;
-  a.timeout_ns = static_cast<unsigned long long>(to_us) * 1000ull;
-  a.status = status;
-  const int64_t m_tiles = ceil_div(c.T, kHeadTile), d_tiles = ceil_div(c.D, kHeadTile);
-  const int d_blocks = static_cast<int>(ceil_div(c.D, kTileK));
-  const int64_t h_plane = rows.plane * 2, z_plane = c.T * l.ldz * 2;
-  TGEMM_TRY(host_map_3d(&m_h, type, rows.h, c.D, c.T, P, l.ldh * 2, h_plane, kTileK, kTileM));
-  void* z = ws + l.z;
-  if (c.backward) {
-    TGEMM_TRY(host_map_3d(&m_zs, type, z, l.ldz, c.T, P, l.ldz * 2, z_plane, 64, 32));
-    if (c.dH) {
-      TGEMM_TRY(host_map_3d(&m_z, type, z, l.ldz, c.T, P, l.ldz * 2, z_plane, kTileK, kTileM));
-      TGEMM_TRY(host_map_3d(&m_acc, 2, ws + l.acc, c.D, c.T, l.splits, l.ld_acc * 4, c.T * l.ld_acc * 4, 32, 32));
-    }
-    if (c.dW) {
-      TGEMM_TRY(host_map_3d(&m_zk, type, z, l.ldz, c.T, P, l.ldz * 2, z_plane, 64, kTileK));
-      TGEMM_TRY(host_map_3d(&m_hn, type, rows.h, c.D, c.T, P, l.ldh * 2, h_plane, 64, kTileK));
-      a.store_granule = host_granule(c.dW, c.lddw, f32 ? 4 : 2);
-      if (!f32 && a.store_granule == 16) {
-        a.store_granule = 0;
-        TGEMM_TRY(host_map_3d(&m_dw, type, c.dW, c.D, c.V, 1, c.lddw * 2, 0, 64, 32));
-      }
-    }
+// The products of one call, launched piece by piece.
+class Products {
+ public:
+  Products(const Call& c, const Layout& l, const HeadRows& rows, char* ws, float scale, float flat, int sms, int pairs,
+           unsigned int* status)
+      : c_(c), l_(l), rows_(rows), ws_(ws), sms_(sms), pairs_(pairs), type_(c.dtype == TGEMM_F16 ? 1 : 0) {
+    std::memset(&a_, 0, sizeof a_);
+    a_.count = rows.count;
+    a_.T = static_cast<int>(c.T);
+    a_.V = static_cast<int>(c.V);
+    a_.K = static_cast<int>(c.K);
+    a_.D = static_cast<int>(c.D);
+    a_.group_m = 8;
+    a_.bf16 = type_ == 0;  // fp32's planes are bf16
+    put_back_ = 1.0f + kStepLoss * static_cast<float>(ceil_div(c.D, 16));
+    a_.k2 = static_cast<float>(scale * put_back_ * kLog2e);
+    a_.flat = flat;
+    a_.targets = c.distill ? nullptr : c.ids;
+    a_.mass = 1.0f - (c.opts ? c.opts->label_smoothing : 0.0f);
+    a_.source = rows.source;
+    a_.ids = rows.ids;
+    a_.q = rows.q;
+    a_.ms = reinterpret_cast<float2*>(ws + l.ms);
+    a_.dot = reinterpret_cast<float*>(ws + l.dot);
+    a_.coef = rows.coef;
+    a_.factor = rows.factor;
+    a_.splits = 1;
+    a_.chunk = kChunkStages;
+    const int to_us = (c.opts && c.opts->wait_timeout_us) ? c.opts->wait_timeout_us : 2000000;
+    a_.timeout_ns = static_cast<unsigned long long>(to_us) * 1000ull;
+    a_.status = status;
   }
-  const auto grid = [pairs](int64_t units) { return static_cast<int>(std::min<int64_t>(pairs, units)); };
-  int launches = 0;
-  for (int64_t i = 0; i < l.pieces; ++i) {
-    const int64_t v0 = i * l.piece, n = std::min(l.piece, c.V - v0);
-    const void* w = c.W;
-    int64_t ldw = c.ldw, w_rows = c.V;
-    const int64_t w_plane = l.piece * l.ldw_p;
-    a.b_row0 = static_cast<int>(v0);
-    if (l.pack) {
-      w = ws + l.w;
-      if (f32) {
-        const float* src = static_cast<const float*>(c.W) + v0 * c.ldw;
-        TGEMM_CUDA(launch_split(src, c.ldw, ws + l.w, l.ldw_p, w_plane, static_cast<int>(n), a.D,
-                                host_granule(src, c.ldw, 4) == 16, c.stream),
-                   "split launch");
-      } else {
-        const char* src = static_cast<const char*>(c.W) + v0 * c.ldw * 2;
-        TGEMM_CUDA(launch_repack(src, c.ldw, ws + l.w, l.ldw_p, static_cast<int>(n), a.D, host_granule(src, c.ldw, 2),
-                                 sms, c.stream),
-                   "repack launch");
-      }
-      ldw = l.ldw_p;
-      w_rows = n;  // the copy's rows past the piece hold an earlier piece
-      a.b_row0 = 0;
+
+  float put_back() const { return put_back_; }
+
+  int run() {
+    for (int64_t i = 0; i < l_.pieces; ++i) {
+      v0_ = i * l_.piece;
+      n_ = std::min(l_.piece, c_.V - v0_);
+      a_.cols = static_cast<int>(n_);
+      a_.col0 = static_cast<int>(v0_);
+      a_.b_row0 = l_.pack ? 0 : a_.col0;
+      a_.tile0 = static_cast<int>(v0_ / kHeadTile);
+      a_.reduce = i > 0;
+      TGEMM_TRY(copy_weight());
+      TGEMM_TRY(logits());
+      if (c_.backward && c_.dH) TGEMM_TRY(hidden_gradient());
+      if (c_.backward && c_.dW) TGEMM_TRY(weight_gradient());
     }
-    a.cols = static_cast<int>(n);
-    a.col0 = static_cast<int>(v0);
-    a.tile0 = static_cast<int>(v0 / kHeadTile);
-    a.k_blocks = d_blocks;
-    TGEMM_TRY(host_map_3d(&m_w, type, w, c.D, w_rows, P, ldw * 2, w_plane * 2, kTileK, kTileM));
-    const int64_t tiles = m_tiles * ceil_div(n, kHeadTile);
-    ++launches;
-    if (!c.backward) {
-      TGEMM_CUDA(launch_head(HEAD_STATS, P, m_h, m_w, m_w, a, grid(tiles), c.stream), "head launch");
-      continue;
-    }
-    TGEMM_CUDA(launch_head(HEAD_DZ, P, m_h, m_w, m_zs, a, grid(tiles), c.stream), "head launch");
-    if (c.dH) {
-      TGEMM_TRY(host_map_3d(&m_wn, type, w, c.D, w_rows, P, ldw * 2, w_plane * 2, 64, kTileK));
-      HeadArgs b = a;
-      b.k_blocks = static_cast<int>(ceil_div(n, kTileK));
-      b.splits = l.splits;
-      b.k_per_split = l.k_per_split;
-      b.reduce = i > 0;
-      b.out = ws + l.acc;
-      b.ld_out = l.ld_acc;
-      b.split_stride = c.T * l.ld_acc;
-      TGEMM_CUDA(launch_head(HEAD_DH, P, m_z, m_wn, m_acc, b, grid(m_tiles * d_tiles * l.splits), c.stream),
-                 "head launch");
-      ++launches;
-    }
-    if (c.dW) {
-      HeadArgs b = a;
-      b.out = c.dW;
-      b.ld_out = c.lddw;
-      b.out_row0 = static_cast<int>(v0);
-      TGEMM_CUDA(launch_head(HEAD_DW, P, m_zk, m_hn, m_dw, b, grid(ceil_div(n, kHeadTile) * d_tiles), c.stream),
-                 "head launch");
-      ++launches;
-    }
+    return TGEMM_OK;
   }
-  host_count_launches(launches);
-  if (!c.backward)
-    TGEMM_CUDA(launch_combine(a.ms, a.dot, static_cast<int>(l.tiles), a.T, scale * put_back, z_loss, rows, c.loss,
-                              c.lse_out, c.stream),
-               "combine launch");
-  else if (c.dH)
-    TGEMM_CUDA(launch_finish_dh(reinterpret_cast<float*>(ws + l.acc), l.ld_acc, c.T * l.ld_acc, l.splits, a.T, a.D, rows,
-                                f32 ? 2 : type, c.dH, c.lddh, c.stream),
-               "dH launch");
-  return TGEMM_OK;
-}
+
+ private:
+  int64_t w_plane() const { return l_.piece * l_.ldw_p; }
+
+  // A weight that cannot be read in place: this piece's copy.
+  int copy_weight() {
+    if (!l_.pack) return TGEMM_OK;
+    const int n = static_cast<int>(n_);
+    if (l_.planes > 1) {
+      const float* src = static_cast<const float*>(c_.W) + v0_ * c_.ldw;
+      TGEMM_CUDA(launch_split(src, c_.ldw, ws_ + l_.w, l_.ldw_p, w_plane(), n, a_.D, host_granule(src, c_.ldw, 4) == 16,
+                              c_.stream),
+                 "split launch");
+    } else {
+      const char* src = static_cast<const char*>(c_.W) + v0_ * c_.ldw * 2;
+      TGEMM_CUDA(launch_repack(src, c_.ldw, ws_ + l_.w, l_.ldw_p, n, a_.D, host_granule(src, c_.ldw, 2), sms_, c_.stream),
+                 "repack launch");
+    }
+    return TGEMM_OK;
+  }
+
+  int map_weight(CUtensorMap* m, uint32_t box_cols, uint32_t box_rows) {
+    if (!l_.pack) return host_map_3d(m, type_, c_.W, c_.D, c_.V, 1, c_.ldw * 2, 0, box_cols, box_rows);
+    // the copy's rows past the piece hold an earlier piece: the map ends before them
+    return host_map_3d(m, type_, ws_ + l_.w, c_.D, n_, l_.planes, l_.ldw_p * 2, w_plane() * 2, box_cols, box_rows);
+  }
+  int map_hidden(CUtensorMap* m, uint32_t box_cols, uint32_t box_rows) {
+    if (l_.direct) return host_map_3d(m, type_, c_.H, c_.D, c_.T, 1, c_.ldh * 2, 0, box_cols, box_rows);
+    return host_map_3d(m, type_, rows_.h, c_.D, c_.T, l_.planes, l_.ldh * 2, rows_.plane * 2, box_cols, box_rows);
+  }
+  int map_dz(CUtensorMap* m, uint32_t box_cols, uint32_t box_rows) {
+    return host_map_3d(m, type_, ws_ + l_.z, l_.ldz, c_.T, l_.planes, l_.ldz * 2, c_.T * l_.ldz * 2, box_cols, box_rows);
+  }
+
+  // `units`: tiles, were every row to count
+  int launch(int mode, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const HeadArgs& a,
+             int64_t units) {
+    const int pairs = static_cast<int>(std::min<int64_t>(pairs_, units));
+    TGEMM_CUDA(launch_head(mode, l_.planes, ma, mb, mc, a, pairs, c_.stream), "head launch");
+    host_count_launches(1);
+    return TGEMM_OK;
+  }
+
+  int logits() {
+    CUtensorMap mh, mw, mz;
+    TGEMM_TRY(map_hidden(&mh, kTileK, kTileM));
+    TGEMM_TRY(map_weight(&mw, kTileK, kTileM));
+    if (c_.backward) TGEMM_TRY(map_dz(&mz, 64, 32));
+    a_.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
+    return launch(c_.backward ? HEAD_DZ : HEAD_STATS, mh, mw, c_.backward ? mz : mw, a_,
+                  ceil_div(c_.T, kHeadTile) * ceil_div(n_, kHeadTile));
+  }
+
+  int hidden_gradient() {
+    HeadArgs b = a_;
+    b.k_blocks = static_cast<int>(ceil_div(n_, kTileK));
+    b.splits = l_.splits;
+    b.k_per_split = l_.k_per_split;
+    b.out = ws_ + l_.acc;
+    b.ld_out = l_.ld_acc;
+    b.split_stride = c_.T * l_.ld_acc;
+    CUtensorMap mz, mw, ma;
+    TGEMM_TRY(map_dz(&mz, kTileK, kTileM));
+    TGEMM_TRY(map_weight(&mw, 64, kTileK));
+    TGEMM_TRY(host_map_3d(&ma, 2, b.out, c_.D, c_.T, l_.splits, l_.ld_acc * 4, c_.T * l_.ld_acc * 4, 32, 32));
+    return launch(HEAD_DH, mz, mw, ma, b, ceil_div(c_.T, kHeadTile) * ceil_div(c_.D, kHeadTile) * l_.splits);
+  }
+
+  int weight_gradient() {
+    HeadArgs b = a_;
+    b.out = c_.dW;
+    b.ld_out = c_.lddw;
+    b.out_row0 = static_cast<int>(v0_);
+    b.store_granule = host_granule(c_.dW, c_.lddw, l_.planes > 1 ? 4 : 2);
+    CUtensorMap mz, mh, mo;
+    TGEMM_TRY(map_dz(&mz, 64, kTileK));
+    TGEMM_TRY(map_hidden(&mh, 64, kTileK));
+    const bool bulk = l_.planes == 1 && b.store_granule == 16;
+    if (bulk) {
+      b.store_granule = 0;
+      TGEMM_TRY(host_map_3d(&mo, type_, c_.dW, c_.D, c_.V, 1, c_.lddw * 2, 0, 64, 32));
+    }
+    return launch(HEAD_DW, mz, mh, bulk ? mo : mh, b, ceil_div(n_, kHeadTile) * ceil_div(c_.D, kHeadTile));
+  }
+
+  const Call& c_;
+  const Layout& l_;
+  const HeadRows& rows_;
+  char* ws_;
+  int sms_, pairs_, type_;
+  int64_t v0_ = 0, n_ = 0;  // this piece's first entry and width
+  float put_back_ = 1.0f;
+  HeadArgs a_;
+};
 
 int run_loss(const Call& c) {
   TGEMM_TRY(check_call(c));
@@ -378,32 +407,40 @@ int run_loss(const Call& c) {
     if (c.dW) TGEMM_CUDA(launch_zero_fill(c.dW, c.V, c.D, c.lddw, es, c.stream), "zero-fill launch");
     return TGEMM_OK;
   }
+  // the gather drops the rows that do not count and aligns the others: one tile
+  // of aligned rows needs neither (its ignored rows touch no other row's sums)
+  const int granule = host_granule(c.H, c.ldh, es);
+  l.direct = !c.backward && (l.few || (l.planes == 1 && c.T <= kHeadTile && granule == 16));
   char* ws = static_cast<char*>(c.workspace);
   GatherArgs g;
   std::memset(&g, 0, sizeof g);
-  g.rows.count = reinterpret_cast<int*>(ws + l.count);
-  g.rows.factor = reinterpret_cast<float*>(ws + l.count) + 1;
-  g.rows.source = reinterpret_cast<int*>(ws + l.source);
-  g.rows.place = reinterpret_cast<int*>(ws + l.place);
-  g.rows.ids = reinterpret_cast<int*>(ws + l.ids);
-  g.rows.q = reinterpret_cast<float*>(ws + l.q);
-  g.rows.own = c.distill ? reinterpret_cast<float*>(ws + l.own) : nullptr;
-  g.rows.flags = c.distill ? reinterpret_cast<unsigned char*>(ws + l.flags) : nullptr;
-  g.rows.coef = c.backward ? reinterpret_cast<float4*>(ws + l.coef) : nullptr;
-  g.rows.h = ws + l.h;
-  g.rows.ldh = l.ldh;
-  g.rows.plane = c.T * l.ldh;
+  HeadRows& rows = g.rows;
+  if (!l.direct) {
+    rows.count = reinterpret_cast<int*>(ws + l.count);
+    rows.factor = reinterpret_cast<float*>(ws + l.count) + 1;
+    rows.source = reinterpret_cast<int*>(ws + l.source);
+    rows.place = reinterpret_cast<int*>(ws + l.place);
+    rows.h = ws + l.h;
+    rows.ldh = l.ldh;
+    rows.plane = c.T * l.ldh;
+  }
+  if (c.distill) {
+    rows.ids = reinterpret_cast<int*>(ws + l.ids);
+    rows.q = reinterpret_cast<float*>(ws + l.q);
+    rows.own = reinterpret_cast<float*>(ws + l.own);
+    rows.flags = reinterpret_cast<unsigned char*>(ws + l.flags);
+  }
+  if (c.backward) rows.coef = reinterpret_cast<float4*>(ws + l.coef);
   g.T = static_cast<int>(c.T);
-  g.V = static_cast<int>(c.V);
   g.D = static_cast<int>(c.D);
-  g.K = static_cast<int>(c.K);
   g.es = es;
   g.H = c.H;
   g.ldh = c.ldh;
-  g.granule = host_granule(c.H, c.ldh, es);
-  g.targets = c.distill ? nullptr : c.ids;
-  g.ignore_index = c.opts ? c.opts->ignore_index : -100;
-  g.smoothing = smoothing;
+  g.granule = granule;
+  g.rule.targets = c.distill ? nullptr : c.ids;
+  g.rule.ignore_index = c.opts ? c.opts->ignore_index : -100;
+  g.rule.flags = rows.flags;
+  g.rule.V = static_cast<int>(c.V);
   g.z_loss = z_loss;
   g.scale = scale;
   g.range = c.dtype == TGEMM_F16 ? kRangeF16 : 1.0f;
@@ -412,10 +449,49 @@ int run_loss(const Call& c) {
   g.loss_out = c.loss;
   g.lse_out = c.lse_out;
   if (c.distill)
-    TGEMM_CUDA(launch_distill_lists(c.ids, c.ld_ids, c.logits, c.ld_logits, g.T, g.V, g.K, scale, g.rows, c.stream),
+    TGEMM_CUDA(launch_distill_lists(c.ids, c.ld_ids, c.logits, c.ld_logits, g.T, g.rule.V, static_cast<int>(c.K), scale,
+                                    rows, c.stream),
                "teacher list launch");
-  TGEMM_CUDA(launch_gather(g, sms, c.stream), "gather launch");
-  return run_products(c, l, g.rows, ws, scale, flat, z_loss, sms, pairs, status);
+  if (!l.direct) TGEMM_CUDA(launch_gather(g, sms, c.stream), "gather launch");
+  const int out_type = c.dtype == TGEMM_F32 ? 2 : c.dtype == TGEMM_F16 ? 1 : 0;
+  float2* ms = reinterpret_cast<float2*>(ws + l.ms);
+  float* dot = reinterpret_cast<float*>(ws + l.dot);
+  float put_back = 1.0f;
+  if (l.few) {
+    FewArgs f;
+    std::memset(&f, 0, sizeof f);
+    f.T = g.T;
+    f.V = g.rule.V;
+    f.D = g.D;
+    f.K = static_cast<int>(c.K);
+    f.H = c.H;
+    f.ldh = c.ldh;
+    f.W = c.W;
+    f.ldw = c.ldw;
+    f.k2 = static_cast<float>(scale * kLog2e);
+    f.flat = flat;
+    f.targets = g.rule.targets;
+    f.mass = 1.0f - smoothing;
+    f.ids = rows.ids;
+    f.q = rows.q;
+    f.ms = ms;
+    f.dot = dot;
+    TGEMM_CUDA(launch_few_stats(f, out_type, host_granule(c.W, c.ldw, es), c.stream), "few-rows launch");
+  } else {
+    if (pairs < 1) return host_cuda_fail(cudaErrorLaunchOutOfResources, "CTA pairs");
+    Products products(c, l, rows, ws, scale, flat, sms, pairs, status);
+    TGEMM_TRY(products.run());
+    put_back = products.put_back();
+  }
+  if (!c.backward)
+    TGEMM_CUDA(launch_combine(ms, dot, static_cast<int>(l.parts), g.T, scale * put_back, z_loss, rows, g.rule, c.loss,
+                              c.lse_out, c.stream),
+               "combine launch");
+  else if (c.dH)
+    TGEMM_CUDA(launch_finish_dh(reinterpret_cast<float*>(ws + l.acc), l.ld_acc, c.T * l.ld_acc, l.splits, g.T, g.D, rows,
+                                out_type, c.dH, c.lddh, c.stream),
+               "dH launch");
+  return TGEMM_OK;
 }
 
 }  // namespace

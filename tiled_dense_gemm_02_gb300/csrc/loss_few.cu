@@ -1,0 +1,287 @@
+// Row statistics of the vocabulary-head losses for a few rows (T <= 8): the
+// scoring of single tokens.
+//
+// The work is one pass over W: 2 T V D operations against V D elements read,
+// far below what the tensor cores need to be worth their set-up.  A tile of 256
+// rows would be nearly empty, and V / 256 tiles rarely fill whole rounds of the
+// pairs.  Here each warp takes four entries of W at a time, lane by lane in
+// 16-byte pieces, multiplies them with the rows of H held in shared memory as
+// fp32 (exact for 16-bit inputs), and keeps the running maximum and sum of a
+// softmax for its entries; blocks share the vocabulary evenly.  Rows of W may
+// have any alignment, so nothing is copied first.
+//
+// Bound by memory.  A lane spends T / 2 paired multiply-adds and one
+// conversion an element of W; an SM takes 11.8 two-byte elements a clock from
+// memory at the measured rate, so 8 rows use two thirds of its lanes.  Four
+// entries a warp share each read of H from shared memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <climits>
+#include <type_traits>
+
+#include "loss_internal.h"
+#include "ptx.cuh"
+
+namespace tgemm {
+namespace {
+
+constexpr int kFewThreads = 512;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kEntries = 4;  // rows of W per warp and step
+
+template <typename E>
+constexpr int lane_elems() { return 16 / static_cast<int>(sizeof(E)); }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// The 16 bytes of a row from element c on, as raw words; elements at or past
+// `cols` read as zero.  G: alignment of the rows in bytes.
+template <typename E, int G>
+__device__ __forceinline__ uint4 load_piece(const E* row, int c, int cols) {
+  constexpr int N = lane_elems<E>();
+  if (G == 16 && c + N <= cols) return __ldg(reinterpret_cast<const uint4*>(row + c));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if constexpr (sizeof(E) == 4 || G >= 4) {
+    constexpr int PER = 4 / static_cast<int>(sizeof(E));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + (i + 1) * PER <= cols)
+        w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + c) + i);
+      else if (PER == 2 && c + i * PER < cols)
+        w[i] = __ldg(reinterpret_cast<const uint16_t*>(row + c) + 2 * i);
+    }
+  } else {
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(row + c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) w[i / 2] |= static_cast<uint32_t>(__ldg(s + i)) << (16 * (i & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename E>
+__device__ __forceinline__ void unpack(const uint4& p, float (&v)[lane_elems<E>()]) {
+  const E* e = reinterpret_cast<const E*>(&p);
+#pragma unroll
+  for (int i = 0; i < lane_elems<E>(); ++i) v[i] = to_f32(e[i]);
+}
+
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  s = s * exp2f(m - ref) + s2 * exp2f(m2 - ref);
+  m = top;
+}
+
+// TN: rows of H, T rounded up to a power of two (the padding is zero).
+template <typename E, int TN, int G>
+__global__ void __launch_bounds__(kFewThreads) few_stats_kernel(const FewArgs a) {
+  constexpr int N = lane_elems<E>();
+  constexpr int VALUES = kEntries * TN;  // sums a warp holds: 4 to 32
+  extern __shared__ __align__(16) float s_h[];  // [t][half of the 16 bytes][group][4]
+  __shared__ float s_part[3][kFewWarps][TN];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = (a.D + N - 1) / N;
+  for (int i = threadIdx.x; i < TN * groups; i += kFewThreads) {
+    const int t = i / groups, g = i - t * groups;
+    float v[N];
+    if (t < a.T) {
+      const E* row = static_cast<const E*>(a.H) + t * a.ldh;
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = g * N + j < a.D ? to_f32(row[g * N + j]) : 0.0f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = 0.0f;
+    }
+#pragma unroll
+    for (int p = 0; p < N / 4; ++p)
+      reinterpret_cast<float4*>(s_h)[(t * (N / 4) + p) * groups + g] =
+          make_float4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+  }
+  __syncthreads();
+
+  // after the reduction lane l holds the sum of value l / (32 / VALUES)
+  const int value = lane / (32 / VALUES);
+  const int t = value % TN, r = value / TN;
+  const bool owner = lane % (32 / VALUES) == 0 && t < a.T;
+  // this lane's row: its target, or its list walked as the entries ascend
+  int next = INT_MAX, pos = 0;
+  const int64_t list = static_cast<int64_t>(t) * a.K;
+  if (owner) {
+    if (a.targets) {
+      const int64_t y = a.targets[t];
+      next = y >= 0 && y < a.V ? static_cast<int>(y) : INT_MAX;
+    } else {
+      next = a.ids[list];
+    }
+  }
+  float m = -INFINITY, s = 0.0f, dot = 0.0f, zs = 0.0f;
+
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kFewWarps * kEntries;
+  for (int64_t at = (static_cast<int64_t>(blockIdx.x) * kFewWarps + warp) * kEntries; at < a.V; at += stride) {
+    const int v0 = static_cast<int>(at);
+    const E* rows[kEntries];
+#pragma unroll
+    for (int e = 0; e < kEntries; ++e)
+      rows[e] = static_cast<const E*>(a.W) + static_cast<int64_t>(min(v0 + e, a.V - 1)) * a.ldw;
+    float2 acc[VALUES];
+#pragma unroll
+    for (int i = 0; i < VALUES; ++i) acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll(TN == 8 ? 1 : 2)
+    for (int g = lane; g < groups; g += 32) {
+      uint4 p[kEntries];
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e) p[e] = load_piece<E, G>(rows[e], g * N, a.D);
+      float w[kEntries][N];
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e) unpack<E>(p[e], w[e]);
+#pragma unroll
+      for (int q = 0; q < TN; ++q)
+#pragma unroll
+        for (int hf = 0; hf < N / 4; ++hf) {
+          const float4 h = reinterpret_cast<const float4*>(s_h)[(q * (N / 4) + hf) * groups + g];
+#pragma unroll
+          for (int e = 0; e < kEntries; ++e) {
+            float2& c = acc[e * TN + q];
+            c = __ffma2_rn(make_float2(w[e][4 * hf], w[e][4 * hf + 1]), make_float2(h.x, h.y), c);
+            c = __ffma2_rn(make_float2(w[e][4 * hf + 2], w[e][4 * hf + 3]), make_float2(h.z, h.w), c);
+          }
+        }
+    }
+    // each step halves the values a lane holds and the lanes that share one
+    float z[VALUES];
+#pragma unroll
+    for (int i = 0; i < VALUES; ++i) z[i] = acc[i].x + acc[i].y;
+    int o = 16;
+#pragma unroll
+    for (int n = VALUES; n > 1; n >>= 1, o >>= 1)
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        const float mine = (lane & o) ? z[i + n / 2] : z[i];
+        const float theirs = (lane & o) ? z[i] : z[i + n / 2];
+        z[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, o);
+      }
+    float sum = z[0];
+#pragma unroll
+    for (; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int v = v0 + r;
+    if (owner && v < a.V) {
+      join(m, s, sum * a.k2, 1.0f);
+      zs += sum;
+      while (next < v) {  // entries other warps and lanes take
+        ++pos;
+        next = !a.targets && pos < a.K ? a.ids[list + pos] : INT_MAX;
+      }
+      while (next == v) {
+        dot = fmaf(a.targets ? a.mass : a.q[list + pos], sum, dot);
+        ++pos;
+        next = !a.targets && pos < a.K ? a.ids[list + pos] : INT_MAX;
+      }
+    }
+  }
+  dot = fmaf(a.flat, zs, dot);
+  // the warp's entries of one row, then the block's warps, in fixed order
+  if (!owner) {
+    m = -INFINITY;
+    s = dot = 0.0f;
+  }
+#pragma unroll
+  for (int o = 32 / kEntries; o < 32; o <<= 1) {  // lanes that differ in r
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const float d2 = __shfl_xor_sync(0xffffffffu, dot, o);
+    join(m, s, m2, s2);
+    dot += d2;
+  }
+  if (lane % (32 / VALUES) == 0 && r == 0) {
+    s_part[0][warp][t] = m;
+    s_part[1][warp][t] = s;
+    s_part[2][warp][t] = dot;
+  }
+  __syncthreads();
+  if (threadIdx.x < a.T) {
+    const int q = threadIdx.x;
+    m = s_part[0][0][q];
+    s = s_part[1][0][q];
+    dot = s_part[2][0][q];
+    for (int w = 1; w < kFewWarps; ++w) {
+      join(m, s, s_part[0][w][q], s_part[1][w][q]);
+      dot += s_part[2][w][q];
+    }
+    a.ms[static_cast<int64_t>(blockIdx.x) * a.T + q] = make_float2(m, s);
+    a.dot[static_cast<int64_t>(blockIdx.x) * a.T + q] = dot;
+  }
+}
+
+template <typename E, int TN, int G>
+cudaError_t launch_few(const FewArgs& a, int blocks, cudaStream_t stream) {
+  auto kernel = few_stats_kernel<E, TN, G>;
+  const int groups = (a.D + lane_elems<E>() - 1) / lane_elems<E>();
+  const int smem = TN * groups * 16 * (lane_elems<E>() / 4);
+  static std::atomic<uint64_t> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done_mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    if (e != cudaSuccess) return e;
+    done_mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename E, int G>
+cudaError_t launch_rows(const FewArgs& a, int blocks, cudaStream_t stream) {
+  if (a.T <= 1) return launch_few<E, 1, G>(a, blocks, stream);
+  if (a.T <= 2) return launch_few<E, 2, G>(a, blocks, stream);
+  if (a.T <= 4) return launch_few<E, 4, G>(a, blocks, stream);
+  return launch_few<E, 8, G>(a, blocks, stream);
+}
+
+template <typename E>
+cudaError_t launch_type(const FewArgs& a, int granule, int blocks, cudaStream_t stream) {
+  if (granule == 16) return launch_rows<E, 16>(a, blocks, stream);
+  if constexpr (sizeof(E) == 4)
+    return launch_rows<E, 4>(a, blocks, stream);
+  else
+    return granule >= 4 ? launch_rows<E, 4>(a, blocks, stream) : launch_rows<E, 2>(a, blocks, stream);
+}
+
+}  // namespace
+
+bool few_rows(int64_t T, int64_t D) {
+  int64_t rows = 1;
+  while (rows < T) rows *= 2;
+  return T <= kFewRows && rows * ((D + 7) / 8 * 8) * 4 <= kFewSmem;
+}
+
+int few_blocks(int64_t V) {
+  // two blocks of 16 warps per SM, each warp with at least one step of entries
+  const int64_t most = (V + kFewWarps * kEntries - 1) / (kFewWarps * kEntries);
+  return static_cast<int>(most < kFewBlocks ? most : kFewBlocks);
+}
+
+cudaError_t launch_few_stats(const FewArgs& a, int type, int granule, cudaStream_t stream) {
+  const int blocks = few_blocks(a.V);
+  if (type == 0) return launch_type<__nv_bfloat16>(a, granule, blocks, stream);
+  if (type == 1) return launch_type<__half>(a, granule, blocks, stream);
+  return launch_type<float>(a, granule, blocks, stream);
+}
+
+}  // namespace tgemm

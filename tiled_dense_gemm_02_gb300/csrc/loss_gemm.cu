@@ -25,7 +25,9 @@
 //   warp 0      bulk-tensor producer of this CTA's 128 rows of A and 128
 //               columns of B; completion on the leader CTA's full barrier
 //   warp 1      tensor-memory allocation; MMA issue by one thread of the leader
-//   warps 2..5  epilogue of this CTA's 128 rows, one row per thread
+//   warps 2..   epilogue of this CTA's 128 rows, one row per thread: four warps
+//               for STATS; eight for the gradients, half of the columns each,
+//               since their stores can outlast a short k axis
 //
 // The number of gathered rows is known on the device only (rows that do not
 // count are not gathered), so every role derives the tile list from it.  Every
@@ -41,12 +43,15 @@ namespace {
 
 constexpr int kSub = kTileM * kTileK * 2;        // 16 KB: one CTA's share of A or B in one stage
 constexpr int kStage = 2 * kSub;
-constexpr bool head_staged(int mode) { return mode != HEAD_STATS; }
+// Warps per quarter of the rows in the epilogue, each with 4 KB to stage stores.
+constexpr int head_halves(int mode) { return mode == HEAD_STATS ? 1 : 2; }
+constexpr int head_threads(int mode) { return 32 * (2 + 4 * head_halves(mode)); }
+constexpr int head_epi_bytes(int mode) { return mode == HEAD_STATS ? 0 : 4 * head_halves(mode) * 4096; }
 constexpr int head_stages(int mode) {
-  return (kSmemLimit - 1024 - (head_staged(mode) ? kEpiBytes : 0) - kBarrierBytes) / kStage;
+  return (kSmemLimit - 1024 - head_epi_bytes(mode) - kBarrierBytes) / kStage;
 }
 constexpr int head_smem(int mode) {
-  return 1024 + head_stages(mode) * kStage + (head_staged(mode) ? kEpiBytes : 0) + kBarrierBytes;
+  return 1024 + head_stages(mode) * kStage + head_epi_bytes(mode) + kBarrierBytes;
 }
 constexpr bool a_m_major(int mode) { return mode == HEAD_DW; }
 constexpr bool b_n_major(int mode) { return mode == HEAD_DH || mode == HEAD_DW; }
@@ -71,25 +76,17 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, int32_
                : "memory");
 }
 
-// The tile list of one launch, derived from the gathered row count.
+// The tile list of a launch, derived from the gathered row count.
 struct Tiles {
-  int m, n, units, k_blocks, group_m;
+  int m, n, units, k_blocks;
 };
 
 template <int MODE>
-__device__ __forceinline__ Tiles head_tiles(const HeadArgs& a) {
+__device__ __forceinline__ Tiles head_tiles(const HeadArgs& a, int rows) {
   Tiles t;
-  const int rows = max(1, min(*a.count, a.T));
-  t.group_m = a.group_m;
-  if constexpr (MODE == HEAD_DW) {
-    t.m = (a.cols + kHeadTile - 1) / kHeadTile;
-    t.n = (a.D + kHeadTile - 1) / kHeadTile;
-    t.k_blocks = (rows + kTileK - 1) / kTileK;
-  } else {
-    t.m = (rows + kHeadTile - 1) / kHeadTile;
-    t.n = ((MODE == HEAD_DH ? a.D : a.cols) + kHeadTile - 1) / kHeadTile;
-    t.k_blocks = a.k_blocks;
-  }
+  t.m = ((MODE == HEAD_DW ? a.cols : rows) + kHeadTile - 1) / kHeadTile;
+  t.n = ((MODE == HEAD_DH || MODE == HEAD_DW ? a.D : a.cols) + kHeadTile - 1) / kHeadTile;
+  t.k_blocks = MODE == HEAD_DW ? (rows + kTileK - 1) / kTileK : a.k_blocks;
   t.units = t.m * t.n * (MODE == HEAD_DH ? a.splits : 1);
   return t;
 }
@@ -106,10 +103,10 @@ __device__ __forceinline__ HeadUnit head_unit(const HeadArgs& a, const Tiles& t,
   const int per = t.m * t.n;
   w.split = MODE == HEAD_DH ? u / per : 0;
   const int i = MODE == HEAD_DH ? u - w.split * per : u;
-  const int per_group = t.group_m * t.n;
+  const int per_group = a.group_m * t.n;
   const int g = i / per_group;
-  const int first = g * t.group_m;
-  const int gsz = min(t.m - first, t.group_m);
+  const int first = g * a.group_m;
+  const int gsz = min(t.m - first, a.group_m);
   const int r = i - g * per_group;
   w.mb = first + r % gsz;
   w.nb = r / gsz;
@@ -118,21 +115,28 @@ __device__ __forceinline__ HeadUnit head_unit(const HeadArgs& a, const Tiles& t,
   return w;
 }
 
-// A row's list of targets, walked in ascending order as its columns go by.
+// A row's targets, walked in ascending order as its columns go by.
 struct Walk {
   const int* ids;
   const float* q;
   int pos, K, next;
+  float one;  // mass of a single target (K = 0)
   __device__ __forceinline__ void start(const HeadArgs& a, int row, int n, int first) {
-    K = a.K;
-    pos = 0;
+    K = pos = 0;
     next = INT_MAX;
-    ids = a.ids;
-    q = a.q;
+    ids = nullptr;
+    q = nullptr;
+    one = a.mass;
     if (row >= n) return;
-    const int64_t at = static_cast<int64_t>(a.source[row]) * K;
-    ids += at;
-    q += at;
+    const int t = a.source ? a.source[row] : row;
+    if (a.targets) {
+      const int64_t y = a.targets[t];
+      if (y >= first && y < a.V) next = static_cast<int>(y);
+      return;
+    }
+    K = a.K;
+    ids = a.ids + static_cast<int64_t>(t) * K;
+    q = a.q + static_cast<int64_t>(t) * K;
     int len = K;
     while (len > 0) {  // first place whose id is not below `first`
       const int half = len >> 1;
@@ -145,30 +149,30 @@ struct Walk {
     }
     next = pos < K ? ids[pos] : INT_MAX;
   }
-  __device__ __forceinline__ float mass() const { return q[pos]; }
+  __device__ __forceinline__ float mass() const { return K ? q[pos] : one; }
   __device__ __forceinline__ void step() {
     ++pos;
     next = pos < K ? ids[pos] : INT_MAX;
   }
 };
 
-// Statistics of this thread's row over the tile's 256 columns.
+// Statistics of this thread's row over the tile's columns.
 __device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, int nb, const HeadArgs& a) {
   const int first = a.col0 + nb * kHeadTile;  // vocabulary entry of the tile's first column
-  const int width = min(kHeadTile, a.cols - nb * kHeadTile);
+  const int width = a.cols - nb * kHeadTile;
   Walk walk;
   walk.start(a, row, n, first);
   float m = -INFINITY, s = 0.0f, dot = 0.0f, zs = 0.0f;
 #pragma unroll 1
   for (int c = 0; c < kHeadTile / 32; ++c) {
-    if (c * 32 >= width) break;
+    const int limit = width - c * 32;
+    if (limit <= 0) break;
     uint32_t raw[32];
     ptx::tmem_ld_32x32b_x32(tbase + c * 32, raw);
     ptx::tmem_wait_ld();
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
-    const int limit = width - c * 32;
     if (limit < 32) {  // columns past the piece are no entries
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = i < limit ? v[i] : -INFINITY;
@@ -232,48 +236,69 @@ __device__ __forceinline__ void gradient_chunk(uint32_t (&raw)[32], int base, in
   }
 }
 
-// Next staging buffer of this warp, free to be written.
-__device__ __forceinline__ uint8_t* staging(uint8_t* stage_base, int& sbuf, int lane) {
-  uint8_t* buf = stage_base + sbuf * 4096;
-  sbuf ^= 1;
-  if (lane == 0) ptx::bulk_wait_group_read<1>();
-  __syncwarp();
-  return buf;
-}
-
+// This warp's staging buffer, once the last copy out of it has been read.
 __device__ __forceinline__ void stage_row(uint8_t* buf, int lane, const uint32_t (&w)[32]) {
+  if (lane == 0) ptx::bulk_wait_group_read<0>();
+  __syncwarp();
 #pragma unroll
   for (int ch = 0; ch < 8; ++ch)
     *reinterpret_cast<uint4*>(buf + sw128_offset(lane, ch * 16)) =
         make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
 }
 
 // One 64-column chunk of 16-bit words of 32 rows, to the tensor at (col, row0, plane).
 __device__ __forceinline__ void store_words(const uint32_t (&w)[32], const CUtensorMap* mapC, int col, int row0,
-                                            int plane, uint8_t* stage_base, int& sbuf, int lane) {
-  uint8_t* buf = staging(stage_base, sbuf, lane);
+                                            int plane, uint8_t* buf, int lane) {
   stage_row(buf, lane, w);
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
   if (lane == 0) {
     ptx::tma_store_3d(mapC, col, row0, plane, ptx::smem_u32(buf));
     ptx::bulk_commit_group();
   }
 }
 
+// The same to rows that are not 16-byte aligned: the warp writes one row after
+// another, neighbouring lanes neighbouring elements.
+__device__ __forceinline__ void store_words_plain(const uint32_t (&w)[32], uint16_t* dst, int64_t ld, int rows,
+                                                  int cols, int granule, uint8_t* buf, int lane) {
+  stage_row(buf, lane, w);
+  __syncwarp();
+#pragma unroll 4
+  for (int r = 0; r < 32; ++r) {
+    if (r >= rows) break;
+    uint16_t* row = dst + r * ld;
+    if (granule >= 4) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(buf + sw128_offset(r, lane * 4));
+      if (2 * lane + 2 <= cols)
+        reinterpret_cast<uint32_t*>(row)[lane] = v;
+      else if (2 * lane < cols)
+        row[2 * lane] = static_cast<uint16_t>(v & 0xFFFFu);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        if (c < cols) row[c] = *reinterpret_cast<const uint16_t*>(buf + sw128_offset(r, c * 2));
+      }
+    }
+  }
+  __syncwarp();
+}
+
 template <int PLANES>
-__device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int nb, const HeadArgs& a,
-                                            const CUtensorMap* mapC, uint8_t* stage_base, int& sbuf, int lane) {
+__device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int nb, int half, const HeadArgs& a,
+                                            const CUtensorMap* mapC, uint8_t* buf, int lane) {
   if (row0 >= a.T) return;
+  const int c0 = half * (kHeadTile / 128), c1 = c0 + kHeadTile / 128;
   const int row = row0 + lane;
   const int first = a.col0 + nb * kHeadTile;
-  const int width = min(kHeadTile, a.cols - nb * kHeadTile);
+  const int width = a.cols - nb * kHeadTile;
   Walk walk;
-  walk.start(a, row, n, first);
+  walk.start(a, row, n, first + c0 * 64);
   const float4 k = row < n ? a.coef[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const int fmt = a.bf16 ? OUT_BF16 : OUT_F16;
 #pragma unroll 1
-  for (int c = 0; c < kHeadTile / 64; ++c) {
+  for (int c = c0; c < c1; ++c) {
     if (c * 64 >= width) break;
     uint32_t lo[32], hi[32], w[32];
     ptx::tmem_ld_32x32b_x32(tbase + c * 64, lo);
@@ -298,7 +323,7 @@ __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int
           v[1] = isfinite(py) ? __float_as_uint(y - py) : 0u;
         }
       }
-      store_words(w, mapC, nb * kHeadTile + c * 64, row0, p, stage_base, sbuf, lane);
+      store_words(w, mapC, nb * kHeadTile + c * 64, row0, p, buf, lane);
     }
   }
 }
@@ -322,34 +347,37 @@ __device__ __forceinline__ void store_row_f32(float* dst, const float (&v)[32], 
 }
 
 // fp32 DH and DW: one chunk's sums of this thread's row, times f.
-__device__ __forceinline__ void epilogue_f32(uint32_t tbase, float* row, bool valid_row, int col0, int cols, float f,
-                                             bool vec, bool add) {
+__device__ __forceinline__ void epilogue_f32(uint32_t tbase, float* row, bool valid_row, int nb, int half, int cols,
+                                             float f, bool vec, bool add) {
+  const int c0 = half * (kHeadTile / 64), c1 = c0 + kHeadTile / 64;
 #pragma unroll 1
-  for (int c = 0; c < kHeadTile / 32; ++c) {
-    const int left = cols - col0 - c * 32;
-    if (left <= 0) break;
+  for (int c = c0; c < c1; ++c) {
+    const int col = nb * kHeadTile + c * 32;
+    if (col >= cols) break;
     uint32_t w[32];
     ptx::tmem_ld_32x32b_x32(tbase + c * 32, w);
     ptx::tmem_wait_ld();
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = f * __uint_as_float(w[i]);
-    if (valid_row) store_row_f32(row + col0 + c * 32, v, left, vec, add);
+    if (valid_row) store_row_f32(row + col, v, cols - col, vec, add);
   }
 }
 
-__device__ __forceinline__ void epilogue_dh(uint32_t tbase, int row0, const HeadUnit& u, const HeadArgs& a,
-                                            const CUtensorMap* mapC, uint8_t* stage_base, int& sbuf, int lane) {
+__device__ __forceinline__ void epilogue_dh(uint32_t tbase, int row0, const HeadUnit& u, int half, const HeadArgs& a,
+                                            const CUtensorMap* mapC, uint8_t* buf, int lane) {
   if (row0 >= a.T) return;
+  const int c0 = half * (kHeadTile / 64), c1 = c0 + kHeadTile / 64;
 #pragma unroll 1
-  for (int c = 0; c < kHeadTile / 32; ++c) {
+  for (int c = c0; c < c1; ++c) {
     const int col = u.nb * kHeadTile + c * 32;
     if (col >= a.D) break;
     uint32_t w[32];
     ptx::tmem_ld_32x32b_x32(tbase + c * 32, w);
     ptx::tmem_wait_ld();
-    uint8_t* buf = staging(stage_base, sbuf, lane);
     stage_row(buf, lane, w);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
     if (lane == 0) {
       if (a.reduce)
         tma_reduce_add_3d(mapC, col, row0, u.split, ptx::smem_u32(buf));
@@ -360,14 +388,14 @@ __device__ __forceinline__ void epilogue_dh(uint32_t tbase, int row0, const Head
   }
 }
 
-__device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, const HeadArgs& a,
-                                            const CUtensorMap* mapC, uint8_t* stage_base, int& sbuf, int lane) {
+__device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, int half, const HeadArgs& a,
+                                            const CUtensorMap* mapC, uint8_t* buf, int lane) {
   if (row0 >= a.cols) return;
   const float f = *a.factor;
   const int fmt = a.bf16 ? OUT_BF16 : OUT_F16;
-  const int row = row0 + lane;
+  const int c0 = half * (kHeadTile / 128), c1 = c0 + kHeadTile / 128;
 #pragma unroll 1
-  for (int c = 0; c < kHeadTile / 64; ++c) {
+  for (int c = c0; c < c1; ++c) {
     const int col = nb * kHeadTile + c * 64;
     if (col >= a.D) break;
     uint32_t lo[32], hi[32], w[32];
@@ -379,20 +407,20 @@ __device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, co
       w[i] = pack_pair(f * __uint_as_float(lo[2 * i]), f * __uint_as_float(lo[2 * i + 1]), fmt);
       w[16 + i] = pack_pair(f * __uint_as_float(hi[2 * i]), f * __uint_as_float(hi[2 * i + 1]), fmt);
     }
-    if (a.store_granule == 0) {
-      store_words(w, mapC, col, a.out_row0 + row0, 0, stage_base, sbuf, lane);
-    } else if (row < a.cols) {
-      uint8_t* dst = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(a.out_row0 + row) * a.ld_out + col) * 2;
-      store_segment(dst, w, min(a.D - col, 64) * 2, a.store_granule, 2);
-    }
+    if (a.store_granule == 0)
+      store_words(w, mapC, col, a.out_row0 + row0, 0, buf, lane);
+    else
+      store_words_plain(w, static_cast<uint16_t*>(a.out) + static_cast<int64_t>(a.out_row0 + row0) * a.ld_out + col,
+                        a.ld_out, a.cols - row0, a.D - col, a.store_granule, buf, lane);
   }
 }
 
 template <int MODE, int PLANES>
-__global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
+__global__ void __launch_bounds__(head_threads(MODE), 1)
     head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ CUtensorMap mapC, const HeadArgs args) {
   constexpr int STAGES = head_stages(MODE);
+  constexpr int TERMS = plane_terms(PLANES);
   constexpr int ACC = 256;
   constexpr uint32_t TMEM_COLS = 512;
   static_assert(head_smem(MODE) <= kSmemLimit, "shared memory per CTA");
@@ -400,7 +428,7 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sC = smem + STAGES * kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sC + (head_staged(MODE) ? kEpiBytes : 0));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sC + head_epi_bytes(MODE));
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint64_t* acc_empty = acc_full + 2;
@@ -411,8 +439,8 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int half = static_cast<int>(ptx::cluster_ctarank() & 1u);
-  const bool leader = half == 0;
+  const int cta = static_cast<int>(ptx::cluster_ctarank() & 1u);  // which 128 rows of the pair's tile
+  const bool leader = cta == 0;
   const int worker = blockIdx.x / 2;
   const int workers = gridDim.x / 2;
 
@@ -423,7 +451,7 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&acc_full[b]), 1);
-      ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * kEpiWarps);
+      ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * 4 * head_halves(MODE));
     }
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0u;
@@ -432,7 +460,7 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
   if (warp == 0 && lane == 0) {
     ptx::tma_prefetch_desc(&mapA);
     ptx::tma_prefetch_desc(&mapB);
-    if (head_staged(MODE)) ptx::tma_prefetch_desc(&mapC);
+    if (MODE != HEAD_STATS) ptx::tma_prefetch_desc(&mapC);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), TMEM_COLS);
@@ -447,8 +475,8 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
   ptx::griddep_wait();
 
   const Ctl ctl{abort_flag, args.timeout_ns, args.status};
-  const Tiles tiles = head_tiles<MODE>(args);
-  constexpr int TERMS = plane_terms(PLANES);
+  const int n = args.count ? min(*args.count, args.T) : args.T;
+  const Tiles tiles = head_tiles<MODE>(args, max(1, n));
   // stages summed in tensor memory at a time: all of a unit's, or a chunk
   const int chunk = PLANES > 1 && (MODE == HEAD_DH || MODE == HEAD_DW) ? args.chunk : INT_MAX / 2;
 
@@ -460,8 +488,8 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
       bool ok = true;
       for (int i = worker; ok && i < tiles.units; i += workers) {
         const HeadUnit u = head_unit<MODE>(args, tiles, i);
-        const int m0 = u.mb * kHeadTile + half * kTileM;
-        const int n0 = u.nb * kHeadTile + half * (kHeadTile / 2);
+        const int m0 = u.mb * kHeadTile + cta * kTileM;
+        const int n0 = u.nb * kHeadTile + cta * (kHeadTile / 2);
         for (int lo = u.lo; ok && lo < u.hi; lo += chunk) {
           const int span = min(chunk, u.hi - lo);
           for (int it = 0; it < TERMS * span; ++it) {
@@ -560,15 +588,15 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
     __syncwarp();
   } else {
     // --------------------------------------------------------- epilogue
-    const int quarter = warp & 3;
-    uint8_t* stage_base = sC + (warp - 2) * 2 * 4096;
-    const int n = min(*args.count, args.T);
-    int acc = 0, sbuf = 0;
+    const int quarter = warp & 3;              // tensor-memory lanes of this warp
+    const int half = (warp - 2) / 4;           // its half of the tile's columns
+    uint8_t* buf = sC + (warp - 2) * 4096;
+    int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int i = worker; ok && i < tiles.units; i += workers) {
       const HeadUnit u = head_unit<MODE>(args, tiles, i);
-      const int row0 = u.mb * kHeadTile + half * kTileM + quarter * 32;
+      const int row0 = u.mb * kHeadTile + cta * kTileM + quarter * 32;
       for (int lo = u.lo; lo < u.hi; lo += chunk) {
         if (!warp_wait(ptx::smem_u32(&acc_full[acc]), acc_phase, ctl, SITE_EPI_ACC_FULL)) {
           ok = false;
@@ -580,7 +608,7 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
         if constexpr (MODE == HEAD_STATS) {
           if (row0 < n) epilogue_stats(tbase, row0 + lane, n, u.nb, args);
         } else if constexpr (MODE == HEAD_DZ) {
-          epilogue_dz<PLANES>(tbase, row0, n, u.nb, args, &mapC, stage_base, sbuf, lane);
+          epilogue_dz<PLANES>(tbase, row0, n, u.nb, half, args, &mapC, buf, lane);
         } else if constexpr (PLANES > 1) {
           // a chunk's sum of the full-size terms took 4 steps a stage
           const float put_back = 1.0f + kStepLoss * static_cast<float>(4 * min(chunk, u.hi - lo));
@@ -589,16 +617,15 @@ __global__ void __launch_bounds__(32 * (2 + kEpiWarps), 1)
           if constexpr (MODE == HEAD_DH) {
             if (row0 < n)
               epilogue_f32(tbase, out + u.split * args.split_stride + static_cast<int64_t>(row) * args.ld_out, row < n,
-                           u.nb * kHeadTile, args.D, put_back, true, args.reduce || lo > u.lo);
-          } else {
-            if (row0 < args.cols)
-              epilogue_f32(tbase, out + static_cast<int64_t>(args.out_row0 + row) * args.ld_out, row < args.cols,
-                           u.nb * kHeadTile, args.D, put_back * *args.factor, args.store_granule == 16, lo > u.lo);
+                           u.nb, half, args.D, put_back, true, args.reduce || lo > u.lo);
+          } else if (row0 < args.cols) {
+            epilogue_f32(tbase, out + static_cast<int64_t>(args.out_row0 + row) * args.ld_out, row < args.cols, u.nb,
+                         half, args.D, put_back * *args.factor, args.store_granule == 16, lo > u.lo);
           }
         } else if constexpr (MODE == HEAD_DH) {
-          epilogue_dh(tbase, row0, u, args, &mapC, stage_base, sbuf, lane);
+          epilogue_dh(tbase, row0, u, half, args, &mapC, buf, lane);
         } else {
-          epilogue_dw(tbase, row0, u.nb, args, &mapC, stage_base, sbuf, lane);
+          epilogue_dw(tbase, row0, u.nb, half, args, &mapC, buf, lane);
         }
         ptx::tc_fence_before_sync();
         __syncwarp();
@@ -637,7 +664,7 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.blockDim = dim3(32 * (2 + kEpiWarps), 1, 1);
+  cfg.blockDim = dim3(head_threads(MODE), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -656,9 +683,9 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
 
 cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUtensorMap& mapB,
                         const CUtensorMap& mapC, const HeadArgs& args, int pairs, cudaStream_t stream) {
-#define TGEMM_HEAD(MODE)                                                                         \
-  case MODE:                                                                                     \
-    return planes == 1 ? launch<MODE, 1>(mapA, mapB, mapC, args, pairs, stream)                  \
+#define TGEMM_HEAD(MODE)                                                                  \
+  case MODE:                                                                              \
+    return planes == 1 ? launch<MODE, 1>(mapA, mapB, mapC, args, pairs, stream)           \
                        : launch<MODE, kPlanes>(mapA, mapB, mapC, args, pairs, stream)
   switch (mode) {
     TGEMM_HEAD(HEAD_STATS);

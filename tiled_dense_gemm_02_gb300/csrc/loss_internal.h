@@ -27,14 +27,16 @@ int host_granule(const void* p, int64_t ld, int es);
 // --------------------------------------------------- rows that count
 // What the row kernels leave for the products, all in the workspace.  Row r of
 // the gathered matrix (r < *count) is row source[r] of H; place[t] is its
-// inverse (-1: row t does not count).  Row t's targets are ids[t*K .. t*K+K),
-// ascending, with masses q; unused places come last with id INT_MAX.
+// inverse (-1: row t does not count).  Distillation: row t's list is ids[t*K ..
+// t*K+K), ascending, with masses q; unused places come last with id INT_MAX.
+// Forward calls that read H in place have no gathered rows: count, source and
+// place are then null, and row r is row r of H.
 struct HeadRows {
   int* count;         // rows that count
   float* factor;      // what the gradient products' sums are multiplied with
   int* source;        // T
   int* place;         // T
-  int* ids;           // T x K
+  int* ids;           // T x K (distillation)
   float* q;           // T x K
   float* own;         // T: sum q log q (distillation), else null
   unsigned char* flags;  // T (distillation), else null
@@ -53,15 +55,22 @@ constexpr unsigned char kRowIgnored = 0, kRowCounts = 1, kRowBad = 2;
 // Gathered rows are zero-filled up to a multiple of this (and at least one such block), capped at T.
 constexpr int kRowBlock = 256;
 
+// Whether row t counts, from its target (targets not null) or its list's flag.
+struct RowRule {
+  const int64_t* targets;    // cross entropy, else null
+  int64_t ignore_index;
+  const unsigned char* flags;
+  int V;
+};
+
 struct GatherArgs {
-  int T, V, D, K;
+  int T, D;
   int es;                    // bytes of an element of H
   const void* H;
   int64_t ldh;
   int granule;               // alignment of H's rows (16, 8, 4 or 2 bytes)
-  const int64_t* targets;    // cross entropy, else null
-  int64_t ignore_index;
-  float smoothing, z_loss, scale;
+  RowRule rule;
+  float z_loss, scale;
   float range;               // power of two that the stored gradients are scaled with
   const float* lse;          // backward: the forward call's, else null
   const float* grad;         // backward
@@ -73,11 +82,11 @@ cudaError_t launch_distill_lists(const int64_t* ids, int64_t ld_ids, const float
                                  int V, int K, float scale, const HeadRows& rows, cudaStream_t stream);
 cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream);
 
-// Row statistics of `tiles` column tiles: ms[i * T + r] = {max, sum of
-// 2^(y - max)} of y = z log2(e) over tile i, dot[i * T + r] = its share of
-// sum q z / scale.
+// Row statistics of `tiles` parts of the columns: ms[i * T + r] = {max, sum of
+// 2^(y - max)} of y = z log2(e) over part i, dot[i * T + r] = its share of
+// sum q z / scale.  Without gathered rows it also writes those that do not count.
 cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T, float scale, float z_loss,
-                           const HeadRows& rows, float* loss, float* lse, cudaStream_t stream);
+                           const HeadRows& rows, const RowRule& rule, float* loss, float* lse, cudaStream_t stream);
 // dH row t = factor * sum over splits of acc[s][place[t]], or 0.
 cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
                              const HeadRows& rows, int type, void* dH, int64_t lddh, cudaStream_t stream);
@@ -97,7 +106,7 @@ enum HeadMode : int {
 struct HeadArgs {
   const int* count;
   int T, V, K, D;
-  int cols;       // columns of this piece
+  int cols;       // entries of this piece of the vocabulary
   int col0;       // vocabulary entry of the piece's column 0
   int b_row0;     // STATS, DZ, DH: row of the weight map for the piece's column 0
   int k_blocks;   // 64-deep stages of the k axis (DW: from the count)
@@ -108,8 +117,10 @@ struct HeadArgs {
   int bf16;
   float k2;       // scale * log2(e)
   float flat;     // eps / V (cross entropy), else 0
-  const int* source;
-  const int* ids;
+  const int64_t* targets;   // cross entropy: one target per row of H, with mass `mass`
+  float mass;
+  const int* source;        // null: row r is row r of H, and count is null
+  const int* ids;           // distillation
   const float* q;
   float2* ms;     // STATS
   float* dot;
@@ -134,10 +145,35 @@ struct HeadArgs {
 // 1.2e-6 off to a few 1e-7.
 constexpr float kStepLoss = 1.0f / (1 << 26);
 
-// Output tile of every mode: 256 x 256 per CTA pair.
+// Output tile of every product: 256 x 256 per CTA pair.
 constexpr int kHeadTile = 256;
 // planes: 1 (16-bit operands) or 3 (fp32).
-cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
-                        const HeadArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUtensorMap& mapB,
+                        const CUtensorMap& mapC, const HeadArgs& args, int pairs, cudaStream_t stream);
+
+// ------------------------------------------------------------- few rows
+// Statistics of T <= kFewRows rows of H, read in place, in one pass over W on
+// the CUDA cores; few_blocks(V) parts.
+struct FewArgs {
+  int T, V, D, K;
+  const void* H;
+  int64_t ldh;
+  const void* W;
+  int64_t ldw;
+  float k2, flat;
+  const int64_t* targets;
+  float mass;
+  const int* ids;
+  const float* q;
+  float2* ms;
+  float* dot;
+};
+constexpr int kFewRows = 8;
+constexpr int kFewSmem = 160 * 1024;
+constexpr int kFewBlocks = 304;
+bool few_rows(int64_t T, int64_t D);
+int few_blocks(int64_t V);
+// type: 0 bf16, 1 f16, 2 f32; granule: alignment of W's rows
+cudaError_t launch_few_stats(const FewArgs& a, int type, int granule, cudaStream_t stream);
 
 }  // namespace tgemm

@@ -121,11 +121,16 @@ __global__ void __launch_bounds__(kListWarps * 32)
 }
 
 // ---------------------------------------------------------------- the gather
-__device__ __forceinline__ unsigned char row_flag(const GatherArgs& a, int t) {
-  if (!a.targets) return a.rows.flags[t];
+__device__ __forceinline__ unsigned char row_flag(const RowRule& a, int t) {
+  if (!a.targets) return a.flags[t];
   const int64_t y = a.targets[t];
   if (y == a.ignore_index) return kRowIgnored;
   return (y >= 0 && y < a.V) ? kRowCounts : kRowBad;
+}
+
+// loss and lse of a row that does not count
+__device__ __forceinline__ float row_value(unsigned char flag) {
+  return flag == kRowBad ? __int_as_float(0x7FC00000) : 0.0f;
 }
 
 __device__ __forceinline__ float grad_p(const GatherArgs& a, int t) {
@@ -133,25 +138,39 @@ __device__ __forceinline__ float grad_p(const GatherArgs& a, int t) {
   return a.z_loss == 0.0f ? g : g * (1.0f + 2.0f * a.z_loss * a.lse[t]);
 }
 
-// Copies `bytes` (a multiple of G) with 32 lanes.
+// Copies `count` rows of `bytes` (a multiple of G) each, src[r] -> dst + r *
+// pitch, with the whole block.
 template <int G>
-__device__ __forceinline__ void copy_row(uint8_t* dst, const uint8_t* src, int64_t bytes, int lane) {
+__device__ __forceinline__ void copy_rows(uint8_t* dst, int64_t pitch, const uint8_t* H, int64_t src_pitch,
+                                          const int* src, int count, int bytes) {
   using Word = typename std::conditional<
       G == 16, uint4, typename std::conditional<G == 8, uint2, typename std::conditional<G == 4, uint32_t, uint16_t>::type>::type>::type;
-  const Word* s = reinterpret_cast<const Word*>(src);
-  Word* d = reinterpret_cast<Word*>(dst);
-  const int64_t n = bytes / G;
+  const int words = bytes / G;
+  if (count * words <= 2 * static_cast<int>(blockDim.x) || words >= static_cast<int>(blockDim.x)) {
+    // long rows, one after another, or hardly any work
+    for (int r = 0; r < count; ++r) {
+      const Word* s = reinterpret_cast<const Word*>(H + static_cast<int64_t>(src[r]) * src_pitch);
+      Word* d = reinterpret_cast<Word*>(dst + r * pitch);
 #pragma unroll 4
-  for (int64_t i = lane; i < n; i += 32) d[i] = s[i];
+      for (int i = threadIdx.x; i < words; i += blockDim.x) d[i] = s[i];
+    }
+  } else {  // short rows, one per warp
+    for (int r = threadIdx.x >> 5; r < count; r += blockDim.x >> 5) {
+      const Word* s = reinterpret_cast<const Word*>(H + static_cast<int64_t>(src[r]) * src_pitch);
+      Word* d = reinterpret_cast<Word*>(dst + r * pitch);
+#pragma unroll 4
+      for (int i = threadIdx.x & 31; i < words; i += 32) d[i] = s[i];
+    }
+  }
 }
 
 // An fp32 row as three bf16 planes.  A value that is not finite goes to the
-// first plane alone.  32 lanes, four elements each; the planes' pitch is a
+// first plane alone.  `lanes` threads, four elements each; the planes' pitch is a
 // multiple of 8, so whole groups are written.
 __device__ __forceinline__ void split_row(uint16_t* dst, int64_t plane, const float* src, int cols, bool vec,
-                                          int lane) {
+                                          int lane, int lanes) {
 #pragma unroll 2
-  for (int c = lane * 4; c < cols; c += 128) {
+  for (int c = lane * 4; c < cols; c += 4 * lanes) {
     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (vec && c + 4 <= cols) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(src + c));
@@ -196,7 +215,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
   int before = 0, total = 0;
   float gmax = 0.0f, cmax = 0.0f;
   for (int t = tid; t < a.T; t += kGatherThreads) {
-    if (row_flag(a, t) != kRowCounts) continue;
+    if (row_flag(a.rule, t) != kRowCounts) continue;
     ++total;
     before += t < t0 ? 1 : 0;
     if (a.grad) {
@@ -210,7 +229,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
   gmax = warp_max(gmax);
   cmax = warp_max(cmax);
   const int t = t0 + tid;
-  const unsigned char flag = t < t1 ? row_flag(a, t) : kRowIgnored;
+  const unsigned char flag = t < t1 ? row_flag(a.rule, t) : kRowIgnored;
   const unsigned ballot = __ballot_sync(0xffffffffu, flag == kRowCounts);
   if (lane == 0) {
     s_before[warp] = before;
@@ -249,10 +268,6 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     const int place = before + local + __popc(ballot & ((1u << lane) - 1u));
     const bool counts = flag == kRowCounts;
     a.rows.place[t] = counts ? place : -1;
-    if (a.targets) {
-      a.rows.ids[t] = counts ? static_cast<int>(a.targets[t]) : INT_MAX;
-      a.rows.q[t] = 1.0f - a.smoothing;
-    }
     if (counts) {
       a.rows.source[place] = t;
       s_src[place - before] = t;
@@ -261,29 +276,30 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
         a.rows.coef[place] = make_float4(grad_p(a, t) / unit * up, a.grad[t] / unit * up, a.lse[t] * kLog2e, 0.0f);
       }
     } else if (a.loss_out) {
-      const float v = flag == kRowBad ? __int_as_float(0x7FC00000) : 0.0f;
-      a.loss_out[t] = v;
-      a.lse_out[t] = v;
+      a.loss_out[t] = a.lse_out[t] = row_value(flag);
     }
   }
   __syncthreads();
-  const int64_t row_bytes = static_cast<int64_t>(a.D) * a.es;
   uint16_t* const out = static_cast<uint16_t*>(a.rows.h);
-  for (int r = warp; r < mine; r += kGatherThreads / 32) {
-    const uint8_t* src = static_cast<const uint8_t*>(a.H) + static_cast<int64_t>(s_src[r]) * a.ldh * a.es;
-    uint16_t* row = out + static_cast<int64_t>(before + r) * a.rows.ldh;
-    if (a.es == 4) {
-      split_row(row, a.rows.plane, reinterpret_cast<const float*>(src), a.D, a.granule == 16, lane);
-      continue;
-    }
-    uint8_t* dst = reinterpret_cast<uint8_t*>(row);
+  if (a.es == 4) {
+    // a row per warp, or the block's warps share rows too few for them
+    const int per = mine < kGatherThreads / 32 ? kGatherThreads / 32 / max(1, mine) : 1;  // warps per row
+    for (int r = warp / per; r < mine; r += kGatherThreads / 32 / per)
+      split_row(out + static_cast<int64_t>(before + r) * a.rows.ldh, a.rows.plane,
+                static_cast<const float*>(a.H) + static_cast<int64_t>(s_src[r]) * a.ldh, a.D, a.granule == 16,
+                (warp % per) * 32 + lane, 32 * per);
+  } else {
+    uint8_t* dst = reinterpret_cast<uint8_t*>(out + static_cast<int64_t>(before) * a.rows.ldh);
+    const uint8_t* H = static_cast<const uint8_t*>(a.H);
+    const int64_t pitch = a.rows.ldh * 2, src_pitch = a.ldh * 2;
+    const int bytes = a.D * 2;
     int g = a.granule;
-    while (row_bytes % g) g >>= 1;
+    while (bytes % g) g >>= 1;
     switch (g) {
-      case 16: copy_row<16>(dst, src, row_bytes, lane); break;
-      case 8: copy_row<8>(dst, src, row_bytes, lane); break;
-      case 4: copy_row<4>(dst, src, row_bytes, lane); break;
-      default: copy_row<2>(dst, src, row_bytes, lane); break;
+      case 16: copy_rows<16>(dst, pitch, H, src_pitch, s_src, mine, bytes); break;
+      case 8: copy_rows<8>(dst, pitch, H, src_pitch, s_src, mine, bytes); break;
+      case 4: copy_rows<4>(dst, pitch, H, src_pitch, s_src, mine, bytes); break;
+      default: copy_rows<2>(dst, pitch, H, src_pitch, s_src, mine, bytes); break;
     }
   }
   // zeros from the last gathered row to the end of its block of rows, which
@@ -311,10 +327,10 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 
 __global__ void __launch_bounds__(kCombineRows * kCombineSlots)
     combine_kernel(const float2* __restrict__ ms, const float* __restrict__ dot, int tiles, int T, float scale,
-                   float z_loss, HeadRows rows, float* __restrict__ loss, float* __restrict__ lse) {
+                   float z_loss, HeadRows rows, RowRule rule, float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ float s_m[kCombineSlots][kCombineRows], s_s[kCombineSlots][kCombineRows], s_d[kCombineSlots][kCombineRows];
   chain();
-  const int n = min(*rows.count, T);
+  const int n = rows.count ? min(*rows.count, T) : T;
   const int r0 = blockIdx.x * kCombineRows;
   if (r0 >= n) return;
   const int lr = threadIdx.x % kCombineRows, slot = threadIdx.x / kCombineRows;
@@ -343,12 +359,13 @@ __global__ void __launch_bounds__(kCombineRows * kCombineSlots)
     __syncthreads();
   }
   if (slot == 0 && r < n) {
-    const int t = rows.source[r];
+    const int t = rows.source ? rows.source[r] : r;
     const float l = s_m[0][lr] * kLn2 + logf(s_s[0][lr]);
     float v = (rows.own ? rows.own[t] : 0.0f) + (l - scale * s_d[0][lr]);
     if (z_loss != 0.0f) v = fmaf(z_loss * l, l, v);
-    loss[t] = v;
-    lse[t] = l;
+    const unsigned char flag = rows.count ? kRowCounts : row_flag(rule, t);
+    loss[t] = flag == kRowCounts ? v : row_value(flag);
+    lse[t] = flag == kRowCounts ? l : row_value(flag);
   }
 }
 
@@ -362,43 +379,47 @@ __device__ __forceinline__ __half to_out<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// One block per row of dH; the sums' pitch is a multiple of four.
+// Four columns of one row per thread; the sums' pitch is a multiple of four.
+constexpr int kFinishThreads = 128;
 template <typename Out>
-__global__ void __launch_bounds__(128) finish_dh_kernel(const float* __restrict__ acc, int64_t ld_acc,
-                                                        int64_t split_stride, int splits, int D, HeadRows rows,
-                                                        Out* __restrict__ dH, int64_t lddh, int wide) {
+__global__ void __launch_bounds__(kFinishThreads) finish_dh_kernel(const float* __restrict__ acc, int64_t ld_acc,
+                                                                   int64_t split_stride, int splits, int T, int D,
+                                                                   HeadRows rows, Out* __restrict__ dH, int64_t lddh,
+                                                                   int wide) {
   chain();
-  const int t = blockIdx.x;
+  const int groups = (D + 3) / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kFinishThreads + threadIdx.x;
+  const int t = static_cast<int>(i / groups), c = static_cast<int>(i - static_cast<int64_t>(t) * groups) * 4;
+  if (t >= T) return;
   const int place = rows.place[t];
   const float f = *rows.factor;
-  Out* out = dH + static_cast<int64_t>(t) * lddh;
-  for (int c = threadIdx.x * 4; c < D; c += blockDim.x * 4) {
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (place >= 0) {
-      const float* src = acc + static_cast<int64_t>(place) * ld_acc + c;
-      for (int s = 0; s < splits; ++s) {
-        const float4 p = *reinterpret_cast<const float4*>(src + s * split_stride);
-        v.x += p.x;
-        v.y += p.y;
-        v.z += p.z;
-        v.w += p.w;
-      }
-      v.x *= f;
-      v.y *= f;
-      v.z *= f;
-      v.w *= f;
+  Out* out = dH + static_cast<int64_t>(t) * lddh + c;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (place >= 0) {
+    const float* src = acc + static_cast<int64_t>(place) * ld_acc + c;
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+      const float4 p = __ldcg(reinterpret_cast<const float4*>(src + s * split_stride));
+      v.x += p.x;
+      v.y += p.y;
+      v.z += p.z;
+      v.w += p.w;
     }
-    const Out o[4] = {to_out<Out>(v.x), to_out<Out>(v.y), to_out<Out>(v.z), to_out<Out>(v.w)};
-    if (wide && c + 4 <= D) {
-      if constexpr (sizeof(Out) == 4)
-        *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(o);
-      else
-        *reinterpret_cast<uint2*>(out + c) = *reinterpret_cast<const uint2*>(o);
-    } else {
+    v.x *= f;
+    v.y *= f;
+    v.z *= f;
+    v.w *= f;
+  }
+  const Out o[4] = {to_out<Out>(v.x), to_out<Out>(v.y), to_out<Out>(v.z), to_out<Out>(v.w)};
+  if (wide && c + 4 <= D) {
+    if constexpr (sizeof(Out) == 4)
+      *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(o);
+    else
+      *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(o);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + i < D) out[c + i] = o[i];
-    }
+    for (int j = 0; j < 4; ++j)
+      if (c + j < D) out[j] = o[j];
   }
 }
 
@@ -408,7 +429,7 @@ __global__ void __launch_bounds__(128) split_kernel(const float* __restrict__ W,
   chain();
   const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (r >= rows) return;
-  split_row(out + r * ld_out, plane, W + r * ldw, cols, vec != 0, threadIdx.x & 31);
+  split_row(out + r * ld_out, plane, W + r * ldw, cols, vec != 0, threadIdx.x & 31, 32);
 }
 
 }  // namespace
@@ -423,28 +444,29 @@ cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
   // a few blocks per SM, at most one row per thread of a block
   const int target = 4 * sms;
   int rows_per = (a.T + target - 1) / target;
-  rows_per = rows_per < 8 ? 8 : (rows_per > kGatherThreads ? kGatherThreads : rows_per);
+  if (rows_per > kGatherThreads) rows_per = kGatherThreads;
   return launch_chained(gather_kernel, (a.T + rows_per - 1) / rows_per, kGatherThreads, stream, a, rows_per);
 }
 
 cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T, float scale, float z_loss,
-                           const HeadRows& rows, float* loss, float* lse, cudaStream_t stream) {
+                           const HeadRows& rows, const RowRule& rule, float* loss, float* lse, cudaStream_t stream) {
   return launch_chained(combine_kernel, (T + kCombineRows - 1) / kCombineRows, kCombineRows * kCombineSlots, stream, ms,
-                        dot, tiles, T, scale, z_loss, rows, loss, lse);
+                        dot, tiles, T, scale, z_loss, rows, rule, loss, lse);
 }
 
 cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
                              const HeadRows& rows, int type, void* dH, int64_t lddh, cudaStream_t stream) {
   const int es = type == 2 ? 4 : 2;
   const int wide = reinterpret_cast<uint64_t>(dH) % (4 * es) == 0 && lddh % 4 == 0 ? 1 : 0;
+  const int64_t blocks = (static_cast<int64_t>(T) * ((D + 3) / 4) + kFinishThreads - 1) / kFinishThreads;
   if (type == 0)
-    return launch_chained(finish_dh_kernel<__nv_bfloat16>, T, 128, stream, acc, ld_acc, split_stride, splits, D, rows,
-                          static_cast<__nv_bfloat16*>(dH), lddh, wide);
+    return launch_chained(finish_dh_kernel<__nv_bfloat16>, blocks, kFinishThreads, stream, acc, ld_acc, split_stride,
+                          splits, T, D, rows, static_cast<__nv_bfloat16*>(dH), lddh, wide);
   if (type == 1)
-    return launch_chained(finish_dh_kernel<__half>, T, 128, stream, acc, ld_acc, split_stride, splits, D, rows,
-                          static_cast<__half*>(dH), lddh, wide);
-  return launch_chained(finish_dh_kernel<float>, T, 128, stream, acc, ld_acc, split_stride, splits, D, rows,
-                        static_cast<float*>(dH), lddh, wide);
+    return launch_chained(finish_dh_kernel<__half>, blocks, kFinishThreads, stream, acc, ld_acc, split_stride, splits, T,
+                          D, rows, static_cast<__half*>(dH), lddh, wide);
+  return launch_chained(finish_dh_kernel<float>, blocks, kFinishThreads, stream, acc, ld_acc, split_stride, splits, T, D,
+                        rows, static_cast<float*>(dH), lddh, wide);
 }
 
 cudaError_t launch_split(const float* W, int64_t ldw, void* out, int64_t ld_out, int64_t plane, int rows, int cols,

@@ -120,7 +120,7 @@ def _pitch(name, t, rows, cols):
         raise ValueError(f"{name} must have rows that do not overlap")
     if cols > 1 and step != 1 and rows:
         raise ValueError(f"{name} must have unit column stride")
-    return ld if ld > 1 else 1
+    return ld or 1
 
 
 def _vector(name, t, n, dtype, device):
@@ -149,62 +149,58 @@ def _on_stream(function):
     return call
 
 
-class _Head:
-    """The arguments every call shares, checked, and its workspace."""
-    __slots__ = ("torch", "T", "V", "D", "code", "device", "matrices", "options", "workspace")
+def _head(hidden, weight, backward, K, options, workspace):
+    """Checks what every call shares: (torch, device, (T, V, D), dtype code, matrices' arguments, options, workspace)."""
+    import torch
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden [T, D] and weight [V, D] must be matrices")
+    T, D = hidden.shape
+    V, columns = weight.shape
+    dtype = hidden.dtype
+    if columns != D or weight.dtype != dtype:
+        raise ValueError(f"weight must be [V, {D}] {dtype}, got {tuple(weight.shape)} {weight.dtype}")
+    code = BF16 if dtype == torch.bfloat16 else F16 if dtype == torch.float16 else F32
+    if code == F32 and dtype != torch.float32:
+        raise ValueError(f"unsupported dtype: {dtype}")
+    device = hidden.get_device()
+    if device < 0 or weight.get_device() != device:
+        raise ValueError("hidden and weight must be on one CUDA device")
+    ldh, ldw = _pitch("hidden", hidden, T, D), _pitch("weight", weight, V, D)
+    w = weight.data_ptr()
+    options = _options(*options)
+    need = _size(backward, T, V, D, K, w % 16, ldw, code, options)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=hidden.device)
+    elif workspace.get_device() != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+            workspace.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on the device of hidden")
+    else:
+        need = workspace.numel()
+    return torch, device, (T, V, D), code, (hidden.data_ptr(), ldh, w, ldw), options, workspace, need
 
-    def __init__(self, hidden, weight, backward, K, options, workspace):
-        import torch
-        self.torch = torch
-        if hidden.dim() != 2 or weight.dim() != 2:
-            raise ValueError("hidden [T, D] and weight [V, D] must be matrices")
-        T, D = hidden.shape
-        V, columns = weight.shape
-        dtype = hidden.dtype
-        if columns != D or weight.dtype != dtype:
-            raise ValueError(f"weight must be [V, {D}] {dtype}, got {tuple(weight.shape)} {weight.dtype}")
-        code = BF16 if dtype == torch.bfloat16 else F16 if dtype == torch.float16 else F32
-        if code == F32 and dtype != torch.float32:
-            raise ValueError(f"unsupported dtype: {dtype}")
-        device = hidden.get_device()
-        if device < 0 or weight.get_device() != device:
-            raise ValueError("hidden and weight must be on one CUDA device")
-        ldh, ldw = _pitch("hidden", hidden, T, D), _pitch("weight", weight, V, D)
-        w = weight.data_ptr()
-        self.T, self.V, self.D, self.code, self.device = T, V, D, code, device
-        self.matrices = (hidden.data_ptr(), ldh, w, ldw)
-        self.options = _options(*options)
-        need = _size(backward, T, V, D, K, w % 16, ldw, code, self.options)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=hidden.device)
-        elif workspace.get_device() != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-                workspace.numel() < need:
-            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on the device of "
-                             "hidden")
-        self.workspace = workspace
 
-    def call(self, function, *args):
-        cuda = self.torch.cuda
-        args += (self.workspace.data_ptr(), self.workspace.numel(), cuda.current_stream(self.device).cuda_stream)
-        if cuda.current_device() == self.device:
+def _call(torch, device, function, args, workspace, need):
+    args += (workspace.data_ptr(), need, torch.cuda.current_stream(device).cuda_stream)
+    if torch.cuda.current_device() == device:
+        st = function(*args)
+    else:
+        with torch.cuda.device(device):
             st = function(*args)
-        else:
-            with cuda.device(self.device):
-                st = function(*args)
-        if st != OK:
-            raise TgemmError(st, function.__name__)
+    if st != OK:
+        raise TgemmError(st, function.__name__)
 
-    def losses(self, hidden):
-        f32 = self.torch.float32
-        return (self.torch.empty(self.T, dtype=f32, device=hidden.device),
-                self.torch.empty(self.T, dtype=f32, device=hidden.device))
 
-    def gradients(self, hidden, weight, want_hidden, want_weight):
-        """Outputs in the operands' type, with their pointers and pitches (0 when not wanted)."""
-        empty, D = self.torch.empty, self.D
-        dh = empty((self.T, D), dtype=hidden.dtype, device=hidden.device) if want_hidden else None
-        dw = empty((self.V, D), dtype=hidden.dtype, device=hidden.device) if want_weight else None
-        return dh, dw, (dh.data_ptr() if want_hidden else 0, D, dw.data_ptr() if want_weight else 0, D)
+def _losses(torch, T, device):
+    # two allocations cost less than two views of one
+    return torch.empty(T, dtype=torch.float32, device=device), torch.empty(T, dtype=torch.float32, device=device)
+
+
+def _gradients(torch, hidden, sizes, want_hidden, want_weight):
+    """Outputs in the operands' type, with their pointers and pitches (0 when not wanted)."""
+    T, V, D = sizes
+    dh = torch.empty((T, D), dtype=hidden.dtype, device=hidden.device) if want_hidden else None
+    dw = torch.empty((V, D), dtype=hidden.dtype, device=hidden.device) if want_weight else None
+    return dh, dw, (dh.data_ptr() if want_hidden else 0, D, dw.data_ptr() if want_weight else 0, D)
 
 
 def _positive(name, value):
@@ -225,11 +221,12 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, scale=1.
     backward call takes.  Reduce as you like: ``loss.sum() / n``.
     """
     options = (_positive("scale", scale), label_smoothing, z_loss, piece, ignore_index)
-    h = _Head(hidden, weight, False, 0, options, workspace)
-    targets = _vector("targets", targets, h.T, h.torch.int64, h.device)
-    loss, lse = h.losses(hidden)
-    h.call(_lib.tgemm_xent_forward, h.T, h.V, h.D, *h.matrices, targets.data_ptr(), h.code, h.options,
-           loss.data_ptr(), lse.data_ptr())
+    torch, device, sizes, code, matrices, options, workspace, need = _head(hidden, weight, False, 0, options, workspace)
+    targets = _vector("targets", targets, sizes[0], torch.int64, device)
+    loss, lse = _losses(torch, sizes[0], hidden.device)
+    _call(torch, device, _lib.tgemm_xent_forward, sizes + matrices + (targets.data_ptr(), code, options,
+                                                                      loss.data_ptr(), lse.data_ptr()),
+          workspace, need)
     return loss, lse
 
 
@@ -241,32 +238,35 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, *, ig
     operands' type; ``lse`` from the forward call with the same options,
     grad_loss [T] float32.  An unwanted gradient is not computed (None)."""
     options = (_positive("scale", scale), label_smoothing, z_loss, piece, ignore_index)
-    h = _Head(hidden, weight, True, 0, options, workspace)
-    f32 = h.torch.float32
-    targets = _vector("targets", targets, h.T, h.torch.int64, h.device)
-    lse, grad_loss = _vector("lse", lse, h.T, f32, h.device), _vector("grad_loss", grad_loss, h.T, f32, h.device)
-    dh, dw, out = h.gradients(hidden, weight, want_hidden, want_weight)
-    h.call(_lib.tgemm_xent_backward, h.T, h.V, h.D, *h.matrices, targets.data_ptr(), lse.data_ptr(),
-           grad_loss.data_ptr(), h.code, h.options, *out)
+    torch, device, sizes, code, matrices, options, workspace, need = _head(hidden, weight, True, 0, options, workspace)
+    targets = _vector("targets", targets, sizes[0], torch.int64, device)
+    lse = _vector("lse", lse, sizes[0], torch.float32, device)
+    grad_loss = _vector("grad_loss", grad_loss, sizes[0], torch.float32, device)
+    dh, dw, out = _gradients(torch, hidden, sizes, want_hidden, want_weight)
+    _call(torch, device, _lib.tgemm_xent_backward,
+          sizes + matrices + (targets.data_ptr(), lse.data_ptr(), grad_loss.data_ptr(), code, options) + out,
+          workspace, need)
     return dh, dw
 
 
 def _teacher(hidden, weight, backward, ids, logits, temperature, piece, workspace):
-    """The head of a distillation call, the teacher's logits in float32, and the lists' arguments."""
+    """What _head gives, the teacher's logits in float32, and the lists' arguments."""
     if ids.dim() != 2 or logits.shape != ids.shape:
         raise ValueError("teacher_ids and teacher_logits must be matrices of one shape [T, K]")
     rows, K = ids.shape
-    h = _Head(hidden, weight, backward, K, (1.0 / _positive("temperature", temperature), 0.0, 0.0, piece, 0), workspace)
-    if rows != h.T or ids.dtype != h.torch.int64:
-        raise ValueError(f"teacher_ids must be [{h.T}, K] int64, got {tuple(ids.shape)} {ids.dtype}")
     if K < 1:
         raise ValueError("the teacher's lists must have at least one place")
-    if ids.get_device() != h.device or logits.get_device() != h.device:
+    head = _head(hidden, weight, backward, K, (1.0 / _positive("temperature", temperature), 0.0, 0.0, piece, 0),
+                 workspace)
+    torch, device, sizes = head[:3]
+    if rows != sizes[0] or ids.dtype != torch.int64:
+        raise ValueError(f"teacher_ids must be [{sizes[0]}, K] int64, got {tuple(ids.shape)} {ids.dtype}")
+    if ids.get_device() != device or logits.get_device() != device:
         raise ValueError("teacher_ids and teacher_logits must be on the device of hidden")
-    if logits.dtype != h.torch.float32:
+    if logits.dtype != torch.float32:
         logits = logits.float()
-    return h, logits, (ids.data_ptr(), _pitch("teacher_ids", ids, rows, K), logits.data_ptr(),
-                       _pitch("teacher_logits", logits, rows, K))
+    return head, logits, (ids.data_ptr(), _pitch("teacher_ids", ids, rows, K), logits.data_ptr(),
+                          _pitch("teacher_logits", logits, rows, K))
 
 
 @_on_stream
@@ -279,10 +279,11 @@ def linear_distillation(hidden, weight, teacher_ids, teacher_logits, *, temperat
     any float type, K up to 256.  A row without a used place gets loss and lse
     0.  The losses are not multiplied by temperature squared.
     """
-    h, logits, lists = _teacher(hidden, weight, False, teacher_ids, teacher_logits, temperature, piece, workspace)
-    loss, lse = h.losses(hidden)
-    h.call(_lib.tgemm_distill_forward, h.T, h.V, h.D, teacher_ids.shape[1], *h.matrices, *lists, h.code, h.options,
-           loss.data_ptr(), lse.data_ptr())
+    head, logits, lists = _teacher(hidden, weight, False, teacher_ids, teacher_logits, temperature, piece, workspace)
+    torch, device, sizes, code, matrices, options, workspace, need = head
+    loss, lse = _losses(torch, sizes[0], hidden.device)
+    _call(torch, device, _lib.tgemm_distill_forward,
+          (*sizes, logits.shape[1], *matrices, *lists, code, options, loss.data_ptr(), lse.data_ptr()), workspace, need)
     return loss, lse
 
 
@@ -291,10 +292,12 @@ def linear_distillation_backward(hidden, weight, teacher_ids, teacher_logits, ls
                                  piece=0, want_hidden=True, want_weight=True, workspace=None):
     """Gradients ``(d_hidden, d_weight)`` of ``sum(grad_loss * loss)``; lse,
     grad_loss and unwanted gradients as in linear_cross_entropy_backward."""
-    h, logits, lists = _teacher(hidden, weight, True, teacher_ids, teacher_logits, temperature, piece, workspace)
-    f32 = h.torch.float32
-    lse, grad_loss = _vector("lse", lse, h.T, f32, h.device), _vector("grad_loss", grad_loss, h.T, f32, h.device)
-    dh, dw, out = h.gradients(hidden, weight, want_hidden, want_weight)
-    h.call(_lib.tgemm_distill_backward, h.T, h.V, h.D, teacher_ids.shape[1], *h.matrices, *lists, lse.data_ptr(),
-           grad_loss.data_ptr(), h.code, h.options, *out)
+    head, logits, lists = _teacher(hidden, weight, True, teacher_ids, teacher_logits, temperature, piece, workspace)
+    torch, device, sizes, code, matrices, options, workspace, need = head
+    lse = _vector("lse", lse, sizes[0], torch.float32, device)
+    grad_loss = _vector("grad_loss", grad_loss, sizes[0], torch.float32, device)
+    dh, dw, out = _gradients(torch, hidden, sizes, want_hidden, want_weight)
+    _call(torch, device, _lib.tgemm_distill_backward,
+          (*sizes, logits.shape[1], *matrices, *lists, lse.data_ptr(), grad_loss.data_ptr(), code, options, *out),
+          workspace, need)
     return dh, dw
