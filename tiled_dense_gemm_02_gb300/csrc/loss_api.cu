@@ -39,6 +39,11 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;
 // and adding 256 KB per tile takes less time than the 96 stages of six plane
 // products that a chunk runs.
 constexpr int kChunkStages = 16;
+// 16-bit forward calls: k-stages of a tile up to which its statistics, not its
+// product, bound the call, and eight epilogue warps (each with statistics of its
+// own) beat four.  Measured at 4096 x 32768: D = 64 75 -> 66 us, 256 79 -> 70 us
+// with eight; 512 104 -> 97 us, 1024 177 -> 168 us with four.
+constexpr int64_t kShortStages = 6;
 constexpr float kRangeF16 = 16384.0f;  // |dz| <= 2: fp16's largest value is 65504, its small normals reach 2^-14
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -79,9 +84,10 @@ struct Layout {
   int64_t piece = 0, pieces = 1;
   int64_t ldh = 0, ldw_p = 0, ldz = 0, ld_acc = 0;
   int splits = 1, k_per_split = 0;
-  int64_t count = 0, source = 0, place = 0, ids = 0, q = 0, own = 0, flags = 0, coef = 0, h = 0;
+  int64_t count = 0, source = 0, place = 0, target = 0, ids = 0, q = 0, own = 0, flags = 0, coef = 0, h = 0;
   int64_t ms = 0, dot = 0, z = 0, w = 0, acc = 0;
   int64_t parts = 0;           // statistics per row
+  int tile_parts = 1;          // of them per tile
   int64_t total = 0;
 };
 
@@ -137,6 +143,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   l.count = take(256);
   l.source = take(T * 4);
   l.place = take(T * 4);
+  l.target = take(distill ? 0 : T * 8);
   l.ids = take(distill ? T * K * 4 : 0);
   l.q = take(distill ? T * K * 4 : 0);
   l.own = take(distill ? T * 4 : 0);
@@ -149,7 +156,8 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
     plan_dh(T, D, ceil_div(std::min(l.piece, V), kTileK), l.planes == 1 ? 1 : 6, l);
     l.acc = take(l.splits * T * l.ld_acc * 4);
   } else {
-    l.parts = l.few ? few_blocks(V) : ceil_div(V, kHeadTile);
+    l.tile_parts = l.planes == 1 && ceil_div(D, kTileK) <= kShortStages ? 2 : 1;
+    l.parts = l.few ? few_blocks(T, V) : ceil_div(V, kHeadTile) * l.tile_parts;
     l.ms = take(l.parts * T * 8);
     l.dot = take(l.parts * T * 4);
   }
@@ -251,12 +259,11 @@ class Products {
     a_.V = static_cast<int>(c.V);
     a_.K = static_cast<int>(c.K);
     a_.D = static_cast<int>(c.D);
-    a_.group_m = 8;
     a_.bf16 = type_ == 0;  // fp32's planes are bf16
     put_back_ = 1.0f + kStepLoss * static_cast<float>(ceil_div(c.D, 16));
     a_.k2 = static_cast<float>(scale * put_back_ * kLog2e);
     a_.flat = flat;
-    a_.targets = c.distill ? nullptr : c.ids;
+    a_.target = c.distill ? nullptr : l.direct ? c.ids : rows.target;
     a_.mass = 1.0f - (c.opts ? c.opts->label_smoothing : 0.0f);
     a_.source = rows.source;
     a_.ids = rows.ids;
@@ -266,6 +273,7 @@ class Products {
     a_.coef = rows.coef;
     a_.factor = rows.factor;
     a_.splits = 1;
+    a_.parts = l.tile_parts;
     a_.chunk = kChunkStages;
     const int to_us = (c.opts && c.opts->wait_timeout_us) ? c.opts->wait_timeout_us : 2000000;
     a_.timeout_ns = static_cast<unsigned long long>(to_us) * 1000ull;
@@ -351,6 +359,7 @@ class Products {
     b.out = ws_ + l_.acc;
     b.ld_out = l_.ld_acc;
     b.split_stride = c_.T * l_.ld_acc;
+    b.store_granule = l_.planes > 1 && l_.k_per_split > kChunkStages ? 16 : 0;
     CUtensorMap mz, mw, ma;
     TGEMM_TRY(map_dz(&mz, kTileK, kTileM));
     TGEMM_TRY(map_weight(&mw, 64, kTileK));
@@ -363,14 +372,18 @@ class Products {
     b.out = c_.dW;
     b.ld_out = c_.lddw;
     b.out_row0 = static_cast<int>(v0_);
-    b.store_granule = host_granule(c_.dW, c_.lddw, l_.planes > 1 ? 4 : 2);
+    b.reduce = 0;
+    const int64_t stages = ceil_div(c_.T, kTileK);
+    const bool f32 = l_.planes > 1;
+    b.store_granule = host_granule(c_.dW, c_.lddw, f32 ? 4 : 2);
     CUtensorMap mz, mh, mo;
     TGEMM_TRY(map_dz(&mz, 64, kTileK));
     TGEMM_TRY(map_hidden(&mh, 64, kTileK));
-    const bool bulk = l_.planes == 1 && b.store_granule == 16;
+    // fp32 sums of several chunks are added by their owners
+    const bool bulk = b.store_granule == 16 && (!f32 || stages <= kChunkStages);
     if (bulk) {
       b.store_granule = 0;
-      TGEMM_TRY(host_map_3d(&mo, type_, c_.dW, c_.D, c_.V, 1, c_.lddw * 2, 0, 64, 32));
+      TGEMM_TRY(host_map_3d(&mo, f32 ? 2 : type_, c_.dW, c_.D, c_.V, 1, c_.lddw * (f32 ? 4 : 2), 0, f32 ? 32 : 64, 32));
     }
     return launch(HEAD_DW, mz, mh, bulk ? mo : mh, b, ceil_div(n_, kHeadTile) * ceil_div(c_.D, kHeadTile));
   }
@@ -420,6 +433,7 @@ int run_loss(const Call& c) {
     rows.factor = reinterpret_cast<float*>(ws + l.count) + 1;
     rows.source = reinterpret_cast<int*>(ws + l.source);
     rows.place = reinterpret_cast<int*>(ws + l.place);
+    if (!c.distill) rows.target = reinterpret_cast<int64_t*>(ws + l.target);
     rows.h = ws + l.h;
     rows.ldh = l.ldh;
     rows.plane = c.T * l.ldh;

@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <type_traits>
@@ -27,9 +28,11 @@
 namespace tgemm {
 namespace {
 
-constexpr int kFewThreads = 512;
-constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kEntries = 4;  // rows of W per warp and step
+// Eight rows of H fill shared memory: one block of 16 warps per SM; with fewer
+// rows, blocks of 8 warps, as many as registers allow.
+constexpr int few_threads(int tn) { return tn == 8 ? 512 : 256; }
+constexpr int few_per_sm(int tn) { return tn == 8 ? 1 : tn == 4 ? 2 : 4; }
 
 template <typename E>
 constexpr int lane_elems() { return 16 / static_cast<int>(sizeof(E)); }
@@ -79,16 +82,17 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 
 // TN: rows of H, T rounded up to a power of two (the padding is zero).
 template <typename E, int TN, int G>
-__global__ void __launch_bounds__(kFewThreads) few_stats_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(few_threads(TN), few_per_sm(TN)) few_stats_kernel(const FewArgs a) {
   constexpr int N = lane_elems<E>();
+  constexpr int THREADS = few_threads(TN), WARPS = THREADS / 32;
   constexpr int VALUES = kEntries * TN;  // sums a warp holds: 4 to 32
   extern __shared__ __align__(16) float s_h[];  // [t][half of the 16 bytes][group][4]
-  __shared__ float s_part[3][kFewWarps][TN];
+  __shared__ float s_part[3][WARPS][TN];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = (a.D + N - 1) / N;
-  for (int i = threadIdx.x; i < TN * groups; i += kFewThreads) {
+  for (int i = threadIdx.x; i < TN * groups; i += THREADS) {
     const int t = i / groups, g = i - t * groups;
     float v[N];
     if (t < a.T) {
@@ -123,13 +127,15 @@ __global__ void __launch_bounds__(kFewThreads) few_stats_kernel(const FewArgs a)
   }
   float m = -INFINITY, s = 0.0f, dot = 0.0f, zs = 0.0f;
 
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kFewWarps * kEntries;
-  for (int64_t at = (static_cast<int64_t>(blockIdx.x) * kFewWarps + warp) * kEntries; at < a.V; at += stride) {
-    const int v0 = static_cast<int>(at);
+  // an even share of the vocabulary, one after another; the places of a last,
+  // incomplete step repeat its last entry, which costs no memory traffic
+  const int64_t worker = static_cast<int64_t>(blockIdx.x) * WARPS + warp, workers = static_cast<int64_t>(gridDim.x) * WARPS;
+  const int v_end = static_cast<int>(a.V * (worker + 1) / workers);
+  for (int v0 = static_cast<int>(a.V * worker / workers); v0 < v_end; v0 += kEntries) {
     const E* rows[kEntries];
 #pragma unroll
     for (int e = 0; e < kEntries; ++e)
-      rows[e] = static_cast<const E*>(a.W) + static_cast<int64_t>(min(v0 + e, a.V - 1)) * a.ldw;
+      rows[e] = static_cast<const E*>(a.W) + static_cast<int64_t>(min(v0 + e, v_end - 1)) * a.ldw;
     float2 acc[VALUES];
 #pragma unroll
     for (int i = 0; i < VALUES; ++i) acc[i] = make_float2(0.0f, 0.0f);
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(kFewThreads) few_stats_kernel(const FewArgs a)
 #pragma unroll
     for (; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int v = v0 + r;
-    if (owner && v < a.V) {
+    if (owner && v < v_end) {
       join(m, s, sum * a.k2, 1.0f);
       zs += sum;
       while (next < v) {  // entries other warps and lanes take
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kFewThreads) few_stats_kernel(const FewArgs a)
     m = s_part[0][0][q];
     s = s_part[1][0][q];
     dot = s_part[2][0][q];
-    for (int w = 1; w < kFewWarps; ++w) {
+    for (int w = 1; w < WARPS; ++w) {
       join(m, s, s_part[0][w][q], s_part[1][w][q]);
       dot += s_part[2][w][q];
     }
@@ -235,7 +241,7 @@ cudaError_t launch_few(const FewArgs& a, int blocks, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, 1, 1);
-  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.blockDim = dim3(few_threads(TN), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -271,14 +277,15 @@ bool few_rows(int64_t T, int64_t D) {
   return T <= kFewRows && rows * ((D + 7) / 8 * 8) * 4 <= kFewSmem;
 }
 
-int few_blocks(int64_t V) {
-  // two blocks of 16 warps per SM, each warp with at least one step of entries
-  const int64_t most = (V + kFewWarps * kEntries - 1) / (kFewWarps * kEntries);
-  return static_cast<int>(most < kFewBlocks ? most : kFewBlocks);
+int few_blocks(int64_t T, int64_t V) {
+  // the blocks that fit the SMs at once, each warp with at least one entry
+  const int tn = T <= 2 ? 1 : static_cast<int>(T <= 4 ? 4 : 8);
+  const int64_t most = (V + few_threads(tn) / 32 - 1) / (few_threads(tn) / 32);
+  return static_cast<int>(std::min<int64_t>(most, kFewSms * few_per_sm(tn)));
 }
 
 cudaError_t launch_few_stats(const FewArgs& a, int type, int granule, cudaStream_t stream) {
-  const int blocks = few_blocks(a.V);
+  const int blocks = few_blocks(a.T, a.V);
   if (type == 0) return launch_type<__nv_bfloat16>(a, granule, blocks, stream);
   if (type == 1) return launch_type<__half>(a, granule, blocks, stream);
   return launch_type<float>(a, granule, blocks, stream);

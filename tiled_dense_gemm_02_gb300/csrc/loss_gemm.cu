@@ -25,9 +25,9 @@
 //   warp 0      bulk-tensor producer of this CTA's 128 rows of A and 128
 //               columns of B; completion on the leader CTA's full barrier
 //   warp 1      tensor-memory allocation; MMA issue by one thread of the leader
-//   warps 2..   epilogue of this CTA's 128 rows, one row per thread: four warps
-//               for STATS; eight for the gradients, half of the columns each,
-//               since their stores can outlast a short k axis
+//   warps 2..   epilogue of this CTA's 128 rows, one row per thread: eight warps
+//               with half of the columns each; four for STATS with a long k
+//               axis, which hides them and wants the space for a seventh stage
 //
 // The number of gathered rows is known on the device only (rows that do not
 // count are not gathered), so every role derives the tile list from it.  Every
@@ -43,15 +43,14 @@ namespace {
 
 constexpr int kSub = kTileM * kTileK * 2;        // 16 KB: one CTA's share of A or B in one stage
 constexpr int kStage = 2 * kSub;
-// Warps per quarter of the rows in the epilogue, each with 4 KB to stage stores.
-constexpr int head_halves(int mode) { return mode == HEAD_STATS ? 1 : 2; }
-constexpr int head_threads(int mode) { return 32 * (2 + 4 * head_halves(mode)); }
-constexpr int head_epi_bytes(int mode) { return mode == HEAD_STATS ? 0 : 4 * head_halves(mode) * 4096; }
-constexpr int head_stages(int mode) {
-  return (kSmemLimit - 1024 - head_epi_bytes(mode) - kBarrierBytes) / kStage;
+// PARTS: epilogue warps per quarter of the rows; each of the gradients' has 4 KB to stage stores.
+constexpr int head_threads(int parts) { return 32 * (2 + 4 * parts); }
+constexpr int head_epi_bytes(int mode, int parts) { return mode == HEAD_STATS ? 0 : 4 * parts * 4096; }
+constexpr int head_stages(int mode, int parts) {
+  return (kSmemLimit - 1024 - head_epi_bytes(mode, parts) - kBarrierBytes) / kStage;
 }
-constexpr int head_smem(int mode) {
-  return 1024 + head_stages(mode) * kStage + head_epi_bytes(mode) + kBarrierBytes;
+constexpr int head_smem(int mode, int parts) {
+  return 1024 + head_stages(mode, parts) * kStage + head_epi_bytes(mode, parts) + kBarrierBytes;
 }
 constexpr bool a_m_major(int mode) { return mode == HEAD_DW; }
 constexpr bool b_n_major(int mode) { return mode == HEAD_DH || mode == HEAD_DW; }
@@ -76,9 +75,12 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, int32_
                : "memory");
 }
 
+constexpr int kGroupM = 8;  // block-rows walked together; a power of two, so that a full group's quotient is a shift
+
 // The tile list of a launch, derived from the gathered row count.
 struct Tiles {
   int m, n, units, k_blocks;
+  float per_inv, group_inv;  // 1 / (m n), 1 / (kGroupM n)
 };
 
 template <int MODE>
@@ -88,28 +90,55 @@ __device__ __forceinline__ Tiles head_tiles(const HeadArgs& a, int rows) {
   t.n = ((MODE == HEAD_DH || MODE == HEAD_DW ? a.D : a.cols) + kHeadTile - 1) / kHeadTile;
   t.k_blocks = MODE == HEAD_DW ? (rows + kTileK - 1) / kTileK : a.k_blocks;
   t.units = t.m * t.n * (MODE == HEAD_DH ? a.splits : 1);
+  t.per_inv = 1.0f / static_cast<float>(t.m * t.n);
+  t.group_inv = 1.0f / static_cast<float>(kGroupM * t.n);
   return t;
+}
+
+// i / d and i % d with a given reciprocal of d.  The product in fp32 is off by
+// less than one quotient while i stays below 2^23; beyond (T V of 2^39), the
+// plain division.  The division of every tile by every role was a third of a
+// short tile's time.
+__device__ __forceinline__ void divide(int i, int d, float inv, int& q, int& r) {
+  if (i < (1 << 23)) {
+    q = __float2int_rz(__int2float_rn(i) * inv);
+    r = i - q * d;
+    if (r < 0) {
+      --q;
+      r += d;
+    } else if (r >= d) {
+      ++q;
+      r -= d;
+    }
+  } else {
+    q = i / d;
+    r = i - q * d;
+  }
 }
 
 struct HeadUnit {
   int mb, nb, split, lo, hi;
 };
 
-// Unit -> tile and k-stage range: groups of group_m block-rows are walked
+// Unit -> tile and k-stage range: groups of kGroupM block-rows are walked
 // column by column (as the plain product does), split after split.
 template <int MODE>
 __device__ __forceinline__ HeadUnit head_unit(const HeadArgs& a, const Tiles& t, int u) {
   HeadUnit w;
-  const int per = t.m * t.n;
-  w.split = MODE == HEAD_DH ? u / per : 0;
-  const int i = MODE == HEAD_DH ? u - w.split * per : u;
-  const int per_group = a.group_m * t.n;
-  const int g = i / per_group;
-  const int first = g * a.group_m;
-  const int gsz = min(t.m - first, a.group_m);
-  const int r = i - g * per_group;
-  w.mb = first + r % gsz;
-  w.nb = r / gsz;
+  int i = u;
+  w.split = 0;
+  if (MODE == HEAD_DH) divide(u, t.m * t.n, t.per_inv, w.split, i);
+  int g, r;
+  divide(i, kGroupM * t.n, t.group_inv, g, r);
+  const int first = g * kGroupM;
+  const int gsz = t.m - first;
+  if (gsz >= kGroupM) {
+    w.mb = first + (r & (kGroupM - 1));
+    w.nb = r / kGroupM;
+  } else {
+    w.nb = r / gsz;
+    w.mb = first + r - w.nb * gsz;
+  }
   w.lo = MODE == HEAD_DH ? min(w.split * a.k_per_split, t.k_blocks) : 0;
   w.hi = MODE == HEAD_DH ? min(w.lo + a.k_per_split, t.k_blocks) : t.k_blocks;
   return w;
@@ -121,19 +150,19 @@ struct Walk {
   const float* q;
   int pos, K, next;
   float one;  // mass of a single target (K = 0)
-  __device__ __forceinline__ void start(const HeadArgs& a, int row, int n, int first) {
+  // `y`: the row's target (cross entropy), loaded ahead
+  __device__ __forceinline__ void start(const HeadArgs& a, int row, int n, int first, int64_t y) {
     K = pos = 0;
     next = INT_MAX;
     ids = nullptr;
     q = nullptr;
     one = a.mass;
     if (row >= n) return;
-    const int t = a.source ? a.source[row] : row;
-    if (a.targets) {
-      const int64_t y = a.targets[t];
+    if (a.target) {
       if (y >= first && y < a.V) next = static_cast<int>(y);
       return;
     }
+    const int t = a.source ? a.source[row] : row;
     K = a.K;
     ids = a.ids + static_cast<int64_t>(t) * K;
     q = a.q + static_cast<int64_t>(t) * K;
@@ -156,20 +185,13 @@ struct Walk {
   }
 };
 
-// Statistics of this thread's row over the tile's columns.
-__device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, int nb, const HeadArgs& a) {
-  const int first = a.col0 + nb * kHeadTile;  // vocabulary entry of the tile's first column
-  const int width = a.cols - nb * kHeadTile;
-  Walk walk;
-  walk.start(a, row, n, first);
+// Running statistics of a row: maximum of the logits so far, sum of 2^(k2 (z -
+// maximum)), sum q z, and sum z (where eps needs it).
+struct RowStats {
   float m = -INFINITY, s = 0.0f, dot = 0.0f, zs = 0.0f;
-#pragma unroll 1
-  for (int c = 0; c < kHeadTile / 32; ++c) {
-    const int limit = width - c * 32;
-    if (limit <= 0) break;
-    uint32_t raw[32];
-    ptx::tmem_ld_32x32b_x32(tbase + c * 32, raw);
-    ptx::tmem_wait_ld();
+
+  // 32 more columns from entry `base` on, `limit` of them inside the piece
+  __device__ __forceinline__ void add(const uint32_t (&raw)[32], int base, int limit, Walk& walk, const HeadArgs& a) {
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
@@ -177,22 +199,25 @@ __device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, i
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = i < limit ? v[i] : -INFINITY;
     }
-    float top = v[0];
+    float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-    const float m_new = fmaxf(m, top);
+    for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+    const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
     const float ref = m_new == -INFINITY ? 0.0f : m_new;  // nothing but -inf so far: every term is 0
-    const float off = -ref * a.k2;
-    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float2 k2 = make_float2(a.k2, a.k2), off = make_float2(-ref * a.k2, -ref * a.k2);
+    float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) part[i & 3] += exp2_fast(fmaf(v[i], a.k2, off));
-    s = fmaf(s, exp2_fast((m - ref) * a.k2), (part[0] + part[1]) + (part[2] + part[3]));
+    for (int i = 0; i < 16; ++i) {
+      const float2 x = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), k2, off);
+      part[i & 1] = __fadd2_rn(part[i & 1], make_float2(exp2_fast(x.x), exp2_fast(x.y)));
+    }
+    const float2 both = __fadd2_rn(part[0], part[1]);
+    s = fmaf(s, exp2_fast((m - ref) * a.k2), both.x + both.y);
     m = m_new;
     if (a.flat != 0.0f) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) zs += i < limit ? v[i] : 0.0f;
     }
-    const int base = first + c * 32;
     while (__any_sync(0xffffffffu, walk.next < base + 32)) {
       if (walk.next < base + 32) {
         const int t = walk.next - base;
@@ -204,10 +229,28 @@ __device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, i
       }
     }
   }
+};
+
+// Statistics of this thread's row over its part of the tile's columns.
+template <int PARTS>
+__device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, int nb, int part, Walk& walk,
+                                               const HeadArgs& a) {
+  constexpr int CHUNKS = kHeadTile / 32 / PARTS;
+  const int first = a.col0 + nb * kHeadTile;  // vocabulary entry of the tile's first column
+  const int width = a.cols - nb * kHeadTile;
+  RowStats st;
+#pragma unroll 1
+  for (int c = part * CHUNKS; c < (part + 1) * CHUNKS; ++c) {
+    if (c * 32 >= width) break;
+    uint32_t raw[32];
+    ptx::tmem_ld_32x32b_x32(tbase + c * 32, raw);
+    ptx::tmem_wait_ld();
+    st.add(raw, first + c * 32, width - c * 32, walk, a);
+  }
   if (row < n) {
-    const int64_t at = static_cast<int64_t>(a.tile0 + nb) * a.T + row;
-    a.ms[at] = make_float2(m * a.k2, s);
-    a.dot[at] = fmaf(a.flat, zs, dot);
+    const int64_t at = (static_cast<int64_t>(a.tile0 + nb) * PARTS + part) * a.T + row;
+    a.ms[at] = make_float2(st.m * a.k2, st.s);
+    a.dot[at] = fmaf(a.flat, st.zs, st.dot);
   }
 }
 
@@ -215,10 +258,14 @@ __device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, i
 __device__ __forceinline__ void gradient_chunk(uint32_t (&raw)[32], int base, int limit, const float4& k,
                                                const HeadArgs& a, Walk& walk) {
   const float flat = k.y * a.flat;
+  const float2 k2 = make_float2(a.k2, a.k2), off = make_float2(-k.z, -k.z);
+  const float2 cp = make_float2(k.x, k.x), cf = make_float2(-flat, -flat);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float p = exp2_fast(fmaf(__uint_as_float(raw[i]), a.k2, -k.z));
-    raw[i] = __float_as_uint(fmaf(k.x, p, -flat));
+  for (int i = 0; i < 16; ++i) {
+    const float2 x = __ffma2_rn(make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1])), k2, off);
+    const float2 d = __ffma2_rn(cp, make_float2(exp2_fast(x.x), exp2_fast(x.y)), cf);
+    raw[2 * i] = __float_as_uint(d.x);
+    raw[2 * i + 1] = __float_as_uint(d.y);
   }
   while (__any_sync(0xffffffffu, walk.next < base + 32)) {
     if (walk.next < base + 32) {
@@ -264,49 +311,75 @@ __device__ __forceinline__ void store_words_plain(const uint32_t (&w)[32], uint1
                                                   int cols, int granule, uint8_t* buf, int lane) {
   stage_row(buf, lane, w);
   __syncwarp();
-#pragma unroll 4
-  for (int r = 0; r < 32; ++r) {
-    if (r >= rows) break;
-    uint16_t* row = dst + r * ld;
-    if (granule >= 4) {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(buf + sw128_offset(r, lane * 4));
-      if (2 * lane + 2 <= cols)
-        reinterpret_cast<uint32_t*>(row)[lane] = v;
-      else if (2 * lane < cols)
-        row[2 * lane] = static_cast<uint16_t>(v & 0xFFFFu);
-    } else {
+  if (granule >= 4) {
+    const bool whole = 2 * lane + 2 <= cols, single = !whole && 2 * lane < cols;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = lane + 32 * h;
-        if (c < cols) row[c] = *reinterpret_cast<const uint16_t*>(buf + sw128_offset(r, c * 2));
+    for (int r0 = 0; r0 < 32; r0 += 8) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint32_t*>(buf + sw128_offset(r0 + i, lane * 4));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint16_t* row = dst + (r0 + i) * ld;
+        if (r0 + i < rows && whole) reinterpret_cast<uint32_t*>(row)[lane] = v[i];
+        if (r0 + i < rows && single) row[2 * lane] = static_cast<uint16_t>(v[i] & 0xFFFFu);
       }
+    }
+  } else {
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 8) {
+      uint16_t v[8][2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[i][h] = *reinterpret_cast<const uint16_t*>(buf + sw128_offset(r0 + i, (lane + 32 * h) * 2));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (r0 + i < rows && lane + 32 * h < cols) dst[(r0 + i) * ld + lane + 32 * h] = v[i][h];
     }
   }
   __syncwarp();
 }
 
-template <int PLANES>
-__device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int nb, int half, const HeadArgs& a,
-                                            const CUtensorMap* mapC, uint8_t* buf, int lane) {
+template <int PLANES, int PARTS>
+__device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int nb, int part, const float4& k,
+                                            Walk& walk, const HeadArgs& a, const CUtensorMap* mapC, uint8_t* buf,
+                                            int lane) {
   if (row0 >= a.T) return;
-  const int c0 = half * (kHeadTile / 128), c1 = c0 + kHeadTile / 128;
+  const int c0 = part * (kHeadTile / 64 / PARTS), c1 = c0 + kHeadTile / 64 / PARTS;
   const int row = row0 + lane;
   const int first = a.col0 + nb * kHeadTile;
   const int width = a.cols - nb * kHeadTile;
-  Walk walk;
-  walk.start(a, row, n, first + c0 * 64);
-  const float4 k = row < n ? a.coef[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const int fmt = a.bf16 ? OUT_BF16 : OUT_F16;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
     if (c * 64 >= width) break;
-    uint32_t lo[32], hi[32], w[32];
+    uint32_t w[32];
+    if constexpr (PLANES == 1) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t d[32];
+        ptx::tmem_ld_32x32b_x32(tbase + c * 64 + h * 32, d);
+        ptx::tmem_wait_ld();
+        gradient_chunk(d, first + c * 64 + h * 32, width - c * 64 - h * 32, k, a, walk);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)  // rows past the count: zeros, which the products read
+          w[16 * h + i] = row < n ? pack_pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]), fmt) : 0u;
+      }
+      store_words(w, mapC, nb * kHeadTile + c * 64, row0, 0, buf, lane);
+      continue;
+    }
+    uint32_t lo[32], hi[32];
     ptx::tmem_ld_32x32b_x32(tbase + c * 64, lo);
-    ptx::tmem_ld_32x32b_x32(tbase + c * 64 + 32, hi);
     ptx::tmem_wait_ld();
+    ptx::tmem_ld_32x32b_x32(tbase + c * 64 + 32, hi);
     gradient_chunk(lo, first + c * 64, width - c * 64, k, a, walk);
+    ptx::tmem_wait_ld();
     gradient_chunk(hi, first + c * 64 + 32, width - c * 64 - 32, k, a, walk);
-    if (row >= n) {  // rows past the count: zeros, which the products read
+    if (row >= n) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) lo[i] = hi[i] = 0u;
     }
@@ -316,7 +389,7 @@ __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int
       for (int i = 0; i < 32; ++i) {
         uint32_t* v = i < 16 ? &lo[2 * i] : &hi[2 * i - 32];
         const float x = __uint_as_float(v[0]), y = __uint_as_float(v[1]);
-        w[i] = pack_pair(x, y, PLANES == 1 ? fmt : OUT_BF16);
+        w[i] = pack_pair(x, y, OUT_BF16);
         if (p + 1 < PLANES) {  // what the plane leaves (0 where it is not finite)
           const float px = __uint_as_float(w[i] << 16), py = __uint_as_float(w[i] & 0xFFFF0000u);
           v[0] = isfinite(px) ? __float_as_uint(x - px) : 0u;
@@ -347,9 +420,10 @@ __device__ __forceinline__ void store_row_f32(float* dst, const float (&v)[32], 
 }
 
 // fp32 DH and DW: one chunk's sums of this thread's row, times f.
-__device__ __forceinline__ void epilogue_f32(uint32_t tbase, float* row, bool valid_row, int nb, int half, int cols,
+template <int PARTS>
+__device__ __forceinline__ void epilogue_f32(uint32_t tbase, float* row, bool valid_row, int nb, int part, int cols,
                                              float f, bool vec, bool add) {
-  const int c0 = half * (kHeadTile / 64), c1 = c0 + kHeadTile / 64;
+  const int c0 = part * (kHeadTile / 32 / PARTS), c1 = c0 + kHeadTile / 32 / PARTS;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
     const int col = nb * kHeadTile + c * 32;
@@ -364,36 +438,39 @@ __device__ __forceinline__ void epilogue_f32(uint32_t tbase, float* row, bool va
   }
 }
 
-__device__ __forceinline__ void epilogue_dh(uint32_t tbase, int row0, const HeadUnit& u, int half, const HeadArgs& a,
-                                            const CUtensorMap* mapC, uint8_t* buf, int lane) {
-  if (row0 >= a.T) return;
-  const int c0 = half * (kHeadTile / 64), c1 = c0 + kHeadTile / 64;
+// fp32 sums of 32 rows, times f, to the tensor at (column, row0, z) by bulk
+// copies: stored, or added.
+template <int PARTS>
+__device__ __forceinline__ void epilogue_sums(uint32_t tbase, int row0, int nb, int z, int part, int cols, float f,
+                                              bool add, const CUtensorMap* mapC, uint8_t* buf, int lane) {
+  const int c0 = part * (kHeadTile / 32 / PARTS), c1 = c0 + kHeadTile / 32 / PARTS;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
-    const int col = u.nb * kHeadTile + c * 32;
-    if (col >= a.D) break;
+    const int col = nb * kHeadTile + c * 32;
+    if (col >= cols) break;
     uint32_t w[32];
     ptx::tmem_ld_32x32b_x32(tbase + c * 32, w);
     ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(f * __uint_as_float(w[i]));
     stage_row(buf, lane, w);
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      if (a.reduce)
-        tma_reduce_add_3d(mapC, col, row0, u.split, ptx::smem_u32(buf));
+      if (add)
+        tma_reduce_add_3d(mapC, col, row0, z, ptx::smem_u32(buf));
       else
-        ptx::tma_store_3d(mapC, col, row0, u.split, ptx::smem_u32(buf));
+        ptx::tma_store_3d(mapC, col, row0, z, ptx::smem_u32(buf));
       ptx::bulk_commit_group();
     }
   }
 }
 
-__device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, int half, const HeadArgs& a,
+template <int PARTS>
+__device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, int part, float f, const HeadArgs& a,
                                             const CUtensorMap* mapC, uint8_t* buf, int lane) {
-  if (row0 >= a.cols) return;
-  const float f = *a.factor;
   const int fmt = a.bf16 ? OUT_BF16 : OUT_F16;
-  const int c0 = half * (kHeadTile / 128), c1 = c0 + kHeadTile / 128;
+  const int c0 = part * (kHeadTile / 64 / PARTS), c1 = c0 + kHeadTile / 64 / PARTS;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
     const int col = nb * kHeadTile + c * 64;
@@ -415,20 +492,20 @@ __device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, in
   }
 }
 
-template <int MODE, int PLANES>
-__global__ void __launch_bounds__(head_threads(MODE), 1)
+template <int MODE, int PLANES, int PARTS>
+__global__ void __launch_bounds__(head_threads(PARTS), 1)
     head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ CUtensorMap mapC, const HeadArgs args) {
-  constexpr int STAGES = head_stages(MODE);
+  constexpr int STAGES = head_stages(MODE, PARTS);
   constexpr int TERMS = plane_terms(PLANES);
   constexpr int ACC = 256;
   constexpr uint32_t TMEM_COLS = 512;
-  static_assert(head_smem(MODE) <= kSmemLimit, "shared memory per CTA");
+  static_assert(head_smem(MODE, PARTS) <= kSmemLimit, "shared memory per CTA");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sC = smem + STAGES * kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sC + head_epi_bytes(MODE));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sC + head_epi_bytes(MODE, PARTS));
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint64_t* acc_empty = acc_full + 2;
@@ -451,7 +528,7 @@ __global__ void __launch_bounds__(head_threads(MODE), 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&acc_full[b]), 1);
-      ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * 4 * head_halves(MODE));
+      ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * 4 * PARTS);
     }
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0u;
@@ -589,14 +666,36 @@ __global__ void __launch_bounds__(head_threads(MODE), 1)
   } else {
     // --------------------------------------------------------- epilogue
     const int quarter = warp & 3;              // tensor-memory lanes of this warp
-    const int half = (warp - 2) / 4;           // its half of the tile's columns
+    const int part = (warp - 2) / 4;           // its part of the tile's columns
     uint8_t* buf = sC + (warp - 2) * 4096;
+    const float factor = MODE == HEAD_DW ? __ldcg(args.factor) : 1.0f;
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
+    // the next tile is found, and its rows' targets and coefficients loaded,
+    // while this one's products run: a short k axis would not hide it
+    HeadUnit u, next;
+    int64_t target = -1;
+    float4 coef = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const auto look_ahead = [&](int i) {
+      if (i >= tiles.units) return;
+      next = head_unit<MODE>(args, tiles, i);
+      if constexpr (MODE == HEAD_STATS || MODE == HEAD_DZ) {
+        const int row = next.mb * kHeadTile + cta * kTileM + quarter * 32 + lane;
+        if (args.target) target = row < n ? __ldcg(args.target + row) : -1;
+        if (MODE == HEAD_DZ) coef = row < n ? __ldcg(args.coef + row) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+    };
+    look_ahead(worker);
     for (int i = worker; ok && i < tiles.units; i += workers) {
-      const HeadUnit u = head_unit<MODE>(args, tiles, i);
+      u = next;
       const int row0 = u.mb * kHeadTile + cta * kTileM + quarter * 32;
+      const int rows_end = MODE == HEAD_DW ? args.cols : MODE == HEAD_DZ ? args.T : n;
+      const float4 k = coef;
+      Walk walk;
+      if constexpr (MODE == HEAD_STATS || MODE == HEAD_DZ)
+        walk.start(args, row0 + lane, n, args.col0 + u.nb * kHeadTile + part * (kHeadTile / PARTS), target);
+      look_ahead(i + workers);
       for (int lo = u.lo; lo < u.hi; lo += chunk) {
         if (!warp_wait(ptx::smem_u32(&acc_full[acc]), acc_phase, ctl, SITE_EPI_ACC_FULL)) {
           ok = false;
@@ -605,31 +704,36 @@ __global__ void __launch_bounds__(head_threads(MODE), 1)
         ptx::tc_fence_after_sync();
         const uint32_t tbase =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * ACC);
-        if constexpr (MODE == HEAD_STATS) {
-          if (row0 < n) epilogue_stats(tbase, row0 + lane, n, u.nb, args);
-        } else if constexpr (MODE == HEAD_DZ) {
-          epilogue_dz<PLANES>(tbase, row0, n, u.nb, half, args, &mapC, buf, lane);
-        } else if constexpr (PLANES > 1) {
-          // a chunk's sum of the full-size terms took 4 steps a stage
-          const float put_back = 1.0f + kStepLoss * static_cast<float>(4 * min(chunk, u.hi - lo));
-          const int row = row0 + lane;
-          float* out = static_cast<float*>(args.out);
-          if constexpr (MODE == HEAD_DH) {
-            if (row0 < n)
-              epilogue_f32(tbase, out + u.split * args.split_stride + static_cast<int64_t>(row) * args.ld_out, row < n,
-                           u.nb, half, args.D, put_back, true, args.reduce || lo > u.lo);
-          } else if (row0 < args.cols) {
-            epilogue_f32(tbase, out + static_cast<int64_t>(args.out_row0 + row) * args.ld_out, row < args.cols, u.nb,
-                         half, args.D, put_back * *args.factor, args.store_granule == 16, lo > u.lo);
+        if (row0 < rows_end) {
+          if constexpr (MODE == HEAD_STATS) {
+            epilogue_stats<PARTS>(tbase, row0 + lane, n, u.nb, part, walk, args);
+          } else if constexpr (MODE == HEAD_DZ) {
+            epilogue_dz<PLANES, PARTS>(tbase, row0, n, u.nb, part, k, walk, args, &mapC, buf, lane);
+          } else if constexpr (PLANES == 1 && MODE == HEAD_DW) {
+            epilogue_dw<PARTS>(tbase, row0, u.nb, part, factor, args, &mapC, buf, lane);
+          } else {
+            // fp32: a chunk's sum of the full-size terms took 4 steps a stage
+            const float f =
+                PLANES == 1 ? 1.0f : factor * (1.0f + kStepLoss * static_cast<float>(4 * min(chunk, u.hi - lo)));
+            // in bulk where a sum is moved once a launch, else by the thread that owns it
+            if (args.store_granule == 0) {
+              epilogue_sums<PARTS>(tbase, MODE == HEAD_DW ? args.out_row0 + row0 : row0, u.nb, u.split, part, args.D, f,
+                                   args.reduce, &mapC, buf, lane);
+            } else {
+              const int row = row0 + lane;
+              float* out = static_cast<float*>(args.out) + u.split * args.split_stride +
+                           static_cast<int64_t>(args.out_row0 + row) * args.ld_out;
+              epilogue_f32<PARTS>(tbase, out, row < rows_end, u.nb, part, args.D, f, args.store_granule == 16,
+                                  args.reduce || lo > u.lo);
+            }
           }
-        } else if constexpr (MODE == HEAD_DH) {
-          epilogue_dh(tbase, row0, u, half, args, &mapC, buf, lane);
-        } else {
-          epilogue_dw(tbase, row0, u.nb, half, args, &mapC, buf, lane);
         }
+        // The accumulator's reads are complete (tcgen05.wait::ld).  The arrival
+        // orders nothing else: a releasing one would wait for this tile's
+        // global stores, 1500 cycles a tile.
         ptx::tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
@@ -647,11 +751,11 @@ __global__ void __launch_bounds__(head_threads(MODE), 1)
   }
 }
 
-template <int MODE, int PLANES>
+template <int MODE, int PLANES, int PARTS>
 cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC, const HeadArgs& args,
                    int pairs, cudaStream_t stream) {
-  constexpr int smem = head_smem(MODE);
-  auto kernel = head_kernel<MODE, PLANES>;
+  constexpr int smem = head_smem(MODE, PARTS);
+  auto kernel = head_kernel<MODE, PLANES, PARTS>;
   static std::atomic<uint64_t> done_mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -664,7 +768,7 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.blockDim = dim3(head_threads(MODE), 1, 1);
+  cfg.blockDim = dim3(head_threads(PARTS), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -683,15 +787,14 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
 
 cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUtensorMap& mapB,
                         const CUtensorMap& mapC, const HeadArgs& args, int pairs, cudaStream_t stream) {
-#define TGEMM_HEAD(MODE)                                                                  \
-  case MODE:                                                                              \
-    return planes == 1 ? launch<MODE, 1>(mapA, mapB, mapC, args, pairs, stream)           \
-                       : launch<MODE, kPlanes>(mapA, mapB, mapC, args, pairs, stream)
+#define TGEMM_HEAD(MODE, PARTS)                                                                 \
+  (planes == 1 ? launch<MODE, 1, PARTS>(mapA, mapB, mapC, args, pairs, stream)                  \
+               : launch<MODE, kPlanes, PARTS>(mapA, mapB, mapC, args, pairs, stream))
   switch (mode) {
-    TGEMM_HEAD(HEAD_STATS);
-    TGEMM_HEAD(HEAD_DZ);
-    TGEMM_HEAD(HEAD_DH);
-    TGEMM_HEAD(HEAD_DW);
+    case HEAD_STATS: return args.parts == 2 ? TGEMM_HEAD(HEAD_STATS, 2) : TGEMM_HEAD(HEAD_STATS, 1);
+    case HEAD_DZ: return TGEMM_HEAD(HEAD_DZ, 2);
+    case HEAD_DH: return TGEMM_HEAD(HEAD_DH, 2);
+    case HEAD_DW: return TGEMM_HEAD(HEAD_DW, 2);
     default: return cudaErrorInvalidValue;
   }
 #undef TGEMM_HEAD

@@ -36,6 +36,7 @@ struct HeadRows {
   float* factor;      // what the gradient products' sums are multiplied with
   int* source;        // T
   int* place;         // T
+  int64_t* target;    // T (cross entropy): the gathered rows' targets
   int* ids;           // T x K (distillation)
   float* q;           // T x K
   float* own;         // T: sum q log q (distillation), else null
@@ -113,11 +114,10 @@ struct HeadArgs {
   int splits, k_per_split;  // DH: ranges of the k axis summed apart
   int chunk;      // fp32, DH and DW: stages summed in tensor memory before they are added to the result
   int reduce;     // DH: add to the sums instead of storing them
-  int group_m;
   int bf16;
   float k2;       // scale * log2(e)
   float flat;     // eps / V (cross entropy), else 0
-  const int64_t* targets;   // cross entropy: one target per row of H, with mass `mass`
+  const int64_t* target;    // cross entropy: the target of row r, with mass `mass`
   float mass;
   const int* source;        // null: row r is row r of H, and count is null
   const int* ids;           // distillation
@@ -125,12 +125,13 @@ struct HeadArgs {
   float2* ms;     // STATS
   float* dot;
   int tile0;      // STATS: index of the piece's first column tile
+  int parts;      // STATS: parts of a tile's columns with statistics of their own, 1 or 2
   const float4* coef;     // DZ
   const float* factor;    // DW
   void* out;              // DW; fp32 DH
   int64_t ld_out;
   int64_t split_stride;   // fp32 DH: elements between the splits' sums
-  int store_granule;      // DW: 0 bulk-tensor stores, else the granule of per-thread stores
+  int store_granule;      // DH, DW: 0 bulk-tensor stores, else the granule of per-thread stores
   int out_row0;           // DW: row of dW for the piece's column 0
   unsigned long long timeout_ns;
   unsigned int* status;
@@ -153,7 +154,7 @@ cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUt
 
 // ------------------------------------------------------------- few rows
 // Statistics of T <= kFewRows rows of H, read in place, in one pass over W on
-// the CUDA cores; few_blocks(V) parts.
+// the CUDA cores; few_blocks(T, V) parts.
 struct FewArgs {
   int T, V, D, K;
   const void* H;
@@ -170,9 +171,9 @@ struct FewArgs {
 };
 constexpr int kFewRows = 8;
 constexpr int kFewSmem = 160 * 1024;
-constexpr int kFewBlocks = 304;
+constexpr int kFewSms = 152;
 bool few_rows(int64_t T, int64_t D);
-int few_blocks(int64_t V);
+int few_blocks(int64_t T, int64_t V);
 // type: 0 bf16, 1 f16, 2 f32; granule: alignment of W's rows
 cudaError_t launch_few_stats(const FewArgs& a, int type, int granule, cudaStream_t stream);
 

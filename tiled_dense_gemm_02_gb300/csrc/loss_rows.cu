@@ -214,14 +214,16 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
   const int t0 = blockIdx.x * rows_per, t1 = min(a.T, t0 + rows_per);
   int before = 0, total = 0;
   float gmax = 0.0f, cmax = 0.0f;
+  // nothing in the loop waits for a row's flag, so the loads of several rows overlap
+#pragma unroll 8
   for (int t = tid; t < a.T; t += kGatherThreads) {
-    if (row_flag(a.rule, t) != kRowCounts) continue;
-    ++total;
-    before += t < t0 ? 1 : 0;
+    const bool counts = row_flag(a.rule, t) == kRowCounts;
+    total += counts ? 1 : 0;
+    before += counts && t < t0 ? 1 : 0;
     if (a.grad) {
-      const float g = fabsf(a.grad[t]), c = fabsf(grad_p(a, t));
-      if (isfinite(g)) gmax = fmaxf(gmax, g);
-      if (isfinite(c)) cmax = fmaxf(cmax, c);
+      const float g = fabsf(a.grad[t]), c = a.z_loss == 0.0f ? g : fabsf(grad_p(a, t));
+      gmax = counts && isfinite(g) ? fmaxf(gmax, g) : gmax;
+      cmax = counts && isfinite(c) ? fmaxf(cmax, c) : cmax;
     }
   }
   before = __reduce_add_sync(0xffffffffu, before);
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     a.rows.place[t] = counts ? place : -1;
     if (counts) {
       a.rows.source[place] = t;
+      if (a.rule.targets) a.rows.target[place] = a.rule.targets[t];
       s_src[place - before] = t;
       if (a.grad) {
         const float up = a.range / pow2;
@@ -315,9 +318,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
 }
 
 // --------------------------------------------------- joining tile statistics
-// A block joins the tiles of 8 rows with 32 threads a row: 64 contiguous bytes
-// per tile are read, and T / 8 blocks suffice even for one long list of tiles.
-constexpr int kCombineRows = 8, kCombineSlots = 32;
+// A block of 256 threads joins the parts of ROWS rows: 8 (64 contiguous bytes
+// of a part are read at a time), or 1 where there are too few rows to fill the
+// SMs and a row's parts are spread over the whole block.
+constexpr int kCombineThreads = 256;
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
   const float ref = top == -INFINITY ? 0.0f : top;
@@ -325,22 +329,24 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   m = top;
 }
 
-__global__ void __launch_bounds__(kCombineRows * kCombineSlots)
-    combine_kernel(const float2* __restrict__ ms, const float* __restrict__ dot, int tiles, int T, float scale,
+template <int ROWS>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_kernel(const float2* ms, const float* dot, int tiles, int T, float scale,
                    float z_loss, HeadRows rows, RowRule rule, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float s_m[kCombineSlots][kCombineRows], s_s[kCombineSlots][kCombineRows], s_d[kCombineSlots][kCombineRows];
+  constexpr int SLOTS = kCombineThreads / ROWS;
+  __shared__ float s_m[SLOTS][ROWS], s_s[SLOTS][ROWS], s_d[SLOTS][ROWS];
   chain();
   const int n = rows.count ? min(*rows.count, T) : T;
-  const int r0 = blockIdx.x * kCombineRows;
+  const int r0 = blockIdx.x * ROWS;
   if (r0 >= n) return;
-  const int lr = threadIdx.x % kCombineRows, slot = threadIdx.x / kCombineRows;
+  const int lr = threadIdx.x % ROWS, slot = threadIdx.x / ROWS;
   const int r = r0 + lr;
   float m = -INFINITY, s = 0.0f, d = 0.0f;
   if (r < n) {
 #pragma unroll 4
-    for (int i = slot; i < tiles; i += kCombineSlots) {
-      const float2 p = ms[static_cast<int64_t>(i) * T + r];
-      d += dot[static_cast<int64_t>(i) * T + r];
+    for (int i = slot; i < tiles; i += SLOTS) {
+      const float2 p = __ldcg(ms + static_cast<int64_t>(i) * T + r);
+      d += __ldcg(dot + static_cast<int64_t>(i) * T + r);
       join(m, s, p.x, p.y);
     }
   }
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kCombineRows * kCombineSlots)
   s_s[slot][lr] = s;
   s_d[slot][lr] = d;
   __syncthreads();
-  for (int w = kCombineSlots / 2; w > 0; w >>= 1) {
+  for (int w = SLOTS / 2; w > 0; w >>= 1) {
     if (slot < w) {
       float m1 = s_m[slot][lr], s1 = s_s[slot][lr];
       join(m1, s1, s_m[slot + w][lr], s_s[slot + w][lr]);
@@ -380,31 +386,47 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 // Four columns of one row per thread; the sums' pitch is a multiple of four.
+// LANES threads share the splits of the same columns (8 for many splits, which
+// one thread would read one after another); their sums join in a fixed order.
 constexpr int kFinishThreads = 128;
-template <typename Out>
-__global__ void __launch_bounds__(kFinishThreads) finish_dh_kernel(const float* __restrict__ acc, int64_t ld_acc,
+template <typename Out, int LANES>
+__global__ void __launch_bounds__(kFinishThreads) finish_dh_kernel(const float* acc, int64_t ld_acc,
                                                                    int64_t split_stride, int splits, int T, int D,
                                                                    HeadRows rows, Out* __restrict__ dH, int64_t lddh,
                                                                    int wide) {
   chain();
   const int groups = (D + 3) / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kFinishThreads + threadIdx.x;
-  const int t = static_cast<int>(i / groups), c = static_cast<int>(i - static_cast<int64_t>(t) * groups) * 4;
-  if (t >= T) return;
-  const int place = rows.place[t];
+  const int lane = threadIdx.x % LANES;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (kFinishThreads / LANES) + threadIdx.x / LANES;
+  const int64_t row = i / groups;
+  const int c = static_cast<int>(i - row * groups) * 4;
+  const bool inside = row < T;
+  const int t = inside ? static_cast<int>(row) : 0;
+  const int place = inside ? rows.place[t] : -1;
   const float f = *rows.factor;
   Out* out = dH + static_cast<int64_t>(t) * lddh + c;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (place >= 0) {
     const float* src = acc + static_cast<int64_t>(place) * ld_acc + c;
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
+    for (int s = lane; s < splits; s += LANES) {
       const float4 p = __ldcg(reinterpret_cast<const float4*>(src + s * split_stride));
       v.x += p.x;
       v.y += p.y;
       v.z += p.z;
       v.w += p.w;
     }
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+  }
+  if (!inside || lane != 0) return;
+  // no sum of a row that does not count: its place holds zeros whatever f is
+  if (place >= 0) {
     v.x *= f;
     v.y *= f;
     v.z *= f;
@@ -450,23 +472,27 @@ cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
 
 cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T, float scale, float z_loss,
                            const HeadRows& rows, const RowRule& rule, float* loss, float* lse, cudaStream_t stream) {
-  return launch_chained(combine_kernel, (T + kCombineRows - 1) / kCombineRows, kCombineRows * kCombineSlots, stream, ms,
-                        dot, tiles, T, scale, z_loss, rows, rule, loss, lse);
+  if (T <= 1024)
+    return launch_chained(combine_kernel<1>, T, kCombineThreads, stream, ms, dot, tiles, T, scale, z_loss, rows, rule,
+                          loss, lse);
+  return launch_chained(combine_kernel<8>, (T + 7) / 8, kCombineThreads, stream, ms, dot, tiles, T, scale, z_loss, rows,
+                        rule, loss, lse);
 }
 
 cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
                              const HeadRows& rows, int type, void* dH, int64_t lddh, cudaStream_t stream) {
   const int es = type == 2 ? 4 : 2;
   const int wide = reinterpret_cast<uint64_t>(dH) % (4 * es) == 0 && lddh % 4 == 0 ? 1 : 0;
-  const int64_t blocks = (static_cast<int64_t>(T) * ((D + 3) / 4) + kFinishThreads - 1) / kFinishThreads;
-  if (type == 0)
-    return launch_chained(finish_dh_kernel<__nv_bfloat16>, blocks, kFinishThreads, stream, acc, ld_acc, split_stride,
-                          splits, T, D, rows, static_cast<__nv_bfloat16*>(dH), lddh, wide);
-  if (type == 1)
-    return launch_chained(finish_dh_kernel<__half>, blocks, kFinishThreads, stream, acc, ld_acc, split_stride, splits, T,
-                          D, rows, static_cast<__half*>(dH), lddh, wide);
-  return launch_chained(finish_dh_kernel<float>, blocks, kFinishThreads, stream, acc, ld_acc, split_stride, splits, T, D,
-                        rows, static_cast<float*>(dH), lddh, wide);
+  const int lanes = splits >= 8 ? 8 : 1;
+  const int64_t per = kFinishThreads / lanes;
+  const int64_t blocks = (static_cast<int64_t>(T) * ((D + 3) / 4) + per - 1) / per;
+#define TGEMM_FINISH(OUT)                                                                                          \
+  launch_chained(lanes == 8 ? finish_dh_kernel<OUT, 8> : finish_dh_kernel<OUT, 1>, blocks, kFinishThreads, stream, \
+                 acc, ld_acc, split_stride, splits, T, D, rows, static_cast<OUT*>(dH), lddh, wide)
+  if (type == 0) return TGEMM_FINISH(__nv_bfloat16);
+  if (type == 1) return TGEMM_FINISH(__half);
+  return TGEMM_FINISH(float);
+#undef TGEMM_FINISH
 }
 
 cudaError_t launch_split(const float* W, int64_t ldw, void* out, int64_t ld_out, int64_t plane, int rows, int cols,
