@@ -3,7 +3,7 @@
 //
 // Forward:  [teacher lists]  gather  STATS (one launch over the vocabulary)  combine
 // Backward: [teacher lists]  gather  { DZ  DH  DW } per piece  last step of dH
-// (loss_rows.cu and loss_gemm.cu hold the kernels.)  A weight whose rows are
+// (loss_rows.cu and loss_gemm.cuh hold the kernels.)  A weight whose rows are
 // not 16-byte aligned is copied to an aligned pitch piece by piece, and an fp32
 // weight to its three bf16 planes.  Forward calls skip the gather where it
 // saves nothing: up to one tile of rows that can be read in place, and the few
@@ -44,6 +44,12 @@ constexpr int kChunkStages = 16;
 // own) beat four.  Measured at 4096 x 32768: D = 64 75 -> 66 us, 256 79 -> 70 us
 // with eight; 512 104 -> 97 us, 1024 177 -> 168 us with four.
 constexpr int64_t kShortStages = 6;
+// 16-bit backward calls: rows up to which dz is kept in two planes.  Few rows
+// leave the rounding of dz nothing to average over: with 2 rows dH was up to 1.6
+// times as far off as its own last rounding makes it, with many 1.2 to 1.4 times.
+// The second plane doubles the gradient products' stages: at 32768 x 2048, dH
+// 64 -> 84 us and 101 us with 16 and 256 rows.
+constexpr int64_t kTwoPlaneRows = 32;
 constexpr float kRangeF16 = 16384.0f;  // |dz| <= 2: fp16's largest value is 65504, its small normals reach 2^-14
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -77,7 +83,8 @@ struct Call {
 
 // Byte offsets into the workspace; every part starts on a 256-byte boundary.
 struct Layout {
-  int planes = 1;
+  int planes = 1;              // of H and W
+  int dz_planes = 1;
   bool few = false;            // forward of a few rows, on the CUDA cores
   bool direct = false;         // forward that reads H in place
   bool pack = false;           // W is copied to an aligned pitch or to planes, piece by piece
@@ -118,6 +125,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   Layout l;
   l.few = !backward && few_rows(T, D);
   l.planes = dtype == TGEMM_F32 ? kPlanes : 1;
+  l.dz_planes = l.planes > 1 ? l.planes : T <= kTwoPlaneRows ? 2 : 1;
   l.ldh = l.ldw_p = round_up(D, 8);
   l.pack = !l.few && (l.planes > 1 || host_granule(W, ldw, 2) < 16);
   l.ld_acc = round_up(D, 4);
@@ -127,7 +135,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   } else if (!backward && !l.pack) {
     l.piece = whole;
   } else {
-    const int64_t per = 2 * l.planes * std::max<int64_t>(backward ? T : 0, l.pack ? l.ldw_p : 0);  // bytes per entry
+    const int64_t per = 2 * std::max<int64_t>(backward ? l.dz_planes * T : 0, l.pack ? l.planes * l.ldw_p : 0);  // bytes per entry
     const int64_t fit = std::max<int64_t>(2048, kPieceBytes / per / kHeadTile * kHeadTile);
     l.piece = std::min(fit, whole);
     l.piece = round_up(ceil_div(V, ceil_div(V, l.piece)), kHeadTile);
@@ -152,8 +160,8 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   l.h = take(T * l.ldh * 2 * l.planes);
   if (l.pack) l.w = take(l.piece * l.ldw_p * 2 * l.planes);
   if (backward) {
-    l.z = take(T * l.ldz * 2 * l.planes);
-    plan_dh(T, D, ceil_div(std::min(l.piece, V), kTileK), l.planes == 1 ? 1 : 6, l);
+    l.z = take(T * l.ldz * 2 * l.dz_planes);
+    plan_dh(T, D, ceil_div(std::min(l.piece, V), kTileK), l.planes > 1 ? 6 : l.dz_planes, l);
     l.acc = take(l.splits * T * l.ld_acc * 4);
   } else {
     l.tile_parts = l.planes == 1 && ceil_div(D, kTileK) <= kShortStages ? 2 : 1;
@@ -329,14 +337,16 @@ class Products {
     return host_map_3d(m, type_, rows_.h, c_.D, c_.T, l_.planes, l_.ldh * 2, rows_.plane * 2, box_cols, box_rows);
   }
   int map_dz(CUtensorMap* m, uint32_t box_cols, uint32_t box_rows) {
-    return host_map_3d(m, type_, ws_ + l_.z, l_.ldz, c_.T, l_.planes, l_.ldz * 2, c_.T * l_.ldz * 2, box_cols, box_rows);
+    return host_map_3d(m, type_, ws_ + l_.z, l_.ldz, c_.T, l_.dz_planes, l_.ldz * 2, c_.T * l_.ldz * 2, box_cols,
+                       box_rows);
   }
 
   // `units`: tiles, were every row to count
-  int launch(int mode, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const HeadArgs& a,
-             int64_t units) {
+  template <typename Launch>
+  int launch(Launch function, int planes, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc,
+             const HeadArgs& a, int64_t units) {
     const int pairs = static_cast<int>(std::min<int64_t>(pairs_, units));
-    TGEMM_CUDA(launch_head(mode, l_.planes, ma, mb, mc, a, pairs, c_.stream), "head launch");
+    TGEMM_CUDA(function(planes, ma, mb, mc, a, pairs, c_.stream), "head launch");
     host_count_launches(1);
     return TGEMM_OK;
   }
@@ -347,8 +357,9 @@ class Products {
     TGEMM_TRY(map_weight(&mw, kTileK, kTileM));
     if (c_.backward) TGEMM_TRY(map_dz(&mz, 64, 32));
     a_.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
-    return launch(c_.backward ? HEAD_DZ : HEAD_STATS, mh, mw, c_.backward ? mz : mw, a_,
-                  ceil_div(c_.T, kHeadTile) * ceil_div(n_, kHeadTile));
+    const int64_t units = ceil_div(c_.T, kHeadTile) * ceil_div(n_, kHeadTile);
+    return c_.backward ? launch(launch_head_dz, l_.dz_planes, mh, mw, mz, a_, units)
+                       : launch(launch_head_stats, l_.planes, mh, mw, mw, a_, units);
   }
 
   int hidden_gradient() {
@@ -364,7 +375,7 @@ class Products {
     TGEMM_TRY(map_dz(&mz, kTileK, kTileM));
     TGEMM_TRY(map_weight(&mw, 64, kTileK));
     TGEMM_TRY(host_map_3d(&ma, 2, b.out, c_.D, c_.T, l_.splits, l_.ld_acc * 4, c_.T * l_.ld_acc * 4, 32, 32));
-    return launch(HEAD_DH, mz, mw, ma, b, ceil_div(c_.T, kHeadTile) * ceil_div(c_.D, kHeadTile) * l_.splits);
+    return launch(launch_head_dh, l_.dz_planes, mz, mw, ma, b, ceil_div(c_.T, kHeadTile) * ceil_div(c_.D, kHeadTile) * l_.splits);
   }
 
   int weight_gradient() {
@@ -385,7 +396,8 @@ class Products {
       b.store_granule = 0;
       TGEMM_TRY(host_map_3d(&mo, f32 ? 2 : type_, c_.dW, c_.D, c_.V, 1, c_.lddw * (f32 ? 4 : 2), 0, f32 ? 32 : 64, 32));
     }
-    return launch(HEAD_DW, mz, mh, bulk ? mo : mh, b, ceil_div(n_, kHeadTile) * ceil_div(c_.D, kHeadTile));
+    return launch(launch_head_dw, l_.dz_planes, mz, mh, bulk ? mo : mh, b,
+                  ceil_div(n_, kHeadTile) * ceil_div(c_.D, kHeadTile));
   }
 
   const Call& c_;

@@ -9,12 +9,15 @@
 //   DH     dz . W             fp32 sums, stored or added (bulk-tensor reduce)
 //   DW     dz^T . H           times a factor, rounded once, stored
 //
-// fp32 operands come as three bf16 planes (loss_rows.cu), and a stage of the k
-// axis is then six stages, one per pair of planes, the small terms first: the
-// last sixth alone adds to a sum of full size, so the adder's truncation is
-// that of a 16-bit product.  DH and DW, whose k axes are long, move their sums
-// out of tensor memory every `chunk` stages and add them in fp32 with rounding
-// to nearest, each element by the one thread that owns it.
+// PLANES = 3: fp32 operands come as three bf16 planes (loss_rows.cu), and a
+// stage of the k axis is then six stages, one per pair of planes, the small
+// terms first: the last sixth alone adds to a sum of full size, so the adder's
+// truncation is that of a 16-bit product.  DH and DW, whose k axes are long,
+// move their sums out of tensor memory every `chunk` stages and add them in
+// fp32 with rounding to nearest, each element by the one thread that owns it.
+// PLANES = 2: 16-bit operands, dz as two planes (its rounding and what that
+// leaves), so that few rows' gradients do not depend on how the one or two
+// entries that matter happen to round.
 //
 // with k2 = scale log2(e), so that one fused multiply-add and one 2^x serve
 // each logit.  H and W are read K-major (their rows are the k axis) by STATS
@@ -32,6 +35,8 @@
 // The number of gathered rows is known on the device only (rows that do not
 // count are not gathered), so every role derives the tile list from it.  Every
 // wait is bounded (tc_common.cuh).
+#pragma once
+
 #include <atomic>
 #include <climits>
 
@@ -55,10 +60,17 @@ constexpr int head_smem(int mode, int parts) {
 constexpr bool a_m_major(int mode) { return mode == HEAD_DW; }
 constexpr bool b_n_major(int mode) { return mode == HEAD_DH || mode == HEAD_DW; }
 
-// Pairs of planes in the order they are summed: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0).
-constexpr int plane_terms(int planes) { return planes == 1 ? 1 : 6; }
-__device__ __forceinline__ int plane_a(int term) { return (0x001102 >> (4 * term)) & 0xF; }
-__device__ __forceinline__ int plane_b(int term) { return (0x010120 >> (4 * term)) & 0xF; }
+// Pairs of planes in the order they are summed: fp32 (2,0) (0,2) (1,1) (1,0)
+// (0,1) (0,0); two planes of dz (1,0) (0,0).
+template <int MODE, int PLANES>
+struct Terms {
+  static constexpr bool logits = MODE == HEAD_STATS || MODE == HEAD_DZ;  // operands H and W
+  static constexpr int count = PLANES == 3 ? 6 : PLANES == 2 && !logits ? 2 : 1;
+  static __device__ __forceinline__ int a(int term) {
+    return count == 6 ? (0x001102 >> (4 * term)) & 0xF : count - 1 - term;
+  }
+  static __device__ __forceinline__ int b(int term) { return count == 6 ? (0x010120 >> (4 * term)) & 0xF : 0; }
+};
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -383,15 +395,20 @@ __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int
 #pragma unroll
       for (int i = 0; i < 32; ++i) lo[i] = hi[i] = 0u;
     }
+    const int plane_fmt = PLANES == 3 ? OUT_BF16 : fmt;
 #pragma unroll
     for (int p = 0; p < PLANES; ++p) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         uint32_t* v = i < 16 ? &lo[2 * i] : &hi[2 * i - 32];
         const float x = __uint_as_float(v[0]), y = __uint_as_float(v[1]);
-        w[i] = pack_pair(x, y, OUT_BF16);
+        w[i] = pack_pair(x, y, plane_fmt);
         if (p + 1 < PLANES) {  // what the plane leaves (0 where it is not finite)
-          const float px = __uint_as_float(w[i] << 16), py = __uint_as_float(w[i] & 0xFFFF0000u);
+          float px = __uint_as_float(w[i] << 16), py = __uint_as_float(w[i] & 0xFFFF0000u);
+          if (PLANES == 2 && plane_fmt == OUT_F16) {
+            px = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] & 0xFFFFu)));
+            py = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] >> 16)));
+          }
           v[0] = isfinite(px) ? __float_as_uint(x - px) : 0u;
           v[1] = isfinite(py) ? __float_as_uint(y - py) : 0u;
         }
@@ -497,7 +514,8 @@ __global__ void __launch_bounds__(head_threads(PARTS), 1)
     head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ CUtensorMap mapC, const HeadArgs args) {
   constexpr int STAGES = head_stages(MODE, PARTS);
-  constexpr int TERMS = plane_terms(PLANES);
+  using Plane = Terms<MODE, PLANES>;
+  constexpr int TERMS = Plane::count;
   constexpr int ACC = 256;
   constexpr uint32_t TMEM_COLS = 512;
   static_assert(head_smem(MODE, PARTS) <= kSmemLimit, "shared memory per CTA");
@@ -555,7 +573,7 @@ __global__ void __launch_bounds__(head_threads(PARTS), 1)
   const int n = args.count ? min(*args.count, args.T) : args.T;
   const Tiles tiles = head_tiles<MODE>(args, max(1, n));
   // stages summed in tensor memory at a time: all of a unit's, or a chunk
-  const int chunk = PLANES > 1 && (MODE == HEAD_DH || MODE == HEAD_DW) ? args.chunk : INT_MAX / 2;
+  const int chunk = PLANES == 3 && (MODE == HEAD_DH || MODE == HEAD_DW) ? args.chunk : INT_MAX / 2;
 
   if (warp == 0) {
     // ------------------------------------------------ bulk-tensor producer
@@ -574,9 +592,11 @@ __global__ void __launch_bounds__(head_threads(PARTS), 1)
               ok = false;
               break;
             }
-            const int term = PLANES == 1 ? 0 : it / span;
-            const int k0 = (lo + it - term * span) * kTileK;  // stages past the k axis load zeros
-            const int pa = PLANES == 1 ? 0 : plane_a(term), pb = PLANES == 1 ? 0 : plane_b(term);
+            // fp32: one pair of planes over all stages after another; two planes
+            // of dz: stage by stage, so that the second finds W in L2
+            const int term = TERMS == 6 ? it / span : it % TERMS;
+            const int k0 = (lo + (TERMS == 6 ? it - term * span : it / TERMS)) * kTileK;  // past the k axis: zeros
+            const int pa = Plane::a(term), pb = Plane::b(term);
             const uint32_t fb_local = ptx::smem_u32(&full[stage]);
             const uint32_t fb = ptx::mapa_shared(fb_local, 0);
             if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2u * kStage);
@@ -709,12 +729,12 @@ __global__ void __launch_bounds__(head_threads(PARTS), 1)
             epilogue_stats<PARTS>(tbase, row0 + lane, n, u.nb, part, walk, args);
           } else if constexpr (MODE == HEAD_DZ) {
             epilogue_dz<PLANES, PARTS>(tbase, row0, n, u.nb, part, k, walk, args, &mapC, buf, lane);
-          } else if constexpr (PLANES == 1 && MODE == HEAD_DW) {
+          } else if constexpr (PLANES < 3 && MODE == HEAD_DW) {
             epilogue_dw<PARTS>(tbase, row0, u.nb, part, factor, args, &mapC, buf, lane);
           } else {
             // fp32: a chunk's sum of the full-size terms took 4 steps a stage
             const float f =
-                PLANES == 1 ? 1.0f : factor * (1.0f + kStepLoss * static_cast<float>(4 * min(chunk, u.hi - lo)));
+                PLANES < 3 ? 1.0f : factor * (1.0f + kStepLoss * static_cast<float>(4 * min(chunk, u.hi - lo)));
             // in bulk where a sum is moved once a launch, else by the thread that owns it
             if (args.store_granule == 0) {
               epilogue_sums<PARTS>(tbase, MODE == HEAD_DW ? args.out_row0 + row0 : row0, u.nb, u.split, part, args.D, f,
@@ -784,20 +804,4 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
 }
 
 }  // namespace
-
-cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUtensorMap& mapB,
-                        const CUtensorMap& mapC, const HeadArgs& args, int pairs, cudaStream_t stream) {
-#define TGEMM_HEAD(MODE, PARTS)                                                                 \
-  (planes == 1 ? launch<MODE, 1, PARTS>(mapA, mapB, mapC, args, pairs, stream)                  \
-               : launch<MODE, kPlanes, PARTS>(mapA, mapB, mapC, args, pairs, stream))
-  switch (mode) {
-    case HEAD_STATS: return args.parts == 2 ? TGEMM_HEAD(HEAD_STATS, 2) : TGEMM_HEAD(HEAD_STATS, 1);
-    case HEAD_DZ: return TGEMM_HEAD(HEAD_DZ, 2);
-    case HEAD_DH: return TGEMM_HEAD(HEAD_DH, 2);
-    case HEAD_DW: return TGEMM_HEAD(HEAD_DW, 2);
-    default: return cudaErrorInvalidValue;
-  }
-#undef TGEMM_HEAD
-}
-
 }  // namespace tgemm

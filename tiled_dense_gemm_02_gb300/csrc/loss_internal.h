@@ -1,4 +1,4 @@
-// Internal interfaces of the vocabulary-head losses (loss_api.cu, loss_gemm.cu,
+// Internal interfaces of the vocabulary-head losses (loss_api.cu, loss_gemm.cuh,
 // loss_rows.cu) and the services of api.cu that they use.
 #pragma once
 
@@ -148,9 +148,15 @@ constexpr float kStepLoss = 1.0f / (1 << 26);
 
 // Output tile of every product: 256 x 256 per CTA pair.
 constexpr int kHeadTile = 256;
-// planes: 1 (16-bit operands) or 3 (fp32).
-cudaError_t launch_head(int mode, int planes, const CUtensorMap& mapA, const CUtensorMap& mapB,
-                        const CUtensorMap& mapC, const HeadArgs& args, int pairs, cudaStream_t stream);
+// planes: 1 (16-bit operands), 2 (the same, with dz in two planes) or 3 (fp32).
+cudaError_t launch_head_stats(int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
+                              const HeadArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_head_dz(int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
+                           const HeadArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_head_dh(int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
+                           const HeadArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_head_dw(int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
+                           const HeadArgs& args, int pairs, cudaStream_t stream);
 
 // ------------------------------------------------------------- few rows
 // Statistics of T <= kFewRows rows of H, read in place, in one pass over W on

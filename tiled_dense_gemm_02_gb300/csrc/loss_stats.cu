@@ -1,0 +1,13 @@
+// The pair product of the vocabulary-head losses: row statistics of the logits (loss_gemm.cuh).
+#include "loss_gemm.cuh"
+
+namespace tgemm {
+
+cudaError_t launch_head_stats(int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
+                          const HeadArgs& args, int pairs, cudaStream_t stream) {
+  if (planes == 3) return launch<HEAD_STATS, 3, 1>(mapA, mapB, mapC, args, pairs, stream);
+  return args.parts == 2 ? launch<HEAD_STATS, 1, 2>(mapA, mapB, mapC, args, pairs, stream)
+                         : launch<HEAD_STATS, 1, 1>(mapA, mapB, mapC, args, pairs, stream);
+}
+
+}  // namespace tgemm
