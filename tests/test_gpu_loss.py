@@ -424,3 +424,26 @@ def test_device_side_timeout_is_not_left_behind():
     assert st == lib.OK
     finished()
     ref.xent(h, w, y).check(loss=loss, lse=lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 8, 9, 16, 31, 32, 33])
+@pytest.mark.parametrize("D,left,right", [(64, 0, 0), (40, 1, 0), (41, 0, 0), (37, 3, 2), (50, 2, 4), (515, 5, 1)])
+def test_few_rows_beside_nan(T, D, left, right, dtype):
+    """Rows of W at every offset from the 16-byte grid, inside a matrix whose other columns are NaN."""
+    lib = H.tg()
+    V = 777
+    gen = torch.Generator(device="cuda").manual_seed(T * 1000 + D)
+    whole = torch.full((V + 2, left + D + right), float("nan"), dtype=dtype, device="cuda")
+    w = whole[1:V + 1, left:left + D]
+    w.copy_((torch.randn(V, D, device="cuda", generator=gen) * (2.0 / math.sqrt(D))).to(dtype))
+    wide = torch.full((T, D + left), float("nan"), dtype=dtype, device="cuda")
+    h = wide[:, left:]
+    h.copy_(torch.randn(T, D, device="cuda", generator=gen).to(dtype))
+    y = targets_for(T, V, gen, 0.2)
+    loss, lse = lib.linear_cross_entropy(h, w, y, label_smoothing=0.1, z_loss=1e-3)
+    ref.xent(h, w, y, smoothing=0.1, z_loss=1e-3).check(loss=loss, lse=lse)
+    ids, logits = lists_for(T, V, 7, gen)
+    loss, lse = lib.linear_distillation(h, w, ids, logits)
+    finished()
+    ref.distill(h, w, ids, logits).check(loss=loss, lse=lse)

@@ -123,7 +123,7 @@ void plan_dh(int64_t T, int64_t D, int64_t kb, int terms, Layout& l) {
 Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bool distill, const void* W, int64_t ldw,
                    int dtype, int64_t piece_opt) {
   Layout l;
-  l.few = !backward && few_rows(T, D);
+  l.few = !backward && few_rows(T, D, dtype == TGEMM_F32, host_granule(W, ldw, dtype == TGEMM_F32 ? 4 : 2) == 16);
   l.planes = dtype == TGEMM_F32 ? kPlanes : 1;
   l.dz_planes = l.planes > 1 ? l.planes : T <= kTwoPlaneRows ? 2 : 1;
   l.ldh = l.ldw_p = round_up(D, 8);
@@ -502,7 +502,9 @@ int run_loss(const Call& c) {
     f.q = rows.q;
     f.ms = ms;
     f.dot = dot;
-    TGEMM_CUDA(launch_few_stats(f, out_type, host_granule(c.W, c.ldw, es), c.stream), "few-rows launch");
+    f.ld_stats = c.T;
+    TGEMM_CUDA(launch_few_stats(f, out_type, host_granule(c.W, c.ldw, es), static_cast<int>(l.parts), c.stream),
+               "few-rows launch");
   } else {
     if (pairs < 1) return host_cuda_fail(cudaErrorLaunchOutOfResources, "CTA pairs");
     Products products(c, l, rows, ws, scale, flat, sms, pairs, status);

@@ -1,19 +1,22 @@
-// Row statistics of the vocabulary-head losses for a few rows (T <= 8): the
-// scoring of single tokens.
+// Row statistics of the vocabulary-head losses for a few rows on the CUDA cores:
+// the scoring of single tokens, of up to eight where rows of W are off the
+// 16-byte grid, and of up to 32 in fp32.
 //
-// The work is one pass over W: 2 T V D operations against V D elements read,
-// far below what the tensor cores need to be worth their set-up.  A tile of 256
-// rows would be nearly empty, and V / 256 tiles rarely fill whole rounds of the
-// pairs.  Here each warp takes four entries of W at a time, lane by lane in
-// 16-byte pieces, multiplies them with the rows of H held in shared memory as
-// fp32 (exact for 16-bit inputs), and keeps the running maximum and sum of a
-// softmax for its entries; blocks share the vocabulary evenly.  Rows of W may
-// have any alignment, so nothing is copied first.
+// The work is one pass over W (fp32: one per eight rows of H): 2 T V D
+// operations against V D elements read.  Each warp takes four entries of W at a
+// time, lane by lane in 16-byte pieces, multiplies them with the rows of H held
+// in shared memory as fp32 (exact for 16-bit inputs), and keeps the running
+// maximum and sum of a softmax for its entries; the warps share the vocabulary
+// evenly.  Nothing is copied first: rows off the 16-byte grid are read in words
+// of 4 or 2 bytes.  (Reading the aligned 16 bytes around a piece and shifting
+// between neighbouring lanes was slower: 236 us against 108 us for one row of
+// 65536 x 4100, since every piece then waits for its load before the next.)
 //
-// Bound by memory.  A lane spends T / 2 paired multiply-adds and one
-// conversion an element of W; an SM takes 11.8 two-byte elements a clock from
-// memory at the measured rate, so 8 rows use two thirds of its lanes.  Four
-// entries a warp share each read of H from shared memory.
+// Bound by memory.  Against the tensor-core product (its tiles nearly empty, W
+// copied first if unaligned or fp32), 65536 x 4096: one bf16 row 94 us (5.7 TB/s)
+// to 100 us; aligned bf16 rows from two on are the product's (two rows 113 us);
+// eight rows at 4100 columns 192 to 329 us; eight fp32 rows 210 us (5.1 TB/s)
+// to 1262 us, which the product takes for any number up to 128.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -48,7 +51,7 @@ __device__ __forceinline__ uint4 load_piece(const E* row, int c, int cols) {
   constexpr int N = lane_elems<E>();
   if (G == 16 && c + N <= cols) return __ldg(reinterpret_cast<const uint4*>(row + c));
   uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if constexpr (sizeof(E) == 4 || G >= 4) {
+  if constexpr (G >= 4) {
     constexpr int PER = 4 / static_cast<int>(sizeof(E));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(few_threads(TN), few_per_sm(TN)) few_stats_ker
   }
   float m = -INFINITY, s = 0.0f, dot = 0.0f, zs = 0.0f;
 
-  // an even share of the vocabulary, one after another; the places of a last,
+  // an even share of the vocabulary, one after another; the groups of a last,
   // incomplete step repeat its last entry, which costs no memory traffic
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * WARPS + warp, workers = static_cast<int64_t>(gridDim.x) * WARPS;
   const int v_end = static_cast<int>(a.V * (worker + 1) / workers);
@@ -219,8 +222,8 @@ __global__ void __launch_bounds__(few_threads(TN), few_per_sm(TN)) few_stats_ker
       join(m, s, s_part[0][w][q], s_part[1][w][q]);
       dot += s_part[2][w][q];
     }
-    a.ms[static_cast<int64_t>(blockIdx.x) * a.T + q] = make_float2(m, s);
-    a.dot[static_cast<int64_t>(blockIdx.x) * a.T + q] = dot;
+    a.ms[static_cast<int64_t>(blockIdx.x) * a.ld_stats + q] = make_float2(m, s);
+    a.dot[static_cast<int64_t>(blockIdx.x) * a.ld_stats + q] = dot;
   }
 }
 
@@ -228,7 +231,7 @@ template <typename E, int TN, int G>
 cudaError_t launch_few(const FewArgs& a, int blocks, cudaStream_t stream) {
   auto kernel = few_stats_kernel<E, TN, G>;
   const int groups = (a.D + lane_elems<E>() - 1) / lane_elems<E>();
-  const int smem = TN * groups * 16 * (lane_elems<E>() / 4);
+  const int smem = TN * groups * lane_elems<E>() * 4;
   static std::atomic<uint64_t> done_mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -255,9 +258,12 @@ cudaError_t launch_few(const FewArgs& a, int blocks, cudaStream_t stream) {
 template <typename E, int G>
 cudaError_t launch_rows(const FewArgs& a, int blocks, cudaStream_t stream) {
   if (a.T <= 1) return launch_few<E, 1, G>(a, blocks, stream);
-  if (a.T <= 2) return launch_few<E, 2, G>(a, blocks, stream);
-  if (a.T <= 4) return launch_few<E, 4, G>(a, blocks, stream);
-  return launch_few<E, 8, G>(a, blocks, stream);
+  if constexpr (sizeof(E) == 4 || G < 16) {
+    if (a.T <= 2) return launch_few<E, 2, G>(a, blocks, stream);
+    if (a.T <= 4) return launch_few<E, 4, G>(a, blocks, stream);
+    return launch_few<E, 8, G>(a, blocks, stream);
+  }
+  return cudaErrorInvalidValue;  // aligned 16-bit rows from two on take the tensor cores
 }
 
 template <typename E>
@@ -269,26 +275,41 @@ cudaError_t launch_type(const FewArgs& a, int granule, int blocks, cudaStream_t 
     return granule >= 4 ? launch_rows<E, 4>(a, blocks, stream) : launch_rows<E, 2>(a, blocks, stream);
 }
 
+int rows_held(int64_t T) { return T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8; }
+
 }  // namespace
 
-bool few_rows(int64_t T, int64_t D) {
-  int64_t rows = 1;
-  while (rows < T) rows *= 2;
-  return T <= kFewRows && rows * ((D + 7) / 8 * 8) * 4 <= kFewSmem;
+bool few_rows(int64_t T, int64_t D, bool f32, bool aligned) {
+  const int64_t most = f32 ? kFewMost : aligned ? 1 : kFewRows;
+  return T <= most && rows_held(T) * (D + 8) * 4 <= kFewSmem;
 }
 
 int few_blocks(int64_t T, int64_t V) {
   // the blocks that fit the SMs at once, each warp with at least one entry
-  const int tn = T <= 2 ? 1 : static_cast<int>(T <= 4 ? 4 : 8);
-  const int64_t most = (V + few_threads(tn) / 32 - 1) / (few_threads(tn) / 32);
-  return static_cast<int>(std::min<int64_t>(most, kFewSms * few_per_sm(tn)));
+  const int tn = rows_held(T), warps = few_threads(tn) / 32;
+  return static_cast<int>(std::min<int64_t>((V + warps - 1) / warps, int64_t(kFewSms) * few_per_sm(tn)));
 }
 
-cudaError_t launch_few_stats(const FewArgs& a, int type, int granule, cudaStream_t stream) {
-  const int blocks = few_blocks(a.T, a.V);
-  if (type == 0) return launch_type<__nv_bfloat16>(a, granule, blocks, stream);
-  if (type == 1) return launch_type<__half>(a, granule, blocks, stream);
-  return launch_type<float>(a, granule, blocks, stream);
+cudaError_t launch_few_stats(const FewArgs& args, int type, int granule, int blocks, cudaStream_t stream) {
+  // eight rows at a time; every group leaves its statistics in the same number of parts
+  const int es = type == 2 ? 4 : 2;
+  for (int t0 = 0; t0 < args.T; t0 += kFewRows) {
+    FewArgs a = args;
+    a.T = std::min(kFewRows, args.T - t0);
+    a.H = static_cast<const char*>(args.H) + t0 * args.ldh * es;
+    if (a.targets) a.targets += t0;
+    if (a.ids) {
+      a.ids += static_cast<int64_t>(t0) * a.K;
+      a.q += static_cast<int64_t>(t0) * a.K;
+    }
+    a.ms += t0;
+    a.dot += t0;
+    const cudaError_t e = type == 0   ? launch_type<__nv_bfloat16>(a, granule, blocks, stream)
+                          : type == 1 ? launch_type<__half>(a, granule, blocks, stream)
+                                      : launch_type<float>(a, granule, blocks, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace tgemm

@@ -159,8 +159,8 @@ cudaError_t launch_head_dw(int planes, const CUtensorMap& mapA, const CUtensorMa
                            const HeadArgs& args, int pairs, cudaStream_t stream);
 
 // ------------------------------------------------------------- few rows
-// Statistics of T <= kFewRows rows of H, read in place, in one pass over W on
-// the CUDA cores; few_blocks(T, V) parts.
+// Statistics of a few rows of H, read in place, in one pass over W (per eight
+// rows) on the CUDA cores; few_blocks(T, V) parts.
 struct FewArgs {
   int T, V, D, K;
   const void* H;
@@ -174,13 +174,16 @@ struct FewArgs {
   const float* q;
   float2* ms;
   float* dot;
+  int64_t ld_stats;  // rows of all passes
 };
-constexpr int kFewRows = 8;
+constexpr int kFewRows = 8;   // held in shared memory at a time
+constexpr int kFewMost = 32;  // fp32: in up to four passes
 constexpr int kFewSmem = 160 * 1024;
 constexpr int kFewSms = 152;
-bool few_rows(int64_t T, int64_t D);
+// Whether these rows take it (`aligned`: W's rows on the 16-byte grid).
+bool few_rows(int64_t T, int64_t D, bool f32, bool aligned);
 int few_blocks(int64_t T, int64_t V);
-// type: 0 bf16, 1 f16, 2 f32; granule: alignment of W's rows
-cudaError_t launch_few_stats(const FewArgs& a, int type, int granule, cudaStream_t stream);
+// type: 0 bf16, 1 f16, 2 f32; granule: alignment of W's rows in bytes
+cudaError_t launch_few_stats(const FewArgs& args, int type, int granule, int blocks, cudaStream_t stream);
 
 }  // namespace tgemm
