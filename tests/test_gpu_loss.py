@@ -447,3 +447,51 @@ def test_few_rows_beside_nan(T, D, left, right, dtype):
     loss, lse = lib.linear_distillation(h, w, ids, logits)
     finished()
     ref.distill(h, w, ids, logits).check(loss=loss, lse=lse)
+
+
+def test_both_losses_train_a_head():
+    """The example: cross entropy and divergence fall together, and padding's NaN reaches no gradient."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_head.py")
+    spec = importlib.util.spec_from_file_location("train_head", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    history = example.train(tokens=300, vocab=2000, depth=128, steps=12)
+    finished()
+    assert all(math.isfinite(v) for row in history for v in row)
+    first, last = history[0], history[-1]
+    assert last[0] < first[0] - 0.5 and last[1] < 0.7 * first[1]
+
+
+def test_calls_from_several_threads():
+    """Threads with streams and workspaces of their own get the bits a single call gives."""
+    import threading
+    lib = H.tg()
+    cases = []
+    for i, dtype in enumerate((BF16, F16, F32, BF16)):
+        h, w, gen = head(130 + 40 * i, 900, 96, dtype, seed=i)
+        y = targets_for(130 + 40 * i, 900, gen, 0.2)
+        g = torch.rand(130 + 40 * i, device="cuda", generator=gen)
+        cases.append((h, w, y, g, xent_both(h, w, y, g)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(case):
+        h, w, y, g, want = case
+        stream = torch.cuda.Stream()
+        for _ in range(5):
+            loss, lse = lib.linear_cross_entropy(h, w, y, stream=stream.cuda_stream)
+            dh, dw = lib.linear_cross_entropy_backward(h, w, y, lse, g, stream=stream.cuda_stream)
+            stream.synchronize()
+            for name, x in (("loss", loss), ("lse", lse), ("dh", dh), ("dw", dw)):
+                if not torch.equal(x, want[name]):
+                    wrong.append(name)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    finished()

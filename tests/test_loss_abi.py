@@ -164,3 +164,33 @@ def test_tensor_functions_refuse_bad_arguments(tg):
                                                 temperature=0.0)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_header_from_c(tg, tmp_path):
+    """The header compiles as C, and a C caller sees the binding's struct layout and the same sizes and refusals."""
+    import subprocess
+    src = tmp_path / "caller.c"
+    src.write_text(r'''
+#include <stddef.h>
+#include <stdio.h>
+#include "tgemm_loss.h"
+int main(void) {
+  tgemm_loss_options o = {0};
+  size_t n = 0;
+  o.ignore_index = -100;
+  printf("%zu %zu %zu ", sizeof o, offsetof(tgemm_loss_options, ignore_index), offsetof(tgemm_loss_options, reserved));
+  printf("%d ", tgemm_loss_workspace_size(1, 64, 5000, 100, 0, (const void*)0x1000, 101, TGEMM_BF16, &o, &n));
+  printf("%zu ", n);
+  printf("%d\n", tgemm_xent_forward(-1, 10, 10, 0, 10, 0, 10, 0, TGEMM_BF16, &o, 0, 0, 0, 0, 0));
+  return 0;
+}
+''')
+    exe = tmp_path / "caller"
+    lib = os.path.join(ROOT, "tiled_dense_gemm_02_gb300")
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe),
+                    os.path.join(lib, "libtgemm.so"), f"-Wl,-rpath,{lib}"], check=True)
+    got = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
+    st, n = tg.loss_workspace_size(True, 64, 5000, 100, 0, 0x1000, 101, tg.BF16)
+    assert st == tg.OK
+    assert [int(v) for v in got] == [ctypes.sizeof(tg.LossOptions), tg.LossOptions.ignore_index.offset,
+                                     tg.LossOptions.reserved.offset, tg.OK, n, tg.ERR_INVALID_VALUE]
