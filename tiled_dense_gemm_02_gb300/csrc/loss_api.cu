@@ -50,6 +50,13 @@ constexpr int64_t kShortStages = 6;
 // The second plane doubles the gradient products' stages: at 32768 x 2048, dH
 // 64 -> 84 us and 101 us with 16 and 256 rows.
 constexpr int64_t kTwoPlaneRows = 32;
+// dH and dW share a launch while together they are at most this many stages of
+// work a pair (an epilogue counts as eight).  Measured, backward calls in two
+// launches and in one: bf16 300 x 10000 x 512 40.6 and 35.4 us, 512 x 8192 x 1024
+// 51.7 and 45.5 us; fp32 900 x 2600 x 128 74.9 and 60.2 us; above the bound,
+// where the fixed shares of the pairs end unevenly, bf16 128 x 32768 x 1024 66.4
+// and 77.4 us.
+constexpr int64_t kBothStages = 96, kEpilogueStages = 8;
 constexpr float kRangeF16 = 16384.0f;  // |dz| <= 2: fp16's largest value is 65504, its small normals reach 2^-14
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -301,8 +308,7 @@ class Products {
       a_.reduce = i > 0;
       TGEMM_TRY(copy_weight());
       TGEMM_TRY(logits());
-      if (c_.backward && c_.dH) TGEMM_TRY(hidden_gradient());
-      if (c_.backward && c_.dW) TGEMM_TRY(weight_gradient());
+      if (c_.backward) TGEMM_TRY(gradients());
     }
     return TGEMM_OK;
   }
@@ -362,8 +368,34 @@ class Products {
                        : launch(launch_head_stats, l_.planes, mh, mw, mw, a_, units);
   }
 
-  int hidden_gradient() {
-    HeadArgs b = a_;
+  int gradients() {
+    HeadLaunch dh, dw;
+    if (c_.dH) TGEMM_TRY(hidden_gradient(dh));
+    if (c_.dW) TGEMM_TRY(weight_gradient(dw));
+    const int64_t m_tiles = ceil_div(c_.T, kHeadTile), d_tiles = ceil_div(c_.D, kHeadTile);
+    const int64_t dh_units = m_tiles * d_tiles * l_.splits, dw_units = ceil_div(n_, kHeadTile) * d_tiles;
+    if (c_.dH && c_.dW && l_.pieces == 1) {
+      // a unit's stages and its epilogue, in stages
+      const int64_t terms = l_.planes > 1 ? 6 : l_.dz_planes;
+      const int64_t dh_work = dh_units * (terms * l_.k_per_split + kEpilogueStages);
+      const int64_t dw_work = dw_units * (terms * ceil_div(c_.T, kTileK) + kEpilogueStages);
+      if (dh_work + dw_work <= kBothStages * pairs_ && pairs_ >= 2) {
+        const int64_t share = std::max<int64_t>(1, std::min<int64_t>(pairs_ - 1, pairs_ * dh_work / (dh_work + dw_work)));
+        TGEMM_CUDA(launch_head_both(l_.dz_planes, dh, static_cast<int>(std::min(share, dh_units)), dw,
+                                    static_cast<int>(std::min(pairs_ - share, dw_units)), c_.stream),
+                   "head launch");
+        host_count_launches(1);
+        return TGEMM_OK;
+      }
+    }
+    if (c_.dH) TGEMM_TRY(launch(launch_head_dh, l_.dz_planes, dh.a, dh.b, dh.c, dh.args, dh_units));
+    if (c_.dW) TGEMM_TRY(launch(launch_head_dw, l_.dz_planes, dw.a, dw.b, dw.c, dw.args, dw_units));
+    return TGEMM_OK;
+  }
+
+  int hidden_gradient(HeadLaunch& out) {
+    HeadArgs& b = out.args;
+    b = a_;
     b.k_blocks = static_cast<int>(ceil_div(n_, kTileK));
     b.splits = l_.splits;
     b.k_per_split = l_.k_per_split;
@@ -371,33 +403,29 @@ class Products {
     b.ld_out = l_.ld_acc;
     b.split_stride = c_.T * l_.ld_acc;
     b.store_granule = l_.planes > 1 && l_.k_per_split > kChunkStages ? 16 : 0;
-    CUtensorMap mz, mw, ma;
-    TGEMM_TRY(map_dz(&mz, kTileK, kTileM));
-    TGEMM_TRY(map_weight(&mw, 64, kTileK));
-    TGEMM_TRY(host_map_3d(&ma, 2, b.out, c_.D, c_.T, l_.splits, l_.ld_acc * 4, c_.T * l_.ld_acc * 4, 32, 32));
-    return launch(launch_head_dh, l_.dz_planes, mz, mw, ma, b, ceil_div(c_.T, kHeadTile) * ceil_div(c_.D, kHeadTile) * l_.splits);
+    TGEMM_TRY(map_dz(&out.a, kTileK, kTileM));
+    TGEMM_TRY(map_weight(&out.b, 64, kTileK));
+    return host_map_3d(&out.c, 2, b.out, c_.D, c_.T, l_.splits, l_.ld_acc * 4, c_.T * l_.ld_acc * 4, 32, 32);
   }
 
-  int weight_gradient() {
-    HeadArgs b = a_;
+  int weight_gradient(HeadLaunch& out) {
+    HeadArgs& b = out.args;
+    b = a_;
     b.out = c_.dW;
     b.ld_out = c_.lddw;
     b.out_row0 = static_cast<int>(v0_);
     b.reduce = 0;
-    const int64_t stages = ceil_div(c_.T, kTileK);
     const bool f32 = l_.planes > 1;
     b.store_granule = host_granule(c_.dW, c_.lddw, f32 ? 4 : 2);
-    CUtensorMap mz, mh, mo;
-    TGEMM_TRY(map_dz(&mz, 64, kTileK));
-    TGEMM_TRY(map_hidden(&mh, 64, kTileK));
+    TGEMM_TRY(map_dz(&out.a, 64, kTileK));
+    TGEMM_TRY(map_hidden(&out.b, 64, kTileK));
     // fp32 sums of several chunks are added by their owners
-    const bool bulk = b.store_granule == 16 && (!f32 || stages <= kChunkStages);
-    if (bulk) {
+    if (b.store_granule == 16 && (!f32 || ceil_div(c_.T, kTileK) <= kChunkStages)) {
       b.store_granule = 0;
-      TGEMM_TRY(host_map_3d(&mo, f32 ? 2 : type_, c_.dW, c_.D, c_.V, 1, c_.lddw * (f32 ? 4 : 2), 0, f32 ? 32 : 64, 32));
+      return host_map_3d(&out.c, f32 ? 2 : type_, c_.dW, c_.D, c_.V, 1, c_.lddw * (f32 ? 4 : 2), 0, f32 ? 32 : 64, 32);
     }
-    return launch(launch_head_dw, l_.dz_planes, mz, mh, bulk ? mo : mh, b,
-                  ceil_div(n_, kHeadTile) * ceil_div(c_.D, kHeadTile));
+    out.c = out.b;  // not used
+    return TGEMM_OK;
   }
 
   const Call& c_;

@@ -509,10 +509,10 @@ __device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, in
   }
 }
 
+// One product, by CTA pair `worker` of `workers`.
 template <int MODE, int PLANES, int PARTS>
-__global__ void __launch_bounds__(head_threads(PARTS), 1)
-    head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                const __grid_constant__ CUtensorMap mapC, const HeadArgs args) {
+__device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
+                                             const HeadArgs& args, const int worker, const int workers) {
   constexpr int STAGES = head_stages(MODE, PARTS);
   using Plane = Terms<MODE, PLANES>;
   constexpr int TERMS = Plane::count;
@@ -536,8 +536,6 @@ __global__ void __launch_bounds__(head_threads(PARTS), 1)
   const int lane = threadIdx.x & 31;
   const int cta = static_cast<int>(ptx::cluster_ctarank() & 1u);  // which 128 rows of the pair's tile
   const bool leader = cta == 0;
-  const int worker = blockIdx.x / 2;
-  const int workers = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -772,11 +770,16 @@ __global__ void __launch_bounds__(head_threads(PARTS), 1)
 }
 
 template <int MODE, int PLANES, int PARTS>
-cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC, const HeadArgs& args,
-                   int pairs, cudaStream_t stream) {
-  constexpr int smem = head_smem(MODE, PARTS);
-  auto kernel = head_kernel<MODE, PLANES, PARTS>;
-  static std::atomic<uint64_t> done_mask{0};
+__global__ void __launch_bounds__(head_threads(PARTS), 1)
+    head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                const __grid_constant__ CUtensorMap mapC, const __grid_constant__ HeadArgs args) {
+  head_product<MODE, PLANES, PARTS>(mapA, mapB, mapC, args, blockIdx.x / 2, gridDim.x / 2);
+}
+
+// Launch of a kernel on `pairs` clusters of two CTAs, dependent on the kernel before it.
+template <typename... Params, typename... Args>
+cudaError_t launch_pairs(void (*kernel)(Params...), int smem, int threads, std::atomic<uint64_t>& done_mask, int pairs,
+                         cudaStream_t stream, const Args&... args) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -788,7 +791,7 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.blockDim = dim3(head_threads(PARTS), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -800,7 +803,15 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, mA, mB, mC, args);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int MODE, int PLANES, int PARTS>
+cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC, const HeadArgs& args,
+                   int pairs, cudaStream_t stream) {
+  static std::atomic<uint64_t> done_mask{0};
+  return launch_pairs(head_kernel<MODE, PLANES, PARTS>, head_smem(MODE, PARTS), head_threads(PARTS), done_mask, pairs,
+                      stream, mA, mB, mC, args);
 }
 
 }  // namespace

@@ -158,6 +158,14 @@ cudaError_t launch_head_dh(int planes, const CUtensorMap& mapA, const CUtensorMa
 cudaError_t launch_head_dw(int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
                            const HeadArgs& args, int pairs, cudaStream_t stream);
 
+// dH by dh_pairs pairs and dW by dw_pairs, side by side.
+struct HeadLaunch {
+  CUtensorMap a, b, c;
+  HeadArgs args;
+};
+cudaError_t launch_head_both(int planes, const HeadLaunch& dh, int dh_pairs, const HeadLaunch& dw, int dw_pairs,
+                             cudaStream_t stream);
+
 // ------------------------------------------------------------- few rows
 // Statistics of a few rows of H, read in place, in one pass over W (per eight
 // rows) on the CUDA cores; few_blocks(T, V) parts.
