@@ -93,8 +93,8 @@ TGEMM_API int tgemm_loss_workspace_size(int backward, int64_t T, int64_t V, int6
  * misaligned or smaller than tgemm_loss_workspace_size;
  * TGEMM_ERR_UNSUPPORTED_DTYPE; TGEMM_ERR_MISALIGNED for a pointer not aligned
  * to its element; TGEMM_ERR_ALIAS when an output overlaps an input, another
- * output or the workspace; TGEMM_ERR_TOO_LARGE for T, V, D or a leading
- * dimension >= 2^31, or K > TGEMM_DISTILL_MAX_K.  They are returned before any
+ * output or the workspace; TGEMM_ERR_TOO_LARGE for T, V >= 2^31 - 256, D >=
+ * 2^28, a leading dimension >= 2^31, or K > TGEMM_DISTILL_MAX_K.  They are returned before any
  * CUDA call.  T == 0: the forward calls do nothing, the backward calls zero dW.
  */
 TGEMM_API int tgemm_xent_forward(int64_t T, int64_t V, int64_t D,

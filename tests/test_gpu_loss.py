@@ -495,3 +495,27 @@ def test_calls_from_several_threads():
         t.join()
     assert not wrong, wrong
     finished()
+
+
+@pytest.mark.parametrize("T", [3, 200], ids=["few_rows", "tiles"])
+def test_captured_in_a_graph(T):
+    """A step captured in a CUDA graph and replayed on new inputs gives the bits of plain calls."""
+    V, D = 1500, 128
+    h, w, gen = head(T, V, D, BF16, seed=1)
+    y = targets_for(T, V, gen, 0.2)
+    g = torch.rand(T, device="cuda", generator=gen)
+    xent_both(h, w, y, g)  # first calls set kernel attributes and device records
+    lib = H.tg()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, lse = lib.linear_cross_entropy(h, w, y)
+        dh, dw = lib.linear_cross_entropy_backward(h, w, y, lse, g)
+    for seed in (2, 3):
+        h2, w2, gen = head(T, V, D, BF16, seed=seed)
+        h.copy_(h2)
+        w.copy_(w2)
+        y.copy_(targets_for(T, V, gen, 0.3))
+        graph.replay()
+        want = xent_both(h, w, y, g)
+        for name, x in (("loss", loss), ("lse", lse), ("dh", dh), ("dw", dw)):
+            assert torch.equal(x, want[name]), name

@@ -197,8 +197,8 @@ int check_shape(int64_t T, int64_t V, int64_t D, int64_t K, bool distill, int dt
   if (dtype != TGEMM_F32 && dtype != TGEMM_F16 && dtype != TGEMM_BF16) return TGEMM_ERR_UNSUPPORTED_DTYPE;
   const int st = check_options(opts, distill);
   if (st != TGEMM_OK) return st;
-  // the last tile's end must stay an int
-  if (T >= kMaxExtent - kHeadTile || V >= kMaxExtent - kHeadTile || D >= kMaxExtent - kHeadTile ||
+  // the last tile's end and a row's bytes must stay ints
+  if (T >= kMaxExtent - kHeadTile || V >= kMaxExtent - kHeadTile || D >= kMaxExtent / 8 ||
       (distill && K > TGEMM_DISTILL_MAX_K))
     return TGEMM_ERR_TOO_LARGE;
   return TGEMM_OK;

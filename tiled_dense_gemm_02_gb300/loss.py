@@ -179,8 +179,14 @@ def _head(hidden, weight, backward, K, options, workspace):
     return torch, device, (T, V, D), code, (hidden.data_ptr(), ldh, w, ldw), options, workspace, need
 
 
+def _current_stream(torch, device):
+    """The current stream's handle; torch's own short way to it where there is one (1 us of a 20 us call)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
+
+
 def _call(torch, device, function, args, workspace, need):
-    args += (workspace.data_ptr(), need, torch.cuda.current_stream(device).cuda_stream)
+    args += (workspace.data_ptr(), need, _current_stream(torch, device))
     if torch.cuda.current_device() == device:
         st = function(*args)
     else:
