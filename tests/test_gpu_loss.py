@@ -449,6 +449,100 @@ def test_few_rows_beside_nan(T, D, left, right, dtype):
     ref.distill(h, w, ids, logits).check(loss=loss, lse=lse)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("V,D,left,right", [(777, 64, 0, 0), (5, 41, 0, 0), (33, 50, 2, 4), (777, 1030, 0, 2),
+                                            (300, 2100, 4, 0), (257, 37, 3, 2)])
+def test_few_rows_gradients_beside_nan(T, V, D, left, right, dtype):
+    """Less than a share of entries, columns past one block's, rows that do not count; the rest of the matrix NaN."""
+    gen = torch.Generator(device="cuda").manual_seed(T * 1000 + D)
+    whole = torch.full((V + 2, left + D + right), float("nan"), dtype=dtype, device="cuda")
+    w = whole[1:V + 1, left:left + D]
+    w.copy_((torch.randn(V, D, device="cuda", generator=gen) * (2.0 / math.sqrt(D))).to(dtype))
+    wide = torch.full((T, D + left), float("nan"), dtype=dtype, device="cuda")
+    h = wide[:, left:]
+    h.copy_(torch.randn(T, D, device="cuda", generator=gen).to(dtype))
+    y = targets_for(T, V, gen)
+    g = torch.randn(T, device="cuda", generator=gen)
+    if T > 2:
+        y[1] = -100
+        h[1] = g[1] = float("nan")
+    more = {"scale": 0.8, "z_loss": 1e-2}
+    ref.xent(h, w, y, smoothing=0.1, g=g, **more).check(**xent_both(h, w, y, g, label_smoothing=0.1, **more))
+    ids, logits = lists_for(T, V, 7, gen)
+    if T > 2:
+        ids[1] = -1
+    ref.distill(h, w, ids, logits, 2.0, g).check(**distill_both(h, w, ids, logits, g, temperature=2.0))
+
+
+@pytest.mark.parametrize("dtype,code,T", [(BF16, 2, 2), (F16, 1, 1), (F32, 0, 5)], ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("pad_w", [0, 1])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (8, 0), (3, 0), (8, 1), (2, 2)])
+def test_few_rows_write_only_their_outputs(dtype, code, T, pad_w, pad, offset):
+    lib = H.tg()
+    V, D = 601, 90
+    h, w, gen = head(T, V, D + pad_w, dtype)
+    D += pad_w
+    y = targets_for(T, V, gen)
+    g = torch.rand(T, device="cuda", generator=gen)
+    loss, lse = lib.linear_cross_entropy(h, w, y)
+    ld = D + pad
+    es = h.element_size()
+    st, need = lib.loss_workspace_size(True, T, V, D, 0, w.data_ptr(), D, code)
+    assert st == lib.OK
+    for want in ((True, True), (True, False), (False, True)):
+        outs = []
+        for rows in (T, V):
+            flat = torch.full((offset + rows * ld + 64,), -77.0, dtype=dtype, device="cuda")
+            outs.append((flat, flat[offset:offset + rows * ld].view(rows, ld)))
+        ptrs = [o[0].data_ptr() + offset * es if on else 0 for o, on in zip(outs, want)]
+        ws = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+        st = lib.xent_backward(T, V, D, h.data_ptr(), D, w.data_ptr(), D, y.data_ptr(), lse.data_ptr(), g.data_ptr(),
+                               code, ptrs[0], ld, ptrs[1], ld, None, ws.data_ptr(), need,
+                               torch.cuda.current_stream().cuda_stream)
+        assert st == lib.OK, lib.status_string(st)
+        finished()
+        assert bool((ws[need:] == 0xA5).all()), "written past the workspace"
+        if all(want):
+            first = [o[1][:, :D].clone() for o in outs]
+            ref.xent(h, w, y, g=g).check(loss=loss, lse=lse, dh=first[0], dw=first[1])
+        for (flat, view), rows, on, both in zip(outs, (T, V), want, first):
+            if not on:
+                assert bool((flat == -77).all())
+                continue
+            assert torch.equal(view[:, :D], both)
+            assert bool((view[:, D:] == -77).all()) and bool((flat[:offset] == -77).all())
+            assert bool((flat[offset + rows * ld:] == -77).all())
+
+
+def test_few_rows_gradients_past_32_bits():
+    """A weight of more than 2^31 elements; its end alone gives the same bits, dH is the formula's."""
+    lib = H.tg()
+    T, V, D, last = 2, 140_000, 16_384, 600
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("not enough free memory")
+    h, w, gen = head(T, V, D, BF16)
+    y = torch.tensor([V - 1, V - last], device="cuda")
+    g = torch.tensor([1.0, -0.5], device="cuda")
+    _, lse = lib.linear_cross_entropy(h, w, y)
+    dh, dw = lib.linear_cross_entropy_backward(h, w, y, lse, g)
+    end_dh, end_dw = lib.linear_cross_entropy_backward(h, w[V - last:], y - (V - last), lse, g)
+    finished()
+    assert torch.equal(dw[V - last:], end_dw)
+    h64, exact, mass = h.double(), 0.0, 0.0
+    z = torch.cat([h64 @ w[v:v + 10_000].double().T for v in range(0, V, 10_000)], 1)
+    dz = torch.softmax(z, 1)
+    dz[torch.arange(T), y] -= 1
+    dz *= g.double()[:, None]
+    for v in range(0, V, 10_000):
+        part = w[v:v + 10_000].double()
+        exact = exact + dz[:, v:v + 10_000] @ part
+        mass = mass + dz[:, v:v + 10_000].abs() @ part.abs()
+    # a logit's 16384 products in sums of 2^8 steps: 2^-16 of sum |h w| (under 256), relative to dz; dH in
+    # sums of under 2^11 steps; its rounding to bf16
+    assert bool(((dh.double() - exact).abs() <= 2 ** -8 * exact.abs() + (2 ** -8 + 2 ** -13) * mass).all())
+
+
 def test_both_losses_train_a_head():
     """The example: cross entropy and divergence fall together, and padding's NaN reaches no gradient."""
     import importlib.util

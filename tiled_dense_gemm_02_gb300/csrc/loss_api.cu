@@ -92,8 +92,8 @@ struct Call {
 struct Layout {
   int planes = 1;              // of H and W
   int dz_planes = 1;
-  bool few = false;            // forward of a few rows, on the CUDA cores
-  bool direct = false;         // forward that reads H in place
+  bool few = false;            // a few rows, on the CUDA cores
+  bool direct = false;         // H is read in place
   bool pack = false;           // W is copied to an aligned pitch or to planes, piece by piece
   int64_t piece = 0, pieces = 1;
   int64_t ldh = 0, ldw_p = 0, ldz = 0, ld_acc = 0;
@@ -130,7 +130,7 @@ void plan_dh(int64_t T, int64_t D, int64_t kb, int terms, Layout& l) {
 Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bool distill, const void* W, int64_t ldw,
                    int dtype, int64_t piece_opt) {
   Layout l;
-  l.few = !backward && few_rows(T, D, dtype == TGEMM_F32, host_granule(W, ldw, dtype == TGEMM_F32 ? 4 : 2) == 16);
+  l.few = few_rows(backward, T, D, dtype == TGEMM_F32, host_granule(W, ldw, dtype == TGEMM_F32 ? 4 : 2) == 16);
   l.planes = dtype == TGEMM_F32 ? kPlanes : 1;
   l.dz_planes = l.planes > 1 ? l.planes : T <= kTwoPlaneRows ? 2 : 1;
   l.ldh = l.ldw_p = round_up(D, 8);
@@ -144,8 +144,15 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   } else {
     const int64_t per = 2 * std::max<int64_t>(backward ? l.dz_planes * T : 0, l.pack ? l.planes * l.ldw_p : 0);  // bytes per entry
     const int64_t fit = std::max<int64_t>(2048, kPieceBytes / per / kHeadTile * kHeadTile);
-    l.piece = std::min(fit, whole);
-    l.piece = round_up(ceil_div(V, ceil_div(V, l.piece)), kHeadTile);
+    if (l.pack && T <= kHeadTile) {
+      // one row of tiles: whole rounds of the grid, though the copy be larger (33
+      // fp32 rows of 131072 x 4096: 43 tiles for 76 pairs were 2414 + 4355 us,
+      // forward and backward, 76 are 1940 + 3417)
+      l.piece = std::min(round_up(fit, kPlanPairs * kHeadTile), whole);
+    } else {
+      l.piece = std::min(fit, whole);
+      l.piece = round_up(ceil_div(V, ceil_div(V, l.piece)), kHeadTile);
+    }
   }
   l.pieces = ceil_div(V, l.piece);
   l.ldz = l.piece;
@@ -166,7 +173,11 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   l.coef = take(backward ? T * 16 : 0);
   l.h = take(T * l.ldh * 2 * l.planes);
   if (l.pack) l.w = take(l.piece * l.ldw_p * 2 * l.planes);
-  if (backward) {
+  if (backward && l.few) {
+    l.splits = few_shares(V, D, dtype == TGEMM_F32);
+    l.z = take(V * few_held(T) * 4);
+    l.acc = take(l.splits * T * l.ld_acc * 4);
+  } else if (backward) {
     l.z = take(T * l.ldz * 2 * l.dz_planes);
     plan_dh(T, D, ceil_div(std::min(l.piece, V), kTileK), l.planes > 1 ? 6 : l.dz_planes, l);
     l.acc = take(l.splits * T * l.ld_acc * 4);
@@ -463,7 +474,7 @@ int run_loss(const Call& c) {
   // the gather drops the rows that do not count and aligns the others: one tile
   // of aligned rows needs neither (its ignored rows touch no other row's sums)
   const int granule = host_granule(c.H, c.ldh, es);
-  l.direct = !c.backward && (l.few || (l.planes == 1 && c.T <= kHeadTile && granule == 16));
+  l.direct = l.few || (!c.backward && l.planes == 1 && c.T <= kHeadTile && granule == 16);
   char* ws = static_cast<char*>(c.workspace);
   GatherArgs g;
   std::memset(&g, 0, sizeof g);
@@ -484,7 +495,7 @@ int run_loss(const Call& c) {
     rows.own = reinterpret_cast<float*>(ws + l.own);
     rows.flags = reinterpret_cast<unsigned char*>(ws + l.flags);
   }
-  if (c.backward) rows.coef = reinterpret_cast<float4*>(ws + l.coef);
+  if (c.backward && !l.few) rows.coef = reinterpret_cast<float4*>(ws + l.coef);
   g.T = static_cast<int>(c.T);
   g.D = static_cast<int>(c.D);
   g.es = es;
@@ -531,8 +542,35 @@ int run_loss(const Call& c) {
     f.ms = ms;
     f.dot = dot;
     f.ld_stats = c.T;
-    TGEMM_CUDA(launch_few_stats(f, out_type, host_granule(c.W, c.ldw, es), static_cast<int>(l.parts), c.stream),
-               "few-rows launch");
+    const int w_granule = host_granule(c.W, c.ldw, es), blocks = few_blocks(c.T, c.V);
+    if (c.backward) {
+      f.rule = g.rule;
+      f.scale = scale;
+      f.z_loss = z_loss;
+      f.lse = c.lse;
+      f.grad = c.grad;
+      f.dz = reinterpret_cast<float*>(ws + l.z);
+      FewGradArgs d;
+      std::memset(&d, 0, sizeof d);
+      d.T = f.T;
+      d.V = f.V;
+      d.D = f.D;
+      d.H = c.H;
+      d.ldh = c.ldh;
+      d.W = c.W;
+      d.ldw = c.ldw;
+      d.dz = f.dz;
+      d.rule = g.rule;
+      d.dW = c.dW;
+      d.lddw = c.lddw;
+      d.store_granule = c.dW ? host_granule(c.dW, c.lddw, es) : 0;
+      d.acc = c.dH ? reinterpret_cast<float*>(ws + l.acc) : nullptr;
+      d.ld_acc = l.ld_acc;
+      d.shares = l.splits;
+      TGEMM_CUDA(launch_few_grad(f, d, out_type, w_granule == 16, blocks, c.stream), "few-rows launch");
+    } else {
+      TGEMM_CUDA(launch_few_stats(f, out_type, w_granule, blocks, c.stream), "few-rows launch");
+    }
   } else {
     if (pairs < 1) return host_cuda_fail(cudaErrorLaunchOutOfResources, "CTA pairs");
     Products products(c, l, rows, ws, scale, flat, sms, pairs, status);
@@ -545,7 +583,7 @@ int run_loss(const Call& c) {
                "combine launch");
   else if (c.dH)
     TGEMM_CUDA(launch_finish_dh(reinterpret_cast<float*>(ws + l.acc), l.ld_acc, c.T * l.ld_acc, l.splits, g.T, g.D, rows,
-                                out_type, c.dH, c.lddh, c.stream),
+                                g.rule, out_type, c.dH, c.lddh, c.stream),
                "dH launch");
   return TGEMM_OK;
 }

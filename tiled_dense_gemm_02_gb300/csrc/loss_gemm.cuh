@@ -9,6 +9,11 @@
 //   DH     dz . W             fp32 sums, stored or added (bulk-tensor reduce)
 //   DW     dz^T . H           times a factor, rounded once, stored
 //
+// with k2 = scale log2(e), so that one fused multiply-add and one 2^x serve
+// each logit.  H and W are read K-major (their rows are the k axis) by STATS
+// and DZ; W as the N-major B of DH; dz as the M-major A and H as the N-major B
+// of DW: no operand is ever transposed in memory.
+//
 // PLANES = 3: fp32 operands come as three bf16 planes (loss_rows.cu), and a
 // stage of the k axis is then six stages, one per pair of planes, the small
 // terms first: the last sixth alone adds to a sum of full size, so the adder's
@@ -18,11 +23,6 @@
 // PLANES = 2: 16-bit operands, dz as two planes (its rounding and what that
 // leaves), so that few rows' gradients do not depend on how the one or two
 // entries that matter happen to round.
-//
-// with k2 = scale log2(e), so that one fused multiply-add and one 2^x serve
-// each logit.  H and W are read K-major (their rows are the k axis) by STATS
-// and DZ; W as the N-major B of DH; dz as the M-major A and H as the N-major B
-// of DW: no operand is ever transposed in memory.
 //
 // Roles (both CTAs unless noted):
 //   warp 0      bulk-tensor producer of this CTA's 128 rows of A and 128

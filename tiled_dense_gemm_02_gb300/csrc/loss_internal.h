@@ -88,9 +88,11 @@ cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream);
 // sum q z / scale.  Without gathered rows it also writes those that do not count.
 cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T, float scale, float z_loss,
                            const HeadRows& rows, const RowRule& rule, float* loss, float* lse, cudaStream_t stream);
-// dH row t = factor * sum over splits of acc[s][place[t]], or 0.
+// dH row t = factor * sum over splits of acc[s][place[t]], or 0.  Without
+// gathered rows: of acc[s][t], factor 1.
 cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
-                             const HeadRows& rows, int type, void* dH, int64_t lddh, cudaStream_t stream);
+                             const HeadRows& rows, const RowRule& rule, int type, void* dH, int64_t lddh,
+                             cudaStream_t stream);
 // The three planes of an fp32 matrix (vec: 16-byte aligned rows); each plane
 // has pitch ld_out, a multiple of 8.
 cudaError_t launch_split(const float* W, int64_t ldw, void* out, int64_t ld_out, int64_t plane, int rows, int cols,
@@ -183,14 +185,42 @@ struct FewArgs {
   float2* ms;
   float* dot;
   int64_t ld_stats;  // rows of all passes
+  // backward
+  RowRule rule;
+  float scale, z_loss;
+  const float* lse;
+  const float* grad;
+  float* dz;         // V x rows_held(T)
 };
 constexpr int kFewRows = 8;   // held in shared memory at a time
 constexpr int kFewMost = 32;  // fp32: in up to four passes
 constexpr int kFewSmem = 160 * 1024;
 constexpr int kFewSms = 152;
 // Whether these rows take it (`aligned`: W's rows on the 16-byte grid).
-bool few_rows(int64_t T, int64_t D, bool f32, bool aligned);
+bool few_rows(bool backward, int64_t T, int64_t D, bool f32, bool aligned);
 int few_blocks(int64_t T, int64_t V);
+// Backward of a few rows: dz first, then dW and dH in one pass over W (each block
+// a share of the vocabulary and up to 256 16-byte pieces of the columns), dH as
+// one sum per share.
+struct FewGradArgs {
+  int T, V, D;
+  const void* H;
+  int64_t ldh;
+  const void* W;
+  int64_t ldw;
+  const float* dz;
+  RowRule rule;
+  void* dW;            // null: not wanted
+  int64_t lddw;
+  int store_granule;   // alignment of dW's rows in bytes
+  float* acc;          // shares x T x ld_acc; null: dH is not wanted
+  int64_t ld_acc;
+  int shares;
+};
+int few_held(int64_t T);  // rows of dz: T rounded up to a power of two
+int few_shares(int64_t V, int64_t D, bool f32);
+cudaError_t launch_few_grad(const FewArgs& f, const FewGradArgs& g, int type, bool aligned, int blocks,
+                            cudaStream_t stream);
 // type: 0 bf16, 1 f16, 2 f32; granule: alignment of W's rows in bytes
 cudaError_t launch_few_stats(const FewArgs& args, int type, int granule, int blocks, cudaStream_t stream);
 

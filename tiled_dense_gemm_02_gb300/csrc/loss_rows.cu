@@ -7,8 +7,7 @@
 
 #include <climits>
 
-#include "loss_internal.h"
-#include "ptx.cuh"
+#include "loss_rows.cuh"
 
 namespace tgemm {
 namespace {
@@ -121,13 +120,6 @@ __global__ void __launch_bounds__(kListWarps * 32)
 }
 
 // ---------------------------------------------------------------- the gather
-__device__ __forceinline__ unsigned char row_flag(const RowRule& a, int t) {
-  if (!a.targets) return a.flags[t];
-  const int64_t y = a.targets[t];
-  if (y == a.ignore_index) return kRowIgnored;
-  return (y >= 0 && y < a.V) ? kRowCounts : kRowBad;
-}
-
 // loss and lse of a row that does not count
 __device__ __forceinline__ float row_value(unsigned char flag) {
   return flag == kRowBad ? __int_as_float(0x7FC00000) : 0.0f;
@@ -322,13 +314,6 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
 // of a part are read at a time), or 1 where there are too few rows to fill the
 // SMs and a row's parts are spread over the whole block.
 constexpr int kCombineThreads = 256;
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float top = fmaxf(m, m2);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  s = s * exp2f(m - ref) + s2 * exp2f(m2 - ref);
-  m = top;
-}
-
 template <int ROWS>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_kernel(const float2* ms, const float* dot, int tiles, int T, float scale,
@@ -392,8 +377,8 @@ constexpr int kFinishThreads = 128;
 template <typename Out, int LANES>
 __global__ void __launch_bounds__(kFinishThreads) finish_dh_kernel(const float* acc, int64_t ld_acc,
                                                                    int64_t split_stride, int splits, int T, int D,
-                                                                   HeadRows rows, Out* __restrict__ dH, int64_t lddh,
-                                                                   int wide) {
+                                                                   HeadRows rows, RowRule rule, Out* __restrict__ dH,
+                                                                   int64_t lddh, int wide) {
   chain();
   const int groups = (D + 3) / 4;
   const int lane = threadIdx.x % LANES;
@@ -402,8 +387,9 @@ __global__ void __launch_bounds__(kFinishThreads) finish_dh_kernel(const float* 
   const int c = static_cast<int>(i - row * groups) * 4;
   const bool inside = row < T;
   const int t = inside ? static_cast<int>(row) : 0;
-  const int place = inside ? rows.place[t] : -1;
-  const float f = *rows.factor;
+  // without gathered rows a row's sums are in its own place
+  const int place = !inside ? -1 : rows.place ? rows.place[t] : row_flag(rule, t) == kRowCounts ? t : -1;
+  const float f = rows.factor ? *rows.factor : 1.0f;
   Out* out = dH + static_cast<int64_t>(t) * lddh + c;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (place >= 0) {
@@ -480,7 +466,8 @@ cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T,
 }
 
 cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
-                             const HeadRows& rows, int type, void* dH, int64_t lddh, cudaStream_t stream) {
+                             const HeadRows& rows, const RowRule& rule, int type, void* dH, int64_t lddh,
+                             cudaStream_t stream) {
   const int es = type == 2 ? 4 : 2;
   const int wide = reinterpret_cast<uint64_t>(dH) % (4 * es) == 0 && lddh % 4 == 0 ? 1 : 0;
   const int lanes = splits >= 8 ? 8 : 1;
@@ -488,7 +475,7 @@ cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_str
   const int64_t blocks = (static_cast<int64_t>(T) * ((D + 3) / 4) + per - 1) / per;
 #define TGEMM_FINISH(OUT)                                                                                          \
   launch_chained(lanes == 8 ? finish_dh_kernel<OUT, 8> : finish_dh_kernel<OUT, 1>, blocks, kFinishThreads, stream, \
-                 acc, ld_acc, split_stride, splits, T, D, rows, static_cast<OUT*>(dH), lddh, wide)
+                 acc, ld_acc, split_stride, splits, T, D, rows, rule, static_cast<OUT*>(dH), lddh, wide)
   if (type == 0) return TGEMM_FINISH(__nv_bfloat16);
   if (type == 1) return TGEMM_FINISH(__half);
   return TGEMM_FINISH(float);
