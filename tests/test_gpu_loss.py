@@ -475,6 +475,36 @@ def test_few_rows_gradients_beside_nan(T, V, D, left, right, dtype):
     ref.distill(h, w, ids, logits, 2.0, g).check(**distill_both(h, w, ids, logits, g, temperature=2.0))
 
 
+@pytest.mark.parametrize("T", [7, 9, 16, 17, 31, 32])
+@pytest.mark.parametrize("V,D,left,right", [(16384, 64, 0, 0), (16641, 37, 3, 2), (20000, 1, 0, 3), (17000, 130, 0, 2),
+                                            (300, 5300, 4, 0)])
+def test_tens_of_fp32_rows_beside_nan(T, V, D, left, right):
+    """Large vocabularies (and rows too long for shared memory), whole and in pieces; the rest of the matrix NaN."""
+    lib = H.tg()
+    gen = torch.Generator(device="cuda").manual_seed(T * 1000 + D)
+    whole = torch.full((V + 2, left + D + right), float("nan"), device="cuda")
+    w = whole[1:V + 1, left:left + D]
+    w.copy_(torch.randn(V, D, device="cuda", generator=gen) * (2.0 / math.sqrt(D)))
+    wide = torch.full((T, D + left), float("nan"), device="cuda")
+    h = wide[:, left:]
+    h.copy_(torch.randn(T, D, device="cuda", generator=gen))
+    y = targets_for(T, V, gen)
+    y[:3] = torch.tensor([V - 1, 0, 255], device="cuda").clamp(max=V - 1)
+    y[3] = -100
+    h[3] = float("inf")
+    for piece in (0, 768):
+        loss, lse = lib.linear_cross_entropy(h, w, y, label_smoothing=0.1, z_loss=1e-3, piece=piece)
+        finished()
+        ref.xent(h, w, y, smoothing=0.1, z_loss=1e-3).check(loss=loss, lse=lse)
+        assert float(loss[3]) == float(lse[3]) == 0
+    ids, logits = lists_for(T, V, 40, gen)
+    ids[3] = -1
+    ids[4, 1:4] = ids[4, 0]
+    loss, lse = lib.linear_distillation(h, w, ids, logits)
+    finished()
+    ref.distill(h, w, ids, logits).check(loss=loss, lse=lse)
+
+
 @pytest.mark.parametrize("dtype,code,T", [(BF16, 2, 2), (F16, 1, 1), (F32, 0, 5)], ids=["bf16", "f16", "f32"])
 @pytest.mark.parametrize("pad_w", [0, 1])
 @pytest.mark.parametrize("pad,offset", [(0, 0), (8, 0), (3, 0), (8, 1), (2, 2)])

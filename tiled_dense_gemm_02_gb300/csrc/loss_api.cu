@@ -93,6 +93,7 @@ struct Layout {
   int planes = 1;              // of H and W
   int dz_planes = 1;
   bool few = false;            // a few rows, on the CUDA cores
+  bool simt = false;           // forward of 9 to 32 fp32 rows, on the CUDA cores
   bool direct = false;         // H is read in place
   bool pack = false;           // W is copied to an aligned pitch or to planes, piece by piece
   int64_t piece = 0, pieces = 1;
@@ -130,11 +131,12 @@ void plan_dh(int64_t T, int64_t D, int64_t kb, int terms, Layout& l) {
 Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bool distill, const void* W, int64_t ldw,
                    int dtype, int64_t piece_opt) {
   Layout l;
-  l.few = few_rows(backward, T, D, dtype == TGEMM_F32, host_granule(W, ldw, dtype == TGEMM_F32 ? 4 : 2) == 16);
+  l.few = few_rows(backward, T, V, D, dtype == TGEMM_F32, host_granule(W, ldw, dtype == TGEMM_F32 ? 4 : 2) == 16);
   l.planes = dtype == TGEMM_F32 ? kPlanes : 1;
   l.dz_planes = l.planes > 1 ? l.planes : T <= kTwoPlaneRows ? 2 : 1;
   l.ldh = l.ldw_p = round_up(D, 8);
-  l.pack = !l.few && (l.planes > 1 || host_granule(W, ldw, 2) < 16);
+  l.simt = !backward && !l.few && l.planes > 1 && T <= kHeadSimtRows;
+  l.pack = !l.few && !l.simt && (l.planes > 1 || host_granule(W, ldw, 2) < 16);
   l.ld_acc = round_up(D, 4);
   const int64_t whole = round_up(V, kHeadTile);
   if (piece_opt > 0) {
@@ -183,7 +185,9 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
     l.acc = take(l.splits * T * l.ld_acc * 4);
   } else {
     l.tile_parts = l.planes == 1 && ceil_div(D, kTileK) <= kShortStages ? 2 : 1;
-    l.parts = l.few ? few_blocks(T, V) : ceil_div(V, kHeadTile) * l.tile_parts;
+    l.parts = l.few    ? few_blocks(T, V)
+              : l.simt ? ceil_div(V, head_simt_tile(T))
+                       : ceil_div(V, kHeadTile) * l.tile_parts;
     l.ms = take(l.parts * T * 8);
     l.dot = take(l.parts * T * 4);
   }
@@ -286,7 +290,7 @@ class Products {
     a_.K = static_cast<int>(c.K);
     a_.D = static_cast<int>(c.D);
     a_.bf16 = type_ == 0;  // fp32's planes are bf16
-    put_back_ = 1.0f + kStepLoss * static_cast<float>(ceil_div(c.D, 16));
+    if (!l.simt) put_back_ = 1.0f + kStepLoss * static_cast<float>(ceil_div(c.D, 16));
     a_.k2 = static_cast<float>(scale * put_back_ * kLog2e);
     a_.flat = flat;
     a_.target = c.distill ? nullptr : l.direct ? c.ids : rows.target;
@@ -369,6 +373,18 @@ class Products {
   }
 
   int logits() {
+    if (l_.simt) {
+      HeadSimtArgs s;
+      s.head = a_;
+      s.head.tile0 = static_cast<int>(v0_ / head_simt_tile(c_.T));
+      s.H = static_cast<const float*>(c_.H);
+      s.ldh = c_.ldh;
+      s.W = static_cast<const float*>(c_.W) + v0_ * c_.ldw;
+      s.ldw = c_.ldw;
+      const bool aligned = host_granule(s.W, s.ldw, 4) == 16 && host_granule(s.H, s.ldh, 4) == 16;
+      TGEMM_CUDA(launch_head_simt(s, aligned, c_.stream), "logits launch");
+      return TGEMM_OK;
+    }
     CUtensorMap mh, mw, mz;
     TGEMM_TRY(map_hidden(&mh, kTileK, kTileM));
     TGEMM_TRY(map_weight(&mw, kTileK, kTileM));
@@ -474,7 +490,7 @@ int run_loss(const Call& c) {
   // the gather drops the rows that do not count and aligns the others: one tile
   // of aligned rows needs neither (its ignored rows touch no other row's sums)
   const int granule = host_granule(c.H, c.ldh, es);
-  l.direct = l.few || (!c.backward && l.planes == 1 && c.T <= kHeadTile && granule == 16);
+  l.direct = l.few || l.simt || (!c.backward && l.planes == 1 && c.T <= kHeadTile && granule == 16);
   char* ws = static_cast<char*>(c.workspace);
   GatherArgs g;
   std::memset(&g, 0, sizeof g);

@@ -28,8 +28,8 @@ cudaError_t launch_type(const FewArgs& a, int granule, int blocks, cudaStream_t 
 
 // Forward: as far as it is faster than the tensor cores (loss_few.cuh); backward:
 // the same (loss_few_grad.cu).
-bool few_rows(bool backward, int64_t T, int64_t D, bool f32, bool aligned) {
-  const int64_t most = backward ? (f32 ? kFewRows : aligned ? 2 : 1) : f32 ? kFewMost : aligned ? 1 : kFewRows;
+bool few_rows(bool backward, int64_t T, int64_t V, int64_t D, bool f32, bool aligned) {
+  const int64_t most = f32 ? (!backward && V < kFewSimtV ? kHeadSimtRows : kFewRows) : backward ? (aligned ? 2 : 1) : aligned ? 1 : kFewRows;
   return T <= most && rows_held(T) * (D + 8) * 4 <= kFewSmem;
 }
 
@@ -40,12 +40,11 @@ int few_blocks(int64_t T, int64_t V) {
 }
 
 cudaError_t launch_few_stats(const FewArgs& args, int type, int granule, int blocks, cudaStream_t stream) {
-  // eight rows at a time; every group leaves its statistics in the same number of parts
-  const int es = type == 2 ? 4 : 2;
+  // eight rows at a time; every pass leaves its statistics in the same number of parts
   for (int t0 = 0; t0 < args.T; t0 += kFewRows) {
     FewArgs a = args;
     a.T = std::min(kFewRows, args.T - t0);
-    a.H = static_cast<const char*>(args.H) + t0 * args.ldh * es;
+    a.H = static_cast<const char*>(args.H) + t0 * args.ldh * (type == 2 ? 4 : 2);
     if (a.targets) a.targets += t0;
     if (a.ids) {
       a.ids += static_cast<int64_t>(t0) * a.K;

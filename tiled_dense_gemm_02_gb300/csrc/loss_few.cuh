@@ -1,23 +1,23 @@
 // Row statistics, and the logits' gradient, of the vocabulary-head losses for a
-// few rows on the CUDA cores: the scoring of single tokens, of up to eight where
-// rows of W are off the 16-byte grid, and of up to 32 in fp32; steps on one or
-// two tokens, and on up to eight in fp32 (loss_few_grad.cu).
+// few rows on the CUDA cores: the scoring of single tokens and of up to eight where
+// rows of W are off the 16-byte grid or fp32; steps on one or two tokens, and on up
+// to eight in fp32 (loss_few_grad.cu).
 //
-// The work is one pass over W (fp32: one per eight rows of H): 2 T V D
-// operations against V D elements read.  Each warp takes four entries of W at a
-// time, lane by lane in 16-byte pieces, multiplies them with the rows of H held
-// in shared memory as fp32 (exact for 16-bit inputs), and keeps the running
-// maximum and sum of a softmax for its entries; the warps share the vocabulary
-// evenly.  Nothing is copied first: rows off the 16-byte grid are read in words
-// of 4 or 2 bytes.  (Reading the aligned 16 bytes around a piece and shifting
-// between neighbouring lanes was slower: 236 us against 108 us for one row of
-// 65536 x 4100, since every piece then waits for its load before the next.)
+// The work is one pass over W: 2 T V D operations against V D elements read.  Each
+// warp takes four entries of W at a time, lane by lane in 16-byte pieces,
+// multiplies them with the rows of H held in shared memory as fp32 (exact for
+// 16-bit inputs), and keeps the running maximum and sum of a softmax for its
+// entries; the warps share the vocabulary evenly.  Nothing is copied first: rows
+// off the 16-byte grid are read in words of 4 or 2 bytes.  (Reading the aligned 16
+// bytes around a piece and shifting between neighbouring lanes was slower: 236 us
+// against 108 us for one row of 65536 x 4100, since every piece then waits for its
+// load before the next.)
 //
 // Bound by memory.  Against the tensor-core product (its tiles nearly empty, W
 // copied first if unaligned or fp32), 65536 x 4096: one bf16 row 94 us (5.7 TB/s)
 // to 100 us; aligned bf16 rows from two on are the product's (two rows 113 us);
-// eight rows at 4100 columns 192 to 329 us; eight fp32 rows 210 us (5.1 TB/s)
-// to 1262 us, which the product takes for any number up to 128.
+// eight rows at 4100 columns 192 to 329 us; eight fp32 rows 210 us (5.1 TB/s) to
+// 1000 us.
 #pragma once
 
 #include <cuda_bf16.h>

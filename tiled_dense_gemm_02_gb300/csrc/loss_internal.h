@@ -168,9 +168,22 @@ struct HeadLaunch {
 cudaError_t launch_head_both(int planes, const HeadLaunch& dh, int dh_pairs, const HeadLaunch& dw, int dw_pairs,
                              cudaStream_t stream);
 
+// ---------------------------------------------- 9 to 32 fp32 rows
+// STATS of rows read in place on the CUDA cores, one part per head_simt_tile(T) entries.
+struct HeadSimtArgs {
+  HeadArgs head;
+  const float* H;
+  int64_t ldh;
+  const float* W;  // the piece's first entry
+  int64_t ldw;
+};
+constexpr int64_t kHeadSimtRows = 32;
+int head_simt_tile(int64_t T);
+cudaError_t launch_head_simt(const HeadSimtArgs& args, bool aligned, cudaStream_t stream);
+
 // ------------------------------------------------------------- few rows
-// Statistics of a few rows of H, read in place, in one pass over W (per eight
-// rows) on the CUDA cores; few_blocks(T, V) parts.
+// Statistics of a few rows of H, read in place, in one pass over W on the CUDA
+// cores; few_blocks(T, V) parts.
 struct FewArgs {
   int T, V, D, K;
   const void* H;
@@ -193,11 +206,14 @@ struct FewArgs {
   float* dz;         // V x rows_held(T)
 };
 constexpr int kFewRows = 8;   // held in shared memory at a time
-constexpr int kFewMost = 32;  // fp32: in up to four passes
+// 9 to 32 fp32 rows take passes of eight over vocabularies below this, whose tiles
+// would leave most SMs idle.  Forward calls, passes and tiles: 4096 x 4096, 9 rows
+// 52 and 187 us, 32 rows 110 and 160 us; 16384 x 2048, 84 and 98, 148 and 86 us.
+constexpr int64_t kFewSimtV = 16384;
 constexpr int kFewSmem = 160 * 1024;
 constexpr int kFewSms = 152;
 // Whether these rows take it (`aligned`: W's rows on the 16-byte grid).
-bool few_rows(bool backward, int64_t T, int64_t D, bool f32, bool aligned);
+bool few_rows(bool backward, int64_t T, int64_t V, int64_t D, bool f32, bool aligned);
 int few_blocks(int64_t T, int64_t V);
 // Backward of a few rows: dz first, then dW and dH in one pass over W (each block
 // a share of the vocabulary and up to 256 16-byte pieces of the columns), dH as
