@@ -29,7 +29,7 @@ cudaError_t launch_type(const FewArgs& a, int granule, int blocks, cudaStream_t 
 // Forward: as far as it is faster than the tensor cores (loss_few.cuh); backward:
 // the same (loss_few_grad.cu).
 bool few_rows(bool backward, int64_t T, int64_t V, int64_t D, bool f32, bool aligned) {
-  const int64_t most = f32 ? (!backward && V < kFewSimtV ? kHeadSimtRows : kFewRows) : backward ? (aligned ? 2 : 1) : aligned ? 1 : kFewRows;
+  const int64_t most = f32 ? (!backward && V < kFewSimtV ? kHeadSimtRows : kFewRows) : backward ? (aligned ? 2 : 0) : aligned ? 1 : kFewRows;
   return T <= most && rows_held(T) * (D + 8) * 4 <= kFewSmem;
 }
 

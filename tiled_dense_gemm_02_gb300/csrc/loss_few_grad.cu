@@ -9,10 +9,10 @@
 // groups of warps take different entries; their sums join in order at the end.
 //
 // Against the tensor-core products, a backward call on 65536 x 4096: bf16 one row
-// 288 us (5.6 TB/s), two 339 to 352 us, from three on the products' (389); at 4100
-// columns, where dW leaves in words of 8 bytes or less, one row 551 to 714 us, two
-// the products' (903); fp32 one row 538 us (6.0 TB/s), four 618, eight 921 (the
-// sums' and dz's registers leave two blocks an SM) to 2112 us.
+// 317 to 353 us, two 334 to 353, from three on the products' (350 to 390 here); off
+// the 16-byte grid, where dW leaves in words of 8 bytes or less, the products' (at
+// 4100 columns one row 807 to 640 us); fp32 one row 540 us (6.0 TB/s), four 590,
+// eight 670 (held to 128 registers for two blocks an SM: 144 took 920) to 1783 us.
 #include "loss_few.cuh"
 
 namespace tgemm {
@@ -65,8 +65,26 @@ __device__ __forceinline__ void store_piece(E* row, int c0, int cols, const uint
   }
 }
 
+// The gradients of one entry's logits, or zeros.
+template <int TN>
+__device__ __forceinline__ void load_dz(float (&d)[TN], const float* src, bool in) {
+  if constexpr (TN >= 4) {
+#pragma unroll
+    for (int t = 0; t < TN; t += 4) {
+      const float4 x = in ? __ldcg(reinterpret_cast<const float4*>(src + t)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      d[t] = x.x;
+      d[t + 1] = x.y;
+      d[t + 2] = x.z;
+      d[t + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) d[t] = in ? __ldcg(src + t) : 0.0f;
+  }
+}
+
 template <typename E, int TN, bool ALIGNED>
-__global__ void __launch_bounds__(kGradThreads) few_grad_kernel(const FewGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, TN >= 4 ? 2 : 1) few_grad_kernel(const FewGradArgs a) {
   constexpr int N = lane_elems<E>();
   constexpr int G = ALIGNED ? 16 : static_cast<int>(sizeof(E));
   __shared__ float s_sum[kGradThreads * N];
@@ -104,8 +122,7 @@ __global__ void __launch_bounds__(kGradThreads) few_grad_kernel(const FewGradArg
         const bool in = v < hi;
         p[u] = in && on && a.acc ? load_piece<E, G>(static_cast<const E*>(a.W) + static_cast<int64_t>(v) * a.ldw, c, a.D)
                                  : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int t = 0; t < TN; ++t) d[u][t] = in ? __ldcg(a.dz + static_cast<int64_t>(v) * TN + t) : 0.0f;
+        load_dz<TN>(d[u], a.dz + static_cast<int64_t>(v) * TN, in);
       }
 #pragma unroll
       for (int u = 0; u < kGradUnroll; ++u) {
@@ -173,8 +190,8 @@ cudaError_t launch_both(const FewArgs& f, const FewGradArgs& g, int blocks, cuda
 
 template <typename E, bool ALIGNED>
 cudaError_t launch_rows(const FewArgs& f, const FewGradArgs& g, int blocks, cudaStream_t stream) {
-  if (f.T <= 1) return launch_both<E, 1, ALIGNED>(f, g, blocks, stream);
   if constexpr (sizeof(E) == 4 || ALIGNED) {
+    if (f.T <= 1) return launch_both<E, 1, ALIGNED>(f, g, blocks, stream);
     if (f.T <= 2) return launch_both<E, 2, ALIGNED>(f, g, blocks, stream);
   }
   if constexpr (sizeof(E) == 4) {
