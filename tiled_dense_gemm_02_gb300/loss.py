@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 
 from . import BF16, F16, F32, OK, TgemmError, library
 
@@ -209,10 +210,15 @@ def _gradients(torch, hidden, sizes, want_hidden, want_weight):
     return dh, dw, (dh.data_ptr() if want_hidden else 0, D, dw.data_ptr() if want_weight else 0, D)
 
 
-def _positive(name, value):
-    if not value > 0:
-        raise ValueError(f"{name} must be positive, got {value}")
-    return float(value)
+def _factor(name, value, invert=False):
+    """The logits' factor from ``value`` or, inverted, its reciprocal.  The library holds it in float32, where 0 stands
+    for the default: what rounds to 0 or to infinity there is refused."""
+    value = float(value)
+    factor = ctypes.c_float(1.0 / value if invert and value else value).value
+    if not (value > 0.0 and 0.0 < factor < math.inf):
+        raise ValueError(f"{name} must be positive{', its reciprocal' if invert else ''} within float32's range, "
+                         f"got {value}")
+    return factor
 
 
 @_on_stream
@@ -226,7 +232,7 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, scale=1.
     loss and lse 0.  ``lse`` is the log of the sum of exponentials, which the
     backward call takes.  Reduce as you like: ``loss.sum() / n``.
     """
-    options = (_positive("scale", scale), label_smoothing, z_loss, piece, ignore_index)
+    options = (_factor("scale", scale), label_smoothing, z_loss, piece, ignore_index)
     torch, device, sizes, code, matrices, options, workspace, need = _head(hidden, weight, False, 0, options, workspace)
     targets = _vector("targets", targets, sizes[0], torch.int64, device)
     loss, lse = _losses(torch, sizes[0], hidden.device)
@@ -243,7 +249,7 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, *, ig
     """Gradients ``(d_hidden, d_weight)`` of ``sum(grad_loss * loss)`` in the
     operands' type; ``lse`` from the forward call with the same options,
     grad_loss [T] float32.  An unwanted gradient is not computed (None)."""
-    options = (_positive("scale", scale), label_smoothing, z_loss, piece, ignore_index)
+    options = (_factor("scale", scale), label_smoothing, z_loss, piece, ignore_index)
     torch, device, sizes, code, matrices, options, workspace, need = _head(hidden, weight, True, 0, options, workspace)
     targets = _vector("targets", targets, sizes[0], torch.int64, device)
     lse = _vector("lse", lse, sizes[0], torch.float32, device)
@@ -262,8 +268,7 @@ def _teacher(hidden, weight, backward, ids, logits, temperature, piece, workspac
     rows, K = ids.shape
     if K < 1:
         raise ValueError("the teacher's lists must have at least one place")
-    head = _head(hidden, weight, backward, K, (1.0 / _positive("temperature", temperature), 0.0, 0.0, piece, 0),
-                 workspace)
+    head = _head(hidden, weight, backward, K, (_factor("temperature", temperature, True), 0.0, 0.0, piece, 0), workspace)
     torch, device, sizes = head[:3]
     if rows != sizes[0] or ids.dtype != torch.int64:
         raise ValueError(f"teacher_ids must be [{sizes[0]}, K] int64, got {tuple(ids.shape)} {ids.dtype}")
