@@ -43,3 +43,42 @@ def test_scales_that_fp32_holds_reach_the_device_check(tg):
             tg.linear_cross_entropy(h, w, y, scale=scale)
         with pytest.raises(ValueError, match="CUDA device"):
             tg.linear_distillation(h, w, ids, logits, temperature=1 / scale)
+
+
+def test_options_held_in_tensors_are_read_at_every_call(tg):
+    """A weight kept in a tensor and changed in place (a schedule) is the value that the next call uses."""
+    import torch
+    from tiled_dense_gemm_02_gb300 import loss
+    z, eps, scale = torch.tensor(1e-4), torch.tensor(0.0), torch.tensor(2.0)
+    first = loss._options(*loss._plain(scale, eps, z, 0, -100))._obj
+    z.fill_(0.5)
+    eps.fill_(0.25)
+    scale.fill_(4.0)
+    then = loss._options(*loss._plain(scale, eps, z, 0, -100))._obj
+    assert (first.scale, first.label_smoothing, first.z_loss) == (2.0, 0.0, pytest.approx(1e-4))
+    assert (then.scale, then.label_smoothing, then.z_loss) == (4.0, 0.25, 0.5)
+
+
+def test_tensor_functions_pass_options_as_plain_numbers(tg, monkeypatch):
+    import torch
+    from tiled_dense_gemm_02_gb300 import loss
+    seen = []
+
+    def options(*values):
+        seen.append(values)
+        raise KeyError  # far enough
+
+    monkeypatch.setattr(loss, "_options", options)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    h, w, y, ids, logits, g = on_no_device()
+    more = {"label_smoothing": torch.tensor(0.25), "z_loss": torch.tensor(0.5), "scale": torch.tensor(2.0),
+            "ignore_index": torch.tensor(7), "piece": torch.tensor(256)}
+    for call in (lambda: tg.linear_cross_entropy(h, w, y, **more),
+                 lambda: tg.linear_cross_entropy_backward(h, w, y, g, g, **more),
+                 lambda: tg.linear_distillation(h, w, ids, logits, temperature=torch.tensor(0.5),
+                                                piece=torch.tensor(256))):
+        with pytest.raises(KeyError):
+            call()
+    assert seen[0] == seen[1] == (2.0, 0.25, 0.5, 256, 7) and seen[2] == (2.0, 0.0, 0.0, 256, 0)
+    for values in seen:
+        assert [type(v) for v in values] == [float, float, float, int, int]

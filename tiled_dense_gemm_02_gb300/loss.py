@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+from operator import index
 
 from . import BF16, F16, F32, OK, TgemmError, library
 
@@ -221,6 +222,11 @@ def _factor(name, value, invert=False):
     return factor
 
 
+def _plain(scale, label_smoothing, z_loss, piece, ignore_index):
+    """The options as plain numbers, read now: the cache of ``_options`` goes by value, a tensor's key is its identity."""
+    return _factor("scale", scale), float(label_smoothing), float(z_loss), index(piece), index(ignore_index)
+
+
 @_on_stream
 def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, scale=1.0, label_smoothing=0.0, z_loss=0.0,
                          piece=0, workspace=None):
@@ -232,7 +238,7 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, scale=1.
     loss and lse 0.  ``lse`` is the log of the sum of exponentials, which the
     backward call takes.  Reduce as you like: ``loss.sum() / n``.
     """
-    options = (_factor("scale", scale), label_smoothing, z_loss, piece, ignore_index)
+    options = _plain(scale, label_smoothing, z_loss, piece, ignore_index)
     torch, device, sizes, code, matrices, options, workspace, need = _head(hidden, weight, False, 0, options, workspace)
     targets = _vector("targets", targets, sizes[0], torch.int64, device)
     loss, lse = _losses(torch, sizes[0], hidden.device)
@@ -249,7 +255,7 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, *, ig
     """Gradients ``(d_hidden, d_weight)`` of ``sum(grad_loss * loss)`` in the
     operands' type; ``lse`` from the forward call with the same options,
     grad_loss [T] float32.  An unwanted gradient is not computed (None)."""
-    options = (_factor("scale", scale), label_smoothing, z_loss, piece, ignore_index)
+    options = _plain(scale, label_smoothing, z_loss, piece, ignore_index)
     torch, device, sizes, code, matrices, options, workspace, need = _head(hidden, weight, True, 0, options, workspace)
     targets = _vector("targets", targets, sizes[0], torch.int64, device)
     lse = _vector("lse", lse, sizes[0], torch.float32, device)
@@ -268,7 +274,8 @@ def _teacher(hidden, weight, backward, ids, logits, temperature, piece, workspac
     rows, K = ids.shape
     if K < 1:
         raise ValueError("the teacher's lists must have at least one place")
-    head = _head(hidden, weight, backward, K, (_factor("temperature", temperature, True), 0.0, 0.0, piece, 0), workspace)
+    head = _head(hidden, weight, backward, K, (_factor("temperature", temperature, True), 0.0, 0.0, index(piece), 0),
+                 workspace)
     torch, device, sizes = head[:3]
     if rows != sizes[0] or ids.dtype != torch.int64:
         raise ValueError(f"teacher_ids must be [{sizes[0]}, K] int64, got {tuple(ids.shape)} {ids.dtype}")
