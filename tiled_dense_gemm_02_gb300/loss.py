@@ -227,6 +227,44 @@ def _plain(scale, label_smoothing, z_loss, piece, ignore_index):
     return _factor("scale", scale), float(label_smoothing), float(z_loss), index(piece), index(ignore_index)
 
 
+@functools.cache
+def _graph_node():
+    """The torch function that records a loss: what a loss of tensors that require a gradient goes through."""
+    import torch
+
+    class HeadLoss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, hidden, weight, forward, backward, lists, more, workspace):
+            ctx.set_materialize_grads(False)
+            loss, lse = forward(hidden, weight, *lists, workspace=workspace, **more)
+            ctx.save_for_backward(hidden, weight, lse, *lists)
+            ctx.call = backward, more
+            return loss, lse
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_loss, grad_lse):
+            if grad_lse is not None:
+                raise RuntimeError("lse has no gradient of its own (z_loss weighs its square): detach it")
+            d_hidden = d_weight = None
+            if grad_loss is not None:
+                hidden, weight, lse, *lists = ctx.saved_tensors
+                backward, more = ctx.call
+                d_hidden, d_weight = backward(hidden, weight, *lists, lse, grad_loss, want_hidden=ctx.needs_input_grad[0],
+                                              want_weight=ctx.needs_input_grad[1], **more)
+            return d_hidden, d_weight, None, None, None, None, None
+
+    return HeadLoss
+
+
+def _recorded(hidden, weight):
+    """Whether a loss of these tensors belongs to torch's graph."""
+    if not (hidden.requires_grad or weight.requires_grad):
+        return False
+    import torch
+    return torch.is_grad_enabled()
+
+
 @_on_stream
 def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, scale=1.0, label_smoothing=0.0, z_loss=0.0,
                          piece=0, workspace=None):
@@ -237,8 +275,15 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, scale=1.
     row stride), targets [T] int64.  Rows whose target is ``ignore_index`` get
     loss and lse 0.  ``lse`` is the log of the sum of exponentials, which the
     backward call takes.  Reduce as you like: ``loss.sum() / n``.
+
+    If hidden or weight requires a gradient, so does ``loss``, and torch's
+    backward pass makes the backward call; ``lse`` has no gradient of its own.
     """
     options = _plain(scale, label_smoothing, z_loss, piece, ignore_index)
+    if _recorded(hidden, weight):
+        more = dict(zip(("scale", "label_smoothing", "z_loss", "piece", "ignore_index"), options))
+        return _graph_node().apply(hidden, weight, linear_cross_entropy, linear_cross_entropy_backward, (targets,),
+                                   more, workspace)
     torch, device, sizes, code, matrices, options, workspace, need = _head(hidden, weight, False, 0, options, workspace)
     targets = _vector("targets", targets, sizes[0], torch.int64, device)
     loss, lse = _losses(torch, sizes[0], hidden.device)
@@ -254,7 +299,8 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, *, ig
                                   workspace=None):
     """Gradients ``(d_hidden, d_weight)`` of ``sum(grad_loss * loss)`` in the
     operands' type; ``lse`` from the forward call with the same options,
-    grad_loss [T] float32.  An unwanted gradient is not computed (None)."""
+    grad_loss [T] float32.  An unwanted gradient is not computed (None).  What
+    it returns is outside torch's graph."""
     options = _plain(scale, label_smoothing, z_loss, piece, ignore_index)
     torch, device, sizes, code, matrices, options, workspace, need = _head(hidden, weight, True, 0, options, workspace)
     targets = _vector("targets", targets, sizes[0], torch.int64, device)
@@ -296,7 +342,18 @@ def linear_distillation(hidden, weight, teacher_ids, teacher_logits, *, temperat
     teacher_ids [T, K] int64 (below 0: unused place), teacher_logits [T, K] in
     any float type, K up to 256.  A row without a used place gets loss and lse
     0.  The losses are not multiplied by temperature squared.
+
+    Gradients of hidden and weight through torch as in linear_cross_entropy;
+    teacher_logits have none and must not require one.
     """
+    if teacher_logits.requires_grad:
+        import torch
+        if torch.is_grad_enabled():
+            raise ValueError("teacher_logits get no gradient: detach them")
+    if _recorded(hidden, weight):
+        return _graph_node().apply(hidden, weight, linear_distillation, linear_distillation_backward,
+                                   (teacher_ids, teacher_logits),
+                                   {"temperature": float(temperature), "piece": index(piece)}, workspace)
     head, logits, lists = _teacher(hidden, weight, False, teacher_ids, teacher_logits, temperature, piece, workspace)
     torch, device, sizes, code, matrices, options, workspace, need = head
     loss, lse = _losses(torch, sizes[0], hidden.device)
