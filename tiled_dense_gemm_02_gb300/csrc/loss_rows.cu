@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kListWarps * 32)
     if (v >= 0) {
       bad |= v >= V;
       id[j] = v >= V ? INT_MAX : static_cast<int>(v);
-      y[j] = logits[t * ld_logits + k] * scale;
+      y[j] = logits[t * ld_logits + k];
       some |= !(y[j] == -INFINITY);
       top = fmaxf(top, y[j]);
     }
@@ -87,10 +87,14 @@ __global__ void __launch_bounds__(kListWarps * 32)
   bad = __any_sync(0xffffffffu, bad);
   some = __any_sync(0xffffffffu, some);
   top = warp_max(top);
+  // scaled after the maximum is taken off: a multiple of the type's lowest or
+  // largest value would leave fp32's range
   float e[PER], total = 0.0f;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    e[j] = y[j] == -INFINITY ? 0.0f : expf(y[j] - top);
+    const bool none = y[j] == -INFINITY;
+    y[j] = (y[j] - top) * scale;
+    e[j] = none ? 0.0f : expf(y[j]);
     total += e[j];
   }
   total = warp_sum(total);
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(kListWarps * 32)
     const int k = lane + 32 * j;
     if (k >= K) continue;
     const float q = some ? e[j] / total : 0.0f;
-    own += q == 0.0f ? 0.0f : q * (y[j] - top - log_total);
+    own += q == 0.0f ? 0.0f : q * (y[j] - log_total);
     int rank = 0;
     for (int i = 0; i < K; ++i) {
       const int other = s_id[warp][i];
