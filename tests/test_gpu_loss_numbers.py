@@ -57,3 +57,31 @@ def test_teacher_logits_whose_multiples_leave_the_range(T, logits_dtype):
         dh, dw = lib.linear_distillation_backward(h, w, ids, logits, lse, g, temperature=temperature)
         finished()
         ref.distill(h, w, ids, logits, temperature, g).check(loss=loss, lse=lse, dh=dh, dw=dw)
+
+
+def masked_head(T, V, D, dtype, seed):
+    """A column of ones in H against one of 0 and -inf in W: every third entry, target aside, is masked out.
+    Returns H, W, the targets, and W and the targets with the masked entries left out."""
+    h, w, gen = head(T, V, D, dtype, seed)
+    h[:, D - 1] = 1.0
+    keep = torch.arange(V, device="cuda") % 3 != 1
+    w[:, D - 1] = 0.0
+    w[~keep, D - 1] = float("-inf")
+    kept = torch.nonzero(keep)[:, 0]
+    at = torch.randint(0, kept.numel(), (T,), device="cuda", generator=gen)
+    return h, w, kept[at], w[keep], at
+
+
+@pytest.mark.parametrize("T,V,D,dtype", [(1, 1000, 64, BF16), (1, 777, 37, F16), (3, 777, 41, BF16), (8, 900, 50, F16),
+                                         (5, 900, 64, F32), (16, 16384, 40, F32), (16, 900, 40, F32), (64, 900, 128, BF16),
+                                         (300, 2000, 600, F16)])
+def test_entries_masked_by_an_infinite_logit(T, V, D, dtype):
+    lib = H.tg()
+    h, w, y, w_kept, y_kept = masked_head(T, V, D, dtype, T + V)
+    loss, lse = lib.linear_cross_entropy(h, w, y)
+    finished()
+    ref.xent(h, w_kept, y_kept).check(loss=loss, lse=lse)
+    ids, logits = y[:, None].expand(T, 2).contiguous(), torch.randn(T, 2, device="cuda")
+    loss, lse = lib.linear_distillation(h, w, ids, logits)
+    finished()
+    ref.distill(h, w_kept, y_kept[:, None].expand(T, 2).contiguous(), logits).check(loss=loss, lse=lse)

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(few_threads(TN), few_per_sm(TN)) few_logits_ke
     }
   }
   if constexpr (GRAD) return;
-  dot = fmaf(a.flat, zs, dot);
+  if (a.flat != 0.0f) dot = fmaf(a.flat, zs, dot);  // 0 times the sum of an infinite logit is no number
   // the warp's entries of one row, then the block's warps, in fixed order
   if (!owner) {
     m = -INFINITY;
