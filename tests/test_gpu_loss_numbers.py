@@ -85,3 +85,20 @@ def test_entries_masked_by_an_infinite_logit(T, V, D, dtype):
     loss, lse = lib.linear_distillation(h, w, ids, logits)
     finished()
     ref.distill(h, w_kept, y_kept[:, None].expand(T, 2).contiguous(), logits).check(loss=loss, lse=lse)
+
+
+@pytest.mark.parametrize("T,V,D,dtype", [(1, 1000, 64, BF16), (2, 777, 40, F16), (3, 777, 41, BF16), (5, 900, 64, F32),
+                                         (16, 16384, 40, F32), (33, 900, 40, F32), (64, 900, 128, BF16),
+                                         (300, 2000, 600, F16), (300, 1000, 70, F32)])
+def test_entries_masked_by_the_lowest_value(T, V, D, dtype):
+    """The type's lowest value, which no sum of logits moves: no mass, no gradient, and none of it in the others'."""
+    lib = H.tg()
+    h, w, y, w_kept, y_kept = masked_head(T, V, D, dtype, T + V)
+    masked = torch.isinf(w[:, D - 1])
+    w[masked, D - 1] = torch.finfo(dtype).min
+    g = torch.rand(T, device="cuda")
+    loss, lse = lib.linear_cross_entropy(h, w, y)
+    dh, dw = lib.linear_cross_entropy_backward(h, w, y, lse, g)
+    finished()
+    assert bool((dw[masked] == 0).all())
+    ref.xent(h, w_kept, y_kept, g=g).check(loss=loss, lse=lse, dh=dh, dw=dw[~masked])

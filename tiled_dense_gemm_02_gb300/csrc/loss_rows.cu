@@ -160,6 +160,12 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, int64_t pitch, const uin
   }
 }
 
+// A finite value past bf16's largest would round to infinity.
+__device__ __forceinline__ float within_bf16(float x) {
+  constexpr float most = 3.38953139e38f;  // (2 - 2^-7) 2^127
+  return fabsf(x) < INFINITY ? fminf(fmaxf(x, -most), most) : x;
+}
+
 // An fp32 row as three bf16 planes.  A value that is not finite goes to the
 // first plane alone.  `lanes` threads, four elements each; the planes' pitch is a
 // multiple of 8, so whole groups are written.
@@ -184,7 +190,7 @@ __device__ __forceinline__ void split_row(uint16_t* dst, int64_t plane, const fl
       uint32_t w[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(within_bf16(x[2 * i]), within_bf16(x[2 * i + 1]));
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
         const float lo = __low2float(b), hi = __high2float(b);
         x[2 * i] = isfinite(lo) ? x[2 * i] - lo : 0.0f;
