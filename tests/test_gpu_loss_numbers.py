@@ -102,3 +102,32 @@ def test_entries_masked_by_the_lowest_value(T, V, D, dtype):
     finished()
     assert bool((dw[masked] == 0).all())
     ref.xent(h, w_kept, y_kept, g=g).check(loss=loss, lse=lse, dh=dh, dw=dw[~masked])
+
+
+@pytest.mark.parametrize("T", [5, 20, 200])
+@pytest.mark.parametrize("kind", ["xent", "distill"])
+def test_fp16_rows_of_small_weight_beside_large_ones(kind, T):
+    """A flat softmax over a large vocabulary whose weights share a mean: the softmax's part of dH is a sum of V equal
+    terms, so a probability that falls out of fp16's range is seen whole."""
+    lib = H.tg()
+    V, D = 100000, 64
+    h, w, gen = head(T, V, D, F16, spread=0.5)
+    h *= 0.125
+    w += torch.randn(D, device="cuda", generator=gen).to(F16)
+    y = torch.randint(0, V, (T,), device="cuda", generator=gen)
+    sizes = torch.tensor([1.0, 1e-1, 1e-2, 1e-3, 1e-4, 1e-5, 1e-6, 3e-7], device="cuda")
+    g = 2000.0 * sizes[torch.arange(T, device="cuda") % 8] * (0.5 + 0.5 * torch.rand(T, device="cuda", generator=gen))
+    g[4] = -g[4]
+    if kind == "xent":
+        more = {"label_smoothing": 0.1, "z_loss": 1e-3}
+        loss, lse = lib.linear_cross_entropy(h, w, y, **more)
+        dh, dw = lib.linear_cross_entropy_backward(h, w, y, lse, g, **more)
+        r = ref.xent(h, w, y, smoothing=0.1, z_loss=1e-3, g=g)
+    else:
+        ids = torch.randint(0, V, (T, 7), device="cuda", generator=gen)
+        logits = torch.randn(T, 7, device="cuda", generator=gen)
+        loss, lse = lib.linear_distillation(h, w, ids, logits)
+        dh, dw = lib.linear_distillation_backward(h, w, ids, logits, lse, g)
+        r = ref.distill(h, w, ids, logits, 1.0, g)
+    finished()
+    r.check(loss=loss, lse=lse, dh=dh, dw=dw)

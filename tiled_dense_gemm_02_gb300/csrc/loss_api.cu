@@ -92,6 +92,7 @@ struct Call {
 struct Layout {
   int planes = 1;              // of H and W
   int dz_planes = 1;
+  int z_planes = 1;            // planes of dz in memory: dz_planes, fp16 twice as many (kSpread)
   bool few = false;            // a few rows, on the CUDA cores
   bool simt = false;           // forward of 9 to 32 fp32 rows, on the CUDA cores
   bool direct = false;         // H is read in place
@@ -134,6 +135,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   l.few = few_rows(backward, T, V, D, dtype == TGEMM_F32, host_granule(W, ldw, dtype == TGEMM_F32 ? 4 : 2) == 16);
   l.planes = dtype == TGEMM_F32 ? kPlanes : 1;
   l.dz_planes = l.planes > 1 ? l.planes : T <= kTwoPlaneRows ? 2 : 1;
+  l.z_planes = l.dz_planes * (dtype == TGEMM_F16 ? 2 : 1);
   l.ldh = l.ldw_p = round_up(D, 8);
   l.simt = !backward && !l.few && l.planes > 1 && T <= kHeadSimtRows;
   l.pack = !l.few && !l.simt && (l.planes > 1 || host_granule(W, ldw, 2) < 16);
@@ -144,7 +146,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
   } else if (!backward && !l.pack) {
     l.piece = whole;
   } else {
-    const int64_t per = 2 * std::max<int64_t>(backward ? l.dz_planes * T : 0, l.pack ? l.planes * l.ldw_p : 0);  // bytes per entry
+    const int64_t per = 2 * std::max<int64_t>(backward ? l.z_planes * T : 0, l.pack ? l.planes * l.ldw_p : 0);  // bytes per entry
     const int64_t fit = std::max<int64_t>(2048, kPieceBytes / per / kHeadTile * kHeadTile);
     if (l.pack && T <= kHeadTile) {
       // one row of tiles: whole rounds of the grid, though the copy be larger (33
@@ -180,7 +182,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
     l.z = take(V * few_held(T) * 4);
     l.acc = take(l.splits * T * l.ld_acc * 4);
   } else if (backward) {
-    l.z = take(T * l.ldz * 2 * l.dz_planes);
+    l.z = take(T * l.ldz * 2 * l.z_planes);
     plan_dh(T, D, ceil_div(std::min(l.piece, V), kTileK), l.planes > 1 ? 6 : l.dz_planes, l);
     l.acc = take(l.splits * T * l.ld_acc * 4);
   } else {
@@ -301,6 +303,7 @@ class Products {
     a_.ms = reinterpret_cast<float2*>(ws + l.ms);
     a_.dot = reinterpret_cast<float*>(ws + l.dot);
     a_.coef = rows.coef;
+    a_.spread = rows.spread;
     a_.factor = rows.factor;
     a_.splits = 1;
     a_.parts = l.tile_parts;
@@ -358,7 +361,7 @@ class Products {
     return host_map_3d(m, type_, rows_.h, c_.D, c_.T, l_.planes, l_.ldh * 2, rows_.plane * 2, box_cols, box_rows);
   }
   int map_dz(CUtensorMap* m, uint32_t box_cols, uint32_t box_rows) {
-    return host_map_3d(m, type_, ws_ + l_.z, l_.ldz, c_.T, l_.dz_planes, l_.ldz * 2, c_.T * l_.ldz * 2, box_cols,
+    return host_map_3d(m, type_, ws_ + l_.z, l_.ldz, c_.T, l_.z_planes, l_.ldz * 2, c_.T * l_.ldz * 2, box_cols,
                        box_rows);
   }
 
@@ -511,7 +514,10 @@ int run_loss(const Call& c) {
     rows.own = reinterpret_cast<float*>(ws + l.own);
     rows.flags = reinterpret_cast<unsigned char*>(ws + l.flags);
   }
-  if (c.backward && !l.few) rows.coef = reinterpret_cast<float4*>(ws + l.coef);
+  if (c.backward && !l.few) {
+    rows.coef = reinterpret_cast<float4*>(ws + l.coef);
+    if (c.dtype == TGEMM_F16) rows.spread = rows.count + 2;
+  }
   g.T = static_cast<int>(c.T);
   g.D = static_cast<int>(c.D);
   g.es = es;

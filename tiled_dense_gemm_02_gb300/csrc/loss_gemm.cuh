@@ -356,10 +356,12 @@ __device__ __forceinline__ void store_words_plain(const uint32_t (&w)[32], uint1
   __syncwarp();
 }
 
+// dz of 32 rows, 64 columns at a time; `own`: a second time, times the row's own
+// scale k.w, to the planes after the first ones.
 template <int PLANES, int PARTS>
 __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int nb, int part, const float4& k,
-                                            Walk& walk, const HeadArgs& a, const CUtensorMap* mapC, uint8_t* buf,
-                                            int lane) {
+                                            Walk& walk, const HeadArgs& a, bool own, const CUtensorMap* mapC,
+                                            uint8_t* buf, int lane) {
   if (row0 >= a.T) return;
   const int c0 = part * (kHeadTile / 64 / PARTS), c1 = c0 + kHeadTile / 64 / PARTS;
   const int row = row0 + lane;
@@ -371,6 +373,7 @@ __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int
     if (c * 64 >= width) break;
     uint32_t w[32];
     if constexpr (PLANES == 1) {
+      uint32_t scaled[32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t d[32];
@@ -378,10 +381,14 @@ __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int
         ptx::tmem_wait_ld();
         gradient_chunk(d, first + c * 64 + h * 32, width - c * 64 - h * 32, k, a, walk);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)  // rows past the count: zeros, which the products read
-          w[16 * h + i] = row < n ? pack_pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]), fmt) : 0u;
+        for (int i = 0; i < 16; ++i) {  // rows past the count: zeros, which the products read
+          const float x = __uint_as_float(d[2 * i]), y = __uint_as_float(d[2 * i + 1]);
+          w[16 * h + i] = row < n ? pack_pair(x, y, fmt) : 0u;
+          scaled[16 * h + i] = row < n ? pack_pair(x * k.w, y * k.w, fmt) : 0u;
+        }
       }
       store_words(w, mapC, nb * kHeadTile + c * 64, row0, 0, buf, lane);
+      if (own) store_words(scaled, mapC, nb * kHeadTile + c * 64, row0, 1, buf, lane);
       continue;
     }
     uint32_t lo[32], hi[32];
@@ -395,25 +402,42 @@ __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int
 #pragma unroll
       for (int i = 0; i < 32; ++i) lo[i] = hi[i] = 0u;
     }
-    const int plane_fmt = PLANES == 3 ? OUT_BF16 : fmt;
+    if constexpr (PLANES == 2) {
+#pragma unroll 1
+      for (int p = 0; p < (own ? 4 : 2); ++p) {
+        const float scale = p >= 2 ? k.w : 1.0f;
 #pragma unroll
-    for (int p = 0; p < PLANES; ++p) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        uint32_t* v = i < 16 ? &lo[2 * i] : &hi[2 * i - 32];
-        const float x = __uint_as_float(v[0]), y = __uint_as_float(v[1]);
-        w[i] = pack_pair(x, y, plane_fmt);
-        if (p + 1 < PLANES) {  // what the plane leaves (0 where it is not finite)
-          float px = __uint_as_float(w[i] << 16), py = __uint_as_float(w[i] & 0xFFFF0000u);
-          if (PLANES == 2 && plane_fmt == OUT_F16) {
-            px = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] & 0xFFFFu)));
-            py = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] >> 16)));
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t* v = i < 16 ? &lo[2 * i] : &hi[2 * i - 32];
+          const float x = scale * __uint_as_float(v[0]), y = scale * __uint_as_float(v[1]);
+          w[i] = pack_pair(x, y, fmt);
+          if (p & 1) {  // what the first plane leaves (0 where it is not finite)
+            float px = __uint_as_float(w[i] << 16), py = __uint_as_float(w[i] & 0xFFFF0000u);
+            if (fmt == OUT_F16) {
+              px = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] & 0xFFFFu)));
+              py = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] >> 16)));
+            }
+            w[i] = pack_pair(isfinite(px) ? x - px : 0.0f, isfinite(py) ? y - py : 0.0f, fmt);
           }
-          v[0] = isfinite(px) ? __float_as_uint(x - px) : 0u;
-          v[1] = isfinite(py) ? __float_as_uint(y - py) : 0u;
         }
+        store_words(w, mapC, nb * kHeadTile + c * 64, row0, p, buf, lane);
       }
-      store_words(w, mapC, nb * kHeadTile + c * 64, row0, p, buf, lane);
+    } else {
+#pragma unroll
+      for (int p = 0; p < PLANES; ++p) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          uint32_t* v = i < 16 ? &lo[2 * i] : &hi[2 * i - 32];
+          const float x = __uint_as_float(v[0]), y = __uint_as_float(v[1]);
+          w[i] = pack_pair(x, y, OUT_BF16);
+          if (p + 1 < PLANES) {  // what the plane leaves (0 where it is not finite)
+            const float px = __uint_as_float(w[i] << 16), py = __uint_as_float(w[i] & 0xFFFF0000u);
+            v[0] = isfinite(px) ? __float_as_uint(x - px) : 0u;
+            v[1] = isfinite(py) ? __float_as_uint(y - py) : 0u;
+          }
+        }
+        store_words(w, mapC, nb * kHeadTile + c * 64, row0, p, buf, lane);
+      }
     }
   }
 }
@@ -579,6 +603,7 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
       int stage = 0;
       uint32_t phase = 0, filled = 0, last_parity = 0;
       bool ok = true;
+      const int first_plane = MODE == HEAD_DH && PLANES < 3 && args.spread && __ldcg(args.spread) ? PLANES : 0;
       for (int i = worker; ok && i < tiles.units; i += workers) {
         const HeadUnit u = head_unit<MODE>(args, tiles, i);
         const int m0 = u.mb * kHeadTile + cta * kTileM;
@@ -594,7 +619,7 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
             // of dz: stage by stage, so that the second finds W in L2
             const int term = TERMS == 6 ? it / span : it % TERMS;
             const int k0 = (lo + (TERMS == 6 ? it - term * span : it / TERMS)) * kTileK;  // past the k axis: zeros
-            const int pa = Plane::a(term), pb = Plane::b(term);
+            const int pa = first_plane + Plane::a(term), pb = Plane::b(term);
             const uint32_t fb_local = ptx::smem_u32(&full[stage]);
             const uint32_t fb = ptx::mapa_shared(fb_local, 0);
             if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2u * kStage);
@@ -687,6 +712,7 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
     const int part = (warp - 2) / 4;           // its part of the tile's columns
     uint8_t* buf = sC + (warp - 2) * 4096;
     const float factor = MODE == HEAD_DW ? __ldcg(args.factor) : 1.0f;
+    const bool own = MODE == HEAD_DZ && PLANES < 3 && args.spread && __ldcg(args.spread);
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -726,7 +752,7 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
           if constexpr (MODE == HEAD_STATS) {
             epilogue_stats<PARTS>(tbase, row0 + lane, n, u.nb, part, walk, args);
           } else if constexpr (MODE == HEAD_DZ) {
-            epilogue_dz<PLANES, PARTS>(tbase, row0, n, u.nb, part, k, walk, args, &mapC, buf, lane);
+            epilogue_dz<PLANES, PARTS>(tbase, row0, n, u.nb, part, k, walk, args, own, &mapC, buf, lane);
           } else if constexpr (PLANES < 3 && MODE == HEAD_DW) {
             epilogue_dw<PARTS>(tbase, row0, u.nb, part, factor, args, &mapC, buf, lane);
           } else {

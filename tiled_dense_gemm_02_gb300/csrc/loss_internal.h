@@ -41,7 +41,8 @@ struct HeadRows {
   float* q;           // T x K
   float* own;         // T: sum q log q (distillation), else null
   unsigned char* flags;  // T (distillation), else null
-  float4* coef;       // T, gathered: {c_p, c_q, lse * log2(e), 0} (backward), else null
+  float4* coef;       // T, gathered: {c_p, c_q, lse * log2(e), the row's own scale} (backward), else null
+  int* spread;        // whether rows have scales of their own (fp16, backward), else null
   void* h;            // gathered rows, pitch ldh 16-bit elements
   int64_t ldh;
   int64_t plane;      // elements between the planes of fp32 rows
@@ -51,6 +52,16 @@ struct HeadRows {
 // significant bits hold all 24 of x.  A product of two of them is then six
 // plane products (those of relative size 2^-24 and below are left out).
 constexpr int kPlanes = 3;
+
+// fp16 gradients of the logits: dW's product sums over the rows and needs one
+// scale for all of them, by which a row of small weight falls among fp16's
+// subnormal numbers: at 2^-20 of the largest gradient, a probability of 2^-17 has
+// three bits left.  The bits that dW loses are below its largest terms' last; dH's
+// rows, each a sum of its own, would lose them whole.  Where a row that counts is
+// below this part of the largest, DZ stores dz twice, the second time with each row
+// scaled to the top of the range, for DH, and the last step of dH takes the row's
+// scale back.  At 2^-6 and above probabilities of 2^-22 are still normal numbers.
+constexpr float kSpread = 1.0f / 64;
 
 constexpr unsigned char kRowIgnored = 0, kRowCounts = 1, kRowBad = 2;
 // Gathered rows are zero-filled up to a multiple of this (and at least one such block), capped at T.
@@ -88,7 +99,7 @@ cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream);
 // sum q z / scale.  Without gathered rows it also writes those that do not count.
 cudaError_t launch_combine(const float2* ms, const float* dot, int tiles, int T, float scale, float z_loss,
                            const HeadRows& rows, const RowRule& rule, float* loss, float* lse, cudaStream_t stream);
-// dH row t = factor * sum over splits of acc[s][place[t]], or 0.  Without
+// dH row t = factor / its own scale * sum over splits of acc[s][place[t]], or 0.  Without
 // gathered rows: of acc[s][t], factor 1.
 cudaError_t launch_finish_dh(const float* acc, int64_t ld_acc, int64_t split_stride, int splits, int T, int D,
                              const HeadRows& rows, const RowRule& rule, int type, void* dH, int64_t lddh,
@@ -129,6 +140,7 @@ struct HeadArgs {
   int tile0;      // STATS: index of the piece's first column tile
   int parts;      // STATS: parts of a tile's columns with statistics of their own, 1 or 2
   const float4* coef;     // DZ
+  const int* spread;      // DZ, DH: not null and not 0: dz is there a second time, for DH
   const float* factor;    // DW
   void* out;              // DW; fp32 DH
   int64_t ld_out;

@@ -209,13 +209,13 @@ __device__ __forceinline__ void split_row(uint16_t* dst, int64_t plane, const fl
 constexpr int kGatherThreads = 256;
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs a, int rows_per) {
   __shared__ int s_before[kGatherThreads / 32], s_total[kGatherThreads / 32], s_warp[kGatherThreads / 32];
-  __shared__ float s_g[kGatherThreads / 32], s_c[kGatherThreads / 32];
+  __shared__ float s_g[kGatherThreads / 32], s_c[kGatherThreads / 32], s_least[kGatherThreads / 32];
   __shared__ int s_src[kGatherThreads];
   chain();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = blockIdx.x * rows_per, t1 = min(a.T, t0 + rows_per);
   int before = 0, total = 0;
-  float gmax = 0.0f, cmax = 0.0f;
+  float gmax = 0.0f, cmax = 0.0f, least = INFINITY;  // least: the smallest row's larger coefficient
   // nothing in the loop waits for a row's flag, so the loads of several rows overlap
 #pragma unroll 8
   for (int t = tid; t < a.T; t += kGatherThreads) {
@@ -226,12 +226,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
       const float g = fabsf(a.grad[t]), c = a.z_loss == 0.0f ? g : fabsf(grad_p(a, t));
       gmax = counts && isfinite(g) ? fmaxf(gmax, g) : gmax;
       cmax = counts && isfinite(c) ? fmaxf(cmax, c) : cmax;
+      const float both = fmaxf(g, c);
+      least = counts && both > 0.0f ? fminf(least, both) : least;
     }
   }
   before = __reduce_add_sync(0xffffffffu, before);
   total = __reduce_add_sync(0xffffffffu, total);
   gmax = warp_max(gmax);
   cmax = warp_max(cmax);
+  least = -warp_max(-least);
   const int t = t0 + tid;
   const unsigned char flag = t < t1 ? row_flag(a.rule, t) : kRowIgnored;
   const unsigned ballot = __ballot_sync(0xffffffffu, flag == kRowCounts);
@@ -240,6 +243,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     s_total[warp] = total;
     s_g[warp] = gmax;
     s_c[warp] = cmax;
+    s_least[warp] = least;
     s_warp[warp] = __popc(ballot);
   }
   __syncthreads();
@@ -252,6 +256,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     total += s_total[w];
     gmax = fmaxf(gmax, s_g[w]);
     cmax = fmaxf(cmax, s_c[w]);
+    least = fminf(least, s_least[w]);
     if (w < warp) local += s_warp[w];
     mine += s_warp[w];
   }
@@ -264,8 +269,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     const float f = frexpf(cmax / unit, &e);
     pow2 = exp2f(static_cast<float>(min(f == 0.5f ? e - 1 : e, 60)));
   }
+  const bool spread = a.rows.spread && least < kSpread * (unit * pow2);
   if (blockIdx.x == 0 && tid == 0) {
     *a.rows.count = total;
+    if (a.rows.spread) *a.rows.spread = spread ? 1 : 0;
     if (a.grad) *a.rows.factor = unit * (a.scale * pow2 / a.range);
   }
   if (t < t1) {
@@ -278,7 +285,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
       s_src[place - before] = t;
       if (a.grad) {
         const float up = a.range / pow2;
-        a.rows.coef[place] = make_float4(grad_p(a, t) / unit * up, a.grad[t] / unit * up, a.lse[t] * kLog2e, 0.0f);
+        const float cp = grad_p(a, t) / unit * up, cq = a.grad[t] / unit * up;
+        float own = 1.0f;
+        const float size = fmaxf(fabsf(cp), fabsf(cq)) / a.range;  // of the row, at most 1
+        if (spread && size > 0.0f && isfinite(size)) {
+          int e;
+          frexpf(size, &e);
+          own = exp2f(static_cast<float>(min(max(-e, 0), 100)));
+        }
+        a.rows.coef[place] = make_float4(cp, cq, a.lse[t] * kLog2e, own);
       }
     } else if (a.loss_out) {
       a.loss_out[t] = a.lse_out[t] = row_value(flag);
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_dh_kernel(const float* 
   const int t = inside ? static_cast<int>(row) : 0;
   // without gathered rows a row's sums are in its own place
   const int place = !inside ? -1 : rows.place ? rows.place[t] : row_flag(rule, t) == kRowCounts ? t : -1;
-  const float f = rows.factor ? *rows.factor : 1.0f;
+  const float f = !rows.factor ? 1.0f : rows.spread && place >= 0 ? *rows.factor / rows.coef[place].w : *rows.factor;
   Out* out = dH + static_cast<int64_t>(t) * lddh + c;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (place >= 0) {
