@@ -258,19 +258,23 @@ __device__ __forceinline__ void store_segment(uint8_t* dst, const uint32_t (&w)[
   }
 }
 
-
 // Bounded wait that only records a timeout (teardown paths: no abort flag).
+// What it waits for is this CTA's own copies and MMAs in flight, which write
+// shared and tensor memory that is given back next, so a caller's short limit,
+// which may be what made the roles give up, does not cut it: they take
+// microseconds, the wait at least kTeardownNs.
+constexpr unsigned long long kTeardownNs = 100000000ull;
 __device__ __forceinline__ void wait_teardown(uint32_t bar, uint32_t parity, const Ctl& c, uint32_t site) {
   if (ptx::mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = ptx::globaltimer_ns();
+  const unsigned long long limit = c.timeout_ns > kTeardownNs ? c.timeout_ns : kTeardownNs;
   while (!ptx::mbar_try_wait(bar, parity)) {
-    if (ptx::globaltimer_ns() - t0 > c.timeout_ns) {
+    if (ptx::globaltimer_ns() - t0 > limit) {
       atomicCAS(c.status, 0u, kTimeoutFlag | site);
       return;
     }
   }
 }
-
 
 // ---------------------------------------------------------------- work units
 // A persistent worker (a CTA, or a CTA pair) processes a list of units: k-stages

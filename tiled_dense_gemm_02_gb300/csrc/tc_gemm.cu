@@ -143,19 +143,9 @@ __global__ void __launch_bounds__(tc_threads(kCopy), 1)
       // Every load this thread issued must land before shared memory is released.
       for (int s = 0; s < STAGES; ++s)
         if ((filled >> s) & 1u) {
-          const Ctl own{abort_flag, ctl.timeout_ns, ctl.status};
           // a fill that completed long ago returns at once; after an abort the
           // wait still runs (bounded) because the copies are real
-          uint32_t par = (last_parity >> s) & 1u;
-          if (!ptx::mbar_try_wait(ptx::smem_u32(&full_tma[s]), par)) {
-            const uint64_t t0 = ptx::globaltimer_ns();
-            while (!ptx::mbar_try_wait(ptx::smem_u32(&full_tma[s]), par)) {
-              if (ptx::globaltimer_ns() - t0 > own.timeout_ns) {
-                atomicCAS(own.status, 0u, kTimeoutFlag | SITE_TEARDOWN);
-                break;
-              }
-            }
-          }
+          wait_teardown(ptx::smem_u32(&full_tma[s]), (last_parity >> s) & 1u, ctl, SITE_TEARDOWN);
         }
     }
   } else if (warp == 1) {
@@ -205,16 +195,7 @@ __global__ void __launch_bounds__(tc_threads(kCopy), 1)
       }
       // All MMAs this thread issued have finished before tensor memory is freed.
       ptx::tc_commit(ptx::smem_u32(drain));
-      const Ctl own{abort_flag, ctl.timeout_ns, ctl.status};
-      if (!ptx::mbar_try_wait(ptx::smem_u32(drain), 0)) {
-        const uint64_t t0 = ptx::globaltimer_ns();
-        while (!ptx::mbar_try_wait(ptx::smem_u32(drain), 0)) {
-          if (ptx::globaltimer_ns() - t0 > own.timeout_ns) {
-            atomicCAS(own.status, 0u, kTimeoutFlag | SITE_DRAIN);
-            break;
-          }
-        }
-      }
+      wait_teardown(ptx::smem_u32(drain), 0, ctl, SITE_DRAIN);
     }
     __syncwarp();
   } else if (warp < 2 + kEpiWarps) {
