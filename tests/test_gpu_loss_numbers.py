@@ -131,3 +131,55 @@ def test_fp16_rows_of_small_weight_beside_large_ones(kind, T):
         r = ref.distill(h, w, ids, logits, 1.0, g)
     finished()
     r.check(loss=loss, lse=lse, dh=dh, dw=dw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("D", [512, 4096, 16384])
+def test_logits_whose_sums_are_exact(D, T, dtype):
+    """One-hot hidden states and weights of few bits: every partial sum is a number that fp32 holds, so nothing may move
+    a logit.  What is left are the roundings of the exponentials (2^-22 each, one way), of their sum and logarithm
+    and of the last sums: 2^-20 (1 + |lse|) in all, as in the tests' reference; a logit of 20 moved by 4e-6
+    of itself is four times that off."""
+    lib = H.tg()
+    V = 700
+    gen = torch.Generator(device="cuda").manual_seed(T + D)
+    h = torch.zeros(T, D, device="cuda", dtype=dtype)
+    at = torch.randint(0, D, (T,), device="cuda", generator=gen)
+    h[torch.arange(T, device="cuda"), at] = 16.0
+    w = torch.randint(-2, 3, (V, D), device="cuda", generator=gen).to(dtype) / 4
+    y = torch.randint(0, V, (T,), device="cuda", generator=gen)
+    w[y] += 0.75  # the targets' logits: up to 20
+    loss, lse = lib.linear_cross_entropy(h, w, y)
+    finished()
+    z = h.double() @ w.double().t()
+    want = torch.logsumexp(z, dim=1)
+    bound = 2.0 ** -20 * (1 + want.abs())
+    assert bool(((lse.double() - want).abs() <= bound).all())
+    exact = want - z.gather(1, y[:, None])[:, 0]
+    assert bool(((loss.double() - exact).abs() <= 2 * bound).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("D", [4096, 32768])
+def test_logits_of_products_of_one_sign(D, T, dtype):
+    """All products positive: the sums grow with every step, and so would the losses of an adder that truncates.  At most
+    64 steps of 16 products truncate one sum, each by less than 2^-23 of it, before it is added to the others with
+    rounding to nearest (2^-24 an addition, one for 1024 or fewer products): the bound does not grow with D but by these."""
+    lib = H.tg()
+    V = 600
+    gen = torch.Generator(device="cuda").manual_seed(T + D)
+    h = torch.rand(T, D, device="cuda", generator=gen).to(dtype)
+    w = (torch.rand(V, D, device="cuda", generator=gen) * (80.0 / D)).to(dtype)  # logits of about 20
+    y = torch.randint(0, V, (T,), device="cuda", generator=gen)
+    loss, lse = lib.linear_cross_entropy(h, w, y)
+    finished()
+    z = h.double() @ w.double().t()
+    want = torch.logsumexp(z, dim=1)
+    e_z = (64 * 2.0 ** -23 + D / 512 * 2.0 ** -24) * z.amax(dim=1)
+    bound = e_z + 2.0 ** -20 * (1 + want.abs())
+    assert bool(((lse.double() - want).abs() <= bound).all()), float(((lse.double() - want).abs() / bound).max())
+    # a common factor of all logits cancels in the loss but for their differences
+    exact = want - z.gather(1, y[:, None])[:, 0]
+    assert bool(((loss.double() - exact).abs() <= 2 * bound).all())

@@ -34,15 +34,21 @@ constexpr int kPlanPairs = 76;
 // the size of L2 run tens of rounds of tiles per product, so the rounds left
 // partly empty cost little; larger ones gain nothing.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
-// fp32: stages of the gradients' k axes (64 deep) summed in tensor memory
-// before they are added in fp32: the truncation of 64 steps stays below 1e-6,
-// and adding 256 KB per tile takes less time than the 96 stages of six plane
-// products that a chunk runs.
-constexpr int kChunkStages = 16;
+// Stages of a k axis (64 deep, four steps of the adder each) summed in tensor
+// memory before they are added in fp32 (loss_gemm.cuh).  Every step truncates, by
+// less than 2^-23 of the sum: 64 steps by less than 7.6e-6 however long the axis,
+// and by an eighth of that where the products' signs are mixed.  Logits of 16-bit
+// operands, 2048 x 131072 x 4096 forward, chunks of 8 / 16 / 24 / 32 / 64 stages:
+// 1326 / 1270 / 1210 / 1200 / 1176 us; error of lse (9.0), 300 x 4096 x 4096, by the
+// first four: 0.6 / 1.0 / 1.4 / 2.0 e-6, against a last bit of 0.95e-6.  fp32: half,
+// as gradients and logits are fp32 alike: 4 to 7 e-7 of their norm.  16-bit
+// gradients are left whole: a sum of 2^16 terms loses up to 6e-5 (mixed signs) of
+// itself, where its rounding to 8 or 11 bits may cost 2^-9 or 2^-12.
+constexpr int kLogitChunk = 16, kPlaneChunk = 8;
 // 16-bit forward calls: k-stages of a tile up to which its statistics, not its
-// product, bound the call, and eight epilogue warps (each with statistics of its
-// own) beat four.  Measured at 4096 x 32768: D = 64 75 -> 66 us, 256 79 -> 70 us
-// with eight; 512 104 -> 97 us, 1024 177 -> 168 us with four.
+// product, bound the call, and eight epilogue warps beat four.  Measured at 4096 x
+// 32768: D = 64 75 -> 64 us, 256 79 -> 70 us with eight; 512 104 -> 97 us, 1024 177 ->
+// 168 us with four.  (Several chunks take eight, for the registers.)
 constexpr int64_t kShortStages = 6;
 // 16-bit backward calls: rows up to which dz is kept in two planes.  Few rows
 // leave the rounding of dz nothing to average over: with 2 rows dH was up to 1.6
@@ -103,7 +109,7 @@ struct Layout {
   int64_t count = 0, source = 0, place = 0, target = 0, ids = 0, q = 0, own = 0, flags = 0, coef = 0, h = 0;
   int64_t ms = 0, dot = 0, z = 0, w = 0, acc = 0;
   int64_t parts = 0;           // statistics per row
-  int tile_parts = 1;          // of them per tile
+  int stats_warps = 1;         // STATS: epilogue warps per quarter of the rows
   int64_t total = 0;
 };
 
@@ -186,10 +192,11 @@ Layout plan_layout(bool backward, int64_t T, int64_t V, int64_t D, int64_t K, bo
     plan_dh(T, D, ceil_div(std::min(l.piece, V), kTileK), l.planes > 1 ? 6 : l.dz_planes, l);
     l.acc = take(l.splits * T * l.ld_acc * 4);
   } else {
-    l.tile_parts = l.planes == 1 && ceil_div(D, kTileK) <= kShortStages ? 2 : 1;
+    const int64_t k_blocks = ceil_div(D, kTileK);
+    l.stats_warps = k_blocks > kShortStages && k_blocks <= kLogitChunk ? 1 : 2;
     l.parts = l.few    ? few_blocks(T, V)
               : l.simt ? ceil_div(V, head_simt_tile(T))
-                       : ceil_div(V, kHeadTile) * l.tile_parts;
+                       : ceil_div(V, kHeadTile);
     l.ms = take(l.parts * T * 8);
     l.dot = take(l.parts * T * 4);
   }
@@ -292,8 +299,7 @@ class Products {
     a_.K = static_cast<int>(c.K);
     a_.D = static_cast<int>(c.D);
     a_.bf16 = type_ == 0;  // fp32's planes are bf16
-    if (!l.simt) put_back_ = 1.0f + kStepLoss * static_cast<float>(ceil_div(c.D, 16));
-    a_.k2 = static_cast<float>(scale * put_back_ * kLog2e);
+    a_.k2 = static_cast<float>(scale * kLog2e);
     a_.flat = flat;
     a_.target = c.distill ? nullptr : l.direct ? c.ids : rows.target;
     a_.mass = 1.0f - (c.opts ? c.opts->label_smoothing : 0.0f);
@@ -306,14 +312,12 @@ class Products {
     a_.spread = rows.spread;
     a_.factor = rows.factor;
     a_.splits = 1;
-    a_.parts = l.tile_parts;
-    a_.chunk = kChunkStages;
+    a_.parts = l.stats_warps;
+    a_.chunk = l.planes > 1 ? kPlaneChunk : kLogitChunk;
     const int to_us = (c.opts && c.opts->wait_timeout_us) ? c.opts->wait_timeout_us : 2000000;
     a_.timeout_ns = static_cast<unsigned long long>(to_us) * 1000ull;
     a_.status = status;
   }
-
-  float put_back() const { return put_back_; }
 
   int run() {
     for (int64_t i = 0; i < l_.pieces; ++i) {
@@ -429,13 +433,9 @@ class Products {
     b.k_blocks = static_cast<int>(ceil_div(n_, kTileK));
     b.splits = l_.splits;
     b.k_per_split = l_.k_per_split;
-    b.out = ws_ + l_.acc;
-    b.ld_out = l_.ld_acc;
-    b.split_stride = c_.T * l_.ld_acc;
-    b.store_granule = l_.planes > 1 && l_.k_per_split > kChunkStages ? 16 : 0;
     TGEMM_TRY(map_dz(&out.a, kTileK, kTileM));
     TGEMM_TRY(map_weight(&out.b, 64, kTileK));
-    return host_map_3d(&out.c, 2, b.out, c_.D, c_.T, l_.splits, l_.ld_acc * 4, c_.T * l_.ld_acc * 4, 32, 32);
+    return host_map_3d(&out.c, 2, ws_ + l_.acc, c_.D, c_.T, l_.splits, l_.ld_acc * 4, c_.T * l_.ld_acc * 4, 32, 32);
   }
 
   int weight_gradient(HeadLaunch& out) {
@@ -446,11 +446,11 @@ class Products {
     b.out_row0 = static_cast<int>(v0_);
     b.reduce = 0;
     const bool f32 = l_.planes > 1;
+    b.k_blocks = static_cast<int>(ceil_div(c_.T, kTileK));  // at most: the count is the device's
     b.store_granule = host_granule(c_.dW, c_.lddw, f32 ? 4 : 2);
     TGEMM_TRY(map_dz(&out.a, 64, kTileK));
     TGEMM_TRY(map_hidden(&out.b, 64, kTileK));
-    // fp32 sums of several chunks are added by their owners
-    if (b.store_granule == 16 && (!f32 || ceil_div(c_.T, kTileK) <= kChunkStages)) {
+    if (b.store_granule == 16) {
       b.store_granule = 0;
       return host_map_3d(&out.c, f32 ? 2 : type_, c_.dW, c_.D, c_.V, 1, c_.lddw * (f32 ? 4 : 2), 0, f32 ? 32 : 64, 32);
     }
@@ -464,7 +464,6 @@ class Products {
   char* ws_;
   int sms_, pairs_, type_;
   int64_t v0_ = 0, n_ = 0;  // this piece's first entry and width
-  float put_back_ = 1.0f;
   HeadArgs a_;
 };
 
@@ -543,7 +542,6 @@ int run_loss(const Call& c) {
   const int out_type = c.dtype == TGEMM_F32 ? 2 : c.dtype == TGEMM_F16 ? 1 : 0;
   float2* ms = reinterpret_cast<float2*>(ws + l.ms);
   float* dot = reinterpret_cast<float*>(ws + l.dot);
-  float put_back = 1.0f;
   if (l.few) {
     FewArgs f;
     std::memset(&f, 0, sizeof f);
@@ -597,10 +595,9 @@ int run_loss(const Call& c) {
     if (pairs < 1) return host_cuda_fail(cudaErrorLaunchOutOfResources, "CTA pairs");
     Products products(c, l, rows, ws, scale, flat, sms, pairs, status);
     TGEMM_TRY(products.run());
-    put_back = products.put_back();
   }
   if (!c.backward)
-    TGEMM_CUDA(launch_combine(ms, dot, static_cast<int>(l.parts), g.T, scale * put_back, z_loss, rows, g.rule, c.loss,
+    TGEMM_CUDA(launch_combine(ms, dot, static_cast<int>(l.parts), g.T, scale, z_loss, rows, g.rule, c.loss,
                               c.lse_out, c.stream),
                "combine launch");
   else if (c.dH)

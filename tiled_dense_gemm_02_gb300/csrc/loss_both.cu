@@ -13,9 +13,9 @@ __global__ void __launch_bounds__(head_threads(2), 1) head_both_kernel(const __g
                                                                        const int dh_pairs) {
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   if (pair < dh_pairs)
-    head_product<HEAD_DH, PLANES, 2>(dh.a, dh.b, dh.c, dh.args, pair, dh_pairs);
+    head_product<HEAD_DH, PLANES, 2, PLANES == 3>(dh.a, dh.b, dh.c, dh.args, pair, dh_pairs);
   else
-    head_product<HEAD_DW, PLANES, 2>(dw.a, dw.b, dw.c, dw.args, pair - dh_pairs, pairs - dh_pairs);
+    head_product<HEAD_DW, PLANES, 2, PLANES == 3>(dw.a, dw.b, dw.c, dw.args, pair - dh_pairs, pairs - dh_pairs);
 }
 
 template <int PLANES>

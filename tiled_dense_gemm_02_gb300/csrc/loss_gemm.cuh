@@ -14,12 +14,18 @@
 // and DZ; W as the N-major B of DH; dz as the M-major A and H as the N-major B
 // of DW: no operand is ever transposed in memory.
 //
+// The adder of tcgen05.mma truncates: every step (16 products added to the fp32
+// sum) moves the sum towards 0 by up to its last bit, so a long k axis would lose
+// D / 16 of them.  Sums leave tensor memory every `chunk` stages and are added
+// in registers with rounding to nearest, by the thread that owns the element,
+// under the next chunk's MMAs.  The last sum goes back to tensor memory, where
+// the epilogues read it.  (One factor for the mean loss, in its place, moved
+// sums that are exact, and covered a quarter of the loss of one sign's.)
+//
 // PLANES = 3: fp32 operands come as three bf16 planes (loss_rows.cu), and a
 // stage of the k axis is then six stages, one per pair of planes, the small
 // terms first: the last sixth alone adds to a sum of full size, so the adder's
-// truncation is that of a 16-bit product.  DH and DW, whose k axes are long,
-// move their sums out of tensor memory every `chunk` stages and add them in
-// fp32 with rounding to nearest, each element by the one thread that owns it.
+// truncation is that of a 16-bit product.
 // PLANES = 2: 16-bit operands, dz as two planes (its rounding and what that
 // leaves), so that few rows' gradients do not depend on how the one or two
 // entries that matter happen to round.
@@ -29,8 +35,8 @@
 //               columns of B; completion on the leader CTA's full barrier
 //   warp 1      tensor-memory allocation; MMA issue by one thread of the leader
 //   warps 2..   epilogue of this CTA's 128 rows, one row per thread: eight warps
-//               with half of the columns each; four for STATS with a long k
-//               axis, which hides them and wants the space for a seventh stage
+//               with half of the columns each, or four for STATS with one chunk
+//               of middle length (loss_api.cu)
 //
 // The number of gathered rows is known on the device only (rows that do not
 // count are not gathered), so every role derives the tile list from it.  Every
@@ -243,10 +249,37 @@ struct RowStats {
   }
 };
 
-// Statistics of this thread's row over its part of the tile's columns.
+// The sums of this thread's row and 128 columns: a first chunk's, one more
+// chunk's added, and the whole ones back in tensor memory.
+__device__ __forceinline__ void load_sums(uint32_t tcol, uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b) ptx::tmem_ld_32x32b_x16(tcol + b * 16, sum[b]);
+  ptx::tmem_wait_ld();
+}
+__device__ __forceinline__ void add_sums(uint32_t tcol, uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    uint32_t raw[16];
+    ptx::tmem_ld_32x32b_x16(tcol + b * 16, raw);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      sum[b][i] = __float_as_uint(__uint_as_float(sum[b][i]) + __uint_as_float(raw[i]));
+  }
+}
+__device__ __forceinline__ void store_sums(uint32_t tcol, const uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b) ptx::tmem_st_32x32b_x16(tcol + b * 16, sum[b]);
+  ptx::tmem_wait_st();
+}
+
+// Statistics of this thread's row over its part of the tile's columns.  Of two
+// parts the second leaves them in the accumulator's columns, which it has read,
+// and the first joins and writes both: `handed` is completed by the one and
+// awaited by the other.  False: the wait ran out.
 template <int PARTS>
-__device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, int nb, int part, Walk& walk,
-                                               const HeadArgs& a) {
+__device__ __forceinline__ bool epilogue_stats(uint32_t tbase, int row, int n, int nb, int part, Walk& walk,
+                                               const HeadArgs& a, uint32_t handed, uint32_t parity, const Ctl& ctl) {
   constexpr int CHUNKS = kHeadTile / 32 / PARTS;
   const int first = a.col0 + nb * kHeadTile;  // vocabulary entry of the tile's first column
   const int width = a.cols - nb * kHeadTile;
@@ -259,11 +292,32 @@ __device__ __forceinline__ void epilogue_stats(uint32_t tbase, int row, int n, i
     ptx::tmem_wait_ld();
     st.add(raw, first + c * 32, width - c * 32, walk, a);
   }
-  if (row < n) {
-    const int64_t at = (static_cast<int64_t>(a.tile0 + nb) * PARTS + part) * a.T + row;
-    a.ms[at] = make_float2(st.m * a.k2, st.s);
-    a.dot[at] = fmaf(a.flat, st.zs, st.dot);
+  float m = st.m * a.k2, s = st.s, dot = fmaf(a.flat, st.zs, st.dot);
+  if constexpr (PARTS == 2) {
+    uint32_t x[4] = {__float_as_uint(m), __float_as_uint(s), __float_as_uint(dot), 0u};
+    if (part == 1) {
+      ptx::tmem_st_32x32b_x4(tbase + kHeadTile / 2, x);
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (ptx::lane_id() == 0) ptx::mbar_arrive(handed);
+      return true;
+    }
+    if (!warp_wait(handed, parity, ctl, SITE_EPI_ACC_FULL)) return false;
+    ptx::tc_fence_after_sync();
+    ptx::tmem_ld_32x32b_x4(tbase + kHeadTile / 2, x);
+    ptx::tmem_wait_ld();
+    const float m2 = __uint_as_float(x[0]), top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
+    s = s * exp2_fast(m - ref) + __uint_as_float(x[1]) * exp2_fast(m2 - ref);
+    m = top;
+    dot += __uint_as_float(x[2]);
   }
+  if (row < n) {
+    const int64_t at = static_cast<int64_t>(a.tile0 + nb) * a.T + row;
+    a.ms[at] = make_float2(m, s);
+    a.dot[at] = dot;
+  }
+  return true;
 }
 
 // 32 logits of a row -> their gradient.
@@ -442,28 +496,10 @@ __device__ __forceinline__ void epilogue_dz(uint32_t tbase, int row0, int n, int
   }
 }
 
-// 32 fp32 values of a row: stored, or added to what is there.  The same thread
-// writes an element in every chunk, so the order of the additions is fixed.
-__device__ __forceinline__ void store_row_f32(float* dst, const float (&v)[32], int valid, bool vec, bool add) {
-  if (vec && valid >= 32) {
-    float4* d = reinterpret_cast<float4*>(dst);
-    float4 o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = add ? __ldcg(d + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      __stcg(d + i, make_float4(o[i].x + v[4 * i], o[i].y + v[4 * i + 1], o[i].z + v[4 * i + 2], o[i].w + v[4 * i + 3]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < valid) __stcg(dst + i, add ? __ldcg(dst + i) + v[i] : v[i]);
-  }
-}
-
-// fp32 DH and DW: one chunk's sums of this thread's row, times f.
+// fp32 DW whose rows are off the 16-byte grid: this thread's row, times f.
 template <int PARTS>
 __device__ __forceinline__ void epilogue_f32(uint32_t tbase, float* row, bool valid_row, int nb, int part, int cols,
-                                             float f, bool vec, bool add) {
+                                             float f) {
   const int c0 = part * (kHeadTile / 32 / PARTS), c1 = c0 + kHeadTile / 32 / PARTS;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
@@ -472,10 +508,9 @@ __device__ __forceinline__ void epilogue_f32(uint32_t tbase, float* row, bool va
     uint32_t w[32];
     ptx::tmem_ld_32x32b_x32(tbase + c * 32, w);
     ptx::tmem_wait_ld();
-    float v[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = f * __uint_as_float(w[i]);
-    if (valid_row) store_row_f32(row + col, v, cols - col, vec, add);
+    for (int i = 0; i < 32; ++i)
+      if (valid_row && col + i < cols) __stcg(row + col + i, f * __uint_as_float(w[i]));
   }
 }
 
@@ -533,8 +568,9 @@ __device__ __forceinline__ void epilogue_dw(uint32_t tbase, int row0, int nb, in
   }
 }
 
-// One product, by CTA pair `worker` of `workers`.
-template <int MODE, int PLANES, int PARTS>
+// One product, by CTA pair `worker` of `workers`.  CHUNKS: its k axis may be
+// longer than a chunk.
+template <int MODE, int PLANES, int PARTS, bool CHUNKS>
 __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
                                              const HeadArgs& args, const int worker, const int workers) {
   constexpr int STAGES = head_stages(MODE, PARTS);
@@ -551,9 +587,10 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* handed = acc_empty + 2;  // STATS: [unit & 1][quarter]
+  uint64_t* drain = handed + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  static_assert((2 * STAGES + 5) * 8 + 8 <= kBarrierBytes, "barrier area");
+  static_assert((2 * STAGES + 13) * 8 + 8 <= kBarrierBytes, "barrier area");
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const int warp = threadIdx.x >> 5;
@@ -570,6 +607,7 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
       ptx::mbar_init(ptx::smem_u32(&acc_full[b]), 1);
       ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * 4 * PARTS);
     }
+    for (int i = 0; i < 8; ++i) ptx::mbar_init(ptx::smem_u32(&handed[i]), 1);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0u;
     ptx::fence_barrier_init();
@@ -594,8 +632,11 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
   const Ctl ctl{abort_flag, args.timeout_ns, args.status};
   const int n = args.count ? min(*args.count, args.T) : args.T;
   const Tiles tiles = head_tiles<MODE>(args, max(1, n));
-  // stages summed in tensor memory at a time: all of a unit's, or a chunk
-  const int chunk = PLANES == 3 && (MODE == HEAD_DH || MODE == HEAD_DW) ? args.chunk : INT_MAX / 2;
+  // stages summed in tensor memory at a time: a unit's, in even parts of at most args.chunk
+  static_assert(!CHUNKS || PARTS == 2, "128 columns a thread");
+  const int stages_all = MODE == HEAD_DH ? min(args.k_per_split, tiles.k_blocks) : tiles.k_blocks;
+  const int chunks = (stages_all + args.chunk - 1) / args.chunk;
+  const int chunk = CHUNKS ? max(1, (stages_all + chunks - 1) / max(1, chunks)) : INT_MAX / 2;
 
   if (warp == 0) {
     // ------------------------------------------------ bulk-tensor producer
@@ -713,74 +754,110 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
     uint8_t* buf = sC + (warp - 2) * 4096;
     const float factor = MODE == HEAD_DW ? __ldcg(args.factor) : 1.0f;
     const bool own = MODE == HEAD_DZ && PLANES < 3 && args.spread && __ldcg(args.spread);
-    int acc = 0;
+    int acc = 0, done = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    // the next tile is found, and its rows' targets and coefficients loaded,
-    // while this one's products run: a short k axis would not hide it
-    HeadUnit u, next;
+    // the next accumulator, once its sums are complete
+    const auto taken = [&]() {
+      ok = warp_wait(ptx::smem_u32(&acc_full[acc]), acc_phase, ctl, SITE_EPI_ACC_FULL);
+      ptx::tc_fence_after_sync();
+      return tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * ACC);
+    };
+    // The accumulator's reads are complete (tcgen05.wait::ld).  The arrival
+    // orders nothing else: a releasing one would wait for this tile's global
+    // stores, 1500 cycles a tile.
+    const auto given_back = [&]() {
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    };
+    HeadUnit u;
     int64_t target = -1;
     float4 coef = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const auto look_ahead = [&](int i) {
-      if (i >= tiles.units) return;
-      next = head_unit<MODE>(args, tiles, i);
+    const auto look_up = [&](const HeadUnit& w) {
       if constexpr (MODE == HEAD_STATS || MODE == HEAD_DZ) {
-        const int row = next.mb * kHeadTile + cta * kTileM + quarter * 32 + lane;
+        const int row = w.mb * kHeadTile + cta * kTileM + quarter * 32 + lane;
         if (args.target) target = row < n ? __ldcg(args.target + row) : -1;
         if (MODE == HEAD_DZ) coef = row < n ? __ldcg(args.coef + row) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     };
-    look_ahead(worker);
+    // One chunk: the next tile is found, and its rows' targets and coefficients
+    // loaded, while this one's products run; a short k axis would not hide it.
+    // Several: they are found behind the last chunk, whose epilogue has the next
+    // tile's first chunk to run under, and no register is theirs beside the sums.
+    HeadUnit next;
+    const auto look_ahead = [&](int i) {
+      if (i >= tiles.units) return;
+      next = head_unit<MODE>(args, tiles, i);
+      look_up(next);
+    };
+    if constexpr (!CHUNKS) look_ahead(worker);
     for (int i = worker; ok && i < tiles.units; i += workers) {
-      u = next;
+      u = CHUNKS ? head_unit<MODE>(args, tiles, i) : next;
       const int row0 = u.mb * kHeadTile + cta * kTileM + quarter * 32;
       const int rows_end = MODE == HEAD_DW ? args.cols : MODE == HEAD_DZ ? args.T : n;
-      const float4 k = coef;
+      const int first = args.col0 + u.nb * kHeadTile + part * (kHeadTile / PARTS);
+      float4 k = coef;
       Walk walk;
-      if constexpr (MODE == HEAD_STATS || MODE == HEAD_DZ)
-        walk.start(args, row0 + lane, n, args.col0 + u.nb * kHeadTile + part * (kHeadTile / PARTS), target);
-      look_ahead(i + workers);
-      for (int lo = u.lo; lo < u.hi; lo += chunk) {
-        if (!warp_wait(ptx::smem_u32(&acc_full[acc]), acc_phase, ctl, SITE_EPI_ACC_FULL)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after_sync();
-        const uint32_t tbase =
-            tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * ACC);
-        if (row0 < rows_end) {
-          if constexpr (MODE == HEAD_STATS) {
-            epilogue_stats<PARTS>(tbase, row0 + lane, n, u.nb, part, walk, args);
-          } else if constexpr (MODE == HEAD_DZ) {
-            epilogue_dz<PLANES, PARTS>(tbase, row0, n, u.nb, part, k, walk, args, own, &mapC, buf, lane);
-          } else if constexpr (PLANES < 3 && MODE == HEAD_DW) {
-            epilogue_dw<PARTS>(tbase, row0, u.nb, part, factor, args, &mapC, buf, lane);
-          } else {
-            // fp32: a chunk's sum of the full-size terms took 4 steps a stage
-            const float f =
-                PLANES < 3 ? 1.0f : factor * (1.0f + kStepLoss * static_cast<float>(4 * min(chunk, u.hi - lo)));
-            // in bulk where a sum is moved once a launch, else by the thread that owns it
-            if (args.store_granule == 0) {
-              epilogue_sums<PARTS>(tbase, MODE == HEAD_DW ? args.out_row0 + row0 : row0, u.nb, u.split, part, args.D, f,
-                                   args.reduce, &mapC, buf, lane);
-            } else {
-              const int row = row0 + lane;
-              float* out = static_cast<float*>(args.out) + u.split * args.split_stride +
-                           static_cast<int64_t>(args.out_row0 + row) * args.ld_out;
-              epilogue_f32<PARTS>(tbase, out, row < rows_end, u.nb, part, args.D, f, args.store_granule == 16,
-                                  args.reduce || lo > u.lo);
+      uint32_t tbase;
+      if (u.lo >= u.hi) continue;
+      if constexpr (CHUNKS) {
+        int lo = u.lo + chunk;  // end of the chunk to come
+        tbase = taken();
+        if (lo < u.hi && row0 < rows_end) {
+          // every path to a use of the sums passes their first load: else they
+          // would be live, and registers short, in all of the epilogue
+          if (ok) {
+            uint32_t sum[8][16];
+            load_sums(tbase + part * (kHeadTile / 2), sum);
+            given_back();
+            for (lo += chunk;; lo += chunk) {
+              tbase = taken();
+              if (!ok) break;
+              add_sums(tbase + part * (kHeadTile / 2), sum);
+              if (lo >= u.hi) {
+                store_sums(tbase + part * (kHeadTile / 2), sum);
+                break;
+              }
+              given_back();
             }
           }
+        } else {
+          for (; ok && lo < u.hi; lo += chunk) {
+            given_back();
+            tbase = taken();
+          }
         }
-        // The accumulator's reads are complete (tcgen05.wait::ld).  The arrival
-        // orders nothing else: a releasing one would wait for this tile's
-        // global stores, 1500 cycles a tile.
-        ptx::tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        look_up(u);
+        k = coef;
+        if constexpr (MODE == HEAD_STATS || MODE == HEAD_DZ) walk.start(args, row0 + lane, n, first, target);
+      } else {
+        if constexpr (MODE == HEAD_STATS || MODE == HEAD_DZ) walk.start(args, row0 + lane, n, first, target);
+        look_ahead(i + workers);
+        tbase = taken();
       }
+      if (!ok) break;
+      if (row0 < rows_end) {
+        if constexpr (MODE == HEAD_STATS) {
+          ok = epilogue_stats<PARTS>(tbase, row0 + lane, n, u.nb, part, walk, args,
+                                     ptx::smem_u32(&handed[(done & 1) * 4 + quarter]), (done >> 1) & 1, ctl);
+          ++done;
+        } else if constexpr (MODE == HEAD_DZ) {
+          epilogue_dz<PLANES, PARTS>(tbase, row0, n, u.nb, part, k, walk, args, own, &mapC, buf, lane);
+        } else if constexpr (PLANES < 3 && MODE == HEAD_DW) {
+          epilogue_dw<PARTS>(tbase, row0, u.nb, part, factor, args, &mapC, buf, lane);
+        } else if (MODE == HEAD_DH || args.store_granule == 0) {
+          epilogue_sums<PARTS>(tbase, MODE == HEAD_DW ? args.out_row0 + row0 : row0, u.nb, u.split, part, args.D, factor,
+                               args.reduce, &mapC, buf, lane);
+        } else {
+          const int row = row0 + lane;
+          float* out = static_cast<float*>(args.out) + static_cast<int64_t>(args.out_row0 + row) * args.ld_out;
+          epilogue_f32<PARTS>(tbase, out, row < rows_end, u.nb, part, args.D, factor);
+        }
+      }
+      given_back();
     }
     if (lane == 0) ptx::bulk_wait_group_read<0>();
     __syncwarp();
@@ -795,11 +872,11 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
   }
 }
 
-template <int MODE, int PLANES, int PARTS>
+template <int MODE, int PLANES, int PARTS, bool CHUNKS>
 __global__ void __launch_bounds__(head_threads(PARTS), 1)
     head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ CUtensorMap mapC, const __grid_constant__ HeadArgs args) {
-  head_product<MODE, PLANES, PARTS>(mapA, mapB, mapC, args, blockIdx.x / 2, gridDim.x / 2);
+  head_product<MODE, PLANES, PARTS, CHUNKS>(mapA, mapB, mapC, args, blockIdx.x / 2, gridDim.x / 2);
 }
 
 // Launch of a kernel on `pairs` clusters of two CTAs, dependent on the kernel before it.
@@ -832,11 +909,11 @@ cudaError_t launch_pairs(void (*kernel)(Params...), int smem, int threads, std::
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int MODE, int PLANES, int PARTS>
+template <int MODE, int PLANES, int PARTS, bool CHUNKS>
 cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC, const HeadArgs& args,
                    int pairs, cudaStream_t stream) {
   static std::atomic<uint64_t> done_mask{0};
-  return launch_pairs(head_kernel<MODE, PLANES, PARTS>, head_smem(MODE, PARTS), head_threads(PARTS), done_mask, pairs,
+  return launch_pairs(head_kernel<MODE, PLANES, PARTS, CHUNKS>, head_smem(MODE, PARTS), head_threads(PARTS), done_mask, pairs,
                       stream, mA, mB, mC, args);
 }
 

@@ -123,9 +123,9 @@ struct HeadArgs {
   int cols;       // entries of this piece of the vocabulary
   int col0;       // vocabulary entry of the piece's column 0
   int b_row0;     // STATS, DZ, DH: row of the weight map for the piece's column 0
-  int k_blocks;   // 64-deep stages of the k axis (DW: from the count)
+  int k_blocks;   // 64-deep stages of the k axis (DW: were every row to count)
   int splits, k_per_split;  // DH: ranges of the k axis summed apart
-  int chunk;      // fp32, DH and DW: stages summed in tensor memory before they are added to the result
+  int chunk;      // stages of the k axis summed in tensor memory, at most, before they are added in fp32 (16-bit DH, DW: all)
   int reduce;     // DH: add to the sums instead of storing them
   int bf16;
   float k2;       // scale * log2(e)
@@ -138,27 +138,17 @@ struct HeadArgs {
   float2* ms;     // STATS
   float* dot;
   int tile0;      // STATS: index of the piece's first column tile
-  int parts;      // STATS: parts of a tile's columns with statistics of their own, 1 or 2
+  int parts;      // STATS: epilogue warps per quarter of a tile's rows, 1 or 2
   const float4* coef;     // DZ
   const int* spread;      // DZ, DH: not null and not 0: dz is there a second time, for DH
   const float* factor;    // DW
-  void* out;              // DW; fp32 DH
+  void* out;              // DW
   int64_t ld_out;
-  int64_t split_stride;   // fp32 DH: elements between the splits' sums
-  int store_granule;      // DH, DW: 0 bulk-tensor stores, else the granule of per-thread stores
+  int store_granule;      // DW: 0 bulk-tensor stores, else the granule of per-thread stores
   int out_row0;           // DW: row of dW for the piece's column 0
   unsigned long long timeout_ns;
   unsigned int* status;
 };
-
-// Mean loss of one tensor-memory accumulation step (a product of 16 terms
-// added to the fp32 sum), relative to the final sum.  The adder truncates, so
-// every step moves the sum towards 0 by a part of its last bit.  Measured
-// against 64-bit sums of signed data, the sums of K terms come out smaller by
-// K / 16 steps of 0.10 to 0.15 units of 2^-23 (bf16, K = 256 to 8192; 0.14 to
-// 0.15 for fp16): an eighth is put back, which takes lse at D = 4096 from
-// 1.2e-6 off to a few 1e-7.
-constexpr float kStepLoss = 1.0f / (1 << 26);
 
 // Output tile of every product: 256 x 256 per CTA pair.
 constexpr int kHeadTile = 256;

@@ -5,9 +5,12 @@ namespace tgemm {
 
 cudaError_t launch_head_stats(int planes, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapC,
                           const HeadArgs& args, int pairs, cudaStream_t stream) {
-  if (planes == 3) return launch<HEAD_STATS, 3, 1>(mapA, mapB, mapC, args, pairs, stream);
-  return args.parts == 2 ? launch<HEAD_STATS, 1, 2>(mapA, mapB, mapC, args, pairs, stream)
-                         : launch<HEAD_STATS, 1, 1>(mapA, mapB, mapC, args, pairs, stream);
+  const bool chunks = args.k_blocks > args.chunk;
+  if (planes == 3) return chunks ? launch<HEAD_STATS, 3, 2, true>(mapA, mapB, mapC, args, pairs, stream)
+                                 : launch<HEAD_STATS, 3, 1, false>(mapA, mapB, mapC, args, pairs, stream);
+  if (chunks) return launch<HEAD_STATS, 1, 2, true>(mapA, mapB, mapC, args, pairs, stream);
+  return args.parts == 2 ? launch<HEAD_STATS, 1, 2, false>(mapA, mapB, mapC, args, pairs, stream)
+                         : launch<HEAD_STATS, 1, 1, false>(mapA, mapB, mapC, args, pairs, stream);
 }
 
 }  // namespace tgemm
