@@ -26,10 +26,18 @@ cudaError_t launch_type(const FewArgs& a, int granule, int blocks, cudaStream_t 
 
 }  // namespace
 
-// Forward: as far as it is faster than the tensor cores (loss_few.cuh); backward:
-// the same (loss_few_grad.cu).
+// As far as it is faster than the tensor cores (loss_few.cuh, loss_few_grad.cu have
+// both sides), and the rows of H fit shared memory.
 bool few_rows(bool backward, int64_t T, int64_t V, int64_t D, bool f32, bool aligned) {
-  const int64_t most = f32 ? (!backward && V < kFewSimtV ? kHeadSimtRows : kFewRows) : backward ? (aligned ? 2 : 0) : aligned ? 1 : kFewRows;
+  int64_t most = kFewRows;
+  if (f32) {
+    // below kFewSimtV entries passes of eight rows beat the tiles of loss_simt.cu too
+    if (!backward && V < kFewSimtV) most = kHeadSimtRows;
+  } else if (backward) {
+    most = aligned ? 2 : 0;
+  } else if (aligned) {
+    most = 1;
+  }
   return T <= most && rows_held(T) * (D + 8) * 4 <= kFewSmem;
 }
 
