@@ -183,3 +183,40 @@ def test_logits_of_products_of_one_sign(D, T, dtype):
     # a common factor of all logits cancels in the loss but for their differences
     exact = want - z.gather(1, y[:, None])[:, 0]
     assert bool(((loss.double() - exact).abs() <= 2 * bound).all())
+
+
+def mean_error(got, want):
+    return float(((got.double() - want) / want).mean())
+
+
+def test_gradient_sums_of_one_sign_over_long_axes():
+    """fp16 gradients whose terms have one sign and are exact: their mean error is what the adder's truncation leaves.
+    256 steps of less than 2^-23 of the sum each are 2^-15; the rounding to fp16 (2^-11 at most, both ways) leaves four
+    of its deviations, 2^-11 / sqrt(3 n), in the mean of n values."""
+    lib = H.tg()
+    gen = torch.Generator(device="cuda").manual_seed(11)
+
+    def bound(n):
+        return 2.0 ** -15 + 4 * 2.0 ** -11 / math.sqrt(3 * n)
+
+    # dW: W = 0, so every probability is 2^-8; 65536 rows of positive h with one target
+    T, V, D = 65536, 256, 1024
+    h = (0.5 + 0.5 * torch.rand(T, D, device="cuda", generator=gen)).to(F16)
+    w = torch.zeros(V, D, device="cuda", dtype=F16)
+    y = torch.zeros(T, device="cuda", dtype=torch.int64)
+    g = torch.ones(T, device="cuda")
+    _, lse = lib.linear_cross_entropy(h, w, y)
+    _, dw = lib.linear_cross_entropy_backward(h, w, y, lse, g, want_hidden=False)
+    finished()
+    assert abs(mean_error(dw[7], h.double().sum(dim=0) / V)) <= bound(D)
+    # dH: h = 0, so every probability is 2^-16; positive W but for the target's row
+    T, V, D = 2560, 65536, 2048
+    h = torch.zeros(T, D, device="cuda", dtype=F16)
+    w = (0.5 + 0.5 * torch.rand(V, D, device="cuda", generator=gen)).to(F16)
+    w[3] = 0
+    y = torch.full((T,), 3, device="cuda")
+    g = torch.ones(T, device="cuda")
+    _, lse = lib.linear_cross_entropy(h, w, y)
+    dh, _ = lib.linear_cross_entropy_backward(h, w, y, lse, g, want_weight=False)
+    finished()
+    assert abs(mean_error(dh[9], w.double().mean(dim=0))) <= bound(D)

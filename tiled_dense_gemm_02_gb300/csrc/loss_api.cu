@@ -42,9 +42,11 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;
 // 1326 / 1270 / 1210 / 1200 / 1176 us; error of lse (9.0), 300 x 4096 x 4096, by the
 // first four: 0.6 / 1.0 / 1.4 / 2.0 e-6, against a last bit of 0.95e-6.  fp32: half,
 // as gradients and logits are fp32 alike: 4 to 7 e-7 of their norm.  16-bit
-// gradients are left whole: a sum of 2^16 terms loses up to 6e-5 (mixed signs) of
-// itself, where its rounding to 8 or 11 bits may cost 2^-9 or 2^-12.
-constexpr int kLogitChunk = 16, kPlaneChunk = 8;
+// gradients, whose outputs keep 8 or 11 bits: 256 steps stay below 2^-15 (whole sums
+// of 65536 terms of one sign were 1.7e-4 off); backward calls of 2048 x 131072 x 4096
+// and of 8192 x 131072 x 1024, chunks of 32 / 64 stages / whole: 4085 / 4020 / 3980
+// and 5345 / 5312 / 5212 us.
+constexpr int kLogitChunk = 16, kPlaneChunk = 8, kGradientChunk = 64;
 // 16-bit forward calls: k-stages of a tile up to which its statistics, not its
 // product, bound the call, and eight epilogue warps beat four.  Measured at 4096 x
 // 32768: D = 64 75 -> 64 us, 256 79 -> 70 us with eight; 512 104 -> 97 us, 1024 177 ->
@@ -433,6 +435,7 @@ class Products {
     b.k_blocks = static_cast<int>(ceil_div(n_, kTileK));
     b.splits = l_.splits;
     b.k_per_split = l_.k_per_split;
+    b.chunk = l_.planes > 1 ? kPlaneChunk : kGradientChunk;
     TGEMM_TRY(map_dz(&out.a, kTileK, kTileM));
     TGEMM_TRY(map_weight(&out.b, 64, kTileK));
     return host_map_3d(&out.c, 2, ws_ + l_.acc, c_.D, c_.T, l_.splits, l_.ld_acc * 4, c_.T * l_.ld_acc * 4, 32, 32);
@@ -446,6 +449,7 @@ class Products {
     b.out_row0 = static_cast<int>(v0_);
     b.reduce = 0;
     const bool f32 = l_.planes > 1;
+    b.chunk = f32 ? kPlaneChunk : kGradientChunk;
     b.k_blocks = static_cast<int>(ceil_div(c_.T, kTileK));  // at most: the count is the device's
     b.store_granule = host_granule(c_.dW, c_.lddw, f32 ? 4 : 2);
     TGEMM_TRY(map_dz(&out.a, 64, kTileK));

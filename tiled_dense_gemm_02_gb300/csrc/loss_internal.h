@@ -125,7 +125,7 @@ struct HeadArgs {
   int b_row0;     // STATS, DZ, DH: row of the weight map for the piece's column 0
   int k_blocks;   // 64-deep stages of the k axis (DW: were every row to count)
   int splits, k_per_split;  // DH: ranges of the k axis summed apart
-  int chunk;      // stages of the k axis summed in tensor memory, at most, before they are added in fp32 (16-bit DH, DW: all)
+  int chunk;      // stages of the k axis summed in tensor memory, at most, before they are added in fp32
   int reduce;     // DH: add to the sums instead of storing them
   int bf16;
   float k2;       // scale * log2(e)
