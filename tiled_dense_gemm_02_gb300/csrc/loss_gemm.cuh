@@ -802,7 +802,10 @@ __device__ __forceinline__ void head_product(const CUtensorMap& mapA, const CUte
       float4 k = coef;
       Walk walk;
       uint32_t tbase;
-      if (u.lo >= u.hi) continue;
+      if (u.lo >= u.hi) {  // a split past the end of a short last piece
+        if constexpr (!CHUNKS) look_ahead(i + workers);
+        continue;
+      }
       if constexpr (CHUNKS) {
         int lo = u.lo + chunk;  // end of the chunk to come
         tbase = taken();
