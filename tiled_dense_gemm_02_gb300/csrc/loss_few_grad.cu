@@ -9,10 +9,11 @@
 // groups of warps take different entries; their sums join in order at the end.
 //
 // Against the tensor-core products, a backward call on 65536 x 4096: bf16 one row
-// 317 to 353 us, two 334 to 353, from three on the products' (350 to 390 here); off
+// 316 to 353 us, two 335 to 353, from three on the products' (350 to 390 here); off
 // the 16-byte grid, where dW leaves in words of 8 bytes or less, the products' (at
-// 4100 columns one row 807 to 640 us); fp32 one row 540 us (6.0 TB/s), four 590,
-// eight 670 (held to 128 registers for two blocks an SM: 144 took 920) to 1783 us.
+// 4100 columns one row 807 to 647 us); fp32 one row 536 us (6.0 TB/s), two 619, four
+// 588 (with the 16-byte loads of dz and the 128 registers that two rows do not
+// have), eight 671 (144 registers, one block an SM, took 920) to 1730 us.
 #include "loss_few.cuh"
 
 namespace tgemm {
