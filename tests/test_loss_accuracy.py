@@ -74,3 +74,31 @@ def test_fp32_distillation_errors_in_the_norm(T):
     dh, dw = lib.linear_distillation_backward(h, w, ids, logits, lse, g)
     r = ref.distill(h, w, ids, logits, 1.0, g)
     acc.check({n: getattr(r, n) for n in ("loss", "lse", "dh", "dw")}, {"loss": loss, "lse": lse, "dh": dh, "dw": dw})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("T,counting,most", [(2, 2, 1.05), (20, 20, 1.05), (32, 7, 1.05), (33, 33, 1.6), (300, 300, 1.6),
+                                             (300, 2, 2.7)])
+def test_16_bit_gradients_beside_their_own_rounding(T, counting, most, dtype):
+    """dH and dW against the exact ones, in units of what their last rounding alone leaves, in the norm.  Up to 32 rows
+    dz has two planes (or is fp32) and adds nothing to it.  Above, dz is rounded to the type too: a rounding of the same
+    size, independent of the last, makes sqrt(2), and a tenth more is left for its spread.  With two rows that
+    count, a gradient may hang on one entry of dz, whose rounding is up to 2.4 times an average one: sqrt(1 + 2.4^2)."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from tests import gpu_harness as H
+    lib = H.tg()
+    V, D = 4096, 512
+    h, w, y, g = acc.operands(T, V, D, "cuda", seed=T)
+    h, w, g = h.to(dtype), (2 * w).to(dtype), 0.5 + g
+    alone = (h[:counting], w, y[:counting], g[:counting])
+    y = y.clone()
+    y[counting:] = -100
+    loss, lse = lib.linear_cross_entropy(h, w, y)
+    dh, dw = lib.linear_cross_entropy_backward(h, w, y, lse, g)
+    assert lib.device_status(torch.cuda.current_stream().cuda_stream) == lib.OK
+    want = acc.definition(*alone)
+    for got, exact in ((dh[:counting], want["dh"]), (dw, want["dw"])):
+        own = (exact.to(dtype).double() - exact).norm()
+        assert float((got.double() - exact).norm() / own) <= most
