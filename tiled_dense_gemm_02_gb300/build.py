@@ -21,7 +21,7 @@ LIBRARY = os.path.join(HERE, "libtgemm.so")
 # the FP32 FMA-throughput probe the benchmark uses for the SIMT roofline (not part of libtgemm.so)
 PROBE_SOURCE = os.path.join(CSRC, "probe", "fp32_peak.cu")
 PROBE_LIBRARY = os.path.join(HERE, "libtgemm_probe.so")
-HEADERS = [os.path.join(ROOT, "include", name) for name in ("tgemm.h", "tgemm_loss.h")]
+HEADERS = [os.path.join(ROOT, "include", name) for name in ("tgemm.h", "tgemm_loss.h", "tgemm_experts.h", "tgemm_grads.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 NVCC_FLAGS = [

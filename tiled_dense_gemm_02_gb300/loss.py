@@ -187,13 +187,16 @@ def _current_stream(torch, device):
     return raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
 
 
-def _call(torch, device, function, args, workspace, need):
-    args += (workspace.data_ptr(), need, _current_stream(torch, device))
+def _guarded(torch, device, function, args):
+    """``function(*args)`` with ``device`` current: the library launches on the current device."""
     if torch.cuda.current_device() == device:
-        st = function(*args)
-    else:
-        with torch.cuda.device(device):
-            st = function(*args)
+        return function(*args)
+    with torch.cuda.device(device):
+        return function(*args)
+
+
+def _call(torch, device, function, args, workspace, need):
+    st = _guarded(torch, device, function, args + (workspace.data_ptr(), need, _current_stream(torch, device)))
     if st != OK:
         raise TgemmError(st, function.__name__)
 
