@@ -96,6 +96,71 @@ TGEMM_API int tgemm_route_backward(int64_t T, int64_t E, int64_t k, const void* 
                const int64_t* ids, const float* grad, const tgemm_route_options* opts, void* d_logits,
                int64_t ld_out, void* stream);
 
+/* Options of the experts' products; NULL means the defaults. */
+typedef struct tgemm_experts_options {
+  int wait_timeout_us; /* bound of every in-kernel wait (0 = 2 s) */
+  int reserved[3];     /* must be 0 */
+} tgemm_experts_options;
+
+/* Bytes of workspace a call needs: device memory owned by the caller, 256-byte
+ * aligned, no initialisation needed, contents unspecified afterwards.  Calls that
+ * may run at the same time must not share one.  backward: 0 or 1.  The weights and
+ * their pitches tell whether their rows are 16-byte aligned (they are copied to
+ * an aligned pitch when they are not; only the pointers' values modulo 16 are
+ * looked at).  Needs no GPU.
+ *
+ * With r = T k rows and up to 31 more per expert that has any: 2 F + 4 D bytes a row
+ * forward, 6 F + 4 D and F / 8 bytes backward, 2 D bytes a token (twice backward),
+ * and the copies. */
+TGEMM_API int tgemm_experts_workspace_size(int backward, int64_t T, int64_t E, int64_t k, int64_t D, int64_t F,
+               const void* W_in, int64_t ld_in, const void* W_out, int64_t ld_out, int dtype, size_t* bytes);
+
+/* Bytes of what the forward call keeps for the backward call (device memory of
+ * the caller's, 256-byte aligned): the order of the rows, and g and u in float32, 8 F bytes a row.
+ * The backward call only reads it. */
+TGEMM_API int tgemm_experts_saved_size(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F, int dtype,
+               size_t* bytes);
+
+/*
+ * The experts' products, forward.  dtype: TGEMM_BF16 or TGEMM_F16.  out: T x D, pitch
+ * ldo >= D, in dtype.  saved: tgemm_experts_saved_size bytes, or NULL where no
+ * backward call follows.
+ *
+ * Errors: TGEMM_ERR_INVALID_VALUE for a negative T, another size below 1, a short
+ * pitch, a null pointer with T > 0, a bad option, a workspace or saved that is not
+ * 256-byte aligned or too small; TGEMM_ERR_UNSUPPORTED_DTYPE; TGEMM_ERR_MISALIGNED
+ * for a pointer not aligned to its element; TGEMM_ERR_ALIAS when an output overlaps
+ * an input, another output, saved or the workspace; TGEMM_ERR_TOO_LARGE for E > 1024, k >=
+ * 2^16, D or F >= 2^24, rows or tiles that 2^31 does not count.  They are returned
+ * before any CUDA call.  T == 0: the forward call does nothing, the backward call
+ * zeroes the weights' gradients.
+ */
+TGEMM_API int tgemm_experts_forward(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F,
+               const void* x, int64_t ldx, const void* W_in, int64_t ld_in, const void* W_out, int64_t ld_out,
+               const int64_t* ids, const float* weights, int dtype, const tgemm_experts_options* opts,
+               void* out, int64_t ldo, void* saved, size_t saved_bytes,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/* The experts' products, backward, for the forward call's operands and what it
+ * kept.  grad: T x D, the gradient of the result with respect to out, in dtype.
+ *
+ *   v = W_out[e]^T grad_t,  s = sigmoid(g)
+ *   d_weights = h . v                                   (T x k float32; unused places 0)
+ *   dg = w v u s (1 + g (1 - s)),  du = w v g s
+ *   dx_t = sum_j W_in[e]^T (dg, du),   dW_in[e] = sum over its rows (dg, du) x_t^T
+ *   dW_out[e] = sum over its rows grad_t (w h)^T
+ *
+ * dg, du and w h are rounded to dtype on their way into the products (fp16: dg and
+ * du times a power of two that brings the largest |grad| to 16), each output once.
+ * dx, dW_in, dW_out (pitches as the operands') and d_weights: any may be NULL when
+ * it is not wanted; an expert without rows gets zeros. */
+TGEMM_API int tgemm_experts_backward(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F,
+               const void* x, int64_t ldx, const void* W_in, int64_t ld_in, const void* W_out, int64_t ld_out,
+               const float* weights, const void* saved, size_t saved_bytes, const void* grad, int64_t ldg,
+               int dtype, const tgemm_experts_options* opts,
+               void* dx, int64_t lddx, void* dW_in, int64_t ldd_in, void* dW_out, int64_t ldd_out,
+               float* d_weights, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -300,10 +300,11 @@ def matmul(a, b, out=None, out_dtype=None, options=None, stream=None):
 from .loss import (DISTILL_MAX_K, LOSS_EXPORTS, LossOptions, distill_backward, distill_forward,  # noqa: E402
                    linear_cross_entropy, linear_cross_entropy_backward, linear_distillation,
                    linear_distillation_backward, loss_workspace_size, xent_backward, xent_forward)
-# a sparse layer's routing (include/tgemm_experts.h)
-from .experts import (EXPERT_EXPORTS, ROUTE_GROUP_MAX, ROUTE_GROUP_TOP2, ROUTE_MAX_EXPERTS, ROUTE_MAX_GROUPS,  # noqa: E402
-                      ROUTE_MAX_K, ROUTE_SIGMOID, ROUTE_SOFTMAX, RouteOptions, route_backward, route_experts,
-                      route_experts_backward, route_forward)
+# a sparse layer: routing and the experts' products (include/tgemm_experts.h)
+from .experts import (EXPERT_EXPORTS, MAX_EXPERTS, ROUTE_GROUP_MAX, ROUTE_GROUP_TOP2, ROUTE_MAX_EXPERTS,  # noqa: E402
+                      ROUTE_MAX_GROUPS, ROUTE_MAX_K, ROUTE_SIGMOID, ROUTE_SOFTMAX, ExpertsOptions, RouteOptions,
+                      expert_mlp, expert_mlp_backward, experts_backward, experts_forward, experts_saved_size,
+                      experts_workspace_size, route_backward, route_experts, route_experts_backward, route_forward)
 # the norm over all gradients and their clipping (include/tgemm_grads.h)
 from .grads import (GRAD_EXPORTS, GRAD_MAX_TENSORS, clip_gradients, grad_clip, grad_norm,  # noqa: E402
                     grad_workspace_size, gradient_norm)

@@ -801,15 +801,15 @@ int encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int6
 
 // 3-D row-major tensor: `depth` matrices of cols x rows, `depth_bytes` apart
 // (a depth of 1 for one matrix or for a batch stride of 0), box box_cols x
-// box_rows x 1.
+// box_rows x box_depth.
 int encode_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols, int64_t rows,
               int64_t depth, int64_t pitch_bytes, int64_t depth_bytes, uint32_t box_cols, uint32_t box_rows,
-              CUtensorMapSwizzle swizzle) {
+              CUtensorMapSwizzle swizzle, uint32_t box_depth = 1) {
   if (depth <= 1) depth_bytes = (rows * pitch_bytes + 15) / 16 * 16;  // unused, but must be valid
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(depth < 1 ? 1 : depth)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch_bytes), static_cast<cuuint64_t>(depth_bytes)};
-  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t box[3] = {box_cols, box_rows, box_depth};
   return encode_cached(map, type, 3, base, dims, strides, box, swizzle);
 }
 
@@ -1117,9 +1117,14 @@ static CUtensorMapDataType host_map_type(int type) {
 }
 
 int host_map_3d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t depth,
-                int64_t pitch_bytes, int64_t depth_bytes, uint32_t box_cols, uint32_t box_rows) {
+                int64_t pitch_bytes, int64_t depth_bytes, uint32_t box_cols, uint32_t box_rows, uint32_t box_depth) {
   return encode_3d(map, host_map_type(type), base, cols, rows, depth, pitch_bytes, depth_bytes, box_cols, box_rows,
-                   CU_TENSOR_MAP_SWIZZLE_128B);
+                   CU_TENSOR_MAP_SWIZZLE_128B, box_depth);
+}
+
+int host_map_2d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t pitch_bytes,
+                uint32_t box_cols, uint32_t box_rows) {
+  return encode_2d(map, host_map_type(type), base, cols, rows, pitch_bytes, box_cols, box_rows);
 }
 
 void host_count_launches(int n) { g_launch_calls.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }

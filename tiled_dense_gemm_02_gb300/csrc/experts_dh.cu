@@ -1,0 +1,11 @@
+// The experts' pair product DH (experts_gemm.cuh).
+#include "experts_gemm.cuh"
+
+namespace tgemm {
+
+cudaError_t launch_expert_dh(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
+                           int pairs, cudaStream_t stream) {
+  return launch_expert<EXPERT_DH>(a, b, c, args, pairs, stream);
+}
+
+}  // namespace tgemm

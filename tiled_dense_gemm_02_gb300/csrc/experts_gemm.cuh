@@ -1,0 +1,561 @@
+// Tensor-core products of the experts, on CTA pairs: tcgen05.mma.cta_group::2, M =
+// 256, fp32 accumulators in tensor memory, two of them, so a tile's epilogue
+// runs under the next tile's MMAs.
+//
+// With e an expert, its rows' tokens t and 1 <= n <= 256 of its rows a tile:
+//
+//   UP    W_in[e] x_t           M = 128 features' gates and ups, N = n, K = D
+//   DOWN  W_out[e] h            M = D, N = n, K = F
+//   DH    W_out[e]^T d_out_t    M = F, N = n, K = D
+//   DX    W_in[e]^T (dg, du)    M = D, N = n, K = 2 F
+//   DIN   (dg, du)^T x          M = 2 F, N = D, K = the expert's rows
+//   DOUT  d_out^T (w h)         M = D, N = F, K = the expert's rows
+//
+// The weight is the M operand and the tokens are N, which tcgen05 takes in steps of
+// 32: an expert with a handful of rows computes 32 columns, not 256, and the same
+// kernel serves one token (bound by the weights' bytes, each read once) and a
+// training batch (bound by the MMAs).  Rows of x and d_out are fetched where they
+// lie by gathering bulk-tensor copies, four rows each (tile::gather4); every lane of
+// the producer warp issues the copies of its own four rows.  No operand is
+// transposed or copied in memory.
+//
+// UP interleaves 16 gate rows with their 16 ups, so that a warp's 32 lanes
+// of tensor memory hold both of 16 features: lanes l and l + 16 exchange one
+// value of two columns and each finishes one.
+//
+// The adder of tcgen05.mma truncates: a step moves the sum towards 0 by up to 2^-23
+// of it.  Sums leave tensor memory every `chunk` stages (four steps each) and are
+// added in registers, with rounding to nearest, under the next chunk's MMAs; the
+// last sum goes back to tensor memory, where the epilogues read it.
+//
+// Roles: warp 0 copies, warp 1 MMAs (one thread of the leader), warps 2.. epilogue,
+// eight of them: a quarter of the lanes and half of the columns each.  Every role
+// derives the units from the tile list, which is known on the device only.  Every
+// wait is bounded (tc_common.cuh).
+#pragma once
+
+#include "experts_internal.h"
+#include "tc_pair.cuh"
+
+namespace tgemm {
+namespace {
+
+constexpr int kEpilogueWarps = 8;
+constexpr int kExpertThreads = 32 * (2 + kEpilogueWarps);
+constexpr bool weight_gradient(int mode) { return mode == EXPERT_DIN || mode == EXPERT_DOUT; }
+constexpr int expert_epi_bytes(int mode) { return weight_gradient(mode) ? kEpilogueWarps * 4096 : 0; }
+constexpr int expert_stages(int mode) {
+  return (kSmemLimit - 1024 - expert_epi_bytes(mode) - kBarrierBytes) / kStage;
+}
+constexpr int expert_smem(int mode) {
+  return 1024 + expert_stages(mode) * kStage + expert_epi_bytes(mode) + kBarrierBytes;
+}
+constexpr bool expert_a_m_major(int mode) { return mode >= EXPERT_DH; }
+constexpr bool expert_b_n_major(int mode) { return weight_gradient(mode); }
+
+// Four rows of a tensor, 64 columns from x on, into 512 bytes of this CTA's shared
+// memory; completion on an mbarrier of either CTA of the pair.
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* map, int32_t x, const int4& rows,
+                                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar_cluster)
+      : "memory");
+}
+
+// Bytes that gathers of both CTAs bring for 256 columns from `first` on: 64 columns are
+// fetched where any is inside.  (What lies outside is some earlier stage's: its
+// sums are not stored.)
+__device__ __forceinline__ uint32_t gathered_bytes(int first, int columns) {
+  return static_cast<uint32_t>(min(4, (columns - first + 63) / 64)) * 8192u;
+}
+
+// A tile of a product: block mb of M, and N's columns (rows row0.. of the sorted
+// matrices, n with the filling and `valid` without; gradients of the weights:
+// column block nb, and rows row0.. are the k axis).
+struct ExpertUnit {
+  int expert, mb, nb, row0, n, valid;
+};
+
+template <int MODE>
+struct ExpertUnits {
+  int count;
+  __device__ __forceinline__ explicit ExpertUnits(const ExpertArgs& a) {
+    count = weight_gradient(MODE) ? a.E * a.m_blocks * a.n_blocks : __ldcg(a.rows.head) * a.m_blocks;
+  }
+  __device__ __forceinline__ ExpertUnit get(const ExpertArgs& a, int i) const {
+    ExpertUnit u = {};
+    if (i >= count) return u;
+    if constexpr (weight_gradient(MODE)) {
+      const int per = a.m_blocks * a.n_blocks;
+      u.expert = i / per;
+      i -= u.expert * per;
+      u.nb = i / a.m_blocks;
+      u.mb = i - u.nb * a.m_blocks;
+      u.row0 = __ldcg(a.rows.first + u.expert);
+      u.n = __ldcg(a.rows.first + u.expert + 1) - u.row0;
+      u.valid = u.n;
+    } else {
+      const int t = i / a.m_blocks;
+      u.mb = i - t * a.m_blocks;
+      const int4 tile = __ldcg(a.rows.tiles + t);
+      u.expert = tile.x;
+      u.row0 = tile.y;
+      u.n = tile.z;
+      u.valid = tile.w;
+    }
+    return u;
+  }
+  __device__ __forceinline__ int stages(const ExpertArgs& a, const ExpertUnit& u) const {
+    return weight_gradient(MODE) ? (u.n + kTileK - 1) / kTileK : a.k_blocks;
+  }
+};
+
+// Sums of up to 128 columns of this thread's lane, `blocks` times 16.
+__device__ __forceinline__ void first_sums(uint32_t tcol, int blocks, uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b)
+    if (b < blocks) ptx::tmem_ld_32x32b_x16(tcol + b * 16, sum[b]);
+  ptx::tmem_wait_ld();
+}
+__device__ __forceinline__ void more_sums(uint32_t tcol, int blocks, uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b)
+    if (b < blocks) {
+      uint32_t raw[16];
+      ptx::tmem_ld_32x32b_x16(tcol + b * 16, raw);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        sum[b][i] = __float_as_uint(__uint_as_float(sum[b][i]) + __uint_as_float(raw[i]));
+    }
+}
+__device__ __forceinline__ void whole_sums(uint32_t tcol, int blocks, const uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b)
+    if (b < blocks) ptx::tmem_st_32x32b_x16(tcol + b * 16, sum[b]);
+  ptx::tmem_wait_st();
+}
+
+__device__ __forceinline__ uint16_t to_half_word(float v, int bf16) {
+  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+// 16 columns of UP: gates in lanes 0..15, ups in lanes 16..31 -> h, and g and u.
+// `row`: the columns' first row, of which `valid` are no filling (which gets 0).
+__device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertArgs& a, int feature, int64_t row,
+                                          int valid, int lane) {
+  const bool low = lane < 16;
+  uint16_t* h = static_cast<uint16_t*>(a.h) + row * a.ldh + feature;
+  float* gu = a.gu ? a.gu + row * 2 * a.ldg + feature : nullptr;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, low ? v[2 * i + 1] : v[2 * i], 16);
+    const float g = __uint_as_float(low ? v[2 * i] : got), u = __uint_as_float(low ? got : v[2 * i + 1]);
+    const int c = 2 * i + (low ? 0 : 1);
+    if (feature < a.F) {
+      const float x = __fdividef(g, 1.0f + __expf(-g)) * u;
+      h[c * a.ldh] = c < valid ? to_half_word(x, a.bf16) : uint16_t(0);
+      if (gu && c < valid) {
+        __stcs(gu + c * 2 * a.ldg, g);
+        __stcs(gu + c * 2 * a.ldg + a.ldg, u);
+      }
+    }
+  }
+}
+
+// 16 columns of DH: v = d_out W_out of this lane's feature.
+//   s = sigmoid(g):  dg = w v u s (1 + g (1 - s)),  du = w v g s,  h = g s u
+__device__ __forceinline__ void finish_dh(const uint32_t (&v)[16], const ExpertArgs& a, int feature, int64_t row,
+                                          int valid, int lane, int part, int parts, float scale) {
+  const bool in = feature < a.F;
+  const float* gu = a.gu + row * 2 * a.ldg + feature;
+  uint16_t* dgu = static_cast<uint16_t*>(a.dgu) + row * a.ld_dgu + feature;
+  uint16_t* hw = static_cast<uint16_t*>(a.h) + row * a.ldh + feature;
+  const float mine = lane < 16 && lane < valid ? __ldg(a.weights + __ldcg(a.rows.place + row + lane)) : 0.0f;
+  float g[16], u[16], dot[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const bool there = in && c < valid;
+    g[c] = there ? __ldcs(gu + c * 2 * a.ldg) : 0.0f;
+    u[c] = there ? __ldcs(gu + c * 2 * a.ldg + a.ldg) : 0.0f;
+  }
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const float w = __shfl_sync(0xffffffffu, mine, c);
+    const float d = __uint_as_float(v[c]);
+    const float s = 1.0f / (1.0f + expf(-g[c]));
+    const float gate = g[c] * s, h = gate * u[c];
+    const bool there = in && c < valid;
+    dot[c] = there ? h * d : 0.0f;
+    if (in) {
+      const float wd = w * d * scale;
+      dgu[c * a.ld_dgu] = there ? to_half_word(wd * u[c] * (s + gate * (1.0f - s)), a.bf16) : uint16_t(0);
+      dgu[c * a.ld_dgu + a.F] = there ? to_half_word(wd * gate, a.bf16) : uint16_t(0);
+      hw[c * a.ldh] = there ? to_half_word(w * h, a.bf16) : uint16_t(0);
+    }
+  }
+  // sums over the 32 lanes: a lane keeps half of its columns at each exchange, and
+  // ends with one column's half
+#pragma unroll
+  for (int width = 8; width >= 1; width >>= 1) {
+    const bool high = (lane & (2 * width)) != 0;
+#pragma unroll
+    for (int c = 0; c < width; ++c) {
+      const float got = __shfl_xor_sync(0xffffffffu, high ? dot[c] : dot[c + width], 2 * width);
+      dot[c] = (high ? dot[c + width] : dot[c]) + got;
+    }
+  }
+  const float sum = dot[0] + __shfl_xor_sync(0xffffffffu, dot[0], 1);
+  const int c = lane >> 1;
+  if ((lane & 1) == 0 && c < valid) __stcg(a.dots + (row + c) * parts + part, sum);
+}
+
+// 16 columns of DOWN or DX: fp32, one row's 32 neighbouring elements a store.
+__device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int valid) {
+  if (d >= a.D) return;
+  float* y = a.y + row * a.ldy + d;
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    if (c < valid) __stcg(y + c * a.ldy, __uint_as_float(v[c]));
+}
+
+// A weight's gradient: this warp's 32 rows of M, its 128 columns of N.  `sums`: 0 for
+// an expert without rows.
+__device__ __forceinline__ void finish_weight(uint32_t tcol, bool sums, const ExpertArgs& a, int expert, int row0, int M,
+                                              int col0, int N, float f, const CUtensorMap* mapC, uint8_t* buf, int lane) {
+  if (row0 >= M) return;
+  const int fmt = a.bf16 ? OUT_BF16 : OUT_F16;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const int col = col0 + c * 64;
+    if (col >= N) break;
+    uint32_t w[32];
+    if (sums) {
+      uint32_t lo[32], hi[32];
+      ptx::tmem_ld_32x32b_x32(tcol + c * 64, lo);
+      ptx::tmem_ld_32x32b_x32(tcol + c * 64 + 32, hi);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        w[i] = pack_pair(f * __uint_as_float(lo[2 * i]), f * __uint_as_float(lo[2 * i + 1]), fmt);
+        w[16 + i] = pack_pair(f * __uint_as_float(hi[2 * i]), f * __uint_as_float(hi[2 * i + 1]), fmt);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = 0u;
+    }
+    if (a.store_granule == 0)
+      store_words(w, mapC, col, row0, expert, buf, lane);
+    else
+      store_words_plain(w, static_cast<uint16_t*>(a.out) + (static_cast<int64_t>(expert) * M + row0) * a.ld_out + col,
+                        a.ld_out, M - row0, N - col, a.store_granule, buf, lane);
+  }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kExpertThreads, 1)
+    expert_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                  const __grid_constant__ CUtensorMap mapC, const __grid_constant__ ExpertArgs args) {
+  constexpr int STAGES = expert_stages(MODE);
+  constexpr bool GRADIENT = weight_gradient(MODE);
+  constexpr int ACC = 256;
+  constexpr uint32_t TMEM_COLS = 512;
+  static_assert(expert_smem(MODE) <= kSmemLimit, "shared memory per CTA");
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sC = smem + STAGES * kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sC + expert_epi_bytes(MODE));
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  static_assert((2 * STAGES + 5) * 8 + 8 <= kBarrierBytes, "barrier area");
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int cta = static_cast<int>(ptx::cluster_ctarank() & 1u);
+  const bool leader = cta == 0;
+  const int worker = blockIdx.x / 2, workers = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_u32(&acc_full[b]), 1);
+      ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * kEpilogueWarps);
+    }
+    ptx::mbar_init(ptx::smem_u32(drain), 1);
+    *abort_flag = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&mapA);
+    ptx::tma_prefetch_desc(&mapB);
+    if (GRADIENT) ptx::tma_prefetch_desc(&mapC);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), TMEM_COLS);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before_sync();
+  ptx::cluster_sync();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  // set-up overlaps the end of the kernel before; its results are read from here on
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+
+  const Ctl ctl{abort_flag, args.timeout_ns, args.status};
+  const ExpertUnits<MODE> units(args);
+
+  if (warp == 0) {
+    // ------------------------------------------------ bulk-tensor producer
+    int stage = 0;
+    uint32_t phase = 0, filled = 0, last_parity = 0;
+    bool ok = true;
+    ExpertUnit next = units.get(args, worker);
+    for (int i = worker; ok && i < units.count; i += workers) {
+      const ExpertUnit u = next;
+      next = units.get(args, i + workers);
+      const int stages = units.stages(args, u);
+      const int half = GRADIENT ? kTileM : u.n / 2;  // this CTA's columns
+      int4 rows = make_int4(0, 0, 0, 0);
+      if constexpr (MODE == EXPERT_UP || MODE == EXPERT_DH) {
+        if (4 * lane < half)
+          rows = __ldcg(reinterpret_cast<const int4*>(args.rows.token + u.row0 + cta * half + 4 * lane));
+      }
+      // gradients: lane l gathers rows 4 (l mod 16).. of a stage, for column block l / 16
+      const int4* tokens = reinterpret_cast<const int4*>(args.rows.token + u.row0) + (lane & 15);
+      if constexpr (GRADIENT) {
+        if (stages > 0) rows = __ldcg(4 * (lane & 15) < u.n ? tokens : tokens - (lane & 15));
+      }
+      for (int it = 0; it < stages; ++it) {
+        int4 ahead = rows;
+        if constexpr (GRADIENT) {  // past the expert's rows: any of them, no MMA reads it
+          if (it + 1 < stages)
+            ahead = __ldcg((it + 1) * kTileK + 4 * (lane & 15) < u.n ? tokens + (it + 1) * (kTileK / 4)
+                                                                     : tokens - (lane & 15));
+        }
+        if (!warp_wait(ptx::smem_u32(&empty[stage]), phase ^ 1u, ctl, SITE_PRODUCER_EMPTY)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb_local = ptx::smem_u32(&full[stage]);
+        const uint32_t fb = ptx::mapa_shared(fb_local, 0);
+        if (leader && lane == 0) {
+          const uint32_t bytes = MODE == EXPERT_DIN    ? 2u * kSub + gathered_bytes(u.nb * 256, args.D)
+                                 : MODE == EXPERT_DOUT ? 2u * kSub + gathered_bytes(u.mb * 256, args.D)
+                                                       : 2u * (kSub + static_cast<uint32_t>(half) * 128u);
+          ptx::mbar_arrive_expect_tx(fb_local, bytes);
+        }
+        __syncwarp();
+        const uint32_t sa = ptx::smem_u32(smem + stage * kStage), sb = sa + kSub;
+        const int k0 = it * kTileK;  // past the k axis: zeros
+        // the weight's 128 rows (gradients: 128 columns of M, 64 rows)
+        if constexpr (MODE == EXPERT_UP) {
+          if (lane < 4)
+            ptx::tma_load_3d_pair(sa + lane * 4096, &mapA, k0, u.mb * kTileM + cta * 64 + lane * 16, 2 * u.expert, fb);
+        } else if constexpr (MODE == EXPERT_DOWN) {
+          if (lane == 0) ptx::tma_load_3d_pair(sa, &mapA, k0, u.mb * 256 + cta * kTileM, u.expert, fb);
+        } else if constexpr (MODE == EXPERT_DH || MODE == EXPERT_DX) {
+          if (lane < 2)
+            ptx::tma_load_3d_pair(sa + lane * 8192, &mapA, u.mb * 256 + cta * kTileM + lane * 64, k0, u.expert, fb);
+        } else if constexpr (MODE == EXPERT_DIN) {
+          if (lane < 2)
+            ptx::tma_load_3d_pair(sa + lane * 8192, &mapA, u.mb * 256 + cta * kTileM + lane * 64, u.row0 + k0, 0, fb);
+        } else {
+          const int col = u.mb * 256 + cta * kTileM + (lane >> 4) * 64;
+          if (col < args.D) tma_gather4_pair(sa + lane * 512, &mapA, col, rows, fb);
+        }
+        // the tokens' rows (gradients: 128 columns of N, 64 rows)
+        if constexpr (MODE == EXPERT_UP || MODE == EXPERT_DH) {
+          if (4 * lane < half) tma_gather4_pair(sb + lane * 512, &mapB, k0, rows, fb);
+        } else if constexpr (MODE == EXPERT_DOWN || MODE == EXPERT_DX) {
+          if (16 * lane < half)
+            ptx::tma_load_3d_pair(sb + lane * 2048, &mapB, k0, u.row0 + cta * half + 16 * lane, 0, fb);
+        } else if constexpr (MODE == EXPERT_DIN) {
+          const int col = u.nb * 256 + cta * kTileM + (lane >> 4) * 64;
+          if (col < args.D) tma_gather4_pair(sb + lane * 512, &mapB, col, rows, fb);
+        } else {
+          if (lane < 2)
+            ptx::tma_load_3d_pair(sb + lane * 8192, &mapB, u.nb * 256 + cta * kTileM + lane * 64, u.row0 + k0, 0, fb);
+        }
+        rows = ahead;
+        filled |= 1u << stage;
+        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // loads in flight land before shared memory is released (see tc_gemm_2sm.cu)
+    if (lane == 0) {
+      for (int s = 0; s < STAGES; ++s)
+        if ((filled >> s) & 1u) {
+          const uint32_t par = (last_parity >> s) & 1u;
+          wait_teardown(ptx::smem_u32(leader ? &full[s] : &empty[s]), par, ctl, SITE_TEARDOWN);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------ MMA issuer (leader CTA only)
+    if (leader && lane == 0) {
+      const uint32_t ab = args.bf16 ? 1u : 0u;
+      const uint32_t fixed = (1u << 4) | (ab << 7) | (ab << 10) | (expert_a_m_major(MODE) ? 1u << 15 : 0u) |
+                             (expert_b_n_major(MODE) ? 1u << 16 : 0u) |
+                             (static_cast<uint32_t>((2 * kTileM) >> 4) << 24);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      ExpertUnit next = units.get(args, worker);
+      for (int i = worker; ok && i < units.count; i += workers) {
+        const ExpertUnit u = next;
+        next = units.get(args, i + workers);
+        const int stages = units.stages(args, u);
+        const uint32_t idesc = fixed | (static_cast<uint32_t>((GRADIENT ? 256 : u.n) >> 3) << 17);
+        for (int lo = 0; ok && lo < stages; lo += args.chunk) {
+          if (!wait_bounded(ptx::smem_u32(&acc_empty[acc]), acc_phase ^ 1u, ctl, SITE_MMA_ACC_EMPTY)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after_sync();
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * ACC);
+          const int end = min(lo + args.chunk, stages);
+          for (int it = lo; it < end; ++it) {
+            if (!wait_bounded(ptx::smem_u32(&full[stage]), phase, ctl, SITE_MMA_FULL)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after_sync();
+            const uint32_t a0 = ptx::smem_u32(smem + stage * kStage), b0 = a0 + kSub;
+            // steps of 16: the expert's rows end at one, what follows is another's
+            const int steps = GRADIENT ? min(kTileK / 16, (u.n - it * kTileK) / 16) : kTileK / 16;
+#pragma unroll
+            for (int k = 0; k < kTileK / 16; ++k) {
+              const uint64_t da = expert_a_m_major(MODE) ? sw128_desc(a0 + k * 2048, 8192, 1024)
+                                                         : sw128_desc(a0 + k * 32, 16, 1024);
+              const uint64_t db = expert_b_n_major(MODE) ? sw128_desc(b0 + k * 2048, 8192, 1024)
+                                                         : sw128_desc(b0 + k * 32, 16, 1024);
+              if (!GRADIENT || k < steps) ptx::tc_mma_f16_pair(d_tmem, da, db, idesc, (it != lo || k != 0) ? 1u : 0u);
+            }
+            ptx::tc_commit_pair_multicast(ptx::smem_u32(&empty[stage]), 0x3);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          ptx::tc_commit_pair_multicast(ptx::smem_u32(&acc_full[acc]), 0x3);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+      }
+      ptx::tc_commit_pair(ptx::smem_u32(drain));
+      wait_teardown(ptx::smem_u32(drain), 0, ctl, SITE_DRAIN);
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------- epilogue
+    const int quarter = warp & 3;          // tensor-memory lanes of this warp
+    const int part = (warp - 2) / 4;       // its half of the columns
+    uint8_t* buf = sC + (warp - 2) * 4096;
+    const float scale = MODE == EXPERT_DH && args.scale    ? __ldcg(args.scale)
+                        : MODE == EXPERT_DIN && args.scale ? __ldcg(args.scale + 1)
+                                                           : 1.0f;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    const auto taken = [&]() {
+      ok = warp_wait(ptx::smem_u32(&acc_full[acc]), acc_phase, ctl, SITE_EPI_ACC_FULL);
+      ptx::tc_fence_after_sync();
+      return tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * ACC);
+    };
+    const auto given_back = [&]() {
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    };
+    ExpertUnit next = units.get(args, worker);
+    for (int i = worker; ok && i < units.count; i += workers) {
+      const ExpertUnit u = next;
+      next = units.get(args, i + workers);
+      const int stages = units.stages(args, u);
+      const int half = GRADIENT ? 128 : u.n / 2, blocks = half / 16;  // this warp's columns
+      uint32_t tcol = 0;
+      if (!GRADIENT || stages > 0) {
+        tcol = taken() + part * half;
+        int lo = args.chunk;  // end of the chunk at hand
+        if (lo < stages && ok) {
+          uint32_t sum[8][16];
+          first_sums(tcol, blocks, sum);
+          given_back();
+          for (lo += args.chunk;; lo += args.chunk) {
+            tcol = taken() + part * half;
+            if (!ok) break;
+            more_sums(tcol, blocks, sum);
+            if (lo >= stages) {
+              whole_sums(tcol, blocks, sum);
+              break;
+            }
+            given_back();
+          }
+        }
+        if (!ok) break;
+      }
+      if constexpr (GRADIENT) {
+        const int M = MODE == EXPERT_DIN ? 2 * args.F : args.D, N = MODE == EXPERT_DIN ? args.D : args.F;
+        finish_weight(tcol, stages > 0, args, u.expert, u.mb * 256 + cta * kTileM + quarter * 32, M,
+                      u.nb * 256 + part * 128, N, scale, &mapC, buf, lane);
+        if (stages > 0) given_back();
+      } else {
+        const int m0 = MODE == EXPERT_UP ? u.mb * kTileM + cta * 64 + quarter * 16 + (lane & 15)
+                                         : u.mb * 256 + cta * kTileM + quarter * 32 + lane;
+#pragma unroll 1
+        for (int b = 0; b < blocks; ++b) {
+          const int c0 = part * half + b * 16;
+          const int valid = u.valid - c0;
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(tcol + b * 16, v);
+          ptx::tmem_wait_ld();
+          if constexpr (MODE == EXPERT_UP)
+            finish_up(v, args, m0, u.row0 + c0, valid, lane);
+          else if constexpr (MODE == EXPERT_DH)
+            finish_dh(v, args, m0, u.row0 + c0, valid, lane, (u.mb * 2 + cta) * 4 + quarter, args.m_blocks * 8, scale);
+          else
+            finish_y(v, args, m0, u.row0 + c0, valid);
+        }
+        given_back();
+      }
+    }
+    if (GRADIENT && lane == 0) ptx::bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+
+  // ------------------------------------------------------------- teardown
+  ptx::tc_fence_before_sync();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+template <int MODE>
+cudaError_t launch_expert(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
+                          int pairs, cudaStream_t stream) {
+  static std::atomic<uint64_t> done_mask{0};
+  return launch_pairs(expert_kernel<MODE>, expert_smem(MODE), kExpertThreads, done_mask, pairs, stream, a, b, c, args);
+}
+
+}  // namespace
+}  // namespace tgemm

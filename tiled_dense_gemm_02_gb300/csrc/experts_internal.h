@@ -1,0 +1,120 @@
+// Internal interfaces of the experts' products (experts_api.cu, experts_rows.cu,
+// experts_gemm.cuh).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "loss_internal.h"
+
+namespace tgemm {
+
+// ------------------------------------------------- rows in their experts' order
+// A place is one (token, j) of ids [T, k], numbered t * k + j; a used place is a row
+// of the sorted matrices.  Each expert's rows are neighbours, in the order of
+// their places, and fill up to a multiple of kRowPad rows; the filling has the
+// token of the expert's first row and no place.  Token tiles are the
+// products' columns: an expert's rows in even parts of at most kTokenTile.
+constexpr int kRowPad = 32;
+constexpr int kTokenTile = 256;
+constexpr int kMaxExperts = 1024;
+constexpr int kPlaceBlock = 2048;  // places of one block of the sort
+
+struct ExpertRows {
+  int* head;       // {tiles, rows with the filling}
+  int* count;      // E: rows of each expert
+  int* first;      // E + 1: its first row
+  int4* tiles;     // {expert, first row, rows with the filling, rows}
+  int* token;      // of each row
+  int* place;      // of each row; -1: filling
+  int* row;        // of each place; -1: unused, -2: no such expert
+  int* partial;    // blocks x E, for many places
+};
+
+struct OrderArgs {
+  const int64_t* ids;
+  int64_t places;
+  int T, E, k;
+  ExpertRows rows;
+};
+cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream);
+
+// out[t] = sum over t's rows of weight * y[row] (weights null: of y[row]), rounded
+// to type (0 bf16, 1 f16); a place of no such expert: NaN.  dots not null: d_weights
+// of each place = the sum of its row's `parts` dots (0 where unused).
+struct JoinArgs {
+  const ExpertRows* rows;
+  const float* weights;
+  int64_t T;
+  int k, D;
+  const float* y;
+  int64_t ldy;
+  int type;
+  void* out;
+  int64_t ld_out;
+  const float* scale;   // a power of two that y is divided by, or null
+  const float* dots;
+  int parts;
+  float* d_weights;
+};
+cudaError_t launch_join(const JoinArgs& a, cudaStream_t stream);
+
+// scale[0] = a power of two that brings the largest finite |g| into [2^kGradExponent,
+// 2^(kGradExponent + 1)), scale[1] = its inverse; 1 where there is none.  largest:
+// kScaleBlocks words.
+constexpr int kGradExponent = 4, kScaleBlocks = 512;
+cudaError_t launch_grad_scale(const void* g, int64_t T, int D, int64_t ld, unsigned int* largest, float* scale,
+                              cudaStream_t stream);
+
+// ---------------------------------------------------------------- products
+// M is a weight's axis, N the tokens' (the gradients of the weights: M and N the
+// weight's two axes, K the expert's rows).
+enum ExpertMode : int {
+  EXPERT_UP = 0,    // W_in x -> h (and g, u)
+  EXPERT_DOWN = 1,  // W_out h -> y
+  EXPERT_DH = 2,    // W_out^T d_out -> dg, du, weight * h, dots
+  EXPERT_DX = 3,    // W_in^T (dg, du) -> y
+  EXPERT_DIN = 4,   // (dg, du)^T x -> dW_in
+  EXPERT_DOUT = 5   // d_out^T (weight * h) -> dW_out
+};
+
+struct ExpertArgs {
+  int E, D, F, T;
+  int m_blocks, n_blocks;  // 256-row (UP: 128-feature) blocks of M; gradients of the weights: 256-column blocks of N
+  int k_blocks;            // 64-deep stages (gradients of the weights: the rows')
+  int chunk;               // stages summed in tensor memory, at most
+  int bf16;
+  ExpertRows rows;
+  void* h;                 // UP: h; DH: weight * h
+  int64_t ldh;
+  float* gu;               // UP: g and u where kept, else null; DH: read.  Row r: g at gu[r * 2 * ldg], u ldg further
+  int64_t ldg;
+  void* dgu;               // DH
+  int64_t ld_dgu;
+  float* dots;             // DH: m_blocks * 8 per row
+  const float* weights;    // DH: of each place
+  const float* scale;      // {s, 1 / s} (fp16), or null: DH multiplies dg and du with s, DIN with 1 / s
+  float* y;                // DOWN, DX
+  int64_t ldy;
+  void* out;               // DIN, DOUT
+  int64_t ld_out;
+  int store_granule;       // 0 bulk-tensor stores, else the granule of per-thread stores
+  unsigned long long timeout_ns;
+  unsigned int* status;
+};
+
+cudaError_t launch_expert_up(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
+                             int pairs, cudaStream_t stream);
+cudaError_t launch_expert_down(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
+                               const ExpertArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_expert_dh(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
+                             int pairs, cudaStream_t stream);
+cudaError_t launch_expert_dx(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
+                             int pairs, cudaStream_t stream);
+cudaError_t launch_expert_din(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
+                              int pairs, cudaStream_t stream);
+cudaError_t launch_expert_dout(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
+                               const ExpertArgs& args, int pairs, cudaStream_t stream);
+
+}  // namespace tgemm

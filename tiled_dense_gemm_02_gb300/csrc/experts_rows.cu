@@ -1,0 +1,429 @@
+// What runs between the experts' products: places sorted by expert, rows joined
+// back into tokens, and the scale of fp16 gradients (experts_internal.h).
+//
+// The sort counts: every warp takes 256 neighbouring places, counts them by
+// expert, and after the counts are summed up places them in their order, so the
+// sorted order is that of the places, whatever the timing.  Up to kPlaceBlock
+// places take one block and one launch (a decoding step's latency); more take three:
+// counts per block, one block that sums them up and lists the tiles, placement.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+
+#include "experts_internal.h"
+#include "ptx.cuh"
+
+namespace tgemm {
+namespace {
+
+constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
+constexpr int kWarpPlaces = kPlaceBlock / kSortWarps;
+constexpr int kOwnExperts = kMaxExperts / kSortThreads;  // experts of a thread, neighbours
+constexpr uint32_t kAll = 0xffffffffu;
+
+// The expert of a place, -1 where unused, -2 where there is no such expert.
+__device__ __forceinline__ int expert_of(const OrderArgs& a, int64_t place) {
+  if (place >= a.places) return -1;
+  const int64_t id = __ldcg(a.ids + place);
+  return id < 0 ? -1 : id < a.E ? static_cast<int>(id) : -2;
+}
+
+// counts[warp][e] of the block's places (zeroed here).
+__device__ __forceinline__ void count_places(const OrderArgs& a, int64_t base, int* counts) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) counts[i] = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int r = 0; r < kWarpPlaces; r += 32) {
+    const int64_t first = base + warp * kWarpPlaces + r;
+    if (first >= a.places) break;
+    const int e = expert_of(a, first + lane);
+    if (e >= 0) atomicAdd(&counts[warp * a.E + e], 1);
+  }
+  __syncthreads();
+}
+
+// Sum over the block before this thread, and of the whole block.
+__device__ __forceinline__ int block_scan(int v, int* total, int* shared) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int sum = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int below = __shfl_up_sync(kAll, sum, d);
+    if (lane >= d) sum += below;
+  }
+  if (lane == 31) shared[warp] = sum;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) {
+    before += w < warp ? shared[w] : 0;
+    all += shared[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before + sum - v;
+}
+
+// From the number of rows n[i] of experts kOwnExperts * threadIdx.x + i: first rows,
+// filling and tiles.  One block.
+__device__ __forceinline__ void list_tiles(const OrderArgs& a, const int (&n)[kOwnExperts], int* shared) {
+  int rows = 0, tiles = 0, padded[kOwnExperts], parts[kOwnExperts];
+#pragma unroll
+  for (int i = 0; i < kOwnExperts; ++i) {
+    padded[i] = (n[i] + kRowPad - 1) / kRowPad * kRowPad;
+    parts[i] = (padded[i] + kTokenTile - 1) / kTokenTile;
+    rows += padded[i];
+    tiles += parts[i];
+  }
+  int all_rows, all_tiles;
+  int row = block_scan(rows, &all_rows, shared), tile = block_scan(tiles, &all_tiles, shared);
+  if (threadIdx.x == 0) {
+    a.rows.head[0] = all_tiles;
+    a.rows.head[1] = all_rows;
+    a.rows.first[a.E] = all_rows;
+  }
+#pragma unroll
+  for (int i = 0; i < kOwnExperts; ++i) {
+    const int e = kOwnExperts * threadIdx.x + i;
+    if (e >= a.E) break;
+    a.rows.first[e] = row;
+    a.rows.count[e] = n[i];
+    if (n[i]) {
+      // the smallest even parts; never fewer of them than `parts`, whose number the scan
+      // counted: with r = padded / 32 >= 8 (parts - 1) + 1, parts of ceil(r / parts) leave
+      // some for the last while (parts - 1)^2 < r, and from 9 parts on are of 8
+      const int even = (padded[i] / parts[i] + kRowPad - 1) / kRowPad * kRowPad;
+      const int each = even * parts[i] < padded[i] ? even + kRowPad : even;
+      for (int at = 0; at < padded[i]; at += each) {
+        const int size = min(each, padded[i] - at);
+        a.rows.tiles[tile++] = make_int4(e, row + at, size, max(0, min(size, n[i] - at)));
+      }
+    }
+    row += padded[i];
+  }
+}
+
+// Places the block's rows; next[warp][e] is where the warp's next row of expert e goes.
+__device__ __forceinline__ void place_rows(const OrderArgs& a, int64_t base, int* next) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int r = 0; r < kWarpPlaces; r += 32) {
+    const int64_t first = base + warp * kWarpPlaces + r;
+    if (first >= a.places) break;
+    const int64_t place = first + lane;
+    const int e = expert_of(a, place);
+    const uint32_t same = __match_any_sync(kAll, e);
+    if (e >= 0) {
+      const int row = next[warp * a.E + e] + __popc(same & ((1u << lane) - 1u));
+      a.rows.token[row] = static_cast<int>(place / a.k);
+      a.rows.place[row] = static_cast<int>(place);
+      a.rows.row[place] = row;
+    } else if (place < a.places) {
+      a.rows.row[place] = e;
+    }
+    __syncwarp();
+    if (e >= 0 && (same >> lane) == 1u) next[warp * a.E + e] += __popc(same);  // the last of them
+    __syncwarp();
+  }
+}
+
+// The filling behind each expert's rows: its first row's token.
+__device__ __forceinline__ void fill_rows(const OrderArgs& a) {
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    const int n = a.rows.count[e], row = a.rows.first[e];
+    if (n == 0) continue;
+    const int token = a.rows.token[row];
+    for (int r = row + n; r < row + (n + kRowPad - 1) / kRowPad * kRowPad; ++r) {
+      a.rows.token[r] = token;
+      a.rows.place[r] = -1;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) order_kernel(const __grid_constant__ OrderArgs a) {
+  extern __shared__ int counts[];  // kSortWarps x E
+  __shared__ int scan[kSortWarps];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  count_places(a, 0, counts);
+  int n[kOwnExperts];
+#pragma unroll
+  for (int i = 0; i < kOwnExperts; ++i) {
+    const int e = kOwnExperts * threadIdx.x + i;
+    n[i] = 0;
+    if (e < a.E)
+      for (int w = 0; w < kSortWarps; ++w) n[i] += counts[w * a.E + e];
+  }
+  list_tiles(a, n, scan);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    int row = a.rows.first[e];
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int c = counts[w * a.E + e];
+      counts[w * a.E + e] = row;
+      row += c;
+    }
+  }
+  __syncthreads();
+  place_rows(a, 0, counts);
+  __syncthreads();
+  fill_rows(a);
+}
+
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ OrderArgs a) {
+  extern __shared__ int counts[];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  count_places(a, static_cast<int64_t>(blockIdx.x) * kPlaceBlock, counts);
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    int n = 0;
+    for (int w = 0; w < kSortWarps; ++w) n += counts[w * a.E + e];
+    a.rows.partial[static_cast<int64_t>(blockIdx.x) * a.E + e] = n;
+  }
+}
+
+// partial[block][e]: the block's rows of e -> the rows of e in the blocks before it.
+__global__ void __launch_bounds__(kSortThreads) tiles_kernel(const __grid_constant__ OrderArgs a, int blocks) {
+  __shared__ int totals[kMaxExperts];
+  __shared__ int scan[kSortWarps];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    int sum = 0;
+    int* p = a.rows.partial + e;
+    int b = 0;
+    for (; b + 8 <= blocks; b += 8) {
+      int v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __ldcg(p + static_cast<int64_t>(b + i) * a.E);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[static_cast<int64_t>(b + i) * a.E] = sum;
+        sum += v[i];
+      }
+    }
+    for (; b < blocks; ++b) {
+      const int v = __ldcg(p + static_cast<int64_t>(b) * a.E);
+      p[static_cast<int64_t>(b) * a.E] = sum;
+      sum += v;
+    }
+    totals[e] = sum;
+  }
+  __syncthreads();
+  int n[kOwnExperts];
+#pragma unroll
+  for (int i = 0; i < kOwnExperts; ++i) {
+    const int e = kOwnExperts * threadIdx.x + i;
+    n[i] = e < a.E ? totals[e] : 0;
+  }
+  list_tiles(a, n, scan);
+}
+
+__global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_constant__ OrderArgs a) {
+  extern __shared__ int counts[];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kPlaceBlock;
+  count_places(a, base, counts);
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    int row = __ldcg(a.rows.first + e) + __ldcg(a.rows.partial + static_cast<int64_t>(blockIdx.x) * a.E + e);
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int c = counts[w * a.E + e];
+      counts[w * a.E + e] = row;
+      row += c;
+    }
+  }
+  __syncthreads();
+  place_rows(a, base, counts);
+}
+
+__global__ void __launch_bounds__(kSortThreads) fill_kernel(const __grid_constant__ OrderArgs a) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  fill_rows(a);
+}
+
+// ------------------------------------------------------------------- join
+// One thread: four columns of a token.  Bound by y's bytes, read once.
+constexpr int kJoinThreads = 128;
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pair_of(float x, float y) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+struct JoinKernelArgs {
+  const int* row;
+  const float* weights;
+  int k, D;
+  const float* y;
+  int64_t ldy;
+  void* out;
+  int64_t ld_out;
+  int vec;  // out's rows are 8-byte aligned and D a multiple of 4
+  const float* scale;
+  const float* dots;
+  int parts;
+  float* d_weights;
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinKernelArgs a) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t t = blockIdx.x;
+  const int* rows = a.row + t * a.k;
+  if (a.d_weights && blockIdx.y == 0) {  // a warp a place
+    const int lane = threadIdx.x & 31;
+    for (int j = threadIdx.x >> 5; j < a.k; j += kJoinThreads / 32) {
+      const int row = __ldcg(rows + j);
+      float sum = 0.0f;
+      if (row >= 0)
+        for (int i = lane; i < a.parts; i += 32) sum += __ldcg(a.dots + static_cast<int64_t>(row) * a.parts + i);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+      if (lane == 0) a.d_weights[t * a.k + j] = row == -2 ? NAN : sum;
+    }
+  }
+  const int d = (blockIdx.y * kJoinThreads + threadIdx.x) * 4;
+  if (!a.out || d >= a.D) return;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int j = 0; j < a.k; ++j) {
+    const int row = __ldcg(rows + j);
+    if (row >= 0) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(a.y + row * a.ldy + d));
+      const float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.0f;
+      sum.x = fmaf(w, v.x, sum.x);
+      sum.y = fmaf(w, v.y, sum.y);
+      sum.z = fmaf(w, v.z, sum.z);
+      sum.w = fmaf(w, v.w, sum.w);
+    } else if (row == -2) {
+      sum.x = sum.y = sum.z = sum.w = NAN;
+    }
+  }
+  if (a.scale) {
+    const float f = __ldcg(a.scale + 1);
+    sum.x *= f;
+    sum.y *= f;
+    sum.z *= f;
+    sum.w *= f;
+  }
+  const uint2 v = make_uint2(pair_of<BF16>(sum.x, sum.y), pair_of<BF16>(sum.z, sum.w));
+  uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.ld_out + d;
+  if (a.vec) {
+    *reinterpret_cast<uint2*>(out) = v;
+  } else {
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (d + i < a.D) out[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+// ------------------------------------------------------ scale of fp16 gradients
+constexpr int kScaleThreads = 256;
+
+// The largest finite |g| of a block's rows, as a half's bits.
+__global__ void __launch_bounds__(kScaleThreads) largest_kernel(const uint16_t* g, int64_t T, int D, int64_t ld,
+                                                                unsigned int* largest) {
+  __shared__ unsigned int shared[kScaleThreads / 32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  unsigned int most = 0u;
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x)
+#pragma unroll 4
+    for (int d = threadIdx.x; d < D; d += kScaleThreads) {
+      const unsigned int v = __ldg(g + t * ld + d) & 0x7FFFu;
+      most = v < 0x7C00u && v > most ? v : most;
+    }
+  most = __reduce_max_sync(kAll, most);
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kScaleThreads / 32; ++w) most = max(most, shared[w]);
+    largest[blockIdx.x] = most;
+  }
+}
+
+__global__ void __launch_bounds__(32) scale_of_kernel(const unsigned int* largest, int blocks, float* scale) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  unsigned int most = 0u;
+  for (int i = threadIdx.x; i < blocks; i += 32) most = max(most, __ldcg(largest + i));
+  most = __reduce_max_sync(kAll, most);
+  if (threadIdx.x != 0) return;
+  const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+  const int e = v > 0.0f ? kGradExponent - ilogbf(v) : 0;
+  scale[0] = ldexpf(1.0f, e);
+  scale[1] = ldexpf(1.0f, -e);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_next(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                        const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream) {
+  const size_t smem = sizeof(int) * kSortWarps * a.E;  // at most 32 KB
+  if (a.places <= kPlaceBlock) return launch_next(order_kernel, dim3(1), kSortThreads, smem, stream, a);
+  const int blocks = static_cast<int>((a.places + kPlaceBlock - 1) / kPlaceBlock);
+  cudaError_t e = launch_next(count_kernel, dim3(blocks), kSortThreads, smem, stream, a);
+  if (e == cudaSuccess) e = launch_next(tiles_kernel, dim3(1), kSortThreads, 0, stream, a, blocks);
+  if (e == cudaSuccess) e = launch_next(place_kernel, dim3(blocks), kSortThreads, smem, stream, a);
+  if (e == cudaSuccess) e = launch_next(fill_kernel, dim3(1), kSortThreads, 0, stream, a);
+  return e;
+}
+
+cudaError_t launch_join(const JoinArgs& j, cudaStream_t stream) {
+  JoinKernelArgs a = {};
+  a.row = j.rows->row;
+  a.weights = j.weights;
+  a.k = j.k;
+  a.D = j.D;
+  a.y = j.y;
+  a.ldy = j.ldy;
+  a.out = j.out;
+  a.ld_out = j.ld_out;
+  a.vec = j.out && j.D % 4 == 0 && j.ld_out % 4 == 0 && reinterpret_cast<uint64_t>(j.out) % 8 == 0;
+  a.scale = j.scale;
+  a.dots = j.dots;
+  a.parts = j.parts;
+  a.d_weights = j.d_weights;
+  const int across = j.out ? (j.D + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : 1;
+  const dim3 grid(static_cast<unsigned>(j.T), across, 1);
+  return j.type == 0 ? launch_next(join_kernel<true>, grid, kJoinThreads, 0, stream, a)
+                     : launch_next(join_kernel<false>, grid, kJoinThreads, 0, stream, a);
+}
+
+cudaError_t launch_grad_scale(const void* g, int64_t T, int D, int64_t ld, unsigned int* largest, float* scale,
+                              cudaStream_t stream) {
+  const int blocks = static_cast<int>(T < kScaleBlocks ? T : kScaleBlocks);
+  cudaError_t e = launch_next(largest_kernel, dim3(blocks), kScaleThreads, 0, stream, static_cast<const uint16_t*>(g), T,
+                              D, ld, largest);
+  if (e == cudaSuccess) e = launch_next(scale_of_kernel, dim3(1), 32, 0, stream, largest, blocks, scale);
+  return e;
+}
+
+}  // namespace tgemm

@@ -43,17 +43,14 @@
 // wait is bounded (tc_common.cuh).
 #pragma once
 
-#include <atomic>
 #include <climits>
 
 #include "loss_internal.h"
-#include "tc_common.cuh"
+#include "tc_pair.cuh"
 
 namespace tgemm {
 namespace {
 
-constexpr int kSub = kTileM * kTileK * 2;        // 16 KB: one CTA's share of A or B in one stage
-constexpr int kStage = 2 * kSub;
 // PARTS: epilogue warps per quarter of the rows; each of the gradients' has 4 KB to stage stores.
 constexpr int head_threads(int parts) { return 32 * (2 + 4 * parts); }
 constexpr int head_epi_bytes(int mode, int parts) { return mode == HEAD_STATS ? 0 : 4 * parts * 4096; }
@@ -77,12 +74,6 @@ struct Terms {
   }
   static __device__ __forceinline__ int b(int term) { return count == 6 ? (0x010120 >> (4 * term)) & 0xF : 0; }
 };
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Adds a shared-memory box to the fp32 tensor at (x, y, z).
 __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
@@ -249,30 +240,6 @@ struct RowStats {
   }
 };
 
-// The sums of this thread's row and 128 columns: a first chunk's, one more
-// chunk's added, and the whole ones back in tensor memory.
-__device__ __forceinline__ void load_sums(uint32_t tcol, uint32_t (&sum)[8][16]) {
-#pragma unroll
-  for (int b = 0; b < 8; ++b) ptx::tmem_ld_32x32b_x16(tcol + b * 16, sum[b]);
-  ptx::tmem_wait_ld();
-}
-__device__ __forceinline__ void add_sums(uint32_t tcol, uint32_t (&sum)[8][16]) {
-#pragma unroll
-  for (int b = 0; b < 8; ++b) {
-    uint32_t raw[16];
-    ptx::tmem_ld_32x32b_x16(tcol + b * 16, raw);
-    ptx::tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      sum[b][i] = __float_as_uint(__uint_as_float(sum[b][i]) + __uint_as_float(raw[i]));
-  }
-}
-__device__ __forceinline__ void store_sums(uint32_t tcol, const uint32_t (&sum)[8][16]) {
-#pragma unroll
-  for (int b = 0; b < 8; ++b) ptx::tmem_st_32x32b_x16(tcol + b * 16, sum[b]);
-  ptx::tmem_wait_st();
-}
-
 // Statistics of this thread's row over its part of the tile's columns.  Of two
 // parts the second leaves them in the accumulator's columns, which it has read,
 // and the first joins and writes both: `handed` is completed by the one and
@@ -347,67 +314,6 @@ __device__ __forceinline__ void gradient_chunk(uint32_t (&raw)[32], int base, in
 #pragma unroll
     for (int i = 0; i < 32; ++i) raw[i] = i < limit ? raw[i] : 0u;
   }
-}
-
-// This warp's staging buffer, once the last copy out of it has been read.
-__device__ __forceinline__ void stage_row(uint8_t* buf, int lane, const uint32_t (&w)[32]) {
-  if (lane == 0) ptx::bulk_wait_group_read<0>();
-  __syncwarp();
-#pragma unroll
-  for (int ch = 0; ch < 8; ++ch)
-    *reinterpret_cast<uint4*>(buf + sw128_offset(lane, ch * 16)) =
-        make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-}
-
-// One 64-column chunk of 16-bit words of 32 rows, to the tensor at (col, row0, plane).
-__device__ __forceinline__ void store_words(const uint32_t (&w)[32], const CUtensorMap* mapC, int col, int row0,
-                                            int plane, uint8_t* buf, int lane) {
-  stage_row(buf, lane, w);
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    ptx::tma_store_3d(mapC, col, row0, plane, ptx::smem_u32(buf));
-    ptx::bulk_commit_group();
-  }
-}
-
-// The same to rows that are not 16-byte aligned: the warp writes one row after
-// another, neighbouring lanes neighbouring elements.
-__device__ __forceinline__ void store_words_plain(const uint32_t (&w)[32], uint16_t* dst, int64_t ld, int rows,
-                                                  int cols, int granule, uint8_t* buf, int lane) {
-  stage_row(buf, lane, w);
-  __syncwarp();
-  if (granule >= 4) {
-    const bool whole = 2 * lane + 2 <= cols, single = !whole && 2 * lane < cols;
-#pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 8) {
-      uint32_t v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint32_t*>(buf + sw128_offset(r0 + i, lane * 4));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint16_t* row = dst + (r0 + i) * ld;
-        if (r0 + i < rows && whole) reinterpret_cast<uint32_t*>(row)[lane] = v[i];
-        if (r0 + i < rows && single) row[2 * lane] = static_cast<uint16_t>(v[i] & 0xFFFFu);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 8) {
-      uint16_t v[8][2];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          v[i][h] = *reinterpret_cast<const uint16_t*>(buf + sw128_offset(r0 + i, (lane + 32 * h) * 2));
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (r0 + i < rows && lane + 32 * h < cols) dst[(r0 + i) * ld + lane + 32 * h] = v[i][h];
-    }
-  }
-  __syncwarp();
 }
 
 // dz of 32 rows, 64 columns at a time; `own`: a second time, times the row's own
@@ -880,36 +786,6 @@ __global__ void __launch_bounds__(head_threads(PARTS), 1)
     head_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ CUtensorMap mapC, const __grid_constant__ HeadArgs args) {
   head_product<MODE, PLANES, PARTS, CHUNKS>(mapA, mapB, mapC, args, blockIdx.x / 2, gridDim.x / 2);
-}
-
-// Launch of a kernel on `pairs` clusters of two CTAs, dependent on the kernel before it.
-template <typename... Params, typename... Args>
-cudaError_t launch_pairs(void (*kernel)(Params...), int smem, int threads, std::atomic<uint64_t>& done_mask, int pairs,
-                         cudaStream_t stream, const Args&... args) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(done_mask.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    done_mask.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int MODE, int PLANES, int PARTS, bool CHUNKS>

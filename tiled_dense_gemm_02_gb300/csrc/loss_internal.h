@@ -18,7 +18,11 @@ int host_cuda_fail(cudaError_t e, const char* what);
 // Cached 3-D tensor map, 128-byte swizzle, zero fill (after host_device).
 // type: 0 bf16, 1 f16, 2 f32.
 int host_map_3d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t depth,
-                int64_t pitch_bytes, int64_t depth_bytes, uint32_t box_cols, uint32_t box_rows);
+                int64_t pitch_bytes, int64_t depth_bytes, uint32_t box_cols, uint32_t box_rows,
+                uint32_t box_depth = 1);
+// The same for one matrix; a box one row high serves gathering copies.
+int host_map_2d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t pitch_bytes,
+                uint32_t box_cols, uint32_t box_rows);
 // Adds tensor-core launches to the host counters.
 void host_count_launches(int n);
 bool host_ranges_overlap(uint64_t a0, uint64_t a1, uint64_t b0, uint64_t b1);

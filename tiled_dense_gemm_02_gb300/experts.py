@@ -2,8 +2,8 @@
 tokens to experts, and the experts' products.
 
 The first functions carry the names of the C ABI and only marshal arguments;
-``route_experts`` and ``route_experts_backward`` take torch tensors (torch
-supplies device memory and streams only).
+``route_experts``, ``expert_mlp`` and their ``_backward`` take torch tensors
+(torch supplies device memory and streams only).
 """
 from __future__ import annotations
 
@@ -19,7 +19,10 @@ ROUTE_MAX_EXPERTS, ROUTE_MAX_K, ROUTE_MAX_GROUPS = 1024, 32, 32  # TGEMM_ROUTE_M
 ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1                              # enum tgemm_route_scoring
 ROUTE_GROUP_MAX, ROUTE_GROUP_TOP2 = 0, 1                         # enum tgemm_route_group_score
 
-EXPERT_EXPORTS = ("tgemm_route_forward", "tgemm_route_backward")
+MAX_EXPERTS = 1024                                               # of the products
+
+EXPERT_EXPORTS = ("tgemm_route_forward", "tgemm_route_backward", "tgemm_experts_workspace_size",
+                  "tgemm_experts_saved_size", "tgemm_experts_forward", "tgemm_experts_backward")
 
 
 class RouteOptions(ctypes.Structure):
@@ -29,9 +32,19 @@ class RouteOptions(ctypes.Structure):
                 ("reserved", ctypes.c_int * 2)]
 
 
+class ExpertsOptions(ctypes.Structure):
+    """struct tgemm_experts_options"""
+    _fields_ = [("wait_timeout_us", ctypes.c_int), ("reserved", ctypes.c_int * 3)]
+
+
 def _declare(lib):
-    i64, vp, ip = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
-    op = ctypes.POINTER(RouteOptions)
+    i64, vp, ip, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    op, eo, sizes = ctypes.POINTER(RouteOptions), ctypes.POINTER(ExpertsOptions), [ctypes.c_int64] * 5
+    lib.tgemm_experts_workspace_size.argtypes = [ip] + sizes + [vp, i64, vp, i64, ip, ctypes.POINTER(sz)]
+    lib.tgemm_experts_saved_size.argtypes = sizes + [ip, ctypes.POINTER(sz)]
+    lib.tgemm_experts_forward.argtypes = sizes + [vp, i64, vp, i64, vp, i64, vp, vp, ip, eo, vp, i64, vp, sz, vp, sz, vp]
+    lib.tgemm_experts_backward.argtypes = sizes + [vp, i64, vp, i64, vp, i64, vp, vp, sz, vp, i64, ip, eo, vp, i64, vp,
+                                                   i64, vp, i64, vp, vp, sz, vp]
     lib.tgemm_route_forward.argtypes = [i64, i64, i64, vp, i64, ip, vp, op, vp, vp, vp]
     lib.tgemm_route_backward.argtypes = [i64, i64, i64, vp, i64, ip, vp, vp, op, vp, i64, vp]
     for name in EXPERT_EXPORTS:
@@ -42,12 +55,12 @@ def _declare(lib):
 _lib = _declare(library())
 
 
-def _opts(options):
+def _opts(options, kind=RouteOptions):
     if options is None:
         return None
-    if isinstance(options, RouteOptions):
+    if isinstance(options, kind):
         return ctypes.byref(options)
-    o = RouteOptions()
+    o = kind()
     for k, v in dict(options).items():
         setattr(o, k, v)
     return ctypes.byref(o)
@@ -61,6 +74,38 @@ def route_forward(T, E, k, logits, ld, dtype, bias, ids, weights, options=None, 
 def route_backward(T, E, k, logits, ld, dtype, ids, grad, d_logits, ld_out, options=None, stream=0) -> int:
     """tgemm_route_backward"""
     return _lib.tgemm_route_backward(T, E, k, logits, ld, dtype, ids, grad, _opts(options), d_logits, ld_out, stream)
+
+
+def experts_workspace_size(backward, T, E, k, D, F, w_in, ld_in, w_out, ld_out, dtype):
+    """tgemm_experts_workspace_size: (status, bytes); needs no GPU."""
+    n = ctypes.c_size_t(0)
+    st = _lib.tgemm_experts_workspace_size(int(backward), T, E, k, D, F, w_in, ld_in, w_out, ld_out, dtype,
+                                           ctypes.byref(n))
+    return st, n.value
+
+
+def experts_saved_size(T, E, k, D, F, dtype):
+    """tgemm_experts_saved_size: (status, bytes); needs no GPU."""
+    n = ctypes.c_size_t(0)
+    st = _lib.tgemm_experts_saved_size(T, E, k, D, F, dtype, ctypes.byref(n))
+    return st, n.value
+
+
+def experts_forward(T, E, k, D, F, x, ldx, w_in, ld_in, w_out, ld_out, ids, weights, dtype, out, ldo, saved=0,
+                    saved_bytes=0, options=None, workspace=0, workspace_bytes=0, stream=0) -> int:
+    """tgemm_experts_forward: device pointers as ints; returns the status."""
+    return _lib.tgemm_experts_forward(T, E, k, D, F, x, ldx, w_in, ld_in, w_out, ld_out, ids, weights, dtype,
+                                      _opts(options, ExpertsOptions), out, ldo, saved, saved_bytes, workspace,
+                                      workspace_bytes, stream)
+
+
+def experts_backward(T, E, k, D, F, x, ldx, w_in, ld_in, w_out, ld_out, weights, saved, saved_bytes, grad, ldg, dtype,
+                     dx, lddx, dw_in, ldd_in, dw_out, ldd_out, d_weights, options=None, workspace=0, workspace_bytes=0,
+                     stream=0) -> int:
+    """tgemm_experts_backward: outputs that are not wanted may be 0."""
+    return _lib.tgemm_experts_backward(T, E, k, D, F, x, ldx, w_in, ld_in, w_out, ld_out, weights, saved, saved_bytes,
+                                       grad, ldg, dtype, _opts(options, ExpertsOptions), dx, lddx, dw_in, ldd_in, dw_out,
+                                       ldd_out, d_weights, workspace, workspace_bytes, stream)
 
 
 # ------------------------------------------------------------ torch functions
@@ -201,3 +246,180 @@ def route_experts_backward(logits, ids, grad_weights, *, scoring="softmax", reno
     if st != OK:
         raise TgemmError(st, "tgemm_route_backward")
     return out
+
+
+# ------------------------------------------------------- the experts' products
+
+@functools.lru_cache(maxsize=1024)
+def _experts_size(backward, sizes, in_offset, ld_in, out_offset, ld_out, code):
+    st, n = experts_workspace_size(backward, *sizes, in_offset, ld_in, out_offset, ld_out, code)
+    if st != OK:
+        raise TgemmError(st, "tgemm_experts_workspace_size")
+    return n
+
+
+@functools.lru_cache(maxsize=1024)
+def _saved_size(sizes, code):
+    st, n = experts_saved_size(*sizes, code)
+    if st != OK:
+        raise TgemmError(st, "tgemm_experts_saved_size")
+    return n
+
+
+def _expert_rows(name, t, rows, cols):
+    """Row pitch of the matrices [E, rows, cols] of one weight, which follow one another."""
+    each, ld, step = t.stride()
+    E = t.shape[0]
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    if rows < 2:
+        ld = each if E > 1 else cols
+    if E > 1 and each != rows * ld:
+        raise ValueError(f"{name}: each expert's rows must follow the last one's")
+    if ld < cols:
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return ld
+
+
+def _experts(hidden, w_in, w_out, ids, weights, backward, workspace):
+    """Checks what both calls share: (torch, device, (T, E, k, D, F), dtype code, matrices' arguments, ids, weights,
+    workspace, its bytes)."""
+    import torch
+    if hidden.dim() != 2 or w_in.dim() != 3 or w_out.dim() != 3 or ids.dim() != 2:
+        raise ValueError("hidden [T, D], w_in [E, 2 F, D], w_out [E, D, F] and ids [T, k] must have these dimensions")
+    T, D = hidden.shape
+    E, _, F = w_out.shape
+    k = ids.shape[1]
+    dtype = hidden.dtype
+    code = {torch.bfloat16: BF16, torch.float16: F16}.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype: {dtype} (bf16 or fp16)")
+    if w_in.shape != (E, 2 * F, D) or w_out.shape != (E, D, F) or w_in.dtype != dtype or w_out.dtype != dtype:
+        raise ValueError(f"w_in must be [E, 2 F, {D}] and w_out [E, {D}, F] {dtype}, got {tuple(w_in.shape)} "
+                         f"{w_in.dtype} and {tuple(w_out.shape)} {w_out.dtype}")
+    device = hidden.get_device()
+    if device < 0 or w_in.get_device() != device or w_out.get_device() != device:
+        raise ValueError("hidden, w_in and w_out must be on one CUDA device")
+    shape = torch.Size((T, k))
+    ids = _places("ids", ids, shape, torch.int64, device)
+    weights = _places("weights", weights, shape, torch.float32, device)
+    sizes = (T, E, k, D, F)
+    ldx, ld_in, ld_out = _pitch("hidden", hidden, T, D), _expert_rows("w_in", w_in, 2 * F, D), \
+        _expert_rows("w_out", w_out, D, F)
+    p_in, p_out = w_in.data_ptr(), w_out.data_ptr()
+    need = _experts_size(backward, sizes, p_in % 16, ld_in, p_out % 16, ld_out, code)
+    workspace, need = _lent("workspace", workspace, need, device, hidden)
+    return torch, device, sizes, code, (hidden.data_ptr(), ldx, p_in, ld_in, p_out, ld_out), ids, weights, workspace, need
+
+
+def _lent(name, buffer, need, device, like):
+    """A buffer of at least `need` bytes, and its size."""
+    import torch
+    if buffer is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device), need
+    if buffer.get_device() != device or buffer.dtype != torch.uint8 or not buffer.is_contiguous() or \
+            buffer.numel() < need:
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {need} bytes on the device of hidden")
+    return buffer, buffer.numel()
+
+
+@functools.cache
+def _mlp_node():
+    """The torch function that records experts' products whose operands require a gradient."""
+    import torch
+
+    class ExpertMLP(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, hidden, w_in, w_out, ids, weights, workspace):
+            ctx.set_materialize_grads(False)
+            out, saved = _mlp(hidden, w_in, w_out, ids, weights, True, workspace)
+            ctx.save_for_backward(hidden, w_in, w_out, ids, weights, saved)
+            ctx.mark_non_differentiable(saved)
+            return out, saved
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad, _):
+            if grad is None:
+                return (None,) * 6
+            hidden, w_in, w_out, ids, weights, saved = ctx.saved_tensors
+            want = ctx.needs_input_grad
+            dx, dw_in, dw_out, dw = expert_mlp_backward(hidden, w_in, w_out, ids, weights, saved, grad,
+                                                        want_hidden=want[0], want_in=want[1], want_out=want[2],
+                                                        want_weights=want[4])
+            return dx, dw_in, dw_out, None, dw, None
+
+    return ExpertMLP
+
+
+def _mlp(hidden, w_in, w_out, ids, weights, save, workspace):
+    torch, device, sizes, code, matrices, ids, weights, workspace, need = \
+        _experts(hidden, w_in, w_out, ids, weights, False, workspace)
+    T, D = hidden.shape
+    out = torch.empty((T, D), dtype=hidden.dtype, device=hidden.device)
+    saved = torch.empty(_saved_size(sizes, code), dtype=torch.uint8, device=hidden.device) if save else None
+    st = _guarded(torch, device, _lib.tgemm_experts_forward,
+                  sizes + matrices + (ids.data_ptr(), weights.data_ptr(), code, None, out.data_ptr(), D,
+                                      saved.data_ptr() if save else 0, saved.numel() if save else 0,
+                                      workspace.data_ptr(), need, _current_stream(torch, device)))
+    if st != OK:
+        raise TgemmError(st, "tgemm_experts_forward")
+    return out, saved
+
+
+@_on_stream
+def expert_mlp(hidden, w_in, w_out, ids, weights, *, save=False, workspace=None):
+    """``out[t] = sum_j weights[t, j] * w_out[e] @ (silu(g) * u)`` with ``e =
+    ids[t, j]`` and ``(g, u) = w_in[e] @ hidden[t]``: ``(out [T, D], saved)``.
+
+    hidden [T, D], w_in [E, 2 F, D] (F gates, then F ups) and w_out [E, D, F] in
+    bf16 or fp16, unit column stride, any row stride; ids [T, k] int64 (below 0:
+    unused place) and weights [T, k] float32, as route_experts gives them.  A
+    row without a used place gives 0, whatever hidden holds there.
+
+    save=True keeps what expert_mlp_backward takes (a uint8 tensor: the rows'
+    order, and g and u in float32); otherwise saved is None.  If hidden, a weight or
+    weights requires a gradient, so does out, and torch's backward pass makes
+    the backward call.
+    """
+    if hidden.requires_grad or w_in.requires_grad or w_out.requires_grad or weights.requires_grad:
+        import torch
+        if torch.is_grad_enabled():
+            return _mlp_node().apply(hidden, w_in, w_out, ids, weights, workspace)
+    return _mlp(hidden, w_in, w_out, ids, weights, bool(save), workspace)
+
+
+@_on_stream
+def expert_mlp_backward(hidden, w_in, w_out, ids, weights, saved, grad_out, *, want_hidden=True, want_in=True,
+                        want_out=True, want_weights=True, workspace=None):
+    """Gradients ``(d_hidden, d_w_in, d_w_out, d_weights)`` of ``sum(grad_out *
+    out)``: in the operands' type, d_weights in float32.  saved from the forward
+    call with the same operands; grad_out [T, D] in their type, unit column stride.  An
+    unwanted gradient is not computed (None).  What it returns is outside
+    torch's graph."""
+    torch, device, sizes, code, matrices, ids, weights, workspace, need = \
+        _experts(hidden, w_in, w_out, ids, weights, True, workspace)
+    T, E, k, D, F = sizes
+    if saved is None:
+        raise ValueError("saved is what expert_mlp(..., save=True) gives")
+    saved, kept = _lent("saved", saved, _saved_size(sizes, code), device, hidden)
+    if grad_out.shape != hidden.shape or grad_out.dtype != hidden.dtype or grad_out.get_device() != device:
+        raise ValueError(f"grad_out must be [{T}, {D}] {hidden.dtype} on the device of hidden")
+    if T and (grad_out.stride(1) != 1 and D > 1 or grad_out.stride(0) < D and T > 1):
+        grad_out = grad_out.contiguous()
+
+    def make(wanted, *shape, dtype=hidden.dtype):
+        return torch.empty(shape, dtype=dtype, device=hidden.device) if wanted else None
+
+    def at(t):
+        return 0 if t is None else t.data_ptr()
+
+    dx, dw_in, dw_out = make(want_hidden, T, D), make(want_in, E, 2 * F, D), make(want_out, E, D, F)
+    dw = make(want_weights, T, k, dtype=torch.float32)
+    st = _guarded(torch, device, _lib.tgemm_experts_backward,
+                  sizes + matrices + (weights.data_ptr(), saved.data_ptr(), kept, grad_out.data_ptr(),
+                                      _pitch("grad_out", grad_out, T, D), code, None, at(dx), D, at(dw_in), D, at(dw_out),
+                                      F, at(dw), workspace.data_ptr(), need, _current_stream(torch, device)))
+    if st != OK:
+        raise TgemmError(st, "tgemm_experts_backward")
+    return dx, dw_in, dw_out, dw
