@@ -2,9 +2,9 @@
 // layout of the workspace and of what is kept for the backward call, and the
 // order of launches.
 //
-// Forward:  sort of the places  UP  DOWN  join
-// Backward: [scale of fp16 gradients]  DH  DX  join  DIN  DOUT
-// (experts_rows.cu and experts_gemm.cuh hold the kernels.)  Operands whose rows are
+// Forward:  sort of the places  [gather of x]  UP  DOWN  join
+// Backward: [scale of fp16 gradients]  gather of grad  DH  DX  join  [gather of x]  DIN  DOUT
+// (experts_rows.cu and experts_gemm.cuh hold the kernels.)  Weights whose rows are
 // not 16-byte aligned are copied to an aligned pitch first.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -28,7 +28,9 @@ constexpr int64_t kMaxExtent = int64_t(1) << 31;
 // the sum, an eighth of that on average where signs are mixed.  16-bit results: 256
 // steps stay below 2^-15.  g, u and d_out W_out, whose product is the fp32
 // gradient of the weights: 32 steps, below 3.9e-6 and about 2e-7 on average each.
-constexpr int kChunk = 64, kExactChunk = 8;
+constexpr int kChunk = 64, kExactChunk = 4;
+// Places up to which UP gathers x's rows by itself.
+constexpr int64_t kGatherPlaces = kPlaceBlock;
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -123,7 +125,7 @@ SavedLayout plan_saved(int64_t T, int64_t E, int64_t k, int64_t F) {
 struct Layout {
   bool copy_in, copy_out;  // weights off the 16-byte grid
   RowsLayout rows;
-  int64_t partial, x, g, w_in, w_out, h, dgu, y, dots, largest, scale;
+  int64_t partial, x, w_in, w_out, h, dgu, y, dots, largest, scale;
   int64_t ldx, ldh, ld_dgu, ldy, ld_in, ld_out;
   int parts;               // DH: dots of a row
   int64_t total;
@@ -142,20 +144,19 @@ Layout plan_layout(bool backward, int64_t T, int64_t E, int64_t k, int64_t D, in
   l.ld_in = round_up(D, 8);
   l.ld_out = round_up(F, 8);
   l.parts = static_cast<int>(ceil_div(F, 256) * 8);
-  l.x = take(T * l.ldx * 2);
+  l.x = take(rows * l.ldx * 2);
   l.w_in = take(l.copy_in ? E * 2 * F * l.ld_in * 2 : 0);
   l.w_out = take(l.copy_out ? E * D * l.ld_out * 2 : 0);
   l.h = take(rows * l.ldh * 2);
   l.y = take(rows * l.ldy * 4);
   if (backward) {
-    l.g = take(T * l.ldx * 2);
     l.dgu = take(rows * l.ld_dgu * 2);
     l.dots = take(rows * l.parts * 4);
     l.largest = take(kScaleBlocks * 4);
     l.scale = take(8);
   } else {
     l.rows = plan_rows(take, places, E);
-    l.partial = take(places > kPlaceBlock ? ceil_div(places, kPlaceBlock) * E * 4 : 0);
+    l.partial = take(order_blocks(places) * E * 4);
   }
   l.total = take.at;
   return l;
@@ -299,7 +300,7 @@ class Experts {
   }
 
   int forward() {
-    TGEMM_TRY(operands());
+    TGEMM_TRY(weights());
     OrderArgs o = {};
     o.ids = c_.ids;
     o.places = c_.T * c_.k;
@@ -309,24 +310,31 @@ class Experts {
     o.rows = a_.rows;
     o.rows.partial = reinterpret_cast<int*>(ws_ + l_.partial);
     TGEMM_CUDA(launch_order(o, c_.stream), "order launch");
-    CUtensorMap ma, mb;
+    ExpertMaps m;
     {
       ExpertArgs a = a_;
-      TGEMM_TRY(host_map_3d(&ma, type_, w_in_.p, c_.D, c_.F, 2 * c_.E, w_in_.ld * 2, c_.F * w_in_.ld * 2, kTileK, 16, 2));
-      TGEMM_TRY(host_map_2d(&mb, type_, x_.p, c_.D, c_.T, x_.ld * 2, 64, 1));
+      TGEMM_TRY(host_map_3d(&m.a, type_, w_in_.p, c_.D, c_.F, 2 * c_.E, w_in_.ld * 2, c_.F * w_in_.ld * 2, kTileK, 16, 2));
+      a.gather = o.places <= kGatherPlaces && host_granule(c_.x, c_.ldx, 2) == 16;
+      if (a.gather) {
+        TGEMM_TRY(host_map_2d(&m.b, type_, c_.x, c_.D, c_.T, c_.ldx * 2, 64, 1));
+        m.b16 = m.b;
+      } else {
+        TGEMM_TRY(gather(c_.x, c_.ldx));
+        TGEMM_TRY(token_maps(m, ws_ + l_.x, c_.D, l_.ldx));
+      }
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 128));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
       a.chunk = c_.saved ? kExactChunk : kChunk;
-      TGEMM_TRY(launch(launch_expert_up, ma, mb, mb, a, tokens(a)));
+      TGEMM_TRY(launch(launch_expert_up, m, a, tokens(a)));
     }
     {
       ExpertArgs a = a_;
-      TGEMM_TRY(host_map_3d(&ma, type_, w_out_.p, c_.F, c_.D, c_.E, w_out_.ld * 2, c_.D * w_out_.ld * 2, kTileK, kTileM));
-      TGEMM_TRY(host_map_3d(&mb, type_, a.h, c_.F, rows_max_, 1, a.ldh * 2, 0, kTileK, 16));
+      TGEMM_TRY(host_map_3d(&m.a, type_, w_out_.p, c_.F, c_.D, c_.E, w_out_.ld * 2, c_.D * w_out_.ld * 2, kTileK, kTileM));
+      TGEMM_TRY(token_maps(m, a.h, c_.F, a.ldh));
       a.m_blocks = static_cast<int>(ceil_div(c_.D, 256));
       a.k_blocks = static_cast<int>(ceil_div(c_.F, kTileK));
       a.chunk = kChunk;
-      TGEMM_TRY(launch(launch_expert_down, ma, mb, mb, a, tokens(a)));
+      TGEMM_TRY(launch(launch_expert_down, m, a, tokens(a)));
     }
     JoinArgs j = {};
     j.weights = c_.weights;
@@ -336,23 +344,31 @@ class Experts {
   }
 
   int backward() {
-    TGEMM_TRY(operands());
-    CUtensorMap ma, mb, mc;
+    TGEMM_TRY(weights());
+    ExpertMaps m;
     if (type_ == 1) {
       float* scale = reinterpret_cast<float*>(ws_ + l_.scale);
-      TGEMM_CUDA(launch_grad_scale(g_.p, c_.T, a_.D, g_.ld, reinterpret_cast<unsigned int*>(ws_ + l_.largest), scale,
+      TGEMM_CUDA(launch_grad_scale(c_.grad, c_.T, a_.D, c_.ldg, reinterpret_cast<unsigned int*>(ws_ + l_.largest), scale,
                                    c_.stream),
                  "gradient scale launch");
       a_.scale = scale;
     }
+    TGEMM_TRY(gather(c_.grad, c_.ldg));
     {
       ExpertArgs a = a_;
-      TGEMM_TRY(host_map_3d(&ma, type_, w_out_.p, c_.F, c_.D, c_.E, w_out_.ld * 2, c_.D * w_out_.ld * 2, 64, kTileK));
-      TGEMM_TRY(host_map_2d(&mb, type_, g_.p, c_.D, c_.T, g_.ld * 2, 64, 1));
+      TGEMM_TRY(host_map_3d(&m.a, type_, w_out_.p, c_.F, c_.D, c_.E, w_out_.ld * 2, c_.D * w_out_.ld * 2, 64, kTileK));
+      TGEMM_TRY(token_maps(m, ws_ + l_.x, c_.D, l_.ldx));
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 256));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
       a.chunk = kExactChunk;
-      TGEMM_TRY(launch(launch_expert_dh, ma, mb, mb, a, tokens(a)));
+      TGEMM_TRY(launch(launch_expert_dh, m, a, tokens(a)));
+    }
+    if (c_.dw_out) {
+      ExpertArgs a = a_;
+      TGEMM_TRY(map_rows(&m.a, ws_ + l_.x, c_.D, l_.ldx, 64));
+      TGEMM_TRY(map_rows(&m.b, a.h, c_.F, a.ldh, 64));
+      TGEMM_TRY(gradient_out(a, m, c_.dw_out, c_.ldd_out, c_.D, c_.F));
+      TGEMM_TRY(launch(launch_expert_dout, m, a, int64_t(a.E) * a.m_blocks * a.n_blocks));
     }
     JoinArgs j = {};
     if (c_.d_weights) {
@@ -362,12 +378,12 @@ class Experts {
     }
     if (c_.dx) {
       ExpertArgs a = a_;
-      TGEMM_TRY(host_map_3d(&ma, type_, w_in_.p, c_.D, 2 * c_.F, c_.E, w_in_.ld * 2, 2 * c_.F * w_in_.ld * 2, 64, kTileK));
-      TGEMM_TRY(host_map_3d(&mb, type_, a.dgu, 2 * c_.F, rows_max_, 1, a.ld_dgu * 2, 0, kTileK, 16));
+      TGEMM_TRY(host_map_3d(&m.a, type_, w_in_.p, c_.D, 2 * c_.F, c_.E, w_in_.ld * 2, 2 * c_.F * w_in_.ld * 2, 64, kTileK));
+      TGEMM_TRY(token_maps(m, a.dgu, 2 * c_.F, a.ld_dgu));
       a.m_blocks = static_cast<int>(ceil_div(c_.D, 256));
       a.k_blocks = static_cast<int>(ceil_div(2 * c_.F, kTileK));
       a.chunk = kChunk;
-      TGEMM_TRY(launch(launch_expert_dx, ma, mb, mb, a, tokens(a)));
+      TGEMM_TRY(launch(launch_expert_dx, m, a, tokens(a)));
       j.scale = a_.scale;
       j.out = c_.dx;
       j.ld_out = c_.lddx;
@@ -375,17 +391,11 @@ class Experts {
     if (c_.dx || c_.d_weights) TGEMM_TRY(join(j));
     if (c_.dw_in) {
       ExpertArgs a = a_;
-      TGEMM_TRY(host_map_3d(&ma, type_, a.dgu, 2 * c_.F, rows_max_, 1, a.ld_dgu * 2, 0, 64, kTileK));
-      TGEMM_TRY(host_map_2d(&mb, type_, x_.p, c_.D, c_.T, x_.ld * 2, 64, 1));
-      TGEMM_TRY(gradient_out(a, mc, ma, c_.dw_in, c_.ldd_in, 2 * c_.F, c_.D));
-      TGEMM_TRY(launch(launch_expert_din, ma, mb, mc, a, int64_t(a.E) * a.m_blocks * a.n_blocks));
-    }
-    if (c_.dw_out) {
-      ExpertArgs a = a_;
-      TGEMM_TRY(host_map_2d(&ma, type_, g_.p, c_.D, c_.T, g_.ld * 2, 64, 1));
-      TGEMM_TRY(host_map_3d(&mb, type_, a.h, c_.F, rows_max_, 1, a.ldh * 2, 0, 64, kTileK));
-      TGEMM_TRY(gradient_out(a, mc, ma, c_.dw_out, c_.ldd_out, c_.D, c_.F));
-      TGEMM_TRY(launch(launch_expert_dout, ma, mb, mc, a, int64_t(a.E) * a.m_blocks * a.n_blocks));
+      TGEMM_TRY(gather(c_.x, c_.ldx));
+      TGEMM_TRY(map_rows(&m.a, a.dgu, 2 * c_.F, a.ld_dgu, 64));
+      TGEMM_TRY(map_rows(&m.b, ws_ + l_.x, c_.D, l_.ldx, 64));
+      TGEMM_TRY(gradient_out(a, m, c_.dw_in, c_.ldd_in, 2 * c_.F, c_.D));
+      TGEMM_TRY(launch(launch_expert_din, m, a, int64_t(a.E) * a.m_blocks * a.n_blocks));
     }
     return TGEMM_OK;
   }
@@ -394,11 +404,25 @@ class Experts {
   int64_t tokens(const ExpertArgs& a) const { return most_tiles(c_.T * c_.k, c_.E) * a.m_blocks; }
 
   template <typename Launch>
-  int launch(Launch function, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& m, const ExpertArgs& args,
-             int64_t units) {
+  int launch(Launch function, const ExpertMaps& m, const ExpertArgs& args, int64_t units) {
     const int pairs = static_cast<int>(std::min<int64_t>(pairs_, units));
-    TGEMM_CUDA(function(a, b, m, args, pairs, c_.stream), "expert launch");
+    TGEMM_CUDA(function(m, args, pairs, c_.stream), "expert launch");
     host_count_launches(1);
+    return TGEMM_OK;
+  }
+
+  // A sorted matrix, in boxes of 64 columns.
+  int map_rows(CUtensorMap* m, const void* p, int64_t cols, int64_t ld, uint32_t box_rows) {
+    return host_map_3d(m, type_, p, cols, rows_max_, 1, ld * 2, 0, 64, box_rows);
+  }
+  int token_maps(ExpertMaps& m, const void* p, int64_t cols, int64_t ld) {
+    TGEMM_TRY(map_rows(&m.b, p, cols, ld, 64));
+    return map_rows(&m.b16, p, cols, ld, 16);
+  }
+  int gather(const void* x, int64_t ld) {
+    TGEMM_CUDA(launch_gather_rows(a_.rows, rows_max_, x, ld, host_granule(x, ld, 2), a_.D, ws_ + l_.x, l_.ldx, sms_,
+                                  c_.stream),
+               "gather launch");
     return TGEMM_OK;
   }
 
@@ -414,17 +438,17 @@ class Experts {
     return TGEMM_OK;
   }
 
-  int gradient_out(ExpertArgs& a, CUtensorMap& m, const CUtensorMap& unused, void* out, int64_t ld, int64_t M, int64_t N) {
+  int gradient_out(ExpertArgs& a, ExpertMaps& m, void* out, int64_t ld, int64_t M, int64_t N) {
     a.m_blocks = static_cast<int>(ceil_div(M, 256));
     a.n_blocks = static_cast<int>(ceil_div(N, 256));
     a.chunk = kChunk;
     a.out = out;
     a.ld_out = ld;
     a.store_granule = host_granule(out, ld, 2);
-    m = unused;
+    m.b16 = m.c = m.a;  // not used, unless c is set here
     if (a.store_granule < 16) return TGEMM_OK;
     a.store_granule = 0;
-    return host_map_3d(&m, type_, out, N, M, c_.E, ld * 2, M * ld * 2, 64, 32);
+    return host_map_3d(&m.c, type_, out, N, M, c_.E, ld * 2, M * ld * 2, 64, 32);
   }
 
   int aligned(Operand& o, const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t at, int64_t ld_copy) {
@@ -437,12 +461,9 @@ class Experts {
                "repack launch");
     return TGEMM_OK;
   }
-  int operands() {
-    TGEMM_TRY(aligned(x_, c_.x, c_.ldx, c_.T, c_.D, l_.x, l_.ldx));
+  int weights() {
     TGEMM_TRY(aligned(w_in_, c_.w_in, c_.ld_in, c_.E * 2 * c_.F, c_.D, l_.w_in, l_.ld_in));
-    TGEMM_TRY(aligned(w_out_, c_.w_out, c_.ld_out, c_.E * c_.D, c_.F, l_.w_out, l_.ld_out));
-    if (c_.backward) TGEMM_TRY(aligned(g_, c_.grad, c_.ldg, c_.T, c_.D, l_.g, l_.ldx));
-    return TGEMM_OK;
+    return aligned(w_out_, c_.w_out, c_.ld_out, c_.E * c_.D, c_.F, l_.w_out, l_.ld_out);
   }
 
   const Call& c_;
@@ -453,7 +474,7 @@ class Experts {
   int sms_, pairs_, type_;
   int64_t rows_max_;
   ExpertArgs a_;
-  Operand x_, w_in_, w_out_, g_;
+  Operand w_in_, w_out_;
 };
 
 int run_experts(const Call& c) {

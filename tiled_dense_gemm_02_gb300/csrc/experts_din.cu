@@ -3,9 +3,8 @@
 
 namespace tgemm {
 
-cudaError_t launch_expert_din(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                           int pairs, cudaStream_t stream) {
-  return launch_expert<EXPERT_DIN>(a, b, c, args, pairs, stream);
+cudaError_t launch_expert_din(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream) {
+  return launch_expert<EXPERT_DIN>(maps, args, pairs, stream);
 }
 
 }  // namespace tgemm

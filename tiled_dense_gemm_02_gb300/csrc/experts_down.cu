@@ -3,9 +3,8 @@
 
 namespace tgemm {
 
-cudaError_t launch_expert_down(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                           int pairs, cudaStream_t stream) {
-  return launch_expert<EXPERT_DOWN>(a, b, c, args, pairs, stream);
+cudaError_t launch_expert_down(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream) {
+  return launch_expert<EXPERT_DOWN>(maps, args, pairs, stream);
 }
 
 }  // namespace tgemm

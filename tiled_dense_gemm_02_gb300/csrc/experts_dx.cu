@@ -3,9 +3,8 @@
 
 namespace tgemm {
 
-cudaError_t launch_expert_dx(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                           int pairs, cudaStream_t stream) {
-  return launch_expert<EXPERT_DX>(a, b, c, args, pairs, stream);
+cudaError_t launch_expert_dx(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream) {
+  return launch_expert<EXPERT_DX>(maps, args, pairs, stream);
 }
 
 }  // namespace tgemm

@@ -14,14 +14,16 @@
 // The weight is the M operand and the tokens are N, which tcgen05 takes in steps of
 // 32: an expert with a handful of rows computes 32 columns, not 256, and the same
 // kernel serves one token (bound by the weights' bytes, each read once) and a
-// training batch (bound by the MMAs).  Rows of x and d_out are fetched where they
-// lie by gathering bulk-tensor copies, four rows each (tile::gather4); every lane of
-// the producer warp issues the copies of its own four rows.  No operand is
-// transposed or copied in memory.
+// training batch (bound by the MMAs).  Rows of x and d_out lie sorted in the
+// workspace (gather_rows); no operand is transposed in memory.  Calls of few rows
+// read x where it lies (GATHER) by gathering bulk-tensor copies of four rows each
+// (tile::gather4), every lane of the producer warp issuing its own: one launch
+// less, but from some hundred rows a tile on these copies are the bound (8192 tokens
+// in 64 experts: UP 1260 us, and 560 with sorted rows).
 //
 // UP interleaves 16 gate rows with their 16 ups, so that a warp's 32 lanes
-// of tensor memory hold both of 16 features: lanes l and l + 16 exchange one
-// value of two columns and each finishes one.
+// of tensor memory hold both of 16 features: of 16 columns, lane l finishes
+// the first eight and lane l + 16 the others, after an exchange of eight values.
 //
 // The adder of tcgen05.mma truncates: a step moves the sum towards 0 by up to 2^-23
 // of it.  Sums leave tensor memory every `chunk` stages (four steps each) and are
@@ -62,13 +64,6 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar_cluster)
       : "memory");
-}
-
-// Bytes that gathers of both CTAs bring for 256 columns from `first` on: 64 columns are
-// fetched where any is inside.  (What lies outside is some earlier stage's: its
-// sums are not stored.)
-__device__ __forceinline__ uint32_t gathered_bytes(int first, int columns) {
-  return static_cast<uint32_t>(min(4, (columns - first + 63) / 64)) * 8192u;
 }
 
 // A tile of a product: block mb of M, and N's columns (rows row0.. of the sorted
@@ -138,29 +133,52 @@ __device__ __forceinline__ void whole_sums(uint32_t tcol, int blocks, const uint
   ptx::tmem_wait_st();
 }
 
-__device__ __forceinline__ uint16_t to_half_word(float v, int bf16) {
-  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// Neighbouring lanes hold neighbouring features of two rows: word = {row 0, row 1}.
+// Each stores both features of one row, or, where a row's features do not pair
+// up in words (`pairs` false), both rows of its own.
+__device__ __forceinline__ void store_rows(uint16_t* p, int64_t ld, uint32_t word, int feature, int F, bool pairs, int lane) {
+  if (pairs) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 1);
+    const bool odd = (lane & 1) != 0;
+    const uint32_t both = odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+    if (feature < F) *reinterpret_cast<uint32_t*>(p + (odd ? ld - 1 : 0)) = both;
+  } else if (feature < F) {
+    p[0] = static_cast<uint16_t>(word & 0xFFFFu);
+    p[ld] = static_cast<uint16_t>(word >> 16);
+  }
 }
 
 // 16 columns of UP: gates in lanes 0..15, ups in lanes 16..31 -> h, and g and u.
 // `row`: the columns' first row, of which `valid` are no filling (which gets 0).
+// g and u lie as {g, u} x features x 4 rows for every four rows: 16 bytes a lane.
 __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertArgs& a, int feature, int64_t row,
-                                          int valid, int lane) {
+                                          int valid, int fmt, int lane) {
   const bool low = lane < 16;
-  uint16_t* h = static_cast<uint16_t*>(a.h) + row * a.ldh + feature;
-  float* gu = a.gu ? a.gu + row * 2 * a.ldg + feature : nullptr;
+  const int c0 = low ? 0 : 8;
+  uint16_t* h = static_cast<uint16_t*>(a.h) + (row + c0) * a.ldh + feature;
+  float g[8], u[8], x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, low ? v[2 * i + 1] : v[2 * i], 16);
-    const float g = __uint_as_float(low ? v[2 * i] : got), u = __uint_as_float(low ? got : v[2 * i + 1]);
-    const int c = 2 * i + (low ? 0 : 1);
-    if (feature < a.F) {
-      const float x = __fdividef(g, 1.0f + __expf(-g)) * u;
-      h[c * a.ldh] = c < valid ? to_half_word(x, a.bf16) : uint16_t(0);
-      if (gu && c < valid) {
-        __stcs(gu + c * 2 * a.ldg, g);
-        __stcs(gu + c * 2 * a.ldg + a.ldg, u);
-      }
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, low ? v[8 + i] : v[i], 16);
+    g[i] = __uint_as_float(low ? v[i] : got);
+    u[i] = __uint_as_float(low ? got : v[8 + i]);
+    x[i] = g[i] * fast_sigmoid(g[i]) * u[i];
+  }
+  if (valid < 16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = c0 + i < valid ? x[i] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    store_rows(h + i * a.ldh, a.ldh, pack_pair(x[i], x[i + 1], fmt), feature, a.F, (a.F & 1) == 0, lane);
+  if (a.gu && feature < a.F) {
+    float4* gu = reinterpret_cast<float4*>(a.gu) + (row + c0) / 4 * 2 * a.ldg + feature;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      __stcs(gu + q * 2 * a.ldg, make_float4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]));
+      __stcs(gu + (q * 2 + 1) * a.ldg, make_float4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]));
     }
   }
 }
@@ -168,32 +186,40 @@ __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertA
 // 16 columns of DH: v = d_out W_out of this lane's feature.
 //   s = sigmoid(g):  dg = w v u s (1 + g (1 - s)),  du = w v g s,  h = g s u
 __device__ __forceinline__ void finish_dh(const uint32_t (&v)[16], const ExpertArgs& a, int feature, int64_t row,
-                                          int valid, int lane, int part, int parts, float scale) {
-  const bool in = feature < a.F;
-  const float* gu = a.gu + row * 2 * a.ldg + feature;
+                                          int valid, int fmt, int lane, int part, int parts, float scale) {
+  const float4* gu = reinterpret_cast<const float4*>(a.gu) + row / 4 * 2 * a.ldg + feature;
   uint16_t* dgu = static_cast<uint16_t*>(a.dgu) + row * a.ld_dgu + feature;
   uint16_t* hw = static_cast<uint16_t*>(a.h) + row * a.ldh + feature;
   const float mine = lane < 16 && lane < valid ? __ldg(a.weights + __ldcg(a.rows.place + row + lane)) : 0.0f;
-  float g[16], u[16], dot[16];
+  const bool pairs = (a.F & 1) == 0;
+  float dot[16];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    const bool there = in && c < valid;
-    g[c] = there ? __ldcs(gu + c * 2 * a.ldg) : 0.0f;
-    u[c] = there ? __ldcs(gu + c * 2 * a.ldg + a.ldg) : 0.0f;
-  }
+  for (int q = 0; q < 4; ++q) {
+    float4 g4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u4 = g4;
+    if (feature < a.F) {
+      g4 = __ldcs(gu + q * 2 * a.ldg);
+      u4 = __ldcs(gu + (q * 2 + 1) * a.ldg);
+    }
+    float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w}, dg[4], du[4], h[4];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    const float w = __shfl_sync(0xffffffffu, mine, c);
-    const float d = __uint_as_float(v[c]);
-    const float s = 1.0f / (1.0f + expf(-g[c]));
-    const float gate = g[c] * s, h = gate * u[c];
-    const bool there = in && c < valid;
-    dot[c] = there ? h * d : 0.0f;
-    if (in) {
-      const float wd = w * d * scale;
-      dgu[c * a.ld_dgu] = there ? to_half_word(wd * u[c] * (s + gate * (1.0f - s)), a.bf16) : uint16_t(0);
-      dgu[c * a.ld_dgu + a.F] = there ? to_half_word(wd * gate, a.bf16) : uint16_t(0);
-      hw[c * a.ldh] = there ? to_half_word(w * h, a.bf16) : uint16_t(0);
+    for (int i = 0; i < 4; ++i) {
+      const int c = 4 * q + i;
+      float d = __uint_as_float(v[c]);
+      if (c >= valid) g[i] = u[i] = d = 0.0f;
+      const float w = __shfl_sync(0xffffffffu, mine, c);
+      const float s = fast_sigmoid(g[i]), gate = g[i] * s, wd = w * d * scale;
+      h[i] = gate * u[i];
+      dot[c] = h[i] * d;
+      h[i] *= w;
+      dg[i] = wd * u[i] * fmaf(gate, 1.0f - s, s);
+      du[i] = wd * gate;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const int c = 4 * q + i;
+      store_rows(dgu + c * a.ld_dgu, a.ld_dgu, pack_pair(dg[i], dg[i + 1], fmt), feature, a.F, pairs, lane);
+      store_rows(dgu + c * a.ld_dgu + a.F, a.ld_dgu, pack_pair(du[i], du[i + 1], fmt), feature, a.F, pairs, lane);
+      store_rows(hw + c * a.ldh, a.ldh, pack_pair(h[i], h[i + 1], fmt), feature, a.F, pairs, lane);
     }
   }
   // sums over the 32 lanes: a lane keeps half of its columns at each exchange, and
@@ -254,10 +280,10 @@ __device__ __forceinline__ void finish_weight(uint32_t tcol, bool sums, const Ex
   }
 }
 
-template <int MODE>
+template <int MODE, bool GATHER>
 __global__ void __launch_bounds__(kExpertThreads, 1)
-    expert_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                  const __grid_constant__ CUtensorMap mapC, const __grid_constant__ ExpertArgs args) {
+    expert_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs args) {
+  const CUtensorMap &mapA = maps.a, &mapB = maps.b, &mapB16 = maps.b16, &mapC = maps.c;
   constexpr int STAGES = expert_stages(MODE);
   constexpr bool GRADIENT = weight_gradient(MODE);
   constexpr int ACC = 256;
@@ -298,6 +324,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   if (warp == 0 && lane == 0) {
     ptx::tma_prefetch_desc(&mapA);
     ptx::tma_prefetch_desc(&mapB);
+    if (!GRADIENT && !GATHER) ptx::tma_prefetch_desc(&mapB16);
     if (GRADIENT) ptx::tma_prefetch_desc(&mapC);
   }
   if (warp == 1) {
@@ -326,68 +353,45 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       next = units.get(args, i + workers);
       const int stages = units.stages(args, u);
       const int half = GRADIENT ? kTileM : u.n / 2;  // this CTA's columns
+      // a CTA's columns in boxes of 64 rows, and of 16 for the rest
+      const int wide = half / 64, boxes = wide + (half & 63) / 16;
+      const int box0 = lane < wide ? 64 * lane : 64 * wide + 16 * (lane - wide);
       int4 rows = make_int4(0, 0, 0, 0);
-      if constexpr (MODE == EXPERT_UP || MODE == EXPERT_DH) {
-        if (4 * lane < half)
-          rows = __ldcg(reinterpret_cast<const int4*>(args.rows.token + u.row0 + cta * half + 4 * lane));
-      }
-      // gradients: lane l gathers rows 4 (l mod 16).. of a stage, for column block l / 16
-      const int4* tokens = reinterpret_cast<const int4*>(args.rows.token + u.row0) + (lane & 15);
-      if constexpr (GRADIENT) {
-        if (stages > 0) rows = __ldcg(4 * (lane & 15) < u.n ? tokens : tokens - (lane & 15));
-      }
+      if (GATHER && 4 * lane < half)
+        rows = __ldcg(reinterpret_cast<const int4*>(args.rows.token + u.row0 + cta * half + 4 * lane));
       for (int it = 0; it < stages; ++it) {
-        int4 ahead = rows;
-        if constexpr (GRADIENT) {  // past the expert's rows: any of them, no MMA reads it
-          if (it + 1 < stages)
-            ahead = __ldcg((it + 1) * kTileK + 4 * (lane & 15) < u.n ? tokens + (it + 1) * (kTileK / 4)
-                                                                     : tokens - (lane & 15));
-        }
         if (!warp_wait(ptx::smem_u32(&empty[stage]), phase ^ 1u, ctl, SITE_PRODUCER_EMPTY)) {
           ok = false;
           break;
         }
         const uint32_t fb_local = ptx::smem_u32(&full[stage]);
         const uint32_t fb = ptx::mapa_shared(fb_local, 0);
-        if (leader && lane == 0) {
-          const uint32_t bytes = MODE == EXPERT_DIN    ? 2u * kSub + gathered_bytes(u.nb * 256, args.D)
-                                 : MODE == EXPERT_DOUT ? 2u * kSub + gathered_bytes(u.mb * 256, args.D)
-                                                       : 2u * (kSub + static_cast<uint32_t>(half) * 128u);
-          ptx::mbar_arrive_expect_tx(fb_local, bytes);
-        }
+        if (leader && lane == 0) ptx::mbar_arrive_expect_tx(fb_local, 2u * (kSub + static_cast<uint32_t>(half) * 128u));
         __syncwarp();
         const uint32_t sa = ptx::smem_u32(smem + stage * kStage), sb = sa + kSub;
-        const int k0 = it * kTileK;  // past the k axis: zeros
-        // the weight's 128 rows (gradients: 128 columns of M, 64 rows)
+        const int k0 = it * kTileK;  // past the k axis: zeros (gradients: other rows, which no MMA reads)
+        // 128 of the 256 of M
+        const int m0 = u.mb * 256 + cta * kTileM;
         if constexpr (MODE == EXPERT_UP) {
           if (lane < 4)
             ptx::tma_load_3d_pair(sa + lane * 4096, &mapA, k0, u.mb * kTileM + cta * 64 + lane * 16, 2 * u.expert, fb);
         } else if constexpr (MODE == EXPERT_DOWN) {
-          if (lane == 0) ptx::tma_load_3d_pair(sa, &mapA, k0, u.mb * 256 + cta * kTileM, u.expert, fb);
-        } else if constexpr (MODE == EXPERT_DH || MODE == EXPERT_DX) {
-          if (lane < 2)
-            ptx::tma_load_3d_pair(sa + lane * 8192, &mapA, u.mb * 256 + cta * kTileM + lane * 64, k0, u.expert, fb);
-        } else if constexpr (MODE == EXPERT_DIN) {
-          if (lane < 2)
-            ptx::tma_load_3d_pair(sa + lane * 8192, &mapA, u.mb * 256 + cta * kTileM + lane * 64, u.row0 + k0, 0, fb);
+          if (lane == 0) ptx::tma_load_3d_pair(sa, &mapA, k0, m0, u.expert, fb);
         } else {
-          const int col = u.mb * 256 + cta * kTileM + (lane >> 4) * 64;
-          if (col < args.D) tma_gather4_pair(sa + lane * 512, &mapA, col, rows, fb);
+          if (lane < 2)
+            ptx::tma_load_3d_pair(sa + lane * 8192, &mapA, m0 + lane * 64, GRADIENT ? u.row0 + k0 : k0,
+                                  GRADIENT ? 0 : u.expert, fb);
         }
-        // the tokens' rows (gradients: 128 columns of N, 64 rows)
-        if constexpr (MODE == EXPERT_UP || MODE == EXPERT_DH) {
-          if (4 * lane < half) tma_gather4_pair(sb + lane * 512, &mapB, k0, rows, fb);
-        } else if constexpr (MODE == EXPERT_DOWN || MODE == EXPERT_DX) {
-          if (16 * lane < half)
-            ptx::tma_load_3d_pair(sb + lane * 2048, &mapB, k0, u.row0 + cta * half + 16 * lane, 0, fb);
-        } else if constexpr (MODE == EXPERT_DIN) {
-          const int col = u.nb * 256 + cta * kTileM + (lane >> 4) * 64;
-          if (col < args.D) tma_gather4_pair(sb + lane * 512, &mapB, col, rows, fb);
-        } else {
+        // half of N
+        if constexpr (GRADIENT) {
           if (lane < 2)
             ptx::tma_load_3d_pair(sb + lane * 8192, &mapB, u.nb * 256 + cta * kTileM + lane * 64, u.row0 + k0, 0, fb);
+        } else if constexpr (GATHER) {
+          if (4 * lane < half) tma_gather4_pair(sb + lane * 512, &mapB, k0, rows, fb);
+        } else {
+          if (lane < boxes)
+            ptx::tma_load_3d_pair(sb + box0 * 128, lane < wide ? &mapB : &mapB16, k0, u.row0 + cta * half + box0, 0, fb);
         }
-        rows = ahead;
         filled |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) {
@@ -467,6 +471,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     const int quarter = warp & 3;          // tensor-memory lanes of this warp
     const int part = (warp - 2) / 4;       // its half of the columns
     uint8_t* buf = sC + (warp - 2) * 4096;
+    const int fmt = args.bf16 ? OUT_BF16 : OUT_F16;
     const float scale = MODE == EXPERT_DH && args.scale    ? __ldcg(args.scale)
                         : MODE == EXPERT_DIN && args.scale ? __ldcg(args.scale + 1)
                                                            : 1.0f;
@@ -528,9 +533,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           ptx::tmem_ld_32x32b_x16(tcol + b * 16, v);
           ptx::tmem_wait_ld();
           if constexpr (MODE == EXPERT_UP)
-            finish_up(v, args, m0, u.row0 + c0, valid, lane);
+            finish_up(v, args, m0, u.row0 + c0, valid, fmt, lane);
           else if constexpr (MODE == EXPERT_DH)
-            finish_dh(v, args, m0, u.row0 + c0, valid, lane, (u.mb * 2 + cta) * 4 + quarter, args.m_blocks * 8, scale);
+            finish_dh(v, args, m0, u.row0 + c0, valid, fmt, lane, (u.mb * 2 + cta) * 4 + quarter, args.m_blocks * 8, scale);
           else
             finish_y(v, args, m0, u.row0 + c0, valid);
         }
@@ -550,11 +555,10 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   }
 }
 
-template <int MODE>
-cudaError_t launch_expert(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                          int pairs, cudaStream_t stream) {
+template <int MODE, bool GATHER = false>
+cudaError_t launch_expert(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream) {
   static std::atomic<uint64_t> done_mask{0};
-  return launch_pairs(expert_kernel<MODE>, expert_smem(MODE), kExpertThreads, done_mask, pairs, stream, a, b, c, args);
+  return launch_pairs(expert_kernel<MODE, GATHER>, expert_smem(MODE), kExpertThreads, done_mask, pairs, stream, maps, args);
 }
 
 }  // namespace

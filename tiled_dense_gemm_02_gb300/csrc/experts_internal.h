@@ -14,12 +14,12 @@ namespace tgemm {
 // A place is one (token, j) of ids [T, k], numbered t * k + j; a used place is a row
 // of the sorted matrices.  Each expert's rows are neighbours, in the order of
 // their places, and fill up to a multiple of kRowPad rows; the filling has the
-// token of the expert's first row and no place.  Token tiles are the
+// token of the expert's first row and no place, and is 0 in the sorted matrices.  Token tiles are the
 // products' columns: an expert's rows in even parts of at most kTokenTile.
 constexpr int kRowPad = 32;
 constexpr int kTokenTile = 256;
 constexpr int kMaxExperts = 1024;
-constexpr int kPlaceBlock = 2048;  // places of one block of the sort
+constexpr int kPlaceBlock = 2048;  // places of one block of the sort, at most
 
 struct ExpertRows {
   int* head;       // {tiles, rows with the filling}
@@ -38,7 +38,13 @@ struct OrderArgs {
   int T, E, k;
   ExpertRows rows;
 };
+int order_blocks(int64_t places);
 cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream);
+
+// out[r] (pitch ld_out, 16-byte aligned) = the row of x of sorted row r's token; the
+// filling is 0.  granule: alignment of x's rows in bytes.
+cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const void* x, int64_t ldx, int granule, int D,
+                               void* out, int64_t ld_out, int sms, cudaStream_t stream);
 
 // out[t] = sum over t's rows of weight * y[row] (weights null: of y[row]), rounded
 // to type (0 bf16, 1 f16); a place of no such expert: NaN.  dots not null: d_weights
@@ -85,10 +91,11 @@ struct ExpertArgs {
   int k_blocks;            // 64-deep stages (gradients of the weights: the rows')
   int chunk;               // stages summed in tensor memory, at most
   int bf16;
+  int gather;              // UP: rows of x where they lie
   ExpertRows rows;
   void* h;                 // UP: h; DH: weight * h
   int64_t ldh;
-  float* gu;               // UP: g and u where kept, else null; DH: read.  Row r: g at gu[r * 2 * ldg], u ldg further
+  float* gu;               // UP: g and u where kept, else null; DH: read.  [row / 4][g, u][feature, pitch ldg][row % 4]
   int64_t ldg;
   void* dgu;               // DH
   int64_t ld_dgu;
@@ -104,17 +111,15 @@ struct ExpertArgs {
   unsigned int* status;
 };
 
-cudaError_t launch_expert_up(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                             int pairs, cudaStream_t stream);
-cudaError_t launch_expert_down(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                               const ExpertArgs& args, int pairs, cudaStream_t stream);
-cudaError_t launch_expert_dh(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                             int pairs, cudaStream_t stream);
-cudaError_t launch_expert_dx(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                             int pairs, cudaStream_t stream);
-cudaError_t launch_expert_din(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                              int pairs, cudaStream_t stream);
-cudaError_t launch_expert_dout(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                               const ExpertArgs& args, int pairs, cudaStream_t stream);
+// Operand A, B (token products: boxes of 64 rows, and of 16), and where DIN and DOUT store.
+struct ExpertMaps {
+  CUtensorMap a, b, b16, c;
+};
+cudaError_t launch_expert_up(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_expert_down(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_expert_dh(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_expert_dx(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_expert_din(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream);
+cudaError_t launch_expert_dout(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream);
 
 }  // namespace tgemm

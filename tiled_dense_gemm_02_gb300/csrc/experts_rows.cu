@@ -1,14 +1,16 @@
-// What runs between the experts' products: places sorted by expert, rows joined
-// back into tokens, and the scale of fp16 gradients (experts_internal.h).
+// What runs between the experts' products: places sorted by expert, rows gathered
+// in that order and joined back into tokens, and the scale of fp16 gradients
+// (experts_internal.h).
 //
-// The sort counts: every warp takes 256 neighbouring places, counts them by
-// expert, and after the counts are summed up places them in their order, so the
+// The sort counts: every warp takes neighbouring places, counts them by expert,
+// and after the counts are summed up places them in their order, so the
 // sorted order is that of the places, whatever the timing.  Up to kPlaceBlock
 // places take one block and one launch (a decoding step's latency); more take three:
 // counts per block, one block that sums them up and lists the tiles, placement.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <climits>
 
 #include "experts_internal.h"
@@ -18,7 +20,6 @@ namespace tgemm {
 namespace {
 
 constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
-constexpr int kWarpPlaces = kPlaceBlock / kSortWarps;
 constexpr int kOwnExperts = kMaxExperts / kSortThreads;  // experts of a thread, neighbours
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -29,16 +30,14 @@ __device__ __forceinline__ int expert_of(const OrderArgs& a, int64_t place) {
   return id < 0 ? -1 : id < a.E ? static_cast<int>(id) : -2;
 }
 
-// counts[warp][e] of the block's places (zeroed here).
-__device__ __forceinline__ void count_places(const OrderArgs& a, int64_t base, int* counts) {
+// counts[warp][e] of the block's places (zeroed here), `each` neighbours a warp.
+__device__ __forceinline__ void count_places(const OrderArgs& a, int64_t base, int each, int* counts) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) counts[i] = 0;
   __syncthreads();
-#pragma unroll 1
-  for (int r = 0; r < kWarpPlaces; r += 32) {
-    const int64_t first = base + warp * kWarpPlaces + r;
-    if (first >= a.places) break;
-    const int e = expert_of(a, first + lane);
+#pragma unroll 2
+  for (int r = 0; r < each; r += 32) {
+    const int e = expert_of(a, base + warp * each + r + lane);
     if (e >= 0) atomicAdd(&counts[warp * a.E + e], 1);
   }
   __syncthreads();
@@ -67,8 +66,8 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* shared) {
 }
 
 // From the number of rows n[i] of experts kOwnExperts * threadIdx.x + i: first rows,
-// filling and tiles.  One block.
-__device__ __forceinline__ void list_tiles(const OrderArgs& a, const int (&n)[kOwnExperts], int* shared) {
+// filling and tiles.  One block.  Returns the thread's first row.
+__device__ __forceinline__ int list_tiles(const OrderArgs& a, const int (&n)[kOwnExperts], int* shared) {
   int rows = 0, tiles = 0, padded[kOwnExperts], parts[kOwnExperts];
 #pragma unroll
   for (int i = 0; i < kOwnExperts; ++i) {
@@ -78,7 +77,8 @@ __device__ __forceinline__ void list_tiles(const OrderArgs& a, const int (&n)[kO
     tiles += parts[i];
   }
   int all_rows, all_tiles;
-  int row = block_scan(rows, &all_rows, shared), tile = block_scan(tiles, &all_tiles, shared);
+  const int start = block_scan(rows, &all_rows, shared);
+  int row = start, tile = block_scan(tiles, &all_tiles, shared);
   if (threadIdx.x == 0) {
     a.rows.head[0] = all_tiles;
     a.rows.head[1] = all_rows;
@@ -103,17 +103,18 @@ __device__ __forceinline__ void list_tiles(const OrderArgs& a, const int (&n)[kO
     }
     row += padded[i];
   }
+  return start;
 }
 
 // Places the block's rows; next[warp][e] is where the warp's next row of expert e goes.
-__device__ __forceinline__ void place_rows(const OrderArgs& a, int64_t base, int* next) {
+__device__ __forceinline__ void place_rows(const OrderArgs& a, int64_t base, int each, int* next) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int ahead = expert_of(a, base + warp * each + lane);
 #pragma unroll 1
-  for (int r = 0; r < kWarpPlaces; r += 32) {
-    const int64_t first = base + warp * kWarpPlaces + r;
-    if (first >= a.places) break;
-    const int64_t place = first + lane;
-    const int e = expert_of(a, place);
+  for (int r = 0; r < each; r += 32) {
+    const int64_t place = base + warp * each + r + lane;
+    const int e = ahead;
+    if (r + 32 < each) ahead = expert_of(a, place + 32);
     const uint32_t same = __match_any_sync(kAll, e);
     if (e >= 0) {
       const int row = next[warp * a.E + e] + __popc(same & ((1u << lane) - 1u));
@@ -129,56 +130,62 @@ __device__ __forceinline__ void place_rows(const OrderArgs& a, int64_t base, int
   }
 }
 
-// The filling behind each expert's rows: its first row's token.
-__device__ __forceinline__ void fill_rows(const OrderArgs& a) {
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-    const int n = a.rows.count[e], row = a.rows.first[e];
-    if (n == 0) continue;
-    const int token = a.rows.token[row];
-    for (int r = row + n; r < row + (n + kRowPad - 1) / kRowPad * kRowPad; ++r) {
-      a.rows.token[r] = token;
-      a.rows.place[r] = -1;
-    }
+// The filling behind an expert's n rows.
+__device__ __forceinline__ void fill_rows(const OrderArgs& a, int row, int n, int token) {
+  const int end = row + (n + kRowPad - 1) / kRowPad * kRowPad;
+  for (int r = row + n; r < end; ++r) {
+    a.rows.token[r] = token;
+    a.rows.place[r] = -1;
   }
 }
 
-__global__ void __launch_bounds__(kSortThreads) order_kernel(const __grid_constant__ OrderArgs a) {
+__global__ void __launch_bounds__(kSortThreads) order_kernel(const __grid_constant__ OrderArgs a, int each) {
   extern __shared__ int counts[];  // kSortWarps x E
   __shared__ int scan[kSortWarps];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  count_places(a, 0, counts);
+  count_places(a, 0, each, counts);
   int n[kOwnExperts];
 #pragma unroll
   for (int i = 0; i < kOwnExperts; ++i) {
     const int e = kOwnExperts * threadIdx.x + i;
     n[i] = 0;
     if (e < a.E)
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) n[i] += counts[w * a.E + e];
   }
-  list_tiles(a, n, scan);
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-    int row = a.rows.first[e];
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = counts[w * a.E + e];
-      counts[w * a.E + e] = row;
-      row += c;
+  int row = list_tiles(a, n, scan);
+#pragma unroll
+  for (int i = 0; i < kOwnExperts; ++i) {
+    const int e = kOwnExperts * threadIdx.x + i;
+    if (e < a.E) {
+      int at = row;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int c = counts[w * a.E + e];
+        counts[w * a.E + e] = at;
+        at += c;
+      }
+      row += (n[i] + kRowPad - 1) / kRowPad * kRowPad;
     }
   }
   __syncthreads();
-  place_rows(a, 0, counts);
+  place_rows(a, 0, each, counts);
   __syncthreads();
-  fill_rows(a);
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    const int first = a.rows.first[e], rows = a.rows.count[e];
+    if (rows) fill_rows(a, first, rows, a.rows.token[first]);
+  }
 }
 
-__global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ OrderArgs a) {
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ OrderArgs a, int each) {
   extern __shared__ int counts[];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  count_places(a, static_cast<int64_t>(blockIdx.x) * kPlaceBlock, counts);
+  count_places(a, static_cast<int64_t>(blockIdx.x) * each * kSortWarps, each, counts);
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
     int n = 0;
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) n += counts[w * a.E + e];
     a.rows.partial[static_cast<int64_t>(blockIdx.x) * a.E + e] = n;
   }
@@ -194,12 +201,12 @@ __global__ void __launch_bounds__(kSortThreads) tiles_kernel(const __grid_consta
     int sum = 0;
     int* p = a.rows.partial + e;
     int b = 0;
-    for (; b + 8 <= blocks; b += 8) {
-      int v[8];
+    for (; b + 16 <= blocks; b += 16) {
+      int v[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __ldcg(p + static_cast<int64_t>(b + i) * a.E);
+      for (int i = 0; i < 16; ++i) v[i] = __ldcg(p + static_cast<int64_t>(b + i) * a.E);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 16; ++i) {
         p[static_cast<int64_t>(b + i) * a.E] = sum;
         sum += v[i];
       }
@@ -218,17 +225,23 @@ __global__ void __launch_bounds__(kSortThreads) tiles_kernel(const __grid_consta
     const int e = kOwnExperts * threadIdx.x + i;
     n[i] = e < a.E ? totals[e] : 0;
   }
-  list_tiles(a, n, scan);
+  int row = list_tiles(a, n, scan);
+#pragma unroll
+  for (int i = 0; i < kOwnExperts; ++i) {
+    fill_rows(a, row, n[i], 0);  // calls of so many places gather no rows by their tokens
+    row += (n[i] + kRowPad - 1) / kRowPad * kRowPad;
+  }
 }
 
-__global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_constant__ OrderArgs a) {
+__global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_constant__ OrderArgs a, int each) {
   extern __shared__ int counts[];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kPlaceBlock;
-  count_places(a, base, counts);
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * each * kSortWarps;
+  count_places(a, base, each, counts);
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
     int row = __ldcg(a.rows.first + e) + __ldcg(a.rows.partial + static_cast<int64_t>(blockIdx.x) * a.E + e);
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
       const int c = counts[w * a.E + e];
       counts[w * a.E + e] = row;
@@ -236,13 +249,47 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_consta
     }
   }
   __syncthreads();
-  place_rows(a, base, counts);
+  place_rows(a, base, each, counts);
 }
 
-__global__ void __launch_bounds__(kSortThreads) fill_kernel(const __grid_constant__ OrderArgs a) {
+// ----------------------------------------------------------------- gather
+// A block a row, 16 bytes a thread and step.  Bound by bytes: a token's row is
+// read k times, the later times from L2, and every sorted row is written once.
+constexpr int kGatherThreads = 128;
+
+template <int G>  // granule of x's rows in bytes
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const int* head, const int* token, const int* place,
+                                                                const uint16_t* x, int64_t ldx, int D, uint16_t* out,
+                                                                int64_t ld_out) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  fill_rows(a);
+  const int rows = __ldcg(head + 1);
+  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+    const bool filling = __ldcg(place + r) < 0;
+    const uint16_t* src = x + (filling ? 0 : __ldcg(token + r) * ldx);
+    uint16_t* dst = out + r * ld_out;
+#pragma unroll 2
+    for (int d = threadIdx.x * 8; d < D; d += kGatherThreads * 8) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (!filling) {
+        if (G == 16 && d + 8 <= D) {
+          v = __ldg(reinterpret_cast<const uint4*>(src + d));
+        } else {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          if (G >= 4 && d + 8 <= D) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(src + d) + i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (d + i < D) w[i / 2] |= static_cast<uint32_t>(__ldg(src + d + i)) << (16 * (i & 1));
+          }
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      *reinterpret_cast<uint4*>(dst + d) = v;  // D is filled up to the pitch, a multiple of 8
+    }
+  }
 }
 
 // ------------------------------------------------------------------- join
@@ -385,15 +432,35 @@ cudaError_t launch_next(void (*kernel)(Params...), dim3 grid, int threads, size_
 
 }  // namespace
 
+// Blocks of the sort: of 512 places, which many blocks make short, while one block can
+// sum up their counts in some microseconds, else of 2048.
+int order_blocks(int64_t places) {
+  if (places <= kPlaceBlock) return 1;
+  const int64_t each = places <= 128 * 1024 ? 512 : kPlaceBlock;
+  return static_cast<int>((places + each - 1) / each);
+}
+
 cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream) {
   const size_t smem = sizeof(int) * kSortWarps * a.E;  // at most 32 KB
-  if (a.places <= kPlaceBlock) return launch_next(order_kernel, dim3(1), kSortThreads, smem, stream, a);
-  const int blocks = static_cast<int>((a.places + kPlaceBlock - 1) / kPlaceBlock);
-  cudaError_t e = launch_next(count_kernel, dim3(blocks), kSortThreads, smem, stream, a);
+  const int blocks = order_blocks(a.places);
+  if (blocks == 1) {
+    const int each = static_cast<int>((a.places + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32);
+    return launch_next(order_kernel, dim3(1), kSortThreads, smem, stream, a, each);
+  }
+  const int each = (a.places <= 128 * 1024 ? 512 : kPlaceBlock) / kSortWarps;
+  cudaError_t e = launch_next(count_kernel, dim3(blocks), kSortThreads, smem, stream, a, each);
   if (e == cudaSuccess) e = launch_next(tiles_kernel, dim3(1), kSortThreads, 0, stream, a, blocks);
-  if (e == cudaSuccess) e = launch_next(place_kernel, dim3(blocks), kSortThreads, smem, stream, a);
-  if (e == cudaSuccess) e = launch_next(fill_kernel, dim3(1), kSortThreads, 0, stream, a);
+  if (e == cudaSuccess) e = launch_next(place_kernel, dim3(blocks), kSortThreads, smem, stream, a, each);
   return e;
+}
+
+cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const void* x, int64_t ldx, int granule, int D,
+                               void* out, int64_t ld_out, int sms, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most_rows, 16 * std::max(1, sms))), 1, 1);
+  const auto kernel = granule == 16 ? gather_kernel<16> : granule >= 4 ? gather_kernel<4> : gather_kernel<2>;
+  return launch_next(kernel, grid, kGatherThreads, 0, stream, static_cast<const int*>(rows.head),
+                     static_cast<const int*>(rows.token), static_cast<const int*>(rows.place),
+                     static_cast<const uint16_t*>(x), ldx, D, static_cast<uint16_t*>(out), ld_out);
 }
 
 cudaError_t launch_join(const JoinArgs& j, cudaStream_t stream) {

@@ -3,9 +3,9 @@
 
 namespace tgemm {
 
-cudaError_t launch_expert_up(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const ExpertArgs& args,
-                           int pairs, cudaStream_t stream) {
-  return launch_expert<EXPERT_UP>(a, b, c, args, pairs, stream);
+cudaError_t launch_expert_up(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream) {
+  return args.gather ? launch_expert<EXPERT_UP, true>(maps, args, pairs, stream)
+                     : launch_expert<EXPERT_UP>(maps, args, pairs, stream);
 }
 
 }  // namespace tgemm
