@@ -4,7 +4,7 @@
 namespace tgemm {
 
 cudaError_t launch_expert_down(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream) {
-  return launch_expert<EXPERT_DOWN>(maps, args, pairs, stream);
+  return launch_expert<EXPERT_DOWN, 2>(maps, args, pairs, stream);
 }
 
 }  // namespace tgemm

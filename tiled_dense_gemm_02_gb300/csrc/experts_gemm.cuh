@@ -31,7 +31,8 @@
 // last sum goes back to tensor memory, where the epilogues read it.
 //
 // Roles: warp 0 copies, warp 1 MMAs (one thread of the leader), warps 2.. epilogue,
-// eight of them: a quarter of the lanes and half of the columns each.  Every role
+// eight, or sixteen (DH, and UP where g and u are kept: they move most bytes): a
+// quarter of the lanes and a share of the columns each.  Every role
 // derives the units from the tile list, which is known on the device only.  Every
 // wait is bounded (tc_common.cuh).
 #pragma once
@@ -42,10 +43,10 @@
 namespace tgemm {
 namespace {
 
-constexpr int kEpilogueWarps = 8;
-constexpr int kExpertThreads = 32 * (2 + kEpilogueWarps);
 constexpr bool weight_gradient(int mode) { return mode == EXPERT_DIN || mode == EXPERT_DOUT; }
-constexpr int expert_epi_bytes(int mode) { return weight_gradient(mode) ? kEpilogueWarps * 4096 : 0; }
+// PARTS: epilogue warps per quarter of the lanes.
+constexpr int expert_threads(int parts) { return 32 * (2 + 4 * parts); }
+constexpr int expert_epi_bytes(int mode) { return weight_gradient(mode) ? 8 * 4096 : 0; }
 constexpr int expert_stages(int mode) {
   return (kSmemLimit - 1024 - expert_epi_bytes(mode) - kBarrierBytes) / kStage;
 }
@@ -107,29 +108,31 @@ struct ExpertUnits {
   }
 };
 
-// Sums of up to 128 columns of this thread's lane, `blocks` times 16.
-__device__ __forceinline__ void first_sums(uint32_t tcol, int blocks, uint32_t (&sum)[8][16]) {
+// Sums of this thread's lane in its MOST blocks of 16 columns, every STEP-th one.
+// (Blocks past the tile's columns are summed too: a condition on each would cost
+// the registers that hold them, and no other warp has them.)
+template <int STEP, int MOST>
+__device__ __forceinline__ void first_sums(uint32_t tcol, uint32_t (&sum)[MOST][16]) {
 #pragma unroll
-  for (int b = 0; b < 8; ++b)
-    if (b < blocks) ptx::tmem_ld_32x32b_x16(tcol + b * 16, sum[b]);
+  for (int b = 0; b < MOST; ++b) ptx::tmem_ld_32x32b_x16(tcol + b * STEP * 16, sum[b]);
   ptx::tmem_wait_ld();
 }
-__device__ __forceinline__ void more_sums(uint32_t tcol, int blocks, uint32_t (&sum)[8][16]) {
+template <int STEP, int MOST>
+__device__ __forceinline__ void more_sums(uint32_t tcol, uint32_t (&sum)[MOST][16]) {
 #pragma unroll
-  for (int b = 0; b < 8; ++b)
-    if (b < blocks) {
-      uint32_t raw[16];
-      ptx::tmem_ld_32x32b_x16(tcol + b * 16, raw);
-      ptx::tmem_wait_ld();
+  for (int b = 0; b < MOST; ++b) {
+    uint32_t raw[16];
+    ptx::tmem_ld_32x32b_x16(tcol + b * STEP * 16, raw);
+    ptx::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        sum[b][i] = __float_as_uint(__uint_as_float(sum[b][i]) + __uint_as_float(raw[i]));
-    }
+    for (int i = 0; i < 16; ++i)
+      sum[b][i] = __float_as_uint(__uint_as_float(sum[b][i]) + __uint_as_float(raw[i]));
+  }
 }
-__device__ __forceinline__ void whole_sums(uint32_t tcol, int blocks, const uint32_t (&sum)[8][16]) {
+template <int STEP, int MOST>
+__device__ __forceinline__ void whole_sums(uint32_t tcol, const uint32_t (&sum)[MOST][16]) {
 #pragma unroll
-  for (int b = 0; b < 8; ++b)
-    if (b < blocks) ptx::tmem_st_32x32b_x16(tcol + b * 16, sum[b]);
+  for (int b = 0; b < MOST; ++b) ptx::tmem_st_32x32b_x16(tcol + b * STEP * 16, sum[b]);
   ptx::tmem_wait_st();
 }
 
@@ -183,59 +186,66 @@ __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertA
   }
 }
 
-// 16 columns of DH: v = d_out W_out of this lane's feature.
+// 8 columns of DH: v = d_out W_out of this lane's feature.
 //   s = sigmoid(g):  dg = w v u s (1 + g (1 - s)),  du = w v g s,  h = g s u
-__device__ __forceinline__ void finish_dh(const uint32_t (&v)[16], const ExpertArgs& a, int feature, int64_t row,
-                                          int valid, int fmt, int lane, int part, int parts, float scale) {
+// `mine`: in lane first + c the weight of column c.
+__device__ __forceinline__ void finish_dh(const uint32_t (&v)[8], const ExpertArgs& a, int feature, int64_t row,
+                                          int valid, int fmt, int lane, float mine, int first, int part, int parts,
+                                          float scale) {
   const float4* gu = reinterpret_cast<const float4*>(a.gu) + row / 4 * 2 * a.ldg + feature;
   uint16_t* dgu = static_cast<uint16_t*>(a.dgu) + row * a.ld_dgu + feature;
   uint16_t* hw = static_cast<uint16_t*>(a.h) + row * a.ldh + feature;
-  const float mine = lane < 16 && lane < valid ? __ldg(a.weights + __ldcg(a.rows.place + row + lane)) : 0.0f;
   const bool pairs = (a.F & 1) == 0;
-  float dot[16];
+  float4 g4[2], u4[2];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float4 g4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u4 = g4;
+  for (int q = 0; q < 2; ++q) {
+    g4[q] = u4[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (feature < a.F) {
-      g4 = __ldcs(gu + q * 2 * a.ldg);
-      u4 = __ldcs(gu + (q * 2 + 1) * a.ldg);
+      g4[q] = __ldcs(gu + q * 2 * a.ldg);
+      u4[q] = __ldcs(gu + (q * 2 + 1) * a.ldg);
     }
-    float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w}, dg[4], du[4], h[4];
+  }
+  float dot[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = 4 * q + i;
-      float d = __uint_as_float(v[c]);
-      if (c >= valid) g[i] = u[i] = d = 0.0f;
-      const float w = __shfl_sync(0xffffffffu, mine, c);
-      const float s = fast_sigmoid(g[i]), gate = g[i] * s, wd = w * d * scale;
-      h[i] = gate * u[i];
-      dot[c] = h[i] * d;
-      h[i] *= w;
-      dg[i] = wd * u[i] * fmaf(gate, 1.0f - s, s);
-      du[i] = wd * gate;
-    }
+  for (int q = 0; q < 2; ++q) {
+    const float g[4] = {g4[q].x, g4[q].y, g4[q].z, g4[q].w}, u[4] = {u4[q].x, u4[q].y, u4[q].z, u4[q].w};
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       const int c = 4 * q + i;
-      store_rows(dgu + c * a.ld_dgu, a.ld_dgu, pack_pair(dg[i], dg[i + 1], fmt), feature, a.F, pairs, lane);
-      store_rows(dgu + c * a.ld_dgu + a.F, a.ld_dgu, pack_pair(du[i], du[i + 1], fmt), feature, a.F, pairs, lane);
-      store_rows(hw + c * a.ldh, a.ldh, pack_pair(h[i], h[i + 1], fmt), feature, a.F, pairs, lane);
+      float dg[2], du[2], h[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool in = c + e < valid;  // the filling: zeros, whatever the weights hold
+        const float d = in ? __uint_as_float(v[c + e]) : 0.0f;
+        const float gate = in ? g[i + e] : 0.0f, up = in ? u[i + e] : 0.0f;
+        const float w = __shfl_sync(0xffffffffu, mine, first + c + e);
+        const float s = fast_sigmoid(gate), silu = gate * s, wd = w * d * scale;
+        h[e] = silu * up;
+        dot[c + e] = h[e] * d;
+        h[e] *= w;
+        dg[e] = wd * up * fmaf(silu, 1.0f - s, s);
+        du[e] = wd * silu;
+      }
+      store_rows(dgu + c * a.ld_dgu, a.ld_dgu, pack_pair(dg[0], dg[1], fmt), feature, a.F, pairs, lane);
+      store_rows(dgu + c * a.ld_dgu + a.F, a.ld_dgu, pack_pair(du[0], du[1], fmt), feature, a.F, pairs, lane);
+      store_rows(hw + c * a.ldh, a.ldh, pack_pair(h[0], h[1], fmt), feature, a.F, pairs, lane);
     }
   }
   // sums over the 32 lanes: a lane keeps half of its columns at each exchange, and
-  // ends with one column's half
+  // ends with a quarter of one column's
 #pragma unroll
-  for (int width = 8; width >= 1; width >>= 1) {
-    const bool high = (lane & (2 * width)) != 0;
+  for (int width = 4; width >= 1; width >>= 1) {
+    const bool high = (lane & (4 * width)) != 0;
 #pragma unroll
     for (int c = 0; c < width; ++c) {
-      const float got = __shfl_xor_sync(0xffffffffu, high ? dot[c] : dot[c + width], 2 * width);
+      const float got = __shfl_xor_sync(0xffffffffu, high ? dot[c] : dot[c + width], 4 * width);
       dot[c] = (high ? dot[c + width] : dot[c]) + got;
     }
   }
-  const float sum = dot[0] + __shfl_xor_sync(0xffffffffu, dot[0], 1);
-  const int c = lane >> 1;
-  if ((lane & 1) == 0 && c < valid) __stcg(a.dots + (row + c) * parts + part, sum);
+  float sum = dot[0] + __shfl_xor_sync(0xffffffffu, dot[0], 2);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  const int c = lane >> 2;
+  if ((lane & 3) == 0 && c < valid) __stcg(a.dots + (row + c) * parts + part, sum);
 }
 
 // 16 columns of DOWN or DX: fp32, one row's 32 neighbouring elements a store.
@@ -280,12 +290,13 @@ __device__ __forceinline__ void finish_weight(uint32_t tcol, bool sums, const Ex
   }
 }
 
-template <int MODE, bool GATHER>
-__global__ void __launch_bounds__(kExpertThreads, 1)
+template <int MODE, int PARTS, bool GATHER>
+__global__ void __launch_bounds__(expert_threads(PARTS), 1)
     expert_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs args) {
   const CUtensorMap &mapA = maps.a, &mapB = maps.b, &mapB16 = maps.b16, &mapC = maps.c;
   constexpr int STAGES = expert_stages(MODE);
   constexpr bool GRADIENT = weight_gradient(MODE);
+  static_assert(!GRADIENT || PARTS == 2, "staging of stores");
   constexpr int ACC = 256;
   constexpr uint32_t TMEM_COLS = 512;
   static_assert(expert_smem(MODE) <= kSmemLimit, "shared memory per CTA");
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&acc_full[b]), 1);
-      ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * kEpilogueWarps);
+      ptx::mbar_init(ptx::smem_u32(&acc_empty[b]), 2 * 4 * PARTS);
     }
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0u;
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   } else {
     // --------------------------------------------------------- epilogue
     const int quarter = warp & 3;          // tensor-memory lanes of this warp
-    const int part = (warp - 2) / 4;       // its half of the columns
+    const int part = (warp - 2) / 4;       // its share of the columns
     uint8_t* buf = sC + (warp - 2) * 4096;
     const int fmt = args.bf16 ? OUT_BF16 : OUT_F16;
     const float scale = MODE == EXPERT_DH && args.scale    ? __ldcg(args.scale)
@@ -493,23 +504,25 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     ExpertUnit next = units.get(args, worker);
     for (int i = worker; ok && i < units.count; i += workers) {
       const ExpertUnit u = next;
-      next = units.get(args, i + workers);
       const int stages = units.stages(args, u);
-      const int half = GRADIENT ? 128 : u.n / 2, blocks = half / 16;  // this warp's columns
+      // this warp's blocks of 16 columns: of a weight's gradient 128 neighbours, else every PARTS-th
+      constexpr int STEP = GRADIENT ? 1 : PARTS, MOST = 16 / PARTS;
+      const int block0 = GRADIENT ? part * MOST : part;
+      const int blocks = GRADIENT ? MOST : (u.n / 16 - part + PARTS - 1) / PARTS;
       uint32_t tcol = 0;
       if (!GRADIENT || stages > 0) {
-        tcol = taken() + part * half;
+        tcol = taken() + block0 * 16;
         int lo = args.chunk;  // end of the chunk at hand
         if (lo < stages && ok) {
-          uint32_t sum[8][16];
-          first_sums(tcol, blocks, sum);
+          uint32_t sum[MOST][16];
+          first_sums<STEP, MOST>(tcol, sum);
           given_back();
           for (lo += args.chunk;; lo += args.chunk) {
-            tcol = taken() + part * half;
+            tcol = taken() + block0 * 16;
             if (!ok) break;
-            more_sums(tcol, blocks, sum);
+            more_sums<STEP, MOST>(tcol, sum);
             if (lo >= stages) {
-              whole_sums(tcol, blocks, sum);
+              whole_sums<STEP, MOST>(tcol, sum);
               break;
             }
             given_back();
@@ -517,6 +530,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         }
         if (!ok) break;
       }
+      next = units.get(args, i + workers);  // under this epilogue; no register is its beside the sums
       if constexpr (GRADIENT) {
         const int M = MODE == EXPERT_DIN ? 2 * args.F : args.D, N = MODE == EXPERT_DIN ? args.D : args.F;
         finish_weight(tcol, stages > 0, args, u.expert, u.mb * 256 + cta * kTileM + quarter * 32, M,
@@ -525,19 +539,38 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       } else {
         const int m0 = MODE == EXPERT_UP ? u.mb * kTileM + cta * 64 + quarter * 16 + (lane & 15)
                                          : u.mb * 256 + cta * kTileM + quarter * 32 + lane;
+        // the weight of each of a block's rows, a lane each, a block ahead
+        const auto weight_of = [&](int b) {
+          const int c = (part + b * PARTS) * 16 + lane;
+          return lane < 16 && b < blocks && c < u.valid
+                     ? __ldg(args.weights + __ldcg(args.rows.place + u.row0 + c))
+                     : 0.0f;
+        };
+        float ahead = MODE == EXPERT_DH ? weight_of(0) : 0.0f;
 #pragma unroll 1
         for (int b = 0; b < blocks; ++b) {
-          const int c0 = part * half + b * 16;
+          const int c0 = (part + b * PARTS) * 16;
           const int valid = u.valid - c0;
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(tcol + b * 16, v);
-          ptx::tmem_wait_ld();
-          if constexpr (MODE == EXPERT_UP)
-            finish_up(v, args, m0, u.row0 + c0, valid, fmt, lane);
-          else if constexpr (MODE == EXPERT_DH)
-            finish_dh(v, args, m0, u.row0 + c0, valid, fmt, lane, (u.mb * 2 + cta) * 4 + quarter, args.m_blocks * 8, scale);
-          else
-            finish_y(v, args, m0, u.row0 + c0, valid);
+          if constexpr (MODE == EXPERT_DH) {
+            const float mine = ahead;
+            ahead = weight_of(b + 1);
+#pragma unroll
+            for (int half = 0; half < 16; half += 8) {
+              uint32_t v[8];
+              ptx::tmem_ld_32x32b_x8(tcol + b * PARTS * 16 + half, v);
+              ptx::tmem_wait_ld();
+              finish_dh(v, args, m0, u.row0 + c0 + half, valid - half, fmt, lane, mine, half,
+                        (u.mb * 2 + cta) * 4 + quarter, args.m_blocks * 8, scale);
+            }
+          } else {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(tcol + b * PARTS * 16, v);
+            ptx::tmem_wait_ld();
+            if constexpr (MODE == EXPERT_UP)
+              finish_up(v, args, m0, u.row0 + c0, valid, fmt, lane);
+            else
+              finish_y(v, args, m0, u.row0 + c0, valid);
+          }
         }
         given_back();
       }
@@ -555,10 +588,11 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   }
 }
 
-template <int MODE, bool GATHER = false>
+template <int MODE, int PARTS, bool GATHER = false>
 cudaError_t launch_expert(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream) {
   static std::atomic<uint64_t> done_mask{0};
-  return launch_pairs(expert_kernel<MODE, GATHER>, expert_smem(MODE), kExpertThreads, done_mask, pairs, stream, maps, args);
+  return launch_pairs(expert_kernel<MODE, PARTS, GATHER>, expert_smem(MODE), expert_threads(PARTS), done_mask, pairs,
+                      stream, maps, args);
 }
 
 }  // namespace
