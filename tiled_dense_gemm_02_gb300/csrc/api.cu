@@ -722,9 +722,9 @@ CUtensorMapDataType tmap_type(int fmt_bytes, bool bf16) {
 // guarded by its own mutex.
 struct MapKey {
   uint64_t base;
-  uint64_t dims[3];
-  uint64_t strides[2];
-  uint32_t box[3];
+  uint64_t dims[5];
+  uint64_t strides[4];
+  uint32_t box[5];
   int32_t device, rank, type, swizzle;
 };
 struct MapSlot {
@@ -772,7 +772,7 @@ int encode_cached(CUtensorMap* map, CUtensorMapDataType type, int rank, const vo
     }
     if (slot.stamp < victim->stamp) victim = &slot;
   }
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   CUresult r = g_encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1114,6 +1114,18 @@ int host_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what);
 static CUtensorMapDataType host_map_type(int type) {
   return type == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                    : (type == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
+}
+
+int host_map(CUtensorMap* map, int type, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+             const uint32_t* box) {
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  return encode_cached(map, host_map_type(type), rank, base, d, st, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int host_map_3d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t depth,

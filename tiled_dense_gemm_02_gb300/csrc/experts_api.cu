@@ -125,22 +125,23 @@ SavedLayout plan_saved(int64_t T, int64_t E, int64_t k, int64_t F) {
 struct Layout {
   bool copy_in, copy_out;  // weights off the 16-byte grid
   RowsLayout rows;
-  int64_t partial, x, w_in, w_out, h, dgu, y, dots, largest, scale;
+  int64_t partial, x, w_in, w_out, h, dgu, y, y_scale, dots, largest, scale;
   int64_t ldx, ldh, ld_dgu, ldy, ld_in, ld_out;
   int parts;               // DH: dots of a row
   int64_t total;
 };
 Layout plan_layout(bool backward, int64_t T, int64_t E, int64_t k, int64_t D, int64_t F, const void* w_in,
-                   int64_t ld_in, const void* w_out, int64_t ld_out) {
+                   int64_t ld_in, const void* w_out, int64_t ld_out, int dtype) {
   Layout l = {};
   Taker take;
   const int64_t places = T * k, rows = most_rows(places, E);
   l.copy_in = host_granule(w_in, ld_in, 2) < 16;
   l.copy_out = host_granule(w_out, ld_out, 2) < 16;
-  l.ldx = round_up(D, 8);
-  l.ldh = round_up(F, 8);
-  l.ld_dgu = round_up(2 * F, 8);
-  l.ldy = round_up(D, 4);
+  // sorted matrices: whole blocks of 64 columns, which the weights' gradients copy
+  l.ldx = round_up(D, 64);
+  l.ldh = round_up(F, 64);
+  l.ld_dgu = round_up(2 * F, 64);
+  l.ldy = round_up(D, 64);
   l.ld_in = round_up(D, 8);
   l.ld_out = round_up(F, 8);
   l.parts = static_cast<int>(ceil_div(F, 256) * 8);
@@ -148,7 +149,8 @@ Layout plan_layout(bool backward, int64_t T, int64_t E, int64_t k, int64_t D, in
   l.w_in = take(l.copy_in ? E * 2 * F * l.ld_in * 2 : 0);
   l.w_out = take(l.copy_out ? E * D * l.ld_out * 2 : 0);
   l.h = take(rows * l.ldh * 2);
-  l.y = take(rows * l.ldy * 4);
+  l.y = take(rows * l.ldy * (dtype == TGEMM_BF16 ? 2 : 4));
+  l.y_scale = take(dtype == TGEMM_BF16 ? rows / 16 * (l.ldy / 32) * 4 : 0);
   if (backward) {
     l.dgu = take(rows * l.ld_dgu * 2);
     l.dots = take(rows * l.parts * 4);
@@ -210,7 +212,8 @@ int check_call(const Call& c) {
     if (c.saved && (reinterpret_cast<uint64_t>(c.saved) % 256 ||
                     c.saved_bytes < static_cast<size_t>(plan_saved(c.T, c.E, c.k, c.F).total)))
       return TGEMM_ERR_INVALID_VALUE;
-    const Layout l = plan_layout(c.backward, c.T, c.E, c.k, c.D, c.F, c.w_in, c.ld_in, c.w_out, c.ld_out);
+    const Layout l = plan_layout(c.backward, c.T, c.E, c.k, c.D, c.F, c.w_in, c.ld_in, c.w_out, c.ld_out,
+                                 c.dtype);
     if (!c.workspace || reinterpret_cast<uint64_t>(c.workspace) % 256 ||
         c.workspace_bytes < static_cast<size_t>(l.total))
       return TGEMM_ERR_INVALID_VALUE;
@@ -269,7 +272,7 @@ class Experts {
  public:
   Experts(const Call& c, int sms, int pairs, unsigned int* status)
       : c_(c),
-        l_(plan_layout(c.backward, c.T, c.E, c.k, c.D, c.F, c.w_in, c.ld_in, c.w_out, c.ld_out)),
+        l_(plan_layout(c.backward, c.T, c.E, c.k, c.D, c.F, c.w_in, c.ld_in, c.w_out, c.ld_out, c.dtype)),
         s_(plan_saved(c.T, c.E, c.k, c.F)),
         ws_(static_cast<char*>(c.workspace)),
         saved_(static_cast<char*>(c.saved)),
@@ -292,7 +295,8 @@ class Experts {
     a_.ld_dgu = l_.ld_dgu;
     a_.dots = reinterpret_cast<float*>(ws_ + l_.dots);
     a_.weights = c.weights;
-    a_.y = reinterpret_cast<float*>(ws_ + l_.y);
+    a_.y = ws_ + l_.y;
+    a_.y_scale = reinterpret_cast<float*>(ws_ + l_.y_scale);
     a_.ldy = l_.ldy;
     const int to_us = (c.opts && c.opts->wait_timeout_us) ? c.opts->wait_timeout_us : 2000000;
     a_.timeout_ns = static_cast<unsigned long long>(to_us) * 1000ull;
@@ -313,11 +317,11 @@ class Experts {
     ExpertMaps m;
     {
       ExpertArgs a = a_;
-      TGEMM_TRY(host_map_3d(&m.a, type_, w_in_.p, c_.D, c_.F, 2 * c_.E, w_in_.ld * 2, c_.F * w_in_.ld * 2, kTileK, 16, 2));
+      TGEMM_TRY(map_gates(m, a));
       a.gather = o.places <= kGatherPlaces && host_granule(c_.x, c_.ldx, 2) == 16;
       if (a.gather) {
         TGEMM_TRY(host_map_2d(&m.b, type_, c_.x, c_.D, c_.T, c_.ldx * 2, 64, 1));
-        m.b16 = m.b;
+        m.b32 = m.b16 = m.b;
       } else {
         TGEMM_TRY(gather(c_.x, c_.ldx));
         TGEMM_TRY(token_maps(m, ws_ + l_.x, c_.D, l_.ldx));
@@ -356,7 +360,7 @@ class Experts {
     TGEMM_TRY(gather(c_.grad, c_.ldg));
     {
       ExpertArgs a = a_;
-      TGEMM_TRY(host_map_3d(&m.a, type_, w_out_.p, c_.F, c_.D, c_.E, w_out_.ld * 2, c_.D * w_out_.ld * 2, 64, kTileK));
+      TGEMM_TRY(map_transposed(m, a, w_out_, c_.F, c_.D));
       TGEMM_TRY(token_maps(m, ws_ + l_.x, c_.D, l_.ldx));
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 256));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
@@ -365,8 +369,8 @@ class Experts {
     }
     if (c_.dw_out) {
       ExpertArgs a = a_;
-      TGEMM_TRY(map_rows(&m.a, ws_ + l_.x, c_.D, l_.ldx, 64));
-      TGEMM_TRY(map_rows(&m.b, a.h, c_.F, a.ldh, 64));
+      TGEMM_TRY(map_blocks(&m.a, ws_ + l_.x, c_.D, l_.ldx));
+      TGEMM_TRY(map_blocks(&m.b, a.h, c_.F, a.ldh));
       TGEMM_TRY(gradient_out(a, m, c_.dw_out, c_.ldd_out, c_.D, c_.F));
       TGEMM_TRY(launch(launch_expert_dout, m, a, int64_t(a.E) * a.m_blocks * a.n_blocks));
     }
@@ -378,7 +382,7 @@ class Experts {
     }
     if (c_.dx) {
       ExpertArgs a = a_;
-      TGEMM_TRY(host_map_3d(&m.a, type_, w_in_.p, c_.D, 2 * c_.F, c_.E, w_in_.ld * 2, 2 * c_.F * w_in_.ld * 2, 64, kTileK));
+      TGEMM_TRY(map_transposed(m, a, w_in_, c_.D, 2 * c_.F));
       TGEMM_TRY(token_maps(m, a.dgu, 2 * c_.F, a.ld_dgu));
       a.m_blocks = static_cast<int>(ceil_div(c_.D, 256));
       a.k_blocks = static_cast<int>(ceil_div(2 * c_.F, kTileK));
@@ -392,8 +396,8 @@ class Experts {
     if (c_.dw_in) {
       ExpertArgs a = a_;
       TGEMM_TRY(gather(c_.x, c_.ldx));
-      TGEMM_TRY(map_rows(&m.a, a.dgu, 2 * c_.F, a.ld_dgu, 64));
-      TGEMM_TRY(map_rows(&m.b, ws_ + l_.x, c_.D, l_.ldx, 64));
+      TGEMM_TRY(map_blocks(&m.a, a.dgu, 2 * c_.F, a.ld_dgu));
+      TGEMM_TRY(map_blocks(&m.b, ws_ + l_.x, c_.D, l_.ldx));
       TGEMM_TRY(gradient_out(a, m, c_.dw_in, c_.ldd_in, 2 * c_.F, c_.D));
       TGEMM_TRY(launch(launch_expert_din, m, a, int64_t(a.E) * a.m_blocks * a.n_blocks));
     }
@@ -411,12 +415,39 @@ class Experts {
     return TGEMM_OK;
   }
 
-  // A sorted matrix, in boxes of 64 columns.
+  // W_in's rows in steps of 16 gates and their 16 ups, 64 features a box, where the
+  // features are whole steps.
+  int map_gates(ExpertMaps& m, ExpertArgs& a) {
+    const uint64_t ld = w_in_.ld * 2, F = c_.F;
+    a.split = F % 16 != 0;
+    if (a.split) return host_map_3d(&m.a, type_, w_in_.p, c_.D, F, 2 * c_.E, ld, F * ld, kTileK, 16, 2);
+    const uint64_t dims[5] = {static_cast<uint64_t>(c_.D), 16, 2, F / 16, static_cast<uint64_t>(c_.E)};
+    const uint64_t strides[4] = {ld, F * ld, 16 * ld, 2 * F * ld};
+    const uint32_t box[5] = {kTileK, 16, 2, 4, 1};
+    return host_map(&m.a, type_, w_in_.p, 5, dims, strides, box);
+  }
+  // A weight's columns as M, 64 of its rows and 128 columns a box, where the columns
+  // are whole blocks of 64 (the box's last columns would else lie past the weight's end).
+  int map_transposed(ExpertMaps& m, ExpertArgs& a, const Operand& w, int64_t cols, int64_t rows) {
+    a.split = cols % 64 != 0;
+    if (a.split) return host_map_3d(&m.a, type_, w.p, cols, rows, c_.E, w.ld * 2, rows * w.ld * 2, 64, kTileK);
+    const uint64_t ld = w.ld * 2, R = rows;
+    const uint64_t dims[4] = {64, R, static_cast<uint64_t>(cols / 64), static_cast<uint64_t>(c_.E)};
+    const uint64_t strides[3] = {ld, 128, R * ld};
+    const uint32_t box[4] = {64, kTileK, 2, 1};
+    return host_map(&m.a, type_, w.p, 4, dims, strides, box);
+  }
+  // A sorted matrix: boxes of 64 columns, of 64 rows and 128 columns (the pitch is whole
+  // blocks of 64; what lies past cols is in rows of M or columns of N that are not stored).
   int map_rows(CUtensorMap* m, const void* p, int64_t cols, int64_t ld, uint32_t box_rows) {
     return host_map_3d(m, type_, p, cols, rows_max_, 1, ld * 2, 0, 64, box_rows);
   }
+  int map_blocks(CUtensorMap* m, const void* p, int64_t cols, int64_t ld) {
+    return host_map_3d(m, type_, p, 64, rows_max_, ceil_div(cols, 64), ld * 2, 128, 64, kTileK, 2);
+  }
   int token_maps(ExpertMaps& m, const void* p, int64_t cols, int64_t ld) {
     TGEMM_TRY(map_rows(&m.b, p, cols, ld, 64));
+    TGEMM_TRY(map_rows(&m.b32, p, cols, ld, 32));
     return map_rows(&m.b16, p, cols, ld, 16);
   }
   int gather(const void* x, int64_t ld) {
@@ -432,6 +463,7 @@ class Experts {
     j.k = static_cast<int>(c_.k);
     j.D = a_.D;
     j.y = a_.y;
+    j.y_scale = a_.y_scale;
     j.ldy = a_.ldy;
     j.type = type_;
     TGEMM_CUDA(launch_join(j, c_.stream), "join launch");
@@ -445,7 +477,7 @@ class Experts {
     a.out = out;
     a.ld_out = ld;
     a.store_granule = host_granule(out, ld, 2);
-    m.b16 = m.c = m.a;  // not used, unless c is set here
+    m.b32 = m.b16 = m.c = m.a;  // not used, unless c is set here
     if (a.store_granule < 16) return TGEMM_OK;
     a.store_granule = 0;
     return host_map_3d(&m.c, type_, out, N, M, c_.E, ld * 2, M * ld * 2, 64, 32);
@@ -507,7 +539,7 @@ int tgemm_experts_workspace_size(int backward, int64_t T, int64_t E, int64_t k, 
   if (ld_in >= tgemm::kMaxExtent || ld_out >= tgemm::kMaxExtent) return TGEMM_ERR_TOO_LARGE;
   *bytes = T == 0 ? 0
                   : static_cast<size_t>(
-                        tgemm::plan_layout(backward != 0, T, E, k, D, F, W_in, ld_in, W_out, ld_out).total);
+                        tgemm::plan_layout(backward != 0, T, E, k, D, F, W_in, ld_in, W_out, ld_out, dtype).total);
   return TGEMM_OK;
 }
 

@@ -248,13 +248,36 @@ __device__ __forceinline__ void finish_dh(const uint32_t (&v)[8], const ExpertAr
   if ((lane & 3) == 0 && c < valid) __stcg(a.dots + (row + c) * parts + part, sum);
 }
 
-// 16 columns of DOWN or DX: fp32, one row's 32 neighbouring elements a store.
+// 16 columns of DOWN or DX for fp16 operands: fp32, one row's 32 neighbouring elements
+// a store.
 __device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int valid) {
   if (d >= a.D) return;
-  float* y = a.y + row * a.ldy + d;
+  float* y = static_cast<float*>(a.y) + row * a.ldy + d;
 #pragma unroll
   for (int c = 0; c < 16; ++c)
     if (c < valid) __stcg(y + c * a.ldy, __uint_as_float(v[c]));
+}
+
+// The same for bf16 operands: halves, with one power of two for 16 rows' 32 neighbours
+// that brings the largest finite one to [2^14, 2^15).  A half's 11 bits are off by
+// 1.4e-4 on average (values below 2^-28 of the largest by more), which beside h's
+// rounding and the result's (1.65e-3 each) is 0.2 % of the error; y's bytes, written
+// here and read by the join, are what DOWN's epilogue costs.
+__device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int lane) {
+  uint16_t* y = static_cast<uint16_t*>(a.y) + row * a.ldy + d;
+  uint32_t most = 0u;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const uint32_t size = v[c] & 0x7FFFFFFFu;
+    most = max(most, size < 0x7F800000u ? size : 0u);
+  }
+  const uint32_t exponent = max(15u, __reduce_max_sync(0xffffffffu, most) >> 23);
+  const float f = __uint_as_float((268u - exponent) << 23);
+#pragma unroll
+  for (int c = 0; c < 16; c += 2)
+    store_rows(y + c * a.ldy, a.ldy, pack_pair(f * __uint_as_float(v[c]), f * __uint_as_float(v[c + 1]), OUT_F16), d,
+               static_cast<int>(a.ldy), true, lane);
+  if (lane == 0 && d < a.ldy) __stcg(a.y_scale + row / 16 * (a.ldy / 32) + d / 32, __uint_as_float((exponent - 14u) << 23));
 }
 
 // A weight's gradient: this warp's 32 rows of M, its 128 columns of N.  `sums`: 0 for
@@ -293,7 +316,7 @@ __device__ __forceinline__ void finish_weight(uint32_t tcol, bool sums, const Ex
 template <int MODE, int PARTS, bool GATHER>
 __global__ void __launch_bounds__(expert_threads(PARTS), 1)
     expert_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs args) {
-  const CUtensorMap &mapA = maps.a, &mapB = maps.b, &mapB16 = maps.b16, &mapC = maps.c;
+  const CUtensorMap &mapA = maps.a, &mapB = maps.b, &mapC = maps.c;
   constexpr int STAGES = expert_stages(MODE);
   constexpr bool GRADIENT = weight_gradient(MODE);
   static_assert(!GRADIENT || PARTS == 2, "staging of stores");
@@ -335,7 +358,10 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
   if (warp == 0 && lane == 0) {
     ptx::tma_prefetch_desc(&mapA);
     ptx::tma_prefetch_desc(&mapB);
-    if (!GRADIENT && !GATHER) ptx::tma_prefetch_desc(&mapB16);
+    if (!GRADIENT && !GATHER) {
+      ptx::tma_prefetch_desc(&maps.b32);
+      ptx::tma_prefetch_desc(&maps.b16);
+    }
     if (GRADIENT) ptx::tma_prefetch_desc(&mapC);
   }
   if (warp == 1) {
@@ -364,9 +390,13 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
       next = units.get(args, i + workers);
       const int stages = units.stages(args, u);
       const int half = GRADIENT ? kTileM : u.n / 2;  // this CTA's columns
-      // a CTA's columns in boxes of 64 rows, and of 16 for the rest
-      const int wide = half / 64, boxes = wide + (half & 63) / 16;
-      const int box0 = lane < wide ? 64 * lane : 64 * wide + 16 * (lane - wide);
+      // a CTA's columns in as few boxes as add up to them (each costs the copy engine
+      // some 20 cycles beside its bytes): lane l's box
+      const int wide = half / 64;
+      const bool mid = (half & 32) != 0, small = (half & 16) != 0;
+      const int boxes = wide + (mid ? 1 : 0) + (small ? 1 : 0);
+      const CUtensorMap* box = lane < wide ? &mapB : lane == wide && mid ? &maps.b32 : &maps.b16;
+      const int box0 = lane < wide ? 64 * lane : lane == wide ? 64 * wide : 64 * wide + 32;
       int4 rows = make_int4(0, 0, 0, 0);
       if (GATHER && 4 * lane < half)
         rows = __ldcg(reinterpret_cast<const int4*>(args.rows.token + u.row0 + cta * half + 4 * lane));
@@ -384,24 +414,28 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
         // 128 of the 256 of M
         const int m0 = u.mb * 256 + cta * kTileM;
         if constexpr (MODE == EXPERT_UP) {
-          if (lane < 4)
-            ptx::tma_load_3d_pair(sa + lane * 4096, &mapA, k0, u.mb * kTileM + cta * 64 + lane * 16, 2 * u.expert, fb);
+          const int f0 = u.mb * kTileM + cta * 64;
+          if (!args.split) {
+            if (lane == 0) ptx::tma_load_5d_pair(sa, &mapA, k0, 0, 0, f0 / 16, u.expert, fb);
+          } else if (lane < 4) {
+            ptx::tma_load_3d_pair(sa + lane * 4096, &mapA, k0, f0 + lane * 16, 2 * u.expert, fb);
+          }
         } else if constexpr (MODE == EXPERT_DOWN) {
           if (lane == 0) ptx::tma_load_3d_pair(sa, &mapA, k0, m0, u.expert, fb);
-        } else {
-          if (lane < 2)
-            ptx::tma_load_3d_pair(sa + lane * 8192, &mapA, m0 + lane * 64, GRADIENT ? u.row0 + k0 : k0,
-                                  GRADIENT ? 0 : u.expert, fb);
+        } else if constexpr (GRADIENT) {
+          if (lane == 0) ptx::tma_load_3d_pair(sa, &mapA, 0, u.row0 + k0, m0 / 64, fb);
+        } else if (!args.split) {
+          if (lane == 0) ptx::tma_load_4d_pair(sa, &mapA, 0, k0, m0 / 64, u.expert, fb);
+        } else if (lane < 2) {
+          ptx::tma_load_3d_pair(sa + lane * 8192, &mapA, m0 + lane * 64, k0, u.expert, fb);
         }
         // half of N
         if constexpr (GRADIENT) {
-          if (lane < 2)
-            ptx::tma_load_3d_pair(sb + lane * 8192, &mapB, u.nb * 256 + cta * kTileM + lane * 64, u.row0 + k0, 0, fb);
+          if (lane == 1) ptx::tma_load_3d_pair(sb, &mapB, 0, u.row0 + k0, u.nb * 4 + cta * 2, fb);
         } else if constexpr (GATHER) {
           if (4 * lane < half) tma_gather4_pair(sb + lane * 512, &mapB, k0, rows, fb);
         } else {
-          if (lane < boxes)
-            ptx::tma_load_3d_pair(sb + box0 * 128, lane < wide ? &mapB : &mapB16, k0, u.row0 + cta * half + box0, 0, fb);
+          if (lane < boxes) ptx::tma_load_3d_pair(sb + box0 * 128, box, k0, u.row0 + cta * half + box0, 0, fb);
         }
         filled |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
@@ -568,6 +602,8 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
             ptx::tmem_wait_ld();
             if constexpr (MODE == EXPERT_UP)
               finish_up(v, args, m0, u.row0 + c0, valid, fmt, lane);
+            else if (args.bf16)
+              finish_y_half(v, args, m0, u.row0 + c0, lane);
             else
               finish_y(v, args, m0, u.row0 + c0, valid);
           }

@@ -54,7 +54,8 @@ struct JoinArgs {
   const float* weights;
   int64_t T;
   int k, D;
-  const float* y;
+  const void* y;        // fp32, or (type 0) halves times y_scale of 16 rows' 32 columns
+  const float* y_scale;
   int64_t ldy;
   int type;
   void* out;
@@ -92,6 +93,7 @@ struct ExpertArgs {
   int chunk;               // stages summed in tensor memory, at most
   int bf16;
   int gather;              // UP: rows of x where they lie
+  int split;               // A comes in several boxes
   ExpertRows rows;
   void* h;                 // UP: h; DH: weight * h
   int64_t ldh;
@@ -102,8 +104,9 @@ struct ExpertArgs {
   float* dots;             // DH: m_blocks * 8 per row
   const float* weights;    // DH: of each place
   const float* scale;      // {s, 1 / s} (fp16), or null: DH multiplies dg and du with s, DIN with 1 / s
-  float* y;                // DOWN, DX
-  int64_t ldy;
+  void* y;                 // DOWN, DX: fp32, or (bf16) halves times y_scale of 16 rows' 32 columns
+  int64_t ldy;             // a multiple of 64
+  float* y_scale;
   void* out;               // DIN, DOUT
   int64_t ld_out;
   int store_granule;       // 0 bulk-tensor stores, else the granule of per-thread stores
@@ -111,9 +114,13 @@ struct ExpertArgs {
   unsigned int* status;
 };
 
-// Operand A, B (token products: boxes of 64 rows, and of 16), and where DIN and DOUT store.
+// Operands A and B (token products: boxes of 64, 32 and 16 rows), and where DIN and
+// DOUT store.  Axes of a, from the innermost: UP {k, feature % 16, gate or up, feature /
+// 16, expert}, or where args.split {k, feature, 2 expert + (gate or up)}; DOWN {k, row,
+// expert}; DH and DX {column % 64, row, column / 64, expert}, or where args.split {column,
+// row, expert}.  DIN's and DOUT's a and b: {column % 64, row, column / 64}.
 struct ExpertMaps {
-  CUtensorMap a, b, b16, c;
+  CUtensorMap a, b, b32, b16, c;
 };
 cudaError_t launch_expert_up(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream);
 cudaError_t launch_expert_down(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream);

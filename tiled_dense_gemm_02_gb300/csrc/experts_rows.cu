@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const int* head,
 }
 
 // ------------------------------------------------------------------- join
-// One thread: four columns of a token.  Bound by y's bytes, read once.
-constexpr int kJoinThreads = 128;
+// One thread: eight columns of a token.  Bound by y's bytes, read once.
+constexpr int kJoinThreads = 128, kJoinColumns = 8;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pair_of(float x, float y) {
@@ -311,11 +311,12 @@ struct JoinKernelArgs {
   const int* row;
   const float* weights;
   int k, D;
-  const float* y;
+  const void* y;
+  const float* y_scale;
   int64_t ldy;
   void* out;
   int64_t ld_out;
-  int vec;  // out's rows are 8-byte aligned and D a multiple of 4
+  int vec;  // out's rows are 16-byte aligned and D a multiple of 8
   const float* scale;
   const float* dots;
   int parts;
@@ -340,39 +341,57 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       if (lane == 0) a.d_weights[t * a.k + j] = row == -2 ? NAN : sum;
     }
   }
-  const int d = (blockIdx.y * kJoinThreads + threadIdx.x) * 4;
+  const int d = (blockIdx.y * kJoinThreads + threadIdx.x) * kJoinColumns;
   if (!a.out || d >= a.D) return;
-  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float sum[kJoinColumns];
+#pragma unroll
+  for (int i = 0; i < kJoinColumns; ++i) sum[i] = 0.0f;
 #pragma unroll 4
   for (int j = 0; j < a.k; ++j) {
     const int row = __ldcg(rows + j);
     if (row >= 0) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(a.y + row * a.ldy + d));
-      const float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.0f;
-      sum.x = fmaf(w, v.x, sum.x);
-      sum.y = fmaf(w, v.y, sum.y);
-      sum.z = fmaf(w, v.z, sum.z);
-      sum.w = fmaf(w, v.w, sum.w);
+      float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.0f;
+      float y[kJoinColumns];
+      if constexpr (BF16) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.y) + row * a.ldy + d));
+        const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+        w *= __ldcg(a.y_scale + row / 16 * (a.ldy / 32) + d / 32);  // a power of two: exact
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+          y[2 * i] = f.x;
+          y[2 * i + 1] = f.y;
+        }
+      } else {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.y) + row * a.ldy + d);
+        const float4 lo = __ldcs(src), hi = __ldcs(src + 1);
+        y[0] = lo.x;
+        y[1] = lo.y;
+        y[2] = lo.z;
+        y[3] = lo.w;
+        y[4] = hi.x;
+        y[5] = hi.y;
+        y[6] = hi.z;
+        y[7] = hi.w;
+      }
+#pragma unroll
+      for (int i = 0; i < kJoinColumns; ++i) sum[i] = fmaf(w, y[i], sum[i]);
     } else if (row == -2) {
-      sum.x = sum.y = sum.z = sum.w = NAN;
+#pragma unroll
+      for (int i = 0; i < kJoinColumns; ++i) sum[i] = NAN;
     }
   }
-  if (a.scale) {
-    const float f = __ldcg(a.scale + 1);
-    sum.x *= f;
-    sum.y *= f;
-    sum.z *= f;
-    sum.w *= f;
-  }
-  const uint2 v = make_uint2(pair_of<BF16>(sum.x, sum.y), pair_of<BF16>(sum.z, sum.w));
+  const float f = a.scale ? __ldcg(a.scale + 1) : 1.0f;
+  uint32_t p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = pair_of<BF16>(f * sum[2 * i], f * sum[2 * i + 1]);
   uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.ld_out + d;
   if (a.vec) {
-    *reinterpret_cast<uint2*>(out) = v;
+    *reinterpret_cast<uint4*>(out) = make_uint4(p[0], p[1], p[2], p[3]);
   } else {
-    const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (d + i < a.D) out[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    for (int i = 0; i < kJoinColumns; ++i)
+      if (d + i < a.D) out[i] = static_cast<uint16_t>(p[i / 2] >> (16 * (i & 1)));
   }
 }
 
@@ -470,15 +489,17 @@ cudaError_t launch_join(const JoinArgs& j, cudaStream_t stream) {
   a.k = j.k;
   a.D = j.D;
   a.y = j.y;
+  a.y_scale = j.y_scale;
   a.ldy = j.ldy;
   a.out = j.out;
   a.ld_out = j.ld_out;
-  a.vec = j.out && j.D % 4 == 0 && j.ld_out % 4 == 0 && reinterpret_cast<uint64_t>(j.out) % 8 == 0;
+  a.vec = j.out && j.D % 8 == 0 && j.ld_out % 8 == 0 && reinterpret_cast<uint64_t>(j.out) % 16 == 0;
   a.scale = j.scale;
   a.dots = j.dots;
   a.parts = j.parts;
   a.d_weights = j.d_weights;
-  const int across = j.out ? (j.D + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : 1;
+  constexpr int kWide = kJoinThreads * kJoinColumns;
+  const int across = j.out ? (j.D + kWide - 1) / kWide : 1;
   const dim3 grid(static_cast<unsigned>(j.T), across, 1);
   return j.type == 0 ? launch_next(join_kernel<true>, grid, kJoinThreads, 0, stream, a)
                      : launch_next(join_kernel<false>, grid, kJoinThreads, 0, stream, a);

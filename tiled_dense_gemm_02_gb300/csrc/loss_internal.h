@@ -23,6 +23,9 @@ int host_map_3d(CUtensorMap* map, int type, const void* base, int64_t cols, int6
 // The same for one matrix; a box one row high serves gathering copies.
 int host_map_2d(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t pitch_bytes,
                 uint32_t box_cols, uint32_t box_rows);
+// The same for any rank up to 5: extents, strides in bytes of the axes after the first, box.
+int host_map(CUtensorMap* map, int type, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+             const uint32_t* box);
 // Adds tensor-core launches to the host counters.
 void host_count_launches(int n);
 bool host_ranges_overlap(uint64_t a0, uint64_t a1, uint64_t b0, uint64_t b1);
