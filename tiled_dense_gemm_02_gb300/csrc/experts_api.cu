@@ -3,7 +3,7 @@
 // order of launches.
 //
 // Forward:  sort of the places  [gather of x]  UP  DOWN  join
-// Backward: [scale of fp16 gradients]  gather of grad  DH  DX  join  [gather of x]  DIN  DOUT
+// Backward: [scale of fp16 gradients]  gather of grad  DH  DOUT  DX  join  DIN
 // (experts_rows.cu and experts_gemm.cuh hold the kernels.)  Weights whose rows are
 // not 16-byte aligned are copied to an aligned pitch first.
 #include <cuda.h>
@@ -107,16 +107,17 @@ ExpertRows rows_at(char* base, const RowsLayout& l) {
   return r;
 }
 
-// Kept for the backward call: the sorted places, g and u of every row.
+// Kept for the backward call: the sorted places, the sorted rows of x, g and u.
 struct SavedLayout {
   RowsLayout rows;
-  int64_t gu, ldg, total;
+  int64_t x, gu, ldg, total;
 };
-SavedLayout plan_saved(int64_t T, int64_t E, int64_t k, int64_t F) {
+SavedLayout plan_saved(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F) {
   SavedLayout l;
   Taker take;
   l.rows = plan_rows(take, T * k, E);
   l.ldg = round_up(F, 4);
+  l.x = take(most_rows(T * k, E) * round_up(D, 64) * 2);
   l.gu = take(most_rows(T * k, E) * 2 * l.ldg * 4);
   l.total = take.at;
   return l;
@@ -210,7 +211,7 @@ int check_call(const Call& c) {
     if (!c.x || !c.w_in || !c.w_out || !c.weights) return TGEMM_ERR_INVALID_VALUE;
     if (c.backward ? (!c.saved || !c.grad) : (!c.ids || !c.out)) return TGEMM_ERR_INVALID_VALUE;
     if (c.saved && (reinterpret_cast<uint64_t>(c.saved) % 256 ||
-                    c.saved_bytes < static_cast<size_t>(plan_saved(c.T, c.E, c.k, c.F).total)))
+                    c.saved_bytes < static_cast<size_t>(plan_saved(c.T, c.E, c.k, c.D, c.F).total)))
       return TGEMM_ERR_INVALID_VALUE;
     const Layout l = plan_layout(c.backward, c.T, c.E, c.k, c.D, c.F, c.w_in, c.ld_in, c.w_out, c.ld_out,
                                  c.dtype);
@@ -273,7 +274,7 @@ class Experts {
   Experts(const Call& c, int sms, int pairs, unsigned int* status)
       : c_(c),
         l_(plan_layout(c.backward, c.T, c.E, c.k, c.D, c.F, c.w_in, c.ld_in, c.w_out, c.ld_out, c.dtype)),
-        s_(plan_saved(c.T, c.E, c.k, c.F)),
+        s_(plan_saved(c.T, c.E, c.k, c.D, c.F)),
         ws_(static_cast<char*>(c.workspace)),
         saved_(static_cast<char*>(c.saved)),
         sms_(sms),
@@ -318,13 +319,14 @@ class Experts {
     {
       ExpertArgs a = a_;
       TGEMM_TRY(map_gates(m, a));
-      a.gather = o.places <= kGatherPlaces && host_granule(c_.x, c_.ldx, 2) == 16;
+      a.gather = !saved_ && o.places <= kGatherPlaces && host_granule(c_.x, c_.ldx, 2) == 16;
       if (a.gather) {
         TGEMM_TRY(host_map_2d(&m.b, type_, c_.x, c_.D, c_.T, c_.ldx * 2, 64, 1));
         m.b32 = m.b16 = m.b;
       } else {
-        TGEMM_TRY(gather(c_.x, c_.ldx));
-        TGEMM_TRY(token_maps(m, ws_ + l_.x, c_.D, l_.ldx));
+        char* rows = saved_ ? saved_ + s_.x : ws_ + l_.x;
+        TGEMM_TRY(gather(c_.x, c_.ldx, rows));
+        TGEMM_TRY(token_maps(m, rows, c_.D, l_.ldx));
       }
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 128));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
@@ -357,7 +359,7 @@ class Experts {
                  "gradient scale launch");
       a_.scale = scale;
     }
-    TGEMM_TRY(gather(c_.grad, c_.ldg));
+    TGEMM_TRY(gather(c_.grad, c_.ldg, ws_ + l_.x));
     {
       ExpertArgs a = a_;
       TGEMM_TRY(map_transposed(m, a, w_out_, c_.F, c_.D));
@@ -395,9 +397,8 @@ class Experts {
     if (c_.dx || c_.d_weights) TGEMM_TRY(join(j));
     if (c_.dw_in) {
       ExpertArgs a = a_;
-      TGEMM_TRY(gather(c_.x, c_.ldx));
       TGEMM_TRY(map_blocks(&m.a, a.dgu, 2 * c_.F, a.ld_dgu));
-      TGEMM_TRY(map_blocks(&m.b, ws_ + l_.x, c_.D, l_.ldx));
+      TGEMM_TRY(map_blocks(&m.b, saved_ + s_.x, c_.D, l_.ldx));
       TGEMM_TRY(gradient_out(a, m, c_.dw_in, c_.ldd_in, 2 * c_.F, c_.D));
       TGEMM_TRY(launch(launch_expert_din, m, a, int64_t(a.E) * a.m_blocks * a.n_blocks));
     }
@@ -450,8 +451,8 @@ class Experts {
     TGEMM_TRY(map_rows(&m.b32, p, cols, ld, 32));
     return map_rows(&m.b16, p, cols, ld, 16);
   }
-  int gather(const void* x, int64_t ld) {
-    TGEMM_CUDA(launch_gather_rows(a_.rows, rows_max_, x, ld, host_granule(x, ld, 2), a_.D, ws_ + l_.x, l_.ldx, sms_,
+  int gather(const void* x, int64_t ld, void* rows) {
+    TGEMM_CUDA(launch_gather_rows(a_.rows, rows_max_, x, ld, host_granule(x, ld, 2), a_.D, rows, l_.ldx, sms_,
                                   c_.stream),
                "gather launch");
     return TGEMM_OK;
@@ -547,7 +548,7 @@ int tgemm_experts_saved_size(int64_t T, int64_t E, int64_t k, int64_t D, int64_t
   if (!bytes) return TGEMM_ERR_INVALID_VALUE;
   const int st = tgemm::check_shape(T, E, k, D, F, dtype);
   if (st != TGEMM_OK) return st;
-  *bytes = T == 0 ? 0 : static_cast<size_t>(tgemm::plan_saved(T, E, k, F).total);
+  *bytes = T == 0 ? 0 : static_cast<size_t>(tgemm::plan_saved(T, E, k, D, F).total);
   return TGEMM_OK;
 }
 

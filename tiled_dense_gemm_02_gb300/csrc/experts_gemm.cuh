@@ -67,6 +67,11 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// Brings `bytes` (a multiple of 16) from p on into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // A tile of a product: block mb of M, and N's columns (rows row0.. of the sorted
 // matrices, n with the filling and `valid` without; gradients of the weights:
 // column block nb, and rows row0.. are the k axis).
@@ -138,29 +143,42 @@ __device__ __forceinline__ void whole_sums(uint32_t tcol, const uint32_t (&sum)[
 
 __device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
-// Neighbouring lanes hold neighbouring features of two rows: word = {row 0, row 1}.
-// Each stores both features of one row, or, where a row's features do not pair
-// up in words (`pairs` false), both rows of its own.
-__device__ __forceinline__ void store_rows(uint16_t* p, int64_t ld, uint32_t word, int feature, int F, bool pairs, int lane) {
-  if (pairs) {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 1);
-    const bool odd = (lane & 1) != 0;
-    const uint32_t both = odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
-    if (feature < F) *reinterpret_cast<uint32_t*>(p + (odd ? ld - 1 : 0)) = both;
-  } else if (feature < F) {
-    p[0] = static_cast<uint16_t>(word & 0xFFFFu);
-    p[ld] = static_cast<uint16_t>(word >> 16);
+// Where a lane stores 16-bit values of its feature, two rows at a time.  Neighbouring
+// lanes hold neighbouring features; PAIRS: each stores both features of one of the
+// two rows (the matrix's features pair up in words), else both rows of its own.
+template <bool PAIRS>
+struct RowStore {
+  uint16_t* p;
+  int64_t ld;
+  bool odd, in;
+  // feature: the lane's, of F
+  __device__ __forceinline__ RowStore(void* base, int64_t row, int64_t pitch, int feature, int F, int lane)
+      : p(static_cast<uint16_t*>(base) + row * pitch + feature), ld(pitch), odd((lane & 1) != 0), in(feature < F) {
+    if (PAIRS && odd) p += ld - 1;
   }
-}
+  // word: {row, next row} of the lane's feature
+  __device__ __forceinline__ void put(uint32_t word) {
+    if constexpr (PAIRS) {
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 1);
+      const uint32_t both = odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+      if (in) *reinterpret_cast<uint32_t*>(p) = both;
+    } else if (in) {
+      p[0] = static_cast<uint16_t>(word & 0xFFFFu);
+      p[ld] = static_cast<uint16_t>(word >> 16);
+    }
+    p += 2 * ld;
+  }
+};
 
 // 16 columns of UP: gates in lanes 0..15, ups in lanes 16..31 -> h, and g and u.
 // `row`: the columns' first row, of which `valid` are no filling (which gets 0).
 // g and u lie as {g, u} x features x 4 rows for every four rows: 16 bytes a lane.
+template <bool PAIRS>
 __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertArgs& a, int feature, int64_t row,
                                           int valid, int fmt, int lane) {
   const bool low = lane < 16;
   const int c0 = low ? 0 : 8;
-  uint16_t* h = static_cast<uint16_t*>(a.h) + (row + c0) * a.ldh + feature;
+  RowStore<PAIRS> h(a.h, row + c0, a.ldh, feature, a.F, lane);
   float g[8], u[8], x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -174,75 +192,79 @@ __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertA
     for (int i = 0; i < 8; ++i) x[i] = c0 + i < valid ? x[i] : 0.0f;
   }
 #pragma unroll
-  for (int i = 0; i < 8; i += 2)
-    store_rows(h + i * a.ldh, a.ldh, pack_pair(x[i], x[i + 1], fmt), feature, a.F, (a.F & 1) == 0, lane);
+  for (int i = 0; i < 8; i += 2) h.put(pack_pair(x[i], x[i + 1], fmt));
   if (a.gu && feature < a.F) {
     float4* gu = reinterpret_cast<float4*>(a.gu) + (row + c0) / 4 * 2 * a.ldg + feature;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      __stcs(gu + q * 2 * a.ldg, make_float4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]));
-      __stcs(gu + (q * 2 + 1) * a.ldg, make_float4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]));
+      __stcs(gu, make_float4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]));
+      __stcs(gu + a.ldg, make_float4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]));
+      gu += 2 * a.ldg;
     }
   }
 }
 
 // 8 columns of DH: v = d_out W_out of this lane's feature.
 //   s = sigmoid(g):  dg = w v u s (1 + g (1 - s)),  du = w v g s,  h = g s u
-// `mine`: in lane first + c the weight of column c.
+// `mine`: in lane first + c the weight of column c, and `scaled` times the gradients' scale.
+template <bool PAIRS>
 __device__ __forceinline__ void finish_dh(const uint32_t (&v)[8], const ExpertArgs& a, int feature, int64_t row,
-                                          int valid, int fmt, int lane, float mine, int first, int part, int parts,
-                                          float scale) {
+                                          int valid, int fmt, int lane, float mine, float scaled, int first, int part,
+                                          int parts) {
   const float4* gu = reinterpret_cast<const float4*>(a.gu) + row / 4 * 2 * a.ldg + feature;
-  uint16_t* dgu = static_cast<uint16_t*>(a.dgu) + row * a.ld_dgu + feature;
-  uint16_t* hw = static_cast<uint16_t*>(a.h) + row * a.ldh + feature;
-  const bool pairs = (a.F & 1) == 0;
   float4 g4[2], u4[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     g4[q] = u4[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (feature < a.F) {
-      g4[q] = __ldcs(gu + q * 2 * a.ldg);
-      u4[q] = __ldcs(gu + (q * 2 + 1) * a.ldg);
+      g4[q] = __ldcg(gu);
+      u4[q] = __ldcg(gu + a.ldg);
+    }
+    gu += 2 * a.ldg;
+  }
+  RowStore<PAIRS> dg_rows(a.dgu, row, a.ld_dgu, feature, a.F, lane), hw_rows(a.h, row, a.ldh, feature, a.F, lane);
+  RowStore<PAIRS> du_rows = dg_rows;
+  du_rows.p += a.F;
+  float g[8] = {g4[0].x, g4[0].y, g4[0].z, g4[0].w, g4[1].x, g4[1].y, g4[1].z, g4[1].w};
+  float u[8] = {u4[0].x, u4[0].y, u4[0].z, u4[0].w, u4[1].x, u4[1].y, u4[1].z, u4[1].w};
+  float d[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) d[c] = __uint_as_float(v[c]);
+  if (valid < 8) {  // the filling: zeros, whatever the weights hold
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c >= valid) g[c] = u[c] = d[c] = 0.0f;
     }
   }
-  float dot[8];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const float g[4] = {g4[q].x, g4[q].y, g4[q].z, g4[q].w}, u[4] = {u4[q].x, u4[q].y, u4[q].z, u4[q].w};
+  for (int c = 0; c < 8; c += 2) {
+    float dg[2], du[2], h[2];
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      const int c = 4 * q + i;
-      float dg[2], du[2], h[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool in = c + e < valid;  // the filling: zeros, whatever the weights hold
-        const float d = in ? __uint_as_float(v[c + e]) : 0.0f;
-        const float gate = in ? g[i + e] : 0.0f, up = in ? u[i + e] : 0.0f;
-        const float w = __shfl_sync(0xffffffffu, mine, first + c + e);
-        const float s = fast_sigmoid(gate), silu = gate * s, wd = w * d * scale;
-        h[e] = silu * up;
-        dot[c + e] = h[e] * d;
-        h[e] *= w;
-        dg[e] = wd * up * fmaf(silu, 1.0f - s, s);
-        du[e] = wd * silu;
-      }
-      store_rows(dgu + c * a.ld_dgu, a.ld_dgu, pack_pair(dg[0], dg[1], fmt), feature, a.F, pairs, lane);
-      store_rows(dgu + c * a.ld_dgu + a.F, a.ld_dgu, pack_pair(du[0], du[1], fmt), feature, a.F, pairs, lane);
-      store_rows(hw + c * a.ldh, a.ldh, pack_pair(h[0], h[1], fmt), feature, a.F, pairs, lane);
+    for (int e = 0; e < 2; ++e) {
+      const float s = fast_sigmoid(g[c + e]), silu = g[c + e] * s;
+      const float wd = __shfl_sync(0xffffffffu, scaled, first + c + e) * d[c + e];
+      h[e] = silu * u[c + e];
+      dg[e] = wd * u[c + e] * fmaf(silu, 1.0f - s, s);
+      du[e] = wd * silu;
+      d[c + e] *= h[e];
+      h[e] *= __shfl_sync(0xffffffffu, mine, first + c + e);
     }
+    dg_rows.put(pack_pair(dg[0], dg[1], fmt));
+    du_rows.put(pack_pair(du[0], du[1], fmt));
+    hw_rows.put(pack_pair(h[0], h[1], fmt));
   }
-  // sums over the 32 lanes: a lane keeps half of its columns at each exchange, and
-  // ends with a quarter of one column's
+  // sums of h v over the 32 lanes: a lane keeps half of its columns at each exchange,
+  // and ends with a quarter of one column's
 #pragma unroll
   for (int width = 4; width >= 1; width >>= 1) {
     const bool high = (lane & (4 * width)) != 0;
 #pragma unroll
     for (int c = 0; c < width; ++c) {
-      const float got = __shfl_xor_sync(0xffffffffu, high ? dot[c] : dot[c + width], 4 * width);
-      dot[c] = (high ? dot[c + width] : dot[c]) + got;
+      const float got = __shfl_xor_sync(0xffffffffu, high ? d[c] : d[c + width], 4 * width);
+      d[c] = (high ? d[c + width] : d[c]) + got;
     }
   }
-  float sum = dot[0] + __shfl_xor_sync(0xffffffffu, dot[0], 2);
+  float sum = d[0] + __shfl_xor_sync(0xffffffffu, d[0], 2);
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
   const int c = lane >> 2;
   if ((lane & 3) == 0 && c < valid) __stcg(a.dots + (row + c) * parts + part, sum);
@@ -254,8 +276,10 @@ __device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertAr
   if (d >= a.D) return;
   float* y = static_cast<float*>(a.y) + row * a.ldy + d;
 #pragma unroll
-  for (int c = 0; c < 16; ++c)
-    if (c < valid) __stcg(y + c * a.ldy, __uint_as_float(v[c]));
+  for (int c = 0; c < 16; ++c) {
+    if (c < valid) __stcg(y, __uint_as_float(v[c]));
+    y += a.ldy;
+  }
 }
 
 // The same for bf16 operands: halves, with one power of two for 16 rows' 32 neighbours
@@ -264,7 +288,7 @@ __device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertAr
 // rounding and the result's (1.65e-3 each) is 0.2 % of the error; y's bytes, written
 // here and read by the join, are what DOWN's epilogue costs.
 __device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int lane) {
-  uint16_t* y = static_cast<uint16_t*>(a.y) + row * a.ldy + d;
+  RowStore<true> y(a.y, row, a.ldy, d, static_cast<int>(a.ldy), lane);
   uint32_t most = 0u;
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
@@ -274,9 +298,7 @@ __device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const Exp
   const uint32_t exponent = max(15u, __reduce_max_sync(0xffffffffu, most) >> 23);
   const float f = __uint_as_float((268u - exponent) << 23);
 #pragma unroll
-  for (int c = 0; c < 16; c += 2)
-    store_rows(y + c * a.ldy, a.ldy, pack_pair(f * __uint_as_float(v[c]), f * __uint_as_float(v[c + 1]), OUT_F16), d,
-               static_cast<int>(a.ldy), true, lane);
+  for (int c = 0; c < 16; c += 2) y.put(pack_pair(f * __uint_as_float(v[c]), f * __uint_as_float(v[c + 1]), OUT_F16));
   if (lane == 0 && d < a.ldy) __stcg(a.y_scale + row / 16 * (a.ldy / 32) + d / 32, __uint_as_float((exponent - 14u) << 23));
 }
 
@@ -517,6 +539,7 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
     const int part = (warp - 2) / 4;       // its share of the columns
     uint8_t* buf = sC + (warp - 2) * 4096;
     const int fmt = args.bf16 ? OUT_BF16 : OUT_F16;
+    const bool pairs = (args.F & 1) == 0;
     const float scale = MODE == EXPERT_DH && args.scale    ? __ldcg(args.scale)
                         : MODE == EXPERT_DIN && args.scale ? __ldcg(args.scale + 1)
                                                            : 1.0f;
@@ -543,6 +566,16 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
       constexpr int STEP = GRADIENT ? 1 : PARTS, MOST = 16 / PARTS;
       const int block0 = GRADIENT ? part * MOST : part;
       const int blocks = GRADIENT ? MOST : (u.n / 16 - part + PARTS - 1) / PARTS;
+      if constexpr (MODE == EXPERT_DH) {
+        // this warp's g and u on their way to L2 under the products: 512 bytes for every
+        // four rows, g or u, 32 features
+        const int feature = u.mb * 256 + cta * kTileM + quarter * 32;
+        const int g = lane >> 1, r = (part + (g >> 2) * PARTS) * 16 + (g & 3) * 4;
+        if (feature < args.F && r < u.valid)
+          prefetch_l2(reinterpret_cast<const float4*>(args.gu) +
+                          ((u.row0 + r) / 4 * 2 + (lane & 1)) * args.ldg + feature,
+                      16 * min(32, static_cast<int>(args.ldg) - feature));
+      }
       uint32_t tcol = 0;
       if (!GRADIENT || stages > 0) {
         tcol = taken() + block0 * 16;
@@ -593,16 +626,24 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
               uint32_t v[8];
               ptx::tmem_ld_32x32b_x8(tcol + b * PARTS * 16 + half, v);
               ptx::tmem_wait_ld();
-              finish_dh(v, args, m0, u.row0 + c0 + half, valid - half, fmt, lane, mine, half,
-                        (u.mb * 2 + cta) * 4 + quarter, args.m_blocks * 8, scale);
+              const int dot = (u.mb * 2 + cta) * 4 + quarter;
+              if (pairs)
+                finish_dh<true>(v, args, m0, u.row0 + c0 + half, valid - half, fmt, lane, mine, scale * mine, half, dot,
+                                args.m_blocks * 8);
+              else
+                finish_dh<false>(v, args, m0, u.row0 + c0 + half, valid - half, fmt, lane, mine, scale * mine, half,
+                                 dot, args.m_blocks * 8);
             }
           } else {
             uint32_t v[16];
             ptx::tmem_ld_32x32b_x16(tcol + b * PARTS * 16, v);
             ptx::tmem_wait_ld();
-            if constexpr (MODE == EXPERT_UP)
-              finish_up(v, args, m0, u.row0 + c0, valid, fmt, lane);
-            else if (args.bf16)
+            if constexpr (MODE == EXPERT_UP) {
+              if (pairs)
+                finish_up<true>(v, args, m0, u.row0 + c0, valid, fmt, lane);
+              else
+                finish_up<false>(v, args, m0, u.row0 + c0, valid, fmt, lane);
+            } else if (args.bf16)
               finish_y_half(v, args, m0, u.row0 + c0, lane);
             else
               finish_y(v, args, m0, u.row0 + c0, valid);

@@ -43,7 +43,10 @@ __device__ __forceinline__ void count_places(const OrderArgs& a, int64_t base, i
   __syncthreads();
 }
 
-// Sum over the block before this thread, and of the whole block.
+__device__ __forceinline__ void sort_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSortThreads) : "memory"); }
+
+// Sum over the first kSortThreads threads of the block before this one, and of all of
+// them; they alone call it.
 __device__ __forceinline__ int block_scan(int v, int* total, int* shared) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int sum = v;
@@ -53,14 +56,14 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* shared) {
     if (lane >= d) sum += below;
   }
   if (lane == 31) shared[warp] = sum;
-  __syncthreads();
+  sort_barrier();
   int before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kSortWarps; ++w) {
     before += w < warp ? shared[w] : 0;
     all += shared[w];
   }
-  __syncthreads();
+  sort_barrier();
   *total = all;
   return before + sum - v;
 }
@@ -191,39 +194,52 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_consta
   }
 }
 
-// partial[block][e]: the block's rows of e -> the rows of e in the blocks before it.
-__global__ void __launch_bounds__(kSortThreads) tiles_kernel(const __grid_constant__ OrderArgs a, int blocks) {
-  __shared__ int totals[kMaxExperts];
+// partial[block][e]: the block's rows of e -> the rows of e in the blocks before it.  The
+// blocks are summed in `segments` parts side by side, then once more with what lies before
+// each part.
+constexpr int kTilesThreads = 1024;
+__global__ void __launch_bounds__(kTilesThreads) tiles_kernel(const __grid_constant__ OrderArgs a, int blocks, int segments) {
+  __shared__ int totals[kTilesThreads];  // [segment][e]
   __shared__ int scan[kSortWarps];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-    int sum = 0;
-    int* p = a.rows.partial + e;
-    int b = 0;
-    for (; b + 16 <= blocks; b += 16) {
-      int v[16];
+  const int segment = threadIdx.x / a.E, e = threadIdx.x - segment * a.E;
+  const int each = (blocks + segments - 1) / segments;
+  const int begin = min(blocks, segment * each), end = segment < segments ? min(blocks, begin + each) : begin;
+  int* p = a.rows.partial + e;
+  int sum = 0;
+#pragma unroll 16
+  for (int b = begin; b < end; ++b) sum += __ldcg(p + static_cast<int64_t>(b) * a.E);
+  totals[threadIdx.x] = sum;
+  __syncthreads();
+  if (segment < segments) {
+    int before = 0;
+    for (int i = 0; i < segment; ++i) before += totals[i * a.E + e];
+    int b = begin;
+    for (; b + 8 <= end; b += 8) {
+      int v[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __ldcg(p + static_cast<int64_t>(b + i) * a.E);
+      for (int i = 0; i < 8; ++i) v[i] = __ldcg(p + static_cast<int64_t>(b + i) * a.E);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[static_cast<int64_t>(b + i) * a.E] = sum;
-        sum += v[i];
+      for (int i = 0; i < 8; ++i) {
+        p[static_cast<int64_t>(b + i) * a.E] = before;
+        before += v[i];
       }
     }
-    for (; b < blocks; ++b) {
+    for (; b < end; ++b) {
       const int v = __ldcg(p + static_cast<int64_t>(b) * a.E);
-      p[static_cast<int64_t>(b) * a.E] = sum;
-      sum += v;
+      p[static_cast<int64_t>(b) * a.E] = before;
+      before += v;
     }
-    totals[e] = sum;
   }
-  __syncthreads();
+  if (threadIdx.x >= kSortThreads) return;
   int n[kOwnExperts];
 #pragma unroll
   for (int i = 0; i < kOwnExperts; ++i) {
-    const int e = kOwnExperts * threadIdx.x + i;
-    n[i] = e < a.E ? totals[e] : 0;
+    const int own = kOwnExperts * threadIdx.x + i;
+    n[i] = 0;
+    if (own < a.E)
+      for (int k = 0; k < segments; ++k) n[i] += totals[k * a.E + own];
   }
   int row = list_tiles(a, n, scan);
 #pragma unroll
@@ -253,41 +269,51 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_consta
 }
 
 // ----------------------------------------------------------------- gather
-// A block a row, 16 bytes a thread and step.  Bound by bytes: a token's row is
-// read k times, the later times from L2, and every sorted row is written once.
-constexpr int kGatherThreads = 128;
+// A warp a row, up to eight 16-byte loads a lane in flight, the next row's token loaded
+// ahead.  Bound by bytes: a token's row is read k times, the later times from L2, and
+// every sorted row is written once (8192 tokens of 2048, 8 places each: a block a row 61 us).
+constexpr int kGatherThreads = 256;
 
 template <int G>  // granule of x's rows in bytes
+__device__ __forceinline__ uint4 load_word(const uint16_t* src, int d, int D) {
+  if (d >= D) return make_uint4(0u, 0u, 0u, 0u);
+  if (G == 16 && d + 8 <= D) return __ldg(reinterpret_cast<const uint4*>(src + d));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (G >= 4 && d + 8 <= D) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(src + d) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (d + i < D) w[i / 2] |= static_cast<uint32_t>(__ldg(src + d + i)) << (16 * (i & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int G>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const int* head, const int* token, const int* place,
                                                                 const uint16_t* x, int64_t ldx, int D, uint16_t* out,
                                                                 int64_t ld_out) {
+  constexpr int kFlight = G == 16 ? 8 : 2;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int rows = __ldcg(head + 1);
-  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    const bool filling = __ldcg(place + r) < 0;
-    const uint16_t* src = x + (filling ? 0 : __ldcg(token + r) * ldx);
+  const int rows = __ldcg(head + 1), lane = threadIdx.x & 31;
+  const int warp = blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kGatherThreads / 32);
+  const auto token_of = [&](int r) { return r >= rows || __ldcg(place + r) < 0 ? -1 : __ldcg(token + r); };
+  int next = token_of(warp);
+  for (int r = warp; r < rows; r += warps) {
+    const int t = next;
+    next = token_of(r + warps);
+    const uint16_t* src = x + (t < 0 ? 0 : t * ldx);
     uint16_t* dst = out + r * ld_out;
-#pragma unroll 2
-    for (int d = threadIdx.x * 8; d < D; d += kGatherThreads * 8) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (!filling) {
-        if (G == 16 && d + 8 <= D) {
-          v = __ldg(reinterpret_cast<const uint4*>(src + d));
-        } else {
-          uint32_t w[4] = {0u, 0u, 0u, 0u};
-          if (G >= 4 && d + 8 <= D) {
+    const int end = t < 0 ? 0 : D;  // the filling: zeros
+    for (int d0 = lane * 8; d0 < D; d0 += kFlight * 256) {
+      uint4 v[kFlight];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(src + d) + i);
-          } else {
+      for (int i = 0; i < kFlight; ++i) v[i] = load_word<G>(src, d0 + i * 256, end);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (d + i < D) w[i / 2] |= static_cast<uint32_t>(__ldg(src + d + i)) << (16 * (i & 1));
-          }
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      *reinterpret_cast<uint4*>(dst + d) = v;  // D is filled up to the pitch, a multiple of 8
+      for (int i = 0; i < kFlight; ++i)  // D is filled up to the pitch, a multiple of 8
+        if (d0 + i * 256 < D) *reinterpret_cast<uint4*>(dst + d0 + i * 256) = v[i];
     }
   }
 }
@@ -468,14 +494,15 @@ cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream) {
   }
   const int each = (a.places <= 128 * 1024 ? 512 : kPlaceBlock) / kSortWarps;
   cudaError_t e = launch_next(count_kernel, dim3(blocks), kSortThreads, smem, stream, a, each);
-  if (e == cudaSuccess) e = launch_next(tiles_kernel, dim3(1), kSortThreads, 0, stream, a, blocks);
+  if (e == cudaSuccess) e = launch_next(tiles_kernel, dim3(1), kTilesThreads, 0, stream, a, blocks, std::min(16, kTilesThreads / a.E));
   if (e == cudaSuccess) e = launch_next(place_kernel, dim3(blocks), kSortThreads, smem, stream, a, each);
   return e;
 }
 
 cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const void* x, int64_t ldx, int granule, int D,
                                void* out, int64_t ld_out, int sms, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most_rows, 16 * std::max(1, sms))), 1, 1);
+  constexpr int kWarps = kGatherThreads / 32;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((most_rows + kWarps - 1) / kWarps, 4 * std::max(1, sms))), 1, 1);
   const auto kernel = granule == 16 ? gather_kernel<16> : granule >= 4 ? gather_kernel<4> : gather_kernel<2>;
   return launch_next(kernel, grid, kGatherThreads, 0, stream, static_cast<const int*>(rows.head),
                      static_cast<const int*>(rows.token), static_cast<const int*>(rows.place),
