@@ -96,7 +96,7 @@ def clip(tg, grads=(A0, B0), counts=(100, 200), dtypes=(0, 2), outputs=None, lim
 def test_gradient_refusals(tg):
     bad = tg.ERR_INVALID_VALUE
     for args in ({"counts": (-1, 5)}, {"grads": (0, B0)}, {"outputs": (0, B0)}, {"limit": -0.5}, {"limit": float("nan")},
-                 {"norm": 0}, {"ws": 0}, {"ws": D0 + 128}, {"n": 9727}):
+                 {"norm": 0}, {"ws": 0}, {"ws": D0 + 128}, {"n": 4863}):
         assert clip(tg, **args) == bad, args
     assert clip(tg, dtypes=(0, 3)) == clip(tg, dtypes=(0, -1)) == tg.ERR_UNSUPPORTED_DTYPE
     assert clip(tg, grads=(A0 + 2, B0)) == clip(tg, grads=(A0, B0 + 1)) == clip(tg, norm=C0 + 2) == \
@@ -111,8 +111,8 @@ def test_gradient_refusals(tg):
 
 
 def test_gradient_workspace(tg):
-    assert tg.grad_workspace_size(0) == tg.grad_workspace_size(1000) == (tg.OK, 9728)
-    assert tg.grad_workspace_size(1001) == (tg.OK, 2 * 9728)
+    assert tg.grad_workspace_size(0) == tg.grad_workspace_size(1000) == (tg.OK, 4864)
+    assert tg.grad_workspace_size(1001) == (tg.OK, 2 * 4864)
     assert tg.grad_workspace_size(-1)[0] == tg.ERR_INVALID_VALUE
     assert tg.grad_workspace_size(1 << 21)[0] == tg.ERR_TOO_LARGE
     assert tg.library().tgemm_grad_workspace_size(4, None) == tg.ERR_INVALID_VALUE

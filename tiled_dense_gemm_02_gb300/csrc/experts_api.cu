@@ -4,12 +4,14 @@
 //
 // Forward:  sort of the places  [gather of x]  UP  DOWN  join
 // Backward: [scale of fp16 gradients]  gather of grad  DH  DOUT  DX  join  DIN
-// (experts_rows.cu and experts_gemm.cuh hold the kernels.)  Weights whose rows are
+// A few places forward: UP and DOWN on the CUDA cores (experts_few.cu).
+// (experts_rows.cu and experts_gemm.cuh hold the other kernels.)  Weights whose rows are
 // not 16-byte aligned are copied to an aligned pitch first.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "../../include/tgemm_experts.h"
@@ -31,6 +33,19 @@ constexpr int64_t kMaxExtent = int64_t(1) << 31;
 constexpr int kChunk = 64, kExactChunk = 4;
 // Places up to which UP gathers x's rows by itself.
 constexpr int64_t kGatherPlaces = kPlaceBlock;
+// Whether a forward call reads the weights place by place on the CUDA cores: two launches
+// that stream p experts' weights at about 4.5 TB/s, or five that read those of the d
+// different ones among them (on average) at about 5.2 TB/s and start 12 us later.
+// Measured, p places, this way and the tensor cores: 2048 x 1024, 64 experts, p = 8 / 16 / 32 / 64
+// 27 / 41 / 72 / 130 and 39 / 60 / 82 / 116 us; 4096 x 4096, 8 experts, p = 2 / 4 / 8 / 16
+// 46 / 79 / 137 / 246 and 64 / 80 / 140 / 142 us; 512 x 256, 8 experts, p = 16 6 and 19 us.
+constexpr int64_t kFewPlaces = 32;
+bool few_places(int64_t places, int64_t E, int64_t D, int64_t F) {
+  if (places > kFewPlaces) return false;
+  const double mb = 6e-6 * static_cast<double>(D) * static_cast<double>(F), p = static_cast<double>(places);
+  const double different = E * (1.0 - std::pow(1.0 - 1.0 / static_cast<double>(E), p));
+  return p * mb / 4.5 <= different * mb / 5.2 + 12.0;
+}
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -149,7 +164,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t E, int64_t k, int64_t D, in
   l.x = take(rows * l.ldx * 2);
   l.w_in = take(l.copy_in ? E * 2 * F * l.ld_in * 2 : 0);
   l.w_out = take(l.copy_out ? E * D * l.ld_out * 2 : 0);
-  l.h = take(rows * l.ldh * 2);
+  l.h = take(rows * l.ldh * 2);  // 32 rows at least; a few places' h in fp32 is at most half as many
   l.y = take(rows * l.ldy * (dtype == TGEMM_BF16 ? 2 : 4));
   l.y_scale = take(dtype == TGEMM_BF16 ? rows / 16 * (l.ldy / 32) * 4 : 0);
   if (backward) {
@@ -305,6 +320,7 @@ class Experts {
   }
 
   int forward() {
+    if (few()) return forward_few();
     TGEMM_TRY(weights());
     OrderArgs o = {};
     o.ids = c_.ids;
@@ -406,6 +422,32 @@ class Experts {
   }
 
  private:
+  bool few() const {
+    return !saved_ && few_places(c_.T * c_.k, c_.E, c_.D, c_.F) && host_granule(c_.x, c_.ldx, 2) == 16 && !l_.copy_in && !l_.copy_out;
+  }
+  int forward_few() {
+    ExpertFewArgs a = {};
+    a.T = a_.T;
+    a.E = a_.E;
+    a.k = static_cast<int>(c_.k);
+    a.D = a_.D;
+    a.F = a_.F;
+    a.x = c_.x;
+    a.ldx = c_.ldx;
+    a.w_in = c_.w_in;
+    a.ld_in = c_.ld_in;
+    a.w_out = c_.w_out;
+    a.ld_out = c_.ld_out;
+    a.ids = c_.ids;
+    a.weights = c_.weights;
+    a.h = reinterpret_cast<float*>(ws_ + l_.h);
+    a.ldh = round_up(c_.F, 4);
+    a.out = c_.out;
+    a.ldo = c_.ldo;
+    TGEMM_CUDA(launch_experts_few(a, type_ == 0, c_.stream), "few places launch");
+    return TGEMM_OK;
+  }
+
   int64_t tokens(const ExpertArgs& a) const { return most_tiles(c_.T * c_.k, c_.E) * a.m_blocks; }
 
   template <typename Launch>

@@ -74,6 +74,26 @@ constexpr int kGradExponent = 4, kScaleBlocks = 512;
 cudaError_t launch_grad_scale(const void* g, int64_t T, int D, int64_t ld, unsigned int* largest, float* scale,
                               cudaStream_t stream);
 
+// ------------------------------------------------------------- a few places
+// Forward for a few places on the CUDA cores; x's and the weights' rows are 16-byte
+// aligned.
+struct ExpertFewArgs {
+  int T, E, k, D, F;
+  const void* x;
+  int64_t ldx;
+  const void* w_in;
+  int64_t ld_in;
+  const void* w_out;
+  int64_t ld_out;
+  const int64_t* ids;
+  const float* weights;
+  float* h;              // places x F
+  int64_t ldh;           // a multiple of 4
+  void* out;
+  int64_t ldo;
+};
+cudaError_t launch_experts_few(const ExpertFewArgs& a, bool bf16, cudaStream_t stream);
+
 // ---------------------------------------------------------------- products
 // M is a weight's axis, N the tokens' (the gradients of the weights: M and N the
 // weight's two axes, K the expert's rows).

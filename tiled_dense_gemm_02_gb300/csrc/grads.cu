@@ -5,12 +5,12 @@
 // read twice; it walks the list backwards, and so finds in L2 what the first pass
 // read last.
 //
-// The tensors are cut into chunks of 16 KB (kChunk) of their 16-byte words, dealt
+// The tensors are cut into chunks of 32 KB (kChunk) of their 16-byte words, dealt
 // to the blocks in turn; a launch carries its list of up to kList tensors in its
 // parameters, so the call keeps no table in device memory and can be captured.
-// Each thread has four 16-byte loads in flight.
+// Each thread has eight 16-byte loads in flight: whole chunks load without a condition.
 //
-// Squares: a thread adds the at most 32 squares of its share of a chunk in fp32
+// Squares: a thread adds the at most 32 squares of half of its share of a chunk in fp32
 // (an error of a few 2^-24, random over threads) and the shares in fp64, one
 // addition per 64 bytes, since fp64 additions per element would take three times
 // the bytes' time.  A share whose fp32 sum leaves [2^-90, 2^100) is summed again in fp64, from registers.
@@ -34,9 +34,10 @@ namespace tgemm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVectors = 4;                          // 16-byte words of a thread's share of a chunk
+constexpr int kVectors = 8;                          // 16-byte words of a thread's share of a chunk
 constexpr int kChunk = kThreads * kVectors;          // words of a chunk
-constexpr int kMaxBlocks = 8 * 152;                  // of one launch: eight resident blocks of 256 threads an SM
+constexpr int kBlocksPerSm = 4;
+constexpr int kMaxBlocks = kBlocksPerSm * 152;       // of one launch
 constexpr int64_t kMaxElements = int64_t(1) << 40;     // chunks stay ints
 constexpr int kShort = 40, kList = 1000;             // tensors of a launch; short lists have less to copy
 
@@ -70,6 +71,17 @@ struct View {
     base = reinterpret_cast<const uint8_t*>(p & ~uint64_t(15));
     skip = static_cast<int>(p & 15) >> (4 - shift);
     words = (skip + count + (1 << shift) - 1) >> shift;
+  }
+  // a chunk's words of this thread, from w0 on
+  __device__ __forceinline__ void load_chunk(int64_t w0, uint4 (&x)[kVectors]) const {
+    const int64_t c0 = w0 - threadIdx.x;
+    if (((c0 << shift) >= skip) && ((c0 + kChunk) << shift) - skip <= count) {  // all words whole
+#pragma unroll
+      for (int j = 0; j < kVectors; ++j) x[j] = __ldcg(reinterpret_cast<const uint4*>(base) + w0 + j * kThreads);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVectors; ++j) x[j] = load(w0 + j * kThreads);
+    }
   }
   // word w; elements outside the tensor are 0 and not read
   __device__ __forceinline__ uint4 load(int64_t w) const {
@@ -107,19 +119,18 @@ __device__ __forceinline__ float square_sum(const uint4& v, int type, float s) {
   return s;
 }
 
-__device__ __noinline__ double square_sum_wide(const uint4 (&v)[kVectors], int type) {
+__device__ __noinline__ double square_sum_wide(uint4 a, uint4 b, uint4 c, uint4 d, int type) {
+  const uint32_t w[16] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
   double s = 0.0;
-  for (int j = 0; j < kVectors; ++j) {
-    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-    for (int i = 0; i < 4; ++i) {
-      if (type == 2) {
-        const double x = __uint_as_float(w[i]);
-        s = fma(x, x, s);
-      } else {
-        const float2 x = halves(w[i], type);
-        s = fma(static_cast<double>(x.x), static_cast<double>(x.x), s);
-        s = fma(static_cast<double>(x.y), static_cast<double>(x.y), s);
-      }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (type == 2) {
+      const double x = __uint_as_float(w[i]);
+      s = fma(x, x, s);
+    } else {
+      const float2 x = halves(w[i], type);
+      s = fma(static_cast<double>(x.x), static_cast<double>(x.x), s);
+      s = fma(static_cast<double>(x.y), static_cast<double>(x.y), s);
     }
   }
   return s;
@@ -151,7 +162,7 @@ __device__ __forceinline__ int tensor_of(const List<MOST>& l, int chunk) {
 }
 
 template <int MOST>
-__global__ void __launch_bounds__(kThreads, 8) square_kernel(const __grid_constant__ List<MOST> l, double* partial) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) square_kernel(const __grid_constant__ List<MOST> l, double* partial) {
   __shared__ double shared[kThreads / 32];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -161,18 +172,20 @@ __global__ void __launch_bounds__(kThreads, 8) square_kernel(const __grid_consta
     const View v(l, t);
     const int64_t w0 = static_cast<int64_t>(c - l.first[t]) * kChunk + threadIdx.x;
     uint4 x[kVectors];
+    v.load_chunk(w0, x);
 #pragma unroll
-    for (int j = 0; j < kVectors; ++j) x[j] = v.load(w0 + j * kThreads);
-    float s = 0.0f;
+    for (int part = 0; part < kVectors; part += 4) {
+      float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kVectors; ++j) s = square_sum(x[j], v.type, s);
-    if (s >= 0x1p-90f && s < 0x1p100f) {
-      sum += s;
-    } else {
-      uint32_t any = 0u;
+      for (int j = 0; j < 4; ++j) s = square_sum(x[part + j], v.type, s);
+      if (s >= 0x1p-90f && s < 0x1p100f) {
+        sum += s;
+      } else {
+        uint32_t any = 0u;
 #pragma unroll
-      for (int j = 0; j < kVectors; ++j) any |= x[j].x | x[j].y | x[j].z | x[j].w;
-      if (any) sum += square_sum_wide(x, v.type);
+        for (int j = 0; j < 4; ++j) any |= x[part + j].x | x[part + j].y | x[part + j].z | x[part + j].w;
+        if (any) sum += square_sum_wide(x[part], x[part + 1], x[part + 2], x[part + 3], v.type);
+      }
     }
   }
   sum = block_sum(sum, shared);
@@ -216,7 +229,7 @@ __device__ __forceinline__ uint4 scaled(const uint4& v, int type, float f) {
 
 // `first`: this launch writes the norm.
 template <int MOST>
-__global__ void __launch_bounds__(kThreads, 8) scale_kernel(const __grid_constant__ List<MOST> l, const double* partial,
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_kernel(const __grid_constant__ List<MOST> l, const double* partial,
                                                             int n, float max_norm, float* norm, int first) {
   __shared__ double shared[kThreads / 32];
   ptx::griddep_launch_dependents();
@@ -232,8 +245,7 @@ __global__ void __launch_bounds__(kThreads, 8) scale_kernel(const __grid_constan
     const View v(l, t);
     const int64_t w0 = static_cast<int64_t>(c - l.first[t]) * kChunk + threadIdx.x;
     uint4 x[kVectors];
-#pragma unroll
-    for (int j = 0; j < kVectors; ++j) x[j] = v.load(w0 + j * kThreads);
+    v.load_chunk(w0, x);
     uint8_t* out = static_cast<uint8_t*>(l.out[t]);
     const int es = 16 >> v.shift, per = 1 << v.shift;
     const bool together = ((reinterpret_cast<uint64_t>(out) ^ reinterpret_cast<uint64_t>(l.in[t])) & 15) == 0;
@@ -371,7 +383,7 @@ void fill(List<MOST>& l, const GradCall& c, int64_t begin, int64_t end) {
 template <int MOST>
 int run_lists(const GradCall& c, int sms) {
   double* partial = static_cast<double*>(c.workspace);
-  const int most = std::min(kMaxBlocks, 8 * std::max(1, sms));
+  const int most = std::min(kMaxBlocks, kBlocksPerSm * std::max(1, sms));
   const auto list = std::unique_ptr<List<MOST>>(new (std::nothrow) List<MOST>);
   if (!list) return host_cuda_fail(cudaErrorMemoryAllocation, "gradient list");
   int parts = 0;

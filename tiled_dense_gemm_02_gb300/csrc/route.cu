@@ -4,16 +4,19 @@
 // coalesced pieces, once, and stays in registers.  Experts are picked by as many
 // rounds of "largest key, lowest index": keys as integers in the order of their
 // numbers, so that a round is a local maximum and two warp reductions
-// (redux.sync).  Rows are bytes-bound from some thousand rows on; below, the call is
-// one launch.
+// (redux.sync).  Bound by instructions: 16384 rows of 256 fp32 logits (2.7 us of bytes)
+// take 8 us for one pick and 1 us for each more, 19 us for eight with sigmoid scores and a
+// bias, 30 us with eight groups of which four are kept.
 //
 // Which keys.  Softmax and sigmoid grow with the logit, so without a bias (and
 // without sums of keys) the logits themselves are compared.  With one, score +
 // bias in fp32 may order two experts otherwise than the real numbers do, and picks
-// are whole numbers that a reader of the weights takes for exact: a row in which
-// two neighbouring picks, or two groups at the border, are closer than the keys'
-// errors (kMargin) is picked again with fp64 keys, unless the two are equal in logit
-// and bias and tie for certain.  About one row in a hundred at 256 experts.
+// are whole numbers that a reader of the weights takes for exact.  So where two
+// neighbours among the picks and the first that is not one are closer than the keys'
+// errors (margin_of), and differ in logit or bias, the picks and what follows them within
+// such steps are ranked by fp64 keys, one a lane.  Softmax scores (their total is a sum over
+// the row), groups that close at the border, and more than 32 candidates take the row's
+// fp64 keys whole.  About one row in a hundred at 256 experts is ranked again.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,11 +33,16 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr uint32_t kAll = 0xffffffffu;
-// Errors of fp32 keys: a score s is off by at most 2^-20.6 s (the exponential's two
-// last bits, the rounding of x - max, which is below 2^-24 |x - max| and weighs s
-// |x - max| < 1/e at most, the sum's and the division's), and key and sum of two
-// keys round once more; a difference of two sums has four such keys.
-constexpr float kMargin = 0x1p-18f;
+// How far two fp32 keys, or sums of two, may be off one another's difference, relative to
+// the largest score plus the largest bias.  A score's exponential is off by 2^-22 of it
+// and by the rounding of its argument, 1.44 |x| 2^-24 (|x| s (1 - s) and |x| s / s_max stay
+// below 0.4); sum, quotient, bias and the sum of two keys round once each; a difference of
+// two sums has four keys: below 2^-19 together.  Softmax: its total, a chain of n + 5
+// additions, is off by one factor for all.  The lowest bits of a key, of n keys a lane, hold
+// which of them it is: n units of 2^-23 on either side.
+constexpr float margin_of(bool sigmoid, int n) {
+  return 0x1p-19f + 2 * n * 0x1p-23f + (sigmoid ? 0.0f : (n + 5) * 0x1p-23f);
+}
 
 struct RouteArgs {
   int T, E, k;
@@ -75,11 +83,6 @@ __device__ __forceinline__ float number(uint32_t o) {
 }
 
 // The warp's largest key and the lowest index that holds it.
-__device__ __forceinline__ void best_of(uint32_t& key, int& at) {
-  const uint32_t top = __reduce_max_sync(kAll, key);
-  at = static_cast<int>(__reduce_min_sync(kAll, key == top ? static_cast<unsigned>(at) : UINT_MAX));
-  key = top;
-}
 __device__ __forceinline__ void best_of(uint64_t& key, int& at) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
@@ -108,6 +111,17 @@ template <typename K>
 __device__ __forceinline__ K sigmoid_of(K x) {
   return K(1) / (K(1) + exp(-x));
 }
+// For keys (margin_of): e^x, and 1 / (1 + e^-x).
+__device__ __forceinline__ float key_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  return y;
+}
+__device__ __forceinline__ float key_sigmoid(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + key_exp(-x)));
+  return y;
+}
 
 template <typename K>
 struct Order;
@@ -120,119 +134,176 @@ struct Order<double> {
   using type = uint64_t;
 };
 
-// Keeps the top_groups groups of the largest value: `keep` is their bit mask.  False:
-// the border is closer than `margin`.
+// A group's value as an ordered number, 0 where it is masked whole: from its two largest keys.
 template <typename K>
-__device__ __forceinline__ bool pick_groups(const K* keys, const RouteArgs& a, int lane, float margin, uint32_t& keep) {
+__device__ __forceinline__ typename Order<K>::type group_value(K first, K second, bool nan, const RouteArgs& a) {
   using O = typename Order<K>::type;
+  const K sum = a.top2 && second > -INFINITY ? first + second : first;
+  return nan ? ordered(K(NAN)) : first > -INFINITY ? ordered(sum) : O(0);
+}
+
+// Groups of any size, their keys in shared memory: lane g gets group g's value.
+template <typename K>
+__device__ __forceinline__ typename Order<K>::type shared_group(const K* keys, const RouteArgs& a, int lane) {
+  if (lane >= a.groups) return 0;
   const int size = a.E / a.groups;
+  K first = -INFINITY, second = -INFINITY;
+  bool nan = false;
+  const K* mine = keys + lane * size;
+  int i = lane % size;  // lanes start apart, so that they meet different banks
+  for (int n = 0; n < size; ++n) {
+    const K v = mine[i];
+    nan |= v != v;
+    if (v > first) {
+      second = first;
+      first = v;
+    } else if (v > second) {
+      second = v;
+    }
+    if (++i == size) i = 0;
+  }
+  return group_value(first, second, nan, a);
+}
+
+// Groups of 32, ordered keys: register g of every lane.
+template <int N>
+__device__ __forceinline__ uint32_t register_group(const uint32_t (&order)[N], const RouteArgs& a, int lane) {
+  uint32_t first = 0u, second = 0u;
+#pragma unroll
+  for (int g = 0; g < N; ++g) {
+    if (g >= a.groups) break;
+    const uint32_t top = __reduce_max_sync(kAll, order[g]);
+    const uint32_t holders = __ballot_sync(kAll, order[g] == top);
+    const uint32_t next = __reduce_max_sync(kAll, lane == __ffs(holders) - 1 ? 0u : order[g]);
+    if (lane == g) {
+      first = top;
+      second = next;
+    }
+  }
+  const float f = first ? number(first) : -INFINITY;
+  return group_value(f, second ? number(second) : -INFINITY, f != f, a);
+}
+
+// Keeps the top_groups groups of the largest value (lane g holds group g's): `keep` is
+// their bit mask.  False: the border is closer than `margin`.
+template <typename O>
+__device__ __forceinline__ bool pick_groups(O value, const RouteArgs& a, int lane, float margin, uint32_t& keep) {
+  int rank = 0;  // groups before this one
+  for (int g = 0; g < a.groups; ++g) {
+    const O other = __shfl_sync(kAll, value, g);
+    rank += other > value || (other == value && g < lane) ? 1 : 0;
+  }
+  const bool there = lane < a.groups && value != 0;
+  keep = __ballot_sync(kAll, there && rank < a.top_groups);
+  if constexpr (sizeof(O) == 4) {
+    const uint32_t last = __ballot_sync(kAll, there && rank == a.top_groups - 1);
+    const uint32_t out = __ballot_sync(kAll, there && rank == a.top_groups);
+    if (!last || !out) return true;
+    return !(number(__shfl_sync(kAll, value, __ffs(last) - 1)) - number(__shfl_sync(kAll, value, __ffs(out) - 1)) <= margin);
+  }
+  return true;
+}
+
+// The row's largest key and the lowest index that holds it, which is taken out.
+template <int N>
+__device__ __forceinline__ void next_pick(uint32_t (&order)[N], bool marked, int lane, uint32_t& top, int& at) {
+  uint32_t most = order[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) most = max(most, order[i]);
+  top = __reduce_max_sync(kAll, most);
+  if (marked) {  // the lowest bits tell which of a lane's keys it is
+    const int holder = __ffs(__ballot_sync(kAll, most == top)) - 1;
+    at = static_cast<int>(N - 1 - (top & (N - 1))) * 32 + holder;
+    const bool mine = lane == holder;
+#pragma unroll
+    for (int i = 0; i < N; ++i) order[i] = mine && order[i] == top ? 0u : order[i];
+  } else {
+    unsigned mine = UINT_MAX;
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i) mine = order[i] == top ? i * 32 + lane : mine;
+    at = static_cast<int>(__reduce_min_sync(kAll, mine));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (at == i * 32 + lane) order[i] = 0u;
+  }
+}
+template <int N>
+__device__ __forceinline__ void next_pick(uint64_t (&order)[N], bool, int lane, uint64_t& top, int& at) {
+  top = order[0];
+  at = lane;
+#pragma unroll
+  for (int i = 1; i < N; ++i)
+    if (order[i] > top) {
+      top = order[i];
+      at = i * 32 + lane;
+    }
+  best_of(top, at);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (at == i * 32 + lane) order[i] = 0;
+}
+
+// The value of x at expert e, which any lane may hold.
+template <int N>
+__device__ __forceinline__ float value_at(const float (&x)[N], int e) {
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float got = __shfl_sync(kAll, x[i], e & 31);
+    if (e >> 5 == i) v = got;
+  }
+  return v;
+}
+
+// The row's keys as ordered numbers, 0 where masked or in a group that is not kept.  False:
+// two groups at the border are closer than margin.  MARKED: the lowest bits of a key tell
+// which of the lane's it is.
+template <bool MARKED, typename K, int N, typename Key>
+__device__ __forceinline__ bool order_keys(typename Order<K>::type (&order)[N], Key key_of, const RouteArgs& a, int lane,
+                                           K* shared, float margin) {
+  using O = typename Order<K>::type;
+  K key[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    key[i] = key_of(i);
+    order[i] = key[i] == -INFINITY ? O(0) : MARKED ? (ordered(key[i]) & ~O(N - 1)) | O(N - 1 - i) : ordered(key[i]);
+  }
+  if (a.groups == 1) return true;
+  const int size = a.E / a.groups;
+  uint32_t keep;
   O value = 0;
-  if (lane < a.groups) {
-    K first = -INFINITY, second = -INFINITY;
-    bool nan = false;
-    const K* mine = keys + lane * size;
-    int i = lane % size;  // lanes start apart, so that they meet different banks
-    for (int n = 0; n < size; ++n) {
-      const K v = mine[i];
-      nan |= v != v;
-      if (v > first) {
-        second = first;
-        first = v;
-      } else if (v > second) {
-        second = v;
-      }
-      if (++i == size) i = 0;
-    }
-    const K sum = a.top2 && second > -INFINITY ? first + second : first;
-    // a group that is masked whole has no part: 0, below every number's order
-    value = nan ? ordered(K(NAN)) : first > -INFINITY ? ordered(sum) : O(0);
+  bool in_registers = false;
+  if constexpr (sizeof(K) == 4) {
+    in_registers = size == 32;
+    if (in_registers) value = register_group(order, a, lane);
   }
-  keep = 0u;
-  O last = 0;
-  bool sure = true;
-  for (int r = 0; r <= a.top_groups; ++r) {
-    O top = value;
-    int at = lane;
-    best_of(top, at);
-    if (top == 0) break;
-    if (r == a.top_groups) {
-      if constexpr (sizeof(K) == 4) sure = !(number(last) - number(top) <= margin);
-      break;
-    }
-    last = top;
-    keep |= 1u << at;
-    if (lane == at) value = 0;
+  if (!in_registers) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * 32 + lane < a.E) shared[i * 32 + lane] = key[i];
+    __syncwarp();
+    value = shared_group(shared, a, lane);
+    __syncwarp();
   }
+  const bool sure = pick_groups(value, a, lane, margin, keep);
+#pragma unroll
+  for (int i = 0; i < N; ++i)  // past the last group: 0 already
+    if (!(keep >> (size == 32 ? i : (i * 32 + lane) / size & 31) & 1u)) order[i] = 0;
   return sure;
 }
 
-// The row's picks: lane r gets the r-th's index, or -1.  False (fp32): not certain.
-template <typename K, int N, typename Key>
-__device__ __forceinline__ bool pick(Key key_of, const RouteArgs& a, int lane, K* shared, bool certain, float margin,
-                                     int& mine, const float (&x)[N]) {
-  using O = typename Order<K>::type;
-  O order[N];
-  bool sure = true;
-  uint32_t keep = kAll;
-  {
-    K key[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = key_of(i);
-    if (a.groups > 1) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i * 32 + lane < a.E) shared[i * 32 + lane] = key[i];
-      __syncwarp();
-      sure = pick_groups(shared, a, lane, margin, keep);
-      if (certain) sure = true;
-      __syncwarp();
-    }
-    const int size = a.E / a.groups;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = i * 32 + lane;
-      const bool in = e < a.E && (a.groups == 1 || (keep >> (e / size) & 1u));
-      // masked: 0, below every number's order (and -inf's)
-      order[i] = in && !(key[i] == -INFINITY) ? ordered(key[i]) : O(0);
-    }
-  }
-  mine = -1;
-  O before = 0;
-  int before_at = 0;
-  const int rounds = certain ? a.k : a.k + 1;  // the first that is not picked decides too
-  for (int r = 0; r < rounds; ++r) {
-    O top = order[0];
-    int at = lane;
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-      if (order[i] > top) {
-        top = order[i];
-        at = i * 32 + lane;
-      }
-    best_of(top, at);
+// The largest k keys: lane r gets the r-th's index, or -1.
+template <typename O, int N>
+__device__ __forceinline__ int pick(O (&order)[N], int k, int lane) {
+  int mine = -1;
+  for (int r = 0; r < k; ++r) {
+    O top;
+    int at;
+    next_pick(order, false, lane, top, at);
     if (top == 0) break;
-    if constexpr (sizeof(K) == 4) {
-      if (!certain && r > 0 && number(before) - number(top) <= margin) {
-        // equal in logit and bias: a tie whatever the arithmetic
-        float xa = 0.0f, xb = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (before_at / 32 == i) xa = x[i];
-          if (at / 32 == i) xb = x[i];
-        }
-        xa = __shfl_sync(kAll, xa, before_at & 31);
-        xb = __shfl_sync(kAll, xb, at & 31);
-        if (xa != xb || (a.bias && a.bias[before_at] != a.bias[at])) sure = false;
-      }
-    }
-    before = top;
-    before_at = at;
-    if (lane == r && r < a.k) mine = at;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (at == i * 32 + lane) order[i] = 0;
+    if (lane == r) mine = at;
   }
-  return sure;
+  return mine;
 }
 
 template <typename In, int N>
@@ -267,6 +338,93 @@ __device__ __forceinline__ float shifted_sigmoid(float x, float shift) {
   return x <= 0.0f ? expf(x - shift) / (1.0f + expf(x)) : 1.0f / (1.0f + expf(-x));
 }
 
+// The picks of a row with fp64 keys.
+template <typename In, int N>
+__device__ __noinline__ int pick_exact(const RouteArgs& a, int row, int lane, double* shared) {
+  float x[N], top = 0.0f;
+  load_row<In>(x, a, row, lane);
+  double total = 1.0;
+  if (!a.sigmoid) softmax_of(x, top, total);
+  uint64_t order[N];
+  order_keys<false>(
+      order,
+      [&](int i) {
+        const double v = x[i];
+        if (x[i] == -INFINITY) return v;
+        const double b = a.bias ? static_cast<double>(a.bias[i * 32 + lane]) : 0.0;
+        return (a.sigmoid ? sigmoid_of(v) : exp(v - static_cast<double>(top)) / total) + b;
+      },
+      a, lane, shared, 0.0f);
+  return pick(order, a.k, lane);
+}
+
+// The picks by fp32 keys of scores, ranked again where they are closer than the margin.
+template <typename In, int N>
+__device__ __forceinline__ int pick_scores(uint32_t (&order)[N], const RouteArgs& a, int row, int lane, float margin,
+                                           bool sure, double* shared) {
+  uint32_t key = 0u, next = 0u;  // lane r: the r-th largest; the one after all of them
+  int mine = -1, next_at = 0, n = 0;
+  for (; n < a.k; ++n) {
+    next_pick(order, true, lane, next, next_at);
+    if (next == 0) break;
+    if (lane == n) {
+      key = next;
+      mine = next_at;
+    }
+  }
+  if (n == a.k) next_pick(order, true, lane, next, next_at);  // the first that is not picked decides too
+  // lane r: the key and the index behind the r-th
+  const auto behind = [&](int& at) {
+    const uint32_t k = __shfl_down_sync(kAll, key, 1);
+    at = __shfl_down_sync(kAll, mine, 1);
+    if (lane == n - 1) at = next_at;
+    return lane == n - 1 ? next : k;
+  };
+  int after_at;
+  const uint32_t after = behind(after_at);
+  const bool close = lane < n && after != 0 && number(key) - number(after) <= margin;
+  if (sure && !__any_sync(kAll, close)) return mine;
+  const In* logits = static_cast<const In*>(a.logits) + row * a.ld;
+  // equal in logit and bias: a tie whatever the arithmetic
+  const bool differ = close && (to_float(logits[mine]) != to_float(logits[after_at]) ||
+                                (a.bias && a.bias[mine] != a.bias[after_at]));
+  if (sure && !__any_sync(kAll, differ)) return mine;
+  if (sure && a.sigmoid) {
+    // as many more as follow one another within the margin
+    uint32_t last = __shfl_sync(kAll, key, n - 1);
+    while (next != 0 && n < 32 && number(last) - number(next) <= margin) {
+      if (lane == n) {
+        key = next;
+        mine = next_at;
+      }
+      last = next;
+      ++n;
+      next_pick(order, true, lane, next, next_at);
+    }
+    if (next == 0 || !(number(last) - number(next) <= margin)) {
+      double exact = -INFINITY;
+      if (lane < n) {
+        const double v = to_float(logits[mine]);
+        exact = sigmoid_of(v) + (a.bias ? static_cast<double>(a.bias[mine]) : 0.0);
+      }
+      const uint64_t own = lane < n ? ordered(exact) : 0ull;
+      int rank = 0;
+      for (int r = 0; r < n; ++r) {
+        const uint64_t other = __shfl_sync(kAll, own, r);
+        const int at = __shfl_sync(kAll, mine, r);
+        rank += other > own || (other == own && at < mine) ? 1 : 0;
+      }
+      int picked = -1;  // lane r takes the candidate of rank r
+      for (int r = 0; r < n; ++r) {
+        const int at = __shfl_sync(kAll, mine, r), place = __shfl_sync(kAll, rank, r);
+        if (place == lane && lane < a.k) picked = at;
+      }
+      return picked;
+    }
+  }
+  return pick_exact<In, N>(a, row, lane, shared);
+}
+
 template <typename In, int N>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ double shared_keys[];
@@ -282,40 +440,34 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   const bool scores = a.bias || (a.groups > 1 && a.top2);  // keys are scores, not logits
   if (!a.sigmoid && (scores || !a.renormalize)) softmax_of(x, top, total);
   int mine;
+  uint32_t order[N];
   if (!scores) {
-    pick<float, N>([&](int i) { return x[i]; }, a, lane, reinterpret_cast<float*>(shared), true, 0.0f, mine, x);
+    order_keys<false>(order, [&](int i) { return x[i]; }, a, lane, reinterpret_cast<float*>(shared), 0.0f);
+    mine = pick(order, a.k, lane);
   } else {
     float b[N], most = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      b[i] = a.bias && i * 32 + lane < a.E ? a.bias[i * 32 + lane] : 0.0f;
+      b[i] = a.bias && i * 32 + lane < a.E ? __ldg(a.bias + i * 32 + lane) : 0.0f;
       most = fmaxf(most, fabsf(b[i]) < INFINITY ? fabsf(b[i]) : 0.0f);
     }
-    most = warp_max(most);
+    if (a.bias) most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most)));
     const float inv = 1.0f / total;
-    const float margin = kMargin * (most + (a.sigmoid ? 1.0f : fminf(inv, 1.0f)));  // softmax's largest is 1 / total
-    const bool sure = pick<float, N>(
+    // softmax's largest score is 1 / total
+    const float margin = a.sigmoid ? margin_of(true, N) * (most + 1.0f) : margin_of(false, N) * (most + fminf(inv, 1.0f));
+    const bool sure = order_keys<true>(
+        order,
         [&](int i) {
           if (x[i] == -INFINITY) return x[i];
-          return (a.sigmoid ? sigmoid_of(x[i]) : expf(x[i] - top) * inv) + b[i];
+          return (a.sigmoid ? key_sigmoid(x[i]) : key_exp(x[i] - top) * inv) + b[i];
         },
-        a, lane, reinterpret_cast<float*>(shared), false, margin, mine, x);
-    if (!sure) {
-      float top64;
-      double total64 = 1.0;
-      if (!a.sigmoid) softmax_of(x, top64, total64);
-      pick<double, N>(
-          [&](int i) {
-            if (x[i] == -INFINITY) return -static_cast<double>(INFINITY);
-            const double v = x[i];
-            return (a.sigmoid ? sigmoid_of(v) : exp(v - static_cast<double>(top)) / total64) + static_cast<double>(b[i]);
-          },
-          a, lane, shared, true, 0.0f, mine, x);
-    }
+        a, lane, reinterpret_cast<float*>(shared), margin);
+    mine = pick_scores<In, N>(order, a, row, lane, margin, sure, shared);
   }
   // lane r: the r-th pick's weight
   const bool used = mine >= 0;
-  const float v = used ? to_float(static_cast<const In*>(a.logits)[row * a.ld + mine]) : -INFINITY;
+  const float at_mine = value_at(x, max(mine, 0));
+  const float v = used ? at_mine : -INFINITY;
   float w = 0.0f;
   if (a.renormalize) {
     const float most = warp_max(v);  // NaN is passed over: it comes back in the sum
@@ -344,19 +496,22 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __gri
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (row >= a.T) return;
-  const In* src = static_cast<const In*>(a.logits) + row * a.ld;
+  float x[N];
+  load_row<In>(x, a, row, lane);  // the picked logits too come from here: no load waits for another
   int mine = -1;
   float g = 0.0f;
   if (lane < a.k) {
     const int64_t at = static_cast<int64_t>(row) * a.k + lane;
     const int64_t id = a.ids_in[at];
+    const float grad = a.grad[at];
     if (id >= 0 && id < a.E) {
       mine = static_cast<int>(id);
-      g = a.grad[at];
+      g = grad;
     }
   }
   const bool used = mine >= 0;
-  const float v = used ? to_float(src[mine]) : -INFINITY;
+  const float at_mine = value_at(x, max(mine, 0));
+  const float v = used ? at_mine : -INFINITY;
   float d[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) d[i] = 0.0f;
@@ -373,8 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __gri
   } else if (a.sigmoid) {
     own = g * sigmoid_of(v) * (1.0f / (1.0f + expf(v)));
   } else {
-    float x[N], top, total;
-    load_row<In>(x, a, row, lane);
+    float top, total;
     softmax_of(x, top, total);
     if (used) own = g * (expf(v - top) / total);
     const float mean = warp_sum(used ? own : 0.0f);

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from array import array
-from operator import index
+from operator import attrgetter, index
 
 from . import BF16, F16, F32, OK, TgemmError, library
 from .loss import _current_stream, _guarded
@@ -74,19 +74,20 @@ def _dense(t):
 
 
 def _tensors(name, tensors):
-    """(device, pointers, counts, dtype codes) of a list of dense tensors on one CUDA device."""
+    """(device, pointers, counts, dtype codes, whether all are contiguous) of dense tensors on one CUDA device.  One pass
+    per property, without a line of Python per tensor: a call may list thousands."""
     import torch
-    codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-    try:
-        kinds = [codes[t.dtype] for t in tensors]
-    except KeyError as e:
-        raise ValueError(f"{name}: unsupported dtype {e.args[0]}") from None
-    devices = {t.get_device() for t in tensors}
+    codes, tensor = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}, torch.Tensor
+    kinds = list(map(codes.get, map(attrgetter("dtype"), tensors)))
+    if None in kinds:
+        raise ValueError(f"{name}: unsupported dtype {tensors[kinds.index(None)].dtype}")
+    devices = set(map(tensor.get_device, tensors))
     if len(devices) != 1 or -1 in devices:
         raise ValueError(f"{name} must be on one CUDA device")
-    if not all([t.is_contiguous() or _dense(t) for t in tensors]):
+    contiguous = all(map(tensor.is_contiguous, tensors))
+    if not contiguous and not all(map(_dense, tensors)):
         raise ValueError(f"{name} must be dense: a view with gaps or repeats has no elements of its own")
-    return devices.pop(), [t.data_ptr() for t in tensors], [t.numel() for t in tensors], kinds
+    return devices.pop(), list(map(tensor.data_ptr, tensors)), list(map(tensor.numel, tensors)), kinds, contiguous
 
 
 def _run(tensors, outputs, max_norm, workspace, stream):
@@ -94,17 +95,18 @@ def _run(tensors, outputs, max_norm, workspace, stream):
     tensors = list(tensors)
     if not tensors:
         raise ValueError("gradients must list at least one tensor")
-    device, pointers, counts, kinds = _tensors("gradients", tensors)
+    device, pointers, counts, kinds, contiguous = _tensors("gradients", tensors)
     places = None
     if outputs is not None:
         outputs = list(outputs)
         if len(outputs) != len(tensors):
             raise ValueError(f"outputs must list {len(tensors)} tensors, got {len(outputs)}")
-        other, places, sizes, types = _tensors("outputs", outputs)
+        other, places, sizes, types, filled = _tensors("outputs", outputs)
         if other != device or sizes != counts or types != kinds:
             raise ValueError("outputs must have the gradients' sizes, dtypes and device")
-        if not all([o.stride() == t.stride() and o.shape == t.shape for o, t in zip(outputs, tensors)]):
-            raise ValueError("outputs must have the gradients' shapes and strides")
+        if not (contiguous and filled) and \
+                not all([o.stride() == t.stride() and o.shape == t.shape for o, t in zip(outputs, tensors)]):
+            raise ValueError("outputs must have the gradients' order of elements: shapes and strides")
     st, need = grad_workspace_size(len(tensors))
     if st != OK:
         raise TgemmError(st, "tgemm_grad_workspace_size")
@@ -148,7 +150,7 @@ def gradient_norm(gradients, *, workspace=None, stream=None):
 def clip_gradients(gradients, max_norm, *, outputs=None, workspace=None, stream=None):
     """Scales ``gradients`` by ``max_norm / norm`` where their norm over all
     tensors is above ``max_norm``, in place or into ``outputs`` (tensors of the
-    same shapes and strides; where nothing is scaled they get copies), and
+    same sizes and order of elements; where nothing is scaled they get copies), and
     returns the norm before it, as ``gradient_norm`` does.
 
     The host does not wait.  A norm that is infinite or NaN scales nothing: the
