@@ -13,7 +13,9 @@ With p the operands' significant bits, u = 2^-p half a step of their type:
 * dg = w v u silu'(g), with |silu''| <= 0.5, and du = w v silu(g) likewise; fp16 holds them
   times a power of two that brings the largest |grad| to 16 or more;
 * the products that follow add their operands' errors to their own 2^-15, the fp32
-  sums over a token's rows 2^-21, and the result is rounded once more.
+  sums over a token's rows 2^-21, and the result is rounded once more;
+* bf16: rows on their way to those sums are halves with a power of two of their own, half a
+  step of 11 bits: 2^-12 of each.
 """
 from __future__ import annotations
 
@@ -29,6 +31,7 @@ class Experts:
         E, _, F = w_in.shape[0], 0, w_out.shape[2]
         unit = torch.finfo(x.dtype).eps / 2
         tiny = 2.0 ** -25 if x.dtype == torch.float16 else 0.0
+        row = 2.0 ** -12 if x.dtype == torch.bfloat16 else 0.0
         exact = grad is not None if exact is None else exact
         first = EXACT_SUM if exact else SUM
         f64 = {"dtype": torch.float64, "device": x.device}
@@ -54,7 +57,7 @@ class Experts:
             e_h0 = 1.1 * up.abs() * e_g + silu.abs() * e_u + 2.0 ** -20 * h.abs()
             e_h = e_h0 + unit * h.abs() + tiny
             y = h @ b.t()
-            e_y = e_h @ b.abs().t() + SUM * (h.abs() @ b.abs().t())
+            e_y = e_h @ b.abs().t() + SUM * (h.abs() @ b.abs().t()) + row * y.abs()
             self.out.index_add_(0, t, w * y)
             self.e_out.index_add_(0, t, w.abs() * e_y)
             size.index_add_(0, t, w.abs() * y.abs())
@@ -71,7 +74,7 @@ class Experts:
             e_du = w.abs() * (e_v * silu.abs() + 1.1 * v.abs() * e_g) + (unit + 2.0 ** -20) * du.abs() + small
             d, e_d = torch.cat([dg, du], dim=1), torch.cat([e_dg, e_du], dim=1)
             self.dx.index_add_(0, t, d @ a)
-            self.e_dx.index_add_(0, t, e_d @ a.abs() + SUM * (d.abs() @ a.abs()))
+            self.e_dx.index_add_(0, t, e_d @ a.abs() + SUM * (d.abs() @ a.abs()) + row * (d @ a).abs())
             size_dx.index_add_(0, t, (d @ a).abs())
             self.dw_in[e] = d.t() @ xe
             self.e_dw_in[e] = e_d.t() @ xe.abs() + SUM * (d.abs().t() @ xe.abs())

@@ -129,3 +129,67 @@ def test_headers_are_c(tmp_path):
     subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o",
                     str(tmp_path / "both")], check=True)
     assert subprocess.run([str(tmp_path / "both")], capture_output=True, text=True, check=True).stdout == "32\n"
+
+
+def forward(tg, T=64, E=4, k=2, D=32, F=48, x=A0, ldx=32, w_in=B0, ld_in=32, w_out=C0, ld_out=48, ids=D0, w=E0, dtype=2, out=F0,
+            ldo=32, saved=0, sn=0, ws=G0, n=1 << 24, **o):
+    return tg.experts_forward(T, E, k, D, F, x, ldx, w_in, ld_in, w_out, ld_out, ids, w, dtype, out, ldo, saved, sn, o or None, ws, n)
+
+
+DX0, DI0, DO0, DW0 = (0x1000000000 * (i + 20) for i in range(4))
+
+
+def backward(tg, T=64, E=4, k=2, D=32, F=48, x=A0, ldx=32, w_in=B0, ld_in=32, w_out=C0, ld_out=48, w=E0, dtype=2, saved=H0, sn=1 << 24,
+             g=F0, ldg=32, dx=DX0, lddx=32, di=DI0, ldi=32, do=DO0, ldo=48, dw=DW0, ws=G0, n=1 << 24, **o):
+    return tg.experts_backward(T, E, k, D, F, x, ldx, w_in, ld_in, w_out, ld_out, w, saved, sn, g, ldg, dtype, dx, lddx, di, ldi, do,
+                               ldo, dw, o or None, ws, n)
+
+
+def test_expert_refusals(tg):
+    bad = tg.ERR_INVALID_VALUE
+    for call in (forward, backward):
+        for args in ({"T": -1}, {"E": 0}, {"k": 0}, {"D": 0}, {"F": 0}, {"ldx": 31}, {"ld_in": 31}, {"ld_out": 47}, {"x": 0}, {"w_in": 0},
+                     {"w_out": 0}, {"w": 0}, {"ws": 0}, {"ws": G0 + 128}, {"n": 1000}, {"wait_timeout_us": -1}):
+            assert call(tg, **args) == bad, args
+        assert call(tg, dtype=0) == call(tg, dtype=3) == tg.ERR_UNSUPPORTED_DTYPE
+        assert call(tg, x=A0 + 1) == call(tg, w_in=B0 + 1) == call(tg, w_out=C0 + 1) == call(tg, w=E0 + 2) == tg.ERR_MISALIGNED
+        big = tg.ERR_TOO_LARGE
+        assert call(tg, E=1025) == call(tg, k=1 << 16) == call(tg, D=1 << 24, ldx=1 << 24, ld_in=1 << 24) == big
+        assert call(tg, T=1 << 30, k=2) == call(tg, ldx=1 << 31) == call(tg, E=1024, F=1 << 21, ld_out=1 << 21) == big
+    assert forward(tg, ids=0) == forward(tg, out=0) == forward(tg, ldo=31) == forward(tg, saved=H0, sn=100) == bad
+    assert forward(tg, saved=H0 + 64, sn=1 << 24) == bad
+    assert backward(tg, saved=0) == backward(tg, sn=100) == backward(tg, g=0) == backward(tg, ldg=31) == bad
+    assert backward(tg, lddx=31) == backward(tg, ldi=31) == backward(tg, ldo=47) == bad
+    assert forward(tg, ids=D0 + 4) == forward(tg, out=F0 + 1) == backward(tg, dw=DW0 + 2) == backward(tg, g=F0 + 1) == tg.ERR_MISALIGNED
+    for args in ({"out": A0}, {"out": B0 + 64}, {"ws": A0}, {"out": E0}, {"saved": G0, "sn": 1 << 24}, {"out": G0}, {"ids": F0}):
+        assert forward(tg, **args) == tg.ERR_ALIAS, args
+    for args in ({"dx": A0}, {"di": B0}, {"do": C0 + 2}, {"dw": E0}, {"dx": DI0}, {"do": DI0 + 4 * 96 * 32 * 2 - 2}, {"ws": H0}, {"dx": H0},
+                 {"g": DX0}):
+        assert backward(tg, **args) == tg.ERR_ALIAS, args
+    assert forward(tg, T=0, x=0, ids=0, out=0, ws=0) == tg.OK
+    assert backward(tg, dx=0, di=0, do=0, dw=0) == tg.OK
+    o = tg.ExpertsOptions()
+    o.reserved[2] = 1
+    assert tg.experts_forward(4, 2, 1, 8, 8, A0, 8, B0, 8, C0, 8, D0, E0, 2, F0, 8, 0, 0, o, G0, 1 << 20) == bad
+
+
+def test_expert_sizes(tg):
+    import itertools
+    decls = fields(header("tgemm_experts.h"), "tgemm_experts_options")
+    assert decls == ["int wait_timeout_us", "int reserved[3]"] and ctypes.sizeof(tg.ExpertsOptions) == 16
+    for T, E, k, D, F in itertools.product((1, 7, 300), (1, 5, 300), (1, 4), (8, 100), (8, 70)):
+        rows = -(-(T * k + 31 * min(E, T * k)) // 32) * 32
+        st, saved = tg.experts_saved_size(T, E, k, D, F, 2)
+        assert st == tg.OK and saved >= rows * (8 * F + 2 * D)
+        for backward in (0, 1):
+            st, n = tg.experts_workspace_size(backward, T, E, k, D, F, 0, D, 0, F, 2)
+            assert st == tg.OK and n >= rows * (2 * F + 2 * D + (4 * F if backward else 0))
+            # misaligned weights are copied
+            copies = (E * 2 * F * D * 2 if D % 8 == 0 else 0) + (E * D * F * 2 if F % 8 == 0 else 0)
+            # (an empty part takes 256 bytes)
+            assert tg.experts_workspace_size(backward, T, E, k, D, F, 2, D, 2, F, 2)[1] >= n + copies - 512
+            assert tg.experts_workspace_size(backward, T, E, k, D, F, 0, D, 0, F, 1)[1] > n  # fp16's rows to join are fp32
+    assert tg.experts_workspace_size(2, 4, 2, 1, 8, 8, 0, 8, 0, 8, 2)[0] == tg.ERR_INVALID_VALUE
+    assert tg.experts_workspace_size(0, 4, 2, 1, 8, 8, 0, 7, 0, 8, 2)[0] == tg.ERR_INVALID_VALUE
+    assert tg.experts_workspace_size(0, 4, 2, 1, 8, 8, 0, 8, 0, 8, 0)[0] == tg.ERR_UNSUPPORTED_DTYPE
+    assert tg.experts_saved_size(0, 2, 1, 8, 8, 2) == tg.experts_workspace_size(1, 0, 2, 1, 8, 8, 0, 8, 0, 8, 2) == (tg.OK, 0)

@@ -141,7 +141,7 @@ SavedLayout plan_saved(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F) {
 struct Layout {
   bool copy_in, copy_out;  // weights off the 16-byte grid
   RowsLayout rows;
-  int64_t partial, x, w_in, w_out, h, dgu, y, y_scale, dots, largest, scale;
+  int64_t partial, x, w_in, w_out, h, dgu, y, y_exponent, dots, largest, scale;
   int64_t ldx, ldh, ld_dgu, ldy, ld_in, ld_out;
   int parts;               // DH: dots of a row
   int64_t total;
@@ -166,7 +166,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t E, int64_t k, int64_t D, in
   l.w_out = take(l.copy_out ? E * D * l.ld_out * 2 : 0);
   l.h = take(rows * l.ldh * 2);  // 32 rows at least; a few places' h in fp32 is at most half as many
   l.y = take(rows * l.ldy * (dtype == TGEMM_BF16 ? 2 : 4));
-  l.y_scale = take(dtype == TGEMM_BF16 ? rows / 16 * (l.ldy / 32) * 4 : 0);
+  l.y_exponent = take(dtype == TGEMM_BF16 ? rows * (l.ldy / 32) : 0);
   if (backward) {
     l.dgu = take(rows * l.ld_dgu * 2);
     l.dots = take(rows * l.parts * 4);
@@ -312,7 +312,7 @@ class Experts {
     a_.dots = reinterpret_cast<float*>(ws_ + l_.dots);
     a_.weights = c.weights;
     a_.y = ws_ + l_.y;
-    a_.y_scale = reinterpret_cast<float*>(ws_ + l_.y_scale);
+    a_.y_exponent = reinterpret_cast<uint8_t*>(ws_ + l_.y_exponent);
     a_.ldy = l_.ldy;
     const int to_us = (c.opts && c.opts->wait_timeout_us) ? c.opts->wait_timeout_us : 2000000;
     a_.timeout_ns = static_cast<unsigned long long>(to_us) * 1000ull;
@@ -506,7 +506,7 @@ class Experts {
     j.k = static_cast<int>(c_.k);
     j.D = a_.D;
     j.y = a_.y;
-    j.y_scale = a_.y_scale;
+    j.y_exponent = a_.y_exponent;
     j.ldy = a_.ldy;
     j.type = type_;
     TGEMM_CUDA(launch_join(j, c_.stream), "join launch");

@@ -282,24 +282,42 @@ __device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertAr
   }
 }
 
-// The same for bf16 operands: halves, with one power of two for 16 rows' 32 neighbours
-// that brings the largest finite one to [2^14, 2^15).  A half's 11 bits are off by
-// 1.4e-4 on average (values below 2^-28 of the largest by more), which beside h's
-// rounding and the result's (1.65e-3 each) is 0.2 % of the error; y's bytes, written
-// here and read by the join, are what DOWN's epilogue costs.
+// The same for bf16 operands: halves, with one power of two for a row's 32 neighbours that
+// brings the largest finite one to [2^14, 2^15).  A half's 11 bits are off by 1.4e-4 on
+// average (values below 2^-28 of the largest by more), which beside h's rounding and the
+// result's (1.65e-3 each) is 0.2 % of the error; y's bytes, written here and read by the
+// join, are what DOWN's epilogue costs (8192 tokens, 64 experts, fp32: join 94 us, 53 so).
 __device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int lane) {
   RowStore<true> y(a.y, row, a.ldy, d, static_cast<int>(a.ldy), lane);
-  uint32_t most = 0u;
+  uint32_t most[16], all = 0u;
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
-    const uint32_t size = v[c] & 0x7FFFFFFFu;
-    most = max(most, size < 0x7F800000u ? size : 0u);
+    most[c] = __reduce_max_sync(0xffffffffu, v[c] & 0x7FFFFFFFu);
+    all = max(all, most[c]);
   }
-  const uint32_t exponent = max(15u, __reduce_max_sync(0xffffffffu, most) >> 23);
-  const float f = __uint_as_float((268u - exponent) << 23);
+  if (all >= 0x7F800000u) {  // infinities and NaN stay what they are, and take nothing from their neighbours
 #pragma unroll
-  for (int c = 0; c < 16; c += 2) y.put(pack_pair(f * __uint_as_float(v[c]), f * __uint_as_float(v[c + 1]), OUT_F16));
-  if (lane == 0 && d < a.ldy) __stcg(a.y_scale + row / 16 * (a.ldy / 32) + d / 32, __uint_as_float((exponent - 14u) << 23));
+    for (int c = 0; c < 16; ++c) {
+      const uint32_t size = v[c] & 0x7FFFFFFFu;
+      most[c] = __reduce_max_sync(0xffffffffu, size < 0x7F800000u ? size : 0u);
+    }
+  }
+  uint32_t exponents[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int c = 0; c < 16; c += 2) {
+    float f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t exponent = max(15u, most[c + e] >> 23);
+      exponents[(c + e) / 4] |= exponent << (8 * ((c + e) & 3));
+      f[e] = __uint_as_float((268u - exponent) << 23) * __uint_as_float(v[c + e]);
+    }
+    y.put(pack_pair(f[0], f[1], OUT_F16));
+  }
+  if (lane < 16 && d - lane < a.ldy) {
+    const uint32_t word = lane < 8 ? (lane < 4 ? exponents[0] : exponents[1]) : (lane < 12 ? exponents[2] : exponents[3]);
+    a.y_exponent[(row + lane) * (a.ldy / 32) + d / 32] = static_cast<uint8_t>(word >> (8 * (lane & 3)));
+  }
 }
 
 // A weight's gradient: this warp's 32 rows of M, its 128 columns of N.  `sums`: 0 for

@@ -54,8 +54,8 @@ struct JoinArgs {
   const float* weights;
   int64_t T;
   int k, D;
-  const void* y;        // fp32, or (type 0) halves times y_scale of 16 rows' 32 columns
-  const float* y_scale;
+  const void* y;        // fp32, or (type 0) halves times 2^(e - 141), e = y_exponent of 32 columns
+  const uint8_t* y_exponent;
   int64_t ldy;
   int type;
   void* out;
@@ -124,9 +124,9 @@ struct ExpertArgs {
   float* dots;             // DH: m_blocks * 8 per row
   const float* weights;    // DH: of each place
   const float* scale;      // {s, 1 / s} (fp16), or null: DH multiplies dg and du with s, DIN with 1 / s
-  void* y;                 // DOWN, DX: fp32, or (bf16) halves times y_scale of 16 rows' 32 columns
+  void* y;                 // DOWN, DX: fp32, or (bf16) halves with an exponent for each 32 columns (JoinArgs)
   int64_t ldy;             // a multiple of 64
-  float* y_scale;
+  uint8_t* y_exponent;     // row's pitch ldy / 32
   void* out;               // DIN, DOUT
   int64_t ld_out;
   int store_granule;       // 0 bulk-tensor stores, else the granule of per-thread stores

@@ -338,7 +338,7 @@ struct JoinKernelArgs {
   const float* weights;
   int k, D;
   const void* y;
-  const float* y_scale;
+  const uint8_t* y_exponent;
   int64_t ldy;
   void* out;
   int64_t ld_out;
@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       if constexpr (BF16) {
         const uint4 v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.y) + row * a.ldy + d));
         const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-        w *= __ldcg(a.y_scale + row / 16 * (a.ldy / 32) + d / 32);  // a power of two: exact
+        const uint32_t e = __ldcg(a.y_exponent + row * (a.ldy / 32) + d / 32);
+        w *= __uint_as_float((e - 14u) << 23);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
@@ -516,7 +517,7 @@ cudaError_t launch_join(const JoinArgs& j, cudaStream_t stream) {
   a.k = j.k;
   a.D = j.D;
   a.y = j.y;
-  a.y_scale = j.y_scale;
+  a.y_exponent = j.y_exponent;
   a.ldy = j.ldy;
   a.out = j.out;
   a.ld_out = j.ld_out;
