@@ -3,7 +3,7 @@
 // order of launches.
 //
 // Forward:  sort of the places  [gather of x]  UP  DOWN  join
-// Backward: [scale of fp16 gradients]  gather of grad  DH  DOUT  DX  join  DIN
+// Backward: gather of grad  DH  DOUT  DX  join  DIN
 // A few places forward: UP and DOWN on the CUDA cores (experts_few.cu).
 // (experts_rows.cu and experts_gemm.cuh hold the other kernels.)  Weights whose rows are
 // not 16-byte aligned are copied to an aligned pitch first.
@@ -170,7 +170,7 @@ Layout plan_layout(bool backward, int64_t T, int64_t E, int64_t k, int64_t D, in
   if (backward) {
     l.dgu = take(rows * l.ld_dgu * 2);
     l.dots = take(rows * l.parts * 4);
-    l.largest = take(kScaleBlocks * 4);
+    l.largest = take(kGatherMost * 4);
     l.scale = take(8);
   } else {
     l.rows = plan_rows(take, places, E);
@@ -369,13 +369,11 @@ class Experts {
     TGEMM_TRY(weights());
     ExpertMaps m;
     if (type_ == 1) {
-      float* scale = reinterpret_cast<float*>(ws_ + l_.scale);
-      TGEMM_CUDA(launch_grad_scale(c_.grad, c_.T, a_.D, c_.ldg, reinterpret_cast<unsigned int*>(ws_ + l_.largest), scale,
-                                   c_.stream),
-                 "gradient scale launch");
-      a_.scale = scale;
+      a_.largest = reinterpret_cast<unsigned int*>(ws_ + l_.largest);
+      a_.gathered = gather_blocks(rows_max_, sms_);
+      a_.scale = reinterpret_cast<float*>(ws_ + l_.scale);
     }
-    TGEMM_TRY(gather(c_.grad, c_.ldg, ws_ + l_.x));
+    TGEMM_TRY(gather(c_.grad, c_.ldg, ws_ + l_.x, const_cast<unsigned int*>(a_.largest)));
     {
       ExpertArgs a = a_;
       TGEMM_TRY(map_transposed(m, a, w_out_, c_.F, c_.D));
@@ -493,8 +491,8 @@ class Experts {
     TGEMM_TRY(map_rows(&m.b32, p, cols, ld, 32));
     return map_rows(&m.b16, p, cols, ld, 16);
   }
-  int gather(const void* x, int64_t ld, void* rows) {
-    TGEMM_CUDA(launch_gather_rows(a_.rows, rows_max_, x, ld, host_granule(x, ld, 2), a_.D, rows, l_.ldx, sms_,
+  int gather(const void* x, int64_t ld, void* rows, unsigned int* largest = nullptr) {
+    TGEMM_CUDA(launch_gather_rows(a_.rows, rows_max_, x, ld, host_granule(x, ld, 2), a_.D, rows, l_.ldx, largest, sms_,
                                   c_.stream),
                "gather launch");
     return TGEMM_OK;

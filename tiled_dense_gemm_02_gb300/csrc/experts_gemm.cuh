@@ -72,6 +72,20 @@ __device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// The power of two that the fp16 gradients of a call are multiplied with (a warp).
+__device__ __forceinline__ float gradient_scale(const ExpertArgs& a, int lane, bool leave) {
+  uint32_t most = 0u;
+  for (int i = lane; i < a.gathered; i += 32) most = max(most, __ldcg(a.largest + i));
+  most = __reduce_max_sync(0xffffffffu, most);
+  const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+  const int e = v > 0.0f ? kGradExponent - ilogbf(v) : 0;
+  if (leave && lane == 0) {
+    a.scale[0] = ldexpf(1.0f, e);
+    a.scale[1] = ldexpf(1.0f, -e);
+  }
+  return ldexpf(1.0f, e);
+}
+
 // A tile of a product: block mb of M, and N's columns (rows row0.. of the sorted
 // matrices, n with the filling and `valid` without; gradients of the weights:
 // column block nb, and rows row0.. are the k axis).
@@ -558,9 +572,9 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
     uint8_t* buf = sC + (warp - 2) * 4096;
     const int fmt = args.bf16 ? OUT_BF16 : OUT_F16;
     const bool pairs = (args.F & 1) == 0;
-    const float scale = MODE == EXPERT_DH && args.scale    ? __ldcg(args.scale)
-                        : MODE == EXPERT_DIN && args.scale ? __ldcg(args.scale + 1)
-                                                           : 1.0f;
+    float scale = 1.0f;
+    if (MODE == EXPERT_DH && args.largest) scale = gradient_scale(args, lane, warp == 2 && blockIdx.x == 0);
+    if (MODE == EXPERT_DIN && args.scale) scale = __ldcg(args.scale + 1);
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;

@@ -42,9 +42,12 @@ int order_blocks(int64_t places);
 cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream);
 
 // out[r] (pitch ld_out, 16-byte aligned) = the row of x of sorted row r's token; the
-// filling is 0.  granule: alignment of x's rows in bytes.
+// filling is 0.  granule: alignment of x's rows in bytes.  largest (or null): the largest
+// finite |x| of each of the gather_blocks blocks' rows, as a half's bits.
+constexpr int kGatherMost = 1024;
+int gather_blocks(int64_t most_rows, int sms);
 cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const void* x, int64_t ldx, int granule, int D,
-                               void* out, int64_t ld_out, int sms, cudaStream_t stream);
+                               void* out, int64_t ld_out, unsigned int* largest, int sms, cudaStream_t stream);
 
 // out[t] = sum over t's rows of weight * y[row] (weights null: of y[row]), rounded
 // to type (0 bf16, 1 f16); a place of no such expert: NaN.  dots not null: d_weights
@@ -67,13 +70,6 @@ struct JoinArgs {
 };
 cudaError_t launch_join(const JoinArgs& a, cudaStream_t stream);
 
-// scale[0] = a power of two that brings the largest finite |g| into [2^kGradExponent,
-// 2^(kGradExponent + 1)), scale[1] = its inverse; 1 where there is none.  largest:
-// kScaleBlocks words.
-constexpr int kGradExponent = 4, kScaleBlocks = 512;
-cudaError_t launch_grad_scale(const void* g, int64_t T, int D, int64_t ld, unsigned int* largest, float* scale,
-                              cudaStream_t stream);
-
 // ------------------------------------------------------------- a few places
 // Forward for a few places on the CUDA cores; x's and the weights' rows are 16-byte
 // aligned.
@@ -95,6 +91,7 @@ struct ExpertFewArgs {
 cudaError_t launch_experts_few(const ExpertFewArgs& a, bool bf16, cudaStream_t stream);
 
 // ---------------------------------------------------------------- products
+constexpr int kGradExponent = 4;
 // M is a weight's axis, N the tokens' (the gradients of the weights: M and N the
 // weight's two axes, K the expert's rows).
 enum ExpertMode : int {
@@ -123,7 +120,12 @@ struct ExpertArgs {
   int64_t ld_dgu;
   float* dots;             // DH: m_blocks * 8 per row
   const float* weights;    // DH: of each place
-  const float* scale;      // {s, 1 / s} (fp16), or null: DH multiplies dg and du with s, DIN with 1 / s
+  // fp16, else null: DH multiplies dg and du with s, a power of two that brings the largest
+  // finite gradient (of `gathered` blocks' rows) into [2^kGradExponent, 2^(kGradExponent + 1)),
+  // and leaves {s, 1 / s}; DIN and the join divide by it
+  const unsigned int* largest;
+  int gathered;
+  float* scale;
   void* y;                 // DOWN, DX: fp32, or (bf16) halves with an exponent for each 32 columns (JoinArgs)
   int64_t ldy;             // a multiple of 64
   uint8_t* y_exponent;     // row's pitch ldy / 32

@@ -1,6 +1,5 @@
 // What runs between the experts' products: places sorted by expert, rows gathered
-// in that order and joined back into tokens, and the scale of fp16 gradients
-// (experts_internal.h).
+// in that order and joined back into tokens (experts_internal.h).
 //
 // The sort counts: every warp takes neighbouring places, counts them by expert,
 // and after the counts are summed up places them in their order, so the
@@ -290,11 +289,20 @@ __device__ __forceinline__ uint4 load_word(const uint16_t* src, int d, int D) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The larger of `most` and a word's finite halves without their signs, two at a time.
+__device__ __forceinline__ uint32_t larger_halves(uint32_t most, uint32_t w) {
+  const uint32_t lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
+  return max(most, max(lo < 0x7C00u ? lo : 0u, hi < 0x7C00u ? hi : 0u));
+}
+
+// largest (or null): of the block's rows, as a half's bits.
 template <int G>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const int* head, const int* token, const int* place,
                                                                 const uint16_t* x, int64_t ldx, int D, uint16_t* out,
-                                                                int64_t ld_out) {
+                                                                int64_t ld_out, unsigned int* largest) {
   constexpr int kFlight = G == 16 ? 8 : 2;
+  __shared__ unsigned int shared[kGatherThreads / 32];
+  uint32_t most = 0u;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int rows = __ldcg(head + 1), lane = threadIdx.x & 31;
@@ -314,7 +322,20 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const int* head,
 #pragma unroll
       for (int i = 0; i < kFlight; ++i)  // D is filled up to the pitch, a multiple of 8
         if (d0 + i * 256 < D) *reinterpret_cast<uint4*>(dst + d0 + i * 256) = v[i];
+      if (largest) {
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i)
+          most = larger_halves(larger_halves(larger_halves(larger_halves(most, v[i].x), v[i].y), v[i].z), v[i].w);
+      }
     }
+  }
+  if (!largest) return;
+  most = __reduce_max_sync(kAll, most);
+  if (lane == 0) shared[threadIdx.x >> 5] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kGatherThreads / 32; ++w) most = max(most, shared[w]);
+    largest[blockIdx.x] = most;
   }
 }
 
@@ -422,44 +443,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   }
 }
 
-// ------------------------------------------------------ scale of fp16 gradients
-constexpr int kScaleThreads = 256;
-
-// The largest finite |g| of a block's rows, as a half's bits.
-__global__ void __launch_bounds__(kScaleThreads) largest_kernel(const uint16_t* g, int64_t T, int D, int64_t ld,
-                                                                unsigned int* largest) {
-  __shared__ unsigned int shared[kScaleThreads / 32];
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  unsigned int most = 0u;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x)
-#pragma unroll 4
-    for (int d = threadIdx.x; d < D; d += kScaleThreads) {
-      const unsigned int v = __ldg(g + t * ld + d) & 0x7FFFu;
-      most = v < 0x7C00u && v > most ? v : most;
-    }
-  most = __reduce_max_sync(kAll, most);
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = most;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kScaleThreads / 32; ++w) most = max(most, shared[w]);
-    largest[blockIdx.x] = most;
-  }
-}
-
-__global__ void __launch_bounds__(32) scale_of_kernel(const unsigned int* largest, int blocks, float* scale) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  unsigned int most = 0u;
-  for (int i = threadIdx.x; i < blocks; i += 32) most = max(most, __ldcg(largest + i));
-  most = __reduce_max_sync(kAll, most);
-  if (threadIdx.x != 0) return;
-  const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
-  const int e = v > 0.0f ? kGradExponent - ilogbf(v) : 0;
-  scale[0] = ldexpf(1.0f, e);
-  scale[1] = ldexpf(1.0f, -e);
-}
-
 template <typename... Params, typename... Args>
 cudaError_t launch_next(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                         const Args&... args) {
@@ -500,14 +483,18 @@ cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream) {
   return e;
 }
 
-cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const void* x, int64_t ldx, int granule, int D,
-                               void* out, int64_t ld_out, int sms, cudaStream_t stream) {
+int gather_blocks(int64_t most_rows, int sms) {
   constexpr int kWarps = kGatherThreads / 32;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((most_rows + kWarps - 1) / kWarps, 4 * std::max(1, sms))), 1, 1);
+  return static_cast<int>(std::min<int64_t>({(most_rows + kWarps - 1) / kWarps, 4 * std::max(1, sms), kGatherMost}));
+}
+
+cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const void* x, int64_t ldx, int granule, int D,
+                               void* out, int64_t ld_out, unsigned int* largest, int sms, cudaStream_t stream) {
   const auto kernel = granule == 16 ? gather_kernel<16> : granule >= 4 ? gather_kernel<4> : gather_kernel<2>;
-  return launch_next(kernel, grid, kGatherThreads, 0, stream, static_cast<const int*>(rows.head),
-                     static_cast<const int*>(rows.token), static_cast<const int*>(rows.place),
-                     static_cast<const uint16_t*>(x), ldx, D, static_cast<uint16_t*>(out), ld_out);
+  return launch_next(kernel, dim3(gather_blocks(most_rows, sms)), kGatherThreads, 0, stream,
+                     static_cast<const int*>(rows.head), static_cast<const int*>(rows.token),
+                     static_cast<const int*>(rows.place), static_cast<const uint16_t*>(x), ldx, D,
+                     static_cast<uint16_t*>(out), ld_out, largest);
 }
 
 cudaError_t launch_join(const JoinArgs& j, cudaStream_t stream) {
@@ -531,15 +518,6 @@ cudaError_t launch_join(const JoinArgs& j, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(j.T), across, 1);
   return j.type == 0 ? launch_next(join_kernel<true>, grid, kJoinThreads, 0, stream, a)
                      : launch_next(join_kernel<false>, grid, kJoinThreads, 0, stream, a);
-}
-
-cudaError_t launch_grad_scale(const void* g, int64_t T, int D, int64_t ld, unsigned int* largest, float* scale,
-                              cudaStream_t stream) {
-  const int blocks = static_cast<int>(T < kScaleBlocks ? T : kScaleBlocks);
-  cudaError_t e = launch_next(largest_kernel, dim3(blocks), kScaleThreads, 0, stream, static_cast<const uint16_t*>(g), T,
-                              D, ld, largest);
-  if (e == cudaSuccess) e = launch_next(scale_of_kernel, dim3(1), 32, 0, stream, largest, blocks, scale);
-  return e;
 }
 
 }  // namespace tgemm

@@ -132,6 +132,15 @@ def _plain(scoring, renormalize, scale, groups=1, top_groups=1, group_score="max
             index(top_groups), _choice("group_score", group_score, ("max", "top2")))
 
 
+_plain_once = functools.lru_cache(maxsize=256)(_plain)
+
+
+def _read(scoring, renormalize, scale, groups=1, top_groups=1, group_score="max"):
+    """``_plain``, kept for options that are plain values themselves (a tensor is read at every call)."""
+    kept = type(scale) is float and type(groups) is type(top_groups) is int and type(renormalize) is bool
+    return (_plain_once if kept else _plain)(scoring, renormalize, scale, groups, top_groups, group_score)
+
+
 def _logits(logits):
     """(torch, device, T, E, dtype code, row pitch)"""
     import torch
@@ -216,7 +225,7 @@ def route_experts(logits, top_k, *, scoring="softmax", bias=None, groups=1, top_
 
     If logits requires a gradient, so do the weights; the picks have none.
     """
-    options = _plain(scoring, renormalize, scale, groups, top_groups, group_score)
+    options = _read(scoring, renormalize, scale, groups, top_groups, group_score)
     if logits.requires_grad or (bias is not None and bias.requires_grad):
         import torch
         if torch.is_grad_enabled() and bias is not None and bias.requires_grad:
@@ -232,7 +241,7 @@ def route_experts_backward(logits, ids, grad_weights, *, scoring="softmax", reno
     """The gradient of ``sum(grad_weights * weights)`` with respect to
     ``logits``, [T, E] in its type, for ``ids`` and the options of the forward
     call.  It is outside torch's graph."""
-    options = _plain(scoring, renormalize, scale)
+    options = _read(scoring, renormalize, scale)
     torch, device, T, E, code, ld = _logits(logits)
     if ids.dim() != 2:
         raise ValueError("ids must be a matrix [T, top_k]")
