@@ -344,6 +344,7 @@ class Experts {
         TGEMM_TRY(gather(c_.x, c_.ldx, rows));
         TGEMM_TRY(token_maps(m, rows, c_.D, l_.ldx));
       }
+      TGEMM_TRY(map_rows(&m.c, a.h, c_.F, a.ldh, 16));
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 128));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
       a.chunk = c_.saved ? kExactChunk : kChunk;
@@ -353,6 +354,7 @@ class Experts {
       ExpertArgs a = a_;
       TGEMM_TRY(host_map_3d(&m.a, type_, w_out_.p, c_.F, c_.D, c_.E, w_out_.ld * 2, c_.D * w_out_.ld * 2, kTileK, kTileM));
       TGEMM_TRY(token_maps(m, a.h, c_.F, a.ldh));
+      TGEMM_TRY(map_joined(m, a));
       a.m_blocks = static_cast<int>(ceil_div(c_.D, 256));
       a.k_blocks = static_cast<int>(ceil_div(c_.F, kTileK));
       a.chunk = kChunk;
@@ -378,6 +380,7 @@ class Experts {
       ExpertArgs a = a_;
       TGEMM_TRY(map_transposed(m, a, w_out_, c_.F, c_.D));
       TGEMM_TRY(token_maps(m, ws_ + l_.x, c_.D, l_.ldx));
+      m.c = m.b;
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 256));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
       a.chunk = kExactChunk;
@@ -400,6 +403,7 @@ class Experts {
       ExpertArgs a = a_;
       TGEMM_TRY(map_transposed(m, a, w_in_, c_.D, 2 * c_.F));
       TGEMM_TRY(token_maps(m, a.dgu, 2 * c_.F, a.ld_dgu));
+      TGEMM_TRY(map_joined(m, a));
       a.m_blocks = static_cast<int>(ceil_div(c_.D, 256));
       a.k_blocks = static_cast<int>(ceil_div(2 * c_.F, kTileK));
       a.chunk = kChunk;
@@ -482,6 +486,11 @@ class Experts {
   // blocks of 64; what lies past cols is in rows of M or columns of N that are not stored).
   int map_rows(CUtensorMap* m, const void* p, int64_t cols, int64_t ld, uint32_t box_rows) {
     return host_map_3d(m, type_, p, cols, rows_max_, 1, ld * 2, 0, 64, box_rows);
+  }
+  // Where DOWN and DX store: halves (type 1) for bf16; fp16's fp32 rows are stored by the threads.
+  int map_joined(ExpertMaps& m, const ExpertArgs& a) {
+    m.c = m.b;
+    return type_ == 0 ? host_map_3d(&m.c, 1, a.y, c_.D, rows_max_, 1, a.ldy * 2, 0, 64, 16) : TGEMM_OK;
   }
   int map_blocks(CUtensorMap* m, const void* p, int64_t cols, int64_t ld) {
     return host_map_3d(m, type_, p, 64, rows_max_, ceil_div(cols, 64), ld * 2, 128, 64, kTileK, 2);

@@ -46,12 +46,17 @@ namespace {
 constexpr bool weight_gradient(int mode) { return mode == EXPERT_DIN || mode == EXPERT_DOUT; }
 // PARTS: epilogue warps per quarter of the lanes.
 constexpr int expert_threads(int parts) { return 32 * (2 + 4 * parts); }
-constexpr int expert_epi_bytes(int mode) { return weight_gradient(mode) ? 8 * 4096 : 0; }
-constexpr int expert_stages(int mode) {
-  return (kSmemLimit - 1024 - expert_epi_bytes(mode) - kBarrierBytes) / kStage;
+// 16-bit results on their way out: 4 KB a warp (weights' gradients), or three blocks of 16
+// rows and a CTA's 64 (UP) or 128 features for each part.
+constexpr int staged_bytes(int mode) { return mode == EXPERT_UP ? 2048 : 4096; }
+constexpr int expert_epi_bytes(int mode, int parts) {
+  return weight_gradient(mode) ? 4 * parts * 4096 : mode == EXPERT_DH ? 0 : 3 * parts * staged_bytes(mode);
 }
-constexpr int expert_smem(int mode) {
-  return 1024 + expert_stages(mode) * kStage + expert_epi_bytes(mode) + kBarrierBytes;
+constexpr int expert_stages(int mode, int parts) {
+  return (kSmemLimit - 1024 - expert_epi_bytes(mode, parts) - kBarrierBytes) / kStage;
+}
+constexpr int expert_smem(int mode, int parts) {
+  return 1024 + expert_stages(mode, parts) * kStage + expert_epi_bytes(mode, parts) + kBarrierBytes;
 }
 constexpr bool expert_a_m_major(int mode) { return mode >= EXPERT_DH; }
 constexpr bool expert_b_n_major(int mode) { return weight_gradient(mode); }
@@ -184,15 +189,65 @@ struct RowStore {
   }
 };
 
+// The same by way of shared memory: the four warps of a part (the quarters of the lanes)
+// put 16 rows of their CTA's features together, 128-byte-swizzled blocks of 64, and one
+// of them stores these by bulk copies.  Stores of 64 bytes a row by the threads themselves
+// share the SM's port with the operands' loads, piece by piece, and cost DOWN a fifth of
+// its time.  Three buffers in turn: the copy out of one has been read when the barrier of
+// the block after next's predecessor is passed.
+struct StagedRows {
+  uint8_t* buffers;
+  int bytes, next, part, quarter;
+
+  // Where the lane's 64 features of the block at hand lie.  feature: the lane's, in the CTA.
+  __device__ __forceinline__ uint8_t* block(int feature) const { return buffers + next * bytes + feature / 64 * 2048; }
+  // word: {row, row + 1} of the lane's feature, row even
+  static __device__ __forceinline__ void put(uint8_t* block, uint32_t word, int row, int feature, int lane) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 1);
+    const bool odd = (lane & 1) != 0;
+    const uint32_t both = odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+    *reinterpret_cast<uint32_t*>(block + sw128_offset(row + (odd ? 1 : 0), (feature & 62) * 2)) = both;
+  }
+  // The block's words are there: one warp stores `columns` of them from column x on.
+  __device__ __forceinline__ void store(const CUtensorMap* map, int x, int columns, int row, int lane) {
+    ptx::fence_proxy_async_smem();
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+    if (quarter == 0 && lane == 0) {
+      const uint32_t src = ptx::smem_u32(buffers + next * bytes);
+      if (columns > 0) ptx::tma_store_3d(map, x, row, 0, src);
+      if (columns > 64) ptx::tma_store_3d(map, x + 64, row, 0, src + 2048);
+      ptx::bulk_commit_group();
+      ptx::bulk_wait_group_read<1>();
+    }
+    if (++next == 3) next = 0;
+  }
+};
+// Whether all four warps of a part go on (a wait that ran out in one of them ends them all:
+// none waits for another at a barrier).
+__device__ __forceinline__ bool part_agrees(bool ok, int part) {
+  uint32_t all;
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "setp.ne.u32 q, %1, 0;\n"
+      "bar.red.and.pred p, %2, 128, q;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "r"(1 + part)
+      : "memory");
+  return all != 0;
+}
+
 // 16 columns of UP: gates in lanes 0..15, ups in lanes 16..31 -> h, and g and u.
 // `row`: the columns' first row, of which `valid` are no filling (which gets 0).
 // g and u lie as {g, u} x features x 4 rows for every four rows: 16 bytes a lane.
-template <bool PAIRS>
+// staged: the lane's feature in the CTA is `own`.
 __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertArgs& a, int feature, int64_t row,
-                                          int valid, int fmt, int lane) {
+                                          int valid, int fmt, int lane, int own, const StagedRows& staged) {
   const bool low = lane < 16;
   const int c0 = low ? 0 : 8;
-  RowStore<PAIRS> h(a.h, row + c0, a.ldh, feature, a.F, lane);
+  uint8_t* h = staged.block(own);
   float g[8], u[8], x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -206,7 +261,7 @@ __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertA
     for (int i = 0; i < 8; ++i) x[i] = c0 + i < valid ? x[i] : 0.0f;
   }
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) h.put(pack_pair(x[i], x[i + 1], fmt));
+  for (int i = 0; i < 8; i += 2) StagedRows::put(h, pack_pair(x[i], x[i + 1], fmt), c0 + i, own, lane);
   if (a.gu && feature < a.F) {
     float4* gu = reinterpret_cast<float4*>(a.gu) + (row + c0) / 4 * 2 * a.ldg + feature;
 #pragma unroll
@@ -301,8 +356,9 @@ __device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertAr
 // average (values below 2^-28 of the largest by more), which beside h's rounding and the
 // result's (1.65e-3 each) is 0.2 % of the error; y's bytes, written here and read by the
 // join, are what DOWN's epilogue costs (8192 tokens, 64 experts, fp32: join 94 us, 53 so).
-__device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int lane) {
-  RowStore<true> y(a.y, row, a.ldy, d, static_cast<int>(a.ldy), lane);
+__device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int lane,
+                                              int own, const StagedRows& staged) {
+  uint8_t* y = staged.block(own);
   uint32_t most[16], all = 0u;
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
@@ -326,7 +382,7 @@ __device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const Exp
       exponents[(c + e) / 4] |= exponent << (8 * ((c + e) & 3));
       f[e] = __uint_as_float((268u - exponent) << 23) * __uint_as_float(v[c + e]);
     }
-    y.put(pack_pair(f[0], f[1], OUT_F16));
+    StagedRows::put(y, pack_pair(f[0], f[1], OUT_F16), c, own, lane);
   }
   if (lane < 16 && d - lane < a.ldy) {
     const uint32_t word = lane < 8 ? (lane < 4 ? exponents[0] : exponents[1]) : (lane < 12 ? exponents[2] : exponents[3]);
@@ -371,17 +427,17 @@ template <int MODE, int PARTS, bool GATHER>
 __global__ void __launch_bounds__(expert_threads(PARTS), 1)
     expert_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs args) {
   const CUtensorMap &mapA = maps.a, &mapB = maps.b, &mapC = maps.c;
-  constexpr int STAGES = expert_stages(MODE);
+  constexpr int STAGES = expert_stages(MODE, PARTS);
   constexpr bool GRADIENT = weight_gradient(MODE);
   static_assert(!GRADIENT || PARTS == 2, "staging of stores");
   constexpr int ACC = 256;
   constexpr uint32_t TMEM_COLS = 512;
-  static_assert(expert_smem(MODE) <= kSmemLimit, "shared memory per CTA");
+  static_assert(expert_smem(MODE, PARTS) <= kSmemLimit, "shared memory per CTA");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sC = smem + STAGES * kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sC + expert_epi_bytes(MODE));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sC + expert_epi_bytes(MODE, PARTS));
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint64_t* acc_empty = acc_full + 2;
@@ -416,7 +472,7 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
       ptx::tma_prefetch_desc(&maps.b32);
       ptx::tma_prefetch_desc(&maps.b16);
     }
-    if (GRADIENT) ptx::tma_prefetch_desc(&mapC);
+    if (MODE != EXPERT_DH) ptx::tma_prefetch_desc(&mapC);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), TMEM_COLS);
@@ -435,8 +491,13 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
 
   if (warp == 0) {
     // ------------------------------------------------ bulk-tensor producer
+    // As few instructions a stage as it takes: they queue behind the epilogues', and
+    // with n = 256 a stage's MMAs last 512 cycles.  Lane 0 copies the weight, lanes 1..
+    // the tokens' boxes.
+    const uint32_t full0 = ptx::smem_u32(&full[0]), empty0 = ptx::smem_u32(&empty[0]);
+    const uint32_t full0_leader = ptx::mapa_shared(full0, 0), ring = ptx::smem_u32(smem);
     int stage = 0;
-    uint32_t phase = 0, filled = 0, last_parity = 0;
+    uint32_t phase = 0, issued = 0;
     bool ok = true;
     ExpertUnit next = units.get(args, worker);
     for (int i = worker; ok && i < units.count; i += workers) {
@@ -444,66 +505,64 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
       next = units.get(args, i + workers);
       const int stages = units.stages(args, u);
       const int half = GRADIENT ? kTileM : u.n / 2;  // this CTA's columns
+      const uint32_t bytes = 2u * (kSub + static_cast<uint32_t>(half) * 128u);
       // a CTA's columns in as few boxes as add up to them (each costs the copy engine
-      // some 20 cycles beside its bytes): lane l's box
-      const int wide = half / 64;
+      // some 20 cycles beside its bytes): lane 1 + b's box
+      const int wide = half / 64, b = lane - 1;
       const bool mid = (half & 32) != 0, small = (half & 16) != 0;
-      const int boxes = wide + (mid ? 1 : 0) + (small ? 1 : 0);
-      const CUtensorMap* box = lane < wide ? &mapB : lane == wide && mid ? &maps.b32 : &maps.b16;
-      const int box0 = lane < wide ? 64 * lane : lane == wide ? 64 * wide : 64 * wide + 32;
+      const bool copies_b = GRADIENT ? lane == 1 : GATHER ? 4 * lane < half : lane >= 1 && b < wide + (mid ? 1 : 0) + (small ? 1 : 0);
+      const CUtensorMap* box = GRADIENT || b < wide ? &mapB : b == wide && mid ? &maps.b32 : &maps.b16;
+      const int box0 = GRADIENT ? 0 : b < wide ? 64 * b : b == wide ? 64 * wide : 64 * wide + 32;
+      const int m0 = u.mb * 256 + cta * kTileM;  // 128 of the 256 of M
+      const int f0 = u.mb * kTileM + cta * 64;   // UP: 64 features
+      const int row = u.row0 + cta * half + box0;
       int4 rows = make_int4(0, 0, 0, 0);
-      if (GATHER && 4 * lane < half)
+      if (GATHER && copies_b)
         rows = __ldcg(reinterpret_cast<const int4*>(args.rows.token + u.row0 + cta * half + 4 * lane));
-      for (int it = 0; it < stages; ++it) {
-        if (!warp_wait(ptx::smem_u32(&empty[stage]), phase ^ 1u, ctl, SITE_PRODUCER_EMPTY)) {
-          ok = false;
-          break;
-        }
-        const uint32_t fb_local = ptx::smem_u32(&full[stage]);
-        const uint32_t fb = ptx::mapa_shared(fb_local, 0);
-        if (leader && lane == 0) ptx::mbar_arrive_expect_tx(fb_local, 2u * (kSub + static_cast<uint32_t>(half) * 128u));
-        __syncwarp();
-        const uint32_t sa = ptx::smem_u32(smem + stage * kStage), sb = sa + kSub;
-        const int k0 = it * kTileK;  // past the k axis: zeros (gradients: other rows, which no MMA reads)
-        // 128 of the 256 of M
-        const int m0 = u.mb * 256 + cta * kTileM;
-        if constexpr (MODE == EXPERT_UP) {
-          const int f0 = u.mb * kTileM + cta * 64;
-          if (!args.split) {
-            if (lane == 0) ptx::tma_load_5d_pair(sa, &mapA, k0, 0, 0, f0 / 16, u.expert, fb);
-          } else if (lane < 4) {
-            ptx::tma_load_3d_pair(sa + lane * 4096, &mapA, k0, f0 + lane * 16, 2 * u.expert, fb);
+      int k0 = 0;  // past the k axis: zeros (gradients: other rows, which no MMA reads)
+      for (int it = 0; it < stages; ++it, k0 += kTileK) {
+        ok = wait_bounded(empty0 + 8 * stage, phase ^ 1u, ctl, SITE_PRODUCER_EMPTY);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t fb = full0_leader + 8 * stage, sa = ring + stage * kStage, sb = sa + kSub;
+        if (lane == 0) {
+          if (leader) ptx::mbar_arrive_expect_tx(full0 + 8 * stage, bytes);
+          if constexpr (MODE == EXPERT_UP) {
+            if (!args.split)
+              ptx::tma_load_5d_pair(sa, &mapA, k0, 0, 0, f0 / 16, u.expert, fb);
+            else
+              for (int q = 0; q < 4; ++q) ptx::tma_load_3d_pair(sa + q * 4096, &mapA, k0, f0 + q * 16, 2 * u.expert, fb);
+          } else if constexpr (MODE == EXPERT_DOWN) {
+            ptx::tma_load_3d_pair(sa, &mapA, k0, m0, u.expert, fb);
+          } else if constexpr (GRADIENT) {
+            ptx::tma_load_3d_pair(sa, &mapA, 0, u.row0 + k0, m0 / 64, fb);
+          } else if (!args.split) {
+            ptx::tma_load_4d_pair(sa, &mapA, 0, k0, m0 / 64, u.expert, fb);
+          } else {
+            for (int q = 0; q < 2; ++q) ptx::tma_load_3d_pair(sa + q * 8192, &mapA, m0 + q * 64, k0, u.expert, fb);
           }
-        } else if constexpr (MODE == EXPERT_DOWN) {
-          if (lane == 0) ptx::tma_load_3d_pair(sa, &mapA, k0, m0, u.expert, fb);
-        } else if constexpr (GRADIENT) {
-          if (lane == 0) ptx::tma_load_3d_pair(sa, &mapA, 0, u.row0 + k0, m0 / 64, fb);
-        } else if (!args.split) {
-          if (lane == 0) ptx::tma_load_4d_pair(sa, &mapA, 0, k0, m0 / 64, u.expert, fb);
-        } else if (lane < 2) {
-          ptx::tma_load_3d_pair(sa + lane * 8192, &mapA, m0 + lane * 64, k0, u.expert, fb);
         }
-        // half of N
-        if constexpr (GRADIENT) {
-          if (lane == 1) ptx::tma_load_3d_pair(sb, &mapB, 0, u.row0 + k0, u.nb * 4 + cta * 2, fb);
-        } else if constexpr (GATHER) {
-          if (4 * lane < half) tma_gather4_pair(sb + lane * 512, &mapB, k0, rows, fb);
-        } else {
-          if (lane < boxes) ptx::tma_load_3d_pair(sb + box0 * 128, box, k0, u.row0 + cta * half + box0, 0, fb);
+        if (copies_b) {
+          if constexpr (GRADIENT)
+            ptx::tma_load_3d_pair(sb, &mapB, 0, u.row0 + k0, u.nb * 4 + cta * 2, fb);
+          else if constexpr (GATHER)
+            tma_gather4_pair(sb + lane * 512, &mapB, k0, rows, fb);
+          else
+            ptx::tma_load_3d_pair(sb + box0 * 128, box, k0, row, 0, fb);
         }
-        filled |= 1u << stage;
-        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+        ++issued;
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
+    __syncwarp();
     // loads in flight land before shared memory is released (see tc_gemm_2sm.cu)
     if (lane == 0) {
-      for (int s = 0; s < STAGES; ++s)
-        if ((filled >> s) & 1u) {
-          const uint32_t par = (last_parity >> s) & 1u;
+      for (uint32_t s = 0; s < STAGES; ++s)
+        if (issued > s) {
+          const uint32_t par = (issued - s - 1) / STAGES & 1u;  // of the stage's last use
           wait_teardown(ptx::smem_u32(leader ? &full[s] : &empty[s]), par, ctl, SITE_TEARDOWN);
         }
     }
@@ -515,6 +574,11 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
       const uint32_t fixed = (1u << 4) | (ab << 7) | (ab << 10) | (expert_a_m_major(MODE) ? 1u << 15 : 0u) |
                              (expert_b_n_major(MODE) ? 1u << 16 : 0u) |
                              (static_cast<uint32_t>((2 * kTileM) >> 4) << 24);
+      // the first stage's operands; a stage and a step of 16 are constants further
+      const uint64_t a_desc = expert_a_m_major(MODE) ? sw128_desc(ptx::smem_u32(smem), 8192, 1024)
+                                                     : sw128_desc(ptx::smem_u32(smem), 16, 1024);
+      const uint64_t b_desc = expert_b_n_major(MODE) ? sw128_desc(ptx::smem_u32(smem) + kSub, 8192, 1024)
+                                                     : sw128_desc(ptx::smem_u32(smem) + kSub, 16, 1024);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -538,17 +602,16 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
               break;
             }
             ptx::tc_fence_after_sync();
-            const uint32_t a0 = ptx::smem_u32(smem + stage * kStage), b0 = a0 + kSub;
+            const uint64_t da = a_desc + static_cast<uint64_t>(stage * (kStage >> 4));
+            const uint64_t db = b_desc + static_cast<uint64_t>(stage * (kStage >> 4));
             // steps of 16: the expert's rows end at one, what follows is another's
             const int steps = GRADIENT ? min(kTileK / 16, (u.n - it * kTileK) / 16) : kTileK / 16;
 #pragma unroll
-            for (int k = 0; k < kTileK / 16; ++k) {
-              const uint64_t da = expert_a_m_major(MODE) ? sw128_desc(a0 + k * 2048, 8192, 1024)
-                                                         : sw128_desc(a0 + k * 32, 16, 1024);
-              const uint64_t db = expert_b_n_major(MODE) ? sw128_desc(b0 + k * 2048, 8192, 1024)
-                                                         : sw128_desc(b0 + k * 32, 16, 1024);
-              if (!GRADIENT || k < steps) ptx::tc_mma_f16_pair(d_tmem, da, db, idesc, (it != lo || k != 0) ? 1u : 0u);
-            }
+            for (int k = 0; k < kTileK / 16; ++k)
+              if (!GRADIENT || k < steps)
+                ptx::tc_mma_f16_pair(d_tmem, da + k * ((expert_a_m_major(MODE) ? 2048 : 32) >> 4),
+                                     db + k * ((expert_b_n_major(MODE) ? 2048 : 32) >> 4), idesc,
+                                     (it != lo || k != 0) ? 1u : 0u);
             ptx::tc_commit_pair_multicast(ptx::smem_u32(&empty[stage]), 0x3);
             if (++stage == STAGES) {
               stage = 0;
@@ -570,6 +633,10 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
     const int quarter = warp & 3;          // tensor-memory lanes of this warp
     const int part = (warp - 2) / 4;       // its share of the columns
     uint8_t* buf = sC + (warp - 2) * 4096;
+    constexpr bool STAGED = !GRADIENT && MODE != EXPERT_DH;
+    StagedRows staged = {};
+    if constexpr (STAGED)
+      staged = StagedRows{sC + part * 3 * staged_bytes(MODE), staged_bytes(MODE), 0, part, quarter};
     const int fmt = args.bf16 ? OUT_BF16 : OUT_F16;
     const bool pairs = (args.F & 1) == 0;
     float scale = 1.0f;
@@ -627,8 +694,9 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
             given_back();
           }
         }
-        if (!ok) break;
       }
+      if constexpr (STAGED) ok = part_agrees(ok, part);
+      if (!ok) break;
       next = units.get(args, i + workers);  // under this epilogue; no register is its beside the sums
       if constexpr (GRADIENT) {
         const int M = MODE == EXPERT_DIN ? 2 * args.F : args.D, N = MODE == EXPERT_DIN ? args.D : args.F;
@@ -670,21 +738,22 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
             uint32_t v[16];
             ptx::tmem_ld_32x32b_x16(tcol + b * PARTS * 16, v);
             ptx::tmem_wait_ld();
+            const int x0 = MODE == EXPERT_UP ? u.mb * kTileM + cta * 64 : u.mb * 256 + cta * kTileM;  // the CTA's first
             if constexpr (MODE == EXPERT_UP) {
-              if (pairs)
-                finish_up<true>(v, args, m0, u.row0 + c0, valid, fmt, lane);
-              else
-                finish_up<false>(v, args, m0, u.row0 + c0, valid, fmt, lane);
-            } else if (args.bf16)
-              finish_y_half(v, args, m0, u.row0 + c0, lane);
-            else
+              finish_up(v, args, m0, u.row0 + c0, valid, fmt, lane, m0 - x0, staged);
+              staged.store(&mapC, x0, min(64, args.F - x0), u.row0 + c0, lane);
+            } else if (args.bf16) {
+              finish_y_half(v, args, m0, u.row0 + c0, lane, m0 - x0, staged);
+              staged.store(&mapC, x0, args.D - x0, u.row0 + c0, lane);
+            } else {
               finish_y(v, args, m0, u.row0 + c0, valid);
+            }
           }
         }
         given_back();
       }
     }
-    if (GRADIENT && lane == 0) ptx::bulk_wait_group_read<0>();
+    if ((GRADIENT || STAGED) && lane == 0) ptx::bulk_wait_group_read<0>();
     __syncwarp();
   }
 
@@ -700,7 +769,7 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
 template <int MODE, int PARTS, bool GATHER = false>
 cudaError_t launch_expert(const ExpertMaps& maps, const ExpertArgs& args, int pairs, cudaStream_t stream) {
   static std::atomic<uint64_t> done_mask{0};
-  return launch_pairs(expert_kernel<MODE, PARTS, GATHER>, expert_smem(MODE), expert_threads(PARTS), done_mask, pairs,
+  return launch_pairs(expert_kernel<MODE, PARTS, GATHER>, expert_smem(MODE, PARTS), expert_threads(PARTS), done_mask, pairs,
                       stream, maps, args);
 }
 

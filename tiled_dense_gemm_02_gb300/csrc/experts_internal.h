@@ -136,8 +136,8 @@ struct ExpertArgs {
   unsigned int* status;
 };
 
-// Operands A and B (token products: boxes of 64, 32 and 16 rows), and where DIN and
-// DOUT store.  Axes of a, from the innermost: UP {k, feature % 16, gate or up, feature /
+// Operands A and B (token products: boxes of 64, 32 and 16 rows), and where all but DH
+// store.  Axes of a, from the innermost: UP {k, feature % 16, gate or up, feature /
 // 16, expert}, or where args.split {k, feature, 2 expert + (gate or up)}; DOWN {k, row,
 // expert}; DH and DX {column % 64, row, column / 64, expert}, or where args.split {column,
 // row, expert}.  DIN's and DOUT's a and b: {column % 64, row, column / 64}.
