@@ -46,11 +46,12 @@ namespace {
 constexpr bool weight_gradient(int mode) { return mode == EXPERT_DIN || mode == EXPERT_DOUT; }
 // PARTS: epilogue warps per quarter of the lanes.
 constexpr int expert_threads(int parts) { return 32 * (2 + 4 * parts); }
-// 16-bit results on their way out: 4 KB a warp (weights' gradients), or three blocks of 16
-// rows and a CTA's 64 (UP) or 128 features for each part.
-constexpr int staged_bytes(int mode) { return mode == EXPERT_UP ? 2048 : 4096; }
+// 16-bit results on their way out: 4 KB a warp (weights' gradients), or for each part three
+// buffers of 16 rows and the CTA's 64 features (UP), or two of 32 rows and its 128.
+constexpr int staged_bytes(int mode) { return mode == EXPERT_UP ? 2048 : 8192; }
+constexpr int staged_buffers(int mode) { return mode == EXPERT_UP ? 3 : 2; }
 constexpr int expert_epi_bytes(int mode, int parts) {
-  return weight_gradient(mode) ? 4 * parts * 4096 : mode == EXPERT_DH ? 0 : 3 * parts * staged_bytes(mode);
+  return weight_gradient(mode) ? 4 * parts * 4096 : mode == EXPERT_DH ? 0 : staged_buffers(mode) * parts * staged_bytes(mode);
 }
 constexpr int expert_stages(int mode, int parts) {
   return (kSmemLimit - 1024 - expert_epi_bytes(mode, parts) - kBarrierBytes) / kStage;
@@ -192,15 +193,26 @@ struct RowStore {
 // The same by way of shared memory: the four warps of a part (the quarters of the lanes)
 // put 16 rows of their CTA's features together, 128-byte-swizzled blocks of 64, and one
 // of them stores these by bulk copies.  Stores of 64 bytes a row by the threads themselves
-// share the SM's port with the operands' loads, piece by piece, and cost DOWN a fifth of
-// its time.  Three buffers in turn: the copy out of one has been read when the barrier of
-// the block after next's predecessor is passed.
+// share the SM's port with the operands' loads, piece by piece.
+template <int BUFFERS, int BYTES>
 struct StagedRows {
   uint8_t* buffers;
-  int bytes, next, part, quarter;
+  int next, part, quarter;
 
-  // Where the lane's 64 features of the block at hand lie.  feature: the lane's, in the CTA.
-  __device__ __forceinline__ uint8_t* block(int feature) const { return buffers + next * bytes + feature / 64 * 2048; }
+  __device__ __forceinline__ void barrier() const { asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory"); }
+  // The buffer at hand may be written.  Of three it may since the last barrier: the copy out
+  // of it was followed by one whose issuer waited for it before that barrier.
+  __device__ __forceinline__ void acquire(int lane) const {
+    if constexpr (BUFFERS == 2) {
+      if (quarter == 0 && lane == 0) ptx::bulk_wait_group_read<1>();
+      barrier();
+    }
+  }
+  // Where the lane's 64 features of the buffer's block (16 rows) lie.  feature: the lane's,
+  // in the CTA.
+  __device__ __forceinline__ uint8_t* block(int feature, int b = 0) const {
+    return buffers + next * BYTES + b * 4096 + feature / 64 * 2048;
+  }
   // word: {row, row + 1} of the lane's feature, row even
   static __device__ __forceinline__ void put(uint8_t* block, uint32_t word, int row, int feature, int lane) {
     const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 1);
@@ -208,18 +220,21 @@ struct StagedRows {
     const uint32_t both = odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
     *reinterpret_cast<uint32_t*>(block + sw128_offset(row + (odd ? 1 : 0), (feature & 62) * 2)) = both;
   }
-  // The block's words are there: one warp stores `columns` of them from column x on.
-  __device__ __forceinline__ void store(const CUtensorMap* map, int x, int columns, int row, int lane) {
+  // The buffer's words are there: one warp stores `columns` of them from column x on, to rows
+  // `row`.. and (blocks 2) `other`...
+  __device__ __forceinline__ void store(const CUtensorMap* map, int x, int columns, int row, int blocks, int other, int lane) {
     ptx::fence_proxy_async_smem();
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+    barrier();
     if (quarter == 0 && lane == 0) {
-      const uint32_t src = ptx::smem_u32(buffers + next * bytes);
-      if (columns > 0) ptx::tma_store_3d(map, x, row, 0, src);
-      if (columns > 64) ptx::tma_store_3d(map, x + 64, row, 0, src + 2048);
+      const uint32_t src = ptx::smem_u32(buffers + next * BYTES);
+      for (int b = 0; b < blocks; ++b) {
+        if (columns > 0) ptx::tma_store_3d(map, x, b ? other : row, 0, src + b * 4096);
+        if (columns > 64) ptx::tma_store_3d(map, x + 64, b ? other : row, 0, src + b * 4096 + 2048);
+      }
       ptx::bulk_commit_group();
-      ptx::bulk_wait_group_read<1>();
+      if (BUFFERS == 3) ptx::bulk_wait_group_read<1>();
     }
-    if (++next == 3) next = 0;
+    if (++next == BUFFERS) next = 0;
   }
 };
 // Whether all four warps of a part go on (a wait that ran out in one of them ends them all:
@@ -243,8 +258,9 @@ __device__ __forceinline__ bool part_agrees(bool ok, int part) {
 // `row`: the columns' first row, of which `valid` are no filling (which gets 0).
 // g and u lie as {g, u} x features x 4 rows for every four rows: 16 bytes a lane.
 // staged: the lane's feature in the CTA is `own`.
+template <typename Staged>
 __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertArgs& a, int feature, int64_t row,
-                                          int valid, int fmt, int lane, int own, const StagedRows& staged) {
+                                          int valid, int fmt, int lane, int own, const Staged& staged) {
   const bool low = lane < 16;
   const int c0 = low ? 0 : 8;
   uint8_t* h = staged.block(own);
@@ -261,7 +277,7 @@ __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertA
     for (int i = 0; i < 8; ++i) x[i] = c0 + i < valid ? x[i] : 0.0f;
   }
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) StagedRows::put(h, pack_pair(x[i], x[i + 1], fmt), c0 + i, own, lane);
+  for (int i = 0; i < 8; i += 2) Staged::put(h, pack_pair(x[i], x[i + 1], fmt), c0 + i, own, lane);
   if (a.gu && feature < a.F) {
     float4* gu = reinterpret_cast<float4*>(a.gu) + (row + c0) / 4 * 2 * a.ldg + feature;
 #pragma unroll
@@ -356,10 +372,9 @@ __device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertAr
 // average (values below 2^-28 of the largest by more), which beside h's rounding and the
 // result's (1.65e-3 each) is 0.2 % of the error; y's bytes, written here and read by the
 // join, are what DOWN's epilogue costs (8192 tokens, 64 experts, fp32: join 94 us, 53 so).
-__device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int lane,
-                                              int own, const StagedRows& staged) {
-  uint8_t* y = staged.block(own);
-  uint32_t most[16], all = 0u;
+// y: the block's words in shared memory; own: the lane's feature in the CTA.
+__device__ __forceinline__ void row_sizes(const uint32_t (&v)[16], uint32_t (&most)[16]) {
+  uint32_t all = 0u;
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
     most[c] = __reduce_max_sync(0xffffffffu, v[c] & 0x7FFFFFFFu);
@@ -372,6 +387,10 @@ __device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const Exp
       most[c] = __reduce_max_sync(0xffffffffu, size < 0x7F800000u ? size : 0u);
     }
   }
+}
+template <typename Staged>
+__device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const uint32_t (&most)[16], const ExpertArgs& a,
+                                              int d, int64_t row, int lane, int own, bool there, uint8_t* y) {
   uint32_t exponents[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int c = 0; c < 16; c += 2) {
@@ -382,11 +401,11 @@ __device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const Exp
       exponents[(c + e) / 4] |= exponent << (8 * ((c + e) & 3));
       f[e] = __uint_as_float((268u - exponent) << 23) * __uint_as_float(v[c + e]);
     }
-    StagedRows::put(y, pack_pair(f[0], f[1], OUT_F16), c, own, lane);
+    Staged::put(y, pack_pair(f[0], f[1], OUT_F16), c, own, lane);
   }
-  if (lane < 16 && d - lane < a.ldy) {
+  if (there && lane < 16 && d - lane < a.ldy) {
     const uint32_t word = lane < 8 ? (lane < 4 ? exponents[0] : exponents[1]) : (lane < 12 ? exponents[2] : exponents[3]);
-    a.y_exponent[(row + lane) * (a.ldy / 32) + d / 32] = static_cast<uint8_t>(word >> (8 * (lane & 3)));
+    a.y_exponent[(row / 16 * (a.ldy / 32) + d / 32) * 16 + lane] = static_cast<uint8_t>(word >> (8 * (lane & 3)));
   }
 }
 
@@ -634,9 +653,8 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
     const int part = (warp - 2) / 4;       // its share of the columns
     uint8_t* buf = sC + (warp - 2) * 4096;
     constexpr bool STAGED = !GRADIENT && MODE != EXPERT_DH;
-    StagedRows staged = {};
-    if constexpr (STAGED)
-      staged = StagedRows{sC + part * 3 * staged_bytes(MODE), staged_bytes(MODE), 0, part, quarter};
+    using Staged = StagedRows<staged_buffers(MODE), staged_bytes(MODE)>;
+    Staged staged{sC + part * staged_buffers(MODE) * staged_bytes(MODE), 0, part, quarter};
     const int fmt = args.bf16 ? OUT_BF16 : OUT_F16;
     const bool pairs = (args.F & 1) == 0;
     float scale = 1.0f;
@@ -714,8 +732,28 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
                      : 0.0f;
         };
         float ahead = MODE == EXPERT_DH ? weight_of(0) : 0.0f;
+        constexpr bool JOINED = MODE == EXPERT_DOWN || MODE == EXPERT_DX;
+        if (JOINED && args.bf16) {
+          // two blocks at a time: their chains of reductions and exchanges run side by side
+          const int x0 = u.mb * 256 + cta * kTileM;
 #pragma unroll 1
-        for (int b = 0; b < blocks; ++b) {
+          for (int b = 0; b < blocks; b += 2) {
+            const bool both = b + 1 < blocks;
+            const int row = u.row0 + (part + b * PARTS) * 16, other = row + PARTS * 16;
+            uint32_t v[16], w[16], v_most[16], w_most[16];
+            ptx::tmem_ld_32x32b_x16(tcol + b * PARTS * 16, v);
+            ptx::tmem_ld_32x32b_x16(tcol + (both ? b + 1 : b) * PARTS * 16, w);
+            ptx::tmem_wait_ld();
+            row_sizes(v, v_most);
+            row_sizes(w, w_most);
+            staged.acquire(lane);
+            finish_y_half<Staged>(v, v_most, args, m0, row, lane, m0 - x0, true, staged.block(m0 - x0));
+            finish_y_half<Staged>(w, w_most, args, m0, other, lane, m0 - x0, both, staged.block(m0 - x0, 1));
+            staged.store(&mapC, x0, args.D - x0, row, both ? 2 : 1, other, lane);
+          }
+        }
+#pragma unroll 1
+        for (int b = JOINED && args.bf16 ? blocks : 0; b < blocks; ++b) {
           const int c0 = (part + b * PARTS) * 16;
           const int valid = u.valid - c0;
           if constexpr (MODE == EXPERT_DH) {
@@ -738,13 +776,10 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
             uint32_t v[16];
             ptx::tmem_ld_32x32b_x16(tcol + b * PARTS * 16, v);
             ptx::tmem_wait_ld();
-            const int x0 = MODE == EXPERT_UP ? u.mb * kTileM + cta * 64 : u.mb * 256 + cta * kTileM;  // the CTA's first
             if constexpr (MODE == EXPERT_UP) {
+              const int x0 = u.mb * kTileM + cta * 64;  // the CTA's first feature
               finish_up(v, args, m0, u.row0 + c0, valid, fmt, lane, m0 - x0, staged);
-              staged.store(&mapC, x0, min(64, args.F - x0), u.row0 + c0, lane);
-            } else if (args.bf16) {
-              finish_y_half(v, args, m0, u.row0 + c0, lane, m0 - x0, staged);
-              staged.store(&mapC, x0, args.D - x0, u.row0 + c0, lane);
+              staged.store(&mapC, x0, min(64, args.F - x0), u.row0 + c0, 1, 0, lane);
             } else {
               finish_y(v, args, m0, u.row0 + c0, valid);
             }

@@ -128,7 +128,7 @@ struct ExpertArgs {
   float* scale;
   void* y;                 // DOWN, DX: fp32, or (bf16) halves with an exponent for each 32 columns (JoinArgs)
   int64_t ldy;             // a multiple of 64
-  uint8_t* y_exponent;     // row's pitch ldy / 32
+  uint8_t* y_exponent;     // [row / 16][column / 32][row % 16]: a warp's 16 bytes lie together
   void* out;               // DIN, DOUT
   int64_t ld_out;
   int store_granule;       // 0 bulk-tensor stores, else the granule of per-thread stores

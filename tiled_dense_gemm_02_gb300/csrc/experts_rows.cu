@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       if constexpr (BF16) {
         const uint4 v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.y) + row * a.ldy + d));
         const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t e = __ldcg(a.y_exponent + row * (a.ldy / 32) + d / 32);
+        const uint32_t e = __ldcg(a.y_exponent + (row / 16 * (a.ldy / 32) + d / 32) * 16 + row % 16);
         w *= __uint_as_float((e - 14u) << 23);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
