@@ -39,7 +39,13 @@
  *
  * x, W_in, W_out and what is computed from them are bf16 or fp16; products run on
  * the tensor cores with fp32 sums, h is rounded to the operands' type on its way
- * into the second product, and out, summed in fp32, is rounded once.  A place whose
+ * into the second product (fp16's largest number is 65504: a larger h is infinite),
+ * and out, summed in fp32, is rounded once.  bf16 rows W_out[e] h lie in the workspace as
+ * halves with a power of two for each 32 elements, 2^-12 of each at most.  The tensor cores'
+ * adder truncates: 256 steps of 16 products at a time stay within 2^-15 of the sum of
+ * magnitudes, however long the axis; where the backward call follows, 16 steps: g and u are
+ * within 2^-18.  Calls of a few places (up to 32, by their number and the weights' size) read
+ * the weights place by place on the CUDA cores, with h in fp32.  A place whose
  * id is below 0 is unused; a row without a used place gives 0 (and x may hold
  * anything there, NaN included).  An id of E or more is an error in the data: its
  * row of out is NaN, and so are its row of dx and its place of dweights; it has no
@@ -109,15 +115,14 @@ typedef struct tgemm_experts_options {
  * an aligned pitch when they are not; only the pointers' values modulo 16 are
  * looked at).  Needs no GPU.
  *
- * With r = T k rows and up to 31 more per expert that has any: 2 F + 4 D bytes a row
- * forward, 6 F + 4 D and F / 8 bytes backward, 2 D bytes a token (twice backward),
- * and the copies. */
+ * With r = T k rows and up to 31 more per expert that has any, F and D to the next 64: 2 F + 4 D
+ * bytes a row forward, 6 F + 4 D and F / 8 bytes backward (fp16 2 D more), and the copies. */
 TGEMM_API int tgemm_experts_workspace_size(int backward, int64_t T, int64_t E, int64_t k, int64_t D, int64_t F,
                const void* W_in, int64_t ld_in, const void* W_out, int64_t ld_out, int dtype, size_t* bytes);
 
-/* Bytes of what the forward call keeps for the backward call (device memory of
- * the caller's, 256-byte aligned): the order of the rows, and g and u in float32, 8 F bytes a row.
- * The backward call only reads it. */
+/* Bytes of what the forward call keeps for the backward call (device memory of the
+ * caller's, 256-byte aligned): the order of the rows, x's rows in it, and g and u in
+ * float32, 8 F + 2 D bytes a row.  The backward call only reads it. */
 TGEMM_API int tgemm_experts_saved_size(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F, int dtype,
                size_t* bytes);
 

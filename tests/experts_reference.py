@@ -4,9 +4,9 @@ elementwise bounds of the library's results.
 With p the operands' significant bits, u = 2^-p half a step of their type:
 
 * a product's sum of n terms: the tensor cores' adder truncates by less than 2^-23 of
-  the sum a step of 16 products, and sums are added in fp32 after 32 steps (g, u and v
-  = grad W_out of a training step: 2^-18 of the sum of magnitudes) or 256 steps
-  (everything else: 2^-15);
+  the sum a step of 16 products, and sums are added in fp32 after 16 steps (g, u and v
+  = grad W_out of a training step: 2^-19 of the sum of magnitudes, and as much again for
+  the additions of up to 32 such sums) or 256 steps (everything else: 2^-15);
 * h = silu(g) u inherits |silu'| <= 1.1 times g's error and u's, 2^-20 for its
   exponential, division and products, and is rounded to the type (u, or half of
   fp16's smallest step);

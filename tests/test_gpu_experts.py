@@ -177,6 +177,19 @@ def test_layouts(T, dtype):
         check(shifted[0], shifted[1], shifted[2], ids, weights, shifted[3])
 
 
+@pytest.mark.parametrize("T,E,k", [(1, 6, 2), (3, 6, 2), (90, 6, 2), (40, 64, 40), (1, 64, 40)])
+@pytest.mark.parametrize("D,F", [(97, 51), (104, 50), (101, 56), (7, 3)])
+def test_odd_sizes_in_aligned_rows_and_many_picks(T, E, k, D, F):
+    """Rows on the 16-byte grid whose last words are partly the next row's filling, which is NaN."""
+    x, w_in, w_out, ids, weights, g, _ = layer(T, E, k, D, F, BF16, seed=D)
+    nan = float("nan")
+    ld, lf = (D + 7) // 8 * 8 + 8, (F + 7) // 8 * 8 + 8
+    wide = [torch.full(s, nan, dtype=BF16, device="cuda") for s in ((T, ld), (E, 2 * F, ld), (E, D, lf), (T, ld))]
+    for a, b in zip(wide, (x, w_in, w_out, g)):
+        a[..., :b.shape[-1]] = b
+    check(wide[0][:, :D], wide[1][:, :, :D], wide[2][:, :, :F], ids, weights, wide[3][:, :D])
+
+
 def test_what_lies_beside_the_outputs_stays():
     """Through the C ABI, into rows with a pitch and guards; dx, dW and d_weights one at a time are the same bits."""
     lib = H.tg()

@@ -29,9 +29,13 @@ constexpr int64_t kMaxExtent = int64_t(1) << 31;
 // before they are added in fp32.  Every step truncates, by less than 2^-23 of
 // the sum, an eighth of that on average where signs are mixed.  16-bit results: 256
 // steps stay below 2^-15.  g, u and d_out W_out, whose product is the fp32
-// gradient of the weights: 32 steps, below 3.9e-6 and about 2e-7 on average each.
+// gradient of the weights: 16 steps, below 2e-6.  Chunks of 2 / 4 / 8 / 16 stages, 8192 x 4
+// rows of 2048 x 1408: that gradient is 3.7e-7 / 6.6e-7 / 1.4e-6 / 2.9e-6 of its norm off (the
+// plain fp32 form 7.3e-7); UP and DH take 340 + 320 us at 4 and 296 + 296 us at 8.
 constexpr int kChunk = 64, kExactChunk = 4;
-// Places up to which UP gathers x's rows by itself.
+// Places up to which UP gathers x's rows by itself: a launch less where tiles have few rows
+// (64 tokens, 128 experts of 2048 x 768: 204 us, and bound by the weights' bytes); many rows
+// a tile are bound by the gathering copies (experts_gemm.cuh).
 constexpr int64_t kGatherPlaces = kPlaceBlock;
 // Whether a forward call reads the weights place by place on the CUDA cores: two launches
 // that stream p experts' weights at about 4.5 TB/s, or five that read those of the d

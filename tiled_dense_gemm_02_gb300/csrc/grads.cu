@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_kernel(const __g
       const uint4 y = clips ? scaled(x[j], v.type, f) : x[j];
       const int64_t e0 = (w << v.shift) - v.skip;
       if (together && e0 >= 0 && e0 + per <= v.count) {
-        *reinterpret_cast<uint4*>(out + e0 * es) = y;
+        __stcs(reinterpret_cast<uint4*>(out + e0 * es), y);  // first to leave L2: the gradients still to be read stay
       } else if (v.type == 2) {
         const uint32_t p[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll

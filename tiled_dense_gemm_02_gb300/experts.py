@@ -387,9 +387,9 @@ def expert_mlp(hidden, w_in, w_out, ids, weights, *, save=False, workspace=None)
     row without a used place gives 0, whatever hidden holds there.
 
     save=True keeps what expert_mlp_backward takes (a uint8 tensor: the rows'
-    order, and g and u in float32); otherwise saved is None.  If hidden, a weight or
-    weights requires a gradient, so does out, and torch's backward pass makes
-    the backward call.
+    order, the rows in it, g and u in float32); otherwise saved is None.  If
+    hidden, a weight or weights requires a gradient, so does out, torch's
+    backward pass makes the backward call, and saved is kept in any case.
     """
     if hidden.requires_grad or w_in.requires_grad or w_out.requires_grad or weights.requires_grad:
         import torch
