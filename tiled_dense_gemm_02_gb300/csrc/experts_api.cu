@@ -30,9 +30,11 @@ constexpr int64_t kMaxExtent = int64_t(1) << 31;
 // the sum, an eighth of that on average where signs are mixed.  16-bit results: 256
 // steps stay below 2^-15.  g, u and d_out W_out, whose product is the fp32
 // gradient of the weights: 16 steps, below 2e-6.  Chunks of 2 / 4 / 8 / 16 stages, 8192 x 4
-// rows of 2048 x 1408: that gradient is 3.7e-7 / 6.6e-7 / 1.4e-6 / 2.9e-6 of its norm off (the
-// plain fp32 form 7.3e-7); UP and DH take 340 + 320 us at 4 and 296 + 296 us at 8.
-constexpr int kChunk = 64, kExactChunk = 4;
+// rows of 2048 x 1408 in bf16: that gradient is 3.7e-7 / 6.6e-7 / 1.4e-6 / 2.9e-6 of its norm
+// off (the plain fp32 form 7.3e-7); UP and DH take 332 + 294 us at 4, 263 + 201 us whole.  fp16's
+// products have 22 bits where bf16's have 16 and lose more: up to 9.8e-7 at 4 stages over drawn
+// sizes (bf16 7.5e-7), 7.6e-7 at 3.
+constexpr int kChunk = 64, kExactChunk = 4, kExactChunkF16 = 3;
 // Places up to which UP gathers x's rows by itself: a launch less where tiles have few rows
 // (64 tokens, 128 experts of 2048 x 768: 204 us, and bound by the weights' bytes); many rows
 // a tile are bound by the gathering copies (experts_gemm.cuh).
@@ -351,7 +353,7 @@ class Experts {
       TGEMM_TRY(map_rows(&m.c, a.h, c_.F, a.ldh, 16));
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 128));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
-      a.chunk = c_.saved ? kExactChunk : kChunk;
+      a.chunk = saved_ ? exact_chunk() : kChunk;
       TGEMM_TRY(launch(launch_expert_up, m, a, tokens(a)));
     }
     {
@@ -387,7 +389,7 @@ class Experts {
       m.c = m.b;
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 256));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
-      a.chunk = kExactChunk;
+      a.chunk = c_.d_weights ? exact_chunk() : kChunk;  // dg, du and w h are 16-bit
       TGEMM_TRY(launch(launch_expert_dh, m, a, tokens(a)));
     }
     if (c_.dw_out) {
@@ -454,6 +456,7 @@ class Experts {
     return TGEMM_OK;
   }
 
+  int exact_chunk() const { return type_ == 1 ? kExactChunkF16 : kExactChunk; }
   int64_t tokens(const ExpertArgs& a) const { return most_tiles(c_.T * c_.k, c_.E) * a.m_blocks; }
 
   template <typename Launch>

@@ -73,11 +73,6 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Brings `bytes` (a multiple of 16) from p on into L2.
-__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // The power of two that the fp16 gradients of a call are multiplied with (a warp).
 __device__ __forceinline__ float gradient_scale(const ExpertArgs& a, int lane, bool leave) {
   uint32_t most = 0u;
@@ -683,16 +678,6 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
       constexpr int STEP = GRADIENT ? 1 : PARTS, MOST = 16 / PARTS;
       const int block0 = GRADIENT ? part * MOST : part;
       const int blocks = GRADIENT ? MOST : (u.n / 16 - part + PARTS - 1) / PARTS;
-      if constexpr (MODE == EXPERT_DH) {
-        // this warp's g and u on their way to L2 under the products: 512 bytes for every
-        // four rows, g or u, 32 features
-        const int feature = u.mb * 256 + cta * kTileM + quarter * 32;
-        const int g = lane >> 1, r = (part + (g >> 2) * PARTS) * 16 + (g & 3) * 4;
-        if (feature < args.F && r < u.valid)
-          prefetch_l2(reinterpret_cast<const float4*>(args.gu) +
-                          ((u.row0 + r) / 4 * 2 + (lane & 1)) * args.ldg + feature,
-                      16 * min(32, static_cast<int>(args.ldg) - feature));
-      }
       uint32_t tcol = 0;
       if (!GRADIENT || stages > 0) {
         tcol = taken() + block0 * 16;
