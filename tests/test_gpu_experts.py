@@ -177,6 +177,41 @@ def test_layouts(T, dtype):
         check(shifted[0], shifted[1], shifted[2], ids, weights, shifted[3])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=NAMES.get)
+@pytest.mark.parametrize("T,E,D,F", [(1, 3, 1, 1), (5, 9, 3, 5), (2, 300, 15, 17), (40, 1024, 9, 34), (64, 12, 333, 90), (300, 5, 1001, 500),
+                                     (9, 7, 530, 64), (9, 7, 64, 530)])
+def test_weights_off_the_grid_give_the_bits_of_aligned_ones(T, E, D, F, dtype):
+    """Every offset and odd pitches, NaN around the weights and in those of experts without rows:
+    the copies that the products read hold the same elements as aligned weights."""
+    lib = H.tg()
+    x, w_in, w_out, ids, weights, g, _ = layer(T, E, 1, D, F, dtype, seed=D + F)
+    ids %= max(1, E // 3)
+    ids = E - 1 - 2 * ids  # from the last expert down, every second one
+    idle = torch.ones(E, dtype=torch.bool, device="cuda")
+    idle[ids.flatten()] = False
+    w_in[idle], w_out[idle] = float("nan"), float("nan")
+
+    def placed(w, lead, pad):
+        rows, cols = w.shape[0] * w.shape[1], w.shape[2]
+        buffer = torch.full((lead + rows * (cols + pad) + 64,), float("nan"), dtype=dtype, device="cuda")
+        view = buffer.as_strided(w.shape, (w.shape[1] * (cols + pad), cols + pad, 1), lead)
+        return view.copy_(w)
+
+    def results(w_in, w_out):
+        out, saved = lib.expert_mlp(x, w_in, w_out, ids, weights, save=True)
+        got = [out, *lib.expert_mlp_backward(x, w_in, w_out, ids, weights, saved, g)]
+        got += lib.expert_mlp_backward(x, w_in, w_out, ids, weights, saved, g, want_hidden=False)[1:]
+        finished()
+        return got
+
+    want = results(placed(w_in, 0, -D % 8), placed(w_out, 0, -F % 8))
+    Experts(x, w_in.nan_to_num(0), w_out.nan_to_num(0), ids, weights, g).check(**dict(zip(("out", "dx", "dw_in", "dw_out", "dw"), want)))
+    for lead in range(8):
+        for pad in (0, 1, 6):
+            for a, b in zip(results(placed(w_in, lead, pad), placed(w_out, 7 - lead, pad)), want):
+                assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("T,E,k", [(1, 6, 2), (3, 6, 2), (90, 6, 2), (40, 64, 40), (1, 64, 40)])
 @pytest.mark.parametrize("D,F", [(97, 51), (104, 50), (101, 56), (7, 3)])
 def test_odd_sizes_in_aligned_rows_and_many_picks(T, E, k, D, F):

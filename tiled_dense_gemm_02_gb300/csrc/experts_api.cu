@@ -19,9 +19,6 @@
 
 namespace tgemm {
 
-cudaError_t launch_repack(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int rows, int cols,
-                          int src_granule, int sms, cudaStream_t stream);
-
 namespace {
 
 constexpr int64_t kMaxExtent = int64_t(1) << 31;
@@ -327,7 +324,6 @@ class Experts {
 
   int forward() {
     if (few()) return forward_few();
-    TGEMM_TRY(weights());
     OrderArgs o = {};
     o.ids = c_.ids;
     o.places = c_.T * c_.k;
@@ -337,6 +333,7 @@ class Experts {
     o.rows = a_.rows;
     o.rows.partial = reinterpret_cast<int*>(ws_ + l_.partial);
     TGEMM_CUDA(launch_order(o, c_.stream), "order launch");
+    TGEMM_TRY(weights(true, true));
     ExpertMaps m;
     {
       ExpertArgs a = a_;
@@ -374,7 +371,7 @@ class Experts {
   }
 
   int backward() {
-    TGEMM_TRY(weights());
+    TGEMM_TRY(weights(c_.dx != nullptr, true));
     ExpertMaps m;
     if (type_ == 1) {
       a_.largest = reinterpret_cast<unsigned int*>(ws_ + l_.largest);
@@ -540,19 +537,19 @@ class Experts {
     return host_map_3d(&m.c, type_, out, N, M, c_.E, ld * 2, M * ld * 2, 64, 32);
   }
 
-  int aligned(Operand& o, const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t at, int64_t ld_copy) {
-    const int granule = host_granule(p, ld, 2);
-    o = Operand{p, ld};
-    if (granule == 16) return TGEMM_OK;
-    o = Operand{ws_ + at, ld_copy};
-    TGEMM_CUDA(launch_repack(p, ld, ws_ + at, ld_copy, static_cast<int>(rows), static_cast<int>(cols), granule, sms_,
-                             c_.stream),
-               "repack launch");
+  // The weights that a call reads, copied where they lie off the 16-byte grid.
+  int weights(bool in, bool out) {
+    in = in && l_.copy_in;
+    out = out && l_.copy_out;
+    w_in_ = in ? Operand{ws_ + l_.w_in, l_.ld_in} : Operand{c_.w_in, c_.ld_in};
+    w_out_ = out ? Operand{ws_ + l_.w_out, l_.ld_out} : Operand{c_.w_out, c_.ld_out};
+    if (!in && !out) return TGEMM_OK;
+    WeightCopy first = {}, second = {};
+    if (in) first = WeightCopy{c_.w_in, ws_ + l_.w_in, c_.ld_in, l_.ld_in, static_cast<int>(2 * c_.F), a_.D};
+    if (out) second = WeightCopy{c_.w_out, ws_ + l_.w_out, c_.ld_out, l_.ld_out, a_.D, a_.F};
+    TGEMM_CUDA(launch_copy_weights(a_.rows.count, a_.E, std::min(c_.E, c_.T * c_.k), first, second, sms_, c_.stream),
+               "copy of the weights");
     return TGEMM_OK;
-  }
-  int weights() {
-    TGEMM_TRY(aligned(w_in_, c_.w_in, c_.ld_in, c_.E * 2 * c_.F, c_.D, l_.w_in, l_.ld_in));
-    return aligned(w_out_, c_.w_out, c_.ld_out, c_.E * c_.D, c_.F, l_.w_out, l_.ld_out);
   }
 
   const Call& c_;

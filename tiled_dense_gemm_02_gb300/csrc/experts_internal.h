@@ -41,6 +41,18 @@ struct OrderArgs {
 int order_blocks(int64_t places);
 cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream);
 
+// E x rows rows of cols 16-bit elements copied from pitch ld_from to ld_to (elements; whole
+// 16-byte words, as `to`), of the experts with a count; rows = 0: nothing.  used: such
+// experts, at most.
+struct WeightCopy {
+  const void* from;
+  void* to;
+  int64_t ld_from, ld_to;
+  int rows, cols;
+};
+cudaError_t launch_copy_weights(const int* count, int E, int64_t used, const WeightCopy& in, const WeightCopy& out, int sms,
+                                cudaStream_t stream);
+
 // out[r] (pitch ld_out, 16-byte aligned) = the row of x of sorted row r's token; the
 // filling is 0.  granule: alignment of x's rows in bytes.  largest (or null): the largest
 // finite |x| of each of the gather_blocks blocks' rows, as a half's bits.

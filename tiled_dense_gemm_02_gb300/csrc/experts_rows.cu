@@ -267,6 +267,96 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_consta
   place_rows(a, base, each, counts);
 }
 
+// ----------------------------------------------------- weights off the 16-byte grid
+// Copies of the weights in an aligned pitch, which the products' bulk-tensor copies need, of
+// the experts that have rows.  A warp a row, 16 bytes a lane: an aligned word, shifted together
+// with the next lane's; what a row's last word takes from behind the row is never used.  Bound by
+// bytes: 50 experts of 477 x 2079 (600 MB read and written) 110 us, 10 of 1001 x 500 (60 MB) 19;
+// two rows a warp 124, four 140 (64 registers).
+constexpr int kCopyThreads = 256;
+
+// The bytes from `off` (a multiple of 2, below 16) on of two neighbouring words.
+__device__ __forceinline__ uint4 across(const uint4& a, const uint4& b, int off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (off & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const uint32_t shift = 8u * (off & 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], shift);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The elements of an aligned word that lie in [begin, end), bytes from p.
+__device__ __forceinline__ uint4 word_inside(const uint8_t* p, int begin, int end) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (2 * i >= begin && 2 * i < end) w[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(kCopyThreads, 8) copy_weights_kernel(const int* count, int E,
+                                                                    const __grid_constant__ WeightCopy in,
+                                                                    const __grid_constant__ WeightCopy out) {
+  __shared__ int used[kMaxExperts];
+  __shared__ int in_warp[kCopyThreads / 32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int listed = 0;
+  for (int e0 = 0; e0 < E; e0 += kCopyThreads) {
+    const int e = e0 + threadIdx.x;
+    const bool some = e < E && __ldcg(count + e) > 0;
+    const uint32_t mask = __ballot_sync(kAll, some);
+    if (lane == 0) in_warp[warp] = __popc(mask);
+    __syncthreads();
+    int at = listed + __popc(mask & ((1u << lane) - 1u));
+    for (int w = 0; w < kCopyThreads / 32; ++w) {
+      if (w < warp) at += in_warp[w];
+      listed += in_warp[w];
+    }
+    if (some) used[at] = e;
+    __syncthreads();
+  }
+  const uint32_t each = in.rows + out.rows;  // rows of an expert
+  const int64_t total = int64_t(listed) * each, warps = int64_t(gridDim.x) * (kCopyThreads / 32);
+  for (int64_t r = int64_t(blockIdx.x) * (kCopyThreads / 32) + warp; r < total; r += warps) {
+    const uint32_t slot = static_cast<uint32_t>(r) / each;
+    uint32_t row = static_cast<uint32_t>(r) - slot * each;
+    const bool second = row >= static_cast<uint32_t>(in.rows);
+    const WeightCopy& m = second ? out : in;
+    if (second) row -= in.rows;
+    const int64_t at = int64_t(used[slot]) * m.rows + row, last = int64_t(E) * m.rows - 1;
+    const uint8_t* src = static_cast<const uint8_t*>(m.from) + at * m.ld_from * 2;
+    uint8_t* dst = static_cast<uint8_t*>(m.to) + at * m.ld_to * 2;
+    const int off = static_cast<int>(reinterpret_cast<uint64_t>(src) & 15u), bytes = 2 * m.cols;
+    src -= off;  // the matrix lies in [low, high) from here
+    const int low = static_cast<int>(max(int64_t(0), off - at * m.ld_from * 2));
+    const int high = static_cast<int>(min(off + ((last - at) * m.ld_from + m.cols) * 2, int64_t(INT_MAX)));
+    for (int d0 = 0; d0 < bytes; d0 += 31 * 16) {  // the last lane has the second word of the one before
+      const int d = d0 + lane * 16;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u), next;
+      if (d < bytes + off) {
+        if (d >= low && d + 16 <= high)
+          v = __ldg(reinterpret_cast<const uint4*>(src + d));
+        else
+          v = word_inside(src + d, low - d, high - d);
+      }
+      next.x = __shfl_down_sync(kAll, v.x, 1);
+      next.y = __shfl_down_sync(kAll, v.y, 1);
+      next.z = __shfl_down_sync(kAll, v.z, 1);
+      next.w = __shfl_down_sync(kAll, v.w, 1);
+      if (lane < 31 && d < bytes) *reinterpret_cast<uint4*>(dst + d) = across(v, next, off);
+    }
+  }
+}
+
 // ----------------------------------------------------------------- gather
 // A warp a row, up to eight 16-byte loads a lane in flight, the next row's token loaded
 // ahead.  Bound by bytes: a token's row is read k times, the later times from L2, and
@@ -481,6 +571,14 @@ cudaError_t launch_order(const OrderArgs& a, cudaStream_t stream) {
   if (e == cudaSuccess) e = launch_next(tiles_kernel, dim3(1), kTilesThreads, 0, stream, a, blocks, std::min(16, kTilesThreads / a.E));
   if (e == cudaSuccess) e = launch_next(place_kernel, dim3(blocks), kSortThreads, smem, stream, a, each);
   return e;
+}
+
+cudaError_t launch_copy_weights(const int* count, int E, int64_t used, const WeightCopy& in, const WeightCopy& out, int sms,
+                                cudaStream_t stream) {
+  constexpr int kRows = kCopyThreads / 32;
+  const int64_t rows = used * (int64_t(in.rows) + out.rows);
+  const int blocks = static_cast<int>(std::min<int64_t>((rows + kRows - 1) / kRows, 32 * std::max(1, sms)));
+  return launch_next(copy_weights_kernel, dim3(blocks), kCopyThreads, 0, stream, count, E, in, out);
 }
 
 int gather_blocks(int64_t most_rows, int sms) {
