@@ -116,7 +116,7 @@ typedef struct tgemm_experts_options {
  * looked at).  Needs no GPU.
  *
  * With r = T k rows and up to 31 more per expert that has any, F and D to the next 64: 2 F + 4 D
- * bytes a row forward, 6 F + 4 D and F / 8 bytes backward (fp16 2 D more), and the copies. */
+ * bytes a row forward, 6 F + 4 D and F / 8 bytes backward (fp16 2 D more, backward 4 F too), and the copies. */
 TGEMM_API int tgemm_experts_workspace_size(int backward, int64_t T, int64_t E, int64_t k, int64_t D, int64_t F,
                const void* W_in, int64_t ld_in, const void* W_out, int64_t ld_out, int dtype, size_t* bytes);
 
@@ -155,8 +155,10 @@ TGEMM_API int tgemm_experts_forward(int64_t T, int64_t E, int64_t k, int64_t D, 
  *   dx_t = sum_j W_in[e]^T (dg, du),   dW_in[e] = sum over its rows (dg, du) x_t^T
  *   dW_out[e] = sum over its rows grad_t (w h)^T
  *
- * dg, du and w h are rounded to dtype on their way into the products (fp16: dg and
- * du times a power of two that brings the largest |grad| to 16), each output once.
+ * dg, du and w h are rounded to dtype on their way into the products, each output once.
+ * fp16: dg and du times a power of two of their expert, which brings the largest finite one
+ * to 2^14 or more; all bits are kept of what is above 2^-28 of that, and 2^-39 of it is half
+ * of the smallest step.
  * dx, dW_in, dW_out (pitches as the operands') and d_weights: any may be NULL when
  * it is not wanted; an expert without rows gets zeros. */
 TGEMM_API int tgemm_experts_backward(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F,

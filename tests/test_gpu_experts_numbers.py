@@ -1,0 +1,94 @@
+"""Numbers at the ends of their range in the experts' products: where a computation that is right in the
+middle of it overflows, underflows or loses what lies beside a larger number (tests/experts_numbers.py)."""
+import math
+
+import pytest
+import torch
+
+from tests import gpu_harness as H
+from tests.experts_numbers import Numbers
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+NAMES = {BF16: "bf16", F16: "f16"}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    H.tg()
+    torch.cuda.set_device(0)
+
+
+def normals(seed):
+    gen = torch.Generator(device="cuda").manual_seed(9000 + seed)
+    return lambda *shape: torch.randn(*shape, device="cuda", generator=gen)
+
+
+def layer(T, E, k, D, F, dtype, seed=0):
+    normal = normals(seed)
+    x, w_in, w_out = normal(T, D), normal(E, 2 * F, D) / math.sqrt(D), normal(E, D, F) / math.sqrt(F)
+    ids = torch.topk(normal(T, E), k, dim=1).indices
+    return x.to(dtype), w_in.to(dtype), w_out.to(dtype), ids, torch.rand_like(ids.float()), (0.1 * normal(T, D)).to(dtype), normal
+
+
+def gradients(x, w_in, w_out, ids, weights, g, **more):
+    lib = H.tg()
+    out, saved = lib.expert_mlp(x, w_in, w_out, ids, weights, save=True)
+    got = dict(zip(("dx", "dw_in", "dw_out", "dw"), lib.expert_mlp_backward(x, w_in, w_out, ids, weights, saved, g, **more)))
+    assert lib.device_status(torch.cuda.current_stream().cuda_stream) == lib.OK
+    return {"out": out, **{n: v for n, v in got.items() if v is not None}}
+
+
+def check(*args):
+    got = gradients(*args)
+    Numbers(*args).check(**got)
+    return got
+
+
+@pytest.mark.parametrize("T,F", [(70, 64), (300, 63)])
+def test_fp16_gradients_that_grow_with_the_depth(T, F):
+    """dg and du sum over D: with a constant gradient and weights of one sign they are thousands of times the gradient."""
+    D, E = 4096, 2
+    x, w_in, w_out, ids, _, _, normal = layer(T, E, 1, D, F, F16, seed=F)
+    g = torch.full((T, D), 2.0 ** -10, device="cuda").half()
+    check(4 * x, w_in, w_out.abs(), ids, torch.ones(T, 1, device="cuda"), g)
+
+
+def test_fp16_gradients_of_large_inputs():
+    """u of size 60: du is, and dg is 60 times as large."""
+    x, w_in, w_out, ids, _, g, _ = layer(90, 2, 1, 8192, 64, F16)
+    check((60 * x.float()).half(), w_in, w_out / 64, ids, torch.ones(90, 1, device="cuda"), g / 64)
+
+
+def test_fp16_gradients_of_large_weights():
+    x, w_in, w_out, ids, _, g, _ = layer(256, 4, 1, 512, 1024, F16)
+    check(x, w_in, (2000 * w_out.float()).half(), ids, torch.ones(256, 1, device="cuda"), g / 2)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -20, 2.0 ** -12, 1.0, 2.0 ** 8])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_fp16_gradients_whatever_the_output_weights_are(size, odd):
+    """dg and du over the gradient from 2^-20 to 2^8; the operands stay in the middle of fp16's range."""
+    x, w_in, w_out, ids, weights, g, _ = layer(200, 3, 2, 256, 128 - odd, F16, seed=3)
+    a, b = (2.0 ** 8, size / 2 ** 8) if size >= 1 else (2.0 ** -8, size * 2 ** 8)
+    # a part of the factor in W_out, the rest in x's gates and ups
+    check((x.float() * math.sqrt(max(1.0, b))).half(), w_in, (w_out.float() * a * min(1.0, b)).half(), ids, weights, (g.float() / 64).half())
+
+
+def test_fp16_rows_beside_an_infinite_gradient():
+    """A row whose gradient is infinite takes nothing from the other rows and the other experts."""
+    x, w_in, w_out, ids, weights, g, _ = layer(130, 4, 1, 128, 96, F16)
+    g[7, 5] = math.inf
+    g[9, 0] = math.nan
+    bad = torch.zeros(130, dtype=torch.bool, device="cuda")
+    bad[[7, 9]] = True
+    got = gradients(x, w_in, w_out, ids, weights, g)
+    hit = torch.unique(ids[bad])
+    keep = torch.tensor([e for e in range(4) if e not in hit.tolist()], device="cuda")
+    assert keep.numel() > 0
+    want = Numbers(x, w_in, w_out, ids, weights, torch.where(bad[:, None], torch.zeros_like(g), g))
+    want.check(rows=~bad, experts=keep, **got)
+    assert not bool(got["dx"][bad].isfinite().any())

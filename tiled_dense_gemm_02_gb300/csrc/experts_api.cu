@@ -3,7 +3,7 @@
 // order of launches.
 //
 // Forward:  sort of the places  [gather of x]  UP  DOWN  join
-// Backward: gather of grad  DH  DOUT  DX  join  DIN
+// Backward: gather of grad  DH  [fp16: rounding of dg, du and w h]  DOUT  DX  join  DIN
 // A few places forward: UP and DOWN on the CUDA cores (experts_few.cu).
 // (experts_rows.cu and experts_gemm.cuh hold the other kernels.)  Weights whose rows are
 // not 16-byte aligned are copied to an aligned pitch first.
@@ -144,7 +144,7 @@ SavedLayout plan_saved(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F) {
 struct Layout {
   bool copy_in, copy_out;  // weights off the 16-byte grid
   RowsLayout rows;
-  int64_t partial, x, w_in, w_out, h, dgu, y, y_exponent, dots, largest, scale;
+  int64_t partial, x, w_in, w_out, h, dgu, y, y_exponent, dots, v, largest;
   int64_t ldx, ldh, ld_dgu, ldy, ld_in, ld_out;
   int parts;               // DH: dots of a row
   int64_t total;
@@ -173,8 +173,10 @@ Layout plan_layout(bool backward, int64_t T, int64_t E, int64_t k, int64_t D, in
   if (backward) {
     l.dgu = take(rows * l.ld_dgu * 2);
     l.dots = take(rows * l.parts * 4);
-    l.largest = take(kGatherMost * 4);
-    l.scale = take(8);
+    if (dtype == TGEMM_F16) {
+      l.v = take(rows * round_up(F, 4) * 4);
+      l.largest = take(E * 2 * 4);
+    }
   } else {
     l.rows = plan_rows(take, places, E);
     l.partial = take(order_blocks(places) * E * 4);
@@ -374,11 +376,10 @@ class Experts {
     TGEMM_TRY(weights(c_.dx != nullptr, true));
     ExpertMaps m;
     if (type_ == 1) {
+      a_.v = reinterpret_cast<float*>(ws_ + l_.v);
       a_.largest = reinterpret_cast<unsigned int*>(ws_ + l_.largest);
-      a_.gathered = gather_blocks(rows_max_, sms_);
-      a_.scale = reinterpret_cast<float*>(ws_ + l_.scale);
     }
-    TGEMM_TRY(gather(c_.grad, c_.ldg, ws_ + l_.x, const_cast<unsigned int*>(a_.largest)));
+    TGEMM_TRY(gather(c_.grad, c_.ldg, ws_ + l_.x, a_.largest, a_.E));
     {
       ExpertArgs a = a_;
       TGEMM_TRY(map_transposed(m, a, w_out_, c_.F, c_.D));
@@ -389,6 +390,7 @@ class Experts {
       a.chunk = c_.d_weights ? exact_chunk() : kChunk;  // dg, du and w h are 16-bit
       TGEMM_TRY(launch(launch_expert_dh, m, a, tokens(a)));
     }
+    if (type_ == 1 && (c_.dx || c_.dw_in || c_.dw_out)) TGEMM_TRY(round_gradients());
     if (c_.dw_out) {
       ExpertArgs a = a_;
       TGEMM_TRY(map_blocks(&m.a, ws_ + l_.x, c_.D, l_.ldx));
@@ -411,7 +413,6 @@ class Experts {
       a.k_blocks = static_cast<int>(ceil_div(2 * c_.F, kTileK));
       a.chunk = kChunk;
       TGEMM_TRY(launch(launch_expert_dx, m, a, tokens(a)));
-      j.scale = a_.scale;
       j.out = c_.dx;
       j.ld_out = c_.lddx;
     }
@@ -504,10 +505,28 @@ class Experts {
     TGEMM_TRY(map_rows(&m.b32, p, cols, ld, 32));
     return map_rows(&m.b16, p, cols, ld, 16);
   }
-  int gather(const void* x, int64_t ld, void* rows, unsigned int* largest = nullptr) {
-    TGEMM_CUDA(launch_gather_rows(a_.rows, rows_max_, x, ld, host_granule(x, ld, 2), a_.D, rows, l_.ldx, largest, sms_,
+  int gather(const void* x, int64_t ld, void* rows, unsigned int* zeros = nullptr, int words = 0) {
+    TGEMM_CUDA(launch_gather_rows(a_.rows, rows_max_, x, ld, host_granule(x, ld, 2), a_.D, rows, l_.ldx, zeros, words, sms_,
                                   c_.stream),
                "gather launch");
+    return TGEMM_OK;
+  }
+
+  int round_gradients() {
+    RoundArgs r = {};
+    r.E = a_.E;
+    r.F = a_.F;
+    r.rows = a_.rows;
+    r.weights = a_.weights;
+    r.gu = a_.gu;
+    r.v = a_.v;
+    r.ldg = a_.ldg;
+    r.largest = a_.largest;
+    r.dgu = a_.dgu;
+    r.ld_dgu = a_.ld_dgu;
+    r.h = a_.h;
+    r.ldh = a_.ldh;
+    TGEMM_CUDA(launch_round_gradients(r, rows_max_, c_.stream), "rounding launch");
     return TGEMM_OK;
   }
 

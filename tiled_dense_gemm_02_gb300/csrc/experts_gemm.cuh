@@ -37,6 +37,7 @@
 // wait is bounded (tc_common.cuh).
 #pragma once
 
+#include "experts_gate.cuh"
 #include "experts_internal.h"
 #include "tc_pair.cuh"
 
@@ -71,20 +72,6 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar_cluster)
       : "memory");
-}
-
-// The power of two that the fp16 gradients of a call are multiplied with (a warp).
-__device__ __forceinline__ float gradient_scale(const ExpertArgs& a, int lane, bool leave) {
-  uint32_t most = 0u;
-  for (int i = lane; i < a.gathered; i += 32) most = max(most, __ldcg(a.largest + i));
-  most = __reduce_max_sync(0xffffffffu, most);
-  const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
-  const int e = v > 0.0f ? kGradExponent - ilogbf(v) : 0;
-  if (leave && lane == 0) {
-    a.scale[0] = ldexpf(1.0f, e);
-    a.scale[1] = ldexpf(1.0f, -e);
-  }
-  return ldexpf(1.0f, e);
 }
 
 // A tile of a product: block mb of M, and N's columns (rows row0.. of the sorted
@@ -155,8 +142,6 @@ __device__ __forceinline__ void whole_sums(uint32_t tcol, const uint32_t (&sum)[
   for (int b = 0; b < MOST; ++b) ptx::tmem_st_32x32b_x16(tcol + b * STEP * 16, sum[b]);
   ptx::tmem_wait_st();
 }
-
-__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 // Where a lane stores 16-bit values of its feature, two rows at a time.  Neighbouring
 // lanes hold neighbouring features; PAIRS: each stores both features of one of the
@@ -284,57 +269,39 @@ __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertA
   }
 }
 
-// 8 columns of DH: v = d_out W_out of this lane's feature.
-//   s = sigmoid(g):  dg = w v u s (1 + g (1 - s)),  du = w v g s,  h = g s u
-// `mine`: in lane first + c the weight of column c, and `scaled` times the gradients' scale.
-template <bool PAIRS>
-__device__ __forceinline__ void finish_dh(const uint32_t (&v)[8], const ExpertArgs& a, int feature, int64_t row,
-                                          int valid, int fmt, int lane, float mine, float scaled, int first, int part,
-                                          int parts) {
-  const float4* gu = reinterpret_cast<const float4*>(a.gu) + row / 4 * 2 * a.ldg + feature;
-  float4 g4[2], u4[2];
+// 8 columns of DH: v = d_out W_out of this lane's feature, with g and u (0 in the filling,
+// whatever the weights hold).
+struct HiddenColumns {
+  float g[8], u[8], d[8];
+  __device__ __forceinline__ HiddenColumns(const uint32_t (&v)[8], const ExpertArgs& a, int feature, int64_t row, int valid) {
+    const float4* gu = reinterpret_cast<const float4*>(a.gu) + row / 4 * 2 * a.ldg + feature;
+    float4 g4[2], u4[2];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    g4[q] = u4[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (feature < a.F) {
-      g4[q] = __ldcg(gu);
-      u4[q] = __ldcg(gu + a.ldg);
+    for (int q = 0; q < 2; ++q) {
+      g4[q] = u4[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (feature < a.F) {
+        g4[q] = __ldcg(gu);
+        u4[q] = __ldcg(gu + a.ldg);
+      }
+      gu += 2 * a.ldg;
+      g[4 * q] = g4[q].x, g[4 * q + 1] = g4[q].y, g[4 * q + 2] = g4[q].z, g[4 * q + 3] = g4[q].w;
+      u[4 * q] = u4[q].x, u[4 * q + 1] = u4[q].y, u[4 * q + 2] = u4[q].z, u[4 * q + 3] = u4[q].w;
     }
-    gu += 2 * a.ldg;
-  }
-  RowStore<PAIRS> dg_rows(a.dgu, row, a.ld_dgu, feature, a.F, lane), hw_rows(a.h, row, a.ldh, feature, a.F, lane);
-  RowStore<PAIRS> du_rows = dg_rows;
-  du_rows.p += a.F;
-  float g[8] = {g4[0].x, g4[0].y, g4[0].z, g4[0].w, g4[1].x, g4[1].y, g4[1].z, g4[1].w};
-  float u[8] = {u4[0].x, u4[0].y, u4[0].z, u4[0].w, u4[1].x, u4[1].y, u4[1].z, u4[1].w};
-  float d[8];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) d[c] = __uint_as_float(v[c]);
-  if (valid < 8) {  // the filling: zeros, whatever the weights hold
+    for (int c = 0; c < 8; ++c) d[c] = __uint_as_float(v[c]);
+    if (valid < 8) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c >= valid) g[c] = u[c] = d[c] = 0.0f;
+      for (int c = 0; c < 8; ++c) {
+        if (c >= valid) g[c] = u[c] = d[c] = 0.0f;
+      }
     }
   }
-#pragma unroll
-  for (int c = 0; c < 8; c += 2) {
-    float dg[2], du[2], h[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float s = fast_sigmoid(g[c + e]), silu = g[c + e] * s;
-      const float wd = __shfl_sync(0xffffffffu, scaled, first + c + e) * d[c + e];
-      h[e] = silu * u[c + e];
-      dg[e] = wd * u[c + e] * fmaf(silu, 1.0f - s, s);
-      du[e] = wd * silu;
-      d[c + e] *= h[e];
-      h[e] *= __shfl_sync(0xffffffffu, mine, first + c + e);
-    }
-    dg_rows.put(pack_pair(dg[0], dg[1], fmt));
-    du_rows.put(pack_pair(du[0], du[1], fmt));
-    hw_rows.put(pack_pair(h[0], h[1], fmt));
-  }
-  // sums of h v over the 32 lanes: a lane keeps half of its columns at each exchange,
-  // and ends with a quarter of one column's
+};
+
+// Sums of h v over the 32 lanes (d: h v of 8 columns): a lane keeps half of its columns at each
+// exchange, and ends with a quarter of one column's.
+__device__ __forceinline__ void finish_dots(float (&d)[8], const ExpertArgs& a, int64_t row, int valid, int lane, int part,
+                                            int parts) {
 #pragma unroll
   for (int width = 4; width >= 1; width >>= 1) {
     const bool high = (lane & (4 * width)) != 0;
@@ -350,14 +317,67 @@ __device__ __forceinline__ void finish_dh(const uint32_t (&v)[8], const ExpertAr
   if ((lane & 3) == 0 && c < valid) __stcg(a.dots + (row + c) * parts + part, sum);
 }
 
-// 16 columns of DOWN or DX for fp16 operands: fp32, one row's 32 neighbouring elements
+// 8 columns of DH for bf16 operands: dg, du and w h in 16 bits.  `mine`: in lane first + c the
+// weight of column c.
+template <bool PAIRS>
+__device__ __forceinline__ void finish_dh(const uint32_t (&v)[8], const ExpertArgs& a, int feature, int64_t row,
+                                          int valid, int fmt, int lane, float mine, int first, int part, int parts) {
+  HiddenColumns x(v, a, feature, row, valid);
+  RowStore<PAIRS> dg_rows(a.dgu, row, a.ld_dgu, feature, a.F, lane), hw_rows(a.h, row, a.ldh, feature, a.F, lane);
+  RowStore<PAIRS> du_rows = dg_rows;
+  du_rows.p += a.F;
+#pragma unroll
+  for (int c = 0; c < 8; c += 2) {
+    float dg[2], du[2], h[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float w = __shfl_sync(0xffffffffu, mine, first + c + e);
+      const GatedGradient d = gated_gradient(x.g[c + e], x.u[c + e], w * x.d[c + e]);
+      dg[e] = d.dg;
+      du[e] = d.du;
+      x.d[c + e] *= d.h;
+      h[e] = w * d.h;
+    }
+    dg_rows.put(pack_pair(dg[0], dg[1], fmt));
+    du_rows.put(pack_pair(du[0], du[1], fmt));
+    hw_rows.put(pack_pair(h[0], h[1], fmt));
+  }
+  finish_dots(x.d, a, row, valid, lane, part, parts);
+}
+
+// The larger of `most` and |x| where x is finite, as floats' bits.
+__device__ __forceinline__ uint32_t larger_finite(uint32_t most, float x) {
+  const uint32_t size = __float_as_uint(x) & 0x7FFFFFFFu;
+  return size < 0x7F800000u ? max(most, size) : most;
+}
+
+// The same for fp16 operands: v in fp32, 16 bytes a lane, and the largest finite |dg| or |du| so far.
+__device__ __forceinline__ void finish_v(const uint32_t (&v)[8], const ExpertArgs& a, int feature, int64_t row, int valid,
+                                         int lane, float mine, int first, int part, int parts, uint32_t& most) {
+  HiddenColumns x(v, a, feature, row, valid);
+  if (feature < a.F) {
+    float4* to = reinterpret_cast<float4*>(a.v) + row / 4 * a.ldg + feature;
+    __stcs(to, make_float4(x.d[0], x.d[1], x.d[2], x.d[3]));
+    __stcs(to + a.ldg, make_float4(x.d[4], x.d[5], x.d[6], x.d[7]));
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float w = __shfl_sync(0xffffffffu, mine, first + c);
+    const GatedGradient d = gated_gradient(x.g[c], x.u[c], w * x.d[c]);
+    most = larger_finite(larger_finite(most, d.dg), d.du);
+    x.d[c] *= d.h;
+  }
+  finish_dots(x.d, a, row, valid, lane, part, parts);
+}
+
+// 16 columns of DOWN or DX for fp16 operands: fp32 times f, one row's 32 neighbouring elements
 // a store.
-__device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int valid) {
+__device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertArgs& a, int d, int64_t row, int valid, float f) {
   if (d >= a.D) return;
   float* y = static_cast<float*>(a.y) + row * a.ldy + d;
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
-    if (c < valid) __stcg(y, __uint_as_float(v[c]));
+    if (c < valid) __stcg(y, f * __uint_as_float(v[c]));
     y += a.ldy;
   }
 }
@@ -652,9 +672,6 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
     Staged staged{sC + part * staged_buffers(MODE) * staged_bytes(MODE), 0, part, quarter};
     const int fmt = args.bf16 ? OUT_BF16 : OUT_F16;
     const bool pairs = (args.F & 1) == 0;
-    float scale = 1.0f;
-    if (MODE == EXPERT_DH && args.largest) scale = gradient_scale(args, lane, warp == 2 && blockIdx.x == 0);
-    if (MODE == EXPERT_DIN && args.scale) scale = __ldcg(args.scale + 1);
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -701,10 +718,12 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
       if constexpr (STAGED) ok = part_agrees(ok, part);
       if (!ok) break;
       next = units.get(args, i + workers);  // under this epilogue; no register is its beside the sums
+      float unscale = 1.0f;  // of the expert's fp16 gradients
+      if ((MODE == EXPERT_DIN || MODE == EXPERT_DX) && args.largest) unscale = expert_unscale(__ldcg(args.largest + u.expert));
       if constexpr (GRADIENT) {
         const int M = MODE == EXPERT_DIN ? 2 * args.F : args.D, N = MODE == EXPERT_DIN ? args.D : args.F;
         finish_weight(tcol, stages > 0, args, u.expert, u.mb * 256 + cta * kTileM + quarter * 32, M,
-                      u.nb * 256 + part * 128, N, scale, &mapC, buf, lane);
+                      u.nb * 256 + part * 128, N, unscale, &mapC, buf, lane);
         if (stages > 0) given_back();
       } else {
         const int m0 = MODE == EXPERT_UP ? u.mb * kTileM + cta * 64 + quarter * 16 + (lane & 15)
@@ -717,6 +736,7 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
                      : 0.0f;
         };
         float ahead = MODE == EXPERT_DH ? weight_of(0) : 0.0f;
+        uint32_t most = 0u;
         constexpr bool JOINED = MODE == EXPERT_DOWN || MODE == EXPERT_DX;
         if (JOINED && args.bf16) {
           // two blocks at a time: their chains of reductions and exchanges run side by side
@@ -750,12 +770,12 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
               ptx::tmem_ld_32x32b_x8(tcol + b * PARTS * 16 + half, v);
               ptx::tmem_wait_ld();
               const int dot = (u.mb * 2 + cta) * 4 + quarter;
-              if (pairs)
-                finish_dh<true>(v, args, m0, u.row0 + c0 + half, valid - half, fmt, lane, mine, scale * mine, half, dot,
-                                args.m_blocks * 8);
+              if (args.v)
+                finish_v(v, args, m0, u.row0 + c0 + half, valid - half, lane, mine, half, dot, args.m_blocks * 8, most);
+              else if (pairs)
+                finish_dh<true>(v, args, m0, u.row0 + c0 + half, valid - half, fmt, lane, mine, half, dot, args.m_blocks * 8);
               else
-                finish_dh<false>(v, args, m0, u.row0 + c0 + half, valid - half, fmt, lane, mine, scale * mine, half,
-                                 dot, args.m_blocks * 8);
+                finish_dh<false>(v, args, m0, u.row0 + c0 + half, valid - half, fmt, lane, mine, half, dot, args.m_blocks * 8);
             }
           } else {
             uint32_t v[16];
@@ -766,11 +786,15 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
               finish_up(v, args, m0, u.row0 + c0, valid, fmt, lane, m0 - x0, staged);
               staged.store(&mapC, x0, min(64, args.F - x0), u.row0 + c0, 1, 0, lane);
             } else {
-              finish_y(v, args, m0, u.row0 + c0, valid);
+              finish_y(v, args, m0, u.row0 + c0, valid, unscale);
             }
           }
         }
         given_back();
+        if (MODE == EXPERT_DH && args.v) {  // a maximum is the same in whatever order
+          const uint32_t all = __reduce_max_sync(0xffffffffu, most);
+          if (lane == 0 && all) atomicMax(args.largest + u.expert, all);
+        }
       }
     }
     if ((GRADIENT || STAGED) && lane == 0) ptx::bulk_wait_group_read<0>();

@@ -54,12 +54,42 @@ cudaError_t launch_copy_weights(const int* count, int E, int64_t used, const Wei
                                 cudaStream_t stream);
 
 // out[r] (pitch ld_out, 16-byte aligned) = the row of x of sorted row r's token; the
-// filling is 0.  granule: alignment of x's rows in bytes.  largest (or null): the largest
-// finite |x| of each of the gather_blocks blocks' rows, as a half's bits.
-constexpr int kGatherMost = 1024;
-int gather_blocks(int64_t most_rows, int sms);
+// filling is 0.  granule: alignment of x's rows in bytes.  zeros (or null): `words` words
+// that become 0.
 cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const void* x, int64_t ldx, int granule, int D,
-                               void* out, int64_t ld_out, unsigned int* largest, int sms, cudaStream_t stream);
+                               void* out, int64_t ld_out, unsigned int* zeros, int words, int sms, cudaStream_t stream);
+
+// fp16 gradients on their way into the products: from v = W_out^T grad in fp32 (as DH leaves
+// it), g and u, the rows of dg and du in halves, times the power of two of their expert
+// (expert_scale), and of weight * h.  The filling is 0.
+struct RoundArgs {
+  int E, F;
+  ExpertRows rows;
+  const float* weights;          // of each place
+  const float* gu;               // [row / 4][g, u][feature, pitch ldg][row % 4]
+  const float* v;                // [row / 4][feature, pitch ldg][row % 4]
+  int64_t ldg;
+  const unsigned int* largest;   // of each expert: |dg| or |du|, floats' bits
+  void* dgu;
+  int64_t ld_dgu;
+  void* h;
+  int64_t ldh;
+};
+cudaError_t launch_round_gradients(const RoundArgs& a, int64_t most_rows, cudaStream_t stream);
+// The exponent of the power of two that brings the largest of some finite values (a float's bits)
+// into [2^14, 2^15), as far as it and its reciprocal are floats with all bits.
+__host__ __device__ inline int expert_exponent(unsigned int largest) {
+  const int e = 14 + 127 - static_cast<int>(largest >> 23);
+  return e < 126 ? e : 126;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ float expert_scale(unsigned int largest) {
+  return __uint_as_float(static_cast<unsigned int>(127 + expert_exponent(largest)) << 23);
+}
+__device__ __forceinline__ float expert_unscale(unsigned int largest) {
+  return __uint_as_float(static_cast<unsigned int>(127 - expert_exponent(largest)) << 23);
+}
+#endif
 
 // out[t] = sum over t's rows of weight * y[row] (weights null: of y[row]), rounded
 // to type (0 bf16, 1 f16); a place of no such expert: NaN.  dots not null: d_weights
@@ -75,7 +105,6 @@ struct JoinArgs {
   int type;
   void* out;
   int64_t ld_out;
-  const float* scale;   // a power of two that y is divided by, or null
   const float* dots;
   int parts;
   float* d_weights;
@@ -103,7 +132,6 @@ struct ExpertFewArgs {
 cudaError_t launch_experts_few(const ExpertFewArgs& a, bool bf16, cudaStream_t stream);
 
 // ---------------------------------------------------------------- products
-constexpr int kGradExponent = 4;
 // M is a weight's axis, N the tokens' (the gradients of the weights: M and N the
 // weight's two axes, K the expert's rows).
 enum ExpertMode : int {
@@ -132,12 +160,11 @@ struct ExpertArgs {
   int64_t ld_dgu;
   float* dots;             // DH: m_blocks * 8 per row
   const float* weights;    // DH: of each place
-  // fp16, else null: DH multiplies dg and du with s, a power of two that brings the largest
-  // finite gradient (of `gathered` blocks' rows) into [2^kGradExponent, 2^(kGradExponent + 1)),
-  // and leaves {s, 1 / s}; DIN and the join divide by it
-  const unsigned int* largest;
-  int gathered;
-  float* scale;
+  // fp16, else null: DH leaves v = W_out^T grad in fp32 and each expert's largest finite numbers
+  // (RoundArgs), from which launch_round_gradients makes dgu and h; DX and DIN take the powers of
+  // two back
+  float* v;
+  unsigned int* largest;
   void* y;                 // DOWN, DX: fp32, or (bf16) halves with an exponent for each 32 columns (JoinArgs)
   int64_t ldy;             // a multiple of 64
   uint8_t* y_exponent;     // [row / 16][column / 32][row % 16]: a warp's 16 bytes lie together

@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "experts_gate.cuh"
 #include "experts_internal.h"
 #include "ptx.cuh"
 
@@ -379,22 +380,15 @@ __device__ __forceinline__ uint4 load_word(const uint16_t* src, int d, int D) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The larger of `most` and a word's finite halves without their signs, two at a time.
-__device__ __forceinline__ uint32_t larger_halves(uint32_t most, uint32_t w) {
-  const uint32_t lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
-  return max(most, max(lo < 0x7C00u ? lo : 0u, hi < 0x7C00u ? hi : 0u));
-}
-
-// largest (or null): of the block's rows, as a half's bits.
 template <int G>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const int* head, const int* token, const int* place,
                                                                 const uint16_t* x, int64_t ldx, int D, uint16_t* out,
-                                                                int64_t ld_out, unsigned int* largest) {
+                                                                int64_t ld_out, unsigned int* zeros, int words) {
   constexpr int kFlight = G == 16 ? 8 : 2;
-  __shared__ unsigned int shared[kGatherThreads / 32];
-  uint32_t most = 0u;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  if (zeros && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < words; i += kGatherThreads) zeros[i] = 0u;
   const int rows = __ldcg(head + 1), lane = threadIdx.x & 31;
   const int warp = blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kGatherThreads / 32);
   const auto token_of = [&](int r) { return r >= rows || __ldcg(place + r) < 0 ? -1 : __ldcg(token + r); };
@@ -412,26 +406,9 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const int* head,
 #pragma unroll
       for (int i = 0; i < kFlight; ++i)  // D is filled up to the pitch, a multiple of 8
         if (d0 + i * 256 < D) *reinterpret_cast<uint4*>(dst + d0 + i * 256) = v[i];
-      if (largest) {
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i)
-          most = larger_halves(larger_halves(larger_halves(larger_halves(most, v[i].x), v[i].y), v[i].z), v[i].w);
-      }
     }
   }
-  if (!largest) return;
-  most = __reduce_max_sync(kAll, most);
-  if (lane == 0) shared[threadIdx.x >> 5] = most;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kGatherThreads / 32; ++w) most = max(most, shared[w]);
-    largest[blockIdx.x] = most;
-  }
 }
-
-// ------------------------------------------------------------------- join
-// One thread: eight columns of a token.  Bound by y's bytes, read once.
-constexpr int kJoinThreads = 128, kJoinColumns = 8;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pair_of(float x, float y) {
@@ -444,6 +421,77 @@ __device__ __forceinline__ uint32_t pair_of(float x, float y) {
   }
 }
 
+// ------------------------------------------------------- fp16 gradients rounded
+// dg and du in halves, after their largest ones are known: a scale from the gradient alone
+// leaves infinities where W_out or u are large and nothing where weights are small, since
+// dg = w v u silu'(g) with v a sum over D.  The largest of an expert at 2^14 keeps all bits of
+// what is above 2^-28 of it.  A block has 32 rows (of one expert) and kRoundFeatures features, a warp
+// four rows and a lane two neighbouring features.  Bound by bytes: v, g and u are read, 12
+// bytes a value, and 6 written.
+constexpr int kRoundThreads = 256, kRoundFeatures = 512;
+
+__global__ void __launch_bounds__(kRoundThreads) round_kernel(const __grid_constant__ RoundArgs a) {
+  __shared__ int owner;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int row0 = blockIdx.x * kRowPad;
+  if (row0 >= __ldcg(a.rows.head + 1)) return;
+  for (int e = threadIdx.x; e < a.E; e += kRoundThreads)
+    if (__ldcg(a.rows.first + e) <= row0 && row0 < __ldcg(a.rows.first + e + 1)) owner = e;
+  __syncthreads();
+  const float scale = expert_scale(__ldcg(a.largest + owner));
+  const int lane = threadIdx.x & 31;
+  const int64_t row = row0 + (threadIdx.x >> 5) * 4;
+  float w[4];
+  bool used[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int place = __ldcg(a.rows.place + row + r);
+    used[r] = place >= 0;
+    w[r] = used[r] ? __ldg(a.weights + place) : 0.0f;
+  }
+  const float4* g4 = reinterpret_cast<const float4*>(a.gu) + row / 4 * 2 * a.ldg;
+  const float4* v4 = reinterpret_cast<const float4*>(a.v) + row / 4 * a.ldg;
+  uint16_t* dg_row = static_cast<uint16_t*>(a.dgu) + row * a.ld_dgu;
+  uint16_t* h_row = static_cast<uint16_t*>(a.h) + row * a.ldh;
+  const bool odd = (a.F & 1) != 0;
+  const int end = min(a.F, (static_cast<int>(blockIdx.y) + 1) * kRoundFeatures);
+#pragma unroll 2
+  for (int f = blockIdx.y * kRoundFeatures + 2 * lane; f < end; f += 64) {
+    float dg[2][4], du[2][4], wh[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // the pitch, a multiple of 4, holds f + 1
+      const float4 g = __ldcs(g4 + f + i), u = __ldcs(g4 + a.ldg + f + i), v = __ldcs(v4 + f + i);
+      const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const GatedGradient d = gated_gradient(gs[r], us[r], w[r] * vs[r]);
+        dg[i][r] = used[r] ? scale * d.dg : 0.0f;
+        du[i][r] = used[r] ? scale * d.du : 0.0f;
+        wh[i][r] = used[r] ? w[r] * d.h : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t p[3] = {pair_of<false>(dg[0][r], dg[1][r]), pair_of<false>(du[0][r], du[1][r]), pair_of<false>(wh[0][r], wh[1][r])};
+      uint16_t* to[3] = {dg_row + r * a.ld_dgu + f, dg_row + r * a.ld_dgu + a.F + f, h_row + r * a.ldh + f};
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (!odd) {
+          *reinterpret_cast<uint32_t*>(to[i]) = p[i];
+        } else {
+          to[i][0] = static_cast<uint16_t>(p[i]);
+          if (f + 1 < a.F) to[i][1] = static_cast<uint16_t>(p[i] >> 16);
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- join
+// One thread: eight columns of a token.  Bound by y's bytes, read once.
+constexpr int kJoinThreads = 128, kJoinColumns = 8;
+
 struct JoinKernelArgs {
   const int* row;
   const float* weights;
@@ -454,7 +502,6 @@ struct JoinKernelArgs {
   void* out;
   int64_t ld_out;
   int vec;  // out's rows are 16-byte aligned and D a multiple of 8
-  const float* scale;
   const float* dots;
   int parts;
   float* d_weights;
@@ -519,10 +566,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       for (int i = 0; i < kJoinColumns; ++i) sum[i] = NAN;
     }
   }
-  const float f = a.scale ? __ldcg(a.scale + 1) : 1.0f;
   uint32_t p[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = pair_of<BF16>(f * sum[2 * i], f * sum[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) p[i] = pair_of<BF16>(sum[2 * i], sum[2 * i + 1]);
   uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.ld_out + d;
   if (a.vec) {
     *reinterpret_cast<uint4*>(out) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -581,18 +627,20 @@ cudaError_t launch_copy_weights(const int* count, int E, int64_t used, const Wei
   return launch_next(copy_weights_kernel, dim3(blocks), kCopyThreads, 0, stream, count, E, in, out);
 }
 
-int gather_blocks(int64_t most_rows, int sms) {
-  constexpr int kWarps = kGatherThreads / 32;
-  return static_cast<int>(std::min<int64_t>({(most_rows + kWarps - 1) / kWarps, 4 * std::max(1, sms), kGatherMost}));
-}
-
 cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const void* x, int64_t ldx, int granule, int D,
-                               void* out, int64_t ld_out, unsigned int* largest, int sms, cudaStream_t stream) {
+                               void* out, int64_t ld_out, unsigned int* zeros, int words, int sms, cudaStream_t stream) {
+  constexpr int kWarps = kGatherThreads / 32;
   const auto kernel = granule == 16 ? gather_kernel<16> : granule >= 4 ? gather_kernel<4> : gather_kernel<2>;
-  return launch_next(kernel, dim3(gather_blocks(most_rows, sms)), kGatherThreads, 0, stream,
+  const int blocks = static_cast<int>(std::min<int64_t>((most_rows + kWarps - 1) / kWarps, 4 * std::max(1, sms)));
+  return launch_next(kernel, dim3(blocks), kGatherThreads, 0, stream,
                      static_cast<const int*>(rows.head), static_cast<const int*>(rows.token),
                      static_cast<const int*>(rows.place), static_cast<const uint16_t*>(x), ldx, D,
-                     static_cast<uint16_t*>(out), ld_out, largest);
+                     static_cast<uint16_t*>(out), ld_out, zeros, words);
+}
+
+cudaError_t launch_round_gradients(const RoundArgs& a, int64_t most_rows, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((most_rows + kRowPad - 1) / kRowPad), (a.F + kRoundFeatures - 1) / kRoundFeatures, 1);
+  return launch_next(round_kernel, grid, kRoundThreads, 0, stream, a);
 }
 
 cudaError_t launch_join(const JoinArgs& j, cudaStream_t stream) {
@@ -607,7 +655,6 @@ cudaError_t launch_join(const JoinArgs& j, cudaStream_t stream) {
   a.out = j.out;
   a.ld_out = j.ld_out;
   a.vec = j.out && j.D % 8 == 0 && j.ld_out % 8 == 0 && reinterpret_cast<uint64_t>(j.out) % 16 == 0;
-  a.scale = j.scale;
   a.dots = j.dots;
   a.parts = j.parts;
   a.d_weights = j.d_weights;
