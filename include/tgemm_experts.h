@@ -156,9 +156,9 @@ TGEMM_API int tgemm_experts_forward(int64_t T, int64_t E, int64_t k, int64_t D, 
  *   dW_out[e] = sum over its rows grad_t (w h)^T
  *
  * dg, du and w h are rounded to dtype on their way into the products, each output once.
- * fp16: dg and du times a power of two of their expert, which brings the largest finite one
- * to 2^14 or more; all bits are kept of what is above 2^-28 of that, and 2^-39 of it is half
- * of the smallest step.
+ * fp16: times two powers of two of their expert, which bring the largest finite |dg| or |du|
+ * and the largest finite |w h| to 2^14 or more; all bits are kept of what is above 2^-28 of that,
+ * and 2^-39 of it is half of the smallest step.
  * dx, dW_in, dW_out (pitches as the operands') and d_weights: any may be NULL when
  * it is not wanted; an expert without rows gets zeros. */
 TGEMM_API int tgemm_experts_backward(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F,

@@ -7,8 +7,8 @@ With u half a step of the operands' type (2^-9 of bf16's, 2^-12 of fp16's leadin
   (16 terms) of a chunk, and by 2^-24 for each addition of a chunk;
 * g and u inherit that, h = silu(g) u as in tests/experts_reference.py (|silu'| <= 1.1, |silu''| <= 0.5, 2^-20 for its
   exponential, division and products);
-* fp16's dg and du are rounded with a power of two of their expert that brings the largest finite one to 2^14 or more:
-  half of the smallest step, 2^-25, is then 2^-39 of the largest; w h is rounded as it is;
+* fp16's dg, du and w h are rounded with a power of two of their expert that brings the largest finite one to 2^14 or more:
+  half of the smallest step, 2^-25, is then 2^-39 of the largest;
 * bf16 rows on their way to a token's sum are off by 2^-12 of each, or by 2^-9 where an element of the same 32 is
   smaller than 2^-27 of the largest;
 * every output is rounded once.
@@ -75,7 +75,7 @@ class Numbers:
             self.dw[t, j] = (h * v).sum(dim=1)
             self.e_dw[t, j] = (h.abs() * e_v + (e_h0 + 2.0 ** -20 * h.abs()) * v.abs()).sum(dim=1)
             dg, du, wh = w * v * up * slope, w * v * silu, w * h
-            small, small_h = (2.0 ** -38.9 * finite_most(dg, du), 2.0 ** -25) if half else (0.0, 0.0)
+            small, small_h = (2.0 ** -38.9 * finite_most(dg, du), 2.0 ** -38.9 * finite_most(wh)) if half else (0.0, 0.0)
             e_dg = w.abs() * (e_v * (up * slope).abs() + v.abs() * (slope.abs() * e_u + 0.5 * up.abs() * e_g)) + \
                 (unit + 2.0 ** -20) * dg.abs() + 2.0 ** -20 * (w * v * up).abs() + small
             e_du = w.abs() * (e_v * silu.abs() + 1.1 * v.abs() * e_g) + (unit + 2.0 ** -20) * du.abs() + small

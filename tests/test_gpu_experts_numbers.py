@@ -78,6 +78,34 @@ def test_fp16_gradients_whatever_the_output_weights_are(size, odd):
     check((x.float() * math.sqrt(max(1.0, b))).half(), w_in, (w_out.float() * a * min(1.0, b)).half(), ids, weights, (g.float() / 64).half())
 
 
+@pytest.mark.parametrize("w", [1e-2, 1e-5, 1e-6, 1e-9])
+def test_fp16_places_of_small_weight_keep_their_gradients(w):
+    """w h below fp16's numbers: dW_out, with gradients of size 64, is well within them."""
+    x, w_in, w_out, ids, _, g, _ = layer(300, 3, 2, 128, 96, F16)
+    got = check((3 * x.float()).half(), w_in, w_out, ids, torch.full((300, 2), w, device="cuda"), (640 * g.float()).half())
+    want = Numbers((3 * x.float()).half(), w_in, w_out, ids, torch.full((300, 2), w, device="cuda"), (640 * g.float()).half())
+    if w >= 1e-6:  # in the norm: w h's rounding and the last one, each below half a step
+        off = (got["dw_out"].double() - want.dw_out).norm() / want.dw_out.norm()
+        assert float(off) <= 2.0 ** -11, float(off)
+
+
+def test_fp16_rows_and_experts_of_very_different_weight():
+    """Rows and experts whose gradients lie 2^-20 apart: each row's dx and each expert's dW keep their bits."""
+    x, w_in, w_out, ids, _, g, normal = layer(400, 4, 1, 128, 96, F16)
+    ids = torch.arange(400, device="cuda")[:, None] % 4
+    weights = torch.ones(400, 1, device="cuda")
+    weights[ids == 1] = 2.0 ** -20
+    weights[ids == 2] = 2.0 ** -30
+    weights[ids == 3] = 2.0 ** -20
+    weights[3:100:4] = 1.0  # expert 3: both kinds
+    g = (640 * g.float()).half()
+    got = check(x, w_in, w_out, ids, weights, g)
+    want = Numbers(x, w_in, w_out, ids, weights, g)
+    large = want.dx.abs().amax(dim=1) >= 2.0 ** -12  # rows whose dx fp16 holds with all bits
+    off = (got["dx"].double() - want.dx).norm(dim=1) / want.dx.norm(dim=1)
+    assert int(large.sum()) > 100 and float(off[large].max()) <= 2.0 ** -10
+
+
 def test_fp16_rows_beside_an_infinite_gradient():
     """A row whose gradient is infinite takes nothing from the other rows and the other experts."""
     x, w_in, w_out, ids, weights, g, _ = layer(130, 4, 1, 128, 96, F16)

@@ -379,7 +379,7 @@ class Experts {
       a_.v = reinterpret_cast<float*>(ws_ + l_.v);
       a_.largest = reinterpret_cast<unsigned int*>(ws_ + l_.largest);
     }
-    TGEMM_TRY(gather(c_.grad, c_.ldg, ws_ + l_.x, a_.largest, a_.E));
+    TGEMM_TRY(gather(c_.grad, c_.ldg, ws_ + l_.x, a_.largest, 2 * a_.E));
     {
       ExpertArgs a = a_;
       TGEMM_TRY(map_transposed(m, a, w_out_, c_.F, c_.D));

@@ -351,9 +351,10 @@ __device__ __forceinline__ uint32_t larger_finite(uint32_t most, float x) {
   return size < 0x7F800000u ? max(most, size) : most;
 }
 
-// The same for fp16 operands: v in fp32, 16 bytes a lane, and the largest finite |dg| or |du| so far.
+// The same for fp16 operands: v in fp32, 16 bytes a lane, and the largest finite |dg|, |du| and
+// |w h| so far.
 __device__ __forceinline__ void finish_v(const uint32_t (&v)[8], const ExpertArgs& a, int feature, int64_t row, int valid,
-                                         int lane, float mine, int first, int part, int parts, uint32_t& most) {
+                                         int lane, float mine, int first, int part, int parts, uint32_t (&most)[2]) {
   HiddenColumns x(v, a, feature, row, valid);
   if (feature < a.F) {
     float4* to = reinterpret_cast<float4*>(a.v) + row / 4 * a.ldg + feature;
@@ -364,7 +365,8 @@ __device__ __forceinline__ void finish_v(const uint32_t (&v)[8], const ExpertArg
   for (int c = 0; c < 8; ++c) {
     const float w = __shfl_sync(0xffffffffu, mine, first + c);
     const GatedGradient d = gated_gradient(x.g[c], x.u[c], w * x.d[c]);
-    most = larger_finite(larger_finite(most, d.dg), d.du);
+    most[0] = larger_finite(larger_finite(most[0], d.dg), d.du);
+    most[1] = larger_finite(most[1], w * d.h);
     x.d[c] *= d.h;
   }
   finish_dots(x.d, a, row, valid, lane, part, parts);
@@ -719,7 +721,8 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
       if (!ok) break;
       next = units.get(args, i + workers);  // under this epilogue; no register is its beside the sums
       float unscale = 1.0f;  // of the expert's fp16 gradients
-      if ((MODE == EXPERT_DIN || MODE == EXPERT_DX) && args.largest) unscale = expert_unscale(__ldcg(args.largest + u.expert));
+      if ((GRADIENT || MODE == EXPERT_DX) && args.largest)
+        unscale = expert_unscale(__ldcg(args.largest + 2 * u.expert + (MODE == EXPERT_DOUT ? 1 : 0)));
       if constexpr (GRADIENT) {
         const int M = MODE == EXPERT_DIN ? 2 * args.F : args.D, N = MODE == EXPERT_DIN ? args.D : args.F;
         finish_weight(tcol, stages > 0, args, u.expert, u.mb * 256 + cta * kTileM + quarter * 32, M,
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
                      : 0.0f;
         };
         float ahead = MODE == EXPERT_DH ? weight_of(0) : 0.0f;
-        uint32_t most = 0u;
+        uint32_t most[2] = {0u, 0u};
         constexpr bool JOINED = MODE == EXPERT_DOWN || MODE == EXPERT_DX;
         if (JOINED && args.bf16) {
           // two blocks at a time: their chains of reductions and exchanges run side by side
@@ -792,8 +795,11 @@ __global__ void __launch_bounds__(expert_threads(PARTS), 1)
         }
         given_back();
         if (MODE == EXPERT_DH && args.v) {  // a maximum is the same in whatever order
-          const uint32_t all = __reduce_max_sync(0xffffffffu, most);
-          if (lane == 0 && all) atomicMax(args.largest + u.expert, all);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t all = __reduce_max_sync(0xffffffffu, most[i]);
+            if (lane == 0 && all) atomicMax(args.largest + 2 * u.expert + i, all);
+          }
         }
       }
     }

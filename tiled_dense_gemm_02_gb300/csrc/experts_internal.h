@@ -60,8 +60,8 @@ cudaError_t launch_gather_rows(const ExpertRows& rows, int64_t most_rows, const 
                                void* out, int64_t ld_out, unsigned int* zeros, int words, int sms, cudaStream_t stream);
 
 // fp16 gradients on their way into the products: from v = W_out^T grad in fp32 (as DH leaves
-// it), g and u, the rows of dg and du in halves, times the power of two of their expert
-// (expert_scale), and of weight * h.  The filling is 0.
+// it), g and u, the rows of dg, du and weight * h in halves, times the powers of two of their
+// expert (expert_scale).  The filling is 0.
 struct RoundArgs {
   int E, F;
   ExpertRows rows;
@@ -69,7 +69,7 @@ struct RoundArgs {
   const float* gu;               // [row / 4][g, u][feature, pitch ldg][row % 4]
   const float* v;                // [row / 4][feature, pitch ldg][row % 4]
   int64_t ldg;
-  const unsigned int* largest;   // of each expert: |dg| or |du|, floats' bits
+  const unsigned int* largest;   // of each expert: {|dg|, |du|; |weight h|}, floats' bits
   void* dgu;
   int64_t ld_dgu;
   void* h;
@@ -161,8 +161,8 @@ struct ExpertArgs {
   float* dots;             // DH: m_blocks * 8 per row
   const float* weights;    // DH: of each place
   // fp16, else null: DH leaves v = W_out^T grad in fp32 and each expert's largest finite numbers
-  // (RoundArgs), from which launch_round_gradients makes dgu and h; DX and DIN take the powers of
-  // two back
+  // (RoundArgs), from which launch_round_gradients makes dgu and h; DX, DIN and DOUT take the
+  // powers of two back
   float* v;
   unsigned int* largest;
   void* y;                 // DOWN, DX: fp32, or (bf16) halves with an exponent for each 32 columns (JoinArgs)

@@ -422,8 +422,8 @@ __device__ __forceinline__ uint32_t pair_of(float x, float y) {
 }
 
 // ------------------------------------------------------- fp16 gradients rounded
-// dg and du in halves, after their largest ones are known: a scale from the gradient alone
-// leaves infinities where W_out or u are large and nothing where weights are small, since
+// dg, du and w h in halves, after their largest ones are known: a scale from the gradient alone
+// (or none) leaves infinities where W_out or u are large and nothing where weights are small, since
 // dg = w v u silu'(g) with v a sum over D.  The largest of an expert at 2^14 keeps all bits of
 // what is above 2^-28 of it.  A block has 32 rows (of one expert) and kRoundFeatures features, a warp
 // four rows and a lane two neighbouring features.  Bound by bytes: v, g and u are read, 12
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kRoundThreads) round_kernel(const __grid_const
   for (int e = threadIdx.x; e < a.E; e += kRoundThreads)
     if (__ldcg(a.rows.first + e) <= row0 && row0 < __ldcg(a.rows.first + e + 1)) owner = e;
   __syncthreads();
-  const float scale = expert_scale(__ldcg(a.largest + owner));
+  const float scale = expert_scale(__ldcg(a.largest + 2 * owner)), scale_h = expert_scale(__ldcg(a.largest + 2 * owner + 1));
   const int lane = threadIdx.x & 31;
   const int64_t row = row0 + (threadIdx.x >> 5) * 4;
   float w[4];
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kRoundThreads) round_kernel(const __grid_const
         const GatedGradient d = gated_gradient(gs[r], us[r], w[r] * vs[r]);
         dg[i][r] = used[r] ? scale * d.dg : 0.0f;
         du[i][r] = used[r] ? scale * d.du : 0.0f;
-        wh[i][r] = used[r] ? w[r] * d.h : 0.0f;
+        wh[i][r] = used[r] ? scale_h * (w[r] * d.h) : 0.0f;
       }
     }
 #pragma unroll
