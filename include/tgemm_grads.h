@@ -18,8 +18,8 @@
  *
  * Clipping writes x * (max_norm / norm) where norm > max_norm, else x: the factor
  * is one fp32 number, the product is rounded once to the output's type.  A norm
- * that is infinite or NaN scales nothing (x as it is): look at norm, and skip the
- * step.
+ * that is infinite or NaN as it is returned (also one past fp32's largest number) scales
+ * nothing (x as it is): look at norm, and skip the step.
  *
  * Errors: TGEMM_ERR_INVALID_VALUE for n < 0, a negative count, a null list or
  * pointer (of a tensor that has elements), a max_norm that is negative or NaN, a

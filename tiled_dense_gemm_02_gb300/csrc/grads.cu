@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_kernel(const __g
   ptx::griddep_wait();
   const double total = norm_of(partial, n, shared);
   if (first && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
-  const bool clips = total > static_cast<double>(max_norm) && total < INFINITY;
+  // by the norm that the caller sees: past fp32's largest number it is infinite
+  const bool clips = total > static_cast<double>(max_norm) && static_cast<float>(total) < INFINITY;
   const float f = clips ? static_cast<float>(static_cast<double>(max_norm) / total) : 1.0f;
   const int last = l.chunks - 1;
   for (int c = last - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
