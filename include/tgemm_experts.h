@@ -160,7 +160,7 @@ TGEMM_API int tgemm_experts_forward(int64_t T, int64_t E, int64_t k, int64_t D, 
  * and the largest finite |w h| to 2^14 or more; all bits are kept of what is above 2^-28 of that,
  * and 2^-39 of it is half of the smallest step.
  * dx, dW_in, dW_out (pitches as the operands') and d_weights: any may be NULL when
- * it is not wanted; an expert without rows gets zeros. */
+ * it is not wanted, and the others are the same bits; an expert without rows gets zeros. */
 TGEMM_API int tgemm_experts_backward(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F,
                const void* x, int64_t ldx, const void* W_in, int64_t ld_in, const void* W_out, int64_t ld_out,
                const float* weights, const void* saved, size_t saved_bytes, const void* grad, int64_t ldg,

@@ -120,3 +120,18 @@ def test_fp16_rows_beside_an_infinite_gradient():
     want = Numbers(x, w_in, w_out, ids, weights, torch.where(bad[:, None], torch.zeros_like(g), g))
     want.check(rows=~bad, experts=keep, **got)
     assert not bool(got["dx"][bad].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=NAMES.get)
+@pytest.mark.parametrize("D,F", [(600, 70), (1100, 300)])
+def test_gradients_do_not_depend_on_which_are_asked_for(D, F, dtype):
+    """Freezing a router, or some weights, leaves the other gradients' bits: sums of several chunks."""
+    x, w_in, w_out, ids, weights, g, _ = layer(300, 4, 2, D, F, dtype, seed=D)
+    names = ("dx", "dw_in", "dw_out", "dw")
+    want = gradients(x, w_in, w_out, ids, weights, g)
+    for mask in range(1, 15):
+        wants = dict(zip(("want_hidden", "want_in", "want_out", "want_weights"), [bool(mask >> i & 1) for i in range(4)]))
+        got = gradients(x, w_in, w_out, ids, weights, g, **wants)
+        assert set(got) == {"out"} | {n for i, n in enumerate(names) if mask >> i & 1}
+        for name, v in got.items():
+            assert torch.equal(v, want[name]), (mask, name)

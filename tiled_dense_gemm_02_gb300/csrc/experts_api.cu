@@ -387,7 +387,7 @@ class Experts {
       m.c = m.b;
       a.m_blocks = static_cast<int>(ceil_div(c_.F, 256));
       a.k_blocks = static_cast<int>(ceil_div(c_.D, kTileK));
-      a.chunk = c_.d_weights ? exact_chunk() : kChunk;  // dg, du and w h are 16-bit
+      a.chunk = exact_chunk();  // whichever gradients are wanted: the others' bits stay
       TGEMM_TRY(launch(launch_expert_dh, m, a, tokens(a)));
     }
     if (type_ == 1 && (c_.dx || c_.dw_in || c_.dw_out)) TGEMM_TRY(round_gradients());

@@ -404,8 +404,8 @@ def expert_mlp_backward(hidden, w_in, w_out, ids, weights, saved, grad_out, *, w
     """Gradients ``(d_hidden, d_w_in, d_w_out, d_weights)`` of ``sum(grad_out *
     out)``: in the operands' type, d_weights in float32.  saved from the forward
     call with the same operands; grad_out [T, D] in their type, unit column stride.  An
-    unwanted gradient is not computed (None).  What it returns is outside
-    torch's graph."""
+    unwanted gradient is not computed (None), the others are the same bits.  What it
+    returns is outside torch's graph."""
     torch, device, sizes, code, matrices, ids, weights, workspace, need = \
         _experts(hidden, w_in, w_out, ids, weights, True, workspace)
     T, E, k, D, F = sizes
