@@ -1,0 +1,48 @@
+"""The tensor functions of a sparse layer and torch's graphs, on the host: what a backward pass reads, what forward
+mode is told, and what is written in place.  No call here reaches the GPU."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def tg():
+    from tests.conftest import build_library
+    build_library()
+    import tiled_dense_gemm_02_gb300 as tg
+    return tg
+
+
+@pytest.fixture
+def on_host(tg, monkeypatch):
+    """The functions on host tensors with the library's calls left out: `calls` lists their arguments."""
+    from tiled_dense_gemm_02_gb300 import experts, grads, loss
+    calls = []
+
+    def guarded(torch, device, function, args):
+        calls.append((function.__name__, args))
+        return tg.OK
+
+    for module in (experts, grads, loss):
+        monkeypatch.setattr(module, "_guarded", guarded)
+        monkeypatch.setattr(module, "_current_stream", lambda torch, device: 0)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    return calls
+
+
+def route_options(args):
+    from tiled_dense_gemm_02_gb300 import RouteOptions
+    return next(a._obj for a in args if hasattr(a, "_obj") and isinstance(a._obj, RouteOptions))
+
+
+def test_routing_options_that_change_before_the_backward_pass(tg, on_host):
+    """A scale or a flag held in a tensor: the gradient is that of the weights that were given."""
+    logits = torch.randn(4, 8).requires_grad_()
+    scale, renormalize = torch.tensor(2.0), torch.tensor(False)
+    _, weights = tg.route_experts(logits, 2, scoring="sigmoid", scale=scale, renormalize=renormalize)
+    scale.fill_(3.0)
+    renormalize.fill_(True)
+    weights.sum().backward()
+    (first, forward), (then, backward) = on_host
+    assert (first, then) == ("tgemm_route_forward", "tgemm_route_backward")
+    for o in (route_options(forward), route_options(backward)):
+        assert (o.scoring, o.scale, o.renormalize) == (1, 2.0, 0)

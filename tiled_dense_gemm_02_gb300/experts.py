@@ -231,8 +231,9 @@ def route_experts(logits, top_k, *, scoring="softmax", bias=None, groups=1, top_
         if torch.is_grad_enabled() and bias is not None and bias.requires_grad:
             raise ValueError("bias gets no gradient: detach it")
         if torch.is_grad_enabled():
+            # the backward call's options are the plain numbers of this one: a tensor may have changed by then
             return _route_node().apply(logits, top_k, bias, options,
-                                       {"scoring": scoring, "renormalize": renormalize, "scale": scale})
+                                       {"scoring": scoring, "renormalize": bool(options[1]), "scale": options[2]})
     return _route(logits, top_k, bias, options)
 
 
