@@ -46,3 +46,35 @@ def test_routing_options_that_change_before_the_backward_pass(tg, on_host):
     assert (first, then) == ("tgemm_route_forward", "tgemm_route_backward")
     for o in (route_options(forward), route_options(backward)):
         assert (o.scoring, o.scale, o.renormalize) == (1, 2.0, 0)
+
+
+def operands(T=4, E=3, k=2, D=8, F=16):
+    return (torch.randn(T, D).bfloat16(), torch.randn(E, 2 * F, D).bfloat16(), torch.randn(E, D, F).bfloat16(),
+            torch.zeros(T, k, dtype=torch.int64), torch.rand(T, k))
+
+
+def test_tangents_of_forward_mode_are_refused(tg, on_host):
+    """There is no forward-mode gradient: a dual tensor must not lose its tangent without a word."""
+    from torch.autograd import forward_ad
+    args = operands()
+    logits, bias = torch.randn(4, 8), torch.randn(8)
+    y, lists = torch.zeros(4, dtype=torch.int64), (torch.zeros(4, 2, dtype=torch.int64), torch.randn(4, 2))
+    weight = torch.randn(10, 8).bfloat16()
+    with forward_ad.dual_level():
+        def dual(t):
+            return forward_ad.make_dual(t, torch.ones_like(t))
+
+        for i in (0, 1, 2, 4):
+            with pytest.raises(RuntimeError, match="forward"):
+                tg.expert_mlp(*[dual(a) if j == i else a for j, a in enumerate(args)])
+        for call in (lambda: tg.route_experts(dual(logits), 2), lambda: tg.route_experts(logits, 2, bias=dual(bias)),
+                     lambda: tg.linear_cross_entropy(dual(args[0]), weight, y), lambda: tg.linear_cross_entropy(args[0], dual(weight), y),
+                     lambda: tg.linear_distillation(dual(args[0]), weight, *lists), lambda: tg.linear_distillation(args[0], dual(weight), *lists),
+                     lambda: tg.linear_distillation(args[0], weight, lists[0], dual(lists[1]))):
+            with pytest.raises(RuntimeError, match="forward"):
+                call()
+        assert on_host == []
+        tg.expert_mlp(*args)  # tensors without a tangent
+        tg.route_experts(logits, 2, bias=bias)
+        tg.linear_cross_entropy(args[0], weight, y)
+    assert len(on_host) == 3

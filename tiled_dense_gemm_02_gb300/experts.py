@@ -13,7 +13,7 @@ import math
 from operator import index
 
 from . import BF16, F16, F32, OK, TgemmError, library
-from .loss import _current_stream, _guarded, _on_stream, _pitch
+from .loss import _current_stream, _guarded, _no_tangents, _on_stream, _pitch
 
 ROUTE_MAX_EXPERTS, ROUTE_MAX_K, ROUTE_MAX_GROUPS = 1024, 32, 32  # TGEMM_ROUTE_MAX_*
 ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1                              # enum tgemm_route_scoring
@@ -223,8 +223,10 @@ def route_experts(logits, top_k, *, scoring="softmax", bias=None, groups=1, top_
     the experts' products pass over.  logits in bf16, fp16 or fp32, any row
     stride; up to 1024 experts, 32 picks, 32 groups.
 
-    If logits requires a gradient, so do the weights; the picks have none.
+    If logits requires a gradient, so do the weights; the picks have none.  Forward-mode
+    tangents are refused.
     """
+    _no_tangents(logits, bias)
     options = _read(scoring, renormalize, scale, groups, top_groups, group_score)
     if logits.requires_grad or (bias is not None and bias.requires_grad):
         import torch
@@ -391,7 +393,9 @@ def expert_mlp(hidden, w_in, w_out, ids, weights, *, save=False, workspace=None)
     order, the rows in it, g and u in float32); otherwise saved is None.  If
     hidden, a weight or weights requires a gradient, so does out, torch's
     backward pass makes the backward call, and saved is kept in any case.
+    Forward-mode tangents are refused.
     """
+    _no_tangents(hidden, w_in, w_out, weights)
     if hidden.requires_grad or w_in.requires_grad or w_out.requires_grad or weights.requires_grad:
         import torch
         if torch.is_grad_enabled():

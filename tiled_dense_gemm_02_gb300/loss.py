@@ -260,6 +260,16 @@ def _graph_node():
     return HeadLoss
 
 
+def _no_tangents(*tensors):
+    """Refuses forward-mode duals: there is no forward-mode gradient, and the library would read past a tangent."""
+    from torch.autograd import forward_ad
+    if getattr(forward_ad, "_current_level", 0) < 0:  # not in forward mode
+        return
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError("there is no forward-mode gradient: unpack the dual tensor")
+
+
 def _recorded(hidden, weight):
     """Whether a loss of these tensors belongs to torch's graph."""
     if not (hidden.requires_grad or weight.requires_grad):
@@ -281,7 +291,9 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, scale=1.
 
     If hidden or weight requires a gradient, so does ``loss``, and torch's
     backward pass makes the backward call; ``lse`` has no gradient of its own.
+    Forward-mode tangents are refused.
     """
+    _no_tangents(hidden, weight)
     options = _plain(scale, label_smoothing, z_loss, piece, ignore_index)
     if _recorded(hidden, weight):
         more = dict(zip(("scale", "label_smoothing", "z_loss", "piece", "ignore_index"), options))
@@ -347,8 +359,9 @@ def linear_distillation(hidden, weight, teacher_ids, teacher_logits, *, temperat
     0.  The losses are not multiplied by temperature squared.
 
     Gradients of hidden and weight through torch as in linear_cross_entropy;
-    teacher_logits have none and must not require one.
+    teacher_logits have none and must not require one.  Forward-mode tangents are refused.
     """
+    _no_tangents(hidden, weight, teacher_logits)
     if teacher_logits.requires_grad:
         import torch
         if torch.is_grad_enabled():
