@@ -78,3 +78,29 @@ def test_tangents_of_forward_mode_are_refused(tg, on_host):
         tg.route_experts(logits, 2, bias=bias)
         tg.linear_cross_entropy(args[0], weight, y)
     assert len(on_host) == 3
+
+
+def test_what_is_clipped_in_place_is_seen_as_changed(tg, on_host):
+    """torch's graph notices that a tensor which it keeps was written."""
+    a, b, c = torch.randn(5), torch.randn(7).half(), torch.randn(3)
+    before = [t._version for t in (a, b, c)]
+    tg.gradient_norm([a, b])
+    assert [t._version for t in (a, b, c)] == before
+    tg.clip_gradients([a, b], 1.0)
+    assert a._version > before[0] and b._version > before[1]
+    seen = a._version
+    tg.clip_gradients([a], 1.0, outputs=[torch.empty(5)])
+    assert a._version == seen
+    out = torch.empty(5)
+    seen = out._version
+    tg.clip_gradients([a], 1.0, outputs=[out])
+    assert out._version > seen
+    with torch.inference_mode():
+        kept = torch.randn(4)
+    tg.clip_gradients([kept, c], 1.0)  # has no counter
+    assert c._version > before[2]
+    x = torch.randn(5, requires_grad=True)
+    y = (x * a).sum()
+    tg.clip_gradients([a], 1.0)
+    with pytest.raises(RuntimeError, match="modified"):
+        y.backward()

@@ -122,6 +122,8 @@ def _run(tensors, outputs, max_norm, workspace, stream):
         st = _guarded(torch, device, grad_norm, (pointers, counts, kinds) + more)
     else:
         st = _guarded(torch, device, grad_clip, (pointers, counts, kinds, places, max_norm) + more)
+        if st == OK:  # torch's graph is told what was written past it
+            torch.autograd.graph.increment_version(tensors if outputs is None else outputs)
     if st != OK:
         raise TgemmError(st, "tgemm_grad_norm" if max_norm is None else "tgemm_grad_clip")
     return norm
@@ -155,7 +157,8 @@ def clip_gradients(gradients, max_norm, *, outputs=None, workspace=None, stream=
 
     The host does not wait.  A norm that is infinite or NaN scales nothing: the
     caller looks at it and skips the step.  In place, a tensor may be listed
-    only once.
+    only once.  Neither the norm nor outputs are part of torch's graph, which does notice
+    that the tensors were written.
     """
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
