@@ -135,3 +135,15 @@ def test_gradients_do_not_depend_on_which_are_asked_for(D, F, dtype):
         assert set(got) == {"out"} | {n for i, n in enumerate(names) if mask >> i & 1}
         for name, v in got.items():
             assert torch.equal(v, want[name]), (mask, name)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=NAMES.get)
+@pytest.mark.parametrize("F", [1, 40, 300])
+def test_an_infinite_gradient_gives_an_infinite_weight_gradient(F, dtype):
+    """Positive numbers all: d_weights is +inf where one gradient is, at widths that do not fill the tiles."""
+    x, w_in, w_out, ids, weights, g, _ = layer(50, 2, 1, 64, F, dtype)
+    g = g.abs()
+    g[3, 5] = math.inf
+    got = gradients(x.abs(), w_in.abs(), w_out.abs(), ids, weights, g)
+    assert float(got["dw"][3, 0]) == math.inf
+    assert bool(got["dw"][torch.arange(50, device="cuda") != 3].isfinite().all())

@@ -269,8 +269,9 @@ __device__ __forceinline__ void finish_up(const uint32_t (&v)[16], const ExpertA
   }
 }
 
-// 8 columns of DH: v = d_out W_out of this lane's feature, with g and u (0 in the filling,
-// whatever the weights hold).
+// 8 columns of DH: v = d_out W_out of this lane's feature, with g and u.  0 in the filling,
+// whatever the weights hold, and past the last feature, where the weights are 0 and an infinite
+// gradient makes NaN of their product, which has no part in the row's dot.
 struct HiddenColumns {
   float g[8], u[8], d[8];
   __device__ __forceinline__ HiddenColumns(const uint32_t (&v)[8], const ExpertArgs& a, int feature, int64_t row, int valid) {
@@ -289,10 +290,11 @@ struct HiddenColumns {
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c) d[c] = __uint_as_float(v[c]);
-    if (valid < 8) {
+    const int there = feature < a.F ? valid : 0;
+    if (there < 8) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        if (c >= valid) g[c] = u[c] = d[c] = 0.0f;
+        if (c >= there) g[c] = u[c] = d[c] = 0.0f;
       }
     }
   }
