@@ -41,7 +41,8 @@
  * the tensor cores with fp32 sums, h is rounded to the operands' type on its way
  * into the second product (fp16's largest number is 65504: a larger h is infinite),
  * and out, summed in fp32, is rounded once.  bf16 rows W_out[e] h lie in the workspace as
- * halves with a power of two for each 32 elements, 2^-12 of each at most.  The tensor cores'
+ * halves with a power of two for each 32 elements, 2^-12 of each at most, or, where one of the
+ * 32 is below 2^-28 of their largest, as bf16: 2^-9 of each.  The tensor cores'
  * adder truncates: 256 steps of 16 products at a time stay within 2^-15 of the sum of
  * magnitudes, however long the axis; where the backward call follows, 16 steps: g and u are
  * within 2^-18.  Calls of a few places (up to 32, by their number and the weights' size) read

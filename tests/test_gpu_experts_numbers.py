@@ -147,3 +147,24 @@ def test_an_infinite_gradient_gives_an_infinite_weight_gradient(F, dtype):
     got = gradients(x.abs(), w_in.abs(), w_out.abs(), ids, weights, g)
     assert float(got["dw"][3, 0]) == math.inf
     assert bool(got["dw"][torch.arange(50, device="cuda") != 3].isfinite().all())
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_bf16_neighbours_of_very_different_size(T):
+    """Elements of out and dx far below their neighbours in a row, which bf16 holds: they keep their own bits."""
+    E, D, F = 3, 200, 96
+    x, w_in, w_out, ids, weights, g, normal = layer(T, E, 2, D, F, BF16, seed=T)
+    sizes = torch.tensor([0.0, 0.0, -12.0, -26.0, -29.0, -33.0, -41.0, -45.0, -80.0, 20.0], device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    scale = torch.exp2(sizes[torch.randint(0, 10, (D,), device="cuda", generator=gen)])
+    scale[32:64] = 1.0
+    scale[33] = 0.0
+    w_out = (w_out.float() * scale[:, None]).bfloat16()
+    w_in = (w_in.float() * scale.clamp_max(1.0)).bfloat16()
+    got = check(x, w_in, w_out, ids, weights, g)
+    assert bool((got["out"][:, 33] == 0).all())
+    want = Numbers(x, w_in, w_out, ids, weights, g)
+    for name in ("out", "dx"):  # the bounds tell them from 0: half of the elements are above twice theirs
+        assert float(((getattr(want, name).abs() > 2 * getattr(want, "e_" + name)).float().mean(dim=0) >= 0.5).float().mean()) > 0.9
+    plain = H.tg().expert_mlp(x, w_in, w_out, ids, weights)[0]
+    Numbers(x, w_in, w_out, ids, weights, g, train=False).check(out=plain)

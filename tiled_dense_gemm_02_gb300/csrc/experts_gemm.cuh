@@ -388,9 +388,10 @@ __device__ __forceinline__ void finish_y(const uint32_t (&v)[16], const ExpertAr
 
 // The same for bf16 operands: halves, with one power of two for a row's 32 neighbours that
 // brings the largest finite one to [2^14, 2^15).  A half's 11 bits are off by 1.4e-4 on
-// average (values below 2^-28 of the largest by more), which beside h's rounding and the
-// result's (1.65e-3 each) is 0.2 % of the error; y's bytes, written here and read by the
-// join, are what DOWN's epilogue costs (8192 tokens, 64 experts, fp32: join 94 us, 53 so).
+// average, which beside h's rounding and the result's (1.65e-3 each) is 0.2 % of the error; y's
+// bytes, written here and read by the join, are what DOWN's epilogue costs (8192 tokens, 64
+// experts, fp32: join 94 us, 53 so).  Where one of the 32 is no 0 and below 2^-28 of the largest, and
+// would lose bits as a half, they are stored as bf16, with its range, under the exponent 0.
 // y: the block's words in shared memory; own: the lane's feature in the CTA.
 __device__ __forceinline__ void row_sizes(const uint32_t (&v)[16], uint32_t (&most)[16]) {
   uint32_t all = 0u;
@@ -411,16 +412,32 @@ template <typename Staged>
 __device__ __forceinline__ void finish_y_half(const uint32_t (&v)[16], const uint32_t (&most)[16], const ExpertArgs& a,
                                               int d, int64_t row, int lane, int own, bool there, uint8_t* y) {
   uint32_t exponents[4] = {0u, 0u, 0u, 0u};
+  float f[16], least = INFINITY;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const uint32_t exponent = max(15u, most[c] >> 23);
+    exponents[c / 4] |= exponent << (8 * (c & 3));
+    f[c] = __uint_as_float((268u - exponent) << 23) * __uint_as_float(v[c]);
+    least = fminf(least, fabsf(f[c]));
+  }
+  uint32_t wide = 0u;  // the rows in bf16
+  if (__any_sync(0xffffffffu, least < 0x1p-14f)) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (__any_sync(0xffffffffu, (v[c] & 0x7FFFFFFFu) != 0u && fabsf(f[c]) < 0x1p-14f)) {
+        wide |= 1u << c;
+        exponents[c / 4] &= ~(0xFFu << (8 * (c & 3)));
+      }
+  }
 #pragma unroll
   for (int c = 0; c < 16; c += 2) {
-    float f[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t exponent = max(15u, most[c + e] >> 23);
-      exponents[(c + e) / 4] |= exponent << (8 * ((c + e) & 3));
-      f[e] = __uint_as_float((268u - exponent) << 23) * __uint_as_float(v[c + e]);
+    uint32_t word = pack_pair(f[c], f[c + 1], OUT_F16);
+    if (wide) {
+      const uint32_t plain = pack_pair(__uint_as_float(v[c]), __uint_as_float(v[c + 1]), OUT_BF16);
+      const uint32_t mask = (wide >> c & 1u ? 0xFFFFu : 0u) | (wide >> (c + 1) & 1u ? 0xFFFF0000u : 0u);
+      word = (word & ~mask) | (plain & mask);
     }
-    Staged::put(y, pack_pair(f[0], f[1], OUT_F16), c, own, lane);
+    Staged::put(y, word, c, own, lane);
   }
   if (there && lane < 16 && d - lane < a.ldy) {
     const uint32_t word = lane < 8 ? (lane < 4 ? exponents[0] : exponents[1]) : (lane < 12 ? exponents[2] : exponents[3]);

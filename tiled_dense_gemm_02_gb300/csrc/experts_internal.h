@@ -99,7 +99,7 @@ struct JoinArgs {
   const float* weights;
   int64_t T;
   int k, D;
-  const void* y;        // fp32, or (type 0) halves times 2^(e - 141), e = y_exponent of 32 columns
+  const void* y;        // fp32, or (type 0) halves times 2^(e - 141), e = y_exponent of 32 columns; e = 0: bf16
   const uint8_t* y_exponent;
   int64_t ldy;
   int type;

@@ -540,12 +540,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         const uint4 v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.y) + row * a.ldy + d));
         const uint32_t p[4] = {v.x, v.y, v.z, v.w};
         const uint32_t e = __ldcg(a.y_exponent + (row / 16 * (a.ldy / 32) + d / 32) * 16 + row % 16);
-        w *= __uint_as_float((e - 14u) << 23);
+        if (e != 0u) {
+          w *= __uint_as_float((e - 14u) << 23);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-          y[2 * i] = f.x;
-          y[2 * i + 1] = f.y;
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+            y[2 * i] = f.x;
+            y[2 * i + 1] = f.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[2 * i] = __uint_as_float(p[i] << 16);
+            y[2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
+          }
         }
       } else {
         const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.y) + row * a.ldy + d);
