@@ -43,16 +43,19 @@
  * and out, summed in fp32, is rounded once.  bf16 rows W_out[e] h lie in the workspace as
  * halves with a power of two for each 32 elements, 2^-12 of each at most, or, where one of the
  * 32 is below 2^-28 of their largest, as bf16: 2^-9 of each.  The tensor cores'
- * adder truncates: 256 steps of 16 products at a time stay within 2^-15 of the sum of
- * magnitudes, however long the axis; where the backward call follows, 16 steps: g and u are
- * within 2^-18.  Calls of a few places (up to 32, by their number and the weights' size) read
+ * adder truncates, by less than 2^-23 of the sum of magnitudes a step of 16 products.  Sums of
+ * up to 256 steps are added in fp32: 2^-15, and 2^-24 more for every 4096 products.
+ * Where the backward call follows, of up to 16 steps (fp16 12): g, u and the gradient of h
+ * are within 2^-19, and 2^-24 more for every 256 products (fp16 192), 2^-18 together for 8192
+ * (6144).  Calls of a few places (up to 32, by their number and the weights' size) read
  * the weights place by place on the CUDA cores, with h in fp32.  A place whose
  * id is below 0 is unused; a row without a used place gives 0 (and x may hold
  * anything there, NaN included).  An id of E or more is an error in the data: its
  * row of out is NaN, and so are its row of dx and its place of dweights; it has no
  * part in any other gradient.  An expert listed twice counts twice.
  *
- * Results do not depend on timing: every sum has a fixed order, no atomics.
+ * Results do not depend on timing: every sum has a fixed order, and the only atomics are
+ * counts and maxima.
  */
 #ifndef TGEMM_EXPERTS_H
 #define TGEMM_EXPERTS_H

@@ -168,3 +168,15 @@ def test_bf16_neighbours_of_very_different_size(T):
         assert float(((getattr(want, name).abs() > 2 * getattr(want, "e_" + name)).float().mean(dim=0) >= 0.5).float().mean()) > 0.9
     plain = H.tg().expert_mlp(x, w_in, w_out, ids, weights)[0]
     Numbers(x, w_in, w_out, ids, weights, g, train=False).check(out=plain)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=NAMES.get)
+@pytest.mark.parametrize("T,D,F", [(40, 40_000, 24), (40, 64, 40_000), (30_000, 64, 24)])
+def test_long_axes_of_one_sign_stay_within_their_bounds(T, D, F, dtype):
+    """Sums of many chunks: a truncation a step and a rounding a chunk, whichever axis is long."""
+    x, w_in, w_out, ids, weights, g, _ = layer(T, 2, 1, D, F, dtype, seed=F)
+    ids.fill_(1)
+    args = (x.abs() / 16 if D > 10_000 else x.abs() / 2, w_in.abs(), w_out.abs() / 4, ids, weights, g.abs() / 64)
+    check(*args)
+    out = H.tg().expert_mlp(*args[:5])[0]
+    Numbers(*args, train=False).check(out=out)

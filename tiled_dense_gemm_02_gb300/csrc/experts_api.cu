@@ -24,9 +24,10 @@ namespace {
 constexpr int64_t kMaxExtent = int64_t(1) << 31;
 // Stages of a k axis (64 deep, four steps of the adder each) summed in tensor memory
 // before they are added in fp32.  Every step truncates, by less than 2^-23 of
-// the sum, an eighth of that on average where signs are mixed.  16-bit results: 256
-// steps stay below 2^-15.  g, u and d_out W_out, whose product is the fp32
-// gradient of the weights: 16 steps, below 2e-6.  Chunks of 2 / 4 / 8 / 16 stages, 8192 x 4
+// the sum, an eighth of that on average where signs are mixed; every chunk's addition rounds,
+// by 2^-24.  16-bit results: 256 steps stay below 2^-15 (and 2^-24 for every 4096 terms).  g, u and
+// d_out W_out, whose product is the fp32 gradient of the weights: 16 steps, below 2^-19 (and 2^-24
+// for every 256 terms).  Chunks of 2 / 4 / 8 / 16 stages, 8192 x 4
 // rows of 2048 x 1408 in bf16: that gradient is 3.7e-7 / 6.6e-7 / 1.4e-6 / 2.9e-6 of its norm
 // off (the plain fp32 form 7.3e-7); UP and DH take 332 + 294 us at 4, 263 + 201 us whole.  fp16's
 // products have 22 bits where bf16's have 16 and lose more: up to 9.8e-7 at 4 stages over drawn
