@@ -75,6 +75,12 @@ struct Terms {
   static __device__ __forceinline__ int b(int term) { return count == 6 ? (0x010120 >> (4 * term)) & 0xF : 0; }
 };
 
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Adds a shared-memory box to the fp32 tensor at (x, y, z).
 __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
                                                   uint32_t src) {
@@ -239,6 +245,30 @@ struct RowStats {
     }
   }
 };
+
+// The sums of this thread's row and 128 columns: a first chunk's, one more
+// chunk's added, and the whole ones back in tensor memory.
+__device__ __forceinline__ void load_sums(uint32_t tcol, uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b) ptx::tmem_ld_32x32b_x16(tcol + b * 16, sum[b]);
+  ptx::tmem_wait_ld();
+}
+__device__ __forceinline__ void add_sums(uint32_t tcol, uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    uint32_t raw[16];
+    ptx::tmem_ld_32x32b_x16(tcol + b * 16, raw);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      sum[b][i] = __float_as_uint(__uint_as_float(sum[b][i]) + __uint_as_float(raw[i]));
+  }
+}
+__device__ __forceinline__ void store_sums(uint32_t tcol, const uint32_t (&sum)[8][16]) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b) ptx::tmem_st_32x32b_x16(tcol + b * 16, sum[b]);
+  ptx::tmem_wait_st();
+}
 
 // Statistics of this thread's row over its part of the tile's columns.  Of two
 // parts the second leaves them in the accumulator's columns, which it has read,

@@ -1,6 +1,5 @@
 // What the CTA-pair products of the losses and of the experts share: their ring's
-// stage, sums that leave tensor memory chunk by chunk, 16-bit results on their way
-// to memory, and the launch.
+// stage, 16-bit results on their way to memory, and the launch.
 #pragma once
 
 #include <atomic>
@@ -12,36 +11,6 @@ namespace {
 
 constexpr int kSub = kTileM * kTileK * 2;        // 16 KB: one CTA's share of A or B in one stage
 constexpr int kStage = 2 * kSub;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The sums of this thread's row and 128 columns: a first chunk's, one more
-// chunk's added, and the whole ones back in tensor memory.
-__device__ __forceinline__ void load_sums(uint32_t tcol, uint32_t (&sum)[8][16]) {
-#pragma unroll
-  for (int b = 0; b < 8; ++b) ptx::tmem_ld_32x32b_x16(tcol + b * 16, sum[b]);
-  ptx::tmem_wait_ld();
-}
-__device__ __forceinline__ void add_sums(uint32_t tcol, uint32_t (&sum)[8][16]) {
-#pragma unroll
-  for (int b = 0; b < 8; ++b) {
-    uint32_t raw[16];
-    ptx::tmem_ld_32x32b_x16(tcol + b * 16, raw);
-    ptx::tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      sum[b][i] = __float_as_uint(__uint_as_float(sum[b][i]) + __uint_as_float(raw[i]));
-  }
-}
-__device__ __forceinline__ void store_sums(uint32_t tcol, const uint32_t (&sum)[8][16]) {
-#pragma unroll
-  for (int b = 0; b < 8; ++b) ptx::tmem_st_32x32b_x16(tcol + b * 16, sum[b]);
-  ptx::tmem_wait_st();
-}
 
 // This warp's staging buffer, once the last copy out of it has been read.
 __device__ __forceinline__ void stage_row(uint8_t* buf, int lane, const uint32_t (&w)[32]) {
