@@ -30,6 +30,14 @@
 // added in registers, with rounding to nearest, under the next chunk's MMAs; the
 // last sum goes back to tensor memory, where the epilogues read it.
 //
+// Rounded to 16 bits between two products, by choice: h into DOWN, and dg, du and w h into DX, DIN
+// and DOUT (fp16: with their expert's powers of two, round_kernel), since the tensor cores take
+// both operands in the weights' type.  Results are then 1.42 times as far off, in the norm, as
+// their own last rounding (1.65e-3 in bf16).  A second plane with what the first loses would make
+// that 1.0 and double those products' steps: 8192 tokens, 8 of 64 experts of 2048 x 1024, DOWN
+// 230 -> 388 us of 746; a step of 8192 x 4 of 32 experts of 2048 x 1408, the four 798 -> 1451 us of 1600
+// (each timed with twice the k axis).  g, u, d_weights and all sums are fp32.
+//
 // Roles: warp 0 copies, warp 1 MMAs (one thread of the leader), warps 2.. epilogue,
 // eight, or sixteen (DH, and UP where g and u are kept: they move most bytes): a
 // quarter of the lanes and a share of the columns each.  Every role

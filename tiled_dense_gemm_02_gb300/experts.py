@@ -387,7 +387,8 @@ def expert_mlp(hidden, w_in, w_out, ids, weights, *, save=False, workspace=None)
     hidden [T, D], w_in [E, 2 F, D] (F gates, then F ups) and w_out [E, D, F] in
     bf16 or fp16, unit column stride, any row stride; ids [T, k] int64 (below 0:
     unused place) and weights [T, k] float32, as route_experts gives them.  A
-    row without a used place gives 0, whatever hidden holds there.
+    row without a used place gives 0, whatever hidden holds there.  h = silu(g) * u is
+    rounded to the operands' type (fp16: beyond 65504 it is infinite), out once more.
 
     save=True keeps what expert_mlp_backward takes (a uint8 tensor: the rows'
     order, the rows in it, g and u in float32); otherwise saved is None.  If
