@@ -41,8 +41,8 @@
  * the tensor cores with fp32 sums, h is rounded to the operands' type on its way
  * into the second product (fp16's largest number is 65504: a larger h is infinite),
  * and out, summed in fp32, is rounded once.  bf16 rows W_out[e] h lie in the workspace as
- * halves with a power of two for each 32 elements, 2^-12 of each at most, or, where one of the
- * 32 is below 2^-28 of their largest, as bf16: 2^-9 of each.  The tensor cores'
+ * halves with a power of two for each 32 elements, 2^-11 of each at most, or, where one of the
+ * 32 is below 2^-28 of their largest, as bf16: 2^-8 of each.  The tensor cores'
  * adder truncates, by less than 2^-23 of the sum of magnitudes a step of 16 products.  Sums of
  * up to 256 steps are added in fp32: 2^-15, and 2^-24 more for every 4096 products.
  * Where the backward call follows, of up to 16 steps (fp16 12): g, u and the gradient of h

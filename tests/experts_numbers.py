@@ -1,7 +1,7 @@
 """The experts' products at the ends of the numbers' range: their definition in 64 bits with elementwise
 bounds that follow each expert's own numbers.
 
-With u half a step of the operands' type (2^-9 of bf16's, 2^-12 of fp16's leading power at most, eps / 2):
+With u half a step of the operands' type (eps / 2, relative: bf16 2^-8, fp16 2^-11):
 
 * a tensor-core sum of n terms is off by 2^-23 of the sum of magnitudes for each of the `steps` truncating steps
   (16 terms) of a chunk, and by 2^-24 for each addition of a chunk;
@@ -9,8 +9,8 @@ With u half a step of the operands' type (2^-9 of bf16's, 2^-12 of fp16's leadin
   exponential, division and products);
 * fp16's dg, du and w h are rounded with a power of two of their expert that brings the largest finite one to 2^14 or more:
   half of the smallest step, 2^-25, is then 2^-39 of the largest;
-* bf16 rows on their way to a token's sum are off by 2^-12 of each, or by 2^-9 where an element of the same 32 is
-  smaller than 2^-27 of the largest;
+* bf16 rows on their way to a token's sum are halves, off by 2^-11 of each, or bf16, off by 2^-8, where an element of the
+  same 32 is smaller than 2^-27 of the largest (2^-28 in the kernel, by the leading powers);
 * every output is rounded once.
 """
 from __future__ import annotations
@@ -35,7 +35,7 @@ def row_bound(y):
     blocks = torch.nn.functional.pad(y.abs().nan_to_num(0.0, 0.0, 0.0), (0, pad)).view(n, -1, 32)
     most = blocks.amax(dim=2, keepdim=True)
     spread = ((blocks > 0) & (blocks < 2.0 ** -27 * most)).any(dim=2, keepdim=True)
-    return torch.where(spread, 2.0 ** -9, 2.0 ** -12).expand_as(blocks).reshape(n, -1)[:, :D]
+    return torch.where(spread, 2.0 ** -8, 2.0 ** -11).expand_as(blocks).reshape(n, -1)[:, :D]
 
 
 class Numbers:
