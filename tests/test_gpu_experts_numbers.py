@@ -180,3 +180,25 @@ def test_long_axes_of_one_sign_stay_within_their_bounds(T, D, F, dtype):
     check(*args)
     out = H.tg().expert_mlp(*args[:5])[0]
     Numbers(*args, train=False).check(out=out)
+
+
+@pytest.mark.parametrize("byte", [0x00, 0x7F, 0xFF])
+@pytest.mark.parametrize("T,D,F", [(1, 8, 1), (130, 200, 121), (700, 264, 72)])
+def test_fp16_workspaces_hold_anything(T, D, F, byte):
+    """Lent to one call after the other, on two streams: each has its own largest numbers."""
+    lib = H.tg()
+    calls = [layer(T, 5, 2, D, F, F16, seed=s)[:6] for s in (1, 2)]
+    calls[1][5].mul_(64)
+    want = [gradients(*c) for c in calls]
+    n = lib.experts_workspace_size(1, T, 5, 2, D, F, calls[0][1].data_ptr(), D, calls[0][2].data_ptr(), F, lib.F16)[1]
+    ws = [torch.full((n,), byte, dtype=torch.uint8, device="cuda") for _ in calls]
+    saved = [lib.expert_mlp(*c[:5], save=True)[1] for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for turn in range(2):
+        got = [lib.expert_mlp_backward(*calls[i ^ turn][:5], saved[i ^ turn], calls[i ^ turn][5], workspace=ws[i], stream=streams[i].cuda_stream)
+               for i in range(2)]
+        torch.cuda.synchronize()
+        for i in range(2):
+            for name, v in zip(("dx", "dw_in", "dw_out", "dw"), got[i]):
+                assert torch.equal(v, want[i ^ turn][name]), (turn, name)
