@@ -36,7 +36,10 @@
 // their own last rounding (1.65e-3 in bf16).  A second plane with what the first loses would make
 // that 1.0 and double those products' steps: 8192 tokens, 8 of 64 experts of 2048 x 1024, DOWN
 // 230 -> 388 us of 746; a step of 8192 x 4 of 32 experts of 2048 x 1408, the four 798 -> 1451 us of 1600
-// (each timed with twice the k axis).  g, u, d_weights and all sums are fp32.
+// (each timed with twice the k axis).  Built for forward calls of up to 2048 places, where the weights'
+// bytes are the bound, it took 64 tokens, 8 of 128 experts of 2048 x 768 from 195 to 207 us and 1024
+// tokens, 2 of 8 of 4096 x 4096 from 459 to 548, and such a call's out was no longer the bits that a
+// call gives which keeps g and u.  g, u, d_weights and all sums are fp32.
 //
 // Roles: warp 0 copies, warp 1 MMAs (one thread of the leader), warps 2.. epilogue,
 // eight, or sixteen (DH, and UP where g and u are kept: they move most bytes): a
